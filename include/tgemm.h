@@ -53,7 +53,8 @@ extern "C" {
 typedef enum tgemm_dtype {
     TGEMM_F32 = 0,
     TGEMM_BF16 = 1,
-    TGEMM_I8 = 2
+    TGEMM_I8 = 2,
+    TGEMM_F16 = 3 /* an input of tgemm_fp8_quantize and tgemm_orthogonalize; no gemm_plan type */
 } tgemm_dtype;
 
 #define TGEMM_OK 0
@@ -352,6 +353,61 @@ int gemm_kernel_occupancy(const tgemm_plan* plan, int32_t packed, int32_t* workg
  * (0 <= i < count) and returns TGEMM_OK, or TGEMM_E_ARG for a bad index. */
 int gemm_variant_count(int32_t dtype);
 int gemm_variant_get(int32_t dtype, int32_t index, tgemm_variant* out);
+
+/* ---- 8-bit floating point products with block scales -----------------------
+ *
+ * A quantised operand is a row-major matrix of 8-bit floats Q (rows x cols,
+ * leading dimension ldq) and a table of scale bytes S (ceil(cols / 128) x
+ * rows, leading dimension lds): element (r, c) stands for
+ *
+ *     Q[r ldq + c] * 2^(S[(c / 128) lds + r] - 127),
+ *
+ * a power-of-two scale for each 128 elements of a row (S 255 means NaN).
+ * Both operands of a product run along K, so the backward products of a
+ * layer take the transposed images that tgemm_fp8_quantize writes beside
+ * the plain ones. */
+#define TGEMM_E4M3 0          /* 4 exponent bits, largest value 448, no infinities */
+#define TGEMM_E5M2 1          /* 5 exponent bits, largest value 57344, infinities */
+#define TGEMM_BLOCK_ROW 0     /* a scale for each 128 elements of a row of the image */
+#define TGEMM_BLOCK_SQUARE 1  /* a scale for each 128 x 128 block, written to each of its rows */
+
+/* Quantise X (rows x cols, float, bfloat16 or float16 by `dtype`, leading
+ * dimension ldx elements) into Q and S as above, in format `fmt`; with Qt and
+ * St not NULL also the image of X transposed (Qt cols x rows, St
+ * ceil(rows / 128) x cols).  BLOCK_ROW: each image's scales follow its own
+ * rows.  BLOCK_SQUARE: the transposed image is Q transposed, with the same
+ * scales.  For a block with largest finite magnitude a the scale is 2^e, e
+ * the least integer with a <= MAX 2^e (MAX the format's largest value), not
+ * below -127, 0 for a block of zeros; values x 2^-e are rounded to nearest,
+ * ties to even.  NaN stays NaN; an infinity becomes the format's infinity, or
+ * NaN in e4m3, and does not enter a.  Any leading dimensions and byte
+ * alignments of Q, S, Qt, St are written (scale tables that a product will
+ * read want rows on 4-byte boundaries).  Elements outside the images are not
+ * written; rows = 0 or cols = 0 does nothing.  The outputs must not overlap X
+ * or each other.  Returns TGEMM_OK or a TGEMM_E_* code. */
+int tgemm_fp8_quantize(int64_t rows, int64_t cols, int32_t dtype, const void* X, int64_t ldx, int32_t fmt,
+                       int32_t block, void* Q, int64_t ldq, void* S, int64_t lds, void* Qt, int64_t ldqt,
+                       void* St, int64_t ldst, void* stream);
+
+/* Enqueue C = A B^T: A is M x K in format fmt_a with scales SA (ceil(K / 128)
+ * x M), B is N x K in format fmt_b with scales SB, C is M x N bfloat16 bits,
+ * row-major, overwritten.  The matrix cores sum in float, but align the
+ * products of a group of eight to the largest of them and keep 13 bits below
+ * it: a sum is off by less than 2^-10 of sum |a b|, by about 2^-17 of it on
+ * random data.  It is rounded once, to nearest even; hence no wider C.
+ * Rows of A and B may start at any byte.  Scale tables: ldsa and ldsb
+ * multiples of 4, pointers 4-byte aligned (TGEMM_E_ALIGN otherwise), and the
+ * bytes of a table's last row up to M (N) rounded up to 4 readable; their
+ * values past M (N) do not matter.  K = 0 writes zeros; M = 0 or N = 0 does
+ * nothing.  C must not overlap an operand.  Returns TGEMM_OK or a TGEMM_E_*
+ * code. */
+int tgemm_fp8_gemm(int64_t M, int64_t N, int64_t K, int32_t fmt_a, const void* A, int64_t lda, const void* SA,
+                   int64_t ldsa, int32_t fmt_b, const void* B, int64_t ldb, const void* SB, int64_t ldsb, void* C,
+                   int64_t ldc, void* stream);
+
+/* Name of the kernel tgemm_fp8_gemm launches for these sizes ("" where it
+ * launches none). */
+const char* tgemm_fp8_gemm_kernel(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb);
 
 /* Library version string. */
 const char* tgemm_version(void);

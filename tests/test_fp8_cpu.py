@@ -1,0 +1,130 @@
+"""CPU: argument checks of the 8-bit block-scaled operators, their choice of
+kernel, and the reference's own pins."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_ref as ref
+
+tl = pytest.importorskip("tiled_software_pipelined_amd.lib")
+P = ctypes.c_void_p
+
+
+@pytest.mark.parametrize("fmt,dtype", [("e4m3", torch.float8_e4m3fn), ("e5m2", torch.float8_e5m2)])
+def test_reference_rounding_matches_the_type(fmt, dtype):
+    bits = torch.arange(256, dtype=torch.uint8).view(dtype).double().numpy()
+    t = ref.TABLE[fmt]
+    assert np.array_equal(bits[: len(t)], t) and np.array_equal(bits[128:128 + len(t)], -t)
+    g = np.random.default_rng(1)
+    y = np.concatenate([g.standard_normal(4000) * 10.0 ** g.integers(-5, 2, 4000), (t[:-1] + t[1:]) / 2, -t, t])
+    y = np.clip(y, -t[-1], t[-1]).astype(np.float32)
+    got = torch.from_numpy(y).to(dtype).double().numpy()
+    assert np.array_equal(ref.round8(y.astype(np.float64), fmt), got)
+
+
+def test_reference_scales():
+    x = np.zeros((3, 130))
+    x[0, 0], x[0, 129], x[1, 5] = 448.0, 448.5, 2.0 ** -140
+    _, e = ref.quantize(x, "e4m3")
+    assert e.shape == (2, 3) and e[0, 0] == 0 and e[1, 0] == 1 and e[0, 1] == -127 and (e[:, 2] == 0).all()
+    _, e = ref.quantize(np.array([[57344.0]]), "e5m2")
+    assert e[0, 0] == 0
+
+
+def q(rows, cols, dtype=0, X=P(64), ldx=None, fmt=0, block=0, Q=P(64), ldq=None, S=P(64), lds=None, Qt=None, ldqt=0,
+      St=None, ldst=0):
+    return tl._lib.tgemm_fp8_quantize(rows, cols, dtype, X, cols if ldx is None else ldx, fmt, block, Q,
+                                      cols if ldq is None else ldq, S, rows if lds is None else lds, Qt, ldqt, St,
+                                      ldst, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1, cols=4), -1), (dict(rows=4, cols=2 ** 31), -1), (dict(rows=4, cols=4, dtype=2), -1),
+    (dict(rows=4, cols=4, dtype=9), -1), (dict(rows=4, cols=4, fmt=2), -1), (dict(rows=4, cols=4, block=2), -1),
+    (dict(rows=4, cols=4, ldx=3), -1), (dict(rows=4, cols=4, ldq=3), -1), (dict(rows=4, cols=4, lds=3), -1),
+    (dict(rows=4, cols=4, Qt=P(64), St=P(64), ldqt=3, ldst=4), -1),
+    (dict(rows=4, cols=4, Qt=P(64), St=P(64), ldqt=4, ldst=3), -1),
+    (dict(rows=4, cols=4, X=None), -2), (dict(rows=4, cols=4, Q=None), -2), (dict(rows=4, cols=4, S=None), -2),
+    (dict(rows=4, cols=4, Qt=P(64), ldqt=4, ldst=4), -2), (dict(rows=4, cols=4, St=P(64), ldqt=4, ldst=4), -2),
+    (dict(rows=4, cols=4, X=P(66)), -3), (dict(rows=4, cols=4, dtype=1, X=P(65)), -3),
+])
+def test_quantize_refuses(kw, code):
+    assert q(**kw) == code and tl.last_error()
+
+
+@pytest.mark.parametrize("rows,cols", [(0, 4), (4, 0), (0, 0)])
+def test_quantize_of_nothing_needs_no_device(rows, cols):
+    assert q(rows, cols, X=None, Q=None, S=None) == 0 and tl.last_error() == ""
+
+
+def g(M, N, K, fa=0, A=P(64), lda=None, SA=P(64), ldsa=None, fb=0, B=P(64), ldb=None, SB=P(64), ldsb=None, C=P(64),
+      ldc=None):
+    d = lambda v, w: w if v is None else v  # noqa: E731
+    return tl._lib.tgemm_fp8_gemm(M, N, K, fa, A, d(lda, K), SA, d(ldsa, (M + 3) // 4 * 4), fb, B, d(ldb, K), SB,
+                                  d(ldsb, (N + 3) // 4 * 4), C, d(ldc, N), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1, N=4, K=4), -1), (dict(M=4, N=2 ** 31, K=4), -1), (dict(M=4, N=4, K=2 ** 31 - 1), -1),
+    (dict(M=4, N=4, K=4, fa=2), -1), (dict(M=4, N=4, K=4, fb=-1), -1), (dict(M=4, N=4, K=4, lda=3), -1),
+    (dict(M=4, N=4, K=4, ldb=3), -1), (dict(M=8, N=4, K=4, ldsa=4), -1), (dict(M=4, N=8, K=4, ldsb=4), -1),
+    (dict(M=4, N=4, K=4, ldc=3), -1), (dict(M=4, N=4, K=4, A=None), -2), (dict(M=4, N=4, K=4, B=None), -2),
+    (dict(M=4, N=4, K=4, SA=None), -2), (dict(M=4, N=4, K=4, SB=None), -2), (dict(M=4, N=4, K=4, C=None), -2),
+    (dict(M=4, N=4, K=0, C=None), -2), (dict(M=4, N=4, K=4, C=P(65)), -3), (dict(M=4, N=4, K=4, ldsa=6), -3),
+    (dict(M=4, N=4, K=4, ldsb=7), -3), (dict(M=4, N=4, K=4, SA=P(66)), -3), (dict(M=4, N=4, K=4, SB=P(65)), -3),
+])
+def test_gemm_refuses(kw, code):
+    assert g(**kw) == code and tl.last_error()
+
+
+@pytest.mark.parametrize("M,N", [(0, 4), (4, 0)])
+def test_gemm_of_nothing_needs_no_device(M, N):
+    assert g(M, N, 4, A=None, B=None, SA=None, SB=None, C=None) == 0 and tl.last_error() == ""
+
+
+def test_kernel_choice():
+    k = tl.gemm_fp8_kernel
+    assert k(0, 4, 4) == k(4, 0, 4) == k(-1, 4, 4) == ""
+    assert [k(m, 4096, 4096).split("_")[0] for m in (1, 16, 17, 32, 33, 64)] == ["rows16", "rows16", "rows32", "rows32",
+                                                                                "rows64", "rows64"]
+    assert k(4096, 4096, 4096).startswith("t256x256x128")
+    # rows too long for a tiled kernel's 32-bit offsets
+    assert k(4096, 4096, 64, lda=2 ** 31).startswith("rows64") and k(4096, 4096, 64, ldb=2 ** 31).startswith("rows64")
+
+
+def test_binding_refuses_before_any_launch():
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="GPU"):
+        tl.quantize_fp8(x)
+    with pytest.raises(TypeError, match="8-bit"):
+        tl.quantize_fp8(x, dtype=torch.int8)
+    with pytest.raises(ValueError, match="block"):
+        tl.quantize_fp8(x, block="column")
+    e = torch.zeros(4, 128).to(torch.float8_e4m3fn)
+    s = torch.zeros(1, 4, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="GPU"):
+        tl.gemm_fp8(e, s, e, s)
+    with pytest.raises(ValueError, match="GPU"):
+        tl.linear_fp8(x, x)
+    with pytest.raises(TypeError, match="8-bit"):
+        tl.linear_fp8(x, x, grad_dtype=torch.float16)
+
+
+def test_scale_table_checks():
+    dev = torch.device("cpu")
+    s = torch.zeros(2, 16, dtype=torch.uint8)
+    assert tl._scales(s, 16, 256, dev, "S") == 16
+    assert tl._scales(s[:, :5], 5, 256, dev, "S") == 16
+    assert tl._scales(s[:1, :5], 5, 7, dev, "S") == 8
+    assert tl._scales(s.view(torch.float8_e8m0fnu), 16, 256, dev, "S") == 16
+    assert tl._scales(s[:0], 16, 0, dev, "S") == 16
+    for bad, rows, cols in ((s, 16, 128), (s, 15, 256), (s[:, 1:5], 4, 256), (torch.zeros(2, 6, dtype=torch.uint8), 6, 256),
+                            (torch.zeros(2, 5, dtype=torch.uint8), 5, 256), (s[:, ::2], 8, 256),
+                            (torch.zeros(1, 5, dtype=torch.uint8), 5, 100),
+                            (torch.zeros(1, 16, dtype=torch.uint8).expand(2, 16), 16, 256)):
+        with pytest.raises(ValueError):
+            tl._scales(bad, rows, cols, dev, "S")
+    with pytest.raises(TypeError):
+        tl._scales(s.float(), 16, 256, dev, "S")

@@ -1,0 +1,199 @@
+// Block-scaled 8-bit products: kernels, and the table that the host picks
+// from.  C = sum over 128-blocks kb of 2^(sa + sb) * (A_kb B_kb^T), C bfloat16.
+#pragma once
+
+#include "tg_nt.hpp"
+
+namespace tg {
+
+struct Fp8Args {
+    NtOperands op;
+    uint16_t* C;
+    int64_t ldc;
+    int32_t tiles_m, tiles_n;
+};
+
+typedef void (*Fp8Fn)(Fp8Args);
+
+// One compiled kernel.  bm, bn: rows and columns of C per workgroup.
+struct Fp8Kernel {
+    Fp8Fn fn;
+    int bm, bn, threads;
+    char name[64];
+};
+
+// Tiles, from the largest; and the kernels for few rows.
+enum Fp8Pick { PICK_256 = 0, PICK_128, PICK_64, PICK_ROWS16, PICK_ROWS32, PICK_ROWS64, PICK_COUNT };
+
+const Fp8Kernel* fp8_kernels_e4m3_e4m3();
+const Fp8Kernel* fp8_kernels_e4m3_e5m2();
+const Fp8Kernel* fp8_kernels_e5m2_e4m3();
+const Fp8Kernel* fp8_kernels_e5m2_e5m2();
+
+// bfloat16 bits, to nearest even: the one rounding of a result
+__device__ __forceinline__ uint16_t bf16_bits(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
+
+// Tiled kernel.
+template <class G>
+__device__ __forceinline__ void fp8_tile(const Fp8Args& g) {
+    __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
+    const int lane = lane_id(), wave = wave_id();
+    constexpr int WAVES_N = G::BN / G::WTN;
+    int tm, tn;
+    grouped_tile(xcd_rank(blockIdx.x, gridDim.x), g.tiles_m, g.tiles_n, 4, tm, tn);
+    const int m0 = tm * G::BM, n0 = tn * G::BN;
+    const int wm0 = (wave / WAVES_N) * G::WTM, wn0 = (wave % WAVES_N) * G::WTN;
+    typename G::Acc acc[G::FM][G::FN];
+    G::product(g.op, m0, n0, (TG_LDS char*)smem_raw, acc, wm0, wn0, lane, wave);
+
+    // a lane's FN results of one row are adjacent: one store, of any
+    // alignment; element stores where the row ends inside them
+    const int n = n0 + wn0 + G::col_of(0, lane);
+    const bool whole = n + G::FN <= g.op.N;
+#pragma unroll
+    for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int m = m0 + wm0 + G::row_of(i, r, lane);
+            uint16_t v[G::FN];
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j) v[j] = bf16_bits(acc[i][j][r]);
+            uint16_t* dst = g.C + (int64_t)m * g.ldc + n;
+            if (m < g.op.M) {
+                if (whole) __builtin_memcpy(dst, v, sizeof v);
+                else {
+#pragma unroll
+                    for (int j = 0; j < G::FN; ++j)
+                        if (n + j < g.op.N) dst[j] = v[j];
+                }
+            }
+        }
+}
+
+template <class G>
+__global__ __launch_bounds__(G::NT) void fp8_tile_kernel(Fp8Args g) {
+    fp8_tile<G>(g);
+}
+
+// Few rows of A (a decode batch): bound by one read of B.  A workgroup takes
+// 16 rows of B and 16 MT rows of A; its NW waves deal the 128-blocks of K
+// among them, operands going straight to registers (a wave's blocks are its
+// own: nothing to share through LDS), and add their sums through LDS at the
+// end.  v_mfma_scale_f32_16x16x128_f8f6f4: lane l holds row l % 16, chunks
+// l / 16 and 4 + l / 16 of the block's eight 16-byte chunks, so one load
+// instruction reads 64 adjacent bytes of each of 16 rows.
+template <int FA, int FB, int MT, int NW, int U>
+__global__ __launch_bounds__(64 * NW) void fp8_rows_kernel(Fp8Args g) {
+    __shared__ float part[NW][MT * 256];
+    const NtOperands& o = g.op;
+    const int lane = lane_id(), wave = wave_id();
+    const int tn = blockIdx.x % g.tiles_n, tm = blockIdx.x / g.tiles_n;
+    const int m0 = tm * 16 * MT, n0 = tn * 16;
+    const int blocks = (o.k + 127) / 128;
+    const int at = (lane >> 4) * 16;
+    const int nb = min(n0 + (lane & 15), o.N - 1);
+    const char* brow = o.b + (int64_t)nb * o.ldb + at;
+    const uint8_t* bs = o.sb + nb;
+    const char* arow[MT];
+    const uint8_t* as[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const int ma = min(m0 + 16 * t + (lane & 15), o.M - 1);
+        arow[t] = o.a + (int64_t)ma * o.lda + at;
+        as[t] = o.sa + ma;
+    }
+    f32x4 acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = f32x4{0, 0, 0, 0};
+
+    struct Block {
+        i32x4 b[2], a[MT][2];
+        int sb, sa[MT];
+    };
+    auto load = [&](Block& x, int kb) {
+        const int64_t k0 = (int64_t)kb * 128;
+        if (k0 + 128 <= o.k) {  // wave-uniform
+            x.b[0] = load16(brow + k0);
+            x.b[1] = load16(brow + k0 + 64);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                x.a[t][0] = load16(arow[t] + k0);
+                x.a[t][1] = load16(arow[t] + k0 + 64);
+            }
+        } else {
+            // the last, partial block: zero past the row's end
+            const int end = o.k - at;
+            auto chunk = [&](const char* row, int64_t p) {
+                union { i32x4 v; uint8_t e[16]; } u;
+#pragma unroll
+                for (int t = 0; t < 16; ++t)
+                    u.e[t] = load_or_zero(reinterpret_cast<const uint8_t*>(row) + p + t, p + t < end);
+                return u.v;
+            };
+            x.b[0] = chunk(brow, k0);
+            x.b[1] = chunk(brow, k0 + 64);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                x.a[t][0] = chunk(arow[t], k0);
+                x.a[t][1] = chunk(arow[t], k0 + 64);
+            }
+        }
+        x.sb = bs[(int64_t)kb * o.ldsb];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) x.sa[t] = as[t][(int64_t)kb * o.ldsa];
+    };
+    auto multiply = [&](const Block& x) {
+        const i32x8 vb = __builtin_shufflevector(x.b[0], x.b[1], 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            const i32x8 va = __builtin_shufflevector(x.a[t][0], x.a[t][1], 0, 1, 2, 3, 4, 5, 6, 7);
+            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, acc[t], FA, FB, 0, x.sa[t], 0, x.sb);
+        }
+    };
+    // U blocks in flight per wave; whole rounds first, then one at a time
+    int kb = wave;
+    for (; kb + (U - 1) * NW < blocks; kb += U * NW) {
+        Block x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) load(x[u], kb + u * NW);
+#pragma unroll
+        for (int u = 0; u < U; ++u) multiply(x[u]);
+    }
+    for (; kb < blocks; kb += NW) {
+        Block x;
+        load(x, kb);
+        multiply(x);
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) part[wave][t * 256 + (4 * (lane >> 4) + r) * 16 + (lane & 15)] = acc[t][r];
+    __syncthreads();
+    for (int e = threadIdx.x; e < MT * 256; e += 64 * NW) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) sum += part[w][e];
+        const int m = m0 + (e >> 4), n = n0 + (e & 15);
+        if (m < o.M && n < o.N) g.C[(int64_t)m * g.ldc + n] = bf16_bits(sum);
+    }
+}
+
+// The kernels of one pair of formats, in the order of Fp8Pick.
+template <int FA, int FB>
+const Fp8Kernel* fp8_kernel_table() {
+    typedef NtF8<FA, FB> Tr;
+    typedef NtGemm<Tr, 256, 256, 2, 4, 2, false> G256;
+    typedef NtGemm<Tr, 128, 128, 2, 2, 4, true> G128;
+    typedef NtGemm<Tr, 64, 64, 2, 2, 8, true> G64;
+    static const Fp8Kernel table[PICK_COUNT] = {
+        {fp8_tile_kernel<G256>, G256::BM, G256::BN, G256::NT, "t256x256x128_w2x4_s2"},
+        {fp8_tile_kernel<G128>, G128::BM, G128::BN, G128::NT, "t128x128x128_w2x2_s4_slice"},
+        {fp8_tile_kernel<G64>, G64::BM, G64::BN, G64::NT, "t64x64x128_w2x2_s8_slice"},
+        {fp8_rows_kernel<FA, FB, 1, 8, 4>, 16, 16, 512, "rows16_w8"},
+        {fp8_rows_kernel<FA, FB, 2, 8, 4>, 32, 16, 512, "rows32_w8"},
+        {fp8_rows_kernel<FA, FB, 4, 8, 2>, 64, 16, 512, "rows64_w8"},
+    };
+    return table;
+}
+
+}  // namespace tg

@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "tg_args.hpp"
+#include "tg_host.hpp"
 #include "tg_pack.hpp"
 #include "tgemm.h"
 
@@ -393,6 +394,23 @@ __global__ void zero_fill_4byte(uint32_t* C, int M, int N, int64_t ldc) {
 }
 
 }  // namespace
+
+namespace tg {
+
+void set_error(const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_err = buf;
+}
+
+void clear_error() { g_err.clear(); }
+
+int current_device_ok() { return check_arch(); }
+
+}  // namespace tg
 
 extern "C" {
 

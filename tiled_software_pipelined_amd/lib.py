@@ -9,6 +9,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -17,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libtgemm.so")
 
 # dtype codes of the C ABI
 F32, BF16, I8 = 0, 1, 2
+F16 = 3  # an input of quantize_fp8 and orthogonalize; no plan's type
 DTYPE_NAMES = {F32: "f32", BF16: "bf16", I8: "i8"}
 
 OK = 0
@@ -65,7 +67,7 @@ EXPORTS = ("gemm_plan", "gemm_plan_variant", "gemm_run", "gemm_destroy", "tgemm_
            "gemm_plan_get_info", "gemm_variant_count", "gemm_variant_get", "tgemm_version",
            "tgemm_lds_read_probe", "tgemm_mfma_rate_probe", "gemm_workspace_bytes", "gemm_run_ws",
            "gemm_kernel_occupancy", "gemm_clock_slots", "gemm_run_clocked", "gemm_run_noalloc",
-           "tgemm_set_c_store_policy")
+           "tgemm_set_c_store_policy", "tgemm_fp8_quantize", "tgemm_fp8_gemm", "tgemm_fp8_gemm_kernel")
 
 
 def _load():
@@ -114,6 +116,12 @@ def _load():
     lib.tgemm_mfma_rate_probe.restype = ctypes.c_int
     lib.tgemm_set_c_store_policy.argtypes = [i32]
     lib.tgemm_set_c_store_policy.restype = ctypes.c_int
+    lib.tgemm_fp8_quantize.argtypes = [i64, i64, i32, vp, i64, i32, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+    lib.tgemm_fp8_quantize.restype = ctypes.c_int
+    lib.tgemm_fp8_gemm.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, i32, vp, i64, vp, i64, vp, i64, vp]
+    lib.tgemm_fp8_gemm.restype = ctypes.c_int
+    lib.tgemm_fp8_gemm_kernel.argtypes = [i64, i64, i64, i64, i64]
+    lib.tgemm_fp8_gemm_kernel.restype = ctypes.c_char_p
     return lib
 
 
@@ -407,3 +415,205 @@ def gemm(A, B, out=None, variant: Variant | None = None, workspace: bool = True)
         else:
             p.run_ptr(A.data_ptr(), B.data_ptr(), out.data_ptr(), stream)
     return out
+
+
+# ---- 8-bit floating point products with block scales --------------------------
+
+FP8_BLOCK = 128  # elements of a row that share a scale
+E4M3, E5M2 = 0, 1
+BLOCKS = {"row": 0, "square": 1}
+
+
+def _fp8_code(dtype):
+    import torch
+    codes = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
+    if dtype not in codes:
+        raise TypeError("unsupported 8-bit type %s (float8_e4m3fn, float8_e5m2)" % dtype)
+    return codes[dtype]
+
+
+def _real_code(t, name):
+    import torch
+    codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+    if t.dtype not in codes:
+        raise TypeError("%s has unsupported dtype %s (float32, bfloat16, float16)" % (name, t.dtype))
+    return codes[t.dtype]
+
+
+def _image(rows, cols, dtype, device):
+    """An empty quantised operand: values, and scales whose rows start on
+    16-byte boundaries."""
+    import torch
+    q = torch.empty((rows, cols), dtype=dtype, device=device)
+    s = torch.empty((-(-cols // FP8_BLOCK), -(-rows // 16) * 16), dtype=torch.float8_e8m0fnu, device=device)
+    return q, s[:, :rows]
+
+
+def quantize_fp8(X, dtype=None, block="row", transpose=False):
+    """(Q, S), the 8-bit image of X with a power-of-two scale for each 128
+    elements of a row; with ``transpose`` (Q, S, Qt, St), also that of X
+    transposed.
+
+    X: (rows, cols) float32, bfloat16 or float16 on the GPU, row-major (row
+    stride may exceed the row length).  Q: (rows, cols) of ``dtype``
+    (float8_e4m3fn, the default, or float8_e5m2); S: (ceil(cols / 128), rows)
+    float8_e8m0fnu; X[r, c] is near Q[r, c] * S[c // 128, r].  With block
+    "square" one scale serves each 128 x 128 block of X, and Qt is Q
+    transposed (weights, whose two images then hold the same values); with
+    "row" each image's scales follow its own rows.  A scale is the least power
+    of two (at least 2^-127) that keeps its block's finite values within the
+    type's range.  NaN stays NaN, and an infinity becomes the type's infinity
+    or NaN.  Runs on the current stream.
+    """
+    import torch
+    dtype = torch.float8_e4m3fn if dtype is None else dtype
+    fmt = _fp8_code(dtype)
+    if block not in BLOCKS:
+        raise ValueError("block must be \"row\" or \"square\", got %r" % (block,))
+    if not X.is_cuda:
+        raise ValueError("X must be a GPU tensor")
+    code, ldx = _real_code(X, "X"), _ld(X, "X")
+    rows, cols = X.shape
+    out = _image(rows, cols, dtype, X.device)
+    if transpose:
+        out += _image(cols, rows, dtype, X.device)
+    q, s, qt, st = out if transpose else out + (None, None)
+    with torch.cuda.device(X.device):
+        rc = _lib.tgemm_fp8_quantize(
+            rows, cols, code, X.data_ptr(), ldx, fmt, BLOCKS[block], q.data_ptr(), max(cols, 1), s.data_ptr(),
+            max(s.stride(0), 1), qt.data_ptr() if transpose else None, max(rows, 1),
+            st.data_ptr() if transpose else None, max(st.stride(0), 1) if transpose else 0,
+            torch.cuda.current_stream(X.device).cuda_stream)
+    if rc != OK:
+        raise TgemmError(rc, last_error())
+    return out
+
+
+def _scales(s, rows, cols, device, name):
+    """Row stride of a scale table (ceil(cols / 128), rows) that a product may read."""
+    import torch
+    if s.dtype not in (torch.float8_e8m0fnu, torch.uint8):
+        raise TypeError("%s must be float8_e8m0fnu (or its bytes as uint8), got %s" % (name, s.dtype))
+    blocks = -(-cols // FP8_BLOCK)
+    if tuple(s.shape) != (blocks, rows) or s.device != device:
+        raise ValueError("%s must be of shape (%d, %d) on %s, got %s on %s" % (
+            name, blocks, rows, device, tuple(s.shape), s.device))
+    if blocks == 0 or rows == 0:
+        return -(-max(rows, 1) // 4) * 4
+    if rows > 1 and s.stride(1) != 1:
+        raise ValueError("%s must have unit stride along its rows" % name)
+    ld = s.stride(0) if blocks > 1 else -(-rows // 4) * 4
+    if ld < rows or ld % 4 or s.data_ptr() % 4:
+        raise ValueError("%s needs rows on 4-byte boundaries (row stride %d for %d rows): quantize_fp8 lays them out so"
+                         % (name, ld, rows))
+    # the product reads whole 4-byte words of the last row
+    end = s.storage_offset() + (blocks - 1) * ld + -(-rows // 4) * 4
+    if end > s.untyped_storage().nbytes():
+        raise ValueError("%s must be readable up to %d rows (a multiple of 4): quantize_fp8 lays tables out so"
+                         % (name, -(-rows // 4) * 4))
+    return ld
+
+
+def gemm_fp8(A, SA, B, SB, out=None):
+    """C = A @ B^T of two quantised operands, on the current stream.
+
+    A: (M, K), B: (N, K), float8_e4m3fn or float8_e5m2 each, row-major (row
+    stride may exceed the row length, rows may start at any byte), with their
+    scale tables SA (ceil(K / 128), M) and SB (ceil(K / 128), N) as
+    :func:`quantize_fp8` returns them.  Returns C (M, N) bfloat16, rounded
+    once from the matrix cores' float sums; ``out`` may be a preallocated
+    row-major C.
+    """
+    import torch
+    if not (A.is_cuda and B.is_cuda):
+        raise ValueError("A and B must be GPU tensors")
+    if A.device != B.device:
+        raise ValueError("A and B must be on the same device (%s, %s)" % (A.device, B.device))
+    fa, fb = _fp8_code(A.dtype), _fp8_code(B.dtype)
+    lda, ldb = _ld(A, "A"), _ld(B, "B")
+    (M, K), (N, K2) = A.shape, B.shape
+    if K != K2:
+        raise ValueError("inner dimensions differ: %d vs %d" % (K, K2))
+    ldsa, ldsb = _scales(SA, M, K, A.device, "SA"), _scales(SB, N, K, A.device, "SB")
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or out.device != A.device:
+        raise ValueError("out must be a bfloat16 tensor of shape (%d, %d) on %s" % (M, N, A.device))
+    ldc = _ld(out, "out")
+    with torch.cuda.device(A.device):
+        rc = _lib.tgemm_fp8_gemm(M, N, K, fa, A.data_ptr(), lda, SA.data_ptr(), ldsa, fb, B.data_ptr(), ldb,
+                                 SB.data_ptr(), ldsb, out.data_ptr(), ldc,
+                                 torch.cuda.current_stream(A.device).cuda_stream)
+    if rc != OK:
+        raise TgemmError(rc, last_error())
+    return out
+
+
+def gemm_fp8_kernel(M, N, K, lda=None, ldb=None) -> str:
+    """Name of the kernel :func:`gemm_fp8` launches for these sizes."""
+    return _lib.tgemm_fp8_gemm_kernel(M, N, K, K if lda is None else lda, K if ldb is None else ldb).decode()
+
+
+def _rows(t):
+    """t as a row-major matrix whose rows do not overlap: itself, or a copy."""
+    ok = (t.shape[1] <= 1 or t.stride(1) == 1) and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1])
+    return t if ok else t.contiguous()
+
+
+def _linear_fp8_function():
+    import torch
+
+    class LinearFp8(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w, grad_dtype):
+            x2 = _rows(x.reshape(math.prod(x.shape[:-1]), x.shape[-1]))
+            need_x, need_w = ctx.needs_input_grad[:2]
+            xq = quantize_fp8(x2, transpose=need_w)
+            wq = quantize_fp8(_rows(w), block="square", transpose=need_x)
+            y = gemm_fp8(xq[0], xq[1], wq[0], wq[1])
+            ctx.grad_dtype, ctx.x_shape, ctx.x_dtype, ctx.w_dtype = grad_dtype, x.shape, x.dtype, w.dtype
+            # kept for the backward pass: one byte an element of x and of w
+            ctx.save_for_backward(*(wq[2:] if need_x else (None, None)), *(xq[2:] if need_w else (None, None)))
+            return y.reshape(*x.shape[:-1], w.shape[0]).to(x.dtype)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, gy):
+            wt, wts, xt, xts = ctx.saved_tensors
+            need_x, need_w = ctx.needs_input_grad[:2]
+            # a broadcast gradient (of a sum, say) has no rows of its own
+            g2 = _rows(gy.reshape(math.prod(gy.shape[:-1]), gy.shape[-1]))
+            gq = quantize_fp8(g2, dtype=ctx.grad_dtype, transpose=need_w)
+            gx = gemm_fp8(gq[0], gq[1], wt, wts).reshape(ctx.x_shape).to(ctx.x_dtype) if need_x else None
+            gw = gemm_fp8(gq[2], gq[3], xt, xts).to(ctx.w_dtype) if need_w else None
+            return gx, gw, None
+
+    return LinearFp8
+
+
+_linear_fn = None
+
+
+def linear_fp8(x, w, grad_dtype=None):
+    """y = x @ w^T with x and w quantised to float8_e4m3fn, differentiable.
+
+    x: (..., K), w: (N, K), each float32, bfloat16 or float16.  x is
+    quantised with a scale for each 128 elements of a row, w for each 128 x
+    128 block; y has x's dtype (the product itself is rounded to bfloat16).
+    The backward pass quantises the gradient of y to ``grad_dtype``
+    (float8_e4m3fn by default, or float8_e5m2), along its rows for x's
+    gradient and along its columns for w's, and takes both products from the
+    8-bit images kept by the forward pass: dx = g w, dw = g^T x.  Rounding is
+    passed straight through.  Gradients have their inputs' dtypes.
+    """
+    global _linear_fn
+    import torch
+    grad_dtype = torch.float8_e4m3fn if grad_dtype is None else grad_dtype
+    _fp8_code(grad_dtype)
+    if not (x.is_cuda and w.is_cuda) or x.device != w.device:
+        raise ValueError("x and w must be on one GPU (%s, %s)" % (x.device, w.device))
+    if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
+        raise ValueError("x %s and w %s do not make x @ w^T" % (tuple(x.shape), tuple(w.shape)))
+    if _linear_fn is None:
+        _linear_fn = _linear_fp8_function()
+    return _linear_fn.apply(x, w, grad_dtype)
