@@ -409,6 +409,43 @@ int tgemm_fp8_gemm(int64_t M, int64_t N, int64_t K, int32_t fmt_a, const void* A
  * launches none). */
 const char* tgemm_fp8_gemm_kernel(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb);
 
+/* ---- orthogonalised update --------------------------------------------------
+ *
+ * For each matrix G (rows x cols; float, bfloat16 or float16 by `dtype`) of a
+ * batch: X = G / (|G| + eps), |G| the root of the sum of squares, then `steps`
+ * times, with coefficients[3 k .. 3 k + 2] = a, b, c of step k,
+ *
+ *     X <- a X + (b A + c A^2) X,   A = X X^T
+ *
+ * (X^T X and products from the right where rows > cols, which is the same
+ * matrix), which brings the singular values of X near one for the usual
+ * coefficients; O (rows x cols bfloat16 bits) gets the result, rounded once.
+ * Matrix z starts stride_g z (stride_o z) elements after the first; ldg, ldo
+ * are leading dimensions, rows may start at any element.  X is held to 22
+ * bits through the steps and products take 11-bit operands with float sums:
+ * the result is off by 0.5 to 1e-3 of its norm before the rounding (up to
+ * 4e-3 where a few equal singular values hold all of it).  Elements of X
+ * below 2^-37 are taken as zero (a matrix far smaller than eps).  A matrix
+ * of zeros gives zeros (for eps > 0); one with a NaN or an infinity gives
+ * NaN everywhere.  Coefficients are refused (TGEMM_E_ARG) when they let
+ * singular values that start in [0, 1] pass 3.5 before the last step, or
+ * |b s^2 + c s^4| pass 14 in any: the workspace's half precision matrices
+ * hold no more.
+ *
+ * workspace: tgemm_orthogonalize_workspace_bytes(batch, rows, cols) bytes
+ * (-1 for sizes out of range: rows and cols up to 2^20, batch up to 2^16) of
+ * device memory, 256-byte aligned; its contents are overwritten, so calls
+ * that share one must be ordered on one stream.  O may be G's own memory
+ * (then with the same element size and strides); otherwise it must not
+ * overlap G, and neither may overlap the workspace.  Elements of O between
+ * its rows are not written.  batch, rows or cols = 0 does nothing.  steps: 1
+ * to 64.  Returns TGEMM_OK or a TGEMM_E_* code. */
+int64_t tgemm_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype, const void* G, int64_t ldg,
+                        int64_t stride_g, void* O, int64_t ldo, int64_t stride_o, int32_t steps,
+                        const double* coefficients, double eps, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+
 /* Library version string. */
 const char* tgemm_version(void);
 

@@ -1,0 +1,66 @@
+"""CPU: argument checks of orthogonalize, and its workspace size."""
+import ctypes
+
+import pytest
+import torch
+
+tl = pytest.importorskip("tiled_software_pipelined_amd.lib")
+P = ctypes.c_void_p
+USUAL = (3.4445, -4.7750, 2.0315)
+
+
+def call(batch=1, rows=4, cols=6, dtype=0, G=P(256), ldg=None, stride_g=None, O=P(256), ldo=None, stride_o=None, steps=5,
+         coef=None, eps=1e-7, ws=P(256), ws_bytes=1 << 40):
+    coef = USUAL * max(steps, 1) if coef is None else coef
+    ldg, ldo = cols if ldg is None else ldg, cols if ldo is None else ldo
+    stride_g, stride_o = rows * ldg if stride_g is None else stride_g, rows * ldo if stride_o is None else stride_o
+    c = (ctypes.c_double * len(coef))(*coef) if coef != () else None
+    return tl._lib.tgemm_orthogonalize(batch, rows, cols, dtype, G, ldg, stride_g, O, ldo, stride_o, steps, c, eps, ws,
+                                       ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=-1), -1), (dict(rows=-1), -1), (dict(cols=(1 << 20) + 1), -1), (dict(batch=(1 << 16) + 1), -1),
+    (dict(dtype=2), -1), (dict(ldg=5), -1), (dict(ldo=5), -1), (dict(batch=2, stride_g=23), -1),
+    (dict(batch=2, stride_o=23), -1), (dict(steps=0), -1), (dict(steps=65), -1), (dict(eps=-1e-9), -1),
+    (dict(eps=float("nan")), -1), (dict(coef=()), -2), (dict(steps=1, coef=(float("nan"), 0, 0)), -1),
+    (dict(steps=1, coef=(1, float("inf"), 0)), -1), (dict(steps=2, coef=(4, 0, 0) * 2), -1),
+    (dict(steps=2, coef=(1, 14.5, 0) * 2), -1), (dict(steps=1, coef=(1, 14.5, 0)), -1),
+    (dict(G=None), -2), (dict(O=None), -2), (dict(ws=None), -2), (dict(G=P(258)), -3), (dict(dtype=1, G=P(257)), -3),
+    (dict(O=P(257)), -3), (dict(ws=P(128)), -3), (dict(ws_bytes=1000), -1),
+])
+def test_refuses(kw, code):
+    assert call(**kw) == code and tl.last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(batch=0), dict(rows=0), dict(cols=0)])
+def test_nothing_to_do_needs_no_device(kw):
+    assert call(**kw, G=None, O=None, ws=None) == 0 and tl.last_error() == ""
+
+
+def test_workspace():
+    w = tl._lib.tgemm_orthogonalize_workspace_bytes
+    assert w(0, 4, 4) == w(1, 0, 4) == w(1, 4, 0) == 0
+    assert w(1, -1, 4) == w(1, 1 << 21, 4) == w(1 << 17, 4, 4) == -1
+    # X as two halves and its transpose twice, A and B, for padded sizes
+    assert w(1, 4096, 4096) >= 2 * (4 * 4096 * 4096 + 2 * 4096 * 4096)
+    assert w(3, 100, 200) == w(3, 200, 100) >= 3 * 2 * (4 * 100 * 200 + 2 * 100 * 100)
+
+
+def test_binding_refuses():
+    with pytest.raises(ValueError, match="GPU"):
+        tl.orthogonalize(torch.zeros(4, 4))
+
+
+def test_matrices_of_a_tensor():
+    t = torch.zeros(4, 3, 10, 8)
+    assert tl._matrices(t) == ((12, 10, 8), 8, 80)
+    assert tl._matrices(t[0, 0]) == ((1, 10, 8), 8, 80)
+    assert tl._matrices(t[..., :5]) == ((12, 10, 5), 8, 80)
+    assert tl._matrices(t[:, 1]) == ((4, 10, 8), 8, 240)
+    assert tl._matrices(t[:1, :, :1]) == ((3, 1, 8), 8, 80)
+    assert tl._matrices(t[:, :2]) is None          # uneven steps
+    assert tl._matrices(t.mT) is None              # columns first
+    assert tl._matrices(t[0, 0].expand(3, 10, 8)) is None
+    assert tl._matrices(t[0, 0, 0].expand(10, 8)) is None
+    assert tl._matrices(t[:0])[0] == (0, 10, 8)

@@ -67,7 +67,8 @@ EXPORTS = ("gemm_plan", "gemm_plan_variant", "gemm_run", "gemm_destroy", "tgemm_
            "gemm_plan_get_info", "gemm_variant_count", "gemm_variant_get", "tgemm_version",
            "tgemm_lds_read_probe", "tgemm_mfma_rate_probe", "gemm_workspace_bytes", "gemm_run_ws",
            "gemm_kernel_occupancy", "gemm_clock_slots", "gemm_run_clocked", "gemm_run_noalloc",
-           "tgemm_set_c_store_policy", "tgemm_fp8_quantize", "tgemm_fp8_gemm", "tgemm_fp8_gemm_kernel")
+           "tgemm_set_c_store_policy", "tgemm_fp8_quantize", "tgemm_fp8_gemm", "tgemm_fp8_gemm_kernel",
+           "tgemm_orthogonalize_workspace_bytes", "tgemm_orthogonalize")
 
 
 def _load():
@@ -122,6 +123,12 @@ def _load():
     lib.tgemm_fp8_gemm.restype = ctypes.c_int
     lib.tgemm_fp8_gemm_kernel.argtypes = [i64, i64, i64, i64, i64]
     lib.tgemm_fp8_gemm_kernel.restype = ctypes.c_char_p
+    f64 = ctypes.c_double
+    lib.tgemm_orthogonalize_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.tgemm_orthogonalize_workspace_bytes.restype = i64
+    lib.tgemm_orthogonalize.argtypes = [i64, i64, i64, i32, vp, i64, i64, vp, i64, i64, i32, ctypes.POINTER(f64), f64, vp,
+                                        i64, vp]
+    lib.tgemm_orthogonalize.restype = ctypes.c_int
     return lib
 
 
@@ -617,3 +624,91 @@ def linear_fp8(x, w, grad_dtype=None):
     if _linear_fn is None:
         _linear_fn = _linear_fp8_function()
     return _linear_fn.apply(x, w, grad_dtype)
+
+
+# ---- orthogonalised update ------------------------------------------------------
+
+ORTHOGONALIZE_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _matrices(t):
+    """(batch, rows, cols), row stride and batch stride of a tensor whose last
+    two axes are row-major matrices that do not overlap and whose leading axes
+    step evenly; None otherwise."""
+    rows, cols = t.shape[-2:]
+    batch = math.prod(t.shape[:-2])
+    if t.numel() == 0:
+        return (batch, rows, cols), max(cols, 1), rows * max(cols, 1)
+    if cols > 1 and t.stride(-1) != 1 or rows > 1 and t.stride(-2) < cols:
+        return None
+    ld = t.stride(-2) if rows > 1 else cols
+    step, span = None, 1  # stride of one matrix, matrices counted so far
+    for n, s in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if n == 1:
+            continue
+        if step is None:
+            step = s
+        elif s != step * span:
+            return None
+        span *= n
+    if step is None:
+        step = (rows - 1) * ld + cols
+    elif step < (rows - 1) * ld + cols:
+        return None
+    return (batch, rows, cols), ld, step
+
+
+def orthogonalize(G, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e-7, out=None):
+    """The orthogonalised update of the Muon optimiser: G with its singular
+    values brought near one by ``steps`` Newton-Schulz steps.
+
+    G: (..., rows, cols) float32, bfloat16 or float16 on the GPU, each matrix
+    by itself.  X = G / (|G| + eps) (Frobenius norm), then for each step
+    X <- a X + (b A + c A^2) X with A = X X^T (on the shorter side).
+    ``coefficients``: (a, b, c), or one such triple for each step; refused
+    where they would let singular values leave the range the kernels hold
+    (3.5).  Returns bfloat16 of G's shape, rounded once; ``out`` may be a
+    preallocated bfloat16 tensor of evenly spaced row-major matrices (G itself
+    included).  The workspace comes from torch's allocator on the current
+    stream.
+    """
+    import torch
+    if not G.is_cuda:
+        raise ValueError("G must be a GPU tensor")
+    code = _real_code(G, "G")
+    if G.dim() < 2:
+        raise ValueError("G must have at least 2 dimensions")
+    flat = list(coefficients)
+    if len(flat) == 3 and not hasattr(flat[0], "__len__"):
+        flat = flat * int(steps)
+    else:
+        if len(flat) != steps or any(len(c) != 3 for c in flat):
+            raise ValueError("coefficients must be (a, b, c) or one such triple for each of the %d steps" % steps)
+        flat = [v for c in flat for v in c]
+    coef = (ctypes.c_double * max(len(flat), 1))(*map(float, flat))
+    if out is None:
+        out = torch.empty(G.shape, dtype=torch.bfloat16, device=G.device)
+    elif out.dtype != torch.bfloat16 or out.shape != G.shape or out.device != G.device:
+        raise ValueError("out must be a bfloat16 tensor of shape %s on %s" % (tuple(G.shape), G.device))
+    place = _matrices(out)
+    if place is None:
+        raise ValueError("out must hold evenly spaced row-major matrices (shape %s, strides %s)" % (
+            tuple(out.shape), out.stride()))
+    if _matrices(G) is None:
+        G = G.contiguous()
+    (batch, rows, cols), ldg, stride_g = _matrices(G)
+    _, ldo, stride_o = place
+    need = _lib.tgemm_orthogonalize_workspace_bytes(batch, rows, cols)
+    if need < 0:
+        raise ValueError("G of shape %s is out of range (2^20 rows and columns, 2^16 matrices)" % (tuple(G.shape),))
+    with torch.cuda.device(G.device):
+        # stream-ordered: the block returns to torch's pool for this stream
+        # when `ws` is dropped, after the work queued here
+        ws = torch.empty(need + 256, dtype=torch.uint8, device=G.device)
+        base = (ws.data_ptr() + 255) // 256 * 256
+        rc = _lib.tgemm_orthogonalize(batch, rows, cols, code, G.data_ptr(), ldg, stride_g, out.data_ptr(), ldo, stride_o,
+                                      int(steps), coef, float(eps), base, need,
+                                      torch.cuda.current_stream(G.device).cuda_stream)
+    if rc != OK:
+        raise TgemmError(rc, last_error())
+    return out
