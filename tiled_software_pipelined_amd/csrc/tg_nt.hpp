@@ -116,7 +116,9 @@ struct NtGemm {
     static constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N;
     static constexpr int FM = WTM / 32, FN = WTN / 32;
     static constexpr int A_BYTES = BM * ROW, B_BYTES = BN * ROW;
-    static constexpr int S_BYTES = Tr::SCALED ? BM + BN : 0;
+    // scales in a slot: 256 bytes for each wave's copy, of which the first
+    // 4 S_PER count (see copy_one)
+    static constexpr int S_BYTES = Tr::SCALED ? 256 * WAVES : 0;
     static constexpr int SLOT = A_BYTES + B_BYTES + S_BYTES;
     static constexpr int LDS_BYTES = STAGES * SLOT;
     static constexpr int A_PER = BM * 8 / NT, B_PER = BN * 8 / NT;
@@ -134,7 +136,8 @@ struct NtGemm {
     static_assert(FM == 1 || FM == 2 || FM == 4, "scale bytes of a lane are read at once");
     static_assert(FN == 1 || FN == 2 || FN == 4, "scale bytes of a lane are read at once");
     static_assert((BM * 8) % NT == 0 && (BN * 8) % NT == 0, "even split of the copies");
-    static_assert(!Tr::SCALED || ((BM / 4) % S_PER == 0 && S_PER <= 64), "a wave's scale copy is of one operand");
+    static_assert(!Tr::SCALED || ((BM / 4) % S_PER == 0 && S_PER <= 64 && (S_PER & (S_PER - 1)) == 0),
+                  "a wave's scale copy is of one operand");
     static_assert(STAGES >= 2 && LDS_BYTES <= 160 * 1024, "LDS per CU");
     static_assert(N_CP * (STAGES - 2) <= 63, "vmcnt range");
     static_assert(SLOT % 16 == 0, "slots stay aligned");
@@ -171,7 +174,7 @@ struct NtGemm {
             o.b[q] = (uint32_t)((int64_t)(min(n0 + row_at<WTN>(p), g.N - 1) - n0) * g.ldb + c * 16);
         }
         if constexpr (Tr::SCALED) {
-            const int d = wave * S_PER + lane;  // dword of the slot's scales: A's, then B's
+            const int d = wave * S_PER + lane % S_PER;  // dword of the tile's scales: A's, then B's
             o.s = d < BM / 4 ? min(m0 + 4 * d, (g.M - 1) & ~3) : min(n0 + 4 * (d - BM / 4), (g.N - 1) & ~3);
         }
     }
@@ -192,21 +195,23 @@ struct NtGemm {
         return r;
     }
 
-    // copy number i of a slice (0 <= i < N_CP)
+    // copy number i of a slice (0 <= i < N_CP).  The scales: S_PER dwords for
+    // each wave, which every group of S_PER lanes fetches again, so that the
+    // copy needs no branch (one splits the K loop for the compiler, which
+    // then spills fragments) and no wave copies more than another (one wait
+    // count serves all).
     __device__ static __forceinline__ void copy_one(int i, TG_LDS char* slot, const Offsets& o, const Source& s,
-                                                    int wave, int lane) {
+                                                    int wave) {
         const uint32_t lds = (uint32_t)(uintptr_t)slot;
         if (i < A_PER) copy16_to_lds(lds + (i * NT + wave * 64) * 16, o.a[i < A_PER ? i : 0], s.a);
         else if (i < A_PER + B_PER)
             copy16_to_lds(lds + A_BYTES + ((i - A_PER) * NT + wave * 64) * 16, o.b[i - A_PER < B_PER ? i - A_PER : 0],
                           s.b);
-        else if (lane < S_PER)
-            copy4_to_lds(lds + A_BYTES + B_BYTES + wave * (S_PER * 4), o.s, s.s);
+        else copy4_to_lds(lds + A_BYTES + B_BYTES + wave * 256, o.s, s.s);
     }
-    __device__ static __forceinline__ void copy_slice(TG_LDS char* slot, const Offsets& o, const Source& s, int wave,
-                                                      int lane) {
+    __device__ static __forceinline__ void copy_slice(TG_LDS char* slot, const Offsets& o, const Source& s, int wave) {
 #pragma unroll
-        for (int i = 0; i < N_CP; ++i) copy_one(i, slot, o, s, wave, lane);
+        for (int i = 0; i < N_CP; ++i) copy_one(i, slot, o, s, wave);
     }
 
     // ---- fragments ---------------------------------------------------------
@@ -214,8 +219,11 @@ struct NtGemm {
         Frag a[FM], b[FN];
         int sa, sb;
     };
+    // The F scale bytes of rows at, at + 1 .. (at a multiple of F) of the
+    // tile's BM + BN rows.
     template <int F>
-    __device__ static __forceinline__ int read_scales(const TG_LDS char* p) {
+    __device__ static __forceinline__ int read_scales(const TG_LDS char* slot, int at) {
+        const TG_LDS char* p = slot + A_BYTES + B_BYTES + at / (4 * S_PER) * 256 + at % (4 * S_PER);
         if constexpr (F == 4) return *reinterpret_cast<const TG_LDS int32_t*>(p);
         else if constexpr (F == 2) return *reinterpret_cast<const TG_LDS uint16_t*>(p);
         else return *reinterpret_cast<const TG_LDS uint8_t*>(p);
@@ -233,9 +241,8 @@ struct NtGemm {
     __device__ static __forceinline__ void read_one(Frags& f, const TG_LDS char* slot, int s, int r, int wm0, int wn0,
                                                     int lane) {
         if (r < NS) {
-            const TG_LDS char* sc = slot + A_BYTES + B_BYTES;
-            if (r == 0) f.sa = read_scales<FM>(sc + wm0 + FM * (lane & 31));
-            else f.sb = read_scales<FN>(sc + BM + wn0 + FN * (lane & 31));
+            if (r == 0) f.sa = read_scales<FM>(slot, wm0 + FM * (lane & 31));
+            else f.sb = read_scales<FN>(slot, BM + wn0 + FN * (lane & 31));
             return;
         }
         const int q = (r - NS) / RB, h = (r - NS) % RB;
@@ -298,7 +305,7 @@ struct NtGemm {
 #pragma unroll
             for (int m = mem_begin(k, BAR_K, TOTAL); m < mem_begin(k + 1, BAR_K, TOTAL); ++m) {
                 if (m < NREAD) read_one(nxt, rslot, rs, m, wm0, wn0, lane);
-                else copy_one(m - NREAD, cslot, off, src, wave, lane);
+                else copy_one(m - NREAD, cslot, off, src, wave);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -337,7 +344,7 @@ struct NtGemm {
                 read_frags(F[s], next, s, wm0, wn0, lane);
             }
             if constexpr (COPY) {
-                if (s == 0) copy_slice(cur, off, src, wave, lane);
+                if (s == 0) copy_slice(cur, off, src, wave);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -375,7 +382,7 @@ struct NtGemm {
                 const uint8_t* p = tid < BM / 4
                     ? g.sa + (int64_t)full * g.ldsa + min(m0 + 4 * tid, (g.M - 1) & ~3)
                     : g.sb + (int64_t)full * g.ldsb + min(n0 + 4 * (tid - BM / 4), (g.N - 1) & ~3);
-                *reinterpret_cast<TG_LDS int32_t*>(slot + A_BYTES + B_BYTES + 4 * tid) =
+                *reinterpret_cast<TG_LDS int32_t*>(slot + A_BYTES + B_BYTES + tid / S_PER * 256 + tid % S_PER * 4) =
                     *reinterpret_cast<const int32_t*>(p);
             }
         }
@@ -394,7 +401,7 @@ struct NtGemm {
         Offsets off;
         offsets(off, g, m0, n0, wave, lane);
         auto slot = [&](int t) { return smem + (t % STAGES) * SLOT; };
-        auto copy = [&](int t) { copy_slice(slot(t), off, source(g, m0, n0, t, wave), wave, lane); };
+        auto copy = [&](int t) { copy_slice(slot(t), off, source(g, m0, n0, t, wave), wave); };
         const Source none{g.a, g.b, g.sa};
         // prologue: slices 0 .. STAGES-2 in flight; with slice 0 in LDS, start
         // slice STAGES-1 and read the first fragments
