@@ -11,6 +11,7 @@ struct Fp8Args {
     uint16_t* C;
     int64_t ldc;
     int32_t tiles_m, tiles_n;
+    int32_t stream;  // 1: C's rows are whole cache lines, written past the L2
 };
 
 typedef void (*Fp8Fn)(Fp8Args);
@@ -32,6 +33,16 @@ const Fp8Kernel* fp8_kernels_e5m2_e5m2();
 
 // bfloat16 bits, to nearest even: the one rounding of a result
 __device__ __forceinline__ uint16_t bf16_bits(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
+
+// N results past the L2: C is not read here, and the launch ends sooner than
+// with 32 MB of it to be written back at its end (e4m3 4096^3 57 -> 53 us).
+template <int N>
+__device__ __forceinline__ void store_stream(uint16_t* dst, const uint16_t (&v)[N]) {
+    typedef uint32_t Words __attribute__((ext_vector_type(N >= 2 ? N / 2 : 1)));
+    Words w;
+    __builtin_memcpy(&w, v, sizeof v);
+    __builtin_nontemporal_store(w, reinterpret_cast<Words*>(dst));
+}
 
 // Tiled kernel.
 template <class G>
@@ -60,7 +71,8 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g) {
             for (int j = 0; j < G::FN; ++j) v[j] = bf16_bits(acc[i][j][r]);
             uint16_t* dst = g.C + (int64_t)m * g.ldc + n;
             if (m < g.op.M) {
-                if (whole) __builtin_memcpy(dst, v, sizeof v);
+                if (G::FN >= 2 && g.stream && whole) store_stream(dst, v);
+                else if (whole) __builtin_memcpy(dst, v, sizeof v);
                 else {
 #pragma unroll
                     for (int j = 0; j < G::FN; ++j)
@@ -182,11 +194,15 @@ __global__ __launch_bounds__(64 * NW) void fp8_rows_kernel(Fp8Args g) {
 template <int FA, int FB>
 const Fp8Kernel* fp8_kernel_table() {
     typedef NtF8<FA, FB> Tr;
-    typedef NtGemm<Tr, 256, 256, 2, 4, 2, false> G256;
+    // 256 x 256: four waves of 128 x 128, one a SIMD.  Against eight of 128 x
+    // 64 they read a third less from LDS for the same matrix instructions,
+    // which leaves the power budget a higher clock (8192^3 e4m3 395 us against
+    // 425).  In the steady loop the matrix cores are busy 91 % of the cycles.
+    typedef NtGemm<Tr, 256, 256, 2, 2, 2, false> G256;
     typedef NtGemm<Tr, 128, 128, 2, 2, 4, true> G128;
     typedef NtGemm<Tr, 64, 64, 2, 2, 8, true> G64;
     static const Fp8Kernel table[PICK_COUNT] = {
-        {fp8_tile_kernel<G256>, G256::BM, G256::BN, G256::NT, "t256x256x128_w2x4_s2"},
+        {fp8_tile_kernel<G256>, G256::BM, G256::BN, G256::NT, "t256x256x128_w2x2_s2"},
         {fp8_tile_kernel<G128>, G128::BM, G128::BN, G128::NT, "t128x128x128_w2x2_s4_slice"},
         {fp8_tile_kernel<G64>, G64::BM, G64::BN, G64::NT, "t64x64x128_w2x2_s8_slice"},
         {fp8_rows_kernel<FA, FB, 1, 8, 4>, 16, 16, 512, "rows16_w8"},

@@ -99,6 +99,7 @@ int tgemm_fp8_gemm(int64_t M, int64_t N, int64_t K, int32_t fmt_a, const void* A
     g.ldc = ldc;
     g.tiles_m = (int32_t)tiles_m;
     g.tiles_n = (int32_t)tiles_n;
+    g.stream = (uintptr_t)C % 128 == 0 && ldc % 64 == 0;
     void* args[] = {&g};
     const hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(k.fn), dim3((unsigned)(tiles_m * tiles_n)),
                                            dim3(k.threads), args, 0, static_cast<hipStream_t>(stream));

@@ -348,7 +348,7 @@ static OrthoKernels ortho_kernels() {
 
 static const OrthoKernels* ortho_table() {
     static const OrthoKernels t[3] = {
-        ortho_kernels<NtGemm<NtF16, 256, 256, 2, 4, 2, false>>(),
+        ortho_kernels<NtGemm<NtF16, 256, 256, 2, 2, 2, false>>(),
         ortho_kernels<NtGemm<NtF16, 128, 128, 2, 2, 4, true>>(),
         ortho_kernels<NtGemm<NtF16, 64, 64, 2, 2, 8, true>>(),
     };
