@@ -133,8 +133,8 @@ struct NtGemm {
     typedef f32x16 Acc;
 
     static_assert(BM % (32 * WAVES_M) == 0 && BN % (32 * WAVES_N) == 0, "wave tile");
-    static_assert(FM == 1 || FM == 2 || FM == 4, "scale bytes of a lane are read at once");
-    static_assert(FN == 1 || FN == 2 || FN == 4, "scale bytes of a lane are read at once");
+    static_assert(!Tr::SCALED || ((FM == 1 || FM == 2 || FM == 4) && (FN == 1 || FN == 2 || FN == 4)),
+                  "scale bytes of a lane are read at once");
     static_assert((BM * 8) % NT == 0 && (BN * 8) % NT == 0, "even split of the copies");
     static_assert(!Tr::SCALED || ((BM / 4) % S_PER == 0 && S_PER <= 64 && (S_PER & (S_PER - 1)) == 0),
                   "a wave's scale copy is of one operand");

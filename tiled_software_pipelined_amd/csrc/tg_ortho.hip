@@ -30,9 +30,9 @@
 // All products have both operands K-contiguous: X X^T; A' A' (symmetric); and
 // B' X with X's transpose, which the update writes beside X, as its second
 // operand.  A and B' are symmetric: tiles on and below the diagonal are
-// computed and written twice.  The workspace's matrices are padded to whole
+// computed and written twice.  The workspace's X is padded to whole update
 // tiles with zeros, which every product keeps zero, so only the first and the
-// last kernel meet edges.
+// last kernel meet the edges of G and O.
 #include <hip/hip_runtime.h>
 
 #include <climits>
@@ -61,8 +61,8 @@ struct OrthoArgs {
     uint16_t* out;         // bfloat16 result
     int64_t ldo, stride_o;
     int32_t mp, np, m, n, tall;
-    int32_t tiles;         // tiles of one matrix
-    int32_t tiles_m, tiles_n;
+    int32_t tiles;             // tiles of one matrix
+    int32_t tiles_m, tiles_n;  // of the update
     float ca, cb, cc;
 };
 
@@ -111,11 +111,13 @@ __device__ __forceinline__ NtOperands ortho_operands(const _Float16* a, const _F
                       rows_a, rows_b, 2 * k, 2 * (int64_t)k, 2 * (int64_t)k, 0, 0};
 }
 
-// Write the wave's block of a symmetric matrix, and its mirror image where the
-// tile lies below the diagonal.  value(i, j, r): element of register r.
+// Write the wave's block of a symmetric matrix (ld rows), and its mirror image
+// where the tile lies below the diagonal.  row(i, r, row, out): the FN values
+// of register r in fragments (i, ..).  Tiles may reach past the last row.
 template <class G, class F>
 __device__ __forceinline__ void store_symmetric(_Float16* S, int ld, const OrthoTile<G>& t, F value) {
-    const int mb = t.m0 + t.wm0, nb = t.n0 + t.wn0;
+    const int mb = t.m0 + t.wm0, nb = t.n0 + t.wn0, n = nb + G::col_of(0, t.lane);
+    const bool inside = t.m0 + G::BM <= ld;  // then t.n0 + BN too: tn <= tm
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         Halves<4 * G::FM> col[G::FN];
@@ -123,20 +125,31 @@ __device__ __forceinline__ void store_symmetric(_Float16* S, int ld, const Ortho
         for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int i = 0; i < G::FM; ++i) {
+                const int m = mb + G::row_of(i, 4 * q + e, t.lane);
                 Halves<G::FN> row;
+                value(i, 4 * q + e, min(m, ld - 1), row);
 #pragma unroll
-                for (int j = 0; j < G::FN; ++j) {
-                    row.v[j] = (_Float16)value(i, j, 4 * q + e);
-                    col[j].v[G::FM * e + i] = row.v[j];
+                for (int j = 0; j < G::FN; ++j) col[j].v[G::FM * e + i] = row.v[j];
+                _Float16* dst = S + (int64_t)m * ld + n;
+                if (inside) __builtin_memcpy(dst, &row, sizeof row);
+                else {
+#pragma unroll
+                    for (int j = 0; j < G::FN; ++j)
+                        if (m < ld && n + j < ld) dst[j] = row.v[j];
                 }
-                __builtin_memcpy(S + (int64_t)(mb + G::row_of(i, 4 * q + e, t.lane)) * ld + nb + G::col_of(0, t.lane),
-                                 &row, sizeof row);
             }
         if (t.tm != t.tn) {
+            const int m = mb + quad_row<G::FM>(q, t.lane);
 #pragma unroll
-            for (int j = 0; j < G::FN; ++j)
-                __builtin_memcpy(S + (int64_t)(nb + G::col_of(j, t.lane)) * ld + mb + quad_row<G::FM>(q, t.lane),
-                                 &col[j], sizeof col[j]);
+            for (int j = 0; j < G::FN; ++j) {
+                _Float16* dst = S + (int64_t)(n + j) * ld + m;
+                if (inside) __builtin_memcpy(dst, &col[j], sizeof col[j]);
+                else {
+#pragma unroll
+                    for (int k = 0; k < 4 * G::FM; ++k)
+                        if (n + j < ld && m + k < ld) dst[k] = col[j].v[k];
+                }
+            }
         }
     }
 }
@@ -151,11 +164,15 @@ __global__ __launch_bounds__(G::NT) void ortho_gram_kernel(OrthoArgs g) {
     G::product(ortho_operands(g.hi + x, g.hi + x, g.mp, g.mp, g.np), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0,
                t.wn0, t.lane, t.wave);
     float* d = g.d + (int64_t)t.z * g.mp;
-    store_symmetric<G>(g.a + s, g.mp, t, [&](int i, int j, int r) {
-        const int row = t.m0 + t.wm0 + G::row_of(i, r, t.lane), col = t.n0 + t.wn0 + G::col_of(j, t.lane);
-        const float v = acc[i][j][r] * (1.0f / (ONE * ONE));
-        if (row == col) d[row] = v;
-        return row == col ? 0.0f : v * ONE;
+    const int n = t.n0 + t.wn0 + G::col_of(0, t.lane);
+    store_symmetric<G>(g.a + s, g.mp, t, [&](int i, int r, int m, Halves<G::FN>& out) {
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j) {
+            const float v = acc[i][j][r] * (1.0f / (ONE * ONE));
+            const bool diagonal = m == n + j;
+            if (diagonal) d[m] = v;
+            out.v[j] = (_Float16)(diagonal ? 0.0f : v * ONE);
+        }
     });
 }
 
@@ -171,15 +188,26 @@ __global__ __launch_bounds__(G::NT) void ortho_poly_kernel(OrthoArgs g) {
                t.wave);
     const float* d = g.d + (int64_t)t.z * g.mp;
     float* e = g.e + (int64_t)t.z * g.mp;
+    const int n = t.n0 + t.wn0 + G::col_of(0, t.lane);
+    const bool whole = n + G::FN <= g.mp;
     float dn[G::FN];
 #pragma unroll
-    for (int j = 0; j < G::FN; ++j) dn[j] = d[t.n0 + t.wn0 + G::col_of(j, t.lane)];
-    store_symmetric<G>(g.b + s, g.mp, t, [&](int i, int j, int r) {
-        const int row = t.m0 + t.wm0 + G::row_of(i, r, t.lane), col = t.n0 + t.wn0 + G::col_of(j, t.lane);
-        const float dm = d[row], sq = acc[i][j][r] * (1.0f / (ONE * ONE));
-        const float av = (float)A[(int64_t)row * g.mp + col] * (1.0f / ONE);
-        if (row == col) e[row] = g.cb * dm + g.cc * (dm * dm + sq);
-        return row == col ? 0.0f : (g.cb * av + g.cc * ((dm + dn[j]) * av + sq)) * ONE;
+    for (int j = 0; j < G::FN; ++j) dn[j] = d[min(n + j, g.mp - 1)];
+    store_symmetric<G>(g.b + s, g.mp, t, [&](int i, int r, int m, Halves<G::FN>& out) {
+        const float dm = d[m];
+        Halves<G::FN> a;
+        if (whole) __builtin_memcpy(&a, A + (int64_t)m * g.mp + n, sizeof a);
+        else {
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j) a.v[j] = A[(int64_t)m * g.mp + min(n + j, g.mp - 1)];
+        }
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j) {
+            const float sq = acc[i][j][r] * (1.0f / (ONE * ONE)), av = (float)a.v[j] * (1.0f / ONE);
+            const bool diagonal = m == n + j;
+            if (diagonal) e[m] = g.cb * dm + g.cc * (dm * dm + sq);
+            out.v[j] = (_Float16)(diagonal ? 0.0f : (g.cb * av + g.cc * ((dm + dn[j]) * av + sq)) * ONE);
+        }
     });
 }
 
@@ -258,125 +286,200 @@ __global__ __launch_bounds__(G::NT) void ortho_update_kernel(OrthoArgs g) {
 struct OrthoInArgs {
     const void* G;
     int64_t ldg, stride_g;
-    int32_t dtype, rows, cols;  // of G
-    double* part;               // PARTS sums of squares for each matrix
+    int32_t rows, cols;  // of G
+    double* part;        // PARTS sums of squares for each matrix
     _Float16 *hi, *lo, *xt;
     int32_t mp, np, tall;
     double eps;
 };
 
-constexpr int PARTS = 64;
+constexpr int PARTS = 256;
 
-__device__ __forceinline__ float element(const void* G, int32_t dtype, int64_t at) {
-    if (dtype == TGEMM_F32) return static_cast<const float*>(G)[at];
-    const uint16_t v = static_cast<const uint16_t*>(G)[at];
-    return dtype == TGEMM_BF16 ? __builtin_bit_cast(float, (uint32_t)v << 16)
-                               : (float)__builtin_bit_cast(_Float16, v);
+struct EF32 {
+    typedef float T;
+    __device__ static __forceinline__ float up(float x) { return x; }
+};
+struct EBF16 {
+    typedef uint16_t T;
+    __device__ static __forceinline__ float up(uint16_t x) { return __builtin_bit_cast(float, (uint32_t)x << 16); }
+};
+struct EF16 {
+    typedef uint16_t T;
+    __device__ static __forceinline__ float up(uint16_t x) { return (float)__builtin_bit_cast(_Float16, x); }
+};
+
+// Elements c .. c + 7 of a row as floats, zero from `end` on.
+template <class E>
+__device__ __forceinline__ void load8(float (&v)[8], const typename E::T* row, int c, int end) {
+    typedef typename E::T T;
+    union { T t[8]; i32x4 w[sizeof(T) / 2]; } u;
+    if (c + 8 <= end) {
+#pragma unroll
+        for (int h = 0; h < (int)sizeof(T) / 2; ++h) u.w[h] = load16(row + c + 16 / (int)sizeof(T) * h);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u.t[k] = load_or_zero(row + c + k, c + k < end);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = E::up(u.t[k]);
 }
 
-// Workgroup (p, z): part p of matrix z's sum of squares, in double (squares
-// of any float fit), in a fixed order.
+// Workgroup (p, z): pieces p, p + PARTS .. of matrix z, a piece 2048 elements
+// of a row; its sum of squares in double (squares of any float fit), always
+// in the same order.
+template <class E>
 __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoInArgs g) {
-    __shared__ double sums[256];
+    __shared__ double sums[4];
     const int p = blockIdx.x % PARTS, z = blockIdx.x / PARTS;
+    const int per = (g.cols + 2047) / 2048;
+    const int64_t pieces = (int64_t)g.rows * per;
     double s = 0.0;
-    for (int r = p; r < g.rows; r += PARTS) {
-        const int64_t row = (int64_t)z * g.stride_g + (int64_t)r * g.ldg;
-        for (int c = threadIdx.x; c < g.cols; c += 256) {
-            const double v = element(g.G, g.dtype, row + c);
-            s += v * v;
+    for (int64_t i = p; i < pieces; i += PARTS) {
+        const int r = (int)(i / per), c = (int)(i % per) * 2048 + 8 * threadIdx.x;
+        if (c < g.cols) {
+            float v[8];
+            load8<E>(v, static_cast<const typename E::T*>(g.G) + (int64_t)z * g.stride_g + (int64_t)r * g.ldg, c, g.cols);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += (double)v[k] * (double)v[k];
         }
     }
-    sums[threadIdx.x] = s;
-    for (int w = 128; w > 0; w >>= 1) {
-        __syncthreads();
-        if (threadIdx.x < w) sums[threadIdx.x] += sums[threadIdx.x + w];
-    }
-    if (threadIdx.x == 0) g.part[(int64_t)z * PARTS + p] = sums[0];
+    for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
+    if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) g.part[(int64_t)z * PARTS + p] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 }
 
 // A workgroup takes a 64 x 64 block of X (padded): X = G / (|G| + eps) times
-// 2^12 as hi + lo, and its transpose.
+// 2^12 as hi + lo, and its transpose.  A thread loads 8 elements of two rows
+// of G, and writes 8 of each image.
+template <class E>
 __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoInArgs g) {
     __shared__ float tile[64][65];
-    __shared__ double factor;
+    __shared__ double sums[4];
+    const int tid = threadIdx.x;
     const int tn = g.np / 64, per = tn * (g.mp / 64);
     const int z = blockIdx.x / per, b = blockIdx.x - z * per;
     const int m0 = b / tn * 64, n0 = b % tn * 64;
-    if (threadIdx.x < 64) {
-        double s = g.part[(int64_t)z * PARTS + threadIdx.x];
-        for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
-        if (threadIdx.x == 0) factor = (double)ONE / (sqrt(s) + g.eps);
-    }
-    __syncthreads();
-    const double f = factor;  // in double: 1 / |G| may leave float's range
     // rows and columns of G: those of X, or the other way round
     const int r0 = g.tall ? n0 : m0, c0 = g.tall ? m0 : n0;
-    for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-        const int r = i >> 6, c = i & 63;
-        float v = 0.0f;
-        if (r0 + r < g.rows && c0 + c < g.cols)
-            v = (float)(element(g.G, g.dtype, (int64_t)z * g.stride_g + (int64_t)(r0 + r) * g.ldg + c0 + c) * f);
-        tile[r][c] = v;
+    float v[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = r0 + 32 * h + (tid >> 3);
+        load8<E>(v[h], static_cast<const typename E::T*>(g.G) + (int64_t)z * g.stride_g + (int64_t)min(r, g.rows - 1) * g.ldg,
+                 c0 + 8 * (tid & 7), r < g.rows ? g.cols : 0);
     }
+    double s = g.part[(int64_t)z * PARTS + tid];
+    static_assert(PARTS == 256, "a part for each thread");
+    for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
+    if ((tid & 63) == 0) sums[tid >> 6] = s;
+    __syncthreads();
+    // in double: 1 / |G| may leave float's range
+    const double f = (double)ONE / (sqrt((sums[0] + sums[1]) + (sums[2] + sums[3])) + g.eps);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) tile[32 * h + (tid >> 3)][8 * (tid & 7) + k] = (float)(v[h][k] * f);
     __syncthreads();
     const int64_t x = (int64_t)z * g.mp * g.np;
-    for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-        const int r = i >> 6, c = i & 63;
-        const float v = g.tall ? tile[c][r] : tile[r][c];
-        const _Float16 h = (_Float16)v;
-        g.hi[x + (int64_t)(m0 + r) * g.np + n0 + c] = h;
-        g.lo[x + (int64_t)(m0 + r) * g.np + n0 + c] = (_Float16)(v - (float)h);
-        const float w = g.tall ? tile[r][c] : tile[c][r];
-        g.xt[x + (int64_t)(n0 + r) * g.mp + m0 + c] = (_Float16)w;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = 32 * h + (tid >> 3), c = 8 * (tid & 7);
+        Halves<8> hi, lo, xt;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float y = g.tall ? tile[c + k][r] : tile[r][c + k];
+            hi.v[k] = (_Float16)y;
+            lo.v[k] = (_Float16)(y - (float)hi.v[k]);
+            xt.v[k] = (_Float16)(g.tall ? tile[r][c + k] : tile[c + k][r]);
+        }
+        __builtin_memcpy(g.hi + x + (int64_t)(m0 + r) * g.np + n0 + c, &hi, 16);
+        __builtin_memcpy(g.lo + x + (int64_t)(m0 + r) * g.np + n0 + c, &lo, 16);
+        __builtin_memcpy(g.xt + x + (int64_t)(n0 + r) * g.mp + m0 + c, &xt, 16);
     }
 }
 
 // ---- host ------------------------------------------------------------------------
 
 typedef void (*OrthoFn)(OrthoArgs);
+typedef void (*OrthoInFn)(OrthoInArgs);
+
+// Kernels of the symmetric products (gram, poly) and of the update (middle
+// steps, last), by tile.  cost: time of one round, a tile on each of the 256
+// compute units, in that of 256 x 256 tiles.
 struct OrthoKernels {
     int tile, threads;
-    OrthoFn gram, poly, update, last;
+    OrthoFn first, second;
+    double cost;
 };
 
 template <class G>
-static OrthoKernels ortho_kernels() {
-    return OrthoKernels{G::BM, G::NT, ortho_gram_kernel<G>, ortho_poly_kernel<G>, ortho_update_kernel<G, false>,
-                        ortho_update_kernel<G, true>};
+static OrthoKernels symmetric_kernels(double cost) {
+    return OrthoKernels{G::BM, G::NT, ortho_gram_kernel<G>, ortho_poly_kernel<G>, cost};
+}
+template <class G>
+static OrthoKernels update_kernels(double cost) {
+    return OrthoKernels{G::BM, G::NT, ortho_update_kernel<G, false>, ortho_update_kernel<G, true>, cost};
 }
 
-static const OrthoKernels* ortho_table() {
-    static const OrthoKernels t[3] = {
-        ortho_kernels<NtGemm<NtF16, 256, 256, 2, 2, 2, false>>(),
-        ortho_kernels<NtGemm<NtF16, 128, 128, 2, 2, 4, true>>(),
-        ortho_kernels<NtGemm<NtF16, 64, 64, 2, 2, 8, true>>(),
-    };
+typedef NtGemm<NtF16, 256, 256, 2, 4, 2, false> Ortho256;
+typedef NtGemm<NtF16, 192, 192, 2, 2, 3, false> Ortho192;
+typedef NtGemm<NtF16, 128, 128, 2, 2, 4, true> Ortho128;
+typedef NtGemm<NtF16, 64, 64, 2, 2, 8, true> Ortho64;
+
+static const OrthoKernels* symmetric_table(int* count) {
+    static const OrthoKernels t[4] = {symmetric_kernels<Ortho256>(1.0), symmetric_kernels<Ortho192>(0.6),
+                                      symmetric_kernels<Ortho128>(0.33), symmetric_kernels<Ortho64>(0.13)};
+    *count = 4;
+    return t;
+}
+static const OrthoKernels* update_table(int* count) {
+    static const OrthoKernels t[3] = {update_kernels<Ortho256>(1.0), update_kernels<Ortho128>(0.33),
+                                      update_kernels<Ortho64>(0.13)};
+    *count = 3;
     return t;
 }
 
 struct OrthoPlan {
     int64_t m, n, mp, np;
     const OrthoKernels *sym, *upd;
+    int64_t tri;  // symmetric tiles of one matrix
     int64_t off_hi, off_lo, off_t0, off_t1, off_a, off_b, off_d, off_e, off_part, bytes;
 };
 
 static int64_t up_to(int64_t v, int64_t step) { return (v + step - 1) / step * step; }
 
-// Tiles, and where things stand in the workspace.
+// The cheapest kernel of a table for tiles(size) workgroups.
+template <class F>
+static const OrthoKernels* cheapest(const OrthoKernels* t, int count, F tiles) {
+    const OrthoKernels* best = t;
+    double least = 0.0;
+    for (int i = 0; i < count; ++i) {
+        const double c = t[i].cost * (double)((tiles(t[i].tile) + 255) / 256);
+        if (i == 0 || c < least) {
+            least = c;
+            best = t + i;
+        }
+    }
+    return best;
+}
+
+// Tiles, and where things stand in the workspace.  X is padded to whole
+// update tiles; symmetric tiles may reach past its rows.
 static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     OrthoPlan p{};
     p.m = rows < cols ? rows : cols;
     p.n = rows < cols ? cols : rows;
-    const OrthoKernels* t = ortho_table();
-    auto tiles = [&](int64_t v, int e) { return (v + t[e].tile - 1) / t[e].tile; };
-    auto grid = [&](int e) { return batch * tiles(p.m, e) * tiles(p.n, e); };
-    auto tri = [&](int e) { return batch * tiles(p.m, e) * (tiles(p.m, e) + 1) / 2; };
-    p.upd = grid(0) >= 192 ? &t[0] : grid(1) >= 128 ? &t[1] : &t[2];
-    p.sym = tri(0) >= 192 ? &t[0] : tri(1) >= 128 ? &t[1] : &t[2];
-    const int64_t tile = p.upd->tile > p.sym->tile ? p.upd->tile : p.sym->tile;
-    p.mp = up_to(p.m, tile);
-    p.np = up_to(p.n, tile);
+    auto tiles = [](int64_t v, int64_t tile) { return (v + tile - 1) / tile; };
+    int count;
+    const OrthoKernels* t = update_table(&count);
+    p.upd = cheapest(t, count, [&](int64_t tile) { return batch * tiles(p.m, tile) * tiles(p.n, tile); });
+    p.mp = up_to(p.m, p.upd->tile);
+    p.np = up_to(p.n, p.upd->tile);
+    auto tri = [&](int64_t tile) { return tiles(p.mp, tile) * (tiles(p.mp, tile) + 1) / 2; };
+    t = symmetric_table(&count);
+    p.sym = cheapest(t, count, [&](int64_t tile) { return batch * tri(tile); });
+    p.tri = tri(p.sym->tile);
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t o = at;
@@ -490,11 +593,11 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
         set_error("workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)p.bytes);
         return TGEMM_E_ARG;
     }
-    const int64_t ut = p.upd->tile, st = p.sym->tile;
-    const int64_t tri = (p.mp / st) * (p.mp / st + 1) / 2, upd = (p.mp / ut) * (p.np / ut);
+    const int64_t ut = p.upd->tile, tri = p.tri, upd = (p.mp / ut) * (p.np / ut);
     const int64_t load = (p.mp / 64) * (p.np / 64);
     if (batch * tri > INT_MAX || batch * upd > INT_MAX || batch * load > INT_MAX ||
-        (p.upd->tile - 1) * 2 * (p.np > p.mp ? p.np : p.mp) + 128 > INT64_C(0xffffffff)) {
+        255 * 2 * p.np + 128 > INT64_C(0xffffffff)) {  // a tile's copies take 32-bit offsets
+
         set_error("too many tiles");
         return TGEMM_E_ARG;
     }
@@ -507,7 +610,6 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     in.G = G;
     in.ldg = ldg;
     in.stride_g = stride_g;
-    in.dtype = dtype;
     in.rows = (int32_t)rows;
     in.cols = (int32_t)cols;
     in.part = (double*)(ws + p.off_part);
@@ -518,9 +620,16 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     in.np = (int32_t)p.np;
     in.tall = rows > cols;
     in.eps = eps;
-    hipLaunchKernelGGL(ortho_norm_kernel, dim3((unsigned)(PARTS * batch)), dim3(256), 0, s, in);
-    hipLaunchKernelGGL(ortho_load_kernel, dim3((unsigned)(batch * load)), dim3(256), 0, s, in);
-    hipError_t err = hipGetLastError();
+    const OrthoInFn norm_fn = dtype == TGEMM_F32 ? ortho_norm_kernel<EF32>
+                              : dtype == TGEMM_BF16 ? ortho_norm_kernel<EBF16> : ortho_norm_kernel<EF16>;
+    const OrthoInFn load_fn = dtype == TGEMM_F32 ? ortho_load_kernel<EF32>
+                              : dtype == TGEMM_BF16 ? ortho_load_kernel<EBF16> : ortho_load_kernel<EF16>;
+    void* in_args[] = {&in};
+    hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(norm_fn), dim3((unsigned)(PARTS * batch)), dim3(256),
+                                     in_args, 0, s);
+    if (err == hipSuccess)
+        err = hipLaunchKernel(reinterpret_cast<const void*>(load_fn), dim3((unsigned)(batch * load)), dim3(256), in_args, 0,
+                              s);
 
     OrthoArgs g{};
     g.hi = g.hi_out = in.hi;
@@ -537,11 +646,11 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     g.m = (int32_t)p.m;
     g.n = (int32_t)p.n;
     g.tall = in.tall;
+    g.tiles_m = (int32_t)(p.mp / ut);
+    g.tiles_n = (int32_t)(p.np / ut);
     auto launch = [&](OrthoFn fn, const OrthoKernels& k, int64_t tiles) {
         if (err != hipSuccess) return;
         g.tiles = (int32_t)tiles;
-        g.tiles_m = (int32_t)(p.mp / k.tile);
-        g.tiles_n = (int32_t)(p.np / k.tile);
         void* args[] = {&g};
         err = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)(batch * tiles)), dim3(k.threads), args, 0,
                               s);
@@ -552,9 +661,9 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
         g.cc = (float)coefficients[3 * k + 2];
         g.xt = (const _Float16*)(ws + (k % 2 ? p.off_t1 : p.off_t0));
         g.xt_out = (_Float16*)(ws + (k % 2 ? p.off_t0 : p.off_t1));
-        launch(p.sym->gram, *p.sym, tri);
-        launch(p.sym->poly, *p.sym, tri);
-        launch(k + 1 < steps ? p.upd->update : p.upd->last, *p.upd, upd);
+        launch(p.sym->first, *p.sym, tri);
+        launch(p.sym->second, *p.sym, tri);
+        launch(k + 1 < steps ? p.upd->first : p.upd->second, *p.upd, upd);
     }
     if (err != hipSuccess) {
         set_error("launch failed: %s", hipGetErrorString(err));
