@@ -54,13 +54,13 @@ struct OrthoArgs {
     _Float16* lo_out;
     const _Float16* xt;    // np x mp: X transposed
     _Float16* xt_out;
-    _Float16* a;           // mp x mp: A'
-    _Float16* b;           // mp x mp: B'
-    float* d;              // mp: diagonal of A
-    float* e;              // mp: diagonal of B
+    _Float16* a;           // ms x ms: A'
+    _Float16* b;           // ms x ms: B'
+    float* d;              // ms: diagonal of A
+    float* e;              // ms: diagonal of B
     uint16_t* out;         // bfloat16 result
     int64_t ldo, stride_o;
-    int32_t mp, np, m, n, tall;
+    int32_t mp, np, ms, m, n, tall;
     int32_t tiles;             // tiles of one matrix
     int32_t tiles_m, tiles_n;  // of the update
     float ca, cb, cc;
@@ -80,6 +80,37 @@ struct Halves {
 template <int FM>
 __device__ __forceinline__ int quad_row(int q, int lane) { return 4 * FM * (2 * q + (lane >> 5)); }
 
+// The diagonal's entries of those 4 FM rows.
+template <int FM>
+struct QuadDiagonal {
+    float v[4 * FM];
+    __device__ __forceinline__ void load(const float* d, int m) { __builtin_memcpy(v, d + m, sizeof v); }
+};
+
+// Tile t of the lower triangle (tn <= tm): bands of BAND tile rows, each
+// walked column by column, so that the tiles that run on one XCD at a time
+// share operand panels.
+constexpr int BAND = 6;
+__device__ __forceinline__ void lower_tile(int t, int tile_rows, int& tm, int& tn) {
+    int row = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);  // if walked row by row
+    while (row * (row + 1) / 2 > t) --row;
+    while ((row + 1) * (row + 2) / 2 <= t) ++row;
+    const int first = row / BAND * BAND;
+    int u = t - first * (first + 1) / 2;
+    // columns 0 .. first hold BAND tiles of the band each (fewer in a last,
+    // partial band), later ones one less each
+    const int rows = min(BAND, tile_rows - first);
+    if (u < (first + 1) * rows) {
+        tn = u / rows;
+        tm = first + u - tn * rows;
+        return;
+    }
+    u -= (first + 1) * rows;
+    tn = first + 1;
+    while (u >= first + rows - tn) u -= first + rows - tn++;
+    tm = tn + u;
+}
+
 template <class G>
 struct OrthoTile {
     int z, tm, tn, m0, n0, wm0, wn0, lane, wave;
@@ -90,11 +121,7 @@ struct OrthoTile {
         z = r / g.tiles;
         const int t = r - z * g.tiles;
         if (symmetric) {
-            // tile t of the lower triangle, row by row
-            tm = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-            while (tm * (tm + 1) / 2 > t) --tm;
-            while ((tm + 1) * (tm + 2) / 2 <= t) ++tm;
-            tn = t - tm * (tm + 1) / 2;
+            lower_tile(t, g.ms / G::BM, tm, tn);
         } else {
             grouped_tile(t, g.tiles_m, g.tiles_n, 4, tm, tn);
         }
@@ -106,20 +133,22 @@ struct OrthoTile {
     }
 };
 
-__device__ __forceinline__ NtOperands ortho_operands(const _Float16* a, const _Float16* b, int rows_a, int rows_b, int k) {
+__device__ __forceinline__ NtOperands ortho_operands(const _Float16* a, int rows_a, int lda, const _Float16* b,
+                                                     int rows_b, int ldb, int k) {
     return NtOperands{reinterpret_cast<const char*>(a), reinterpret_cast<const char*>(b), nullptr, nullptr,
-                      rows_a, rows_b, 2 * k, 2 * (int64_t)k, 2 * (int64_t)k, 0, 0};
+                      rows_a, rows_b, 2 * k, 2 * (int64_t)lda, 2 * (int64_t)ldb, 0, 0};
 }
 
-// Write the wave's block of a symmetric matrix (ld rows), and its mirror image
-// where the tile lies below the diagonal.  row(i, r, row, out): the FN values
-// of register r in fragments (i, ..).  Tiles may reach past the last row.
-template <class G, class F>
-__device__ __forceinline__ void store_symmetric(_Float16* S, int ld, const OrthoTile<G>& t, F value) {
+// Write the wave's block of a symmetric matrix (leading dimension ld), and its
+// mirror image where the tile lies below the diagonal.  value(i, r, row, out):
+// the FN values of register r in fragments (i, ..); request(q) is called
+// before registers 4 q .. are stored.
+template <class G, class R, class F>
+__device__ __forceinline__ void store_symmetric(_Float16* S, int ld, const OrthoTile<G>& t, R request, F value) {
     const int mb = t.m0 + t.wm0, nb = t.n0 + t.wn0, n = nb + G::col_of(0, t.lane);
-    const bool inside = t.m0 + G::BM <= ld;  // then t.n0 + BN too: tn <= tm
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
+        request(q);
         Halves<4 * G::FM> col[G::FN];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -127,29 +156,15 @@ __device__ __forceinline__ void store_symmetric(_Float16* S, int ld, const Ortho
             for (int i = 0; i < G::FM; ++i) {
                 const int m = mb + G::row_of(i, 4 * q + e, t.lane);
                 Halves<G::FN> row;
-                value(i, 4 * q + e, min(m, ld - 1), row);
+                value(i, 4 * q + e, m, row);
 #pragma unroll
                 for (int j = 0; j < G::FN; ++j) col[j].v[G::FM * e + i] = row.v[j];
-                _Float16* dst = S + (int64_t)m * ld + n;
-                if (inside) __builtin_memcpy(dst, &row, sizeof row);
-                else {
-#pragma unroll
-                    for (int j = 0; j < G::FN; ++j)
-                        if (m < ld && n + j < ld) dst[j] = row.v[j];
-                }
+                __builtin_memcpy(S + (int64_t)m * ld + n, &row, sizeof row);
             }
         if (t.tm != t.tn) {
-            const int m = mb + quad_row<G::FM>(q, t.lane);
 #pragma unroll
-            for (int j = 0; j < G::FN; ++j) {
-                _Float16* dst = S + (int64_t)(n + j) * ld + m;
-                if (inside) __builtin_memcpy(dst, &col[j], sizeof col[j]);
-                else {
-#pragma unroll
-                    for (int k = 0; k < 4 * G::FM; ++k)
-                        if (n + j < ld && m + k < ld) dst[k] = col[j].v[k];
-                }
-            }
+            for (int j = 0; j < G::FN; ++j)
+                __builtin_memcpy(S + (int64_t)(n + j) * ld + mb + quad_row<G::FM>(q, t.lane), &col[j], sizeof col[j]);
         }
     }
 }
@@ -159,13 +174,13 @@ template <class G>
 __global__ __launch_bounds__(G::NT) void ortho_gram_kernel(OrthoArgs g) {
     __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
     const OrthoTile<G> t(g, true);
-    const int64_t x = (int64_t)t.z * g.mp * g.np, s = (int64_t)t.z * g.mp * g.mp;
+    const int64_t x = (int64_t)t.z * g.mp * g.np, s = (int64_t)t.z * g.ms * g.ms;
     typename G::Acc acc[G::FM][G::FN];
-    G::product(ortho_operands(g.hi + x, g.hi + x, g.mp, g.mp, g.np), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0,
+    G::product(ortho_operands(g.hi + x, g.mp, g.np, g.hi + x, g.mp, g.np, g.np), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0,
                t.wn0, t.lane, t.wave);
-    float* d = g.d + (int64_t)t.z * g.mp;
+    float* d = g.d + (int64_t)t.z * g.ms;
     const int n = t.n0 + t.wn0 + G::col_of(0, t.lane);
-    store_symmetric<G>(g.a + s, g.mp, t, [&](int i, int r, int m, Halves<G::FN>& out) {
+    store_symmetric<G>(g.a + s, g.ms, t, [](int) {}, [&](int i, int r, int m, Halves<G::FN>& out) {
 #pragma unroll
         for (int j = 0; j < G::FN; ++j) {
             const float v = acc[i][j][r] * (1.0f / (ONE * ONE));
@@ -181,34 +196,53 @@ template <class G>
 __global__ __launch_bounds__(G::NT) void ortho_poly_kernel(OrthoArgs g) {
     __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
     const OrthoTile<G> t(g, true);
-    const int64_t s = (int64_t)t.z * g.mp * g.mp;
+    const int64_t s = (int64_t)t.z * g.ms * g.ms;
     const _Float16* A = g.a + s;
     typename G::Acc acc[G::FM][G::FN];
-    G::product(ortho_operands(A, A, g.mp, g.mp, g.mp), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0, t.wn0, t.lane,
+    G::product(ortho_operands(A, g.mp, g.ms, A, g.mp, g.ms, g.mp), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0, t.wn0, t.lane,
                t.wave);
-    const float* d = g.d + (int64_t)t.z * g.mp;
-    float* e = g.e + (int64_t)t.z * g.mp;
-    const int n = t.n0 + t.wn0 + G::col_of(0, t.lane);
-    const bool whole = n + G::FN <= g.mp;
+    const float* d = g.d + (int64_t)t.z * g.ms;
+    float* e = g.e + (int64_t)t.z * g.ms;
+    // A' and d of one register quad, requested a quad ahead of their use: the
+    // compiler may not move a load over a store, and a load's latency for
+    // each row would add up (110 us against 99 at 4096 x 4096, 9.8 against
+    // 6.6 at 256 x 256)
+    const int mb = t.m0 + t.wm0, n = t.n0 + t.wn0 + G::col_of(0, t.lane);
+    struct Quad {
+        Halves<G::FN> a[G::FM][4];
+        QuadDiagonal<G::FM> d;
+    };
+    Quad ahead[2];
+    auto load = [&](Quad& x, int q) {
+        x.d.load(d, mb + quad_row<G::FM>(q, t.lane));
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int i = 0; i < G::FM; ++i)
+                __builtin_memcpy(&x.a[i][p], A + (int64_t)(mb + G::row_of(i, 4 * q + p, t.lane)) * g.ms + n,
+                                 sizeof x.a[0][0]);
+    };
     float dn[G::FN];
 #pragma unroll
-    for (int j = 0; j < G::FN; ++j) dn[j] = d[min(n + j, g.mp - 1)];
-    store_symmetric<G>(g.b + s, g.mp, t, [&](int i, int r, int m, Halves<G::FN>& out) {
-        const float dm = d[m];
-        Halves<G::FN> a;
-        if (whole) __builtin_memcpy(&a, A + (int64_t)m * g.mp + n, sizeof a);
-        else {
+    for (int j = 0; j < G::FN; ++j) dn[j] = d[n + j];
+    load(ahead[0], 0);
+    store_symmetric<G>(
+        g.b + s, g.ms, t,
+        [&](int q) {
+            if (q < 3) load(ahead[(q + 1) & 1], q + 1);
+            __builtin_amdgcn_sched_barrier(0);
+        },
+        [&](int i, int r, int m, Halves<G::FN>& out) {
+            const Quad& x = ahead[(r >> 2) & 1];
+            const float di = x.d.v[G::FM * (r & 3) + i];
 #pragma unroll
-            for (int j = 0; j < G::FN; ++j) a.v[j] = A[(int64_t)m * g.mp + min(n + j, g.mp - 1)];
-        }
-#pragma unroll
-        for (int j = 0; j < G::FN; ++j) {
-            const float sq = acc[i][j][r] * (1.0f / (ONE * ONE)), av = (float)a.v[j] * (1.0f / ONE);
-            const bool diagonal = m == n + j;
-            if (diagonal) e[m] = g.cb * dm + g.cc * (dm * dm + sq);
-            out.v[j] = (_Float16)(diagonal ? 0.0f : (g.cb * av + g.cc * ((dm + dn[j]) * av + sq)) * ONE);
-        }
-    });
+            for (int j = 0; j < G::FN; ++j) {
+                const float sq = acc[i][j][r] * (1.0f / (ONE * ONE)), av = (float)x.a[i][r & 3].v[j] * (1.0f / ONE);
+                const bool diagonal = m == n + j;
+                if (diagonal) e[m] = g.cb * di + g.cc * (di * di + sq);
+                out.v[j] = (_Float16)(diagonal ? 0.0f : (g.cb * av + g.cc * ((di + dn[j]) * av + sq)) * ONE);
+            }
+        });
 }
 
 // X <- (a + e) X + B' X; LAST writes the result instead.
@@ -216,14 +250,36 @@ template <class G, bool LAST>
 __global__ __launch_bounds__(G::NT) void ortho_update_kernel(OrthoArgs g) {
     __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
     const OrthoTile<G> t(g, false);
-    const int64_t x = (int64_t)t.z * g.mp * g.np, s = (int64_t)t.z * g.mp * g.mp;
+    const int64_t x = (int64_t)t.z * g.mp * g.np, s = (int64_t)t.z * g.ms * g.ms;
     typename G::Acc acc[G::FM][G::FN];
-    G::product(ortho_operands(g.b + s, g.xt + x, g.mp, g.np, g.mp), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0,
+    G::product(ortho_operands(g.b + s, g.mp, g.ms, g.xt + x, g.np, g.mp, g.mp), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0,
                t.wn0, t.lane, t.wave);
-    const float* e = g.e + (int64_t)t.z * g.mp;
+    const float* e = g.e + (int64_t)t.z * g.ms;
     const int mb = t.m0 + t.wm0, nb = t.n0 + t.wn0, n = nb + G::col_of(0, t.lane);
+    // X and e of one register quad, requested a quad ahead of their use (a
+    // load may not move over a store)
+    struct Quad {
+        Halves<G::FN> h[G::FM][4], l[G::FM][4];
+        QuadDiagonal<G::FM> e;
+    };
+    auto load = [&](Quad& x4, int q) {
+        x4.e.load(e, mb + quad_row<G::FM>(q, t.lane));
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int i = 0; i < G::FM; ++i) {
+                const int64_t at = x + (int64_t)(mb + G::row_of(i, 4 * q + p, t.lane)) * g.np + n;
+                __builtin_memcpy(&x4.h[i][p], g.hi + at, sizeof x4.h[0][0]);
+                __builtin_memcpy(&x4.l[i][p], g.lo + at, sizeof x4.l[0][0]);
+            }
+    };
+    Quad ahead[2];
+    load(ahead[0], 0);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
+        if (q < 3) load(ahead[(q + 1) & 1], q + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        Quad& x4 = ahead[q & 1];
         Halves<4 * G::FM> col[G::FN];
 #pragma unroll
         for (int p = 0; p < 4; ++p)
@@ -231,10 +287,8 @@ __global__ __launch_bounds__(G::NT) void ortho_update_kernel(OrthoArgs g) {
             for (int i = 0; i < G::FM; ++i) {
                 const int m = mb + G::row_of(i, 4 * q + p, t.lane);
                 const int64_t at = x + (int64_t)m * g.np + n;
-                Halves<G::FN> h, l;
-                __builtin_memcpy(&h, g.hi + at, sizeof h);
-                __builtin_memcpy(&l, g.lo + at, sizeof l);
-                const float k = g.ca + e[m];
+                Halves<G::FN>&h = x4.h[i][p], &l = x4.l[i][p];
+                const float k = g.ca + x4.e.v[G::FM * p + i];
                 uint16_t o[G::FN];
 #pragma unroll
                 for (int j = 0; j < G::FN; ++j) {
@@ -423,7 +477,7 @@ static OrthoKernels update_kernels(double cost) {
 }
 
 typedef NtGemm<NtF16, 256, 256, 2, 4, 2, false> Ortho256;
-typedef NtGemm<NtF16, 192, 192, 2, 2, 3, false> Ortho192;
+typedef NtGemm<NtF16, 192, 192, 2, 6, 3, true> Ortho192;
 typedef NtGemm<NtF16, 128, 128, 2, 2, 4, true> Ortho128;
 typedef NtGemm<NtF16, 64, 64, 2, 2, 8, true> Ortho64;
 
@@ -441,7 +495,7 @@ static const OrthoKernels* update_table(int* count) {
 }
 
 struct OrthoPlan {
-    int64_t m, n, mp, np;
+    int64_t m, n, mp, np, ms;
     const OrthoKernels *sym, *upd;
     int64_t tri;  // symmetric tiles of one matrix
     int64_t off_hi, off_lo, off_t0, off_t1, off_a, off_b, off_d, off_e, off_part, bytes;
@@ -465,7 +519,8 @@ static const OrthoKernels* cheapest(const OrthoKernels* t, int count, F tiles) {
 }
 
 // Tiles, and where things stand in the workspace.  X is padded to whole
-// update tiles; symmetric tiles may reach past its rows.
+// update tiles, with zeros that every product keeps.  A and B have room for
+// whole symmetric tiles; what lies past X's rows there is read by no product.
 static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     OrthoPlan p{};
     p.m = rows < cols ? rows : cols;
@@ -480,21 +535,22 @@ static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     t = symmetric_table(&count);
     p.sym = cheapest(t, count, [&](int64_t tile) { return batch * tri(tile); });
     p.tri = tri(p.sym->tile);
+    p.ms = up_to(p.mp, p.sym->tile);
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t o = at;
         at += up_to(bytes, 256);
         return o;
     };
-    const int64_t x = 2 * batch * p.mp * p.np, s = 2 * batch * p.mp * p.mp;
+    const int64_t x = 2 * batch * p.mp * p.np, s = 2 * batch * p.ms * p.ms;
     p.off_hi = take(x);
     p.off_lo = take(x);
     p.off_t0 = take(x);
     p.off_t1 = take(x);
     p.off_a = take(s);
     p.off_b = take(s);
-    p.off_d = take(4 * batch * p.mp);
-    p.off_e = take(4 * batch * p.mp);
+    p.off_d = take(4 * batch * p.ms);
+    p.off_e = take(4 * batch * p.ms);
     p.off_part = take(8 * batch * PARTS);
     p.bytes = at;
     return p;
@@ -596,7 +652,7 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     const int64_t ut = p.upd->tile, tri = p.tri, upd = (p.mp / ut) * (p.np / ut);
     const int64_t load = (p.mp / 64) * (p.np / 64);
     if (batch * tri > INT_MAX || batch * upd > INT_MAX || batch * load > INT_MAX ||
-        255 * 2 * p.np + 128 > INT64_C(0xffffffff)) {  // a tile's copies take 32-bit offsets
+        255 * 2 * (p.np > p.ms ? p.np : p.ms) + 128 > INT64_C(0xffffffff)) {  // a tile's copies take 32-bit offsets
 
         set_error("too many tiles");
         return TGEMM_E_ARG;
@@ -643,6 +699,7 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     g.stride_o = stride_o;
     g.mp = in.mp;
     g.np = in.np;
+    g.ms = (int32_t)p.ms;
     g.m = (int32_t)p.m;
     g.n = (int32_t)p.n;
     g.tall = in.tall;
