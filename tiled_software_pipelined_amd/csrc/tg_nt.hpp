@@ -124,6 +124,8 @@ struct NtGemm {
     static constexpr int A_PER = BM * 8 / NT, B_PER = BN * 8 / NT;
     static constexpr int S_PER = (BM + BN) / 4 / WAVES;  // scale dwords each wave copies
     static constexpr int N_CP = A_PER + B_PER + (Tr::SCALED ? 1 : 0);
+    // an epilogue's inputs fit in registers beside the product's
+    static constexpr bool EARLY = FM * FN * WAVES <= 16;
     static constexpr int NM = FM * FN;
     static constexpr int RB = LB / 16;  // LDS reads per fragment
     static constexpr int NS = Tr::SCALED ? 2 : 0;

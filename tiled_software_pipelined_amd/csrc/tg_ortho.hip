@@ -198,21 +198,19 @@ __global__ __launch_bounds__(G::NT) void ortho_poly_kernel(OrthoArgs g) {
     const OrthoTile<G> t(g, true);
     const int64_t s = (int64_t)t.z * g.ms * g.ms;
     const _Float16* A = g.a + s;
-    typename G::Acc acc[G::FM][G::FN];
-    G::product(ortho_operands(A, g.mp, g.ms, A, g.mp, g.ms, g.mp), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0, t.wn0, t.lane,
-               t.wave);
     const float* d = g.d + (int64_t)t.z * g.ms;
     float* e = g.e + (int64_t)t.z * g.ms;
-    // A' and d of one register quad, requested a quad ahead of their use: the
-    // compiler may not move a load over a store, and a load's latency for
-    // each row would add up (110 us against 99 at 4096 x 4096, 9.8 against
-    // 6.6 at 256 x 256)
+    // A' and d of one register quad.  Large tiles request them a quad ahead of
+    // their use: the compiler may not move a load over a store, and a load's
+    // latency for each row would add up (110 us against 99 at 4096 x 4096).
+    // Small ones have the registers to request all before the product.
     const int mb = t.m0 + t.wm0, n = t.n0 + t.wn0 + G::col_of(0, t.lane);
     struct Quad {
         Halves<G::FN> a[G::FM][4];
         QuadDiagonal<G::FM> d;
     };
-    Quad ahead[2];
+    constexpr int HELD = G::EARLY ? 4 : 2;
+    Quad ahead[HELD];
     auto load = [&](Quad& x, int q) {
         x.d.load(d, mb + quad_row<G::FM>(q, t.lane));
 #pragma unroll
@@ -225,15 +223,22 @@ __global__ __launch_bounds__(G::NT) void ortho_poly_kernel(OrthoArgs g) {
     float dn[G::FN];
 #pragma unroll
     for (int j = 0; j < G::FN; ++j) dn[j] = d[n + j];
-    load(ahead[0], 0);
+    if constexpr (G::EARLY) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load(ahead[q], q);
+    }
+    typename G::Acc acc[G::FM][G::FN];
+    G::product(ortho_operands(A, g.mp, g.ms, A, g.mp, g.ms, g.mp), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0, t.wn0, t.lane,
+               t.wave);
+    if constexpr (!G::EARLY) load(ahead[0], 0);
     store_symmetric<G>(
         g.b + s, g.ms, t,
         [&](int q) {
-            if (q < 3) load(ahead[(q + 1) & 1], q + 1);
+            if (!G::EARLY && q < 3) load(ahead[(q + 1) % HELD], q + 1);
             __builtin_amdgcn_sched_barrier(0);
         },
         [&](int i, int r, int m, Halves<G::FN>& out) {
-            const Quad& x = ahead[(r >> 2) & 1];
+            const Quad& x = ahead[(r >> 2) % HELD];
             const float di = x.d.v[G::FM * (r & 3) + i];
 #pragma unroll
             for (int j = 0; j < G::FN; ++j) {
@@ -251,13 +256,9 @@ __global__ __launch_bounds__(G::NT) void ortho_update_kernel(OrthoArgs g) {
     __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
     const OrthoTile<G> t(g, false);
     const int64_t x = (int64_t)t.z * g.mp * g.np, s = (int64_t)t.z * g.ms * g.ms;
-    typename G::Acc acc[G::FM][G::FN];
-    G::product(ortho_operands(g.b + s, g.mp, g.ms, g.xt + x, g.np, g.mp, g.mp), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0,
-               t.wn0, t.lane, t.wave);
     const float* e = g.e + (int64_t)t.z * g.ms;
     const int mb = t.m0 + t.wm0, nb = t.n0 + t.wn0, n = nb + G::col_of(0, t.lane);
-    // X and e of one register quad, requested a quad ahead of their use (a
-    // load may not move over a store)
+    // X and e of one register quad, requested as in the kernel above
     struct Quad {
         Halves<G::FN> h[G::FM][4], l[G::FM][4];
         QuadDiagonal<G::FM> e;
@@ -273,13 +274,21 @@ __global__ __launch_bounds__(G::NT) void ortho_update_kernel(OrthoArgs g) {
                 __builtin_memcpy(&x4.l[i][p], g.lo + at, sizeof x4.l[0][0]);
             }
     };
-    Quad ahead[2];
-    load(ahead[0], 0);
+    constexpr int HELD = G::EARLY ? 4 : 2;
+    Quad ahead[HELD];
+    if constexpr (G::EARLY) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load(ahead[q], q);
+    }
+    typename G::Acc acc[G::FM][G::FN];
+    G::product(ortho_operands(g.b + s, g.mp, g.ms, g.xt + x, g.np, g.mp, g.mp), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0,
+               t.wn0, t.lane, t.wave);
+    if constexpr (!G::EARLY) load(ahead[0], 0);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        if (q < 3) load(ahead[(q + 1) & 1], q + 1);
+        if (!G::EARLY && q < 3) load(ahead[(q + 1) % HELD], q + 1);
         __builtin_amdgcn_sched_barrier(0);
-        Quad& x4 = ahead[q & 1];
+        Quad& x4 = ahead[q % HELD];
         Halves<4 * G::FM> col[G::FN];
 #pragma unroll
         for (int p = 0; p < 4; ++p)
@@ -459,37 +468,59 @@ typedef void (*OrthoFn)(OrthoArgs);
 typedef void (*OrthoInFn)(OrthoInArgs);
 
 // Kernels of the symmetric products (gram, poly) and of the update (middle
-// steps, last), by tile.  cost: time of one round, a tile on each of the 256
-// compute units, in that of 256 x 256 tiles.
+// steps, last), by tile, with a model of their time in microseconds fitted to
+// runs of all of them at K = 64 .. 4096 and 1 .. 2080 tiles (medians of
+// kernel times): start + rounds (fixed + per_k K), K the product's inner
+// size.  Tiles of which two share a compute unit (`shared`) overlap their
+// rounds; the others run whole rounds of 256.
+//   gram, us          64     128    192    256
+//   K =  256 (256^2)    4.3    5.9   10.1   10.6
+//   K = 1024 (1024^2)   7.6   11.2   18.5   26.4
+//   K = 2048 (2048^2)  22.3   18.2   28.6   43.6
+//   K = 4096 (4096^2) 117     97     76     93
+//   update, us        64     128    256
+//   K = 1024 (1024^2)   9.8   14.4   32.7
+//   K = 1024 (x 4096)  22.9   19.6   35.4
+//   K = 2048 (2048^2)  34.8   26.3   52.7
+//   K = 4096 (4096^2) 207    155    133
 struct OrthoKernels {
     int tile, threads;
     OrthoFn first, second;
-    double cost;
+    bool shared;
+    double start, fixed, per_k;
 };
 
 template <class G>
-static OrthoKernels symmetric_kernels(double cost) {
-    return OrthoKernels{G::BM, G::NT, ortho_gram_kernel<G>, ortho_poly_kernel<G>, cost};
+static OrthoKernels symmetric_kernels(bool shared, double start, double fixed, double per_k) {
+    return OrthoKernels{G::BM, G::NT, ortho_gram_kernel<G>, ortho_poly_kernel<G>, shared, start, fixed, per_k};
 }
 template <class G>
-static OrthoKernels update_kernels(double cost) {
-    return OrthoKernels{G::BM, G::NT, ortho_update_kernel<G, false>, ortho_update_kernel<G, true>, cost};
+static OrthoKernels update_kernels(bool shared, double start, double fixed, double per_k) {
+    return OrthoKernels{G::BM, G::NT, ortho_update_kernel<G, false>, ortho_update_kernel<G, true>, shared, start, fixed,
+                        per_k};
 }
 
+// 64: four slots, so that two workgroups fit a compute unit (eight slots and
+// one: 10 % slower alone, 1.5 times as long where there are several rounds).
+// 128: eight waves of 64 x 32 (four of 64 x 64: 11.2 -> 12.8 us at 1024^2).
+// 192: twelve waves of 96 x 32 (four of 96 x 96: 74 -> 79 us at 4096^2).
 typedef NtGemm<NtF16, 256, 256, 2, 4, 2, false> Ortho256;
 typedef NtGemm<NtF16, 192, 192, 2, 6, 3, true> Ortho192;
-typedef NtGemm<NtF16, 128, 128, 2, 2, 4, true> Ortho128;
-typedef NtGemm<NtF16, 64, 64, 2, 2, 8, true> Ortho64;
+typedef NtGemm<NtF16, 128, 128, 2, 4, 4, true> Ortho128;
+typedef NtGemm<NtF16, 64, 64, 2, 2, 4, true> Ortho64;
 
 static const OrthoKernels* symmetric_table(int* count) {
-    static const OrthoKernels t[4] = {symmetric_kernels<Ortho256>(1.0), symmetric_kernels<Ortho192>(0.6),
-                                      symmetric_kernels<Ortho128>(0.33), symmetric_kernels<Ortho64>(0.13)};
+    static const OrthoKernels t[4] = {symmetric_kernels<Ortho256>(false, 0.0, 9.0, 0.0205),
+                                      symmetric_kernels<Ortho192>(false, 0.0, 5.0, 0.0165),
+                                      symmetric_kernels<Ortho128>(false, 0.0, 4.3, 0.0060),
+                                      symmetric_kernels<Ortho64>(true, 0.0, 3.3, 0.0028)};
     *count = 4;
     return t;
 }
 static const OrthoKernels* update_table(int* count) {
-    static const OrthoKernels t[3] = {update_kernels<Ortho256>(1.0), update_kernels<Ortho128>(0.33),
-                                      update_kernels<Ortho64>(0.13)};
+    static const OrthoKernels t[3] = {update_kernels<Ortho256>(false, 0.0, 28.0, 0.0255),
+                                      update_kernels<Ortho128>(false, 0.0, 10.0, 0.0075),
+                                      update_kernels<Ortho64>(true, 3.5, 2.9, 0.0026)};
     *count = 3;
     return t;
 }
@@ -503,13 +534,15 @@ struct OrthoPlan {
 
 static int64_t up_to(int64_t v, int64_t step) { return (v + step - 1) / step * step; }
 
-// The cheapest kernel of a table for tiles(size) workgroups.
+// The cheapest kernel of a table for tiles(size) workgroups and inner size k.
 template <class F>
-static const OrthoKernels* cheapest(const OrthoKernels* t, int count, F tiles) {
+static const OrthoKernels* cheapest(const OrthoKernels* t, int count, int64_t k, F tiles) {
     const OrthoKernels* best = t;
     double least = 0.0;
     for (int i = 0; i < count; ++i) {
-        const double c = t[i].cost * (double)((tiles(t[i].tile) + 255) / 256);
+        const int64_t n = tiles(t[i].tile);
+        const double rounds = !t[i].shared ? (double)((n + 255) / 256) : n > 256 ? n / 256.0 : 1.0;
+        const double c = t[i].start + rounds * (t[i].fixed + t[i].per_k * (double)k);
         if (i == 0 || c < least) {
             least = c;
             best = t + i;
@@ -528,12 +561,12 @@ static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     auto tiles = [](int64_t v, int64_t tile) { return (v + tile - 1) / tile; };
     int count;
     const OrthoKernels* t = update_table(&count);
-    p.upd = cheapest(t, count, [&](int64_t tile) { return batch * tiles(p.m, tile) * tiles(p.n, tile); });
+    p.upd = cheapest(t, count, p.m, [&](int64_t tile) { return batch * tiles(p.m, tile) * tiles(p.n, tile); });
     p.mp = up_to(p.m, p.upd->tile);
     p.np = up_to(p.n, p.upd->tile);
     auto tri = [&](int64_t tile) { return tiles(p.mp, tile) * (tiles(p.mp, tile) + 1) / 2; };
     t = symmetric_table(&count);
-    p.sym = cheapest(t, count, [&](int64_t tile) { return batch * tri(tile); });
+    p.sym = cheapest(t, count, (p.np + p.mp) / 2, [&](int64_t tile) { return batch * tri(tile); });  // gram: np, poly: mp
     p.tri = tri(p.sym->tile);
     p.ms = up_to(p.mp, p.sym->tile);
     int64_t at = 0;
