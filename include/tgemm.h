@@ -405,6 +405,33 @@ int tgemm_fp8_gemm(int64_t M, int64_t N, int64_t K, int32_t fmt_a, const void* A
                    int64_t ldsa, int32_t fmt_b, const void* B, int64_t ldb, const void* SB, int64_t ldsb, void* C,
                    int64_t ldc, void* stream);
 
+/* A linear layer in 8 bits, y = x w^T, and its gradients: the calls above
+ * chained on `stream`, for callers that pay for every call.
+ *
+ * forward: x (M x K) and w (N x K), each float, bfloat16 or float16, are
+ * quantised to e4m3 (x by rows, w by square blocks) and multiplied into y (M
+ * x N bfloat16).  `keep` says which gradients will be asked for: TGEMM_KEEP_X
+ * (dx, from w) and TGEMM_KEEP_W (dw, from x); the transposed images they need
+ * go to `saved`.  backward: g (M x N), the gradient of y, is quantised to
+ * `grad_fmt`, by rows for dx = g w (M x K bfloat16) and by columns for dw = g^T
+ * x (N x K bfloat16); dx and dw are written where `keep` (the same as
+ * before) has their bit, and are ignored otherwise.  `saved` is only read.
+ * tgemm_fp8_linear_bytes fills bytes[0 .. 2] with the sizes of `saved`, of
+ * forward's `scratch` and of backward's `scratch`; all are device memory,
+ * 256-byte aligned, and a scratch's contents are overwritten.  M, N or K = 0
+ * are the empty products they make.  The outputs must not overlap anything
+ * else.  Each returns TGEMM_OK or a TGEMM_E_* code; a call that is refused
+ * enqueues nothing. */
+#define TGEMM_KEEP_X 1
+#define TGEMM_KEEP_W 2
+int tgemm_fp8_linear_bytes(int64_t M, int64_t N, int64_t K, int32_t keep, int64_t* bytes);
+int tgemm_fp8_linear_forward(int64_t M, int64_t N, int64_t K, int32_t x_dtype, const void* x, int64_t ldx,
+                             int32_t w_dtype, const void* w, int64_t ldw, void* y, int64_t ldy, int32_t keep,
+                             void* saved, void* scratch, void* stream);
+int tgemm_fp8_linear_backward(int64_t M, int64_t N, int64_t K, int32_t g_dtype, const void* g, int64_t ldg,
+                              int32_t grad_fmt, int32_t keep, const void* saved, void* dx, int64_t lddx, void* dw,
+                              int64_t lddw, void* scratch, void* stream);
+
 /* Name of the kernel tgemm_fp8_gemm launches for these sizes ("" where it
  * launches none). */
 const char* tgemm_fp8_gemm_kernel(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb);

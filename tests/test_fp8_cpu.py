@@ -128,3 +128,43 @@ def test_scale_table_checks():
             tl._scales(bad, rows, cols, dev, "S")
     with pytest.raises(TypeError):
         tl._scales(s.float(), 16, 256, dev, "S")
+
+
+def lin(forward, M=4, N=6, K=8, **kw):
+    a = dict(xd=1, x=P(256), ldx=K, wd=1, w=P(256), ldw=K, y=P(256), ldy=N, keep=3, saved=P(256), scratch=P(256), gd=1,
+             g=P(256), ldg=N, fmt=0, dx=P(256), lddx=K, dw=P(256), lddw=K)
+    a.update(kw)
+    if forward:
+        return tl._lib.tgemm_fp8_linear_forward(M, N, K, a["xd"], a["x"], a["ldx"], a["wd"], a["w"], a["ldw"], a["y"], a["ldy"],
+                                                a["keep"], a["saved"], a["scratch"], None)
+    return tl._lib.tgemm_fp8_linear_backward(M, N, K, a["gd"], a["g"], a["ldg"], a["fmt"], a["keep"], a["saved"], a["dx"],
+                                             a["lddx"], a["dw"], a["lddw"], a["scratch"], None)
+
+
+@pytest.mark.parametrize("forward,kw,code", [
+    (True, dict(M=-1), -1), (True, dict(N=2 ** 31), -1), (True, dict(keep=4), -1), (True, dict(xd=2), -1),
+    (True, dict(wd=5), -1), (True, dict(ldx=7), -1), (True, dict(ldw=7), -1), (True, dict(ldy=5), -1),
+    (True, dict(x=None), -2), (True, dict(w=None), -2), (True, dict(y=None), -2), (True, dict(saved=None), -2),
+    (True, dict(scratch=None), -2), (True, dict(x=P(257)), -3), (True, dict(xd=0, x=P(258)), -3), (True, dict(y=P(257)), -3),
+    (True, dict(saved=P(16)), -3), (True, dict(scratch=P(16)), -3),
+    (False, dict(M=-1), -1), (False, dict(keep=-1), -1), (False, dict(gd=2), -1), (False, dict(fmt=2), -1),
+    (False, dict(ldg=5), -1), (False, dict(lddx=7), -1), (False, dict(lddw=7), -1), (False, dict(g=None), -2),
+    (False, dict(dx=None), -2), (False, dict(dw=None), -2), (False, dict(saved=None), -2), (False, dict(scratch=None), -2),
+    (False, dict(g=P(257)), -3), (False, dict(saved=P(16)), -3), (False, dict(scratch=P(16)), -3),
+])
+def test_linear_refuses(forward, kw, code):
+    assert lin(forward, **kw) == code and tl.last_error()
+
+
+def test_linear_bytes():
+    b = tl._linear_bytes
+    assert b(0, 0, 0, 3) == (1, 1, 1)
+    # images of one byte an element, tables, each on a 256-byte boundary
+    assert b(100, 200, 300, 0) == (1, 30208 + 512 + 60160 + 768, 20224 + 256)
+    saved, fwd, bwd = b(100, 200, 300, 3)
+    assert saved == 60160 + 768 + 30208 + 512 and bwd == 20224 + 256 + 20224 + 256
+    assert tl._lib.tgemm_fp8_linear_bytes(1, 1, 1, 0, None) == -2
+    with pytest.raises(tl.TgemmError):
+        b(1, 1, 1, 4)
+    assert lin(True, M=0, N=0, K=0, keep=0, saved=None, scratch=None, x=None, w=None, y=None) == 0
+    assert lin(False, M=0, N=0, K=0, keep=0, saved=None, scratch=None, g=None) == 0

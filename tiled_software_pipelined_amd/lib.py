@@ -9,6 +9,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -68,7 +69,7 @@ EXPORTS = ("gemm_plan", "gemm_plan_variant", "gemm_run", "gemm_destroy", "tgemm_
            "tgemm_lds_read_probe", "tgemm_mfma_rate_probe", "gemm_workspace_bytes", "gemm_run_ws",
            "gemm_kernel_occupancy", "gemm_clock_slots", "gemm_run_clocked", "gemm_run_noalloc",
            "tgemm_set_c_store_policy", "tgemm_fp8_quantize", "tgemm_fp8_gemm", "tgemm_fp8_gemm_kernel",
-           "tgemm_orthogonalize_workspace_bytes", "tgemm_orthogonalize")
+           "tgemm_fp8_linear_bytes", "tgemm_fp8_linear_forward", "tgemm_fp8_linear_backward", "tgemm_orthogonalize_workspace_bytes", "tgemm_orthogonalize")
 
 
 def _load():
@@ -123,6 +124,12 @@ def _load():
     lib.tgemm_fp8_gemm.restype = ctypes.c_int
     lib.tgemm_fp8_gemm_kernel.argtypes = [i64, i64, i64, i64, i64]
     lib.tgemm_fp8_gemm_kernel.restype = ctypes.c_char_p
+    lib.tgemm_fp8_linear_bytes.argtypes = [i64, i64, i64, i32, ctypes.POINTER(i64)]
+    lib.tgemm_fp8_linear_bytes.restype = ctypes.c_int
+    lib.tgemm_fp8_linear_forward.argtypes = [i64, i64, i64, i32, vp, i64, i32, vp, i64, vp, i64, i32, vp, vp, vp]
+    lib.tgemm_fp8_linear_forward.restype = ctypes.c_int
+    lib.tgemm_fp8_linear_backward.argtypes = [i64, i64, i64, i32, vp, i64, i32, i32, vp, vp, i64, vp, i64, vp, vp]
+    lib.tgemm_fp8_linear_backward.restype = ctypes.c_int
     f64 = ctypes.c_double
     lib.tgemm_orthogonalize_workspace_bytes.argtypes = [i64, i64, i64]
     lib.tgemm_orthogonalize_workspace_bytes.restype = i64
@@ -426,44 +433,64 @@ def gemm(A, B, out=None, variant: Variant | None = None, workspace: bool = True)
 
 # ---- 8-bit floating point products with block scales --------------------------
 
+import torch  # noqa: E402  (_load has imported it)
+
 FP8_BLOCK = 128  # elements of a row that share a scale
 E4M3, E5M2 = 0, 1
 BLOCKS = {"row": 0, "square": 1}
+KEEP_X, KEEP_W = 1, 2
+_FP8_CODES = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
+_REAL_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+# Small calls are bound by their way here: the raw handle of the current
+# stream costs 0.1 us where torch.cuda.current_stream makes an object in 2 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(device, fn, *args):
+    """fn(*args, current stream of device), on that device; raises on an error code."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc != OK:
+        raise TgemmError(rc, last_error())
 
 
 def _fp8_code(dtype):
-    import torch
-    codes = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
-    if dtype not in codes:
+    code = _FP8_CODES.get(dtype)
+    if code is None:
         raise TypeError("unsupported 8-bit type %s (float8_e4m3fn, float8_e5m2)" % dtype)
-    return codes[dtype]
+    return code
 
 
 def _real_code(t, name):
-    import torch
-    codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
-    if t.dtype not in codes:
+    code = _REAL_CODES.get(t.dtype)
+    if code is None:
         raise TypeError("%s has unsupported dtype %s (float32, bfloat16, float16)" % (name, t.dtype))
-    return codes[t.dtype]
+    return code
 
 
 def _image(rows, cols, dtype, device):
-    """An empty quantised operand: values, and scales whose rows start on
-    16-byte boundaries."""
-    import torch
+    """An empty quantised operand: values, scales whose rows start on 16-byte
+    boundaries, and the row stride of the scales."""
     q = torch.empty((rows, cols), dtype=dtype, device=device)
-    s = torch.empty((-(-cols // FP8_BLOCK), -(-rows // 16) * 16), dtype=torch.float8_e8m0fnu, device=device)
-    return q, s[:, :rows]
+    lds = -(-rows // 16) * 16
+    s = torch.empty((-(-cols // FP8_BLOCK), lds), dtype=torch.float8_e8m0fnu, device=device)
+    return q, s if lds == rows else s[:, :rows], lds
 
 
-def quantize_fp8(X, dtype=None, block="row", transpose=False):
+def quantize_fp8(X, dtype=torch.float8_e4m3fn, block="row", transpose=False):
     """(Q, S), the 8-bit image of X with a power-of-two scale for each 128
     elements of a row; with ``transpose`` (Q, S, Qt, St), also that of X
     transposed.
 
     X: (rows, cols) float32, bfloat16 or float16 on the GPU, row-major (row
     stride may exceed the row length).  Q: (rows, cols) of ``dtype``
-    (float8_e4m3fn, the default, or float8_e5m2); S: (ceil(cols / 128), rows)
+    (float8_e4m3fn or float8_e5m2); S: (ceil(cols / 128), rows)
     float8_e8m0fnu; X[r, c] is near Q[r, c] * S[c // 128, r].  With block
     "square" one scale serves each 128 x 128 block of X, and Qt is Q
     transposed (weights, whose two images then hold the same values); with
@@ -472,39 +499,37 @@ def quantize_fp8(X, dtype=None, block="row", transpose=False):
     type's range.  NaN stays NaN, and an infinity becomes the type's infinity
     or NaN.  Runs on the current stream.
     """
-    import torch
-    dtype = torch.float8_e4m3fn if dtype is None else dtype
     fmt = _fp8_code(dtype)
     if block not in BLOCKS:
         raise ValueError("block must be \"row\" or \"square\", got %r" % (block,))
     if not X.is_cuda:
         raise ValueError("X must be a GPU tensor")
-    code, ldx = _real_code(X, "X"), _ld(X, "X")
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D")
+    code, device = _real_code(X, "X"), X.device
     rows, cols = X.shape
-    out = _image(rows, cols, dtype, X.device)
-    if transpose:
-        out += _image(cols, rows, dtype, X.device)
-    q, s, qt, st = out if transpose else out + (None, None)
-    with torch.cuda.device(X.device):
-        rc = _lib.tgemm_fp8_quantize(
-            rows, cols, code, X.data_ptr(), ldx, fmt, BLOCKS[block], q.data_ptr(), max(cols, 1), s.data_ptr(),
-            max(s.stride(0), 1), qt.data_ptr() if transpose else None, max(rows, 1),
-            st.data_ptr() if transpose else None, max(st.stride(0), 1) if transpose else 0,
-            torch.cuda.current_stream(X.device).cuda_stream)
-    if rc != OK:
-        raise TgemmError(rc, last_error())
-    return out
+    ldx = cols if X.is_contiguous() else _ld(X, "X")
+    q, s, lds = _image(rows, cols, dtype, device)
+    if not transpose:
+        _call(device, _lib.tgemm_fp8_quantize, rows, cols, code, X.data_ptr(), ldx, fmt, BLOCKS[block], q.data_ptr(), cols,
+              s.data_ptr(), lds, None, 0, None, 0)
+        return q, s
+    qt, st, ldst = _image(cols, rows, dtype, device)
+    _call(device, _lib.tgemm_fp8_quantize, rows, cols, code, X.data_ptr(), ldx, fmt, BLOCKS[block], q.data_ptr(), cols,
+          s.data_ptr(), lds, qt.data_ptr(), rows, st.data_ptr(), ldst)
+    return q, s, qt, st
 
 
 def _scales(s, rows, cols, device, name):
     """Row stride of a scale table (ceil(cols / 128), rows) that a product may read."""
-    import torch
-    if s.dtype not in (torch.float8_e8m0fnu, torch.uint8):
+    if s.dtype is not torch.float8_e8m0fnu and s.dtype is not torch.uint8:
         raise TypeError("%s must be float8_e8m0fnu (or its bytes as uint8), got %s" % (name, s.dtype))
     blocks = -(-cols // FP8_BLOCK)
     if tuple(s.shape) != (blocks, rows) or s.device != device:
         raise ValueError("%s must be of shape (%d, %d) on %s, got %s on %s" % (
             name, blocks, rows, device, tuple(s.shape), s.device))
+    if rows % 4 == 0 and s.is_contiguous() and s.data_ptr() % 4 == 0:
+        return rows
     if blocks == 0 or rows == 0:
         return -(-max(rows, 1) // 4) * 4
     if rows > 1 and s.stride(1) != 1:
@@ -531,28 +556,29 @@ def gemm_fp8(A, SA, B, SB, out=None):
     once from the matrix cores' float sums; ``out`` may be a preallocated
     row-major C.
     """
-    import torch
+    device = A.device
     if not (A.is_cuda and B.is_cuda):
         raise ValueError("A and B must be GPU tensors")
-    if A.device != B.device:
-        raise ValueError("A and B must be on the same device (%s, %s)" % (A.device, B.device))
+    if device != B.device:
+        raise ValueError("A and B must be on the same device (%s, %s)" % (device, B.device))
     fa, fb = _fp8_code(A.dtype), _fp8_code(B.dtype)
-    lda, ldb = _ld(A, "A"), _ld(B, "B")
+    if A.dim() != 2 or B.dim() != 2:
+        raise ValueError("A and B must be 2-D")
     (M, K), (N, K2) = A.shape, B.shape
+    lda = K if A.is_contiguous() else _ld(A, "A")
+    ldb = K2 if B.is_contiguous() else _ld(B, "B")
     if K != K2:
         raise ValueError("inner dimensions differ: %d vs %d" % (K, K2))
-    ldsa, ldsb = _scales(SA, M, K, A.device, "SA"), _scales(SB, N, K, A.device, "SB")
+    ldsa, ldsb = _scales(SA, M, K, device, "SA"), _scales(SB, N, K, device, "SB")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
-    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or out.device != A.device:
-        raise ValueError("out must be a bfloat16 tensor of shape (%d, %d) on %s" % (M, N, A.device))
-    ldc = _ld(out, "out")
-    with torch.cuda.device(A.device):
-        rc = _lib.tgemm_fp8_gemm(M, N, K, fa, A.data_ptr(), lda, SA.data_ptr(), ldsa, fb, B.data_ptr(), ldb,
-                                 SB.data_ptr(), ldsb, out.data_ptr(), ldc,
-                                 torch.cuda.current_stream(A.device).cuda_stream)
-    if rc != OK:
-        raise TgemmError(rc, last_error())
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=device)
+        ldc = N
+    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N) or out.device != device:
+        raise ValueError("out must be a bfloat16 tensor of shape (%d, %d) on %s" % (M, N, device))
+    else:
+        ldc = _ld(out, "out")
+    _call(device, _lib.tgemm_fp8_gemm, M, N, K, fa, A.data_ptr(), lda, SA.data_ptr(), ldsa, fb, B.data_ptr(), ldb,
+          SB.data_ptr(), ldsb, out.data_ptr(), ldc)
     return out
 
 
@@ -567,63 +593,77 @@ def _rows(t):
     return t if ok else t.contiguous()
 
 
-def _linear_fp8_function():
-    import torch
-
-    class LinearFp8(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, x, w, grad_dtype):
-            x2 = _rows(x.reshape(math.prod(x.shape[:-1]), x.shape[-1]))
-            need_x, need_w = ctx.needs_input_grad[:2]
-            xq = quantize_fp8(x2, transpose=need_w)
-            wq = quantize_fp8(_rows(w), block="square", transpose=need_x)
-            y = gemm_fp8(xq[0], xq[1], wq[0], wq[1])
-            ctx.grad_dtype, ctx.x_shape, ctx.x_dtype, ctx.w_dtype = grad_dtype, x.shape, x.dtype, w.dtype
-            # kept for the backward pass: one byte an element of x and of w
-            ctx.save_for_backward(*(wq[2:] if need_x else (None, None)), *(xq[2:] if need_w else (None, None)))
-            return y.reshape(*x.shape[:-1], w.shape[0]).to(x.dtype)
-
-        @staticmethod
-        @torch.autograd.function.once_differentiable
-        def backward(ctx, gy):
-            wt, wts, xt, xts = ctx.saved_tensors
-            need_x, need_w = ctx.needs_input_grad[:2]
-            # a broadcast gradient (of a sum, say) has no rows of its own
-            g2 = _rows(gy.reshape(math.prod(gy.shape[:-1]), gy.shape[-1]))
-            gq = quantize_fp8(g2, dtype=ctx.grad_dtype, transpose=need_w)
-            gx = gemm_fp8(gq[0], gq[1], wt, wts).reshape(ctx.x_shape).to(ctx.x_dtype) if need_x else None
-            gw = gemm_fp8(gq[2], gq[3], xt, xts).to(ctx.w_dtype) if need_w else None
-            return gx, gw, None
-
-    return LinearFp8
+@functools.lru_cache(maxsize=512)
+def _linear_bytes(M, N, K, keep):
+    """Bytes of (saved, forward's scratch, backward's scratch), at least one each."""
+    n = (ctypes.c_int64 * 3)()
+    rc = _lib.tgemm_fp8_linear_bytes(M, N, K, keep, n)
+    if rc != OK:
+        raise TgemmError(rc, last_error())
+    return tuple(max(v, 1) for v in n)
 
 
-_linear_fn = None
+class _LinearFp8(torch.autograd.Function):
+    # torch's allocator gives blocks on 512-byte boundaries, stream-ordered:
+    # a scratch that is dropped here is reused after the work queued on it
+
+    @staticmethod
+    def forward(ctx, x, w, grad_dtype):
+        device, K, N = x.device, x.shape[-1], w.shape[0]
+        M = math.prod(x.shape[:-1])
+        x2, w2 = _rows(x.reshape(M, K)), _rows(w)
+        keep = (KEEP_X if ctx.needs_input_grad[0] else 0) | (KEEP_W if ctx.needs_input_grad[1] else 0)
+        sizes = _linear_bytes(M, N, K, keep)
+        # kept for the backward pass: one byte an element of x and of w
+        saved = torch.empty(sizes[0], dtype=torch.uint8, device=device)
+        scratch = torch.empty(sizes[1], dtype=torch.uint8, device=device)
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=device)
+        _call(device, _lib.tgemm_fp8_linear_forward, M, N, K, _real_code(x, "x"), x2.data_ptr(), _ld(x2, "x"),
+              _real_code(w, "w"), w2.data_ptr(), _ld(w2, "w"), y.data_ptr(), N, keep, saved.data_ptr(), scratch.data_ptr())
+        if keep:
+            ctx.save_for_backward(saved)
+            ctx.args = M, N, K, keep, grad_dtype, x.shape, x.dtype, w.dtype
+        y = y.reshape(x.shape[:-1] + (N,)) if x.dim() != 2 else y
+        return y if x.dtype == torch.bfloat16 else y.to(x.dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gy):
+        (saved,) = ctx.saved_tensors
+        M, N, K, keep, grad_dtype, x_shape, x_dtype, w_dtype = ctx.args
+        device = gy.device
+        g = _rows(gy.reshape(M, N))  # a broadcast gradient (of a sum, say) has no rows of its own
+        scratch = torch.empty(_linear_bytes(M, N, K, keep)[2], dtype=torch.uint8, device=device)
+        dx = torch.empty((M, K), dtype=torch.bfloat16, device=device) if keep & KEEP_X else None
+        dw = torch.empty((N, K), dtype=torch.bfloat16, device=device) if keep & KEEP_W else None
+        _call(device, _lib.tgemm_fp8_linear_backward, M, N, K, _real_code(g, "gradient"), g.data_ptr(), _ld(g, "gradient"),
+              _fp8_code(grad_dtype), keep, saved.data_ptr(), None if dx is None else dx.data_ptr(), K,
+              None if dw is None else dw.data_ptr(), K, scratch.data_ptr())
+        if dx is not None:
+            dx = dx.reshape(x_shape).to(x_dtype)
+        return dx, None if dw is None else dw.to(w_dtype), None
 
 
-def linear_fp8(x, w, grad_dtype=None):
+def linear_fp8(x, w, grad_dtype=torch.float8_e4m3fn):
     """y = x @ w^T with x and w quantised to float8_e4m3fn, differentiable.
 
     x: (..., K), w: (N, K), each float32, bfloat16 or float16.  x is
     quantised with a scale for each 128 elements of a row, w for each 128 x
     128 block; y has x's dtype (the product itself is rounded to bfloat16).
     The backward pass quantises the gradient of y to ``grad_dtype``
-    (float8_e4m3fn by default, or float8_e5m2), along its rows for x's
-    gradient and along its columns for w's, and takes both products from the
-    8-bit images kept by the forward pass: dx = g w, dw = g^T x.  Rounding is
-    passed straight through.  Gradients have their inputs' dtypes.
+    (float8_e4m3fn or float8_e5m2), along its rows for x's gradient and along
+    its columns for w's, and takes both products from the 8-bit images kept by
+    the forward pass: dx = g w, dw = g^T x.  Rounding is passed straight
+    through.  Gradients have their inputs' dtypes.  A weight that does not
+    change between calls is better quantised once (:func:`quantize_fp8`, then
+    :func:`gemm_fp8`).
     """
-    global _linear_fn
-    import torch
-    grad_dtype = torch.float8_e4m3fn if grad_dtype is None else grad_dtype
     _fp8_code(grad_dtype)
     if not (x.is_cuda and w.is_cuda) or x.device != w.device:
         raise ValueError("x and w must be on one GPU (%s, %s)" % (x.device, w.device))
     if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
         raise ValueError("x %s and w %s do not make x @ w^T" % (tuple(x.shape), tuple(w.shape)))
-    if _linear_fn is None:
-        _linear_fn = _linear_fp8_function()
-    return _linear_fn.apply(x, w, grad_dtype)
+    return _LinearFp8.apply(x, w, grad_dtype)
 
 
 # ---- orthogonalised update ------------------------------------------------------
@@ -672,7 +712,6 @@ def orthogonalize(G, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e-7,
     included).  The workspace comes from torch's allocator on the current
     stream.
     """
-    import torch
     if not G.is_cuda:
         raise ValueError("G must be a GPU tensor")
     code = _real_code(G, "G")
@@ -701,14 +740,10 @@ def orthogonalize(G, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e-7,
     need = _lib.tgemm_orthogonalize_workspace_bytes(batch, rows, cols)
     if need < 0:
         raise ValueError("G of shape %s is out of range (2^20 rows and columns, 2^16 matrices)" % (tuple(G.shape),))
-    with torch.cuda.device(G.device):
-        # stream-ordered: the block returns to torch's pool for this stream
-        # when `ws` is dropped, after the work queued here
-        ws = torch.empty(need + 256, dtype=torch.uint8, device=G.device)
-        base = (ws.data_ptr() + 255) // 256 * 256
-        rc = _lib.tgemm_orthogonalize(batch, rows, cols, code, G.data_ptr(), ldg, stride_g, out.data_ptr(), ldo, stride_o,
-                                      int(steps), coef, float(eps), base, need,
-                                      torch.cuda.current_stream(G.device).cuda_stream)
-    if rc != OK:
-        raise TgemmError(rc, last_error())
+    # stream-ordered: the block returns to torch's pool for this stream when
+    # `ws` is dropped, after the work queued here; the pool's blocks start on
+    # 512-byte boundaries
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=G.device)
+    _call(G.device, _lib.tgemm_orthogonalize, batch, rows, cols, code, G.data_ptr(), ldg, stride_g, out.data_ptr(), ldo,
+          stride_o, int(steps), coef, float(eps), ws.data_ptr(), need)
     return out
