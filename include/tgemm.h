@@ -432,9 +432,10 @@ int tgemm_fp8_linear_backward(int64_t M, int64_t N, int64_t K, int32_t g_dtype, 
                               int32_t grad_fmt, int32_t keep, const void* saved, void* dx, int64_t lddx, void* dw,
                               int64_t lddw, void* scratch, void* stream);
 
-/* Name of the kernel tgemm_fp8_gemm launches for these sizes ("" where it
- * launches none). */
-const char* tgemm_fp8_gemm_kernel(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb);
+/* Name of the kernel tgemm_fp8_gemm launches for these sizes: of its first
+ * launch (piece 0) or, where it splits off the last columns or rows, of its
+ * second (piece 1); "" where there is no such launch. */
+const char* tgemm_fp8_gemm_kernel(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int32_t piece);
 
 /* ---- orthogonalised update --------------------------------------------------
  *

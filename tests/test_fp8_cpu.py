@@ -86,12 +86,18 @@ def test_gemm_of_nothing_needs_no_device(M, N):
 
 def test_kernel_choice():
     k = tl.gemm_fp8_kernel
-    assert k(0, 4, 4) == k(4, 0, 4) == k(-1, 4, 4) == ""
-    assert [k(m, 4096, 4096).split("_")[0] for m in (1, 16, 17, 32, 33, 64)] == ["rows16", "rows16", "rows32", "rows32",
-                                                                                "rows64", "rows64"]
-    assert k(4096, 4096, 4096).startswith("t256x256x128")
+    assert k(0, 4, 4) == k(4, 0, 4) == k(-1, 4, 4) == k(4, 4, 4, piece=1) == k(4, 4, 4, piece=-1) == ""
+    name = lambda *a, **kw: k(*a, **kw).split("_")[0]  # noqa: E731
+    assert [name(m, 4096, 4096) for m in (1, 16, 17, 32)] == ["rows16", "rows16", "rows32", "rows32"]
+    assert [name(4096, n, 4096) for n in (1, 16, 17, 32)] == ["rows16", "rows16", "rows32", "rows32"]
+    assert name(100, 4096, 4096) == name(512, 4096, 4096) == "t64x64x128"
+    assert k(1024, 4096, 4096) == "t128x128x128_w2x4_s4_slice" and k(2048, 4096, 4096) == "t128x128x128_w2x2_s2_slice"
+    assert name(4096, 4096, 4096) == "t256x256x128"
+    # whole tiles, then the last columns or rows
+    for m, n in ((4095, 4097), (4097, 4096), (4100, 4096)):
+        assert name(m, n, 4104) == "t256x256x128" and name(m, n, 4104, piece=1).startswith("rows")
     # rows too long for a tiled kernel's 32-bit offsets
-    assert k(4096, 4096, 64, lda=2 ** 31).startswith("rows64") and k(4096, 4096, 64, ldb=2 ** 31).startswith("rows64")
+    assert name(4096, 4096, 64, lda=2 ** 31).startswith("rows") and name(4096, 4096, 64, ldb=2 ** 31).startswith("rows")
 
 
 def test_binding_refuses_before_any_launch():

@@ -176,12 +176,16 @@ def test_gemm_formats(M, N, K, fa, fb):
 
 # sizes that reach each kernel of the choice; the large ones against a product
 # in float64 on the GPU
-@pytest.mark.parametrize("M,N,K,kernel", [
-    (7, 520, 1300, "rows16"), (20, 520, 1300, "rows32"), (50, 520, 1300, "rows64"), (300, 520, 1300, "t64x64"),
-    (1500, 1400, 700, "t128x128"), (1500, 1400, 1000, "t128x128"), (3600, 3500, 300, "t256x256"),
-    (3585, 3583, 1290, "t256x256"), (4096, 4096, 128, "t256x256"), (3500, 3600, 100, "t256x256")])
-def test_gemm_every_kernel(M, N, K, kernel):
+@pytest.mark.parametrize("M,N,K,kernel,last", [
+    (7, 520, 1300, "rows16", ""), (20, 5000, 1300, "rows32", ""), (520, 9, 1300, "rows16", ""),
+    (5001, 30, 1300, "rows32", ""), (300, 1400, 1300, "t64x64", ""), (1500, 1400, 1000, "t64x64", ""),
+    (1900, 1990, 2100, "t128x128x128_w2x4_s4", ""), (2048, 2031, 3001, "t128x128x128_w2x4_s4", ""),
+    (2000, 3900, 2500, "t128x128x128_w2x2_s2", ""), (3600, 3500, 300, "t256x256", ""),
+    (3585, 3583, 1290, "t256x256", ""), (4096, 4096, 128, "t256x256", ""), (3500, 3600, 100, "t256x256", ""),
+    (4095, 4097, 520, "t256x256", "rows16"), (4128, 4090, 300, "t256x256", "rows32"), (4070, 4106, 700, "t256x256", "rows16")])
+def test_gemm_every_kernel(M, N, K, kernel, last):
     assert tl.gemm_fp8_kernel(M, N, K).startswith(kernel)
+    assert tl.gemm_fp8_kernel(M, N, K, piece=1).startswith(last) and bool(tl.gemm_fp8_kernel(M, N, K, piece=1)) == bool(last)
     fa = "e5m2" if M % 2 else "e4m3"
     a, sa = tl.quantize_fp8(draw(M, K, 1).cuda(), dtype=FMT[fa])
     b, sb = tl.quantize_fp8(draw(N, K, 2).cuda())
@@ -318,7 +322,7 @@ def test_rows_longer_than_32_bit_offsets():
     buf = torch.empty((M - 1) * ld + K, dtype=torch.uint8, device="cuda")
     big = buf.as_strided((M, K), (ld, 1))
     big.copy_(a.view(torch.uint8))
-    assert tl.gemm_fp8_kernel(M, N, K, lda=1 << 27).startswith("rows64")
+    assert tl.gemm_fp8_kernel(M, N, K, lda=1 << 27).startswith("rows")
     c = tl.gemm_fp8(big.view(a.dtype), sa, b, sb)
     check_product(c, av, bv, K)
 

@@ -8,8 +8,8 @@ namespace tg {
 
 struct Fp8Args {
     NtOperands op;
-    uint16_t* C;
-    int64_t ldc;
+    uint16_t* C;             // element (m, n) at C[m row + n col]; tiled kernels: col = 1
+    int64_t row, col;
     int32_t tiles_m, tiles_n;
     int32_t stream;  // 1: C's rows are whole cache lines, written past the L2
 };
@@ -23,8 +23,8 @@ struct Fp8Kernel {
     char name[64];
 };
 
-// Tiles, from the largest; and the kernels for few rows.
-enum Fp8Pick { PICK_256 = 0, PICK_128, PICK_64, PICK_ROWS16, PICK_ROWS32, PICK_ROWS64, PICK_COUNT };
+// Tiles, from the largest; and the kernels for few rows of A.
+enum Fp8Pick { PICK_256 = 0, PICK_128, PICK_128_PAIR, PICK_64, PICK_ROWS16, PICK_ROWS32, PICK_COUNT };
 
 const Fp8Kernel* fp8_kernels_e4m3_e4m3();
 const Fp8Kernel* fp8_kernels_e4m3_e5m2();
@@ -69,7 +69,7 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g) {
             uint16_t v[G::FN];
 #pragma unroll
             for (int j = 0; j < G::FN; ++j) v[j] = bf16_bits(acc[i][j][r]);
-            uint16_t* dst = g.C + (int64_t)m * g.ldc + n;
+            uint16_t* dst = g.C + (int64_t)m * g.row + n;
             if (m < g.op.M) {
                 if (G::FN >= 2 && g.stream && whole) store_stream(dst, v);
                 else if (whole) __builtin_memcpy(dst, v, sizeof v);
@@ -87,7 +87,8 @@ __global__ __launch_bounds__(G::NT) void fp8_tile_kernel(Fp8Args g) {
     fp8_tile<G>(g);
 }
 
-// Few rows of A (a decode batch): bound by one read of B.  A workgroup takes
+// Few rows of A (a decode batch; or, with the operands and C's strides
+// swapped, few rows of B): bound by one read of B.  A workgroup takes
 // 16 rows of B and 16 MT rows of A; its NW waves deal the 128-blocks of K
 // among them, operands going straight to registers (a wave's blocks are its
 // own: nothing to share through LDS), and add their sums through LDS at the
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(64 * NW) void fp8_rows_kernel(Fp8Args g) {
 #pragma unroll
         for (int w = 0; w < NW; ++w) sum += part[w][e];
         const int m = m0 + (e >> 4), n = n0 + (e & 15);
-        if (m < o.M && n < o.N) g.C[(int64_t)m * g.ldc + n] = bf16_bits(sum);
+        if (m < o.M && n < o.N) g.C[(int64_t)m * g.row + (int64_t)n * g.col] = bf16_bits(sum);
     }
 }
 
@@ -196,18 +197,25 @@ const Fp8Kernel* fp8_kernel_table() {
     typedef NtF8<FA, FB> Tr;
     // 256 x 256: four waves of 128 x 128, one a SIMD.  Against eight of 128 x
     // 64 they read a third less from LDS for the same matrix instructions,
-    // which leaves the power budget a higher clock (8192^3 e4m3 395 us against
-    // 425).  In the steady loop the matrix cores are busy 91 % of the cycles.
+    // which leaves the power budget a higher clock (e4m3 8192^3 354 us against
+    // 366, 4096^3 both 52.5).  In the steady loop the matrix cores are busy
+    // 91 % of the cycles.
     typedef NtGemm<Tr, 256, 256, 2, 2, 2, false> G256;
-    typedef NtGemm<Tr, 128, 128, 2, 2, 4, true> G128;
-    typedef NtGemm<Tr, 64, 64, 2, 2, 8, true> G64;
+    // 128 x 128 with a compute unit to itself: eight waves, four slots (four
+    // waves: 1024x4096x4096 24.5 us against 22.7).  Where there are several
+    // rounds: two slots, two workgroups a unit (2048x4096x4096 42 us -> 34.5).
+    typedef NtGemm<Tr, 128, 128, 2, 4, 4, true> G128;
+    typedef NtGemm<Tr, 128, 128, 2, 2, 2, true> G128P;
+    // 64 x 64: four slots, two workgroups a unit (eight and one: as fast
+    // alone, 512x4096x4096 19.9 us against 16.5).
+    typedef NtGemm<Tr, 64, 64, 2, 2, 4, true> G64;
     static const Fp8Kernel table[PICK_COUNT] = {
         {fp8_tile_kernel<G256>, G256::BM, G256::BN, G256::NT, "t256x256x128_w2x2_s2"},
-        {fp8_tile_kernel<G128>, G128::BM, G128::BN, G128::NT, "t128x128x128_w2x2_s4_slice"},
-        {fp8_tile_kernel<G64>, G64::BM, G64::BN, G64::NT, "t64x64x128_w2x2_s8_slice"},
+        {fp8_tile_kernel<G128>, G128::BM, G128::BN, G128::NT, "t128x128x128_w2x4_s4_slice"},
+        {fp8_tile_kernel<G128P>, G128P::BM, G128P::BN, G128P::NT, "t128x128x128_w2x2_s2_slice"},
+        {fp8_tile_kernel<G64>, G64::BM, G64::BN, G64::NT, "t64x64x128_w2x2_s4_slice"},
         {fp8_rows_kernel<FA, FB, 1, 8, 4>, 16, 16, 512, "rows16_w8"},
         {fp8_rows_kernel<FA, FB, 2, 8, 4>, 32, 16, 512, "rows32_w8"},
-        {fp8_rows_kernel<FA, FB, 4, 8, 2>, 64, 16, 512, "rows64_w8"},
     };
     return table;
 }

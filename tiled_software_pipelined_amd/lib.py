@@ -122,7 +122,7 @@ def _load():
     lib.tgemm_fp8_quantize.restype = ctypes.c_int
     lib.tgemm_fp8_gemm.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, i32, vp, i64, vp, i64, vp, i64, vp]
     lib.tgemm_fp8_gemm.restype = ctypes.c_int
-    lib.tgemm_fp8_gemm_kernel.argtypes = [i64, i64, i64, i64, i64]
+    lib.tgemm_fp8_gemm_kernel.argtypes = [i64, i64, i64, i64, i64, i32]
     lib.tgemm_fp8_gemm_kernel.restype = ctypes.c_char_p
     lib.tgemm_fp8_linear_bytes.argtypes = [i64, i64, i64, i32, ctypes.POINTER(i64)]
     lib.tgemm_fp8_linear_bytes.restype = ctypes.c_int
@@ -582,9 +582,10 @@ def gemm_fp8(A, SA, B, SB, out=None):
     return out
 
 
-def gemm_fp8_kernel(M, N, K, lda=None, ldb=None) -> str:
-    """Name of the kernel :func:`gemm_fp8` launches for these sizes."""
-    return _lib.tgemm_fp8_gemm_kernel(M, N, K, K if lda is None else lda, K if ldb is None else ldb).decode()
+def gemm_fp8_kernel(M, N, K, lda=None, ldb=None, piece=0) -> str:
+    """Name of the kernel :func:`gemm_fp8` launches first for these sizes, or
+    (piece 1) for the columns or rows it splits off; "" where there is none."""
+    return _lib.tgemm_fp8_gemm_kernel(M, N, K, K if lda is None else lda, K if ldb is None else ldb, piece).decode()
 
 
 def _rows(t):
