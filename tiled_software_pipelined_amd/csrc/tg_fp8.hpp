@@ -135,20 +135,13 @@ __global__ __launch_bounds__(64 * NW) void fp8_rows_kernel(Fp8Args g) {
             }
         } else {
             // the last, partial block: zero past the row's end
-            const int end = o.k - at;
-            auto chunk = [&](const char* row, int64_t p) {
-                union { i32x4 v; uint8_t e[16]; } u;
-#pragma unroll
-                for (int t = 0; t < 16; ++t)
-                    u.e[t] = load_or_zero(reinterpret_cast<const uint8_t*>(row) + p + t, p + t < end);
-                return u.v;
-            };
-            x.b[0] = chunk(brow, k0);
-            x.b[1] = chunk(brow, k0 + 64);
+            const int p = (int)k0 + at;
+            x.b[0] = row_end_chunk(brow - at, p, o.k);
+            x.b[1] = row_end_chunk(brow - at, p + 64, o.k);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-                x.a[t][0] = chunk(arow[t], k0);
-                x.a[t][1] = chunk(arow[t], k0 + 64);
+                x.a[t][0] = row_end_chunk(arow[t] - at, p, o.k);
+                x.a[t][1] = row_end_chunk(arow[t] - at, p + 64, o.k);
             }
         }
         x.sb = bs[(int64_t)kb * o.ldsb];

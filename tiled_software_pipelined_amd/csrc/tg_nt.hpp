@@ -101,6 +101,22 @@ __device__ __forceinline__ void grouped_tile(int r, int tiles_m, int tiles_n, in
     tn = in_group / rows;
 }
 
+// Bytes at .. at + 15 of a row of `end` bytes, zero past its end: one 16-byte
+// load that ends inside the row, shifted into place (rows shorter than that:
+// byte loads).
+__device__ __forceinline__ i32x4 row_end_chunk(const char* row, int at, int end) {
+    if (end >= 16) {  // wave-uniform
+        const int sh = max(at - (end - 16), 0);
+        const i32x4 x = load16(row + (at - sh));
+        const i32x4 y = funnel16(x, i32x4{0, 0, 0, 0}, sh & 15);
+        return sh < 16 ? y : i32x4{0, 0, 0, 0};
+    }
+    union { i32x4 v; uint8_t b[16]; } u;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) u.b[t] = load_or_zero(reinterpret_cast<const uint8_t*>(row) + at + t, at + t < end);
+    return u.v;
+}
+
 // AHEAD: every fragment register is refilled with the next slice's values
 // right after its use, a whole slice ahead (waves with few matrix
 // instructions per K step); otherwise fragments are double-buffered by K
@@ -361,30 +377,23 @@ struct NtGemm {
     // ---- the last, partial slice -----------------------------------------------
     // `left` (1 .. 127) bytes of each row, through registers: zero past the
     // row's end (a zero in both operands adds nothing).
-    __device__ static __forceinline__ i32x4 tail_chunk(const char* rowp, int at, int end) {
-        if (at + 16 <= end) return load16(rowp + at);
-        union { i32x4 v; uint8_t b[16]; } u;
-#pragma unroll
-        for (int t = 0; t < 16; ++t)
-            u.b[t] = load_or_zero(reinterpret_cast<const uint8_t*>(rowp) + at + t, at + t < end);
-        return u.v;
-    }
     __device__ static __forceinline__ void fill_tail(TG_LDS char* slot, const NtOperands& g, int m0, int n0, int full,
                                                      int wave, int lane) {
         const int tid = threadIdx.x;
-#pragma unroll 1
-        for (int q = 0; q < A_PER; ++q) {
-            const int p = (q * NT + tid) >> 3, c = chunk_of(p, tid & 7);
-            const char* rowp = g.a + (int64_t)min(m0 + row_at<WTM>(p), g.M - 1) * g.lda;
-            *reinterpret_cast<TG_LDS i32x4*>(slot + (q * NT + tid) * 16) = tail_chunk(rowp, full * ROW + c * 16, g.k);
+        // every chunk's load is in flight before the first is stored
+        i32x4 v[A_PER + B_PER];
+#pragma unroll
+        for (int q = 0; q < A_PER + B_PER; ++q) {
+            const bool a = q < A_PER;
+            const int p = ((a ? q : q - A_PER) * NT + tid) >> 3, c = chunk_of(p, tid & 7);
+            const char* rowp = a ? g.a + (int64_t)min(m0 + row_at<WTM>(p), g.M - 1) * g.lda
+                                 : g.b + (int64_t)min(n0 + row_at<WTN>(p), g.N - 1) * g.ldb;
+            v[q] = row_end_chunk(rowp, full * ROW + c * 16, g.k);
         }
-#pragma unroll 1
-        for (int q = 0; q < B_PER; ++q) {
-            const int p = (q * NT + tid) >> 3, c = chunk_of(p, tid & 7);
-            const char* rowp = g.b + (int64_t)min(n0 + row_at<WTN>(p), g.N - 1) * g.ldb;
-            *reinterpret_cast<TG_LDS i32x4*>(slot + A_BYTES + (q * NT + tid) * 16) =
-                tail_chunk(rowp, full * ROW + c * 16, g.k);
-        }
+#pragma unroll
+        for (int q = 0; q < A_PER + B_PER; ++q)
+            *reinterpret_cast<TG_LDS i32x4*>(slot + (q < A_PER ? 0 : A_BYTES) +
+                                             ((q < A_PER ? q : q - A_PER) * NT + tid) * 16) = v[q];
         if constexpr (Tr::SCALED) {
             if (tid < (BM + BN) / 4) {
                 const uint8_t* p = tid < BM / 4
