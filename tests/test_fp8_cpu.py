@@ -46,6 +46,7 @@ def q(rows, cols, dtype=0, X=P(64), ldx=None, fmt=0, block=0, Q=P(64), ldq=None,
     (dict(rows=4, cols=4, ldx=3), -1), (dict(rows=4, cols=4, ldq=3), -1), (dict(rows=4, cols=4, lds=3), -1),
     (dict(rows=4, cols=4, Qt=P(64), St=P(64), ldqt=3, ldst=4), -1),
     (dict(rows=4, cols=4, Qt=P(64), St=P(64), ldqt=4, ldst=3), -1),
+    (dict(rows=4, cols=4, ldx=2 ** 41), -1), (dict(rows=4, cols=4, lds=2 ** 62), -1),
     (dict(rows=4, cols=4, X=None), -2), (dict(rows=4, cols=4, Q=None), -2), (dict(rows=4, cols=4, S=None), -2),
     (dict(rows=4, cols=4, Qt=P(64), ldqt=4, ldst=4), -2), (dict(rows=4, cols=4, St=P(64), ldqt=4, ldst=4), -2),
     (dict(rows=4, cols=4, X=P(66)), -3), (dict(rows=4, cols=4, dtype=1, X=P(65)), -3),
@@ -70,6 +71,7 @@ def g(M, N, K, fa=0, A=P(64), lda=None, SA=P(64), ldsa=None, fb=0, B=P(64), ldb=
     (dict(M=-1, N=4, K=4), -1), (dict(M=4, N=2 ** 31, K=4), -1), (dict(M=4, N=4, K=2 ** 31 - 1), -1),
     (dict(M=4, N=4, K=4, fa=2), -1), (dict(M=4, N=4, K=4, fb=-1), -1), (dict(M=4, N=4, K=4, lda=3), -1),
     (dict(M=4, N=4, K=4, ldb=3), -1), (dict(M=8, N=4, K=4, ldsa=4), -1), (dict(M=4, N=8, K=4, ldsb=4), -1),
+    (dict(M=4, N=4, K=4, lda=2 ** 62), -1), (dict(M=4, N=4, K=4, ldc=2 ** 41), -1),
     (dict(M=4, N=4, K=4, ldc=3), -1), (dict(M=4, N=4, K=4, A=None), -2), (dict(M=4, N=4, K=4, B=None), -2),
     (dict(M=4, N=4, K=4, SA=None), -2), (dict(M=4, N=4, K=4, SB=None), -2), (dict(M=4, N=4, K=4, C=None), -2),
     (dict(M=4, N=4, K=0, C=None), -2), (dict(M=4, N=4, K=4, C=P(65)), -3), (dict(M=4, N=4, K=4, ldsa=6), -3),
@@ -148,7 +150,8 @@ def lin(forward, M=4, N=6, K=8, **kw):
 
 
 @pytest.mark.parametrize("forward,kw,code", [
-    (True, dict(M=-1), -1), (True, dict(N=2 ** 31), -1), (True, dict(keep=4), -1), (True, dict(xd=2), -1),
+    (True, dict(M=-1), -1), (True, dict(N=2 ** 31), -1), (True, dict(M=2 ** 30, N=2 ** 30), -1),
+    (True, dict(ldx=2 ** 41), -1), (True, dict(keep=4), -1), (True, dict(xd=2), -1),
     (True, dict(wd=5), -1), (True, dict(ldx=7), -1), (True, dict(ldw=7), -1), (True, dict(ldy=5), -1),
     (True, dict(x=None), -2), (True, dict(w=None), -2), (True, dict(y=None), -2), (True, dict(saved=None), -2),
     (True, dict(scratch=None), -2), (True, dict(x=P(257)), -3), (True, dict(xd=0, x=P(258)), -3), (True, dict(y=P(257)), -3),

@@ -201,6 +201,43 @@ def test_gemm_every_kernel(M, N, K, kernel, last):
     assert float((c - want).norm()) <= 2.0 ** -8 * float(want.norm())
 
 
+def test_gemm_random_shapes():
+    import random
+    r = random.Random(7)
+    for i in range(60):
+        M, N, K = (max(1, int(2 ** r.uniform(0, top))) for top in (11.5, 11.5, 12))
+        fa, fb = r.choice(["e4m3", "e5m2"]), r.choice(["e4m3", "e5m2"])
+        a, sa = tl.quantize_fp8(draw(M, K, i, spread=0.5).cuda(), dtype=FMT[fa])
+        b, sb = tl.quantize_fp8(draw(N, K, i + 100, spread=0.5).cuda(), dtype=FMT[fb])
+
+        def v(q, s):
+            e = (s.contiguous().view(torch.uint8).double() - 127).t().repeat_interleave(128, 1)[:, :K]
+            return q.double() * torch.exp2(e)
+        av, bv = v(a, sa), v(b, sb)
+        want, mag = av @ bv.t(), av.abs() @ bv.abs().t()
+        off = (2.0 ** -10 + (K / 8 + 16) * 2.0 ** -24) * mag
+        c = tl.gemm_fp8(a, sa, b, sb).double()
+        assert bool(((c - want).abs() <= 2.0 ** -8 * (want.abs() + off) + off).all()), (M, N, K, fa, fb)
+
+
+def test_gemm_two_at_once():
+    # two products on two streams, over and over, each against its own result
+    sets = []
+    for M, N, K, s in ((300, 900, 700, 1), (4, 3000, 1500, 2)):
+        a, sa, _ = operand(M, K, s)
+        b, sb, _ = operand(N, K, s + 10)
+        sets.append((a, sa, b, sb, tl.gemm_fp8(a, sa, b, sb)))
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for st, x in zip(streams, sets):
+            with torch.cuda.stream(st):
+                got.append((tl.gemm_fp8(*x[:4]), x[4]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(c, want) for c, want in got)
+
+
 def test_matrix_instruction_alignment():
     # what gemm_bound rests on: a product 13 binades below the largest of its
     # group of eight survives, and groups are added to 26 binades; the large
@@ -315,16 +352,18 @@ def test_gemm_refusals():
 
 
 def test_rows_longer_than_32_bit_offsets():
-    # lda of 2^25: the tile's 32-bit offsets do not hold 127 rows of it
-    M, N, K, ld = 70, 70, 200, 1 << 25
+    # lda of 2^26: a 64-row tile's offsets pass 2^31 and still fit in 32 bits; of
+    # 2^27 they do not, and 64-bit addresses take over
+    M, N, K, ld = 70, 4100, 1000, 1 << 26
     a, sa, av = operand(M, K, 1)
     b, sb, bv = operand(N, K, 2)
     buf = torch.empty((M - 1) * ld + K, dtype=torch.uint8, device="cuda")
-    big = buf.as_strided((M, K), (ld, 1))
-    big.copy_(a.view(torch.uint8))
-    assert tl.gemm_fp8_kernel(M, N, K, lda=1 << 27).startswith("rows")
-    c = tl.gemm_fp8(big.view(a.dtype), sa, b, sb)
-    check_product(c, av, bv, K)
+    for m, step, kernel in ((M, ld, "t64x64"), (M // 2, 2 * ld, "rows")):
+        assert tl.gemm_fp8_kernel(m, N, K, lda=step).startswith(kernel)
+        big = buf[:(m - 1) * step + K].as_strided((m, K), (step, 1))
+        big.copy_(a[:m].view(torch.uint8))
+        s = sa.view(torch.uint8)[:, :m]
+        check_product(tl.gemm_fp8(big.view(a.dtype), s, b, sb), av[:m], bv, K)
 
 
 def test_on_another_stream_and_replayed_from_a_graph():
@@ -424,6 +463,15 @@ def test_linear_shapes_strides_and_partial_gradients():
         tl.linear_fp8(x3, w[:, :95])
     with pytest.raises(ValueError):
         tl.linear_fp8(x3, w.cpu())
+    # parameters that want gradients, where none are recorded
+    a, b = x3.clone().requires_grad_(), w.clone().requires_grad_()
+    with torch.no_grad():
+        z = tl.linear_fp8(a, b)
+    assert torch.equal(z, y) and not z.requires_grad
+    # second derivatives are refused, not wrong
+    (gx,) = torch.autograd.grad(tl.linear_fp8(a, b).float().square().sum(), a, create_graph=True)
+    with pytest.raises(RuntimeError):
+        gx.sum().backward()
 
 
 def test_linear_without_rows():

@@ -21,7 +21,7 @@ def call(batch=1, rows=4, cols=6, dtype=0, G=P(256), ldg=None, stride_g=None, O=
 
 @pytest.mark.parametrize("kw,code", [
     (dict(batch=-1), -1), (dict(rows=-1), -1), (dict(cols=(1 << 20) + 1), -1), (dict(batch=(1 << 16) + 1), -1),
-    (dict(dtype=2), -1), (dict(ldg=5), -1), (dict(ldo=5), -1), (dict(batch=2, stride_g=23), -1),
+    (dict(dtype=2), -1), (dict(ldg=2 ** 62), -1), (dict(batch=2, stride_o=2 ** 62), -1), (dict(ldg=5), -1), (dict(ldo=5), -1), (dict(batch=2, stride_g=23), -1),
     (dict(batch=2, stride_o=23), -1), (dict(steps=0), -1), (dict(steps=65), -1), (dict(eps=-1e-9), -1),
     (dict(eps=float("nan")), -1), (dict(coef=()), -2), (dict(steps=1, coef=(float("nan"), 0, 0)), -1),
     (dict(steps=1, coef=(1, float("inf"), 0)), -1), (dict(steps=2, coef=(4, 0, 0) * 2), -1),

@@ -72,7 +72,8 @@ static Piece best_piece(const Fp8Kernel* t, int64_t m0, int64_t n0, int64_t M, i
         if (p <= PICK_64 && !offsets_fit(t[i], lda, ldb)) continue;
         const bool swap = p >= PICK_ROWS16 && N < M;
         const int64_t few = swap ? N : M, many = swap ? M : N;
-        if (((few + t[i].bm - 1) / t[i].bm) * ((many + t[i].bn - 1) / t[i].bn) > INT_MAX) continue;
+        const int64_t n = ((few + t[i].bm - 1) / t[i].bm) * ((many + t[i].bn - 1) / t[i].bn);
+        if (n > INT_MAX || !grid_fits((double)n, t[i].threads)) continue;
         const double c = time_of(p, t[i], few, many, K);
         if (best.pick == PICK_COUNT || c < best.time) best = Piece{p, swap, m0, n0, M, N, c};
     }
@@ -113,7 +114,7 @@ extern "C" {
 
 const char* tgemm_fp8_gemm_kernel(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int32_t piece) {
     using namespace tg;
-    if (!sizes_ok(M, N, K) || M == 0 || N == 0) return "";
+    if (!sizes_ok(M, N, K) || M == 0 || N == 0 || lda > MOST_STRIDE || ldb > MOST_STRIDE) return "";
     const Fp8Kernel* t = fp8_kernels_e4m3_e4m3();
     Piece p[2];
     return piece >= 0 && piece < pieces_of(t, M, N, K, lda, ldb, p) ? t[p[piece].pick].name : "";
@@ -133,6 +134,10 @@ int tgemm_fp8_gemm(int64_t M, int64_t N, int64_t K, int32_t fmt_a, const void* A
     }
     if (lda < K || ldb < K || ldsa < M || ldsb < N || ldc < N) {
         set_error("a leading dimension is shorter than its row");
+        return TGEMM_E_ARG;
+    }
+    if (lda > MOST_STRIDE || ldb > MOST_STRIDE || ldsa > MOST_STRIDE || ldsb > MOST_STRIDE || ldc > MOST_STRIDE) {
+        set_error("a leading dimension is out of range");
         return TGEMM_E_ARG;
     }
     if (M == 0 || N == 0) {

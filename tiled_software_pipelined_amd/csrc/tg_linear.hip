@@ -45,7 +45,9 @@ static LinearLayout linear_layout(int64_t M, int64_t N, int64_t K, int keep) {
 
 static bool linear_sizes_ok(int64_t M, int64_t N, int64_t K, int32_t keep) {
     const int64_t most = INT_MAX - 256;
-    if (M < 0 || N < 0 || K < 0 || M > most || N > most || K > most || (keep & ~3)) {
+    const double area = 281474976710656.0;  // 2^48 elements: more than any memory, sums stay inside 64 bits
+    if (M < 0 || N < 0 || K < 0 || M > most || N > most || K > most || (keep & ~3) || (double)M * N > area ||
+        (double)M * K > area || (double)N * K > area) {
         set_error("M=%lld N=%lld K=%lld keep=%d out of range", (long long)M, (long long)N, (long long)K, keep);
         return false;
     }
@@ -58,8 +60,8 @@ static int check_operand(const char* name, int32_t dtype, const void* p, int64_t
         set_error("%s: dtype %d is not float32, bfloat16 or float16", name, dtype);
         return TGEMM_E_ARG;
     }
-    if (ld < cols) {
-        set_error("%s: leading dimension shorter than its row", name);
+    if (ld < cols || ld > MOST_STRIDE) {
+        set_error("%s: leading dimension shorter than its row, or out of range", name);
         return TGEMM_E_ARG;
     }
     if (rows > 0 && cols > 0 && !p) {

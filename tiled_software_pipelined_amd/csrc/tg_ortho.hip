@@ -653,6 +653,10 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
         set_error("a leading dimension is shorter than its row");
         return TGEMM_E_ARG;
     }
+    if (ldg > MOST_STRIDE || ldo > MOST_STRIDE || (batch > 1 && (stride_g > MOST_STRIDE || stride_o > MOST_STRIDE))) {
+        set_error("a stride is out of range");
+        return TGEMM_E_ARG;
+    }
     if (batch > 1 && ((rows - 1) * ldg + cols > stride_g || (rows - 1) * ldo + cols > stride_o)) {
         set_error("matrices of the batch overlap");
         return TGEMM_E_ARG;
@@ -695,7 +699,8 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     }
     const int64_t ut = p.upd->tile, tri = p.tri, upd = (p.mp / ut) * (p.np / ut);
     const int64_t load = (p.mp / 64) * (p.np / 64);
-    if (batch * tri > INT_MAX || batch * upd > INT_MAX || batch * load > INT_MAX ||
+    if (!grid_fits((double)(batch * tri), p.sym->threads) || !grid_fits((double)(batch * upd), p.upd->threads) ||
+        !grid_fits((double)(batch * load), 256) ||
         255 * 2 * (p.np > p.ms ? p.np : p.ms) + 128 > INT64_C(0xffffffff)) {  // a tile's copies take 32-bit offsets
 
         set_error("too many tiles");

@@ -361,6 +361,10 @@ extern "C" int tgemm_fp8_quantize(int64_t rows, int64_t cols, int32_t dtype, con
         set_error("a leading dimension is shorter than its row");
         return TGEMM_E_ARG;
     }
+    if (ldx > MOST_STRIDE || ldq > MOST_STRIDE || lds > MOST_STRIDE || (trans && (ldqt > MOST_STRIDE || ldst > MOST_STRIDE))) {
+        set_error("a leading dimension is out of range");
+        return TGEMM_E_ARG;
+    }
     if (rows == 0 || cols == 0) {
         clear_error();
         return TGEMM_OK;
@@ -374,7 +378,7 @@ extern "C" int tgemm_fp8_quantize(int64_t rows, int64_t cols, int32_t dtype, con
         return TGEMM_E_ALIGN;
     }
     const int64_t blocks_c = (cols + 127) / 128, blocks = blocks_c * ((rows + 127) / 128);
-    if (blocks > INT_MAX) {
+    if (blocks > INT_MAX || !grid_fits((double)blocks, 256)) {
         set_error("%lld x %lld has too many blocks", (long long)rows, (long long)cols);
         return TGEMM_E_ARG;
     }

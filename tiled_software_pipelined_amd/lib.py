@@ -604,28 +604,32 @@ def _linear_bytes(M, N, K, keep):
     return tuple(max(v, 1) for v in n)
 
 
-class _LinearFp8(torch.autograd.Function):
-    # torch's allocator gives blocks on 512-byte boundaries, stream-ordered:
-    # a scratch that is dropped here is reused after the work queued on it
+def _linear_forward(x, w, keep):
+    """y of shape (..., N) in x's dtype, and the buffer for the backward pass.
+    (torch's allocator gives stream-ordered blocks on 512-byte boundaries: a
+    scratch that is dropped here is reused after the work queued on it.)"""
+    device, K, N = x.device, x.shape[-1], w.shape[0]
+    M = math.prod(x.shape[:-1])
+    x2, w2 = _rows(x.reshape(M, K)), _rows(w)
+    sizes = _linear_bytes(M, N, K, keep)
+    # kept for the backward pass: one byte an element of x and of w
+    saved = torch.empty(sizes[0], dtype=torch.uint8, device=device)
+    scratch = torch.empty(sizes[1], dtype=torch.uint8, device=device)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=device)
+    _call(device, _lib.tgemm_fp8_linear_forward, M, N, K, _real_code(x, "x"), x2.data_ptr(), _ld(x2, "x"),
+          _real_code(w, "w"), w2.data_ptr(), _ld(w2, "w"), y.data_ptr(), N, keep, saved.data_ptr(), scratch.data_ptr())
+    y = y.reshape(x.shape[:-1] + (N,)) if x.dim() != 2 else y
+    return y if x.dtype == torch.bfloat16 else y.to(x.dtype), saved
 
+
+class _LinearFp8(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, grad_dtype):
-        device, K, N = x.device, x.shape[-1], w.shape[0]
-        M = math.prod(x.shape[:-1])
-        x2, w2 = _rows(x.reshape(M, K)), _rows(w)
         keep = (KEEP_X if ctx.needs_input_grad[0] else 0) | (KEEP_W if ctx.needs_input_grad[1] else 0)
-        sizes = _linear_bytes(M, N, K, keep)
-        # kept for the backward pass: one byte an element of x and of w
-        saved = torch.empty(sizes[0], dtype=torch.uint8, device=device)
-        scratch = torch.empty(sizes[1], dtype=torch.uint8, device=device)
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=device)
-        _call(device, _lib.tgemm_fp8_linear_forward, M, N, K, _real_code(x, "x"), x2.data_ptr(), _ld(x2, "x"),
-              _real_code(w, "w"), w2.data_ptr(), _ld(w2, "w"), y.data_ptr(), N, keep, saved.data_ptr(), scratch.data_ptr())
-        if keep:
-            ctx.save_for_backward(saved)
-            ctx.args = M, N, K, keep, grad_dtype, x.shape, x.dtype, w.dtype
-        y = y.reshape(x.shape[:-1] + (N,)) if x.dim() != 2 else y
-        return y if x.dtype == torch.bfloat16 else y.to(x.dtype)
+        y, saved = _linear_forward(x, w, keep)
+        ctx.save_for_backward(saved)
+        ctx.args = math.prod(x.shape[:-1]), w.shape[0], x.shape[-1], keep, grad_dtype, x.shape, x.dtype, w.dtype
+        return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -655,15 +659,20 @@ def linear_fp8(x, w, grad_dtype=torch.float8_e4m3fn):
     (float8_e4m3fn or float8_e5m2), along its rows for x's gradient and along
     its columns for w's, and takes both products from the 8-bit images kept by
     the forward pass: dx = g w, dw = g^T x.  Rounding is passed straight
-    through.  Gradients have their inputs' dtypes.  A weight that does not
-    change between calls is better quantised once (:func:`quantize_fp8`, then
-    :func:`gemm_fp8`).
+    through.  Gradients have their inputs' dtypes; second derivatives are
+    refused.  A weight that does not change between calls is better quantised
+    once (:func:`quantize_fp8`, then :func:`gemm_fp8`).  To capture a training
+    step into a graph, capture torch.autograd.grad, or make sure that no eager
+    graph of the same leaves is alive: torch's nodes that accumulate into
+    ``.grad`` stay on the stream of the first one.
     """
     _fp8_code(grad_dtype)
     if not (x.is_cuda and w.is_cuda) or x.device != w.device:
         raise ValueError("x and w must be on one GPU (%s, %s)" % (x.device, w.device))
     if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
         raise ValueError("x %s and w %s do not make x @ w^T" % (tuple(x.shape), tuple(w.shape)))
+    if not (torch.is_grad_enabled() and (x.requires_grad or w.requires_grad)):
+        return _linear_forward(x, w, 0)[0]
     return _LinearFp8.apply(x, w, grad_dtype)
 
 
@@ -720,7 +729,7 @@ def orthogonalize(G, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e-7,
         raise ValueError("G must have at least 2 dimensions")
     flat = list(coefficients)
     if len(flat) == 3 and not hasattr(flat[0], "__len__"):
-        flat = flat * int(steps)
+        flat = flat * max(0, min(int(steps), 65))  # past 64 the library refuses the count
     else:
         if len(flat) != steps or any(len(c) != 3 for c in flat):
             raise ValueError("coefficients must be (a, b, c) or one such triple for each of the %d steps" % steps)
