@@ -168,10 +168,15 @@ def test_linear_refuses(forward, kw, code):
 def test_linear_bytes():
     b = tl._linear_bytes
     assert b(0, 0, 0, 3) == (1, 1, 1)
-    # images of one byte an element, tables, each on a 256-byte boundary
-    assert b(100, 200, 300, 0) == (1, 30208 + 512 + 60160 + 768, 20224 + 256)
-    saved, fwd, bwd = b(100, 200, 300, 3)
-    assert saved == 60160 + 768 + 30208 + 512 and bwd == 20224 + 256 + 20224 + 256
+    # an image: one byte an element, rows of whole 128 bytes; its table: rows of 16;
+    # each on a 256-byte boundary
+    def image(rows, cols):
+        up = lambda v, n: -(-v // n) * n  # noqa: E731
+        return up(rows * up(cols, 128), 256) + up(up(rows, 16) * -(-cols // 128), 256)
+    M, N, K = 100, 200, 300
+    assert b(M, N, K, 0) == (1, image(M, K) + image(N, K), image(M, N))
+    assert b(M, N, K, 3) == (image(K, N) + image(K, M), image(M, K) + image(N, K), image(M, N) + image(N, M))
+    assert b(M, N, K, 1)[0] == image(K, N) and b(M, N, K, 2)[0] == image(K, M)
     assert tl._lib.tgemm_fp8_linear_bytes(1, 1, 1, 0, None) == -2
     with pytest.raises(tl.TgemmError):
         b(1, 1, 1, 4)
