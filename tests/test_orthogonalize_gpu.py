@@ -86,10 +86,54 @@ def test_shapes(rows, cols, dtype):
 
 # sizes that reach the larger tiles of either kind of product, batches too
 @pytest.mark.parametrize("batch,rows,cols", [(1, 1500, 1400), (1, 1100, 4200), (6, 530, 1100), (1, 3500, 3600),
-                                             (2, 2600, 2500), (40, 200, 190), (300, 40, 70), (3, 129, 2000)])
+                                             (2, 2600, 2500), (40, 200, 190), (300, 40, 70), (3, 129, 2000),
+                                             (1, 4300, 4400)])
 def test_large_and_batched(batch, rows, cols):
     G = randn(batch, rows, cols, seed=rows, dtype=torch.bfloat16)
     check(tl.orthogonalize(G), want(G))
+
+
+# few rows and a long axis: the first product is shared by several workgroups,
+# whose last one takes fewer columns
+@pytest.mark.parametrize("batch,rows,cols", [(1, 1, 4096), (1, 64, 4096), (1, 5000, 130), (3, 70, 4500), (2, 200, 8200),
+                                             (5, 64, 6000), (1, 129, 40000), (1, 3, 300001)])
+def test_few_rows(batch, rows, cols):
+    import ctypes
+    G = randn(batch, rows, cols, seed=cols, dtype=torch.bfloat16)
+    got = tl.orthogonalize(G)
+    check(got, want(G))
+    # the same every time, and whatever the workspace held
+    need = tl._lib.tgemm_orthogonalize_workspace_bytes(batch, rows, cols)
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+    out, co = torch.zeros_like(got), (ctypes.c_double * 15)(*USUAL * 5)
+    for _ in range(8):
+        assert tl._lib.tgemm_orthogonalize(batch, rows, cols, tl.BF16, G.data_ptr(), cols, rows * cols, out.data_ptr(),
+                                           cols, rows * cols, 5, co, 1e-7, (ws.data_ptr() + 255) // 256 * 256, need,
+                                           torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(out, got)
+
+
+def test_few_rows_at_once_and_replayed():
+    xs = randn(100, 5000, seed=21), randn(2, 4200, 60, seed=22)
+    ref = [tl.orthogonalize(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = []
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, x in zip(streams, xs):
+            with torch.cuda.stream(s):
+                got.append(tl.orthogonalize(x))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, ref[i % 2]) for i, g in enumerate(got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        held = tl.orthogonalize(xs[0])
+    for r in range(4):
+        xs[0].add_(0.5 * torch.randn_like(xs[0]))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(held, tl.orthogonalize(xs[0])), r
 
 
 def spectrum(kind, m, n):

@@ -58,11 +58,14 @@ struct OrthoArgs {
     _Float16* b;           // ms x ms: B'
     float* d;              // ms: diagonal of A
     float* e;              // ms: diagonal of B
+    float* part;           // split gram: parts x 4096 floats for each tile
+    int32_t* arrived;      // split gram: one counter a tile, zero between launches
     uint16_t* out;         // bfloat16 result
     int64_t ldo, stride_o;
     int32_t mp, np, ms, m, n, tall;
     int32_t tiles;             // tiles of one matrix
     int32_t tiles_m, tiles_n;  // of the update
+    int32_t parts, run;        // split gram: workgroups a tile, columns of X for each
     float ca, cb, cc;
 };
 
@@ -114,10 +117,12 @@ __device__ __forceinline__ void lower_tile(int t, int tile_rows, int& tm, int& t
 template <class G>
 struct OrthoTile {
     int z, tm, tn, m0, n0, wm0, wn0, lane, wave;
-    __device__ __forceinline__ OrthoTile(const OrthoArgs& g, bool symmetric) {
+    __device__ __forceinline__ OrthoTile(const OrthoArgs& g, bool symmetric)
+        : OrthoTile(g, symmetric, xcd_rank(blockIdx.x, gridDim.x)) {}
+    // tile r of the batch's
+    __device__ __forceinline__ OrthoTile(const OrthoArgs& g, bool symmetric, int r) {
         lane = lane_id();
         wave = wave_id();
-        const int r = xcd_rank(blockIdx.x, gridDim.x);
         z = r / g.tiles;
         const int t = r - z * g.tiles;
         if (symmetric) {
@@ -169,18 +174,12 @@ __device__ __forceinline__ void store_symmetric(_Float16* S, int ld, const Ortho
     }
 }
 
-// A = X X^T: A' (diagonal zero) and d.
+// A' (diagonal zero) and d from the sums of a tile of X X^T.
 template <class G>
-__global__ __launch_bounds__(G::NT) void ortho_gram_kernel(OrthoArgs g) {
-    __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
-    const OrthoTile<G> t(g, true);
-    const int64_t x = (int64_t)t.z * g.mp * g.np, s = (int64_t)t.z * g.ms * g.ms;
-    typename G::Acc acc[G::FM][G::FN];
-    G::product(ortho_operands(g.hi + x, g.mp, g.np, g.hi + x, g.mp, g.np, g.np), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0,
-               t.wn0, t.lane, t.wave);
+__device__ __forceinline__ void store_gram(const OrthoArgs& g, const OrthoTile<G>& t, const typename G::Acc (&acc)[G::FM][G::FN]) {
     float* d = g.d + (int64_t)t.z * g.ms;
     const int n = t.n0 + t.wn0 + G::col_of(0, t.lane);
-    store_symmetric<G>(g.a + s, g.ms, t, [](int) {}, [&](int i, int r, int m, Halves<G::FN>& out) {
+    store_symmetric<G>(g.a + (int64_t)t.z * g.ms * g.ms, g.ms, t, [](int) {}, [&](int i, int r, int m, Halves<G::FN>& out) {
 #pragma unroll
         for (int j = 0; j < G::FN; ++j) {
             const float v = acc[i][j][r] * (1.0f / (ONE * ONE));
@@ -189,6 +188,63 @@ __global__ __launch_bounds__(G::NT) void ortho_gram_kernel(OrthoArgs g) {
             out.v[j] = (_Float16)(diagonal ? 0.0f : v * ONE);
         }
     });
+}
+
+// A = X X^T.
+template <class G>
+__global__ __launch_bounds__(G::NT) void ortho_gram_kernel(OrthoArgs g) {
+    __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
+    const OrthoTile<G> t(g, true);
+    const _Float16* X = g.hi + (int64_t)t.z * g.mp * g.np;
+    typename G::Acc acc[G::FM][G::FN];
+    G::product(ortho_operands(X, g.mp, g.np, X, g.mp, g.np, g.np), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0, t.wn0,
+               t.lane, t.wave);
+    store_gram<G>(g, t, acc);
+}
+
+// The same with each tile's long axis split over g.parts workgroups, for few
+// tiles: what bounds a workgroup there is the rate at which one compute unit's
+// copies arrive (kernel times, one workgroup a tile -> eight: 64 x 4096 12.4 ->
+// 8.4 us, 64 x 16384 40 -> 12, 128 x 4096 13.1 -> 8.9, 256 x 4096 13.7 -> 10.1).
+// Each leaves its sums in the workspace and counts itself; the one that counts
+// last adds all of them, in their order, so the result does not depend on which
+// that is.  No workgroup waits for another.  Sums and counters are atomics of
+// device scope, which go past the caches that XCDs do not share.  Every wave
+// waits for its sums' stores before the barrier ahead of the count, whose
+// release and acquire order them between workgroups: one a workgroup, since
+// each flushes its XCD's cache (a device fence in every wave: 128 x 4096 10.7).
+template <class G>
+__global__ __launch_bounds__(G::NT) void ortho_gram_split_kernel(OrthoArgs g) {
+    static_assert(G::FM == 1 && G::FN == 1, "16 sums a lane");
+    __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
+    __shared__ int last;
+    const int tile = blockIdx.x / g.parts, part = blockIdx.x - tile * g.parts;
+    const OrthoTile<G> t(g, true, tile);
+    const _Float16* X = g.hi + (int64_t)t.z * g.mp * g.np;
+    const int from = part * g.run;  // below np for every part
+    X += from;
+    typename G::Acc acc[1][1];
+    G::product(ortho_operands(X, g.mp, g.np, X, g.mp, g.np, min(g.run, g.np - from)), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0, t.wn0, t.lane, t.wave);
+
+    constexpr int TILE = G::BM * G::BN;
+    float* sums = g.part + (int64_t)tile * g.parts * TILE + 1024 * t.wave + t.lane;
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+        __hip_atomic_store(sums + (int64_t)part * TILE + 64 * r, acc[0][0][r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = __hip_atomic_fetch_add(g.arrived + tile, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == g.parts - 1;
+    __syncthreads();
+    if (!last) return;
+    if (threadIdx.x == 0) g.arrived[tile] = 0;  // for the next step's launch
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[0][0][r] = 0.0f;
+    for (int p = 0; p < g.parts; ++p)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            acc[0][0][r] += __hip_atomic_load(sums + (int64_t)p * TILE + 64 * r, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    store_gram<G>(g, t, acc);
 }
 
 // B = b A + c A^2: B' (diagonal zero) and e.
@@ -353,6 +409,8 @@ struct OrthoInArgs {
     double* part;        // PARTS sums of squares for each matrix
     _Float16 *hi, *lo, *xt;
     int32_t mp, np, tall;
+    int32_t* arrived;    // counters to clear
+    int32_t counters;    // at most 256
     double eps;
 };
 
@@ -443,6 +501,7 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoInArgs g) {
         load8<E>(v[h], static_cast<const typename E::T*>(g.G) + (int64_t)z * g.stride_g + (int64_t)min(r, g.rows - 1) * g.ldg,
                  c0 + 8 * (tid & 7), r < g.rows ? g.cols : 0);
     }
+    if (blockIdx.x == 0 && tid < g.counters) g.arrived[tid] = 0;
     double s = g.part[(int64_t)z * PARTS + tid];
     static_assert(PARTS == 256, "a part for each thread");
     for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
@@ -540,7 +599,11 @@ struct OrthoPlan {
     int64_t m, n, mp, np, ms;
     const OrthoKernels *sym, *upd;
     int64_t tri;  // symmetric tiles of one matrix
-    int64_t off_hi, off_lo, off_t0, off_t1, off_a, off_b, off_d, off_e, off_part, bytes;
+    // workgroups a tile of the gram product (more than 1: the split kernel), and
+    // the columns of X that each takes, the last perhaps fewer
+    int parts;
+    int64_t run;
+    int64_t off_hi, off_lo, off_t0, off_t1, off_a, off_b, off_d, off_e, off_part, off_sums, off_arrived, bytes;
 };
 
 static int64_t up_to(int64_t v, int64_t step) { return (v + step - 1) / step * step; }
@@ -580,6 +643,22 @@ static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     p.sym = cheapest(t, count, (p.np + p.mp) / 2, [&](int64_t tile) { return batch * tri(tile); });  // gram: np, poly: mp
     p.tri = tri(p.sym->tile);
     p.ms = up_to(p.mp, p.sym->tile);
+    // Split the gram product of few 64 x 64 tiles: at least 4 slices each, 8 parts
+    // at most (64 x 4096: 8.4 us, 16 parts 11.0) and 256 workgroups.  It saves
+    // 2.8 us for each 1024 columns that others take over; joining costs 3.5 us
+    // and 0.023 a workgroup (128 x 2048: 8.2 us split, 8.3 not; 256 x 2048 9.5,
+    // 8.6; 512 x 4096 14.3, 13.8).
+    p.parts = 1;
+    p.run = p.np;
+    if (p.sym->tile == 64) {
+        const int64_t groups = batch * p.tri, slices = p.np / 64;
+        int64_t most = 256 / groups < 8 ? 256 / groups : 8;
+        if (slices / 4 < most) most = slices / 4;
+        if (most > 1 && 0.0028 * (double)p.np * (1.0 - 1.0 / (double)most) > 4.0 + 0.025 * (double)(groups * most)) {
+            p.run = 64 * tiles(slices, most);
+            p.parts = (int)tiles(p.np, p.run);
+        }
+    }
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t o = at;
@@ -596,6 +675,8 @@ static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     p.off_d = take(4 * batch * p.ms);
     p.off_e = take(4 * batch * p.ms);
     p.off_part = take(8 * batch * PARTS);
+    p.off_sums = take(p.parts > 1 ? 4 * batch * p.tri * p.parts * 4096 : 0);
+    p.off_arrived = take(p.parts > 1 ? 4 * batch * p.tri : 0);
     p.bytes = at;
     return p;
 }
@@ -725,6 +806,8 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     in.np = (int32_t)p.np;
     in.tall = rows > cols;
     in.eps = eps;
+    in.arrived = (int32_t*)(ws + p.off_arrived);
+    in.counters = p.parts > 1 ? (int32_t)(batch * p.tri) : 0;
     const OrthoInFn norm_fn = dtype == TGEMM_F32 ? ortho_norm_kernel<EF32>
                               : dtype == TGEMM_BF16 ? ortho_norm_kernel<EBF16> : ortho_norm_kernel<EF16>;
     const OrthoInFn load_fn = dtype == TGEMM_F32 ? ortho_load_kernel<EF32>
@@ -743,6 +826,10 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     g.b = (_Float16*)(ws + p.off_b);
     g.d = (float*)(ws + p.off_d);
     g.e = (float*)(ws + p.off_e);
+    g.part = (float*)(ws + p.off_sums);
+    g.arrived = in.arrived;
+    g.parts = p.parts;
+    g.run = (int32_t)p.run;
     g.out = (uint16_t*)O;
     g.ldo = ldo;
     g.stride_o = stride_o;
@@ -754,12 +841,12 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     g.tall = in.tall;
     g.tiles_m = (int32_t)(p.mp / ut);
     g.tiles_n = (int32_t)(p.np / ut);
-    auto launch = [&](OrthoFn fn, const OrthoKernels& k, int64_t tiles) {
+    auto launch = [&](OrthoFn fn, const OrthoKernels& k, int64_t tiles, int64_t parts) {
         if (err != hipSuccess) return;
         g.tiles = (int32_t)tiles;
         void* args[] = {&g};
-        err = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)(batch * tiles)), dim3(k.threads), args, 0,
-                              s);
+        err = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)(batch * tiles * parts)), dim3(k.threads),
+                              args, 0, s);
     };
     for (int k = 0; k < steps; ++k) {
         g.ca = (float)coefficients[3 * k];
@@ -767,9 +854,9 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
         g.cc = (float)coefficients[3 * k + 2];
         g.xt = (const _Float16*)(ws + (k % 2 ? p.off_t1 : p.off_t0));
         g.xt_out = (_Float16*)(ws + (k % 2 ? p.off_t0 : p.off_t1));
-        launch(p.sym->first, *p.sym, tri);
-        launch(p.sym->second, *p.sym, tri);
-        launch(k + 1 < steps ? p.upd->first : p.upd->second, *p.upd, upd);
+        launch(p.parts > 1 ? ortho_gram_split_kernel<Ortho64> : p.sym->first, *p.sym, tri, p.parts);
+        launch(p.sym->second, *p.sym, tri, 1);
+        launch(k + 1 < steps ? p.upd->first : p.upd->second, *p.upd, upd, 1);
     }
     if (err != hipSuccess) {
         set_error("launch failed: %s", hipGetErrorString(err));
