@@ -409,6 +409,7 @@ struct OrthoInArgs {
     double* part;        // PARTS sums of squares for each matrix
     _Float16 *hi, *lo, *xt;
     int32_t mp, np, tall;
+    int32_t lane_bits;   // the norm's: 2^lane_bits threads take one row together
     int32_t* arrived;    // counters to clear
     int32_t counters;    // at most 256
     double eps;
@@ -449,26 +450,30 @@ __device__ __forceinline__ void load8(float (&v)[8], const typename E::T* row, i
 }
 
 // Workgroup (p, z): pieces p, p + PARTS .. of matrix z, a piece 2048 elements
-// of a row; its sum of squares in double (squares of any float fit), always
-// in the same order.  Four pieces are requested at a time (one: 4096x4096
-// 20 us; now 13).
+// of a row, or as many rows together as 256 threads reach where rows are
+// short; its sum of squares in double (squares of any float fit), always in
+// the same order.  Four pieces are requested at a time (one: 4096x4096 20 us;
+// now 13).
 template <class E>
 __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoInArgs g) {
     __shared__ double sums[4];
     constexpr int AT_ONCE = 4;
     const int p = blockIdx.x % PARTS, z = blockIdx.x / PARTS;
-    const int per = (g.cols + 2047) / 2048;
-    const int64_t pieces = (int64_t)g.rows * per;
+    const int tid = threadIdx.x, lanes = 1 << g.lane_bits, rows = 256 >> g.lane_bits;
+    const int per = (g.cols + 8 * lanes - 1) / (8 * lanes);
+    const int64_t pieces = (int64_t)((g.rows + rows - 1) / rows) * per;
     double s = 0.0;
     for (int64_t i = p; i < pieces; i += AT_ONCE * PARTS) {
         float v[AT_ONCE][8];
 #pragma unroll
         for (int u = 0; u < AT_ONCE; ++u) {
             const int64_t k = min(i + u * PARTS, pieces - 1);
-            const int r = (int)(k / per), c = (int)(k % per) * 2048 + 8 * threadIdx.x;
-            // a piece past the last, or columns past the last: zeros
-            const int end = i + u * PARTS < pieces ? g.cols : 0;
-            load8<E>(v[u], static_cast<const typename E::T*>(g.G) + (int64_t)z * g.stride_g + (int64_t)r * g.ldg, c, end);
+            const int r = (int)(k / per) * rows + (tid >> g.lane_bits);
+            const int c = (int)(k % per) * 8 * lanes + 8 * (tid & (lanes - 1));
+            // a piece, rows or columns past the last: zeros
+            const int end = i + u * PARTS < pieces && r < g.rows ? g.cols : 0;
+            load8<E>(v[u], static_cast<const typename E::T*>(g.G) + (int64_t)z * g.stride_g +
+                               (int64_t)min(r, g.rows - 1) * g.ldg, c, end);
         }
 #pragma unroll
         for (int u = 0; u < AT_ONCE; ++u)
@@ -805,6 +810,7 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     in.mp = (int32_t)p.mp;
     in.np = (int32_t)p.np;
     in.tall = rows > cols;
+    while (in.lane_bits < 8 && (INT64_C(8) << in.lane_bits) < cols) ++in.lane_bits;
     in.eps = eps;
     in.arrived = (int32_t*)(ws + p.off_arrived);
     in.counters = p.parts > 1 ? (int32_t)(batch * p.tri) : 0;
