@@ -182,3 +182,10 @@ def test_linear_bytes():
         b(1, 1, 1, 4)
     assert lin(True, M=0, N=0, K=0, keep=0, saved=None, scratch=None, x=None, w=None, y=None) == 0
     assert lin(False, M=0, N=0, K=0, keep=0, saved=None, scratch=None, g=None) == 0
+
+
+def test_package_offers_the_operators():
+    import tiled_software_pipelined_amd as package
+    for name in package.__all__:
+        assert getattr(package, name) is getattr(tl, name)
+    assert not hasattr(package, "no_such_name")

@@ -151,7 +151,10 @@ int tgemm_fp8_linear_backward(int64_t M, int64_t N, int64_t K, int32_t g_dtype, 
     if (rc == TGEMM_OK) rc = check_buffer("scratch", scratch, l.bytes[2]);
     if (rc == TGEMM_OK && (M > 0 || N > 0)) rc = current_device_ok();
     if (rc != TGEMM_OK) return rc;
-    if (!kx && !kw) return TGEMM_OK;
+    if (!kx && !kw) {
+        clear_error();
+        return TGEMM_OK;
+    }
     const char* v = static_cast<const char*>(saved);
     char* s = static_cast<char*>(scratch);
     rc = tgemm_fp8_quantize(M, N, g_dtype, g, ldg, grad_fmt, TGEMM_BLOCK_ROW, s + l.g.q, l.g.ldq, s + l.g.s,

@@ -204,15 +204,16 @@ __global__ __launch_bounds__(G::NT) void ortho_gram_kernel(OrthoArgs g) {
 
 // The same with each tile's long axis split over g.parts workgroups, for few
 // tiles: what bounds a workgroup there is the rate at which one compute unit's
-// copies arrive (kernel times, one workgroup a tile -> eight: 64 x 4096 12.4 ->
-// 8.4 us, 64 x 16384 40 -> 12, 128 x 4096 13.1 -> 8.9, 256 x 4096 13.7 -> 10.1).
+// copies arrive (kernel times, one workgroup a tile and split: 64 x 4096 12.4, 8.0
+// us, 64 x 16384 40, 11.2, 128 x 4096 13.1, 8.4, 512 x 4096 13.8, 10.2).
 // Each leaves its sums in the workspace and counts itself; the one that counts
 // last adds all of them, in their order, so the result does not depend on which
 // that is.  No workgroup waits for another.  Sums and counters are atomics of
 // device scope, which go past the caches that XCDs do not share.  Every wave
 // waits for its sums' stores before the barrier ahead of the count, whose
 // release and acquire order them between workgroups: one a workgroup, since
-// each flushes its XCD's cache (a device fence in every wave: 128 x 4096 10.7).
+// each flushes its XCD's cache (128 x 4096 in 8 parts: 8.9 us, with a device
+// fence in every wave 10.7).
 template <class G>
 __global__ __launch_bounds__(G::NT) void ortho_gram_split_kernel(OrthoArgs g) {
     static_assert(G::FM == 1 && G::FN == 1, "16 sums a lane");
@@ -224,7 +225,8 @@ __global__ __launch_bounds__(G::NT) void ortho_gram_split_kernel(OrthoArgs g) {
     const int from = part * g.run;  // below np for every part
     X += from;
     typename G::Acc acc[1][1];
-    G::product(ortho_operands(X, g.mp, g.np, X, g.mp, g.np, min(g.run, g.np - from)), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0, t.wn0, t.lane, t.wave);
+    G::product(ortho_operands(X, g.mp, g.np, X, g.mp, g.np, min(g.run, g.np - from)), t.m0, t.n0,
+               (TG_LDS char*)smem_raw, acc, t.wm0, t.wn0, t.lane, t.wave);
 
     constexpr int TILE = G::BM * G::BN;
     float* sums = g.part + (int64_t)tile * g.parts * TILE + 1024 * t.wave + t.lane;
@@ -240,10 +242,20 @@ __global__ __launch_bounds__(G::NT) void ortho_gram_split_kernel(OrthoArgs g) {
     if (threadIdx.x == 0) g.arrived[tile] = 0;  // for the next step's launch
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[0][0][r] = 0.0f;
-    for (int p = 0; p < g.parts; ++p)
+    // four parts' sums in flight at a time
+    for (int p = 0; p < g.parts; p += 4) {
+        float v[4][16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-            acc[0][0][r] += __hip_atomic_load(sums + (int64_t)p * TILE + 64 * r, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                v[u][r] = __hip_atomic_load(sums + (int64_t)min(p + u, g.parts - 1) * TILE + 64 * r, __ATOMIC_RELAXED,
+                                            __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[0][0][r] += p + u < g.parts ? v[u][r] : 0.0f;
+    }
     store_gram<G>(g, t, acc);
 }
 
@@ -648,19 +660,24 @@ static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     p.sym = cheapest(t, count, (p.np + p.mp) / 2, [&](int64_t tile) { return batch * tri(tile); });  // gram: np, poly: mp
     p.tri = tri(p.sym->tile);
     p.ms = up_to(p.mp, p.sym->tile);
-    // Split the gram product of few 64 x 64 tiles: at least 4 slices each, 8 parts
-    // at most (64 x 4096: 8.4 us, 16 parts 11.0) and 256 workgroups.  It saves
-    // 2.8 us for each 1024 columns that others take over; joining costs 3.5 us
-    // and 0.023 a workgroup (128 x 2048: 8.2 us split, 8.3 not; 256 x 2048 9.5,
-    // 8.6; 512 x 4096 14.3, 13.8).
+    // Split the gram product of few 64 x 64 tiles, at least 4 slices a part and
+    // 256 workgroups at most.  A part's columns take 2.6 us for each 1024 of
+    // them; joining takes about 1 us (1.8 here, to split only where it gains), 0.24
+    // for each part to add and 0.025 for each workgroup (fitted to 4 .. 32 parts of 1 .. 36
+    // tiles; us, 8, 16, 32 parts: 64 x 4096 7.6, 8.8,
+    // 64 x 16384 11.2, 10.7, 12.8, 64 x 100000 36.3, 23.3, 19.0, 256 x 4096 9.1,
+    // 12.3).
     p.parts = 1;
     p.run = p.np;
     if (p.sym->tile == 64) {
         const int64_t groups = batch * p.tri, slices = p.np / 64;
-        int64_t most = 256 / groups < 8 ? 256 / groups : 8;
-        if (slices / 4 < most) most = slices / 4;
-        if (most > 1 && 0.0028 * (double)p.np * (1.0 - 1.0 / (double)most) > 4.0 + 0.025 * (double)(groups * most)) {
-            p.run = 64 * tiles(slices, most);
+        const double columns = 0.0026 * (double)p.np;
+        double least = columns;
+        for (int64_t n = 2; n <= slices / 4 && n * groups <= 256; ++n) {
+            const double t = 1.8 + columns / (double)n + (double)n * (0.24 + 0.025 * (double)groups);
+            if (t >= least) continue;
+            least = t;
+            p.run = 64 * tiles(slices, n);
             p.parts = (int)tiles(p.np, p.run);
         }
     }

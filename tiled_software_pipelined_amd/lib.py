@@ -69,7 +69,8 @@ EXPORTS = ("gemm_plan", "gemm_plan_variant", "gemm_run", "gemm_destroy", "tgemm_
            "tgemm_lds_read_probe", "tgemm_mfma_rate_probe", "gemm_workspace_bytes", "gemm_run_ws",
            "gemm_kernel_occupancy", "gemm_clock_slots", "gemm_run_clocked", "gemm_run_noalloc",
            "tgemm_set_c_store_policy", "tgemm_fp8_quantize", "tgemm_fp8_gemm", "tgemm_fp8_gemm_kernel",
-           "tgemm_fp8_linear_bytes", "tgemm_fp8_linear_forward", "tgemm_fp8_linear_backward", "tgemm_orthogonalize_workspace_bytes", "tgemm_orthogonalize")
+           "tgemm_fp8_linear_bytes", "tgemm_fp8_linear_forward", "tgemm_fp8_linear_backward",
+           "tgemm_orthogonalize_workspace_bytes", "tgemm_orthogonalize")
 
 
 def _load():
