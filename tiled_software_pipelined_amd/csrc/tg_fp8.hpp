@@ -16,9 +16,10 @@ struct Fp8Args {
 
 typedef void (*Fp8Fn)(Fp8Args);
 
-// One compiled kernel.  bm, bn: rows and columns of C per workgroup.
+// One compiled kernel.  bm, bn: rows and columns of C per workgroup.  bytes:
+// for operands with rows that do not start on 4-byte boundaries.
 struct Fp8Kernel {
-    Fp8Fn fn;
+    Fp8Fn fn, bytes;
     int bm, bn, threads;
     char name[64];
 };
@@ -94,8 +95,11 @@ __global__ __launch_bounds__(G::NT) void fp8_tile_kernel(Fp8Args g) {
 // own: nothing to share through LDS), and add their sums through LDS at the
 // end.  v_mfma_scale_f32_16x16x128_f8f6f4: lane l holds row l % 16, chunks
 // l / 16 and 4 + l / 16 of the block's eight 16-byte chunks, so one load
-// instruction reads 64 adjacent bytes of each of 16 rows.
-template <int FA, int FB, int MT, int NW, int U>
+// instruction reads 64 adjacent bytes of each of 16 rows.  BYTES: rows may
+// start at any byte.  Loads that are not 4-byte aligned take three times as
+// long (20x64x6681 19.4 us, with rows 6684 apart 7.5), so a chunk is then the
+// four words it starts in and the word behind them, shifted together.
+template <int FA, int FB, int MT, int NW, int U, bool BYTES>
 __global__ __launch_bounds__(64 * NW) void fp8_rows_kernel(Fp8Args g) {
     __shared__ float part[NW][MT * 256];
     const NtOperands& o = g.op;
@@ -119,29 +123,49 @@ __global__ __launch_bounds__(64 * NW) void fp8_rows_kernel(Fp8Args g) {
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[t] = f32x4{0, 0, 0, 0};
 
+    // bytes past a 4-byte boundary at which a row starts
+    const int off_b = BYTES ? (int)((uintptr_t)brow & 3) : 0;
+    int off_a[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) off_a[t] = BYTES ? (int)((uintptr_t)arow[t] & 3) : 0;
+    struct Chunk {
+        i32x4 v;
+        uint32_t next;  // BYTES: the word behind
+    };
     struct Block {
-        i32x4 b[2], a[MT][2];
+        Chunk b[2], a[MT][2];
         int sb, sa[MT];
+        bool whole;
+    };
+    auto load_chunk = [&](Chunk& x, const char* p, int off) {
+        x.v = load16(__builtin_assume_aligned(p - off, 4));
+        // a chunk on a boundary has no part in the word behind, which may be
+        // past the operand's end
+        if constexpr (BYTES) x.next = *reinterpret_cast<const uint32_t*>(p - off + (off ? 16 : 12));
+    };
+    auto chunk = [&](const Chunk& x, int off) {
+        if constexpr (!BYTES) return x.v;
+        return i32x4{(int)__builtin_amdgcn_alignbyte(x.v[1], x.v[0], off), (int)__builtin_amdgcn_alignbyte(x.v[2], x.v[1], off),
+                     (int)__builtin_amdgcn_alignbyte(x.v[3], x.v[2], off), (int)__builtin_amdgcn_alignbyte(x.next, x.v[3], off)};
     };
     auto load = [&](Block& x, int kb) {
         const int64_t k0 = (int64_t)kb * 128;
-        if (k0 + 128 <= o.k) {  // wave-uniform
-            x.b[0] = load16(brow + k0);
-            x.b[1] = load16(brow + k0 + 64);
+        x.whole = k0 + 128 <= o.k;  // wave-uniform
+        if (x.whole) {
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                x.a[t][0] = load16(arow[t] + k0);
-                x.a[t][1] = load16(arow[t] + k0 + 64);
+            for (int h = 0; h < 2; ++h) {
+                load_chunk(x.b[h], brow + k0 + 64 * h, off_b);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) load_chunk(x.a[t][h], arow[t] + k0 + 64 * h, off_a[t]);
             }
         } else {
             // the last, partial block: zero past the row's end
             const int p = (int)k0 + at;
-            x.b[0] = row_end_chunk(brow - at, p, o.k);
-            x.b[1] = row_end_chunk(brow - at, p + 64, o.k);
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                x.a[t][0] = row_end_chunk(arow[t] - at, p, o.k);
-                x.a[t][1] = row_end_chunk(arow[t] - at, p + 64, o.k);
+            for (int h = 0; h < 2; ++h) {
+                x.b[h] = Chunk{row_end_chunk(brow - at, p + 64 * h, o.k), 0};
+#pragma unroll
+                for (int t = 0; t < MT; ++t) x.a[t][h] = Chunk{row_end_chunk(arow[t] - at, p + 64 * h, o.k), 0};
             }
         }
         x.sb = bs[(int64_t)kb * o.ldsb];
@@ -149,10 +173,12 @@ __global__ __launch_bounds__(64 * NW) void fp8_rows_kernel(Fp8Args g) {
         for (int t = 0; t < MT; ++t) x.sa[t] = as[t][(int64_t)kb * o.ldsa];
     };
     auto multiply = [&](const Block& x) {
-        const i32x8 vb = __builtin_shufflevector(x.b[0], x.b[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        const int ob = x.whole ? off_b : 0;
+        const i32x8 vb = __builtin_shufflevector(chunk(x.b[0], ob), chunk(x.b[1], ob), 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            const i32x8 va = __builtin_shufflevector(x.a[t][0], x.a[t][1], 0, 1, 2, 3, 4, 5, 6, 7);
+            const int oa = x.whole ? off_a[t] : 0;
+            const i32x8 va = __builtin_shufflevector(chunk(x.a[t][0], oa), chunk(x.a[t][1], oa), 0, 1, 2, 3, 4, 5, 6, 7);
             acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, acc[t], FA, FB, 0, x.sa[t], 0, x.sb);
         }
     };
@@ -203,12 +229,12 @@ const Fp8Kernel* fp8_kernel_table() {
     // alone, 512x4096x4096 19.9 us against 16.5).
     typedef NtGemm<Tr, 64, 64, 2, 2, 4, true> G64;
     static const Fp8Kernel table[PICK_COUNT] = {
-        {fp8_tile_kernel<G256>, G256::BM, G256::BN, G256::NT, "t256x256x128_w2x2_s2"},
-        {fp8_tile_kernel<G128>, G128::BM, G128::BN, G128::NT, "t128x128x128_w2x4_s4_slice"},
-        {fp8_tile_kernel<G128P>, G128P::BM, G128P::BN, G128P::NT, "t128x128x128_w2x2_s2_slice"},
-        {fp8_tile_kernel<G64>, G64::BM, G64::BN, G64::NT, "t64x64x128_w2x2_s4_slice"},
-        {fp8_rows_kernel<FA, FB, 1, 8, 4>, 16, 16, 512, "rows16_w8"},
-        {fp8_rows_kernel<FA, FB, 2, 8, 4>, 32, 16, 512, "rows32_w8"},
+        {fp8_tile_kernel<G256>, fp8_tile_kernel<G256>, G256::BM, G256::BN, G256::NT, "t256x256x128_w2x2_s2"},
+        {fp8_tile_kernel<G128>, fp8_tile_kernel<G128>, G128::BM, G128::BN, G128::NT, "t128x128x128_w2x4_s4_slice"},
+        {fp8_tile_kernel<G128P>, fp8_tile_kernel<G128P>, G128P::BM, G128P::BN, G128P::NT, "t128x128x128_w2x2_s2_slice"},
+        {fp8_tile_kernel<G64>, fp8_tile_kernel<G64>, G64::BM, G64::BN, G64::NT, "t64x64x128_w2x2_s4_slice"},
+        {fp8_rows_kernel<FA, FB, 1, 8, 4, false>, fp8_rows_kernel<FA, FB, 1, 8, 4, true>, 16, 16, 512, "rows16_w8"},
+        {fp8_rows_kernel<FA, FB, 2, 8, 4, false>, fp8_rows_kernel<FA, FB, 2, 8, 4, true>, 32, 16, 512, "rows32_w8"},
     };
     return table;
 }

@@ -50,8 +50,8 @@ static double time_of(Fp8Pick p, const Fp8Kernel& k, int64_t M, int64_t N, int64
         case PICK_128: return 2.5 + ceil(n / 256.0) * (3.5 + 4.1 * k1);
         case PICK_128_PAIR: return 2.0 + (n > 410.0 ? more : 1.6) * (2.3 + 3.67 * k1);
         case PICK_64: return 2.9 + more * (0.95 + 2.05 * k1);
-        case PICK_ROWS16: return 2.6 + more * 1.0 * k1;
-        default: return 2.4 + more * 1.5 * k1;
+        case PICK_ROWS16: return 2.6 + 1.0 * k1 + (more - 1.0) * fmax(1.0 * k1, 1.6);
+        default: return 2.4 + 1.5 * k1 + (more - 1.0) * fmax(1.5 * k1, 1.9);
     }
 }
 
@@ -164,6 +164,7 @@ int tgemm_fp8_gemm(int64_t M, int64_t N, int64_t K, int32_t fmt_a, const void* A
     }
     const int rc = current_device_ok();
     if (rc != TGEMM_OK) return rc;
+    const bool bytes = (((uintptr_t)A | (uintptr_t)B) % 4) || lda % 4 || ldb % 4;
     for (int i = 0; i < count; ++i) {
         const NtOperands a{(const char*)A + p[i].m0 * lda, (const char*)B + p[i].n0 * ldb, (const uint8_t*)SA + p[i].m0,
                            (const uint8_t*)SB + p[i].n0, (int32_t)p[i].M, (int32_t)p[i].N, (int32_t)K, lda, ldb, ldsa, ldsb};
@@ -178,7 +179,7 @@ int tgemm_fp8_gemm(int64_t M, int64_t N, int64_t K, int32_t fmt_a, const void* A
         g.tiles_n = (g.op.N + k.bn - 1) / k.bn;
         g.stream = (uintptr_t)g.C % 128 == 0 && ldc % 64 == 0;
         void* args[] = {&g};
-        const hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(k.fn), dim3((unsigned)(g.tiles_m * g.tiles_n)),
+        const hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(bytes ? k.bytes : k.fn), dim3((unsigned)(g.tiles_m * g.tiles_n)),
                                                dim3(k.threads), args, 0, static_cast<hipStream_t>(stream));
         if (err != hipSuccess) {
             set_error("launch of %s failed: %s", k.name, hipGetErrorString(err));

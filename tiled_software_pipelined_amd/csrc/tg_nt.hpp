@@ -49,6 +49,7 @@ template <int FA, int FB>
 struct NtF8 {
     static constexpr int LB = 32;     // bytes a lane holds of its row in one K step
     static constexpr bool SCALED = true;
+    static constexpr bool PARTIAL = true;  // rows may end inside a slice
     typedef NtFrag<32> Frag;
     template <int OA, int OB>
     __device__ static __forceinline__ f32x16 mma(const Frag& a, const Frag& b, f32x16 c, int sa, int sb) {
@@ -62,6 +63,7 @@ struct NtF8 {
 struct NtF16 {
     static constexpr int LB = 16;
     static constexpr bool SCALED = false;
+    static constexpr bool PARTIAL = false;
     typedef NtFrag<16> Frag;
     template <int, int>
     __device__ static __forceinline__ f32x16 mma(const Frag& a, const Frag& b, f32x16 c, int, int) {
@@ -197,7 +199,9 @@ struct NtGemm {
         }
     }
 
-    // where the copies of one slice come from: wave-uniform addresses
+    // where the copies of one slice come from: wave-uniform addresses.  A last,
+    // partial slice is the row's last 128 bytes, of which the first were in the
+    // slice before: no copy leaves its row.
     struct Source {
         const char* a;
         const char* b;
@@ -205,8 +209,9 @@ struct NtGemm {
     };
     __device__ static __forceinline__ Source source(const NtOperands& g, int m0, int n0, int sl, int wave) {
         Source r;
-        r.a = g.a + (int64_t)m0 * g.lda + (int64_t)sl * ROW;
-        r.b = g.b + (int64_t)n0 * g.ldb + (int64_t)sl * ROW;
+        const int64_t at = Tr::PARTIAL ? min((int64_t)sl * ROW, (int64_t)g.k - ROW) : (int64_t)sl * ROW;
+        r.a = g.a + (int64_t)m0 * g.lda + at;
+        r.b = g.b + (int64_t)n0 * g.ldb + at;
         r.s = nullptr;
         if constexpr (Tr::SCALED)
             r.s = wave * S_PER < BM / 4 ? g.sa + (int64_t)sl * g.ldsa : g.sb + (int64_t)sl * g.ldsb;
@@ -326,8 +331,8 @@ struct NtGemm {
                 // have less than a slice to land (8192^3 e4m3: 439 us against
                 // 425), reads after all the copies would come late for the
                 // next K step with one wave a SIMD (4096^3: 61 against 57)
-                constexpr int NC = TOTAL - NREAD;
-                const int c0 = m * NC / TOTAL, c1 = (m + 1) * NC / TOTAL;
+                constexpr int NC = TOTAL - NREAD, PER = TOTAL > 0 ? TOTAL : 1;
+                const int c0 = m * NC / PER, c1 = (m + 1) * NC / PER;
                 if (c1 > c0) copy_one(c0, cslot, off, src, wave);
                 else read_one(nxt, rslot, rs, m - c1, wm0, wn0, lane);
             }
@@ -374,11 +379,10 @@ struct NtGemm {
         }
     }
 
-    // ---- the last, partial slice -----------------------------------------------
-    // `left` (1 .. 127) bytes of each row, through registers: zero past the
-    // row's end (a zero in both operands adds nothing).
-    __device__ static __forceinline__ void fill_tail(TG_LDS char* slot, const NtOperands& g, int m0, int n0, int full,
-                                                     int wave, int lane) {
+    // ---- rows of less than one slice -------------------------------------------
+    // Through registers: zero past the row's end (a zero in both operands adds
+    // nothing).
+    __device__ static __forceinline__ void fill_short(TG_LDS char* slot, const NtOperands& g, int m0, int n0) {
         const int tid = threadIdx.x;
         // every chunk's load is in flight before the first is stored
         i32x4 v[A_PER + B_PER];
@@ -388,7 +392,7 @@ struct NtGemm {
             const int p = ((a ? q : q - A_PER) * NT + tid) >> 3, c = chunk_of(p, tid & 7);
             const char* rowp = a ? g.a + (int64_t)min(m0 + row_at<WTM>(p), g.M - 1) * g.lda
                                  : g.b + (int64_t)min(n0 + row_at<WTN>(p), g.N - 1) * g.ldb;
-            v[q] = row_end_chunk(rowp, full * ROW + c * 16, g.k);
+            v[q] = row_end_chunk(rowp, c * 16, g.k);
         }
 #pragma unroll
         for (int q = 0; q < A_PER + B_PER; ++q)
@@ -397,11 +401,29 @@ struct NtGemm {
         if constexpr (Tr::SCALED) {
             if (tid < (BM + BN) / 4) {
                 const uint8_t* p = tid < BM / 4
-                    ? g.sa + (int64_t)full * g.ldsa + min(m0 + 4 * tid, (g.M - 1) & ~3)
-                    : g.sb + (int64_t)full * g.ldsb + min(n0 + 4 * (tid - BM / 4), (g.N - 1) & ~3);
+                    ? g.sa + min(m0 + 4 * tid, (g.M - 1) & ~3)
+                    : g.sb + min(n0 + 4 * (tid - BM / 4), (g.N - 1) & ~3);
                 *reinterpret_cast<TG_LDS int32_t*>(slot + A_BYTES + B_BYTES + tid / S_PER * 256 + tid % S_PER * 4) =
                     *reinterpret_cast<const int32_t*>(p);
             }
+        }
+    }
+
+    // Fragments of K step s without the slice's first `drop` bytes.
+    __device__ static __forceinline__ void drop_first(Frags& f, int s, int drop, int lane) {
+#pragma unroll
+        for (int h = 0; h < RB; ++h) {
+            const int gone = drop - 16 * (2 * RB * s + 2 * h + (lane >> 5));  // bytes of this lane's chunk
+            i32x4 keep;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int n = min(max(gone - 4 * w, 0), 4);
+                keep[w] = n == 4 ? 0 : (int)(0xffffffffu << (8 * n));
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i) f.a[i].v[h] &= keep;
+#pragma unroll
+            for (int j = 0; j < FN; ++j) f.b[j].v[h] &= keep;
         }
     }
 
@@ -414,7 +436,9 @@ struct NtGemm {
             for (int j = 0; j < FN; ++j)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-        const int full = g.k / ROW, left = g.k % ROW;
+        // whole slices, and with a partial one (of `left` bytes) behind them,
+        // which is copied like the others
+        const int full = g.k / ROW, left = g.k % ROW, total = Tr::PARTIAL && full > 0 && left > 0 ? full + 1 : full;
         Offsets off;
         offsets(off, g, m0, n0, wave, lane);
         auto slot = [&](int t) { return smem + (t % STAGES) * SLOT; };
@@ -424,50 +448,54 @@ struct NtGemm {
         // slice STAGES-1 and read the first fragments
 #pragma unroll
         for (int t = 0; t < STAGES - 1; ++t)
-            if (t < full) copy(t);
+            if (t < total) copy(t);
         if constexpr (AHEAD) {
             Frags F[KSUB];
             if (full > 0) {
-                wait_slice(min(STAGES - 2, full - 1));
-                if (STAGES - 1 < full) copy(STAGES - 1);
+                wait_slice(min(STAGES - 2, total - 1));
+                if (STAGES - 1 < total) copy(STAGES - 1);
 #pragma unroll
                 for (int s = 0; s < KSUB; ++s) read_frags(F[s], smem, s, wm0, wn0, lane);
             }
             int t = 0;
-            for (; t + STAGES < full; ++t)
+            for (; t + STAGES < total; ++t)
                 slice_ahead<true, true>(acc, F, slot(t), slot(t + 1), STAGES - 2, off,
                                         source(g, m0, n0, t + STAGES, wave), wm0, wn0, lane, wave);
             for (; t + 1 < full; ++t)
-                slice_ahead<true, false>(acc, F, slot(t), slot(t + 1), min(STAGES - 2, full - 2 - t), off, none, wm0,
+                slice_ahead<true, false>(acc, F, slot(t), slot(t + 1), min(STAGES - 2, total - 2 - t), off, none, wm0,
                                          wn0, lane, wave);
             if (t < full) slice_ahead<false, false>(acc, F, smem, smem, 0, off, none, wm0, wn0, lane, wave);
         } else {
             Frags f[2];
             static_assert(AHEAD || KSUB % 2 == 0, "a slice starts on buffer 0");
             if (full > 0) {
-                wait_slice(min(STAGES - 2, full - 1));
-                if (STAGES - 1 < full) copy(STAGES - 1);
+                wait_slice(min(STAGES - 2, total - 1));
+                if (STAGES - 1 < total) copy(STAGES - 1);
                 read_frags(f[0], smem, 0, wm0, wn0, lane);
             }
             int t = 0;
-            for (; t + STAGES < full; ++t)
+            for (; t + STAGES < total; ++t)
                 slice_steps<0, true, true>(acc, f, slot(t), slot(t + 1), STAGES - 2, off,
                                            source(g, m0, n0, t + STAGES, wave), wm0, wn0, lane, wave);
             for (; t + 1 < full; ++t)
-                slice_steps<0, true, false>(acc, f, slot(t), slot(t + 1), min(STAGES - 2, full - 2 - t), off, none,
+                slice_steps<0, true, false>(acc, f, slot(t), slot(t + 1), min(STAGES - 2, total - 2 - t), off, none,
                                             wm0, wn0, lane, wave);
             if (t < full) slice_steps<0, false, false>(acc, f, slot(t), smem, 0, off, none, wm0, wn0, lane, wave);
         }
-        if (left > 0) {
-            // into slot full % STAGES: every wave passed the barrier (in
-            // slice full-2, or the prologue's) before which it had finished
-            // reading it, and that barrier's wait drained the copies
+        if (Tr::PARTIAL && left > 0) {
+            // the partial slice (of a short row: the only one)
             TG_LDS char* s = slot(full);
-            fill_tail(s, g, m0, n0, full, wave, lane);
-            wait_lds_then_barrier();
+            if (full > 0) {
+                wait_slice(0);
+            } else {
+                fill_short(s, g, m0, n0);
+                wait_lds_then_barrier();
+            }
+            const int drop = full > 0 ? ROW - left : 0, end = full > 0 ? ROW : left;
             Frags f;
-            for (int u = 0; u * (2 * LB) < left; ++u) {
+            for (int u = drop / (2 * LB); u * (2 * LB) < end; ++u) {
                 read_frags(f, s, u, wm0, wn0, lane);
+                drop_first(f, u, drop, lane);
 #pragma unroll
                 for (int k = 0; k < NM; ++k) mma_one(k, acc, f);
             }
