@@ -166,6 +166,22 @@ def test_gemm(M, N, K):
     check_product(tl.gemm_fp8(a, sa, b, sb), av, bv, K)
 
 
+@pytest.mark.parametrize("K", [1, 5, 15, 16, 17, 31, 64, 80, 100, 112, 127, 128, 129, 143, 145, 192, 250, 255, 257, 400])
+@pytest.mark.parametrize("M,N", [(70, 90), (300, 1400), (1900, 1990), (3500, 3600)])
+def test_gemm_short_rows_and_partial_slices(M, N, K):
+    # every element is 1: C is K exactly (rounded), whatever repeats a byte shows;
+    # then an infinity or a NaN in one place, which only its row and column see
+    one = torch.ones((M, K), device="cuda"), torch.ones((N, K), device="cuda")
+    (a, sa), (b, sb) = (tl.quantize_fp8(x, dtype=torch.float8_e5m2) for x in one)
+    want = torch.full((M, N), float(K), device="cuda").bfloat16()
+    assert torch.equal(tl.gemm_fp8(a, sa, b, sb), want)
+    for k in sorted({0, K // 2, max(K - 17, 0), K - 1}):
+        bits = a.clone().view(torch.uint8)
+        bits[M - 1, k] = 0x7C  # infinity
+        c = tl.gemm_fp8(bits.view(a.dtype), sa, b, sb)
+        assert bool(torch.isposinf(c[M - 1]).all()) and torch.equal(c[:M - 1], want[:M - 1]), k
+
+
 @pytest.mark.parametrize("fa,fb", [("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
 @pytest.mark.parametrize("M,N,K", [(3, 200, 700), (30, 48, 300), (60, 64, 1200), (130, 140, 520), (520, 640, 333)])
 def test_gemm_formats(M, N, K, fa, fb):

@@ -179,19 +179,20 @@ struct NtGemm {
     // per-lane byte offsets of the copies from the slice's first byte of the
     // tile's first row (scales: from the wave's operand's table row); rows
     // past the operand's last are read from the last: they only feed elements
-    // of C that are never stored
+    // of C that are never stored.  Rows shorter than a slice: chunks that pass
+    // the row's end are its last 16 bytes.
     __device__ static __forceinline__ void offsets(Offsets& o, const NtOperands& g, int m0, int n0, int wave,
                                                    int lane) {
-        const int tid = threadIdx.x;
+        const int tid = threadIdx.x, most = Tr::PARTIAL ? g.k - 16 : ROW;
 #pragma unroll
         for (int q = 0; q < A_PER; ++q) {
             const int p = (q * NT + tid) >> 3, c = chunk_of(p, tid & 7);
-            o.a[q] = (uint32_t)((int64_t)(min(m0 + row_at<WTM>(p), g.M - 1) - m0) * g.lda + c * 16);
+            o.a[q] = (uint32_t)((int64_t)(min(m0 + row_at<WTM>(p), g.M - 1) - m0) * g.lda + min(c * 16, most));
         }
 #pragma unroll
         for (int q = 0; q < B_PER; ++q) {
             const int p = (q * NT + tid) >> 3, c = chunk_of(p, tid & 7);
-            o.b[q] = (uint32_t)((int64_t)(min(n0 + row_at<WTN>(p), g.N - 1) - n0) * g.ldb + c * 16);
+            o.b[q] = (uint32_t)((int64_t)(min(n0 + row_at<WTN>(p), g.N - 1) - n0) * g.ldb + min(c * 16, most));
         }
         if constexpr (Tr::SCALED) {
             const int d = wave * S_PER + lane % S_PER;  // dword of the tile's scales: A's, then B's
@@ -209,7 +210,7 @@ struct NtGemm {
     };
     __device__ static __forceinline__ Source source(const NtOperands& g, int m0, int n0, int sl, int wave) {
         Source r;
-        const int64_t at = Tr::PARTIAL ? min((int64_t)sl * ROW, (int64_t)g.k - ROW) : (int64_t)sl * ROW;
+        const int64_t at = Tr::PARTIAL ? max(min((int64_t)sl * ROW, (int64_t)g.k - ROW), (int64_t)0) : (int64_t)sl * ROW;
         r.a = g.a + (int64_t)m0 * g.lda + at;
         r.b = g.b + (int64_t)n0 * g.ldb + at;
         r.s = nullptr;
@@ -379,7 +380,7 @@ struct NtGemm {
         }
     }
 
-    // ---- rows of less than one slice -------------------------------------------
+    // ---- rows of less than 16 bytes --------------------------------------------
     // Through registers: zero past the row's end (a zero in both operands adds
     // nothing).
     __device__ static __forceinline__ void fill_short(TG_LDS char* slot, const NtOperands& g, int m0, int n0) {
@@ -409,11 +410,15 @@ struct NtGemm {
         }
     }
 
-    // Fragments of K step s without the slice's first `drop` bytes.
-    __device__ static __forceinline__ void drop_first(Frags& f, int s, int drop, int lane) {
+    // Fragments of K step s of the partial slice, zero where its copies hold
+    // bytes that do not count: the first 128 - left of them, which were in the
+    // slice before; in rows shorter than a slice (`alone`), those that the last
+    // chunk repeats and the chunks behind it.
+    __device__ static __forceinline__ void mask_partial(Frags& f, int s, int left, bool alone, int lane) {
 #pragma unroll
         for (int h = 0; h < RB; ++h) {
-            const int gone = drop - 16 * (2 * RB * s + 2 * h + (lane >> 5));  // bytes of this lane's chunk
+            const int c = 2 * RB * s + 2 * h + (lane >> 5);  // this lane's chunk
+            const int gone = !alone ? ROW - left - 16 * c : c < left / 16 ? 0 : c == left / 16 ? 16 - left % 16 : 16;
             i32x4 keep;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -438,7 +443,7 @@ struct NtGemm {
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
         // whole slices, and with a partial one (of `left` bytes) behind them,
         // which is copied like the others
-        const int full = g.k / ROW, left = g.k % ROW, total = Tr::PARTIAL && full > 0 && left > 0 ? full + 1 : full;
+        const int full = g.k / ROW, left = g.k % ROW, total = Tr::PARTIAL && g.k >= 16 && left > 0 ? full + 1 : full;
         Offsets off;
         offsets(off, g, m0, n0, wave, lane);
         auto slot = [&](int t) { return smem + (t % STAGES) * SLOT; };
@@ -483,19 +488,18 @@ struct NtGemm {
             if (t < full) slice_steps<0, false, false>(acc, f, slot(t), smem, 0, off, none, wm0, wn0, lane, wave);
         }
         if (Tr::PARTIAL && left > 0) {
-            // the partial slice (of a short row: the only one)
             TG_LDS char* s = slot(full);
-            if (full > 0) {
+            if (g.k >= 16) {
                 wait_slice(0);
             } else {
                 fill_short(s, g, m0, n0);
                 wait_lds_then_barrier();
             }
-            const int drop = full > 0 ? ROW - left : 0, end = full > 0 ? ROW : left;
+            const bool alone = full == 0;
             Frags f;
-            for (int u = drop / (2 * LB); u * (2 * LB) < end; ++u) {
+            for (int u = alone ? 0 : (ROW - left) / (2 * LB); u * (2 * LB) < (alone ? left : ROW); ++u) {
                 read_frags(f, s, u, wm0, wn0, lane);
-                drop_first(f, u, drop, lane);
+                if (g.k >= 16) mask_partial(f, u, left, alone, lane);
 #pragma unroll
                 for (int k = 0; k < NM; ++k) mma_one(k, acc, f);
             }
