@@ -476,12 +476,15 @@ def _real_code(t, name):
 
 
 def _image(rows, cols, dtype, device):
-    """An empty quantised operand: values, scales whose rows start on 16-byte
-    boundaries, and the row stride of the scales."""
-    q = torch.empty((rows, cols), dtype=dtype, device=device)
+    """An empty quantised operand: values, their row stride, scales, theirs.
+    Rows start where a product reads them fastest: long ones on 128-byte lines
+    (4096x4096 with K = 4099: 73 us back to back, 54 so), short ones and those of
+    the scales on 16-byte boundaries."""
+    ldq = -(-cols // 128) * 128 if cols >= 1024 else -(-cols // 16) * 16
     lds = -(-rows // 16) * 16
+    q = torch.empty((rows, ldq), dtype=dtype, device=device)
     s = torch.empty((-(-cols // FP8_BLOCK), lds), dtype=torch.float8_e8m0fnu, device=device)
-    return q, s if lds == rows else s[:, :rows], lds
+    return q if ldq == cols else q[:, :cols], ldq, s if lds == rows else s[:, :rows], lds
 
 
 def quantize_fp8(X, dtype=torch.float8_e4m3fn, block="row", transpose=False):
@@ -492,7 +495,8 @@ def quantize_fp8(X, dtype=torch.float8_e4m3fn, block="row", transpose=False):
     X: (rows, cols) float32, bfloat16 or float16 on the GPU, row-major (row
     stride may exceed the row length).  Q: (rows, cols) of ``dtype``
     (float8_e4m3fn or float8_e5m2); S: (ceil(cols / 128), rows)
-    float8_e8m0fnu; X[r, c] is near Q[r, c] * S[c // 128, r].  With block
+    float8_e8m0fnu; X[r, c] is near Q[r, c] * S[c // 128, r].  Both are views of
+    padded rows where a product reads those faster.  With block
     "square" one scale serves each 128 x 128 block of X, and Qt is Q
     transposed (weights, whose two images then hold the same values); with
     "row" each image's scales follow its own rows.  A scale is the least power
@@ -510,14 +514,14 @@ def quantize_fp8(X, dtype=torch.float8_e4m3fn, block="row", transpose=False):
     code, device = _real_code(X, "X"), X.device
     rows, cols = X.shape
     ldx = cols if X.is_contiguous() else _ld(X, "X")
-    q, s, lds = _image(rows, cols, dtype, device)
+    q, ldq, s, lds = _image(rows, cols, dtype, device)
     if not transpose:
-        _call(device, _lib.tgemm_fp8_quantize, rows, cols, code, X.data_ptr(), ldx, fmt, BLOCKS[block], q.data_ptr(), cols,
+        _call(device, _lib.tgemm_fp8_quantize, rows, cols, code, X.data_ptr(), ldx, fmt, BLOCKS[block], q.data_ptr(), ldq,
               s.data_ptr(), lds, None, 0, None, 0)
         return q, s
-    qt, st, ldst = _image(cols, rows, dtype, device)
-    _call(device, _lib.tgemm_fp8_quantize, rows, cols, code, X.data_ptr(), ldx, fmt, BLOCKS[block], q.data_ptr(), cols,
-          s.data_ptr(), lds, qt.data_ptr(), rows, st.data_ptr(), ldst)
+    qt, ldqt, st, ldst = _image(cols, rows, dtype, device)
+    _call(device, _lib.tgemm_fp8_quantize, rows, cols, code, X.data_ptr(), ldx, fmt, BLOCKS[block], q.data_ptr(), ldq,
+          s.data_ptr(), lds, qt.data_ptr(), ldqt, st.data_ptr(), ldst)
     return q, s, qt, st
 
 
