@@ -25,7 +25,9 @@ static bool offsets_fit(const Fp8Kernel& k, int64_t lda, int64_t ldb) {
 
 // Model of a kernel's time in microseconds, fitted to runs of every kernel at
 // 23 shapes (1 .. 8192 rows and columns, K = 512 .. 16384; graph replays, a
-// different B each time).  A round is 256 workgroups, one a compute unit.
+// different B each time).  A round is 256 workgroups, one a compute unit; a
+// further round of the kernels for few rows has a least time, however short K
+// (509x3712x114 on rows32: 32 us).
 //   us               256    128  128 pair   64   rows16  32
 //   1x1024x1024                             4.4    2.9   3.1
 //   1x4096x4096                             9.5    6.0   6.2
@@ -82,7 +84,8 @@ static Piece best_piece(const Fp8Kernel* t, int64_t m0, int64_t n0, int64_t M, i
 
 // The launches of a product: one, or a part of whole 256 x 256 tiles and the
 // last columns (or rows) on the kernels for few, where that is quicker: 17
-// tile columns for 4097 take two rounds (4095x4097x4104: 130 us, split 66).
+// tile columns for 4097 take two rounds (4095x4097x4096: 86 us in one launch,
+// split 59).
 static int pieces_of(const Fp8Kernel* t, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, Piece (&out)[2]) {
     out[0] = best_piece(t, 0, 0, M, N, K, lda, ldb);
     int count = 1;
