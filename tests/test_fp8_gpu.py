@@ -163,7 +163,10 @@ GEMMS = [(1, 1, 1), (1, 16, 128), (1, 4096, 1024), (2, 17, 100), (5, 333, 1025),
 def test_gemm(M, N, K):
     a, sa, av = operand(M, K, M + K)
     b, sb, bv = operand(N, K, N + 2 * K)
-    check_product(tl.gemm_fp8(a, sa, b, sb), av, bv, K)
+    c = tl.gemm_fp8(a, sa, b, sb)
+    check_product(c, av, bv, K)
+    # rows back to back, at any byte, where the quantiser padded them
+    assert torch.equal(tl.gemm_fp8(a.contiguous(), sa, b.contiguous(), sb), c)
 
 
 @pytest.mark.parametrize("K", [1, 5, 15, 16, 17, 31, 64, 80, 100, 112, 127, 128, 129, 143, 145, 192, 250, 255, 257, 400])
@@ -211,7 +214,9 @@ def test_gemm_every_kernel(M, N, K, kernel, last):
         return q.double() * torch.exp2(e)
     av, bv = v(a, sa), v(b, sb)
     want, mag = av @ bv.t(), av.abs() @ bv.abs().t()
-    c = tl.gemm_fp8(a, sa, b, sb).double()
+    c = tl.gemm_fp8(a, sa, b, sb)
+    assert torch.equal(tl.gemm_fp8(a.contiguous(), sa, b.contiguous(), sb), c)
+    c = c.double()
     off = (2.0 ** -10 + (K / 8 + 16) * 2.0 ** -24) * mag
     assert bool(((c - want).abs() <= 2.0 ** -8 * (want.abs() + off) + off).all())
     assert float((c - want).norm()) <= 2.0 ** -8 * float(want.norm())
@@ -232,7 +237,9 @@ def test_gemm_random_shapes():
         av, bv = v(a, sa), v(b, sb)
         want, mag = av @ bv.t(), av.abs() @ bv.abs().t()
         off = (2.0 ** -10 + (K / 8 + 16) * 2.0 ** -24) * mag
-        c = tl.gemm_fp8(a, sa, b, sb).double()
+        c = tl.gemm_fp8(a, sa, b, sb)
+        assert torch.equal(tl.gemm_fp8(a.contiguous(), sa, b.contiguous(), sb), c), (M, N, K, fa, fb)
+        c = c.double()
         assert bool(((c - want).abs() <= 2.0 ** -8 * (want.abs() + off) + off).all()), (M, N, K, fa, fb)
 
 
