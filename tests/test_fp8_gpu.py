@@ -389,6 +389,29 @@ def test_rows_longer_than_32_bit_offsets():
         check_product(tl.gemm_fp8(big.view(a.dtype), s, b, sb), av[:m], bv, K)
 
 
+def test_more_than_2_to_the_31_elements():
+    M, K = 66000, 33000
+    x = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    x[:M // 2] = torch.randn((M // 2, K), device="cuda")
+    x[M // 2:] = torch.randn((M - M // 2, K), device="cuda")
+    q, s, qt, st = tl.quantize_fp8(x, transpose=True)
+    r, c = M // 128 * 128 - 256, K // 128 * 128 - 256  # the last blocks of rows, of columns
+    for got, want in ((q[r:], 0), (s[:, r:], 1), (qt[:, r:], 2), (st[r // 128:], 3)):
+        assert torch.equal(got.contiguous().view(torch.uint8),
+                           tl.quantize_fp8(x[r:], transpose=True)[want].contiguous().view(torch.uint8))
+    for got, want in ((q[:, c:], 0), (s[c // 128:], 1), (qt[c:], 2), (st[:, c:], 3)):
+        assert torch.equal(got.contiguous().view(torch.uint8),
+                           tl.quantize_fp8(x[:, c:], transpose=True)[want].contiguous().view(torch.uint8))
+    # a product of as many results: its last rows against those of the last rows alone
+    w, ws = tl.quantize_fp8(torch.randn((K, 200), device="cuda"))
+    a, sa = q[:, :200], s[:2]
+    y = tl.gemm_fp8(a, sa, w, ws)
+    assert y.shape == (M, K) and y.numel() > 2 ** 31
+    for rows in (slice(0, 128), slice(r, M)):
+        want = tl.gemm_fp8(a[rows], sa[:, rows], w, ws).double()
+        assert float((y[rows].double() - want).norm()) <= 2.0 ** -7 * float(want.norm())  # two roundings
+
+
 def test_on_another_stream_and_replayed_from_a_graph():
     x = draw(130, 300, 1, torch.bfloat16).cuda()
     w = draw(200, 300, 2, torch.bfloat16).cuda()
