@@ -455,10 +455,10 @@ const char* tgemm_fp8_gemm_kernel(int64_t M, int64_t N, int64_t K, int64_t lda, 
  * 4e-3 where a few equal singular values hold all of it).  Elements of X
  * below 2^-37 are taken as zero (a matrix far smaller than eps).  A matrix
  * of zeros gives zeros (for eps > 0); one with a NaN or an infinity gives
- * NaN everywhere.  Coefficients are refused (TGEMM_E_ARG) when they let
- * singular values that start in [0, 1] pass 3.5 before the last step, or
- * |b s^2 + c s^4| pass 14 in any: the workspace's half precision matrices
- * hold no more.
+ * NaN everywhere.  Coefficients are refused (TGEMM_E_ARG) when they are not
+ * finite or above 1e15, or let singular values that start in [0, 1] pass 3.5
+ * before the last step, or |b s^2 + c s^4| pass 14 in any: the workspace's half
+ * precision matrices hold no more.
  *
  * workspace: tgemm_orthogonalize_workspace_bytes(batch, rows, cols) bytes
  * (-1 for sizes out of range: rows and cols up to 2^20, batch up to 2^16) of

@@ -64,3 +64,45 @@ def test_matrices_of_a_tensor():
     assert tl._matrices(t[0, 0].expand(3, 10, 8)) is None
     assert tl._matrices(t[0, 0, 0].expand(10, 8)) is None
     assert tl._matrices(t[:0])[0] == (0, 10, 8)
+
+
+def reach(coef):
+    """What each step's coefficients can make of singular values in [0, 1], on a
+    fine grid: the largest before the last step, and of |b s^2 + c s^4|."""
+    import numpy as np
+    top, most, poly = 1.0, 1.0, 0.0
+    for k, (a, b, c) in enumerate(coef):
+        s = np.linspace(0.0, top, 20001)
+        q = b * s ** 2 + c * s ** 4
+        poly = max(poly, float(abs(q).max()))
+        top = float(abs((a + q) * s).max())
+        if k + 1 < len(coef):
+            most = max(most, top)
+        if most > 3.5 or poly > 14.0:
+            break
+    return most, poly
+
+
+def test_range_of_coefficients():
+    import random
+    r = random.Random(5)
+    seen = set()
+    for _ in range(600):
+        n = r.randint(1, 6)
+        coef = [(r.uniform(-4, 4), r.choice([0.0, r.uniform(-8, 8)]), r.choice([0.0, r.uniform(-6, 6)])) for _ in range(n)]
+        if r.random() < 0.3:
+            coef = [USUAL] * n
+            coef[r.randrange(n)] = tuple(v * r.uniform(0.8, 1.3) for v in USUAL)
+        most, poly = reach(coef)
+        if min(abs(most - 3.5) / 3.5, abs(poly - 14.0) / 14.0) < 1e-4:
+            continue
+        fits = most <= 3.5 and poly <= 14.0
+        assert (call(batch=0, steps=n, coef=[v for t in coef for v in t]) == 0) == fits, (coef, most, poly)
+        seen.add((fits, n))
+    assert len(seen) > 8
+    # values whose powers leave the range of double
+    for t in ((1e200, 0.0, 0.0), (1e308, -1e308, 1e308), (0.0, 1e308, -1e308), (-1e300, 1e-300, 0.0), (0.0, 0.0, 1e308)):
+        assert call(batch=0, steps=4, coef=t * 4) == -1
+        assert call(batch=0, steps=4, coef=(1.0, 0.0, 0.0) * 2 + t * 2) == -1
+    for t in ((0.0, 0.0, 0.0), (1e-300, 0.0, 0.0), (1.0, 1e-300, -1e-300)):
+        assert call(batch=0, steps=4, coef=t * 4) == 0

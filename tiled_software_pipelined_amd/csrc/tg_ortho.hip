@@ -202,6 +202,49 @@ __global__ __launch_bounds__(G::NT) void ortho_gram_kernel(OrthoArgs g) {
     store_gram<G>(g, t, acc);
 }
 
+// B' and e of a matrix of one tile from the sums of X X^T: A' goes to LDS as the
+// one slice that A' A' walks, d beside it.
+template <class G>
+__device__ __forceinline__ void poly_of_one_tile(const OrthoArgs& g, const OrthoTile<G>& t, typename G::Acc& acc,
+                                                 TG_LDS char* slot, float* d) {
+    static_assert(G::FM == 1 && G::FN == 1 && G::BM == 64 && G::BN == 64, "64 half precision columns are one slice");
+    const int n = t.wn0 + (t.lane & 31);
+    __syncthreads();  // the product's slices are read
+    _Float16 a[16];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int m = t.wm0 + quad_row<1>(q, t.lane);
+        Halves<4> four;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float v = acc[4 * q + k] * (1.0f / (ONE * ONE));
+            if (m + k == n) d[n] = v;
+            a[4 * q + k] = four.v[k] = (_Float16)(m + k == n ? 0.0f : v * ONE);
+        }
+        // A' is symmetric: rows m .. m + 3 of column n are columns of row n
+        __builtin_memcpy(slot + n * G::ROW + G::chunk_of(n, m / 8) * 16 + m % 8 * 2, &four, sizeof four);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
+#pragma unroll
+    for (int s = 0; s < G::KSUB; ++s) {
+        typename G::Frag x, y;
+        x.v[0] = G::read_chunk(slot, t.wm0, s, 0, t.lane);
+        y.v[0] = G::read_chunk(slot, t.wn0, s, 0, t.lane);
+        acc = NtF16::mma<0, 0>(x, y, acc, 0, 0);
+    }
+    _Float16* B = g.b + (int64_t)t.z * g.ms * g.ms;
+    const float dn = d[n];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const int m = t.wm0 + G::row_of(0, r, t.lane);
+        const float di = d[m], sq = acc[r] * (1.0f / (ONE * ONE)), av = (float)a[r] * (1.0f / ONE);
+        if (m == n) g.e[(int64_t)t.z * g.ms + m] = g.cb * di + g.cc * (di * di + sq);
+        B[(int64_t)m * g.ms + n] = (_Float16)(m == n ? 0.0f : (g.cb * av + g.cc * ((di + dn) * av + sq)) * ONE);
+    }
+}
+
 // The same with each tile's long axis split over g.parts workgroups, for few
 // tiles: what bounds a workgroup there is the rate at which one compute unit's
 // copies arrive (kernel times, one workgroup a tile and split: 64 x 4096 12.4, 8.0
@@ -214,7 +257,11 @@ __global__ __launch_bounds__(G::NT) void ortho_gram_kernel(OrthoArgs g) {
 // release and acquire order them between workgroups: one a workgroup, since
 // each flushes its XCD's cache (128 x 4096 in 8 parts: 8.9 us, with a device
 // fence in every wave 10.7).
-template <class G>
+//
+// POLY: the matrix is this one tile (up to 64 rows), and its workgroup goes on
+// to B' and e: a launch less each step (64 x 1024: a call's kernels 80 us,
+// now 62).
+template <class G, bool POLY>
 __global__ __launch_bounds__(G::NT) void ortho_gram_split_kernel(OrthoArgs g) {
     static_assert(G::FM == 1 && G::FN == 1, "16 sums a lane");
     __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
@@ -228,35 +275,42 @@ __global__ __launch_bounds__(G::NT) void ortho_gram_split_kernel(OrthoArgs g) {
     G::product(ortho_operands(X, g.mp, g.np, X, g.mp, g.np, min(g.run, g.np - from)), t.m0, t.n0,
                (TG_LDS char*)smem_raw, acc, t.wm0, t.wn0, t.lane, t.wave);
 
-    constexpr int TILE = G::BM * G::BN;
-    float* sums = g.part + (int64_t)tile * g.parts * TILE + 1024 * t.wave + t.lane;
+    if (g.parts > 1) {
+        constexpr int TILE = G::BM * G::BN;
+        float* sums = g.part + (int64_t)tile * g.parts * TILE + 1024 * t.wave + t.lane;
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-        __hip_atomic_store(sums + (int64_t)part * TILE + 64 * r, acc[0][0][r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (threadIdx.x == 0)
-        last = __hip_atomic_fetch_add(g.arrived + tile, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == g.parts - 1;
-    __syncthreads();
-    if (!last) return;
-    if (threadIdx.x == 0) g.arrived[tile] = 0;  // for the next step's launch
+        for (int r = 0; r < 16; ++r)
+            __hip_atomic_store(sums + (int64_t)part * TILE + 64 * r, acc[0][0][r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (threadIdx.x == 0)
+            last = __hip_atomic_fetch_add(g.arrived + tile, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == g.parts - 1;
+        __syncthreads();
+        if (!last) return;
+        if (threadIdx.x == 0) g.arrived[tile] = 0;  // for the next step's launch
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[0][0][r] = 0.0f;
-    // four parts' sums in flight at a time
-    for (int p = 0; p < g.parts; p += 4) {
-        float v[4][16];
+        for (int r = 0; r < 16; ++r) acc[0][0][r] = 0.0f;
+        // four parts' sums in flight at a time
+        for (int p = 0; p < g.parts; p += 4) {
+            float v[4][16];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                v[u][r] = __hip_atomic_load(sums + (int64_t)min(p + u, g.parts - 1) * TILE + 64 * r, __ATOMIC_RELAXED,
-                                            __HIP_MEMORY_SCOPE_AGENT);
+                for (int r = 0; r < 16; ++r)
+                    v[u][r] = __hip_atomic_load(sums + (int64_t)min(p + u, g.parts - 1) * TILE + 64 * r, __ATOMIC_RELAXED,
+                                                __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[0][0][r] += p + u < g.parts ? v[u][r] : 0.0f;
+                for (int r = 0; r < 16; ++r) acc[0][0][r] += p + u < g.parts ? v[u][r] : 0.0f;
+        }
     }
-    store_gram<G>(g, t, acc);
+    if constexpr (POLY) {
+        __shared__ float d[G::BM];
+        poly_of_one_tile<G>(g, t, acc[0][0], (TG_LDS char*)smem_raw, d);
+    } else {
+        store_gram<G>(g, t, acc);
+    }
 }
 
 // B = b A + c A^2: B' (diagonal zero) and e.
@@ -418,7 +472,8 @@ struct OrthoInArgs {
     const void* G;
     int64_t ldg, stride_g;
     int32_t rows, cols;  // of G
-    double* part;        // PARTS sums of squares for each matrix
+    double* part;        // room for PARTS sums of squares for each matrix
+    int32_t parts;       // of which are used
     _Float16 *hi, *lo, *xt;
     int32_t mp, np, tall;
     int32_t lane_bits;   // the norm's: 2^lane_bits threads take one row together
@@ -461,7 +516,7 @@ __device__ __forceinline__ void load8(float (&v)[8], const typename E::T* row, i
     for (int k = 0; k < 8; ++k) v[k] = E::up(u.t[k]);
 }
 
-// Workgroup (p, z): pieces p, p + PARTS .. of matrix z, a piece 2048 elements
+// Workgroup (p, z): pieces p, p + parts .. of matrix z, a piece 2048 elements
 // of a row, or as many rows together as 256 threads reach where rows are
 // short; its sum of squares in double (squares of any float fit), always in
 // the same order.  Four pieces are requested at a time (one: 4096x4096 20 us;
@@ -470,20 +525,20 @@ template <class E>
 __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoInArgs g) {
     __shared__ double sums[4];
     constexpr int AT_ONCE = 4;
-    const int p = blockIdx.x % PARTS, z = blockIdx.x / PARTS;
+    const int p = blockIdx.x % g.parts, z = blockIdx.x / g.parts;
     const int tid = threadIdx.x, lanes = 1 << g.lane_bits, rows = 256 >> g.lane_bits;
     const int per = (g.cols + 8 * lanes - 1) / (8 * lanes);
     const int64_t pieces = (int64_t)((g.rows + rows - 1) / rows) * per;
     double s = 0.0;
-    for (int64_t i = p; i < pieces; i += AT_ONCE * PARTS) {
+    for (int64_t i = p; i < pieces; i += AT_ONCE * g.parts) {
         float v[AT_ONCE][8];
 #pragma unroll
         for (int u = 0; u < AT_ONCE; ++u) {
-            const int64_t k = min(i + u * PARTS, pieces - 1);
+            const int64_t k = min(i + u * g.parts, pieces - 1);
             const int r = (int)(k / per) * rows + (tid >> g.lane_bits);
             const int c = (int)(k % per) * 8 * lanes + 8 * (tid & (lanes - 1));
             // a piece, rows or columns past the last: zeros
-            const int end = i + u * PARTS < pieces && r < g.rows ? g.cols : 0;
+            const int end = i + u * g.parts < pieces && r < g.rows ? g.cols : 0;
             load8<E>(v[u], static_cast<const typename E::T*>(g.G) + (int64_t)z * g.stride_g +
                                (int64_t)min(r, g.rows - 1) * g.ldg, c, end);
         }
@@ -519,7 +574,7 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoInArgs g) {
                  c0 + 8 * (tid & 7), r < g.rows ? g.cols : 0);
     }
     if (blockIdx.x == 0 && tid < g.counters) g.arrived[tid] = 0;
-    double s = g.part[(int64_t)z * PARTS + tid];
+    double s = tid < g.parts ? g.part[(int64_t)z * PARTS + tid] : 0.0;
     static_assert(PARTS == 256, "a part for each thread");
     for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
     if ((tid & 63) == 0) sums[tid >> 6] = s;
@@ -709,20 +764,33 @@ static bool ortho_sizes_ok(int64_t batch, int64_t rows, int64_t cols) {
 }
 
 // The largest singular value the steps before the last can reach from [0, 1],
-// and the largest |b s^2 + c s^4|: NaN or large where the coefficients make
-// the iteration leave the range that the workspace holds.
+// and the largest |b s^2 + c s^4| in any, up to the first step that passes what
+// the workspace holds.  Both polynomials are largest at an end of the range or
+// where their derivative is zero.
+constexpr double MOST_X = 3.5, MOST_POLY = 14.0;
 static void ortho_reach(int steps, const double* coef, double* x, double* poly) {
     double top = 1.0, most = 1.0, p = 0.0;
     for (int k = 0; k < steps; ++k) {
         const double a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2];
         double next = 0.0;
-        for (int i = 0; i <= 4096; ++i) {
-            const double s = top * i / 4096.0, q = b * s * s + c * s * s * s * s, y = fabs((a + q) * s);
+        auto look = [&](double t) {  // t = s^2
+            if (!(t >= 0.0 && t <= top * top)) return;
+            const double q = (b + c * t) * t, y = fabs((a + q) * sqrt(t));
             if (!(y <= next)) next = y;
             if (!(fabs(q) <= p)) p = fabs(q);
+        };
+        look(top * top);
+        if (c != 0.0) look(-b / (2.0 * c));
+        // a + 3 b t + 5 c t^2 = 0, by the quotients that lose no digits
+        const double r = 9.0 * b * b - 20.0 * a * c;
+        if (r >= 0.0) {
+            const double u = -0.5 * (3.0 * b + copysign(sqrt(r), b));
+            if (c != 0.0) look(u / (5.0 * c));
+            if (u != 0.0) look(a / u);
         }
         top = next;
         if (k + 1 < steps && !(top <= most)) most = top;
+        if (!(most <= MOST_X) || !(p <= MOST_POLY)) break;
     }
     *x = most;
     *poly = p;
@@ -773,14 +841,15 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
         return TGEMM_E_NULL;
     }
     for (int i = 0; i < 3 * steps; ++i)
-        if (!std::isfinite(coefficients[i])) {
-            set_error("coefficient %d is not finite", i);
+        if (!(fabs(coefficients[i]) <= 1e15)) {  // the kernels take them as float, their squares are taken here
+            set_error("coefficient %d is not finite or above 1e15", i);
             return TGEMM_E_ARG;
         }
     double reach, poly;
     ortho_reach(steps, coefficients, &reach, &poly);
-    if (!(reach <= 3.5) || !(poly <= 14.0)) {
-        set_error("these coefficients let singular values reach %g (3.5) or b s^2 + c s^4 reach %g (14)", reach, poly);
+    if (!(reach <= MOST_X) || !(poly <= MOST_POLY)) {
+        set_error("these coefficients let singular values reach %g (%g) or b s^2 + c s^4 reach %g (%g)", reach, MOST_X, poly,
+                  MOST_POLY);
         return TGEMM_E_ARG;
     }
     if (batch == 0 || rows == 0 || cols == 0) {
@@ -828,6 +897,10 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     in.np = (int32_t)p.np;
     in.tall = rows > cols;
     while (in.lane_bits < 8 && (INT64_C(8) << in.lane_bits) < cols) ++in.lane_bits;
+    // a workgroup for each piece, up to PARTS (PARTS for every matrix: 300 of
+    // 40 x 70 61 us, now 5.5)
+    const int64_t pieces = ((rows + (256 >> in.lane_bits) - 1) / (256 >> in.lane_bits)) * ((cols + 2047) / 2048);
+    in.parts = (int32_t)(pieces < PARTS ? pieces : PARTS);
     in.eps = eps;
     in.arrived = (int32_t*)(ws + p.off_arrived);
     in.counters = p.parts > 1 ? (int32_t)(batch * p.tri) : 0;
@@ -836,7 +909,7 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     const OrthoInFn load_fn = dtype == TGEMM_F32 ? ortho_load_kernel<EF32>
                               : dtype == TGEMM_BF16 ? ortho_load_kernel<EBF16> : ortho_load_kernel<EF16>;
     void* in_args[] = {&in};
-    hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(norm_fn), dim3((unsigned)(PARTS * batch)), dim3(256),
+    hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(norm_fn), dim3((unsigned)(in.parts * batch)), dim3(256),
                                      in_args, 0, s);
     if (err == hipSuccess)
         err = hipLaunchKernel(reinterpret_cast<const void*>(load_fn), dim3((unsigned)(batch * load)), dim3(256), in_args, 0,
@@ -877,8 +950,12 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
         g.cc = (float)coefficients[3 * k + 2];
         g.xt = (const _Float16*)(ws + (k % 2 ? p.off_t1 : p.off_t0));
         g.xt_out = (_Float16*)(ws + (k % 2 ? p.off_t0 : p.off_t1));
-        launch(p.parts > 1 ? ortho_gram_split_kernel<Ortho64> : p.sym->first, *p.sym, tri, p.parts);
-        launch(p.sym->second, *p.sym, tri, 1);
+        if (p.sym->tile == 64 && tri == 1) {
+            launch(ortho_gram_split_kernel<Ortho64, true>, *p.sym, tri, p.parts);
+        } else {
+            launch(p.parts > 1 ? ortho_gram_split_kernel<Ortho64, false> : p.sym->first, *p.sym, tri, p.parts);
+            launch(p.sym->second, *p.sym, tri, 1);
+        }
         launch(k + 1 < steps ? p.upd->first : p.upd->second, *p.upd, upd, 1);
     }
     if (err != hipSuccess) {
