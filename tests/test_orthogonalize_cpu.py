@@ -106,3 +106,23 @@ def test_range_of_coefficients():
         assert call(batch=0, steps=4, coef=(1.0, 0.0, 0.0) * 2 + t * 2) == -1
     for t in ((0.0, 0.0, 0.0), (1e-300, 0.0, 0.0), (1.0, 1e-300, -1e-300)):
         assert call(batch=0, steps=4, coef=t * 4) == 0
+
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that passes for one on the GPU, where nothing is launched."""
+    is_cuda = property(lambda self: True)
+
+
+def test_steps_that_a_32_bit_count_does_not_hold(monkeypatch):
+    # 2^32 + 5 would run as 5 steps, 5 - 2^32 as 5 with coefficients for none
+    calls = []
+    monkeypatch.setattr(tl, "_call", lambda device, fn, *args: calls.append(args))
+    G = torch.zeros(4, 6).as_subclass(OnGpu)
+    for steps in (2 ** 32 + 5, 5 - 2 ** 32, -(2 ** 40), 2 ** 63, 0, 65, -1, 2.5, float("nan")):
+        with pytest.raises(tl.TgemmError):
+            tl.orthogonalize(G, steps=steps)
+    assert not calls
+    for steps, co, want in ((5, USUAL, USUAL * 5), (1, [USUAL], USUAL), (3, [(1, 0, 0)] * 3, (1, 0, 0) * 3),
+                            (3, (1, 0, 0), (1, 0, 0) * 3), (2.0, USUAL, USUAL * 2)):
+        tl.orthogonalize(G, steps=steps, coefficients=co)
+        assert calls[-1][10] == steps and tuple(calls[-1][11]) == tuple(want)

@@ -713,9 +713,24 @@ def _matrices(t):
     return (batch, rows, cols), ld, step
 
 
+def _newton_schulz(steps, coefficients):
+    """The number of steps and their coefficients as the library takes them:
+    three doubles for each of 1 to 64 steps (a 32-bit count reads no others)."""
+    if not 1 <= steps <= 64 or steps != int(steps):
+        raise TgemmError(-1, "steps=%s (1 .. 64)" % (steps,))
+    steps, flat = int(steps), list(coefficients)
+    if len(flat) == 3 and not hasattr(flat[0], "__len__"):
+        flat = flat * steps
+    elif len(flat) != steps or any(len(c) != 3 for c in flat):
+        raise ValueError("coefficients must be (a, b, c) or one such triple for each of the %d steps" % steps)
+    else:
+        flat = [v for c in flat for v in c]
+    return steps, (ctypes.c_double * (3 * steps))(*map(float, flat))
+
+
 def orthogonalize(G, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e-7, out=None):
     """The orthogonalised update of the Muon optimiser: G with its singular
-    values brought near one by ``steps`` Newton-Schulz steps.
+    values brought near one by ``steps`` (1 to 64) Newton-Schulz steps.
 
     G: (..., rows, cols) float32, bfloat16 or float16 on the GPU, each matrix
     by itself.  X = G / (|G| + eps) (Frobenius norm), then for each step
@@ -732,14 +747,7 @@ def orthogonalize(G, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e-7,
     code = _real_code(G, "G")
     if G.dim() < 2:
         raise ValueError("G must have at least 2 dimensions")
-    flat = list(coefficients)
-    if len(flat) == 3 and not hasattr(flat[0], "__len__"):
-        flat = flat * max(0, min(int(steps), 65))  # past 64 the library refuses the count
-    else:
-        if len(flat) != steps or any(len(c) != 3 for c in flat):
-            raise ValueError("coefficients must be (a, b, c) or one such triple for each of the %d steps" % steps)
-        flat = [v for c in flat for v in c]
-    coef = (ctypes.c_double * max(len(flat), 1))(*map(float, flat))
+    steps, coef = _newton_schulz(steps, coefficients)
     if out is None:
         out = torch.empty(G.shape, dtype=torch.bfloat16, device=G.device)
     elif out.dtype != torch.bfloat16 or out.shape != G.shape or out.device != G.device:
@@ -760,5 +768,5 @@ def orthogonalize(G, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e-7,
     # 512-byte boundaries
     ws = torch.empty(max(need, 1), dtype=torch.uint8, device=G.device)
     _call(G.device, _lib.tgemm_orthogonalize, batch, rows, cols, code, G.data_ptr(), ldg, stride_g, out.data_ptr(), ldo,
-          stride_o, int(steps), coef, float(eps), ws.data_ptr(), need)
+          stride_o, steps, coef, float(eps), ws.data_ptr(), need)
     return out
