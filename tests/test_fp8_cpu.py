@@ -189,3 +189,26 @@ def test_package_offers_the_operators():
     for name in package.__all__:
         assert getattr(package, name) is getattr(tl, name)
     assert not hasattr(package, "no_such_name")
+
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that passes for one on the GPU, where nothing is launched."""
+    is_cuda = property(lambda self: True)
+
+
+@pytest.mark.parametrize("dual", ["x", "w", "both"])
+@pytest.mark.parametrize("grad", [True, False])
+def test_linear_refuses_forward_mode(monkeypatch, dual, grad):
+    # a dual tensor has no requires_grad: its tangent must not be dropped in silence
+    monkeypatch.setattr(tl, "_linear_forward",
+                        lambda x, w, keep: (torch.zeros(x.shape[0], w.shape[0]), torch.zeros(1)))
+    x, w = torch.ones(4, 8).as_subclass(OnGpu), torch.ones(6, 8).as_subclass(OnGpu)
+    assert tl.linear_fp8(x, w).shape == (4, 6)
+    ad = torch.autograd.forward_ad
+    with ad.dual_level(), torch.set_grad_enabled(grad):
+        assert tl.linear_fp8(x, w).shape == (4, 6)  # no tangent: as outside
+        xd = ad.make_dual(x, torch.ones(4, 8)) if dual != "w" else x
+        wd = ad.make_dual(w, torch.ones(6, 8)) if dual != "x" else w
+        with pytest.raises(NotImplementedError):
+            tl.linear_fp8(xd, wd)
+    assert tl.linear_fp8(x, w).shape == (4, 6)

@@ -556,3 +556,18 @@ def test_linear_step_replayed_from_a_graph():
         torch.cuda.synchronize()
         want = step()
         assert all(torch.equal(p, q) for p, q in zip(held, want)), r
+
+
+def test_linear_refuses_forward_mode():
+    x, w = draw(20, 40, 1).cuda(), draw(30, 40, 2).cuda()
+    want = tl.linear_fp8(x, w)
+    ad = torch.autograd.forward_ad
+    with ad.dual_level():
+        assert torch.equal(tl.linear_fp8(x, w), want)
+        for a, b in ((ad.make_dual(x, torch.ones_like(x)), w), (x, ad.make_dual(w, torch.ones_like(w)))):
+            with pytest.raises(NotImplementedError):
+                tl.linear_fp8(a, b)
+            with torch.no_grad(), pytest.raises(NotImplementedError):
+                tl.linear_fp8(a, b)
+    with pytest.raises((NotImplementedError, RuntimeError)):
+        torch.func.jvp(lambda t: tl.linear_fp8(t, w), (x,), (x,))

@@ -435,6 +435,7 @@ def gemm(A, B, out=None, variant: Variant | None = None, workspace: bool = True)
 # ---- 8-bit floating point products with block scales --------------------------
 
 import torch  # noqa: E402  (_load has imported it)
+from torch.autograd import forward_ad  # noqa: E402
 
 FP8_BLOCK = 128  # elements of a row that share a scale
 E4M3, E5M2 = 0, 1
@@ -664,8 +665,8 @@ def linear_fp8(x, w, grad_dtype=torch.float8_e4m3fn):
     (float8_e4m3fn or float8_e5m2), along its rows for x's gradient and along
     its columns for w's, and takes both products from the 8-bit images kept by
     the forward pass: dx = g w, dw = g^T x.  Rounding is passed straight
-    through.  Gradients have their inputs' dtypes; second derivatives are
-    refused.  A weight that does not change between calls is better quantised
+    through.  Gradients have their inputs' dtypes; second derivatives and
+    forward-mode ones are refused.  A weight that does not change between calls is better quantised
     once (:func:`quantize_fp8`, then :func:`gemm_fp8`).  To capture a training
     step into a graph, capture torch.autograd.grad, or make sure that no eager
     graph of the same leaves is alive: torch's nodes that accumulate into
@@ -676,7 +677,10 @@ def linear_fp8(x, w, grad_dtype=torch.float8_e4m3fn):
         raise ValueError("x and w must be on one GPU (%s, %s)" % (x.device, w.device))
     if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
         raise ValueError("x %s and w %s do not make x @ w^T" % (tuple(x.shape), tuple(w.shape)))
-    if not (torch.is_grad_enabled() and (x.requires_grad or w.requires_grad)):
+    # straight to the kernels where nothing can want a derivative: a dual tensor
+    # of torch.autograd.forward_ad has a tangent and no requires_grad, and the
+    # autograd function refuses it (it has no forward-mode rule)
+    if forward_ad._current_level < 0 and not (torch.is_grad_enabled() and (x.requires_grad or w.requires_grad)):
         return _linear_forward(x, w, 0)[0]
     return _LinearFp8.apply(x, w, grad_dtype)
 
