@@ -4,6 +4,8 @@ import ctypes
 import pytest
 import torch
 
+import ortho_ref
+
 tl = pytest.importorskip("tiled_software_pipelined_amd.lib")
 P = ctypes.c_void_p
 USUAL = (3.4445, -4.7750, 2.0315)
@@ -126,3 +128,27 @@ def test_steps_that_a_32_bit_count_does_not_hold(monkeypatch):
                             (3, (1, 0, 0), (1, 0, 0) * 3), (2.0, USUAL, USUAL * 2)):
         tl.orthogonalize(G, steps=steps, coefficients=co)
         assert calls[-1][10] == steps and tuple(calls[-1][11]) == tuple(want)
+
+
+def emulated_error(G):
+    want = ortho_ref.exact(G)
+    return float((ortho_ref.emulate(G) - want).norm() / want.norm())
+
+
+# what the header states of the error before the result's own rounding, and the
+# tests on the GPU rest on: 1.3e-3 of the norm for random matrices, 4.5e-3 for any
+@pytest.mark.parametrize("m,n", [(2, 3), (16, 16), (31, 33), (63, 200), (65, 64), (100, 1000), (128, 384), (257, 129)])
+def test_emulated_error_of_random_matrices(m, n):
+    for seed in range(3):
+        G = torch.randn((m, n), generator=torch.Generator().manual_seed(m + n + seed))
+        assert emulated_error(G) <= 1.3e-3
+        assert emulated_error(G.bfloat16()) <= 1.3e-3
+
+
+SMALL = [(2, 4), (3, 21), (5, 193), (17, 4), (40, 1000), (64, 65)]
+
+
+@pytest.mark.parametrize("m,n", SMALL)
+def test_emulated_error_of_low_rank(m, n):
+    for kind, G in ortho_ref.low_rank(m, n).items():
+        assert emulated_error(G) <= 4.5e-3, kind

@@ -317,3 +317,27 @@ def test_a_training_step_of_one_layer():
     gt, xt = ref8.values(*ref8.quantize(h(gy).T.copy())), ref8.values(*ref8.quantize(h(x).T.copy()))
     p, mag = ref8.product(gt, xt)
     assert (np.abs(h(w.grad) - p) <= ref8.gemm_bound(p, mag, M)).all()
+
+
+# ---- matrices whose roundings do not average out ---------------------------------
+
+def check_emulated(G):
+    """Within what the roundings make of it: the result's own (half a step is 2^-8
+    of a value, all of them off the same way where elements are equal), and float
+    sums where the emulation's are in double.  Those, some 2^-22 off, turn a half
+    precision rounding (2^-11 of a value, one element in 2^11 near enough to a
+    border) at most: 2^-11 2^-5.5 of the norm, and times 6 for what each of five
+    steps makes of it, below 5e-4."""
+    import ortho_ref
+    got = tl.orthogonalize(G.cuda())
+    check(got, want(G), CHOSEN)
+    emulated = ortho_ref.emulate(G)
+    off = float((got.cpu().double() - emulated).norm() / emulated.norm())
+    assert off <= 2.0 ** -8 + 5e-4, off
+
+
+@pytest.mark.parametrize("m,n", [(2, 4), (3, 21), (5, 193), (17, 4), (40, 1000), (64, 65), (60, 9000)])
+def test_low_rank(m, n):
+    import ortho_ref
+    for G in ortho_ref.low_rank(m, n).values():
+        check_emulated(G)

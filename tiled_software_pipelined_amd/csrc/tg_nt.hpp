@@ -138,7 +138,8 @@ struct NtGemm {
     // 4 S_PER count (see copy_one)
     static constexpr int S_BYTES = Tr::SCALED ? 256 * WAVES : 0;
     static constexpr int SLOT = A_BYTES + B_BYTES + S_BYTES;
-    static constexpr int LDS_BYTES = STAGES * SLOT;
+    static constexpr int SLOTS = STAGES;
+    static constexpr int LDS_BYTES = SLOTS * SLOT;
     static constexpr int A_PER = BM * 8 / NT, B_PER = BN * 8 / NT;
     static constexpr int S_PER = (BM + BN) / 4 / WAVES;  // scale dwords each wave copies
     static constexpr int N_CP = A_PER + B_PER + (Tr::SCALED ? 1 : 0);

@@ -10,7 +10,8 @@
 // a rounding of X is amplified with them, by hundreds over five steps, where
 // a rounding inside B X is not (it lies along large singular values).  So X
 // is held as two half precision numbers, hi + lo (22 bits), and a X is taken
-// from both; products use hi alone.  The diagonals of A and B are far larger
+// from both; products use hi alone (with up to 64 rows lo too, see below).  The
+// diagonals of A and B are far larger
 // than their other elements and would leave only rounding noise of their own
 // size: they are held apart in float (d), so with A = D + A' (A' zero on the
 // diagonal) the elements are
@@ -18,6 +19,15 @@
 //   B'_ij = b A'_ij + c ((d_i + d_j) A'_ij + (A'^2)_ij)     (i != j)
 //   e_i   = b d_i + c (d_i^2 + (A'^2)_ii)
 //   X_i  <- (a + e_i) X_i + (B' X)_i.
+//
+// e_i X_i takes lo, and B' X only hi: what is left out is B' lo.  Of matrices of
+// low rank B lo is next to nothing, but e_i lo_i alone is noise of full rank, of
+// which the part outside X's few singular vectors grows by |a| a step.  e_i is
+// about the sum of B's eigenvalues over m, so this shows where rows are few (rank
+// one: 4e-2 of the result's norm at 3 x 21, 6e-3 at 64 x 65).  Up to 64 rows,
+// where a product is bound by its launch and copies, lo is taken into X X^T and B
+// X: rank one then comes to 1e-3 (a call of 64 x 256 49 -> 52 us, of 64 x 4096 73
+// -> 81, of 300 of 40 x 70 93 -> 106).
 //
 // Matrices are stored times 2^12: half precision then holds magnitudes from
 // 2^-36 to 15 to full precision, and the host refuses coefficients that could
@@ -37,6 +47,7 @@
 
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "tg_host.hpp"
 #include "tg_nt.hpp"
@@ -202,6 +213,62 @@ __global__ __launch_bounds__(G::NT) void ortho_gram_kernel(OrthoArgs g) {
     store_gram<G>(g, t, acc);
 }
 
+// X X^T of a matrix of one tile (up to 64 rows), with hi and lo: hi hi^T + (hi
+// lo^T + lo hi^T), what is left out is 2^-22 of it.  The copies bring hi as rows
+// of A and lo as rows of B, no more bytes than hi twice; both are read for the
+// wave's rows and for its columns.  The sums are kept apart until the end, which
+// leaves X X^T symmetric bit for bit.  Fragments are read a slice ahead,
+// as in the tiled product.
+template <class G>
+__device__ __forceinline__ void gram_of_one_tile(const NtOperands& o, TG_LDS char* smem, typename G::Acc& acc, int wm0,
+                                                 int wn0, int lane, int wave) {
+    typename G::Offsets off;
+    G::offsets(off, o, 0, 0, wave, lane);
+    const int slices = o.k / G::ROW;
+    auto slot = [&](int t) { return smem + (t % G::SLOTS) * G::SLOT; };
+    auto copy = [&](int t) { G::copy_slice(slot(t), off, G::source(o, 0, 0, t, wave), wave); };
+    typename G::Acc high, low;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] = high[r] = low[r] = 0.0f;
+    typename G::Frag f[G::KSUB][4];
+    auto read = [&](int s, int t) {
+        const TG_LDS char* hi = slot(t);
+        const TG_LDS char* lo = hi + G::A_BYTES;
+        f[s][0].v[0] = G::read_chunk(hi, wm0, s, 0, lane);
+        f[s][1].v[0] = G::read_chunk(hi, wn0, s, 0, lane);
+        f[s][2].v[0] = G::read_chunk(lo, wm0, s, 0, lane);
+        f[s][3].v[0] = G::read_chunk(lo, wn0, s, 0, lane);
+    };
+#pragma unroll
+    for (int t = 0; t < G::SLOTS - 1; ++t)
+        if (t < slices) copy(t);
+    G::wait_slice(min(G::SLOTS - 2, slices - 1));
+    if (G::SLOTS - 1 < slices) copy(G::SLOTS - 1);
+#pragma unroll
+    for (int s = 0; s < G::KSUB; ++s) read(s, 0);
+    auto slice = [&](int t, auto next) {
+#pragma unroll
+        for (int s = 0; s < G::KSUB; ++s) {
+            acc = NtF16::mma<0, 0>(f[s][0], f[s][1], acc, 0, 0);
+            high = NtF16::mma<0, 0>(f[s][0], f[s][3], high, 0, 0);
+            low = NtF16::mma<0, 0>(f[s][2], f[s][1], low, 0, 0);
+            if constexpr (decltype(next)::value) {
+                if (s == 0) {
+                    // slice t + 1 has landed, and every wave has read slice t
+                    G::wait_slice(min(G::SLOTS - 2, slices - 2 - t));
+                    if (t + G::SLOTS < slices) copy(t + G::SLOTS);
+                }
+                read(s, t + 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    for (int t = 0; t + 1 < slices; ++t) slice(t, std::true_type{});
+    slice(slices - 1, std::false_type{});
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] += high[r] + low[r];
+}
+
 // B' and e of a matrix of one tile from the sums of X X^T: A' goes to LDS as the
 // one slice that A' A' walks, d beside it.
 template <class G>
@@ -268,12 +335,15 @@ __global__ __launch_bounds__(G::NT) void ortho_gram_split_kernel(OrthoArgs g) {
     __shared__ int last;
     const int tile = blockIdx.x / g.parts, part = blockIdx.x - tile * g.parts;
     const OrthoTile<G> t(g, true, tile);
-    const _Float16* X = g.hi + (int64_t)t.z * g.mp * g.np;
-    const int from = part * g.run;  // below np for every part
-    X += from;
+    const int from = part * g.run, k = min(g.run, g.np - from);  // from: below np for every part
+    const int64_t x = (int64_t)t.z * g.mp * g.np + from;
     typename G::Acc acc[1][1];
-    G::product(ortho_operands(X, g.mp, g.np, X, g.mp, g.np, min(g.run, g.np - from)), t.m0, t.n0,
-               (TG_LDS char*)smem_raw, acc, t.wm0, t.wn0, t.lane, t.wave);
+    if constexpr (POLY)
+        gram_of_one_tile<G>(ortho_operands(g.hi + x, g.mp, g.np, g.lo + x, g.mp, g.np, k), (TG_LDS char*)smem_raw, acc[0][0],
+                            t.wm0, t.wn0, t.lane, t.wave);
+    else
+        G::product(ortho_operands(g.hi + x, g.mp, g.np, g.hi + x, g.mp, g.np, k), t.m0, t.n0, (TG_LDS char*)smem_raw, acc,
+                   t.wm0, t.wn0, t.lane, t.wave);
 
     if (g.parts > 1) {
         constexpr int TILE = G::BM * G::BN;
@@ -372,8 +442,36 @@ __global__ __launch_bounds__(G::NT) void ortho_poly_kernel(OrthoArgs g) {
         });
 }
 
-// X <- (a + e) X + B' X; LAST writes the result instead.
-template <class G, bool LAST>
+// B' lo for X of one tile of rows, added to a tile's B' hi: the tile's own block
+// of lo is all of B' lo's second operand there, so it goes from the registers of
+// the epilogue to the ring's second slot (the product took one slice), transposed.
+// B' is still in the first.
+template <class G, class Q>
+__device__ __forceinline__ void add_low(typename G::Acc& acc, TG_LDS char* smem, const Q (&x)[4], const OrthoTile<G>& t) {
+    static_assert(G::BM == 64 && G::BN == 64 && G::FM == 1 && G::FN == 1 && G::SLOTS > 1, "one slice of 64 rows");
+    TG_LDS char* lo = smem + G::SLOT;
+    const int n = t.wn0 + (t.lane & 31);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int m = t.wm0 + quad_row<1>(q, t.lane);
+        Halves<4> four;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) four.v[p] = x[q].l[0][p].v[0];
+        __builtin_memcpy(lo + n * G::ROW + G::chunk_of(n, m / 8) * 16 + m % 8 * 2, &four, sizeof four);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < G::KSUB; ++s) {
+        typename G::Frag a, b;
+        a.v[0] = G::read_chunk(smem, t.wm0, s, 0, t.lane);
+        b.v[0] = G::read_chunk(lo, t.wn0, s, 0, t.lane);
+        acc = NtF16::mma<0, 0>(a, b, acc, 0, 0);
+    }
+}
+
+// X <- (a + e) X + B' X; LAST writes the result instead.  LOW: X has up to 64
+// rows, and B' lo is taken too.
+template <class G, bool LAST, bool LOW>
 __global__ __launch_bounds__(G::NT) void ortho_update_kernel(OrthoArgs g) {
     __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
     const OrthoTile<G> t(g, false);
@@ -405,6 +503,7 @@ __global__ __launch_bounds__(G::NT) void ortho_update_kernel(OrthoArgs g) {
     typename G::Acc acc[G::FM][G::FN];
     G::product(ortho_operands(g.b + s, g.mp, g.ms, g.xt + x, g.np, g.mp, g.mp), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0,
                t.wn0, t.lane, t.wave);
+    if constexpr (LOW) add_low<G>(acc[0][0], (TG_LDS char*)smem_raw, ahead, t);
     if constexpr (!G::EARLY) load(ahead[0], 0);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -638,8 +737,8 @@ static OrthoKernels symmetric_kernels(bool shared, double start, double fixed, d
 }
 template <class G>
 static OrthoKernels update_kernels(bool shared, double start, double fixed, double per_k) {
-    return OrthoKernels{G::BM, G::NT, ortho_update_kernel<G, false>, ortho_update_kernel<G, true>, shared, start, fixed,
-                        per_k};
+    return OrthoKernels{G::BM, G::NT, ortho_update_kernel<G, false, false>, ortho_update_kernel<G, true, false>, shared,
+                        start, fixed, per_k};
 }
 
 // 64: four slots, so that two workgroups fit a compute unit (eight slots and
@@ -707,12 +806,14 @@ static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     auto tiles = [](int64_t v, int64_t tile) { return (v + tile - 1) / tile; };
     int count;
     const OrthoKernels* t = update_table(&count);
-    p.upd = cheapest(t, count, p.m, [&](int64_t tile) { return batch * tiles(p.m, tile) * tiles(p.n, tile); });
+    // up to 64 rows the kernels for one tile of rows (64 x 64, the cheapest there by
+    // the model too)
+    p.upd = p.m <= 64 ? t + count - 1 : cheapest(t, count, p.m, [&](int64_t tile) { return batch * tiles(p.m, tile) * tiles(p.n, tile); });
     p.mp = up_to(p.m, p.upd->tile);
     p.np = up_to(p.n, p.upd->tile);
     auto tri = [&](int64_t tile) { return tiles(p.mp, tile) * (tiles(p.mp, tile) + 1) / 2; };
     t = symmetric_table(&count);
-    p.sym = cheapest(t, count, (p.np + p.mp) / 2, [&](int64_t tile) { return batch * tri(tile); });  // gram: np, poly: mp
+    p.sym = p.m <= 64 ? t + count - 1 : cheapest(t, count, (p.np + p.mp) / 2, [&](int64_t tile) { return batch * tri(tile); });  // gram: np, poly: mp
     p.tri = tri(p.sym->tile);
     p.ms = up_to(p.mp, p.sym->tile);
     // Split the gram product of few 64 x 64 tiles, at least 4 slices a part and
@@ -944,19 +1045,23 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
         err = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)(batch * tiles * parts)), dim3(k.threads),
                               args, 0, s);
     };
+    // up to 64 rows: one symmetric tile, tiles of 64 rows, and products that take lo
+    const bool small = p.mp == 64;
+    const OrthoFn update = small ? ortho_update_kernel<Ortho64, false, true> : p.upd->first;
+    const OrthoFn last = small ? ortho_update_kernel<Ortho64, true, true> : p.upd->second;
     for (int k = 0; k < steps; ++k) {
         g.ca = (float)coefficients[3 * k];
         g.cb = (float)coefficients[3 * k + 1];
         g.cc = (float)coefficients[3 * k + 2];
         g.xt = (const _Float16*)(ws + (k % 2 ? p.off_t1 : p.off_t0));
         g.xt_out = (_Float16*)(ws + (k % 2 ? p.off_t0 : p.off_t1));
-        if (p.sym->tile == 64 && tri == 1) {
+        if (small) {
             launch(ortho_gram_split_kernel<Ortho64, true>, *p.sym, tri, p.parts);
         } else {
             launch(p.parts > 1 ? ortho_gram_split_kernel<Ortho64, false> : p.sym->first, *p.sym, tri, p.parts);
             launch(p.sym->second, *p.sym, tri, 1);
         }
-        launch(k + 1 < steps ? p.upd->first : p.upd->second, *p.upd, upd, 1);
+        launch(k + 1 < steps ? update : last, *p.upd, upd, 1);
     }
     if (err != hipSuccess) {
         set_error("launch failed: %s", hipGetErrorString(err));
