@@ -46,7 +46,8 @@ def emulate(G, steps=5, coefficients=USUAL, eps=1e-7):
         e = b * d + c * (d * d + square.diagonal())
         B = b * A + c * ((d[:, None] + d) * A + square)
         B = half((B - B.diagonal().diag()) * ONE) / ONE
-        X = ((a + e)[:, None] * (hi + lo) + B @ (hi + lo if small else hi)).float().double()
+        low = a + e * (small | (square.diagonal() <= 1.5 * d * d))
+        X = ((a + e)[:, None] * hi + low[:, None] * lo + B @ (hi + lo if small else hi)).float().double()
     X = X / ONE
     return X.t() if tall else X
 

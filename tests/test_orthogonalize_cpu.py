@@ -145,10 +145,8 @@ def test_emulated_error_of_random_matrices(m, n):
         assert emulated_error(G.bfloat16()) <= 1.3e-3
 
 
-SMALL = [(2, 4), (3, 21), (5, 193), (17, 4), (40, 1000), (64, 65)]
-
-
-@pytest.mark.parametrize("m,n", SMALL)
+@pytest.mark.parametrize("m,n", [(2, 4), (3, 21), (5, 193), (17, 4), (40, 1000), (64, 65), (65, 70), (100, 128), (70, 1000),
+                                 (200, 90), (129, 300)])
 def test_emulated_error_of_low_rank(m, n):
     for kind, G in ortho_ref.low_rank(m, n).items():
         assert emulated_error(G) <= 4.5e-3, kind

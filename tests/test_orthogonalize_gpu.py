@@ -336,7 +336,8 @@ def check_emulated(G):
     assert off <= 2.0 ** -8 + 5e-4, off
 
 
-@pytest.mark.parametrize("m,n", [(2, 4), (3, 21), (5, 193), (17, 4), (40, 1000), (64, 65), (60, 9000)])
+@pytest.mark.parametrize("m,n", [(2, 4), (3, 21), (5, 193), (17, 4), (40, 1000), (64, 65), (60, 9000), (65, 70),
+                                 (100, 128), (70, 1000), (200, 90), (129, 300), (300, 280)])
 def test_low_rank(m, n):
     import ortho_ref
     for G in ortho_ref.low_rank(m, n).values():

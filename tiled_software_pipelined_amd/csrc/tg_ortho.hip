@@ -27,7 +27,11 @@
 // one: 4e-2 of the result's norm at 3 x 21, 6e-3 at 64 x 65).  Up to 64 rows,
 // where a product is bound by its launch and copies, lo is taken into X X^T and B
 // X: rank one then comes to 1e-3 (a call of 64 x 256 49 -> 52 us, of 64 x 4096 73
-// -> 81, of 300 of 40 x 70 93 -> 106).
+// -> 81, of 300 of 40 x 70 93 -> 106).  More rows: a row i whose A' is large beside
+// d_i, |A'_i|^2 > 1.5 d_i^2, has few singular vectors under it, and takes e_i from
+// hi as well (the two errors cancel); others take it from hi + lo (what is left
+// out, B' lo, is the smaller one: a square of random elements has a ratio of 1,
+// and comes to 7e-4 against 1.3e-3).  Rank one, 65 x 70: 6e-3 -> 7e-4.
 //
 // Matrices are stored times 2^12: half precision then holds magnitudes from
 // 2^-36 to 15 to full precision, and the host refuses coefficients that could
@@ -83,6 +87,12 @@ struct OrthoArgs {
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+
+// e_i's last bit says which of the two its row takes (see above).
+__device__ __forceinline__ float with_choice(float e, bool high_only) {
+    return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, e) & ~1u) | (uint32_t)high_only);
+}
+__device__ __forceinline__ bool high_only(float e) { return __builtin_bit_cast(uint32_t, e) & 1u; }
 
 template <int N>
 struct Halves {
@@ -436,7 +446,7 @@ __global__ __launch_bounds__(G::NT) void ortho_poly_kernel(OrthoArgs g) {
             for (int j = 0; j < G::FN; ++j) {
                 const float sq = acc[i][j][r] * (1.0f / (ONE * ONE)), av = (float)x.a[i][r & 3].v[j] * (1.0f / ONE);
                 const bool diagonal = m == n + j;
-                if (diagonal) e[m] = g.cb * di + g.cc * (di * di + sq);
+                if (diagonal) e[m] = with_choice(g.cb * di + g.cc * (di * di + sq), sq > 1.5f * di * di);
                 out.v[j] = (_Float16)(diagonal ? 0.0f : (g.cb * av + g.cc * ((di + dn[j]) * av + sq)) * ONE);
             }
         });
@@ -518,11 +528,11 @@ __global__ __launch_bounds__(G::NT) void ortho_update_kernel(OrthoArgs g) {
                 const int m = mb + G::row_of(i, 4 * q + p, t.lane);
                 const int64_t at = x + (int64_t)m * g.np + n;
                 Halves<G::FN>&h = x4.h[i][p], &l = x4.l[i][p];
-                const float k = g.ca + x4.e.v[G::FM * p + i];
+                const float ei = x4.e.v[G::FM * p + i], k = g.ca + ei, kl = !LOW && high_only(ei) ? g.ca : k;
                 uint16_t o[G::FN];
 #pragma unroll
                 for (int j = 0; j < G::FN; ++j) {
-                    const float y = k * ((float)h.v[j] + (float)l.v[j]) + acc[i][j][4 * q + p] * (1.0f / ONE);
+                    const float y = fmaf(k, (float)h.v[j], fmaf(kl, (float)l.v[j], acc[i][j][4 * q + p] * (1.0f / ONE)));
                     if constexpr (LAST) {
                         o[j] = __builtin_bit_cast(uint16_t, (__bf16)(y * (1.0f / ONE)));
                         col[j].v[G::FM * p + i] = __builtin_bit_cast(_Float16, o[j]);
