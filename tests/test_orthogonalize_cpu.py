@@ -150,3 +150,8 @@ def test_emulated_error_of_random_matrices(m, n):
 def test_emulated_error_of_low_rank(m, n):
     for kind, G in ortho_ref.low_rank(m, n).items():
         assert emulated_error(G) <= 4.5e-3, kind
+
+
+@pytest.mark.parametrize("kind", sorted(ortho_ref.repeated()))
+def test_emulated_error_of_repeated_elements(kind):
+    assert emulated_error(ortho_ref.repeated()[kind]) <= 4.5e-3

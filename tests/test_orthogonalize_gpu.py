@@ -325,15 +325,15 @@ def check_emulated(G):
     """Within what the roundings make of it: the result's own (half a step is 2^-8
     of a value, all of them off the same way where elements are equal), and float
     sums where the emulation's are in double.  Those, some 2^-22 off, turn a half
-    precision rounding (2^-11 of a value, one element in 2^11 near enough to a
-    border) at most: 2^-11 2^-5.5 of the norm, and times 6 for what each of five
-    steps makes of it, below 5e-4."""
+    precision rounding (2^-10 of a value, one element in 2^11 near enough to its
+    threshold) at most: 2^-10 2^-5.5 of the norm, and times 6 for what each of five
+    steps makes of it, below 7e-4."""
     import ortho_ref
     got = tl.orthogonalize(G.cuda())
     check(got, want(G), CHOSEN)
     emulated = ortho_ref.emulate(G)
     off = float((got.cpu().double() - emulated).norm() / emulated.norm())
-    assert off <= 2.0 ** -8 + 5e-4, off
+    assert off <= 2.0 ** -8 + 7e-4, off
 
 
 @pytest.mark.parametrize("m,n", [(2, 4), (3, 21), (5, 193), (17, 4), (40, 1000), (64, 65), (60, 9000), (65, 70),
@@ -342,3 +342,11 @@ def test_low_rank(m, n):
     import ortho_ref
     for G in ortho_ref.low_rank(m, n).values():
         check_emulated(G)
+
+
+def test_repeated_elements():
+    import ortho_ref
+    for kind, G in ortho_ref.repeated().items():
+        print(kind, flush=True)
+        check_emulated(G)
+        check_emulated(G.t())

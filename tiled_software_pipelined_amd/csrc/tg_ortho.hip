@@ -9,12 +9,11 @@
 // Where the precision is spent.  Small singular values grow by |a| a step, so
 // a rounding of X is amplified with them, by hundreds over five steps, where
 // a rounding inside B X is not (it lies along large singular values).  So X
-// is held as two half precision numbers, hi + lo (22 bits), and a X is taken
-// from both; products use hi alone (with up to 64 rows lo too, see below).  The
-// diagonals of A and B are far larger
-// than their other elements and would leave only rounding noise of their own
-// size: they are held apart in float (d), so with A = D + A' (A' zero on the
-// diagonal) the elements are
+// is held as two half precision numbers, hi + lo, and a X is taken from both;
+// products use hi alone (with up to 64 rows lo too, see below).  The diagonals of
+// A and B are far larger than their other elements and would leave only rounding
+// noise of their own size: they are held apart in float (d), so with A = D + A'
+// (A' zero on the diagonal) the elements are
 //
 //   B'_ij = b A'_ij + c ((d_i + d_j) A'_ij + (A'^2)_ij)     (i != j)
 //   e_i   = b d_i + c (d_i^2 + (A'^2)_ii)
@@ -28,18 +27,21 @@
 // where a product is bound by its launch and copies, lo is taken into X X^T and B
 // X: rank one then comes to 1e-3 (a call of 64 x 256 49 -> 52 us, of 64 x 4096 73
 // -> 81, of 300 of 40 x 70 93 -> 106).  More rows: a row i whose A' is large beside
-// d_i, |A'_i|^2 > 1.5 d_i^2, has few singular vectors under it, and takes e_i from
-// hi as well (the two errors cancel); others take it from hi + lo (what is left
-// out, B' lo, is the smaller one: a square of random elements has a ratio of 1,
-// and comes to 7e-4 against 1.3e-3).  Rank one, 65 x 70: 6e-3 -> 7e-4.
+// d_i, |A'_i|^2 > d_i^2 (for a projection: less than half of the row's unit vector
+// lies in it), takes e_i from hi as well, so that what is left out is B lo;
+// others take it from hi + lo, where B' lo is the smaller (random elements, 300 x
+// 301: 6e-4 against 1.3e-3).  Rank one, 65 x 70: 6e-3 -> 7e-4.
+//
+// hi, A' and B' are rounded up or down by thresholds of an element's place, not
+// to nearest (see Dither below).
 //
 // Matrices are stored times 2^12: half precision then holds magnitudes from
-// 2^-36 to 15 to full precision, and the host refuses coefficients that could
-// leave that range.  Against 64 bits the result is off by 0.5 - 1e-3 of its
-// norm before its one rounding to bfloat16 (itself 1.7e-3); by up to 4e-3
-// where a few equal singular values hold all of the norm, from the rounding
-// of X in B X (taking lo into that product would cost half of the update's
-// time again).
+// 2^-26 to 15 to full precision, and smaller ones in steps of 2^-36; the host
+// refuses coefficients that could leave that range.  hi + lo is off by up to
+// 2^-21 of an element, or by 2^-37 where that is more.  Against 64 bits the result is off by
+// 0.5 - 1.3e-3 of its norm before its one rounding to bfloat16 (itself 1.7e-3)
+// for random matrices, and by at most 5e-3 in 3000 of low rank or with repeated
+// elements (emulated; the tests hold the kernels to the emulation).
 //
 // All products have both operands K-contiguous: X X^T; A' A' (symmetric); and
 // B' X with X's transpose, which the update writes beside X, as its second
@@ -97,6 +99,45 @@ __device__ __forceinline__ bool high_only(float e) { return __builtin_bit_cast(u
 template <int N>
 struct Halves {
     _Float16 v[N];
+};
+
+// Rounding to half precision, up or down by a threshold of the element's place,
+// so that equal elements are not all off the same way: rounded to nearest, equal
+// elements of X, A' and B' move a singular value together (4 blocks of 50 x 125
+// ones on the diagonal: result off by 1.5e-2 of its norm, now 1e-3; one
+// rounding's error at random places grows by a half).  The thresholds of matrix S
+// are the fractions of (m n C + m R + n D) / 2^32.  C / 2^32 is far from simple
+// fractions, so they are spread evenly along every row and column, like the phases
+// of a chirp, and rows do not resemble each other; for A and B, R = D keeps them
+// symmetric.  A NaN may change in A' or B'; X keeps it.
+//
+// Elements are visited one after the other, down a column or along a row: an
+// addition makes the next threshold (a call of 256 x 256: a product for each
+// 74.6 us, so 72.5, rounding to nearest 70.5).
+// The 13 bits that a float has beyond half precision are carried into by the
+// threshold's, and cut off by the conversion.
+enum Rounded { ROUND_X = 0, ROUND_A, ROUND_B };
+template <Rounded S>
+struct Dither {
+    static constexpr uint32_t C = S == ROUND_X ? 0xd1b54a33u : S == ROUND_A ? 0x9e3779b1u : 0xb5297a4du;
+    static constexpr uint32_t R = S == ROUND_X ? 0x8cb92ba7u : S == ROUND_A ? 0x68e31da4u : 0x1b56c4e9u;
+    static constexpr uint32_t D = S == ROUND_X ? 0xabc98389u : R;
+    uint32_t at, step;
+    // from element (m, n): the next is (m + 1, n) or (m, n + 1)
+    __device__ __forceinline__ static Dither down(int m, int n) {
+        const uint32_t step = (uint32_t)n * C + R;
+        return Dither{(uint32_t)m * step + (uint32_t)n * D, step};
+    }
+    __device__ __forceinline__ static Dither along(int m, int n) {
+        const uint32_t step = (uint32_t)m * C + D;
+        return Dither{(uint32_t)n * step + (uint32_t)m * R, step};
+    }
+    __device__ __forceinline__ _Float16 round(float x) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, x) + (at >> 19);
+        at += step;
+        const auto h = __builtin_amdgcn_cvt_pkrtz(__builtin_bit_cast(float, b), 0.0f);
+        return (_Float16)h[0];
+    }
 };
 
 // The 4 FM values of one column that lane `lane` holds in registers 4 q .. 4 q
@@ -167,8 +208,8 @@ __device__ __forceinline__ NtOperands ortho_operands(const _Float16* a, int rows
 
 // Write the wave's block of a symmetric matrix (leading dimension ld), and its
 // mirror image where the tile lies below the diagonal.  value(i, r, row, out):
-// the FN values of register r in fragments (i, ..); request(q) is called
-// before registers 4 q .. are stored.
+// the FN values of register r in fragments (i, ..), row by row; request(q) is
+// called before registers 4 q .. are stored.
 template <class G, class R, class F>
 __device__ __forceinline__ void store_symmetric(_Float16* S, int ld, const OrthoTile<G>& t, R request, F value) {
     const int mb = t.m0 + t.wm0, nb = t.n0 + t.wn0, n = nb + G::col_of(0, t.lane);
@@ -199,14 +240,19 @@ __device__ __forceinline__ void store_symmetric(_Float16* S, int ld, const Ortho
 template <class G>
 __device__ __forceinline__ void store_gram(const OrthoArgs& g, const OrthoTile<G>& t, const typename G::Acc (&acc)[G::FM][G::FN]) {
     float* d = g.d + (int64_t)t.z * g.ms;
-    const int n = t.n0 + t.wn0 + G::col_of(0, t.lane);
-    store_symmetric<G>(g.a + (int64_t)t.z * g.ms * g.ms, g.ms, t, [](int) {}, [&](int i, int r, int m, Halves<G::FN>& out) {
+    const int mb = t.m0 + t.wm0, n = t.n0 + t.wn0 + G::col_of(0, t.lane);
+    Dither<ROUND_A> dither[G::FN];
+    auto request = [&](int q) {
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j) dither[j] = Dither<ROUND_A>::down(mb + quad_row<G::FM>(q, t.lane), n + j);
+    };
+    store_symmetric<G>(g.a + (int64_t)t.z * g.ms * g.ms, g.ms, t, request, [&](int i, int r, int m, Halves<G::FN>& out) {
 #pragma unroll
         for (int j = 0; j < G::FN; ++j) {
             const float v = acc[i][j][r] * (1.0f / (ONE * ONE));
             const bool diagonal = m == n + j;
             if (diagonal) d[m] = v;
-            out.v[j] = (_Float16)(diagonal ? 0.0f : v * ONE);
+            out.v[j] = dither[j].round(diagonal ? 0.0f : v * ONE);
         }
     });
 }
@@ -224,7 +270,7 @@ __global__ __launch_bounds__(G::NT) void ortho_gram_kernel(OrthoArgs g) {
 }
 
 // X X^T of a matrix of one tile (up to 64 rows), with hi and lo: hi hi^T + (hi
-// lo^T + lo hi^T), what is left out is 2^-22 of it.  The copies bring hi as rows
+// lo^T + lo hi^T), what is left out is below 2^-20 of it.  The copies bring hi as rows
 // of A and lo as rows of B, no more bytes than hi twice; both are read for the
 // wave's rows and for its columns.  The sums are kept apart until the end, which
 // leaves X X^T symmetric bit for bit.  Fragments are read a slice ahead,
@@ -291,12 +337,13 @@ __device__ __forceinline__ void poly_of_one_tile(const OrthoArgs& g, const Ortho
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const int m = t.wm0 + quad_row<1>(q, t.lane);
+        auto dither = Dither<ROUND_A>::down(m, n);
         Halves<4> four;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float v = acc[4 * q + k] * (1.0f / (ONE * ONE));
             if (m + k == n) d[n] = v;
-            a[4 * q + k] = four.v[k] = (_Float16)(m + k == n ? 0.0f : v * ONE);
+            a[4 * q + k] = four.v[k] = dither.round(m + k == n ? 0.0f : v * ONE);
         }
         // A' is symmetric: rows m .. m + 3 of column n are columns of row n
         __builtin_memcpy(slot + n * G::ROW + G::chunk_of(n, m / 8) * 16 + m % 8 * 2, &four, sizeof four);
@@ -314,11 +361,16 @@ __device__ __forceinline__ void poly_of_one_tile(const OrthoArgs& g, const Ortho
     _Float16* B = g.b + (int64_t)t.z * g.ms * g.ms;
     const float dn = d[n];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int m = t.wm0 + G::row_of(0, r, t.lane);
-        const float di = d[m], sq = acc[r] * (1.0f / (ONE * ONE)), av = (float)a[r] * (1.0f / ONE);
-        if (m == n) g.e[(int64_t)t.z * g.ms + m] = g.cb * di + g.cc * (di * di + sq);
-        B[(int64_t)m * g.ms + n] = (_Float16)(m == n ? 0.0f : (g.cb * av + g.cc * ((di + dn) * av + sq)) * ONE);
+    for (int q = 0; q < 4; ++q) {
+        const int m0 = t.wm0 + quad_row<1>(q, t.lane);
+        auto dither = Dither<ROUND_B>::down(m0, n);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int m = m0 + k, r = 4 * q + k;
+            const float di = d[m], sq = acc[r] * (1.0f / (ONE * ONE)), av = (float)a[r] * (1.0f / ONE);
+            if (m == n) g.e[(int64_t)t.z * g.ms + m] = g.cb * di + g.cc * (di * di + sq);
+            B[(int64_t)m * g.ms + n] = dither.round(m == n ? 0.0f : (g.cb * av + g.cc * ((di + dn) * av + sq)) * ONE);
+        }
     }
 }
 
@@ -433,11 +485,14 @@ __global__ __launch_bounds__(G::NT) void ortho_poly_kernel(OrthoArgs g) {
     G::product(ortho_operands(A, g.mp, g.ms, A, g.mp, g.ms, g.mp), t.m0, t.n0, (TG_LDS char*)smem_raw, acc, t.wm0, t.wn0, t.lane,
                t.wave);
     if constexpr (!G::EARLY) load(ahead[0], 0);
+    Dither<ROUND_B> dither[G::FN];
     store_symmetric<G>(
         g.b + s, g.ms, t,
         [&](int q) {
             if (!G::EARLY && q < 3) load(ahead[(q + 1) % HELD], q + 1);
             __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j) dither[j] = Dither<ROUND_B>::down(mb + quad_row<G::FM>(q, t.lane), n + j);
         },
         [&](int i, int r, int m, Halves<G::FN>& out) {
             const Quad& x = ahead[(r >> 2) % HELD];
@@ -446,8 +501,8 @@ __global__ __launch_bounds__(G::NT) void ortho_poly_kernel(OrthoArgs g) {
             for (int j = 0; j < G::FN; ++j) {
                 const float sq = acc[i][j][r] * (1.0f / (ONE * ONE)), av = (float)x.a[i][r & 3].v[j] * (1.0f / ONE);
                 const bool diagonal = m == n + j;
-                if (diagonal) e[m] = with_choice(g.cb * di + g.cc * (di * di + sq), sq > 1.5f * di * di);
-                out.v[j] = (_Float16)(diagonal ? 0.0f : (g.cb * av + g.cc * ((di + dn[j]) * av + sq)) * ONE);
+                if (diagonal) e[m] = with_choice(g.cb * di + g.cc * (di * di + sq), sq > di * di);
+                out.v[j] = dither[j].round(diagonal ? 0.0f : (g.cb * av + g.cc * ((di + dn[j]) * av + sq)) * ONE);
             }
         });
 }
@@ -520,6 +575,9 @@ __global__ __launch_bounds__(G::NT) void ortho_update_kernel(OrthoArgs g) {
         if (!G::EARLY && q < 3) load(ahead[(q + 1) % HELD], q + 1);
         __builtin_amdgcn_sched_barrier(0);
         Quad& x4 = ahead[q % HELD];
+        Dither<ROUND_X> dither[G::FN];
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j) dither[j] = Dither<ROUND_X>::down(mb + quad_row<G::FM>(q, t.lane), n + j);
         Halves<4 * G::FM> col[G::FN];
 #pragma unroll
         for (int p = 0; p < 4; ++p)
@@ -537,7 +595,7 @@ __global__ __launch_bounds__(G::NT) void ortho_update_kernel(OrthoArgs g) {
                         o[j] = __builtin_bit_cast(uint16_t, (__bf16)(y * (1.0f / ONE)));
                         col[j].v[G::FM * p + i] = __builtin_bit_cast(_Float16, o[j]);
                     } else {
-                        h.v[j] = (_Float16)y;
+                        h.v[j] = dither[j].round(y);
                         l.v[j] = (_Float16)(y - (float)h.v[j]);
                         col[j].v[G::FM * p + i] = h.v[j];
                     }
@@ -700,12 +758,13 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(OrthoInArgs g) {
     for (int h = 0; h < 2; ++h) {
         const int r = 32 * h + (tid >> 3), c = 8 * (tid & 7);
         Halves<8> hi, lo, xt;
+        auto row = Dither<ROUND_X>::along(m0 + r, n0 + c), column = Dither<ROUND_X>::down(m0 + c, n0 + r);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const float y = g.tall ? tile[c + k][r] : tile[r][c + k];
-            hi.v[k] = (_Float16)y;
+            hi.v[k] = row.round(y);
             lo.v[k] = (_Float16)(y - (float)hi.v[k]);
-            xt.v[k] = (_Float16)(g.tall ? tile[r][c + k] : tile[c + k][r]);
+            xt.v[k] = column.round(g.tall ? tile[r][c + k] : tile[c + k][r]);
         }
         __builtin_memcpy(g.hi + x + (int64_t)(m0 + r) * g.np + n0 + c, &hi, 16);
         __builtin_memcpy(g.lo + x + (int64_t)(m0 + r) * g.np + n0 + c, &lo, 16);
