@@ -212,3 +212,22 @@ def test_linear_refuses_forward_mode(monkeypatch, dual, grad):
         with pytest.raises(NotImplementedError):
             tl.linear_fp8(xd, wd)
     assert tl.linear_fp8(x, w).shape == (4, 6)
+
+
+def test_kernel_choice_few_rows_and_many_columns():
+    # bound by one read of B: the kernel measured fastest (microseconds of the
+    # fastest and of the next)
+    k = tl.gemm_fp8_kernel
+    for M, N, K, name in ((1, 11008, 4096, "rows16"),    # 11.9, 13.2
+                          (1, 28672, 8192, "rows16"),    # 43, 46
+                          (1, 50257, 4096, "rows16"),    # 42, 48
+                          (1, 50257, 8192, "rows16"),    # 73, 84
+                          (1, 128256, 1024, "t64x64"),   # 27, 30
+                          (16, 28672, 4096, "t64x64"),   # 28, 30
+                          (16, 128256, 4096, "t64x64"),  # 102, 120
+                          (33, 128256, 4096, "t64x64"),  # 106, 123
+                          (64, 4096, 1024, "t64x64"),    # 5.3, 6.4
+                          (32, 8192, 1024, "t64x64"),    # 5.6, 6.7
+                          (100, 28672, 4096, "t128x128x128_w2x4")):  # 31, 39
+        assert k(M, N, K).startswith(name), (M, N, K)
+        assert k(N, M, K).startswith(name), (N, M, K)

@@ -40,20 +40,34 @@ static bool offsets_fit(const Fp8Kernel& k, int64_t lda, int64_t ldb) {
 //   2048x2048x2048   24.9    14.2   16.5   18.2
 //   2048x4096x4096   42.3    41.9   34.5   57.6
 //   4096x4096x4096   52.5    81.8   67.4  107
+// Few rows and many columns are bound by one read of B, which each kernel takes
+// at a rate of its own (tiles: `read`, megabytes of A and B over TB/s), and the
+// kernels for few rows by the rows that they do hold as well (184 shapes of 1 ..
+// 128 rows, 1024 .. 128256 columns and K = 1024 .. 8192, B cold: the choice is
+// within 4 % of the best kernel at each, 0.07 % in the mean).
+//   1x11008x4096             18.9   34.4   13.2   11.9
+//   1x50257x4096             51.6   50.8   47.7   41.8
+//   1x128256x4096           119    124     95.8   94.3
+//   16x128256x4096          120    125    102    126    188
+//   64x128256x4096  137     129    129    118    490    450
+//   100x28672x4096   48.6    31.5   40.6   38.9         179
 static double time_of(Fp8Pick p, const Fp8Kernel& k, int64_t M, int64_t N, int64_t K) {
-    const double n = (double)((M + k.bm - 1) / k.bm) * (double)((N + k.bn - 1) / k.bn), k1 = (double)K / 1024.0;
-    const double more = n > 256.0 ? n / 256.0 : 1.0;
+    const double tiles_m = (double)((M + k.bm - 1) / k.bm), n = tiles_m * (double)((N + k.bn - 1) / k.bn);
+    const double k1 = (double)K / 1024.0, more = n > 256.0 ? n / 256.0 : 1.0;
+    const double read = ((double)M + (double)N) * (double)K * 1e-6;
+    const double held = (double)M / (tiles_m * k.bm);  // share of a tile's rows that are A's
     switch (p) {
         case PICK_256: {
             // a partial round leaves clock and bandwidth to the busy units
             const double whole = floor(n / 256.0), rest = n / 256.0 - whole;
-            return (whole + (rest > 0.0 ? 0.72 + 0.28 * rest : 0.0)) * (9.5 + 11.0 * k1);
+            return fmax((whole + (rest > 0.0 ? 0.72 + 0.28 * rest : 0.0)) * (9.5 + 11.0 * k1), 2.0 + read / 3.8);
         }
-        case PICK_128: return 2.5 + ceil(n / 256.0) * (3.5 + 4.1 * k1);
-        case PICK_128_PAIR: return 2.0 + (n > 410.0 ? more : 1.6) * (2.3 + 3.67 * k1);
-        case PICK_64: return 2.9 + more * (0.95 + 2.05 * k1);
-        case PICK_ROWS16: return 2.6 + 1.0 * k1 + (more - 1.0) * fmax(1.0 * k1, 1.6);
-        default: return 2.4 + 1.5 * k1 + (more - 1.0) * fmax(1.5 * k1, 1.9);
+        case PICK_128: return fmax(2.5 + ceil(n / 256.0) * (3.5 + 4.1 * k1), 2.5 + read / 4.4);
+        case PICK_128_PAIR:
+            return fmax(2.0 + (n > 410.0 ? more : n > 256.0 ? 1.6 : 2.0) * (2.3 + 3.67 * k1), 2.5 + read / 4.2);
+        case PICK_64: return fmax(2.9 + more * (0.95 + 2.05 * k1), 3.0 + read / 5.2);
+        case PICK_ROWS16: return 2.6 + 1.0 * k1 + (more - 1.0) * fmax((0.7 + 0.3 * held) * k1, 1.2 + 0.4 * held);
+        default: return 2.4 + 1.5 * k1 + (more - 1.0) * fmax((1.2 + 0.6 * held) * k1, 2.2);
     }
 }
 
