@@ -461,11 +461,11 @@ const char* tgemm_fp8_gemm_kernel(int64_t M, int64_t N, int64_t K, int64_t lda, 
  * precision matrices hold no more.
  *
  * workspace: tgemm_orthogonalize_workspace_bytes(batch, rows, cols) bytes
- * (-1 for sizes out of range: rows and cols up to 2^20, batch up to 2^16) of
- * device memory, 256-byte aligned; its contents are overwritten, so calls
- * that share one must be ordered on one stream.  O may be G's own memory
- * (then with the same element size and strides); otherwise it must not
- * overlap G, and neither may overlap the workspace.  Elements of O between
+ * (-1 for sizes out of range: rows and cols up to 2^20, batch up to 2^16, and
+ * launches that no grid holds) of device memory, 256-byte aligned; its contents
+ * are overwritten, so calls that share one must be ordered on one stream.  O may
+ * be G's own memory (then with the same element size and strides); otherwise it
+ * must not overlap G, and neither may overlap the workspace.  Elements of O between
  * its rows are not written.  batch, rows or cols = 0 does nothing.  steps: 1
  * to 64.  Returns TGEMM_OK or a TGEMM_E_* code. */
 int64_t tgemm_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);

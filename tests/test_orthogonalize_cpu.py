@@ -155,3 +155,12 @@ def test_emulated_error_of_low_rank(m, n):
 @pytest.mark.parametrize("kind", sorted(ortho_ref.repeated()))
 def test_emulated_error_of_repeated_elements(kind):
     assert emulated_error(ortho_ref.repeated()[kind]) <= 4.5e-3
+
+
+def test_launches_that_no_grid_holds_are_refused():
+    w = tl._lib.tgemm_orthogonalize_workspace_bytes
+    # 2^16 matrices of 256 pieces for the norm: 2^32 threads
+    for batch, rows, cols in ((1 << 16, 256, 1025), (1 << 16, 1 << 16, 1), (1 << 16, 1 << 20, 1 << 20)):
+        assert w(batch, rows, cols) == -1
+        assert call(batch=batch, rows=rows, cols=cols, ws_bytes=1 << 62) == -1 and tl.last_error()
+    assert w((1 << 16) - 1, 256, 1025) > 0 and w(1 << 16, 255, 1025) > 0

@@ -350,3 +350,17 @@ def test_repeated_elements():
         print(kind, flush=True)
         check_emulated(G)
         check_emulated(G.t())
+
+
+def test_not_a_number_of_any_pattern():
+    # all mantissa bits set: adding a threshold to the pattern leaves the NaNs
+    for dtype, pattern, ints in ((torch.float32, 0x7FFFFFFF, torch.int32), (torch.float32, -1, torch.int32),
+                                 (torch.bfloat16, 0x7FFF, torch.int16), (torch.float16, -1, torch.int16)):
+        for m, n in ((50, 70), (70, 90), (300, 280)):
+            G = randn(2, m, n, seed=m, dtype=dtype)
+            clean = tl.orthogonalize(G)
+            G.view(ints)[1, m // 2, n // 3] = pattern
+            for steps in (1, 5):
+                got = tl.orthogonalize(G, steps=steps)
+                assert bool(got[1].isnan().all()), (dtype, pattern, m, steps)
+            assert torch.equal(got[0], clean[0])

@@ -843,6 +843,10 @@ struct OrthoPlan {
     // the columns of X that each takes, the last perhaps fewer
     int parts;
     int64_t run;
+    int64_t upd_tiles, load_tiles;  // workgroups of one matrix: update, load
+    // the norm's: 2^lane_bits threads take one row together; workgroups a matrix
+    int lane_bits, norm_parts;
+    bool fits;  // every launch fits a grid
     int64_t off_hi, off_lo, off_t0, off_t1, off_a, off_b, off_d, off_e, off_part, off_sums, off_arrived, bytes;
 };
 
@@ -925,12 +929,24 @@ static OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols) {
     p.off_sums = take(p.parts > 1 ? 4 * batch * p.tri * p.parts * 4096 : 0);
     p.off_arrived = take(p.parts > 1 ? 4 * batch * p.tri : 0);
     p.bytes = at;
+    p.upd_tiles = (p.mp / p.upd->tile) * (p.np / p.upd->tile);
+    p.load_tiles = (p.mp / 64) * (p.np / 64);
+    while (p.lane_bits < 8 && (INT64_C(8) << p.lane_bits) < cols) ++p.lane_bits;
+    // a workgroup for each piece, up to PARTS (PARTS for every matrix: 300 of
+    // 40 x 70 61 us, now 5.5)
+    const int64_t pieces = tiles(rows, 256 >> p.lane_bits) * tiles(cols, 2048);
+    p.norm_parts = (int)(pieces < PARTS ? pieces : PARTS);
+    p.fits = grid_fits((double)(batch * p.tri), p.sym->threads) && grid_fits((double)(batch * p.upd_tiles), p.upd->threads) &&
+             grid_fits((double)(batch * p.load_tiles), 256) && grid_fits((double)(batch * p.norm_parts), 256);
     return p;
 }
 
+// Products of padded sizes stay far inside 64 bits, and a tile's copies reach
+// its rows by 32-bit offsets.
+constexpr int64_t MOST_SIDE = 1 << 20, MOST_BATCH = 1 << 16;
+static_assert(255 * 2 * (MOST_SIDE + 256) + 128 <= INT64_C(0xffffffff), "offsets of a tile's copies");
 static bool ortho_sizes_ok(int64_t batch, int64_t rows, int64_t cols) {
-    // products of padded sizes stay far inside 64 bits, grids inside 32
-    return batch >= 0 && rows >= 0 && cols >= 0 && rows <= (1 << 20) && cols <= (1 << 20) && batch <= (1 << 16);
+    return batch >= 0 && rows >= 0 && cols >= 0 && rows <= MOST_SIDE && cols <= MOST_SIDE && batch <= MOST_BATCH;
 }
 
 // The largest singular value the steps before the last can reach from [0, 1],
@@ -974,7 +990,8 @@ int64_t tgemm_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t
     using namespace tg;
     if (!ortho_sizes_ok(batch, rows, cols)) return -1;
     if (batch == 0 || rows == 0 || cols == 0) return 0;
-    return ortho_plan(batch, rows, cols).bytes;
+    const OrthoPlan p = ortho_plan(batch, rows, cols);
+    return p.fits ? p.bytes : -1;
 }
 
 int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype, const void* G, int64_t ldg,
@@ -1035,17 +1052,12 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
         return TGEMM_E_ALIGN;
     }
     const OrthoPlan p = ortho_plan(batch, rows, cols);
-    if (workspace_bytes < p.bytes) {
-        set_error("workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)p.bytes);
+    if (!p.fits) {
+        set_error("batch=%lld rows=%lld cols=%lld: too many tiles", (long long)batch, (long long)rows, (long long)cols);
         return TGEMM_E_ARG;
     }
-    const int64_t ut = p.upd->tile, tri = p.tri, upd = (p.mp / ut) * (p.np / ut);
-    const int64_t load = (p.mp / 64) * (p.np / 64);
-    if (!grid_fits((double)(batch * tri), p.sym->threads) || !grid_fits((double)(batch * upd), p.upd->threads) ||
-        !grid_fits((double)(batch * load), 256) ||
-        255 * 2 * (p.np > p.ms ? p.np : p.ms) + 128 > INT64_C(0xffffffff)) {  // a tile's copies take 32-bit offsets
-
-        set_error("too many tiles");
+    if (workspace_bytes < p.bytes) {
+        set_error("workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)p.bytes);
         return TGEMM_E_ARG;
     }
     const int rc = current_device_ok();
@@ -1066,11 +1078,8 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     in.mp = (int32_t)p.mp;
     in.np = (int32_t)p.np;
     in.tall = rows > cols;
-    while (in.lane_bits < 8 && (INT64_C(8) << in.lane_bits) < cols) ++in.lane_bits;
-    // a workgroup for each piece, up to PARTS (PARTS for every matrix: 300 of
-    // 40 x 70 61 us, now 5.5)
-    const int64_t pieces = ((rows + (256 >> in.lane_bits) - 1) / (256 >> in.lane_bits)) * ((cols + 2047) / 2048);
-    in.parts = (int32_t)(pieces < PARTS ? pieces : PARTS);
+    in.lane_bits = p.lane_bits;
+    in.parts = p.norm_parts;
     in.eps = eps;
     in.arrived = (int32_t*)(ws + p.off_arrived);
     in.counters = p.parts > 1 ? (int32_t)(batch * p.tri) : 0;
@@ -1082,7 +1091,7 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     hipError_t err = hipLaunchKernel(reinterpret_cast<const void*>(norm_fn), dim3((unsigned)(in.parts * batch)), dim3(256),
                                      in_args, 0, s);
     if (err == hipSuccess)
-        err = hipLaunchKernel(reinterpret_cast<const void*>(load_fn), dim3((unsigned)(batch * load)), dim3(256), in_args, 0,
+        err = hipLaunchKernel(reinterpret_cast<const void*>(load_fn), dim3((unsigned)(batch * p.load_tiles)), dim3(256), in_args, 0,
                               s);
 
     OrthoArgs g{};
@@ -1105,8 +1114,8 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
     g.m = (int32_t)p.m;
     g.n = (int32_t)p.n;
     g.tall = in.tall;
-    g.tiles_m = (int32_t)(p.mp / ut);
-    g.tiles_n = (int32_t)(p.np / ut);
+    g.tiles_m = (int32_t)(p.mp / p.upd->tile);
+    g.tiles_n = (int32_t)(p.np / p.upd->tile);
     auto launch = [&](OrthoFn fn, const OrthoKernels& k, int64_t tiles, int64_t parts) {
         if (err != hipSuccess) return;
         g.tiles = (int32_t)tiles;
@@ -1125,12 +1134,12 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
         g.xt = (const _Float16*)(ws + (k % 2 ? p.off_t1 : p.off_t0));
         g.xt_out = (_Float16*)(ws + (k % 2 ? p.off_t0 : p.off_t1));
         if (small) {
-            launch(ortho_gram_split_kernel<Ortho64, true>, *p.sym, tri, p.parts);
+            launch(ortho_gram_split_kernel<Ortho64, true>, *p.sym, p.tri, p.parts);
         } else {
-            launch(p.parts > 1 ? ortho_gram_split_kernel<Ortho64, false> : p.sym->first, *p.sym, tri, p.parts);
-            launch(p.sym->second, *p.sym, tri, 1);
+            launch(p.parts > 1 ? ortho_gram_split_kernel<Ortho64, false> : p.sym->first, *p.sym, p.tri, p.parts);
+            launch(p.sym->second, *p.sym, p.tri, 1);
         }
-        launch(k + 1 < steps ? update : last, *p.upd, upd, 1);
+        launch(k + 1 < steps ? update : last, *p.upd, p.upd_tiles, 1);
     }
     if (err != hipSuccess) {
         set_error("launch failed: %s", hipGetErrorString(err));
