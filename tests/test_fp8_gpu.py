@@ -571,3 +571,114 @@ def test_linear_refuses_forward_mode():
                 tl.linear_fp8(a, b)
     with pytest.raises((NotImplementedError, RuntimeError)):
         torch.func.jvp(lambda t: tl.linear_fp8(t, w), (x,), (x,))
+
+
+# ---- special values of the 16-bit types, other types of the layer, long rows ----
+
+@pytest.mark.parametrize("block", ["row", "square"])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_quantize_every_pattern_of_16_bits(dtype, fmt, block):
+    # in order (a block's values are alike: borders of scales, subnormals, all of
+    # a block NaN or infinite) and mixed
+    bits = torch.arange(-2 ** 15, 2 ** 15, dtype=torch.int32).to(torch.int16)
+    mixed = bits[torch.randperm(2 ** 16, generator=torch.Generator().manual_seed(1))]
+    small = mixed[(mixed.int() & 0x7FFF) < 0x0400]  # the smallest: subnormals and zeros among them
+    for x in (bits.view(512, 128), mixed.view(512, 128), mixed[:65520].view(252, 260), small[:2040].view(15, 136)):
+        x = x.contiguous().view(dtype)
+        q, s, qt, st = tl.quantize_fp8(x.cuda(), dtype=FMT[fmt], block=block, transpose=True)
+        check_image(host(x), fmt, block, q, s)
+        check_image(np.ascontiguousarray(host(x).T), fmt, block, qt, st)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_quantize_16_bit_borders(dtype, fmt):
+    # a block's largest value on the largest of the format times 2^k, next above
+    # and next below, beside values that end halfway between two of the format
+    top, t = ref.TABLE[fmt][-1], ref.TABLE[fmt]
+    rows = []
+    for k in (-100, -40, -16, -8, -3, 0, 5) if dtype == torch.bfloat16 else (-20, -16, -8, -3, 0):
+        if top * 2.0 ** k > torch.finfo(dtype).max:
+            continue
+        big = torch.tensor([top * 2.0 ** k], dtype=dtype).view(torch.int16)
+        for step in (-1, 0, 1):
+            v = float((big + step).view(dtype))
+            mids = np.concatenate([(t[:-1] + t[1:]) / 2, t])[:127] * 2.0 ** k
+            rows.append(np.concatenate([[v], np.minimum(mids, abs(v)), np.zeros(127 - len(mids))]))
+    x = torch.from_numpy(np.array(rows)).to(dtype)
+    q, s, qt, st = tl.quantize_fp8(x.cuda(), dtype=FMT[fmt], transpose=True)
+    check_image(host(x), fmt, "row", q, s)
+    check_image(np.ascontiguousarray(host(x).T), fmt, "row", qt, st)
+
+
+@pytest.mark.parametrize("xd,wd", [(torch.float32, torch.float32), (torch.float16, torch.float16), (torch.bfloat16, torch.float32),
+                                   (torch.float32, torch.bfloat16), (torch.float16, torch.bfloat16)])
+@pytest.mark.parametrize("M,N,K", [(5, 130, 257), (300, 520, 390), (900, 700, 1100)])
+def test_linear_of_other_types(M, N, K, xd, wd):
+    # values that every type holds in full; results are the bfloat16 ones, and over
+    # all elements within one rounding of them, which a lost slice would exceed
+    x, w, gy = (draw(r, c, s, torch.float32, 0.3).to(xd if s != 2 else wd) for r, c, s in ((M, K, 1), (N, K, 2), (M, N, 3)))
+    want = linear_reference(host(x), host(w), host(gy))
+    xg, wg = x.cuda().requires_grad_(), w.cuda().requires_grad_()
+    y = tl.linear_fp8(xg, wg)
+    dx, dw = torch.autograd.grad(y, (xg, wg), gy.cuda())
+    for got, dtype, (ref_, mag), k in zip((y, dx, dw), (xd, xd, wd), want, (K, N, M)):
+        assert got.dtype == dtype and torch.equal(got, got.bfloat16().to(dtype))
+        err = np.abs(host(got) - ref_)
+        assert (err <= ref.gemm_bound(ref_, mag, k)).all()
+        assert np.linalg.norm(err) <= 2.0 ** -8 * np.linalg.norm(ref_)
+
+
+def check_on_gpu(c, a, sa, b, sb, K):
+    def v(q, s):
+        e = (s.contiguous().view(torch.uint8).double() - 127).t().repeat_interleave(128, 1)[:, :K]
+        return q.double() * torch.exp2(e)
+    av, bv = v(a, sa), v(b, sb)
+    want, mag = av @ bv.t(), av.abs() @ bv.abs().t()
+    off = (2.0 ** -10 + (K / 8 + 16) * 2.0 ** -24) * mag
+    c = c.double()
+    assert bool(((c - want).abs() <= 2.0 ** -8 * (want.abs() + off) + off).all())
+    assert float((c - want).norm()) <= 2.0 ** -8 * float(want.norm())
+
+
+def test_gemm_random_shapes_over_all_elements():
+    # over all elements a rounding is 0.42 2^-8 of the norm; one element lost of a
+    # row of 4096 adds 2^-6
+    import random
+    r = random.Random(11)
+    for i in range(40):
+        M, N, K = (max(1, int(2 ** r.uniform(0, top))) for top in (11.5, 11.5, 12))
+        a, sa = tl.quantize_fp8(draw(max(M, 4), K, i, spread=0.3).cuda()[:M], dtype=FMT[r.choice(["e4m3", "e5m2"])])
+        b, sb = tl.quantize_fp8(draw(max(N, 40), K, i + 100, spread=0.3).cuda())
+        print(M, max(N, 40), K, flush=True)
+        check_on_gpu(tl.gemm_fp8(a, sa, b, sb), a, sa, b, sb, K)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 50257, 300), (1, 17000, 4200), (16, 33000, 700), (33, 16400, 1030), (20000, 2, 1300)])
+def test_gemm_few_rows_and_many_columns(M, N, K):
+    a, sa = tl.quantize_fp8(draw(M, K, 1, spread=0.3).cuda())
+    b, sb = tl.quantize_fp8(draw(N, K, 2, spread=0.3).cuda())
+    c = tl.gemm_fp8(a, sa, b, sb)
+    check_on_gpu(c, a, sa, b, sb, K)
+    assert torch.equal(tl.gemm_fp8(a.contiguous(), sa, b.contiguous(), sb), c)
+
+
+@pytest.mark.parametrize("K", [1000, 1023, 1025, 2049, 4095, 4097, 4100])
+@pytest.mark.parametrize("M,N", [(5, 100), (20, 300), (300, 1400), (1900, 1990), (3500, 3600)])
+def test_gemm_counts_the_last_elements_once(M, N, K):
+    one = torch.ones((N, K), device="cuda").to(FMT["e4m3"])
+    sb = torch.full((-(-K // 128), -(-N // 16) * 16), 127, dtype=torch.uint8, device="cuda")[:, :N]
+    sa = torch.full((-(-K // 128), -(-M // 16) * 16), 127, dtype=torch.uint8, device="cuda")[:, :M]
+    for count in (1, 2, 17, 130):
+        a = torch.zeros((M, K), device="cuda")
+        a[:, K - count:] = 1
+        a[::2, 0] = -1  # and the first
+        want = torch.full((M, N), float(count), device="cuda")
+        want[::2] -= 1
+        a = a.to(FMT["e4m3"])
+        assert torch.equal(tl.gemm_fp8(a, sa, one, sb), want.bfloat16()), count
+        ld = -(-K // 128) * 128
+        ap, bp = (torch.full((r, ld), 0x7F, dtype=torch.uint8, device="cuda") for r in (M, N))  # NaN behind the rows
+        ap[:, :K], bp[:, :K] = a.view(torch.uint8), one.view(torch.uint8)
+        assert torch.equal(tl.gemm_fp8(ap.view(a.dtype)[:, :K], sa, bp.view(a.dtype)[:, :K], sb), want.bfloat16()), count
