@@ -223,8 +223,8 @@ const Fp8Kernel* fp8_kernel_table() {
     // 256 x 256: four waves of 128 x 128, one a SIMD.  Against eight of 128 x
     // 64 they read a third less from LDS for the same matrix instructions,
     // which leaves the power budget a higher clock (e4m3 8192^3 354 us against
-    // 366, 4096^3 both 52.5).  In the steady loop the matrix cores are busy
-    // 91 % of the cycles.
+    // 366, 4096^3 both 52.5).  Of the cycles that a longer K adds (4096 x 4096, K
+    // from 4096 to 32768) the matrix cores are busy 85 %.
     typedef NtGemm<Tr, 256, 256, 2, 2, 2, false> G256;
     // 128 x 128 with a compute unit to itself: eight waves, four slots (four
     // waves: 1024x4096x4096 24.5 us against 22.7).  Where there are several

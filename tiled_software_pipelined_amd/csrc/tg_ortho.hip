@@ -30,7 +30,7 @@
 // d_i, |A'_i|^2 > d_i^2 (for a projection: less than half of the row's unit vector
 // lies in it), takes e_i from hi as well, so that what is left out is B lo;
 // others take it from hi + lo, where B' lo is the smaller (random elements, 300 x
-// 301: 6e-4 against 1.3e-3).  Rank one, 65 x 70: 6e-3 -> 7e-4.
+// 301: 6e-4 against 1.3e-3).  Rank one, 65 x 70: 6e-3 -> 1e-3.
 //
 // hi, A' and B' are rounded up or down by thresholds of an element's place, not
 // to nearest (see Dither below).
@@ -456,7 +456,8 @@ __global__ __launch_bounds__(G::NT) void ortho_poly_kernel(OrthoArgs g) {
     float* e = g.e + (int64_t)t.z * g.ms;
     // A' and d of one register quad.  Large tiles request them a quad ahead of
     // their use: the compiler may not move a load over a store, and a load's
-    // latency for each row would add up (110 us against 99 at 4096 x 4096).
+    // latency for each row would add up (4096 x 4096
+    // on 256 x 256 tiles: 110 us against 99).
     // Small ones have the registers to request all before the product.
     const int mb = t.m0 + t.wm0, n = t.n0 + t.wn0 + G::col_of(0, t.lane);
     struct Quad {
@@ -686,8 +687,8 @@ __device__ __forceinline__ void load8(float (&v)[8], const typename E::T* row, i
 // Workgroup (p, z): pieces p, p + parts .. of matrix z, a piece 2048 elements
 // of a row, or as many rows together as 256 threads reach where rows are
 // short; its sum of squares in double (squares of any float fit), always in
-// the same order.  Four pieces are requested at a time (one: 4096x4096 20 us;
-// now 13).
+// the same order.  Four pieces are requested at a time (one: 4096x4096 25 us;
+// now 16).
 template <class E>
 __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoInArgs g) {
     __shared__ double sums[4];
@@ -779,10 +780,11 @@ typedef void (*OrthoInFn)(OrthoInArgs);
 
 // Kernels of the symmetric products (gram, poly) and of the update (middle
 // steps, last), by tile, with a model of their time in microseconds fitted to
-// runs of all of them at K = 64 .. 4096 and 1 .. 2080 tiles (medians of
-// kernel times): start + rounds (fixed + per_k K), K the product's inner
-// size.  Tiles of which two share a compute unit (`shared`) overlap their
-// rounds; the others run whole rounds of 256.
+// runs of all of them at K = 64 .. 4096 and 1 .. 2080 tiles: start + rounds
+// (fixed + per_k K), K the product's inner size.  Tiles of which two share a
+// compute unit (`shared`) overlap their rounds; the others run whole rounds of
+// 256.  Medians of kernel times, when all roundings were to nearest (the choice
+// at 4096^2 takes 80 and 140 us now):
 //   gram, us          64     128    192    256
 //   K =  256 (256^2)    4.3    5.9   10.1   10.6
 //   K = 1024 (1024^2)   7.6   11.2   18.5   26.4
@@ -813,7 +815,8 @@ static OrthoKernels update_kernels(bool shared, double start, double fixed, doub
 // 64: four slots, so that two workgroups fit a compute unit (eight slots and
 // one: 10 % slower alone, 1.5 times as long where there are several rounds).
 // 128: eight waves of 64 x 32 (four of 64 x 64: 11.2 -> 12.8 us at 1024^2).
-// 192: twelve waves of 96 x 32 (four of 96 x 96: 74 -> 79 us at 4096^2).
+// 192: twelve waves of 96 x 32 (four of 96 x 96: gram 80 -> 88 us, poly 84 -> 95
+// at 4096^2).
 typedef NtGemm<NtF16, 256, 256, 2, 4, 2, false> Ortho256;
 typedef NtGemm<NtF16, 192, 192, 2, 6, 3, true> Ortho192;
 typedef NtGemm<NtF16, 128, 128, 2, 4, 4, true> Ortho128;

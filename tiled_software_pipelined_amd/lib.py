@@ -503,7 +503,8 @@ def quantize_fp8(X, dtype=torch.float8_e4m3fn, block="row", transpose=False):
     "row" each image's scales follow its own rows.  A scale is the least power
     of two (at least 2^-127) that keeps its block's finite values within the
     type's range.  NaN stays NaN, and an infinity becomes the type's infinity
-    or NaN.  Runs on the current stream.
+    or NaN.  Runs on the current stream.  Not differentiable: the images carry no
+    gradient of an X that requires one (:func:`linear_fp8` does).
     """
     fmt = _fp8_code(dtype)
     if block not in BLOCKS:
@@ -560,7 +561,7 @@ def gemm_fp8(A, SA, B, SB, out=None):
     scale tables SA (ceil(K / 128), M) and SB (ceil(K / 128), N) as
     :func:`quantize_fp8` returns them.  Returns C (M, N) bfloat16, rounded
     once from the matrix cores' float sums; ``out`` may be a preallocated
-    row-major C.
+    row-major C.  Not differentiable: C carries no gradient.
     """
     device = A.device
     if not (A.is_cuda and B.is_cuda):
@@ -665,8 +666,8 @@ def linear_fp8(x, w, grad_dtype=torch.float8_e4m3fn):
     (float8_e4m3fn or float8_e5m2), along its rows for x's gradient and along
     its columns for w's, and takes both products from the 8-bit images kept by
     the forward pass: dx = g w, dw = g^T x.  Rounding is passed straight
-    through.  Gradients have their inputs' dtypes; second derivatives and
-    forward-mode ones are refused.  A weight that does not change between calls is better quantised
+    through.  Gradients are rounded to bfloat16 like y and have their inputs'
+    dtypes; second derivatives and forward-mode ones are refused.  A weight that does not change between calls is better quantised
     once (:func:`quantize_fp8`, then :func:`gemm_fp8`).  To capture a training
     step into a graph, capture torch.autograd.grad, or make sure that no eager
     graph of the same leaves is alive: torch's nodes that accumulate into
@@ -744,7 +745,7 @@ def orthogonalize(G, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e-7,
     (3.5).  Returns bfloat16 of G's shape, rounded once; ``out`` may be a
     preallocated bfloat16 tensor of evenly spaced row-major matrices (G itself
     included).  The workspace comes from torch's allocator on the current
-    stream.
+    stream.  Not differentiable: the result carries no gradient of G.
     """
     if not G.is_cuda:
         raise ValueError("G must be a GPU tensor")
