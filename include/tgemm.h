@@ -455,8 +455,8 @@ const char* tgemm_fp8_gemm_kernel(int64_t M, int64_t N, int64_t K, int64_t lda, 
  * as zero: a matrix far smaller than eps); products take 11-bit operands, for
  * up to 64 rows or columns 22-bit X, with float sums.  With five steps of the
  * usual coefficients the result is off by 0.5 to 1.3e-3 of its norm before its
- * rounding to bfloat16 (itself 1.7e-3) for random matrices, and by at most 5e-3
- * in 3000 of low rank or with repeated elements.  A matrix of zeros gives zeros
+ * rounding to bfloat16 (itself 1.7e-3) for random matrices, and by at most 5.5e-3
+ * in 6000 of low rank or with repeated elements.  A matrix of zeros gives zeros
  * (for eps > 0); one with a NaN or an infinity gives NaN everywhere.  Coefficients are refused (TGEMM_E_ARG) when they are not
  * finite or above 1e15, or let singular values that start in [0, 1] pass 3.5
  * before the last step, or |b s^2 + c s^4| pass 14 in any: the workspace's half

@@ -40,7 +40,7 @@
 // refuses coefficients that could leave that range.  hi + lo is off by up to
 // 2^-21 of an element, or by 2^-37 where that is more.  Against 64 bits the result is off by
 // 0.5 - 1.3e-3 of its norm before its one rounding to bfloat16 (itself 1.7e-3)
-// for random matrices, and by at most 5e-3 in 3000 of low rank or with repeated
+// for random matrices, and by at most 5.5e-3 in 6000 of low rank or with repeated
 // elements (emulated; the tests hold the kernels to the emulation).
 //
 // All products have both operands K-contiguous: X X^T; A' A' (symmetric); and
