@@ -20,6 +20,13 @@ A matrix far smaller than eps: half precision's subnormal step is 2^-24, and
 stands for 2^-36 of X (held times 2^12), so hi + lo is off by up to 2^-37 at
 each step, which later steps multiply by a: at most (3.4445^5 - 1) / 2.4445
 2^-37 < 2e-9 for an element, FLOOR below.
+
+These derivations take roundings to nearest.  X's high half, A' and B' are now
+rounded by thresholds of an element's place, off by up to a whole step and, over
+many elements, by 1.41 times as much; X is held to 21 bits.  What that makes of
+matrices like those below is emulated rounding by rounding (ortho_ref, and its
+tests on the CPU): up to 1.2e-3 of the norm for random ones, and below 4.5e-3
+for the others, so the bounds stay.
 """
 import pytest
 import torch
@@ -364,3 +371,44 @@ def test_not_a_number_of_any_pattern():
                 got = tl.orthogonalize(G, steps=steps)
                 assert bool(got[1].isnan().all()), (dtype, pattern, m, steps)
             assert torch.equal(got[0], clean[0])
+
+
+def test_few_steps_of_small_matrices():
+    for m, n in ((1, 1), (40, 70), (64, 64), (3, 5000), (64, 4200), (70, 90)):
+        G = randn(m, n, seed=m + n)
+        for steps in (1, 2, 3):
+            got, ref = tl.orthogonalize(G, steps=steps), want(G, steps)
+            if m * n > 1:
+                check(got, ref)
+            else:
+                # 0.42 of half a step is for many values; one is off by up to all of
+                # it (three steps make 1.1136 of one element, between 1.1094 and
+                # 1.1172: off by 0.0036 rounded to nearest, 0.42 2^-8 of it is 0.0018)
+                assert float((got.double() - ref).abs()) <= (2.0 ** -8 + RANDOM) * float(ref.abs())
+
+
+def test_small_matrices_at_once_and_replayed():
+    # up to 64 rows, the first product shared by several workgroups or not
+    xs = randn(64, 4200, seed=31), randn(3, 40, 90, seed=32)
+    ref = [tl.orthogonalize(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = []
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, x in zip(streams, xs):
+            with torch.cuda.stream(s):
+                got.append(tl.orthogonalize(x))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, ref[i % 2]) for i, g in enumerate(got))
+    graphs = []
+    for x in xs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=streams[0]):
+            graphs.append((graph, tl.orthogonalize(x), x))
+    for r in range(4):
+        for graph, held, x in graphs:
+            x.add_(0.5 * torch.randn_like(x))
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(held, tl.orthogonalize(x)), r
