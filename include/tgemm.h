@@ -476,6 +476,96 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
                         const double* coefficients, double eps, void* workspace, int64_t workspace_bytes,
                         void* stream);
 
+/* ---- products of a training step with fused ends -----------------------------
+ *
+ * bfloat16 or float16 operands (`dtype`, the same for every tensor of a call),
+ * row-major with leading dimensions, float sums on the matrix cores.  Sizes that
+ * are contracted and leading dimensions: up to 2^22; rows up to 2^30.  Operands may
+ * start at any element.  Outputs must not overlap anything else. */
+
+/* The gated feed-forward block, for x (M x K), wg and wu (F x K), wd (N x F):
+ *
+ *     g = x wg^T,  u = x wu^T,  h = act(g) u,  y = h wd^T   (M x N)
+ *
+ * act: silu g / (1 + e^-g), gelu g Phi(g), its tanh form, or relu.  h is rounded
+ * to `dtype` (the operand of the second product), y once from float sums.  `keep`
+ * says which gradients will be asked for; g and u, rounded, are then kept in
+ * `saved` (only h for TGEMM_FFN_DOWN alone).  backward, for dy (M x N):
+ *
+ *     dh = dy wd,  dg = dh u act'(g),  du = dh act(g),
+ *     dx = dg wg + du wu,  dwg = dg^T x,  dwu = du^T x,  dwd = dy^T h
+ *
+ * with dg, du and h rounded to `dtype`; outputs are written where `keep` (the same
+ * as before) has their bit, and ignored otherwise.  relu'(0) = 0.  tgemm_ffn_bytes
+ * fills bytes[0 .. 2] with the sizes of `saved`, of forward's `scratch` and of
+ * backward's `scratch`: device memory, 256-byte aligned; a scratch's contents are
+ * overwritten, `saved` is only read by backward.  Sizes of zero are the empty
+ * products they make.  Each returns TGEMM_OK or a TGEMM_E_* code. */
+#define TGEMM_SILU 0
+#define TGEMM_GELU 1
+#define TGEMM_GELU_TANH 2
+#define TGEMM_RELU 3
+#define TGEMM_FFN_X 1
+#define TGEMM_FFN_GATE 2
+#define TGEMM_FFN_UP 4
+#define TGEMM_FFN_DOWN 8
+int tgemm_ffn_bytes(int64_t M, int64_t K, int64_t F, int64_t N, int32_t keep, int64_t* bytes);
+int tgemm_ffn_forward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype, int32_t act, const void* x, int64_t ldx,
+                      const void* wg, int64_t ldg, const void* wu, int64_t ldu, const void* wd, int64_t ldd, void* y,
+                      int64_t ldy, int32_t keep, void* saved, void* scratch, void* stream);
+int tgemm_ffn_backward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype, int32_t act, const void* x, int64_t ldx,
+                       const void* wg, int64_t ldg, const void* wu, int64_t ldu, const void* wd, int64_t ldd,
+                       const void* dy, int64_t lddy, int32_t keep, const void* saved, void* dx, int64_t lddx, void* dwg,
+                       int64_t lddwg, void* dwu, int64_t lddwu, void* dwd, int64_t lddwd, void* scratch, void* stream);
+
+/* Softmax cross entropy of a linear layer's logits z = x w^T, for x (M x K), w
+ * (V x K) and a target for each row:
+ *
+ *     lse = log sum_v exp z_v,   loss = lse - z[target]
+ *
+ * The logits are not stored.  Rows whose target is `ignore` do not count: they
+ * are left out of every product, and their loss and gradient are zero, whatever
+ * they hold.  A target that is neither `ignore` nor in [0, V) makes its row's loss
+ * NaN, and the gradients that the row enters.  reduction: TGEMM_NONE (loss: M
+ * floats), TGEMM_SUM, or TGEMM_MEAN over the rows that count (one float; NaN where
+ * none does).  saved: which rows count and their lse, for the backward pass, which
+ * only reads it.  backward, with dloss the gradient of the loss (M floats or one):
+ *
+ *     dz = c (exp(z - lse) - [target]),  dx = dz w,  dw = dz^T x,
+ *
+ * c the row's share of dloss.  It makes z again, a piece of the vocabulary at a
+ * time, and rounds dz to `dtype`, scaled by a power of two to at most 2^15; dx is
+ * summed in float over the pieces and rounded once.  keep: TGEMM_KEEP_X (dx) and
+ * TGEMM_KEEP_W (dw).  tgemm_xent_bytes fills bytes[0 .. 2] with the sizes of
+ * `saved`, forward's `scratch` (both for any keep) and backward's: device memory,
+ * 256-byte aligned; a scratch's contents are overwritten.  Sizes of zero are the
+ * empty sums they make.  Each returns TGEMM_OK or a TGEMM_E_* code. */
+#define TGEMM_NONE 0
+#define TGEMM_SUM 1
+#define TGEMM_MEAN 2
+int tgemm_xent_bytes(int64_t M, int64_t V, int64_t K, int32_t keep, int64_t* bytes);
+int tgemm_xent_forward(int64_t M, int64_t V, int64_t K, int32_t dtype, const void* x, int64_t ldx, const void* w,
+                       int64_t ldw, const int64_t* target, int64_t ignore, int32_t reduction, float* loss, void* saved,
+                       void* scratch, void* stream);
+int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const void* x, int64_t ldx, const void* w,
+                        int64_t ldw, const int64_t* target, int32_t reduction, const float* dloss, const void* saved,
+                        int32_t keep, void* dx, int64_t lddx, void* dw, int64_t lddw, void* scratch, void* stream);
+
+/* Clipping by the norm of many tensors taken as one vector: *norm (a float in
+ * device memory) = root of the sum of squares of all elements, summed in 64 bits;
+ * out[i] = in[i] min(1, max_norm / (norm + eps)), the factor rounded to float and
+ * the product to the tensor's type.  Tensor i has counts[i] adjacent elements of
+ * type dtypes[i] (TGEMM_F32, TGEMM_BF16, TGEMM_F16); out[i] may be in[i], and
+ * otherwise must not overlap any tensor; no tensor may be given twice.  A norm of
+ * infinity makes the factor zero (infinite elements become NaN), a NaN makes
+ * everything NaN.  in, out, counts, dtypes are host arrays, read during the call.
+ * workspace: tgemm_clip_workspace_bytes(tensors, counts) bytes (-1 for sizes out of
+ * range: 2^40 elements in all) of device memory, 256-byte aligned, overwritten.
+ * Returns TGEMM_OK or a TGEMM_E_* code. */
+int64_t tgemm_clip_workspace_bytes(int64_t tensors, const int64_t* counts);
+int tgemm_clip(int64_t tensors, const void* const* in, void* const* out, const int64_t* counts, const int32_t* dtypes,
+               double max_norm, double eps, float* norm, void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Library version string. */
 const char* tgemm_version(void);
 

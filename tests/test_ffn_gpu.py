@@ -1,0 +1,204 @@
+"""GPU: the gated feed-forward block and its gradients against a plain form in 64 bits."""
+import itertools
+
+import pytest
+import torch
+
+import step_ref as ref
+
+tl = pytest.importorskip("tiled_software_pipelined_amd.lib")
+pytestmark = pytest.mark.gpu
+NAMES = ("dx", "dw_gate", "dw_up", "dw_down")
+
+
+def make(M, K, F, N, dtype, seed=0, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed + 7919 * M + 31 * K + F + N)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    return [t.to(dtype) for t in (r(M, K) * scale, r(F, K) / max(K, 1) ** 0.5, r(F, K) / max(K, 1) ** 0.5, r(N, F) / max(F, 1) ** 0.5, r(M, N))]
+
+
+def run(leaves, dy, act, needs=(True,) * 4):
+    leaves = [t.detach().requires_grad_(n) for t, n in zip(leaves, needs)]
+    y = tl.gated_ffn(*leaves, activation=act)
+    wanted = [t for t, n in zip(leaves, needs) if n]
+    grads = iter(torch.autograd.grad(y, wanted, dy))
+    return {"y": y.detach(), **{name: next(grads) for name, n in zip(NAMES, needs) if n}}
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,K,F,N", [
+    (1, 1, 1, 1), (3, 5, 2, 9), (1, 64, 128, 64), (7, 8, 16, 24), (16, 100, 33, 70), (17, 65, 66, 67), (32, 512, 1024, 256),
+    (33, 64, 64, 64), (65, 127, 129, 63), (130, 200, 513, 77), (63, 2050, 70, 2050), (300, 264, 520, 264),
+    (2050, 72, 4100, 136), (1030, 1000, 2100, 515), (5, 4096, 3, 2), (2, 3, 4096, 5), (4099, 8, 9, 10)])
+def test_sizes(M, K, F, N, dtype):
+    *leaves, dy = make(M, K, F, N, dtype)
+    ref.check(run(leaves, dy, "silu"), ref.ffn(*leaves, "silu", dy))
+    with torch.no_grad():
+        ref.check({"y": tl.gated_ffn(*leaves)}, ref.ffn(*leaves, "silu"))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("act", list(tl.ACTIVATIONS))
+@pytest.mark.parametrize("M", [9, 150])
+def test_activations(act, M, dtype):
+    *leaves, dy = make(M, 96, 200, 80, dtype, scale=3.0)
+    ref.check(run(leaves, dy, act), ref.ffn(*leaves, act, dy))
+
+
+@pytest.mark.parametrize("act", list(tl.ACTIVATIONS))
+def test_activations_over_their_range(act):
+    """Gate values from far below to far above, each alone in its product: h itself."""
+    g = torch.cat([torch.linspace(-30, 30, 1201), torch.tensor([-200.0, -88.5, 88.5, 200.0, 0.0, -0.0, 1e-6, -1e-6])]).to(torch.float16)
+    F = g.numel()
+    x, one = torch.ones(40, 1, dtype=torch.float16, device="cuda"), torch.ones(F, 1, dtype=torch.float16, device="cuda")
+    eye = torch.eye(F, dtype=torch.float16, device="cuda")
+    gd = g.double()
+    want = ref.act(gd, act)[0]
+    for rows in (1, 40):  # the kernel for few rows, the tiles
+        y = tl.gated_ffn(x[:rows], g[:, None].cuda(), one, eye, activation=act).double().cpu()
+        # two roundings to float16; the activation is good to 2^-20 of its value and 2^-23 of its argument
+        bound = 2 * 2.0 ** -11 * want.abs() + 2.0 ** -24 + 2.0 ** -20 * want.abs() + 2.0 ** -23 * gd.abs() * (gd > -20)
+        assert ((y - want).abs() <= bound).all(), float(((y - want).abs() - bound).max())
+
+
+@pytest.mark.parametrize("needs", [n for n in itertools.product((False, True), repeat=4) if any(n)])
+def test_only_the_gradients_that_are_asked_for(needs):
+    *leaves, dy = make(70, 96, 130, 64, torch.bfloat16)
+    got = run(leaves, dy, "gelu", needs)
+    assert set(got) == {"y"} | {n for n, k in zip(NAMES, needs) if k}
+    ref.check(got, ref.ffn(*leaves, "gelu", dy), got)
+
+
+def test_gradients_against_differences():
+    """Float16 inputs, and differences of the form in 64 bits: no formula of the derivative in between."""
+    *leaves, dy = make(6, 12, 10, 8, torch.float16)
+    got = run(leaves, dy, "gelu_tanh")
+    wide = [t.double().cpu() for t in leaves]
+
+    def value():
+        g, u = wide[0] @ wide[1].t(), wide[0] @ wide[2].t()
+        return float(((ref.act(g, "gelu_tanh")[0] * u) @ wide[3].t() * dy.double().cpu()).sum())
+
+    for name, t in zip(NAMES, wide):
+        bound = ref.ffn(*leaves, "gelu_tanh", dy)[name][1].cpu()
+        flat = t.view(-1)
+        for i in range(0, flat.numel(), 7):
+            old = flat[i].item()
+            flat[i] = old + 1e-5
+            up = value()
+            flat[i] = old - 1e-5
+            down = value()
+            flat[i] = old
+            assert abs(got[name].double().cpu().reshape(-1)[i].item() - (up - down) / 2e-5) <= bound.reshape(-1)[i].item() + 1e-7
+
+
+@pytest.mark.parametrize("M", [4, 100])
+def test_strides_and_views(M):
+    K, F, N, t = 70, 90, 50, torch.bfloat16
+    x, wg, wu, wd, dy = make(M, K, F, N, t)
+    both = torch.cat([wg, wu])  # one tensor of both projections
+    wide = torch.full((N, F + 13), float("nan"), dtype=t, device="cuda")
+    wide[:, 5:5 + F] = wd
+    apart = torch.full((M, K + 3), float("nan"), dtype=t, device="cuda")
+    apart[:, 1:1 + K] = x
+    views = [apart[:, 1:1 + K], both[:F], both[F:], wide[:, 5:5 + F]]
+    want = ref.ffn(x, wg, wu, wd, "silu", dy)
+    ref.check(run(views, dy, "silu"), want)
+    ref.check(run([x.t().contiguous().t(), wg.t().contiguous().t(), wu, wd], dy, "silu"), want)  # columns apart: copies
+    ref.check({"y": tl.gated_ffn(*views)}, want, ("y",))
+    # a broadcast gradient, and more axes
+    ones = torch.ones((), dtype=t, device="cuda").expand(M, N)
+    ref.check(run([x, wg, wu, wd], ones, "silu"), ref.ffn(x, wg, wu, wd, "silu", ones))
+    y = tl.gated_ffn(x.view(2, M // 2, K), wg, wu, wd)
+    assert y.shape == (2, M // 2, N) and torch.equal(y.view(M, N), tl.gated_ffn(x, wg, wu, wd))
+    assert torch.equal(tl.gated_ffn(x[0], wg, wu, wd), tl.gated_ffn(x[:1], wg, wu, wd)[0])
+
+
+@pytest.mark.parametrize("M,K,F,N", [(0, 8, 8, 8), (4, 0, 8, 8), (4, 8, 0, 8), (4, 8, 8, 0), (40, 0, 8, 8), (40, 8, 0, 8)])
+def test_empty_sizes(M, K, F, N):
+    *leaves, dy = make(M, K, F, N, torch.bfloat16)
+    got = run(leaves, dy, "silu")
+    assert got["y"].shape == (M, N) and not got["y"].any() or K and F
+    for name, t in zip(NAMES, leaves):
+        assert got[name].shape == t.shape and not got[name].any()
+
+
+def test_values_that_are_not_finite_stay_in_their_rows():
+    *leaves, dy = make(200, 80, 96, 64, torch.bfloat16)
+    clean = tl.gated_ffn(*leaves)
+    leaves[0][3, 5], leaves[0][150, 0] = float("nan"), float("inf")
+    y = tl.gated_ffn(*leaves)
+    rows = [i for i in range(200) if i not in (3, 150)]
+    assert torch.equal(y[rows], clean[rows]) and y[3].isnan().all() and not y[150].isfinite().any()
+    few = tl.gated_ffn(leaves[0][:8], *leaves[1:])
+    assert few[3].isnan().all() and few[[0, 1, 2, 4, 5, 6, 7]].isfinite().all()
+
+
+def test_same_bits_every_time():
+    *leaves, dy = make(500, 512, 1376, 512, torch.bfloat16)
+    first = run(leaves, dy, "silu")
+    for _ in range(3):
+        again = run(leaves, dy, "silu")
+        assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+def test_captured_and_replayed():
+    *leaves, dy = make(100, 128, 344, 128, torch.bfloat16)
+    leaves = [t.requires_grad_() for t in leaves]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(tl.gated_ffn(*leaves), leaves, dy)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for _ in range(2):  # two graphs with workspaces of one pool
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=graphs[0].pool() if graphs else None):
+            y = tl.gated_ffn(*leaves)
+            outs.append((y, *torch.autograd.grad(y, leaves, dy)))
+        graphs.append(g)
+    for seed in range(3):
+        *new, ndy = make(100, 128, 344, 128, torch.bfloat16, seed=100 + seed)
+        with torch.no_grad():
+            for t, n in zip((*leaves, dy), (*new, ndy)):
+                t.copy_(n)
+        want = run(new, ndy, "silu")
+        for g, out in zip(graphs, outs):
+            g.replay()
+            torch.cuda.synchronize()
+            for name, o in zip(("y",) + NAMES, out):
+                assert torch.equal(o, want[name]), (seed, name)
+
+
+def test_streams_side_by_side():
+    cases = [make(M, 256, 700, 256, torch.bfloat16, seed=M) for M in (1, 40, 300)]
+    want = [run(c[:4], c[4], "silu") for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    for c, s in zip(cases, streams):
+        with torch.cuda.stream(s):
+            got.append(run(c[:4], c[4], "silu"))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w[k], g[k]) for k in w)
+
+
+def test_no_write_outside_the_outputs():
+    """Rows of y and of the gradients end at odd places: what stands behind them stays."""
+    M, K, F, N = 37, 33, 35, 39
+    *leaves, dy = make(M, K, F, N, torch.bfloat16)
+    x, wg, wu, wd = leaves
+    held = {k: torch.full((r + 2, c + 5), 7.0, dtype=torch.bfloat16, device="cuda") for k, (r, c) in
+            {"y": (M, N), "dx": (M, K), "dw_gate": (F, K), "dw_up": (F, K), "dw_down": (N, F)}.items()}
+    sizes = tl._ffn_bytes(M, K, F, N, 15)
+    saved, s1, s2 = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes)
+    at = lambda k: (held[k][1:].data_ptr(), held[k].shape[1])  # noqa: E731
+    p = lambda t: (t.data_ptr(), t.shape[1])  # noqa: E731
+    tl._call(x.device, tl._lib.tgemm_ffn_forward, M, K, F, N, tl.BF16, 0, *p(x), *p(wg), *p(wu), *p(wd), *at("y"), 15,
+             saved.data_ptr(), s1.data_ptr())
+    tl._call(x.device, tl._lib.tgemm_ffn_backward, M, K, F, N, tl.BF16, 0, *p(x), *p(wg), *p(wu), *p(wd), *p(dy), 15,
+             saved.data_ptr(), *at("dx"), *at("dw_gate"), *at("dw_up"), *at("dw_down"), s2.data_ptr())
+    got = run(leaves, dy, "silu")
+    for k, t in held.items():
+        assert torch.equal(t[1:-1, :-5], got[k]) and (t[0] == 7).all() and (t[-1] == 7).all() and (t[:, -5:] == 7).all(), k

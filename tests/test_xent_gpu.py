@@ -1,0 +1,246 @@
+"""GPU: the cross entropy of a linear layer's logits against a plain form in 64 bits."""
+import pytest
+import torch
+
+import step_ref as ref
+
+tl = pytest.importorskip("tiled_software_pipelined_amd.lib")
+pytestmark = pytest.mark.gpu
+DTYPES = [torch.bfloat16, torch.float16]
+
+
+def make(M, V, K, dtype, seed=0, ignored=0.25, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed + 7919 * M + 31 * K + V)
+    x = (torch.randn((M, K), generator=g, device="cuda") * scale).to(dtype)
+    w = (torch.randn((V, K), generator=g, device="cuda") / max(K, 1) ** 0.5).to(dtype)
+    target = torch.randint(0, max(V, 1), (M,), generator=g, device="cuda")
+    gone = torch.rand((M,), generator=g, device="cuda") < ignored
+    if M:
+        gone[0] = False
+    return x, w, torch.where(gone, -100, target)
+
+
+def run(x, w, target, dloss=1.0, reduction="mean", ignore=-100):
+    x, w = x.detach().requires_grad_(), w.detach().requires_grad_()
+    loss = tl.linear_cross_entropy(x, w, target, ignore, reduction)
+    g = torch.as_tensor(dloss, dtype=torch.float32, device=x.device).expand(loss.shape)
+    dx, dw = torch.autograd.grad(loss, (x, w), g)
+    return {"loss": loss.detach(), "dx": dx, "dw": dw}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,V,K", [
+    (1, 1, 1), (1, 2, 3), (2, 7, 5), (1, 1000, 64), (5, 129, 16), (64, 128, 64), (65, 127, 66), (33, 1000, 100), (130, 513, 200),
+    (200, 3001, 72), (700, 300, 520), (2050, 4100, 40), (3, 50257, 24), (515, 2049, 1000), (4100, 5, 9)])
+def test_sizes(M, V, K, dtype):
+    x, w, t = make(M, V, K, dtype)
+    ref.check(run(x, w, t, 3.0), ref.xent(x, w, t, dloss=3.0))
+    with torch.no_grad():
+        ref.check({"loss": tl.linear_cross_entropy(x, w, t)}, ref.xent(x, w, t))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("reduction", ["none", "sum", "mean"])
+def test_reductions(reduction, dtype):
+    x, w, t = make(150, 700, 96, dtype, ignored=0.5)
+    g = torch.linspace(-2, 3, 150, device="cuda") if reduction == "none" else 0.3
+    ref.check(run(x, w, t, g, reduction), ref.xent(x, w, t, reduction=reduction, dloss=g))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size", [2.0 ** -30, 1e-6, 65536.0, 2.0 ** 40])
+def test_gradients_of_scaled_losses(size, dtype):
+    """The loss's own gradient may be of any size: results keep their digits as far as their type goes."""
+    x, w, t = make(70, 300, 64, dtype)
+    got, want = run(x, w, t, size), ref.xent(x, w, t, dloss=size)
+    for k in ("dx", "dw"):
+        top = torch.finfo(dtype).max
+        fits = want[k][0].abs() < top / 2
+        over = want[k][0].abs() > top * 2
+        assert ((got[k].double() - want[k][0]).abs() <= want[k][1])[fits].all() and got[k][over].isinf().all()
+
+
+def test_small_probabilities_in_float16():
+    """dw rows of unlikely words come from probabilities around 2^-23, below float16's normal numbers."""
+    K, V, M = 64, 2000, 90
+    x, w, t = make(M, V, K, torch.float16, ignored=0.0)
+    x[:, 0], w[:, 0] = 4.0, -4.0
+    w[0, 0] = 0.0
+    t[:] = 0
+    want = ref.xent(x, w, t, reduction="sum", dloss=1024.0)
+    got = run(x, w, t, 1024.0, "sum")
+    ref.check(got, want)
+    small = want["dw"][0][1:]
+    p = torch.softmax(x.double() @ w.double().t(), 1)[:, 1:]
+    assert p.max() < 2.0 ** -14 and p.median() < 2.0 ** -22
+    # the roundings of dz and of dw are 2^-11 of each value
+    assert (got["dw"].double()[1:] - small).norm() / small.norm() < 2e-3
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-3, 30.0, 300.0])
+def test_flat_and_peaked_rows(scale):
+    x, w, t = make(140, 600, 128, torch.bfloat16, scale=scale)
+    ref.check(run(x, w, t), ref.xent(x, w, t, dloss=1.0))
+
+
+def test_rows_that_do_not_count():
+    x, w, t = make(300, 500, 64, torch.bfloat16, ignored=0.6)
+    x[t == -100] = float("nan")  # whatever they hold
+    t[1] = -100
+    x[1] = float("inf")
+    got = run(x, w, t)
+    keep = t != -100
+    want = ref.xent(x[keep], w, t[keep], dloss=1.0)
+    ref.check({**got, "dx": got["dx"][keep]}, want)
+    assert not got["dx"][~keep].any()
+    clean = torch.where(keep[:, None], x, 1.0)
+    again = run(clean, w, t)
+    assert all(torch.equal(got[k], again[k]) for k in got)
+
+
+def test_no_row_counts():
+    x, w, t = make(40, 100, 32, torch.float16)
+    t[:] = -100
+    got = run(x, w, t)
+    assert got["loss"].isnan() and not got["dx"].any() and not got["dw"].any()
+    assert run(x, w, t, reduction="sum")["loss"] == 0 and not run(x, w, t, 1.0, "none")["loss"].any()
+
+
+@pytest.mark.parametrize("ignore", [0, 7, -1, 2 ** 40])
+def test_other_ignore_indices(ignore):
+    x, w, t = make(60, 90, 40, torch.bfloat16, ignored=0.0)
+    t[::3] = ignore
+    ref.check(run(x, w, t, ignore=ignore), ref.xent(x, w, t, ignore, dloss=1.0))
+
+
+@pytest.mark.parametrize("bad", [-1, 500, 2 ** 33, -2 ** 62])
+def test_targets_outside_the_vocabulary_make_nan(bad):
+    x, w, t = make(100, 500, 64, torch.bfloat16, ignored=0.1)
+    t[10] = bad
+    each = run(x, w, t, 1.0, "none")
+    rest = [i for i in range(100) if i != 10]
+    assert each["loss"][10].isnan() and each["loss"][rest].isfinite().all()
+    assert each["dx"][10].isnan().all() and each["dx"][rest].isfinite().all() and each["dw"].isnan().all()
+    assert run(x, w, t)["loss"].isnan()
+
+
+def test_logits_that_are_not_finite():
+    x, w, t = make(80, 200, 64, torch.bfloat16, ignored=0.0)
+    x[3, 0] = float("nan")
+    x[4, 0] = float("inf")
+    got = run(x, w, t, 1.0, "none")
+    rest = [i for i in range(80) if i not in (3, 4)]
+    assert got["loss"][3].isnan() and not got["loss"][4].isfinite()
+    ref.check({"loss": got["loss"][rest], "dx": got["dx"][rest]}, ref.xent(x[rest], w, t[rest], reduction="none", dloss=1.0), ("loss", "dx"))
+
+
+@pytest.mark.parametrize("M,V", [(0, 10), (5, 0), (0, 0)])
+def test_empty_sizes(M, V):
+    x, w, t = make(M, V, 16, torch.bfloat16)
+    t[:] = -100
+    got = run(x, w, t, reduction="sum")
+    assert got["loss"] == 0 and got["dx"].shape == x.shape and got["dw"].shape == w.shape
+    assert not got["dx"].any() and not got["dw"].any()
+    assert run(x, w, t, reduction="none")["loss"].shape == (M,)
+    x0, w0, t0 = make(6, 9, 0, torch.bfloat16)  # no features: every word as likely
+    ref.check(run(x0, w0, t0), ref.xent(x0, w0, t0, dloss=1.0))
+
+
+def test_gradients_against_differences():
+    x, w, t = make(7, 11, 6, torch.float16)
+    got, bounds = run(x, w, t), ref.xent(x, w, t, dloss=1.0)
+    wide = [x.double().cpu(), w.double().cpu()]
+    keep = (t != -100).cpu()
+
+    def value():
+        z = (wide[0] @ wide[1].t())[keep]
+        return float((torch.logsumexp(z, 1) - z.gather(1, t.cpu()[keep][:, None])[:, 0]).mean())
+
+    for name, v in zip(("dx", "dw"), wide):
+        flat = v.view(-1)
+        for i in range(flat.numel()):
+            old = flat[i].item()
+            flat[i] = old + 1e-5
+            up = value()
+            flat[i] = old - 1e-5
+            down = value()
+            flat[i] = old
+            assert abs(got[name].double().cpu().reshape(-1)[i].item() - (up - down) / 2e-5) <= bounds[name][1].cpu().reshape(-1)[i].item() + 1e-8
+
+
+def test_strides_axes_and_single_gradients():
+    x, w, t = make(60, 300, 70, torch.bfloat16)
+    wide = torch.full((300, 79), float("nan"), dtype=w.dtype, device="cuda")
+    wide[:, 3:73] = w
+    apart = torch.full((60, 75), float("nan"), dtype=w.dtype, device="cuda")
+    apart[:, 1:71] = x
+    want = run(x, w, t)
+    got = run(apart[:, 1:71], wide[:, 3:73], t)
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    got = run(x.view(3, 20, 70), w, t.view(3, 20))
+    assert torch.equal(got["loss"], want["loss"]) and torch.equal(got["dx"].view(60, 70), want["dx"])
+    got = run(x, w, torch.stack([t, t], 1)[:, 0])  # a target with a stride
+    assert torch.equal(got["dw"], want["dw"])
+    one = x.detach().requires_grad_()
+    assert torch.equal(torch.autograd.grad(tl.linear_cross_entropy(one, w, t), one)[0], want["dx"])
+    one = w.detach().requires_grad_()
+    assert torch.equal(torch.autograd.grad(tl.linear_cross_entropy(x, one, t), one)[0], want["dw"])
+    single = tl.linear_cross_entropy(x[0], w, t[0])
+    assert single.shape == () and torch.equal(single, tl.linear_cross_entropy(x[:1], w, t[:1]))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_several_pieces_of_the_vocabulary(dtype):
+    """More logits than one piece holds: dx is summed over pieces, the last of them partial."""
+    M, V, K = 33000, 20001, 24
+    x, w, t = make(M, V, K, dtype)
+    n = tl._xent_bytes(M, V, K, 3)[2]
+    assert n < 2 * M * V
+    got = run(x, w, t)
+    some = torch.arange(0, M, 97, device="cuda")
+    count = int((t != -100).sum())
+    want = ref.xent(x[some], w, t[some], reduction="sum", dloss=1.0 / count)
+    ref.check({"dx": got["dx"][some]}, want, ("dx",))
+    # dw: added up over blocks of rows
+    dw, bound = 0.0, 0.0
+    for rows in torch.arange(M, device="cuda").split(4096):
+        v, b = ref.xent(x[rows], w, t[rows], reduction="sum", dloss=1.0 / count)["dw"]
+        dw, bound = dw + v, bound + b
+    assert ((got["dw"].double() - dw).abs() <= bound + ref.U[dtype] * dw.abs()).all()
+    assert torch.equal(run(x, w, t)["dx"], got["dx"])
+
+
+def test_captured_and_replayed():
+    x, w, t = make(100, 1000, 64, torch.bfloat16)
+    x, w = x.requires_grad_(), w.requires_grad_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(tl.linear_cross_entropy(x, w, t), (x, w))
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        loss = tl.linear_cross_entropy(x, w, t)
+        out = (loss, *torch.autograd.grad(loss, (x, w)))
+    for seed in range(3):
+        nx, nw, nt = make(100, 1000, 64, torch.bfloat16, seed=50 + seed)
+        with torch.no_grad():
+            x.copy_(nx), w.copy_(nw), t.copy_(nt)
+        want = run(nx, nw, nt)
+        g.replay()
+        torch.cuda.synchronize()
+        for name, o in zip(("loss", "dx", "dw"), out):
+            assert torch.equal(o, want[name]), (seed, name)
+
+
+def test_streams_side_by_side():
+    cases = [make(M, 900, 128, torch.bfloat16, seed=M) for M in (1, 60, 400)]
+    want = [run(*c) for c in cases]
+    torch.cuda.synchronize()
+    got = []
+    for c in cases:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got.append(run(*c))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w[k], g[k]) for k in w)

@@ -6,7 +6,8 @@ library is opened on first use by :mod:`tiled_software_pipelined_amd.lib`,
 which raises if it is missing (there is no CPU fallback).
 """
 
-__all__ = ["gemm", "Plan", "Variant", "quantize_fp8", "gemm_fp8", "linear_fp8", "orthogonalize"]
+__all__ = ["gemm", "Plan", "Variant", "quantize_fp8", "gemm_fp8", "linear_fp8", "orthogonalize",
+           "gated_ffn", "linear_cross_entropy", "clip_grad_norm"]
 
 
 def __getattr__(name):

@@ -1,0 +1,221 @@
+// The gated feed-forward block, y = (act(x Wg^T) * (x Wu^T)) Wd^T, and its
+// gradients: what stands where in the caller's buffers, and the launches.
+//
+// Forward: gate and up projections in one kernel that ends with h; the down
+// projection.  Backward: dh = dy Wd in one that ends with dg, du and h made again
+// from the gate and up projections kept; dx = dg Wg + du Wu as one product; the
+// three weights' gradients in one launch.
+#include <climits>
+
+#include "tg_mm_host.hpp"
+
+namespace tg {
+
+struct FfnLayout {
+    int64_t g, u, h;         // forward: kept, or in scratch (h); -1: not there
+    bool h_kept;             // only the down projection's gradient is wanted
+    int64_t part;            // forward's scratch: the down projection's partial sums
+    int64_t dg, du, h2;      // backward's scratch
+    int64_t dx_part, dw_part[3];
+    bool rows;               // few tokens: the kernels that read each weight once
+    MmPlan gate, down, dh, dx, dw;
+    int64_t bytes[3];        // saved, forward's scratch, backward's scratch
+};
+
+static const int FFN_INNER = TGEMM_FFN_X | TGEMM_FFN_GATE | TGEMM_FFN_UP;
+
+static FfnLayout ffn_layout(int64_t M, int64_t K, int64_t F, int64_t N, int keep) {
+    FfnLayout l{};
+    auto take = [&](int which, int64_t n) {
+        const int64_t at = l.bytes[which];
+        l.bytes[which] += (n + 255) / 256 * 256;
+        return at;
+    };
+    l.rows = M <= 32;
+    const MmShape inner{M, F}, y{M, N}, dx{M, K}, dw[3] = {{F, K}, {F, K}, {N, F}};
+    l.gate = mm_plan(FORM_GATE, &inner, 1, mm_slices(K), false);
+    l.down = mm_plan(FORM_NT, &y, 1, mm_slices(F), true);
+    l.g = l.u = l.dg = l.du = l.h2 = -1;
+    l.h_kept = keep == TGEMM_FFN_DOWN;
+    if (keep & FFN_INNER) {
+        l.g = take(0, 2 * M * F);
+        l.u = take(0, 2 * M * F);
+    }
+    l.h = take(l.h_kept ? 0 : 1, 2 * M * F);
+    if (!l.rows) l.part = take(1, mm_part_bytes(l.down, M, N, false));
+    if (keep & FFN_INNER) {
+        l.dh = mm_plan(FORM_DH, &inner, 1, mm_slices(N), false);
+        if (keep & (TGEMM_FFN_X | TGEMM_FFN_GATE)) l.dg = take(2, 2 * M * F);
+        if (keep & (TGEMM_FFN_X | TGEMM_FFN_UP)) l.du = take(2, 2 * M * F);
+        if (keep & TGEMM_FFN_DOWN) l.h2 = take(2, 2 * M * F);
+    }
+    if (keep & TGEMM_FFN_X) {
+        l.dx = mm_plan(FORM_NN, &dx, 1, 2 * mm_slices(F), true);
+        l.dx_part = take(2, mm_part_bytes(l.dx, M, K, false));
+    }
+    MmShape wanted[3];
+    int n = 0;
+    for (int i = 0; i < 3; ++i)
+        if (keep & (TGEMM_FFN_GATE << i)) wanted[n++] = dw[i];
+    if (n > 0) {
+        l.dw = mm_plan(FORM_TN, wanted, n, mm_slices(M), true);
+        for (int i = 0; i < 3; ++i)
+            if (keep & (TGEMM_FFN_GATE << i)) l.dw_part[i] = take(2, mm_part_bytes(l.dw, dw[i].M, dw[i].N, false));
+    }
+    return l;
+}
+
+static bool ffn_sizes_ok(int64_t M, int64_t K, int64_t F, int64_t N, int32_t keep) {
+    if (M < 0 || K < 0 || F < 0 || N < 0 || M > MM_MOST_ROWS || K > MM_MOST || F > MM_MOST || N > MM_MOST || (keep & ~15)) {
+        set_error("M=%lld K=%lld F=%lld N=%lld keep=%d out of range", (long long)M, (long long)K, (long long)F, (long long)N, keep);
+        return false;
+    }
+    return true;
+}
+
+static int ffn_common(int32_t dtype, int32_t act) {
+    if (dtype != TGEMM_BF16 && dtype != TGEMM_F16) {
+        set_error("dtype %d is not bfloat16 or float16", dtype);
+        return TGEMM_E_ARG;
+    }
+    if (act < TGEMM_SILU || act > TGEMM_RELU) {
+        set_error("unknown activation %d", act);
+        return TGEMM_E_ARG;
+    }
+    return TGEMM_OK;
+}
+
+static MmOperands operands(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K) {
+    return MmOperands{static_cast<const char*>(a), static_cast<const char*>(b), nullptr, 2 * lda, 2 * ldb, 0,
+                      (int32_t)M, (int32_t)N, (int32_t)K};
+}
+
+template <bool PAIR>
+static const void* rows_kernel(int dtype, int64_t M) {
+    typedef void (*Fn)(MmRowsArgs);
+    const Fn fn = dtype == TGEMM_BF16 ? (M <= 16 ? (Fn)mm_rows_kernel<MmBf16, 1, 4, PAIR> : (Fn)mm_rows_kernel<MmBf16, 2, 2, PAIR>)
+                                      : (M <= 16 ? (Fn)mm_rows_kernel<MmF16, 1, 4, PAIR> : (Fn)mm_rows_kernel<MmF16, 2, 2, PAIR>);
+    return reinterpret_cast<const void*>(fn);
+}
+
+}  // namespace tg
+
+extern "C" {
+
+int tgemm_ffn_bytes(int64_t M, int64_t K, int64_t F, int64_t N, int32_t keep, int64_t* bytes) {
+    using namespace tg;
+    if (!bytes) {
+        set_error("NULL bytes");
+        return TGEMM_E_NULL;
+    }
+    if (!ffn_sizes_ok(M, K, F, N, keep)) return TGEMM_E_ARG;
+    const FfnLayout l = ffn_layout(M, K, F, N, keep);
+    for (int i = 0; i < 3; ++i) bytes[i] = l.bytes[i];
+    clear_error();
+    return TGEMM_OK;
+}
+
+int tgemm_ffn_forward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype, int32_t act, const void* x, int64_t ldx,
+                      const void* wg, int64_t ldg, const void* wu, int64_t ldu, const void* wd, int64_t ldd, void* y,
+                      int64_t ldy, int32_t keep, void* saved, void* scratch, void* stream) {
+    using namespace tg;
+    if (!ffn_sizes_ok(M, K, F, N, keep)) return TGEMM_E_ARG;
+    const FfnLayout l = ffn_layout(M, K, F, N, keep);
+    int rc = ffn_common(dtype, act);
+    if (rc == TGEMM_OK) rc = mm_check("x", x, M, K, ldx);
+    if (rc == TGEMM_OK) rc = mm_check("w_gate", wg, F, K, ldg);
+    if (rc == TGEMM_OK) rc = mm_check("w_up", wu, F, K, ldu);
+    if (rc == TGEMM_OK) rc = mm_check("w_down", wd, N, F, ldd);
+    if (rc == TGEMM_OK) rc = mm_check("y", y, M, N, ldy);
+    if (rc == TGEMM_OK) rc = mm_check_buffer("saved", saved, l.bytes[0]);
+    if (rc == TGEMM_OK) rc = mm_check_buffer("scratch", scratch, l.bytes[1]);
+    if (rc == TGEMM_OK && M > 0) rc = current_device_ok();
+    if (rc != TGEMM_OK) return rc;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    char* v = static_cast<char*>(saved);
+    char* s = static_cast<char*>(scratch);
+    char* h = (l.h_kept ? v : s) + l.h;
+    if (M > 0 && F > 0) {
+        MmOperands o = operands(x, ldx, wg, ldg, M, F, K);
+        o.b2 = static_cast<const char*>(wu);
+        o.ldb2 = 2 * ldu;
+        if (l.rows && l.g < 0) {
+            MmRowsArgs a{o, h, F, act};
+            rc = mm_launch(rows_kernel<true>(dtype, M), (F + 15) / 16, 512, &a, "gate and up projections", st);
+        } else {
+            const MmKernel& k = mm_kernels(dtype, FORM_GATE)[l.gate.size];
+            MmGateArgs a{o, mm_grid(k, l.gate, M, F), h, l.g < 0 ? nullptr : v + l.g, l.u < 0 ? nullptr : v + l.u, act};
+            rc = mm_launch(k.fn, (int64_t)a.grid.tiles_m * a.grid.tiles_n, k.threads, &a, "gate and up projections", st);
+        }
+    }
+    if (rc == TGEMM_OK && M > 0 && N > 0) {
+        if (l.rows) {
+            MmRowsArgs a{operands(h, F, wd, ldd, M, N, F), y, ldy, 0};
+            rc = mm_launch(rows_kernel<false>(dtype, M), (N + 15) / 16, 512, &a, "down projection", st);
+        } else {
+            MmStoreArgs a{};
+            a.jobs = 1;
+            a.job[0] = MmJob{{operands(h, F, wd, ldd, M, N, F), {}}, 1, {}, y, ldy,
+                             l.down.splits > 1 ? reinterpret_cast<float*>(s + l.part) : nullptr, 0};
+            rc = mm_store(dtype, FORM_NT, l.down, a, st);
+            if (rc == TGEMM_OK && l.down.splits > 1) rc = mm_join(dtype, l.down, a, st);
+        }
+    }
+    if (rc == TGEMM_OK) clear_error();
+    return rc;
+}
+
+int tgemm_ffn_backward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype, int32_t act, const void* x, int64_t ldx,
+                       const void* wg, int64_t ldg, const void* wu, int64_t ldu, const void* wd, int64_t ldd, const void* dy,
+                       int64_t lddy, int32_t keep, const void* saved, void* dx, int64_t lddx, void* dwg, int64_t lddwg,
+                       void* dwu, int64_t lddwu, void* dwd, int64_t lddwd, void* scratch, void* stream) {
+    using namespace tg;
+    if (!ffn_sizes_ok(M, K, F, N, keep)) return TGEMM_E_ARG;
+    const FfnLayout l = ffn_layout(M, K, F, N, keep);
+    int rc = ffn_common(dtype, act);
+    if (rc == TGEMM_OK) rc = mm_check("x", x, M, K, ldx);
+    if (rc == TGEMM_OK) rc = mm_check("w_gate", wg, F, K, ldg);
+    if (rc == TGEMM_OK) rc = mm_check("w_up", wu, F, K, ldu);
+    if (rc == TGEMM_OK) rc = mm_check("w_down", wd, N, F, ldd);
+    if (rc == TGEMM_OK) rc = mm_check("dy", dy, M, N, lddy);
+    if (rc == TGEMM_OK && (keep & TGEMM_FFN_X)) rc = mm_check("dx", dx, M, K, lddx);
+    if (rc == TGEMM_OK && (keep & TGEMM_FFN_GATE)) rc = mm_check("dw_gate", dwg, F, K, lddwg);
+    if (rc == TGEMM_OK && (keep & TGEMM_FFN_UP)) rc = mm_check("dw_up", dwu, F, K, lddwu);
+    if (rc == TGEMM_OK && (keep & TGEMM_FFN_DOWN)) rc = mm_check("dw_down", dwd, N, F, lddwd);
+    if (rc == TGEMM_OK) rc = mm_check_buffer("saved", saved, l.bytes[0]);
+    if (rc == TGEMM_OK) rc = mm_check_buffer("scratch", scratch, l.bytes[2]);
+    if (rc == TGEMM_OK && keep && (M > 0 || F > 0)) rc = current_device_ok();
+    if (rc != TGEMM_OK) return rc;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const char* v = static_cast<const char*>(saved);
+    char* s = static_cast<char*>(scratch);
+    auto in_scratch = [&](int64_t at) { return at < 0 ? nullptr : s + at; };
+    char *dg = in_scratch(l.dg), *du = in_scratch(l.du);
+    const char* h = l.h_kept ? v + l.h : in_scratch(l.h2);
+    if ((keep & FFN_INNER) && M > 0 && F > 0) {
+        const MmKernel& k = mm_kernels(dtype, FORM_DH)[l.dh.size];
+        MmDhArgs a{operands(dy, lddy, wd, ldd, M, F, N), mm_grid(k, l.dh, M, F), v + l.g, v + l.u, dg, du, in_scratch(l.h2), act};
+        rc = mm_launch(k.fn, (int64_t)a.grid.tiles_m * a.grid.tiles_n, k.threads, &a, "gradient of the inner values", st);
+    }
+    if (rc == TGEMM_OK && (keep & TGEMM_FFN_X)) {
+        MmStoreArgs a{};
+        a.jobs = 1;
+        a.job[0] = MmJob{{operands(dg, F, wg, ldg, M, K, F), operands(du, F, wu, ldu, M, K, F)}, 2, {}, dx, lddx,
+                         l.dx.splits > 1 ? reinterpret_cast<float*>(s + l.dx_part) : nullptr, 0};
+        rc = mm_store(dtype, FORM_NN, l.dx, a, st);
+        if (rc == TGEMM_OK && l.dx.splits > 1) rc = mm_join(dtype, l.dx, a, st);
+    }
+    if (rc == TGEMM_OK && (keep & (TGEMM_FFN_GATE | TGEMM_FFN_UP | TGEMM_FFN_DOWN))) {
+        MmStoreArgs a{};
+        auto part = [&](int i) { return l.dw.splits > 1 ? reinterpret_cast<float*>(s + l.dw_part[i]) : nullptr; };
+        if (keep & TGEMM_FFN_GATE) a.job[a.jobs++] = MmJob{{operands(dg, F, x, ldx, F, K, M), {}}, 1, {}, dwg, lddwg, part(0), 0};
+        if (keep & TGEMM_FFN_UP) a.job[a.jobs++] = MmJob{{operands(du, F, x, ldx, F, K, M), {}}, 1, {}, dwu, lddwu, part(1), 0};
+        if (keep & TGEMM_FFN_DOWN) a.job[a.jobs++] = MmJob{{operands(dy, lddy, h, F, N, F, M), {}}, 1, {}, dwd, lddwd, part(2), 0};
+        rc = mm_store(dtype, FORM_TN, l.dw, a, st);
+        if (rc == TGEMM_OK && l.dw.splits > 1) rc = mm_join(dtype, l.dw, a, st);
+    }
+    if (rc == TGEMM_OK) clear_error();
+    return rc;
+}
+
+}  // extern "C"

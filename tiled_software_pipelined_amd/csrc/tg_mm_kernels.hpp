@@ -1,0 +1,511 @@
+// Kernels on the 16-bit product tiles, one for each fused end, and the table
+// that the host picks from.
+#pragma once
+
+#include <climits>
+
+#include "tg_mm.hpp"
+
+namespace tg {
+
+// Workgroup rank -> (split of k, tile) of a job with this many tiles.
+struct MmGrid {
+    int32_t tiles_m, tiles_n, splits, per;  // per: slices of 64 k a split takes
+};
+
+// ---- products that are only stored -------------------------------------------
+// One C = alpha (a b^T [+ a' b'^T]); up to three of them share a launch.
+struct MmJob {
+    MmOperands op[2];
+    int32_t pairs;
+    MmGrid grid;
+    void* C;        // result, row stride ldc elements
+    int64_t ldc;
+    float* part;    // not NULL: float sums instead, split s at part + s M N
+    int32_t add;    // part: add to what is there
+};
+struct MmStoreArgs {
+    MmJob job[3];
+    int32_t jobs;
+    const float* alpha;  // NULL: one
+    // A number of rows that only the device knows (NULL: as the operands say): the
+    // first job's M, or its K (rows_are_k), up to what the operands say.
+    const int32_t* rows;
+    int32_t rows_are_k;
+    const int32_t* map;  // not NULL: row m of the result is row map[m] of C
+};
+
+// ---- gated feed-forward: gate and up projections ---------------------------------
+struct MmGateArgs {
+    MmOperands op;
+    MmGrid grid;
+    void *h, *g, *u;  // M x N, row stride N; g and u NULL where nothing is kept
+    int32_t act;
+};
+// ---- its backward: dh = dy Wd, then dg, du and h from it and g, u ----------------
+struct MmDhArgs {
+    MmOperands op;
+    MmGrid grid;
+    const void *g, *u;
+    void *dg, *du, *h;  // M x N, row stride N; any of them NULL where it is not wanted
+    int32_t act;
+};
+
+// ---- cross entropy ---------------------------------------------------------------
+// Rows of x are those that count, gathered; how many only the device knows.
+struct MmStatsArgs {
+    MmOperands op;
+    MmGrid grid;
+    const int32_t* rows;
+    const int32_t* map;     // their places in target
+    const int64_t* target;
+    float2* part;  // (max, sum of 2^((z - max) log2 e)) of each wave's columns: part[piece M + row]
+    float* hit;    // the target's logit of a row, where it has one
+};
+struct MmDzArgs {
+    MmOperands op;   // b: rows v0 .. of W
+    MmGrid grid;
+    const int32_t* rows;
+    const int32_t* map;
+    const int64_t* target;
+    int64_t v0;
+    const float* lse;
+    const float* coef;  // of each row
+    void* dz;           // M x N, row stride ldz elements
+    int64_t ldz;
+};
+
+// Activations and their derivatives, by the C ABI's numbers.
+enum MmAct { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_RELU = 3 };
+
+__device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(-1.44269504f * x); }
+
+// a = act(g), d = act'(g), 8 at a time (the choice of activation is outside).
+template <bool D>
+__device__ __forceinline__ void activate8(int act, const float (&g)[8], float (&a)[8], float (&d)[8]) {
+    switch (act) {
+        case ACT_SILU:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                // exp past float's range makes s zero
+                const float s = __builtin_amdgcn_rcpf(1.0f + exp_neg(g[e]));
+                a[e] = g[e] * s;
+                if (D) d[e] = s * (1.0f + g[e] * (1.0f - s));
+            }
+            break;
+        case ACT_GELU:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float p = 0.5f * erfcf(-0.70710678f * g[e]);  // erfc: small tails keep their digits
+                a[e] = g[e] * p;
+                if (D) d[e] = p + g[e] * 0.39894228f * exp_neg(0.5f * g[e] * g[e]);
+            }
+            break;
+        case ACT_GELU_TANH:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                // (1 + tanh t) / 2 = 1 / (1 + exp(-2 t))
+                const float g2 = g[e] * g[e];
+                const float s = __builtin_amdgcn_rcpf(1.0f + exp_neg(1.59576912f * g[e] * (1.0f + 0.044715f * g2)));
+                a[e] = g[e] * s;
+                if (D) d[e] = s * (1.0f + (1.0f - s) * 1.59576912f * g[e] * (1.0f + 0.134145f * g2));
+            }
+            break;
+        default:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                a[e] = g[e] > 0.0f ? g[e] : g[e] != g[e] ? g[e] : 0.0f;
+                if (D) d[e] = g[e] > 0.0f ? 1.0f : 0.0f;
+            }
+    }
+}
+
+// Where a workgroup's tile is, and its wave's block.
+template <class G>
+struct MmPlace {
+    int m0, n0, wm0, wn0, wave, lane, split;
+    __device__ __forceinline__ MmPlace(const MmGrid& g, int rank) {
+        wave = wave_id();
+        lane = lane_id();
+        const int tiles = g.tiles_m * g.tiles_n;
+        split = g.splits > 1 ? rank / tiles : 0;
+        int tm, tn;
+        grouped_tile(rank - split * tiles, g.tiles_m, g.tiles_n, 4, tm, tn);
+        m0 = tm * G::BM;
+        n0 = tn * G::TILE_N;
+        wm0 = (wave / G::WAVES_N) * G::WTM;
+        wn0 = (wave % G::WAVES_N) * G::WTN;
+    }
+    // first row and column of C of the wave's block
+    __device__ __forceinline__ int row0() const { return m0 + wm0; }
+    __device__ __forceinline__ int col0() const { return n0 + (wn0 / G::WTN) * G::WAVE_N; }
+};
+
+template <class G>
+__global__ __launch_bounds__(G::NT) void mm_store_kernel(MmStoreArgs g) {
+    __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
+    TG_LDS char* smem = (TG_LDS char*)smem_raw;
+    int which = 0, total = gridDim.x, M = g.job[0].op[0].M, most_k = INT_MAX;
+    MmGrid grid = g.job[0].grid;
+    if (g.rows) {
+        const int rows = *g.rows;
+        if (g.rows_are_k) {
+            most_k = rows;
+            grid.per = ((rows + 63) / 64 + grid.splits - 1) / grid.splits;
+        } else {
+            M = rows;
+            grid.tiles_m = (rows + G::BM - 1) / G::BM;
+            total = grid.tiles_m * grid.tiles_n * grid.splits;
+            if ((int)blockIdx.x >= total) return;
+        }
+    }
+    int rank = xcd_rank(blockIdx.x, total);
+    if (g.jobs > 1) {
+        for (; which + 1 < g.jobs; ++which) {
+            const MmGrid& r = g.job[which].grid;
+            const int n = r.tiles_m * r.tiles_n * r.splits;
+            if (rank < n) break;
+            rank -= n;
+        }
+        M = g.job[which].op[0].M;
+        grid = g.job[which].grid;
+    }
+    const MmJob& job = g.job[which];
+    const MmPlace<G> at(grid, rank);
+    typename G::Acc acc;
+    G::clear(acc);
+    int t0 = at.split * grid.per, t1 = t0 + grid.per;
+    for (int p = 0; p < job.pairs; ++p) {
+        MmOperands op = job.op[p];
+        op.M = M;
+        op.K = min(op.K, most_k);
+        const int slices = (op.K + 63) / 64;
+        if (t0 < slices && t1 > 0)
+            G::product(op, at.m0, at.n0, max(t0, 0), min(t1, slices), smem, acc, at.wm0, at.wn0, at.lane, at.wave);
+        t0 -= slices;
+        t1 -= slices;
+    }
+    const int N = job.op[0].N, m1 = at.row0(), n1 = at.col0();
+    if (job.part) {
+        float* part = job.part + (int64_t)at.split * job.op[0].M * N;
+        const bool add = job.add != 0;
+        G::each_row(acc, smem, at.lane, at.wave, [&](int r, int c, float (&v)[8], float (&)[8]) {
+            const int m = m1 + r, n = n1 + c;
+            if (m >= M || n >= N) return;
+            float* dst = part + (int64_t)m * N + n;
+            if (n + 8 <= N) {
+                if (add) {
+                    float o[8];
+                    __builtin_memcpy(o, dst, 32);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] += o[e];
+                }
+                __builtin_memcpy(dst, v, 32);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 7; ++e)
+                    if (n + e < N) dst[e] = add ? dst[e] + v[e] : v[e];
+            }
+        });
+    } else {
+        typedef typename G::T T;
+        const float alpha = g.alpha ? *g.alpha : 1.0f;
+        T* C = static_cast<T*>(job.C);
+        const int64_t ldc = job.ldc;
+        G::each_row(acc, smem, at.lane, at.wave, [&](int r, int c, float (&v)[8], float (&)[8]) {
+            const int m = m1 + r, n = n1 + c;
+            if (m >= M || n >= N) return;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= alpha;
+            store8(C + (g.map ? g.map[m] : m) * ldc + n, v, N - n);
+        });
+    }
+}
+
+template <class G>
+__global__ __launch_bounds__(G::NT) void mm_gate_kernel(MmGateArgs g) {
+    __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
+    TG_LDS char* smem = (TG_LDS char*)smem_raw;
+    typedef typename G::T T;
+    const MmPlace<G> at(g.grid, xcd_rank(blockIdx.x, gridDim.x));
+    typename G::Acc acc;
+    G::clear(acc);
+    G::product(g.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, smem, acc, at.wm0, at.wn0, at.lane, at.wave);
+    const int M = g.op.M, N = g.op.N, m1 = at.row0(), n1 = at.col0();
+    G::each_row(acc, smem, at.lane, at.wave, [&](int r, int c, float (&v)[8], float (&w)[8]) {
+        const int m = m1 + r, n = n1 + c;
+        if (m >= M || n >= N) return;
+        const int64_t to = (int64_t)m * N + n;
+        if (g.g) {
+            store8(static_cast<T*>(g.g) + to, v, N - n);
+            store8(static_cast<T*>(g.u) + to, w, N - n);
+        }
+        float a[8], d[8];
+        activate8<false>(g.act, v, a, d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] *= w[e];
+        // h's rounding: the down projection's operand
+        store8(static_cast<T*>(g.h) + to, a, N - n);
+    });
+}
+
+template <class G>
+__global__ __launch_bounds__(G::NT) void mm_dh_kernel(MmDhArgs g) {
+    __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
+    TG_LDS char* smem = (TG_LDS char*)smem_raw;
+    typedef typename G::T T;
+    const MmPlace<G> at(g.grid, xcd_rank(blockIdx.x, gridDim.x));
+    typename G::Acc acc;
+    G::clear(acc);
+    G::product(g.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, smem, acc, at.wm0, at.wn0, at.lane, at.wave);
+    const int M = g.op.M, N = g.op.N, m1 = at.row0(), n1 = at.col0();
+    G::each_row(acc, smem, at.lane, at.wave, [&](int r, int c, float (&v)[8], float (&)[8]) {
+        const int m = m1 + r, n = n1 + c, count = N - n;
+        if (m >= M || n >= N) return;
+        const int64_t to = (int64_t)m * N + n;
+        float gate[8], up[8], a[8], d[8], o[8];
+        load8(gate, static_cast<const T*>(g.g) + to, count);
+        load8(up, static_cast<const T*>(g.u) + to, count);
+        activate8<true>(g.act, gate, a, d);
+        // roundings of dg, du, h: operands of the products that follow
+        if (g.dg) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = v[e] * up[e] * d[e];
+            store8(static_cast<T*>(g.dg) + to, o, count);
+        }
+        if (g.du) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = v[e] * a[e];
+            store8(static_cast<T*>(g.du) + to, o, count);
+        }
+        if (g.h) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = a[e] * up[e];
+            store8(static_cast<T*>(g.h) + to, o, count);
+        }
+    });
+}
+
+constexpr float LOG2E = 1.44269504f;
+
+// A product with as many rows as the device says.
+template <class G>
+struct MmKnown {
+    MmOperands op;
+    MmGrid grid;
+    int total;
+    __device__ __forceinline__ MmKnown(const MmOperands& o, const MmGrid& r, const int32_t* rows) : op(o), grid(r) {
+        op.M = *rows;
+        grid.tiles_m = (op.M + G::BM - 1) / G::BM;
+        total = grid.tiles_m * grid.tiles_n;
+    }
+};
+
+// The piece of the softmax that a wave's columns make: for each row their
+// maximum and the sum of the powers above it.  A row is in lanes l and l + 32.
+template <class G>
+__global__ __launch_bounds__(G::NT) void mm_stats_kernel(MmStatsArgs g) {
+    __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
+    const MmKnown<G> known(g.op, g.grid, g.rows);
+    if ((int)blockIdx.x >= known.total) return;
+    const MmPlace<G> at(known.grid, xcd_rank(blockIdx.x, known.total));
+    typename G::Acc acc;
+    G::clear(acc);
+    G::product(known.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, (TG_LDS char*)smem_raw, acc, at.wm0, at.wn0, at.lane, at.wave);
+    const int M = known.op.M, N = g.op.N, n1 = at.col0(), half = 4 * (at.lane >> 5);
+    if (n1 >= N) return;                // wave-uniform, as is the next
+    const bool edge = n1 + G::WTN > N;
+    float2* part = g.part + (int64_t)(n1 / G::WTN) * g.op.M;
+#pragma unroll
+    for (int i = 0; i < G::FM; ++i) {
+        const int m = at.row0() + 32 * i + (at.lane & 31);
+        if (edge) {
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (n1 + 32 * j + 8 * (r >> 2) + half + (r & 3) >= N) acc[i][j][r] = -INFINITY;
+        }
+        float most = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) most = fmaxf(most, acc[i][j][r]);
+        most = fmaxf(most, __shfl_xor(most, 32));
+        const float base = most == -INFINITY ? 0.0f : most;  // nothing here, or nothing but -inf
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f((acc[i][j][r] - base) * LOG2E);
+        sum += __shfl_xor(sum, 32);
+        if (at.lane < 32 && m < M) part[m] = float2{most, sum};
+        const int64_t t = (m < M ? g.target[g.map[m]] : -1) - n1;
+        const int want = t >= 0 && t < G::WTN ? (int)t : -1;
+        if (__any(want >= 0)) {
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (32 * j + 8 * (r >> 2) + half + (r & 3) == want) g.hit[m] = acc[i][j][r];
+        }
+    }
+}
+
+// dz = coef (softmax - [target]), rounded: the operand of the products for dx
+// and dw.
+template <class G>
+__global__ __launch_bounds__(G::NT) void mm_dz_kernel(MmDzArgs g) {
+    __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
+    TG_LDS char* smem = (TG_LDS char*)smem_raw;
+    typedef typename G::T T;
+    const MmKnown<G> known(g.op, g.grid, g.rows);
+    if ((int)blockIdx.x >= known.total) return;
+    const MmPlace<G> at(known.grid, xcd_rank(blockIdx.x, known.total));
+    typename G::Acc acc;
+    G::clear(acc);
+    G::product(known.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, smem, acc, at.wm0, at.wn0, at.lane, at.wave);
+    const int M = known.op.M, N = g.op.N, m1 = at.row0(), n1 = at.col0(), half = 4 * (at.lane >> 5);
+#pragma unroll
+    for (int i = 0; i < G::FM; ++i) {
+        const int m = m1 + 32 * i + (at.lane & 31);
+        const float coef = m < M ? g.coef[m] : 0.0f, lse = m < M ? g.lse[m] : 0.0f;
+        const int64_t t = (m < M ? g.target[g.map[m]] - g.v0 : -1) - n1;
+        const int want = t >= 0 && t < G::WTN ? (int)t : -1;
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                float p = __builtin_amdgcn_exp2f((acc[i][j][r] - lse) * LOG2E);
+                if (32 * j + 8 * (r >> 2) + half + (r & 3) == want) p -= 1.0f;
+                acc[i][j][r] = p * coef;
+            }
+    }
+    T* dz = static_cast<T*>(g.dz);
+    G::each_row(acc, smem, at.lane, at.wave, [&](int r, int c, float (&v)[8], float (&)[8]) {
+        const int m = m1 + r, n = n1 + c;
+        if (m < M && n < N) store8(dz + m * g.ldz + n, v, N - n);
+    });
+}
+
+// ---- few rows of A -----------------------------------------------------------
+// A served batch of up to 32 tokens is bound by one read of the weights.  A
+// workgroup takes 16 rows of B (PAIR: of both matrices) and all rows of A; its
+// eight waves deal blocks of 64 k among them, operands going straight to
+// registers, and add their sums through LDS.  v_mfma_f32_16x16x32: lane l
+// holds row l % 16, k 8 (l / 16) .. + 7 of 32; of a block's 128 bytes of a row it
+// reads chunks l / 16 and 4 + l / 16, so one load reads 64 adjacent bytes of
+// each of 16 rows.
+struct MmRowsArgs {
+    MmOperands op;
+    void* C;  // M x N, row stride ldc elements
+    int64_t ldc;
+    int32_t act;
+};
+
+template <class Tr, int MT, int U, bool PAIR>
+__global__ __launch_bounds__(512) void mm_rows_kernel(MmRowsArgs g) {
+    constexpr int NW = 8, NB = PAIR ? 2 : 1;
+    __shared__ float part[NW][NB * MT * 256];
+    typedef typename Tr::T T;
+    const MmOperands& o = g.op;
+    const int lane = lane_id(), wave = wave_id();
+    const int n0 = blockIdx.x * 16;
+    const int blocks = (o.K + 63) / 64, bytes = o.K * 2, at = (lane >> 4) * 16;
+    const char* brow[NB];
+    brow[0] = o.b + (int64_t)min(n0 + (lane & 15), o.N - 1) * o.ldb;
+    if constexpr (PAIR) brow[1] = o.b2 + (int64_t)min(n0 + (lane & 15), o.N - 1) * o.ldb2;
+    const char* arow[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) arow[t] = o.a + (int64_t)min(16 * t + (lane & 15), o.M - 1) * o.lda;
+    f32x4 acc[NB][MT];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[b][t] = f32x4{0, 0, 0, 0};
+    struct Block {
+        i32x4 b[NB][2], a[MT][2];
+    };
+    auto load = [&](Block& x, int kb) {
+        const int64_t k0 = (int64_t)kb * 128 + at;
+        if ((kb + 1) * 64 <= o.K) {  // wave-uniform
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) x.b[b][h] = load16(brow[b] + k0 + 64 * h);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) x.a[t][h] = load16(arow[t] + k0 + 64 * h);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) x.b[b][h] = row_end_chunk(brow[b], (int)k0 + 64 * h, bytes);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) x.a[t][h] = row_end_chunk(arow[t], (int)k0 + 64 * h, bytes);
+            }
+        }
+    };
+    auto multiply = [&](const Block& x) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) acc[b][t] = Tr::mma16(x.a[t][h], x.b[b][h], acc[b][t]);
+    };
+    int kb = wave;
+    for (; kb + (U - 1) * NW < blocks; kb += U * NW) {
+        Block x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) load(x[u], kb + u * NW);
+#pragma unroll
+        for (int u = 0; u < U; ++u) multiply(x[u]);
+    }
+    for (; kb < blocks; kb += NW) {
+        Block x;
+        load(x, kb);
+        multiply(x);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                part[wave][(b * MT + t) * 256 + (4 * (lane >> 4) + r) * 16 + (lane & 15)] = acc[b][t][r];
+    __syncthreads();
+    for (int e = threadIdx.x; e < MT * 256; e += 512) {
+        float v[8] = {}, w[8] = {}, a[8], d[8];
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+            v[0] += part[k][e];
+            if constexpr (PAIR) w[0] += part[k][MT * 256 + e];
+        }
+        if constexpr (PAIR) {
+            activate8<false>(g.act, v, a, d);
+            v[0] = a[0] * w[0];
+        }
+        const int m = e >> 4, n = n0 + (e & 15);
+        if (m < o.M && n < o.N) static_cast<T*>(g.C)[m * g.ldc + n] = (T)v[0];
+    }
+}
+
+// ---- the table ---------------------------------------------------------------
+enum MmForm { FORM_NT = 0, FORM_NN, FORM_TN, FORM_GATE, FORM_DH, FORM_STATS, FORM_DZ, FORM_COUNT };
+enum MmSize { SIZE_256 = 0, SIZE_128, SIZE_64, SIZE_COUNT };
+struct MmKernel {
+    const void* fn;
+    int bm, bn, threads;  // rows and columns of C a workgroup takes
+};
+
+// The tiles.  256 x 256: four waves of 128 x 128, one a SIMD.  128 x 128: four
+// waves, two workgroups a compute unit.  64 x 128: likewise.
+template <class Tr, int LA, int LB, bool PAIR>
+struct MmTiles {
+    typedef MmTile<Tr, LA, LB, 256, 256, 2, 2, 2, false, PAIR> T256;
+    typedef MmTile<Tr, LA, LB, 128, 128, 2, 2, 2, false, PAIR> T128;
+    typedef MmTile<Tr, LA, LB, 64, 128, 2, 2, 3, true, PAIR> T64;
+};
+
+}  // namespace tg

@@ -1,0 +1,441 @@
+// Softmax cross entropy of a linear layer's logits z = x W^T, which are never
+// stored: loss = log sum exp z - z[target].
+//
+// Rows that do not count (a prompt's tokens, padding) are left out of every
+// product: the rows of x that count are gathered (and stand on 128-byte lines
+// then), their number stays on the device, and workgroups past it end at once.
+//
+// Forward: the product's kernel ends with the maximum and the sum of powers of
+// each wave's 64 or 128 columns; a second one joins them to lse, the logarithm of the
+// row's sum, and the row's loss.  Backward: pieces of the vocabulary, for each the
+// product again, ended by dz = coef (exp(z - lse) - [target]), and the two
+// products that take it, dx += dz W and dW = dz^T x.
+#include <climits>
+
+#include "tg_mm_host.hpp"
+
+namespace tg {
+
+// Elements of dz that are held at once: 512 MB.  Fewer and larger pieces read and
+// write dx's float sums less often.
+constexpr int64_t XENT_PIECE = INT64_C(1) << 28;
+
+struct XentLayout {
+    MmPlan stats, dz, dx, dw;
+    int64_t parts;             // pieces of a row that the forward pass joins
+    int64_t ldx;               // row stride of the gathered rows of x
+    int64_t cols, ldz;         // backward: columns of a piece, row stride of dz
+    int64_t count, map, rank, lse;                  // kept
+    int64_t x, hit, each, part;                     // forward's scratch
+    int64_t x2, coef, alpha, dzs, dx_part, dw_part; // backward's
+    int64_t bytes[3];
+};
+
+static int wave_cols(MmSize s) { return s == SIZE_256 ? 128 : 64; }
+
+static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
+    XentLayout l{};
+    auto take = [&](int which, int64_t n) {
+        const int64_t at = l.bytes[which];
+        l.bytes[which] += (n + 255) / 256 * 256;
+        return at;
+    };
+    l.count = take(0, 4);  // how many rows count
+    l.map = take(0, 4 * M);   // where they stand
+    l.rank = take(0, 4 * M);  // each row's number among them, -1
+    l.lse = take(0, 4 * M);   // of each of them
+    const MmShape z{M, V};
+    l.ldx = (K + 63) / 64 * 64;
+    l.stats = mm_plan(FORM_STATS, &z, 1, mm_slices(K), false);
+    l.parts = (V + wave_cols(l.stats.size) - 1) / wave_cols(l.stats.size);
+    l.x = take(1, 2 * M * l.ldx);
+    l.hit = take(1, 4 * M);   // the target's logit of each of them
+    l.each = take(1, 4 * M);  // each row's loss
+    l.part = take(1, 8 * M * l.parts);
+    if (!keep) return l;
+    // at least 8192 columns: dz is then four times as wide as x often is
+    const int64_t fit = M > 0 ? XENT_PIECE / M : V;
+    const int64_t most = fit < 8192 ? 8192 : fit;
+    const int64_t pieces = V > 0 ? (V + most - 1) / most : 1;
+    l.cols = ((V + pieces - 1) / pieces + 255) / 256 * 256;
+    if (l.cols < 256) l.cols = 256;  // of an empty vocabulary too: the walk over pieces ends
+    l.ldz = l.cols;
+    const int64_t cols = l.cols < V ? l.cols : V;
+    const MmShape piece{M, cols}, dx{M, K}, dw{cols, K};
+    l.dz = mm_plan(FORM_DZ, &piece, 1, mm_slices(K), false);
+    l.x2 = take(2, 2 * M * l.ldx);
+    l.coef = take(2, 4 * M);
+    l.alpha = take(2, 4);
+    l.dzs = take(2, 2 * M * l.ldz);
+    if (keep & TGEMM_KEEP_X) {
+        l.dx = mm_plan(FORM_NN, &dx, 1, mm_slices(cols), true);
+        l.dx_part = take(2, mm_part_bytes(l.dx, M, K, pieces > 1));
+    }
+    if (keep & TGEMM_KEEP_W) {
+        l.dw = mm_plan(FORM_TN, &dw, 1, mm_slices(M), true);
+        l.dw_part = take(2, mm_part_bytes(l.dw, cols, K, false));
+    }
+    return l;
+}
+
+static bool xent_sizes_ok(int64_t M, int64_t V, int64_t K, int32_t keep) {
+    if (M < 0 || V < 0 || K < 0 || M > MM_MOST_ROWS || V > MM_MOST_ROWS || K > MM_MOST || (keep & ~3)) {
+        set_error("M=%lld V=%lld K=%lld keep=%d out of range", (long long)M, (long long)V, (long long)K, keep);
+        return false;
+    }
+    return true;
+}
+
+static int xent_common(int32_t dtype, int32_t reduction, const void* target, int64_t M) {
+    if (dtype != TGEMM_BF16 && dtype != TGEMM_F16) {
+        set_error("dtype %d is not bfloat16 or float16", dtype);
+        return TGEMM_E_ARG;
+    }
+    if (reduction < TGEMM_NONE || reduction > TGEMM_MEAN) {
+        set_error("unknown reduction %d", reduction);
+        return TGEMM_E_ARG;
+    }
+    if (M > 0 && !target) {
+        set_error("target: NULL pointer");
+        return TGEMM_E_NULL;
+    }
+    if ((uintptr_t)target % 8) {
+        set_error("target: not aligned to its element size");
+        return TGEMM_E_ALIGN;
+    }
+    return TGEMM_OK;
+}
+static int check_floats(const char* name, const void* p, int64_t count) {
+    if (count > 0 && !p) {
+        set_error("%s: NULL pointer", name);
+        return TGEMM_E_NULL;
+    }
+    if ((uintptr_t)p % 4) {
+        set_error("%s: not aligned to its element size", name);
+        return TGEMM_E_ALIGN;
+    }
+    return TGEMM_OK;
+}
+
+// ---- the rows that count -------------------------------------------------------
+struct ScanArgs {
+    int64_t M, ignore;
+    const int64_t* target;
+    int32_t *count, *map, *rank;
+};
+
+// One workgroup: each wave takes a run of rows, counts its own, and after the
+// waves' counts are added gives them their numbers.
+__global__ __launch_bounds__(1024) void xent_scan_kernel(ScanArgs g) {
+    __shared__ int held[16];
+    const int lane = lane_id(), wave = wave_id();
+    const int64_t run = ((g.M + 15) / 16 + 63) / 64 * 64, begin = run * wave, end = min(begin + run, g.M);
+    int n = 0;
+    for (int64_t m = begin + lane; m < end; m += 64) n += g.target[m] != g.ignore;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d);
+    if (lane == 0) held[wave] = n;
+    __syncthreads();
+    int at = 0, total = 0;
+    for (int w = 0; w < 16; ++w) {
+        if (w < wave) at += held[w];
+        total += held[w];
+    }
+    if (threadIdx.x == 0) *g.count = total;
+    for (int64_t m0 = begin; m0 < end; m0 += 64) {
+        const int64_t m = m0 + lane;
+        const bool counts = m < end && g.target[m] != g.ignore;
+        const uint64_t mask = __ballot(counts);
+        const int mine = at + __popcll(mask & ((uint64_t(1) << lane) - 1));
+        if (m < end) g.rank[m] = counts ? mine : -1;
+        if (counts) g.map[mine] = (int32_t)m;
+        at += __popcll(mask);
+    }
+}
+
+struct GatherArgs {
+    int64_t M, K, ldx, ldto, lddx;
+    const uint16_t* x;
+    const int32_t* rank;
+    uint16_t* to;
+    float* loss;   // not NULL: zero for rows that do not count
+    uint16_t* dx;  // likewise
+};
+
+// A wave a row.
+__global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
+    const int lane = lane_id();
+    const int64_t m = (int64_t)blockIdx.x * 4 + wave_id();
+    if (m >= g.M) return;
+    const int r = g.rank[m];
+    if (r < 0) {
+        if (g.loss && lane == 0) g.loss[m] = 0.0f;
+        if (g.dx) {
+            uint16_t* dst = g.dx + m * g.lddx;
+            const i32x4 zero{0, 0, 0, 0};
+            for (int64_t k = 8 * lane; k < g.K; k += 512) {
+                if (k + 8 <= g.K) __builtin_memcpy(dst + k, &zero, 16);
+                else
+                    for (int64_t e = k; e < g.K; ++e) dst[e] = 0;
+            }
+        }
+        return;
+    }
+    const uint16_t* src = g.x + m * g.ldx;
+    uint16_t* dst = g.to + r * g.ldto;  // rows of whole lines
+    for (int64_t k = 8 * lane; k < g.K; k += 512) {
+        i32x4 v;
+        if (k + 8 <= g.K) {
+            v = load16(src + k);
+        } else {
+            union { i32x4 v; uint16_t e[8]; } u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u.e[e] = load_or_zero(src + k + e, k + e < g.K);
+            v = u.v;
+        }
+        *reinterpret_cast<i32x4*>(dst + k) = v;
+    }
+}
+
+// ---- the loss ------------------------------------------------------------------
+struct RowsArgs {
+    int64_t M, V, parts;
+    const int32_t *count, *map;
+    const int64_t* target;
+    const float2* part;
+    const float* hit;
+    float *lse, *loss;  // lse of each row that counts, loss of each row
+};
+
+// 16 rows a workgroup, 32 threads a row.
+__global__ __launch_bounds__(512) void xent_rows_kernel(RowsArgs g) {
+    __shared__ float2 held[32][16];
+    const int r = threadIdx.x & 15, y = threadIdx.x >> 4;
+    const int64_t m = (int64_t)blockIdx.x * 16 + r;
+    const int M = *g.count;
+    float most = -INFINITY, sum = 0.0f;
+    auto join = [&](float2 p) {
+        // NaN sums come through; pieces of nothing but -inf add nothing
+        const float to = fmaxf(most, p.x), base = to == -INFINITY ? 0.0f : to;
+        sum = sum * expf(most - base) + p.y * expf(p.x - base);
+        most = to;
+    };
+    if (m < M) {
+        int64_t p = y;
+        for (; p + 96 < g.parts; p += 128) {
+            float2 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = g.part[(p + 32 * u) * g.M + m];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) join(v[u]);
+        }
+        for (; p < g.parts; p += 32) join(g.part[p * g.M + m]);
+    }
+    held[y][r] = float2{most, sum};
+    __syncthreads();
+    if (y != 0 || m >= M) return;
+    for (int k = 1; k < 32; ++k) join(held[k][r]);
+    const float lse = most + logf(sum);
+    g.lse[m] = lse;
+    const int to = g.map[m];
+    const int64_t t = g.target[to];
+    // a target outside the vocabulary has no logit: its loss is NaN
+    g.loss[to] = t >= 0 && t < g.V ? lse - g.hit[m] : NAN;
+}
+
+struct ReduceArgs {
+    const int32_t *count, *map;
+    const float* rows;
+    float* loss;
+    int32_t mean;
+};
+
+__global__ __launch_bounds__(1024) void xent_reduce_kernel(ReduceArgs g) {
+    __shared__ double held[16];
+    const int M = *g.count;
+    double sum = 0.0;
+    for (int m = threadIdx.x; m < M; m += 1024) sum += g.rows[g.map[m]];
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    if ((threadIdx.x & 63) == 0) held[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < 16; ++w) sum += held[w];
+    *g.loss = (float)(g.mean ? sum / M : sum);
+}
+
+struct CoefArgs {
+    int64_t V;
+    const int32_t *count, *map;
+    const int64_t* target;
+    const float* dloss;
+    float *coef, *alpha;
+    int32_t reduction;
+};
+
+// The factor of each row's dz and the products' factor alpha.  Rows' factors are
+// brought near 2^15 by a power of two, which alpha takes out again: dz holds
+// values from 2^15 down, where float16 keeps 11 bits to 2^-14 (probabilities of
+// 2^-29), whatever the loss was scaled by.
+__global__ __launch_bounds__(1024) void xent_coef_kernel(CoefArgs g) {
+    __shared__ float held[16];
+    const int M = *g.count;
+    const float scalar = g.reduction == TGEMM_NONE ? 0.0f : g.reduction == TGEMM_MEAN ? *g.dloss / (float)M : *g.dloss;
+    auto of = [&](int m) {
+        const int to = g.map[m];
+        const int64_t t = g.target[to];
+        if (t < 0 || t >= g.V) return NAN;
+        return g.reduction == TGEMM_NONE ? g.dloss[to] : scalar;
+    };
+    float most = 0.0f;  // of the finite ones
+    for (int m = threadIdx.x; m < M; m += 1024) {
+        const float a = fabsf(of(m));
+        if (a < INFINITY) most = fmaxf(most, a);
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor(most, d));
+    if ((threadIdx.x & 63) == 0) held[threadIdx.x >> 6] = most;
+    __syncthreads();
+    for (int w = 0; w < 16; ++w) most = fmaxf(most, held[w]);
+    int e = most > 0.0f ? 14 - ilogbf(most) : 0;
+    e = e < -100 ? -100 : e > 100 ? 100 : e;
+    for (int m = threadIdx.x; m < M; m += 1024) g.coef[m] = ldexpf(of(m), e);
+    if (threadIdx.x == 0) *g.alpha = ldexpf(1.0f, -e);
+}
+
+static int gather(const void* x, int64_t ldx, int64_t M, int64_t K, const int32_t* rank, void* to, int64_t ldto, float* loss,
+                  void* dx, int64_t lddx, hipStream_t st) {
+    GatherArgs a{M, K, ldx, ldto, lddx, static_cast<const uint16_t*>(x), rank, static_cast<uint16_t*>(to), loss,
+                 static_cast<uint16_t*>(dx)};
+    return mm_launch(reinterpret_cast<const void*>(xent_gather_kernel), (M + 3) / 4, 256, &a, "rows that count", st);
+}
+
+}  // namespace tg
+
+extern "C" {
+
+int tgemm_xent_bytes(int64_t M, int64_t V, int64_t K, int32_t keep, int64_t* bytes) {
+    using namespace tg;
+    if (!bytes) {
+        set_error("NULL bytes");
+        return TGEMM_E_NULL;
+    }
+    if (!xent_sizes_ok(M, V, K, keep)) return TGEMM_E_ARG;
+    const XentLayout l = xent_layout(M, V, K, keep);
+    for (int i = 0; i < 3; ++i) bytes[i] = l.bytes[i];
+    clear_error();
+    return TGEMM_OK;
+}
+
+int tgemm_xent_forward(int64_t M, int64_t V, int64_t K, int32_t dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                       const int64_t* target, int64_t ignore, int32_t reduction, float* loss, void* saved, void* scratch,
+                       void* stream) {
+    using namespace tg;
+    if (!xent_sizes_ok(M, V, K, 0)) return TGEMM_E_ARG;
+    const XentLayout l = xent_layout(M, V, K, 0);
+    int rc = xent_common(dtype, reduction, target, M);
+    if (rc == TGEMM_OK) rc = mm_check("x", x, M, K, ldx);
+    if (rc == TGEMM_OK) rc = mm_check("w", w, V, K, ldw);
+    if (rc == TGEMM_OK) rc = check_floats("loss", loss, reduction == TGEMM_NONE ? M : 1);
+    if (rc == TGEMM_OK) rc = mm_check_buffer("saved", saved, l.bytes[0]);
+    if (rc == TGEMM_OK) rc = mm_check_buffer("scratch", scratch, l.bytes[1]);
+    if (rc == TGEMM_OK) rc = current_device_ok();
+    if (rc != TGEMM_OK) return rc;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    char *v = static_cast<char*>(saved), *s = static_cast<char*>(scratch);
+    int32_t *count = reinterpret_cast<int32_t*>(v + l.count), *map = reinterpret_cast<int32_t*>(v + l.map),
+            *rank = reinterpret_cast<int32_t*>(v + l.rank);
+    float *hit = reinterpret_cast<float*>(s + l.hit), *lse = reinterpret_cast<float*>(v + l.lse);
+    float2* part = reinterpret_cast<float2*>(s + l.part);
+    float* each = reduction == TGEMM_NONE ? loss : reinterpret_cast<float*>(s + l.each);
+    ScanArgs c{M, ignore, target, count, map, rank};
+    rc = mm_launch(reinterpret_cast<const void*>(xent_scan_kernel), 1, 1024, &c, "rows that count", st);
+    if (rc == TGEMM_OK && M > 0)
+        rc = gather(x, ldx, M, K, rank, s + l.x, l.ldx, reduction == TGEMM_NONE ? loss : nullptr, nullptr, 0, st);
+    if (rc == TGEMM_OK && M > 0 && V > 0) {
+        const MmKernel& k = mm_kernels(dtype, FORM_STATS)[l.stats.size];
+        MmStatsArgs a{MmOperands{s + l.x, static_cast<const char*>(w), nullptr, 2 * l.ldx, 2 * ldw, 0, (int32_t)M, (int32_t)V,
+                                 (int32_t)K},
+                      mm_grid(k, l.stats, M, V), count, map, target, part, hit};
+        rc = mm_launch(k.fn, (int64_t)a.grid.tiles_m * a.grid.tiles_n, k.threads, &a, "logits", st);
+    }
+    if (rc == TGEMM_OK && M > 0) {
+        RowsArgs a{M, V, V > 0 ? l.parts : 0, count, map, target, part, hit, lse, each};
+        rc = mm_launch(reinterpret_cast<const void*>(xent_rows_kernel), (M + 15) / 16, 512, &a, "rows of the loss", st);
+    }
+    if (rc == TGEMM_OK && reduction != TGEMM_NONE) {
+        ReduceArgs a{count, map, each, loss, reduction == TGEMM_MEAN};
+        rc = mm_launch(reinterpret_cast<const void*>(xent_reduce_kernel), 1, 1024, &a, "sum of the loss", st);
+    }
+    if (rc == TGEMM_OK) clear_error();
+    return rc;
+}
+
+int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                        const int64_t* target, int32_t reduction, const float* dloss, const void* saved, int32_t keep, void* dx,
+                        int64_t lddx, void* dw, int64_t lddw, void* scratch, void* stream) {
+    using namespace tg;
+    if (!xent_sizes_ok(M, V, K, keep)) return TGEMM_E_ARG;
+    const XentLayout l = xent_layout(M, V, K, keep);
+    const bool kx = keep & TGEMM_KEEP_X, kw = keep & TGEMM_KEEP_W;
+    int rc = xent_common(dtype, reduction, target, M);
+    if (rc == TGEMM_OK) rc = mm_check("x", x, M, K, ldx);
+    if (rc == TGEMM_OK) rc = mm_check("w", w, V, K, ldw);
+    if (rc == TGEMM_OK && kx) rc = mm_check("dx", dx, M, K, lddx);
+    if (rc == TGEMM_OK && kw) rc = mm_check("dw", dw, V, K, lddw);
+    if (rc == TGEMM_OK) rc = check_floats("dloss", dloss, reduction == TGEMM_NONE ? M : 1);
+    if (rc == TGEMM_OK) rc = mm_check_buffer("saved", saved, l.bytes[0]);
+    if (rc == TGEMM_OK) rc = mm_check_buffer("scratch", scratch, l.bytes[2]);
+    if (rc == TGEMM_OK && keep && (M > 0 || V > 0)) rc = current_device_ok();
+    if (rc != TGEMM_OK) return rc;
+    if (!keep) {
+        clear_error();
+        return TGEMM_OK;
+    }
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const char* v = static_cast<const char*>(saved);
+    char* s = static_cast<char*>(scratch);
+    const int32_t *count = reinterpret_cast<const int32_t*>(v + l.count), *map = reinterpret_cast<const int32_t*>(v + l.map);
+    float *coef = reinterpret_cast<float*>(s + l.coef), *alpha = reinterpret_cast<float*>(s + l.alpha);
+    const char* wp = static_cast<const char*>(w);
+    CoefArgs c{V, count, map, target, dloss, coef, alpha, reduction};
+    rc = mm_launch(reinterpret_cast<const void*>(xent_coef_kernel), 1, 1024, &c, "factors of the rows", st);
+    if (rc == TGEMM_OK && M > 0)
+        rc = gather(x, ldx, M, K, reinterpret_cast<const int32_t*>(v + l.rank), s + l.x2, l.ldx, nullptr, kx ? dx : nullptr, lddx, st);
+    const bool pieces = l.cols < V;
+    MmStoreArgs into_x{}, into_w{};
+    into_x.alpha = into_w.alpha = alpha;
+    into_x.rows = into_w.rows = count;
+    into_x.jobs = into_w.jobs = 1;
+    into_x.map = map;
+    into_w.rows_are_k = 1;
+    // at least one round: without a vocabulary dx is zero
+    for (int64_t v0 = 0; rc == TGEMM_OK && (v0 < V || v0 == 0); v0 += l.cols) {
+        const int64_t n = V - v0 < l.cols ? V - v0 : l.cols;
+        const char* wv = wp + v0 * ldw * 2;
+        if (M > 0 && n > 0) {
+            const MmKernel& k = mm_kernels(dtype, FORM_DZ)[l.dz.size];
+            MmDzArgs a{MmOperands{s + l.x2, wv, nullptr, 2 * l.ldx, 2 * ldw, 0, (int32_t)M, (int32_t)n, (int32_t)K},
+                       mm_grid(k, l.dz, M, n), count, map, target, v0, reinterpret_cast<const float*>(v + l.lse), coef, s + l.dzs,
+                       l.ldz};
+            rc = mm_launch(k.fn, (int64_t)a.grid.tiles_m * a.grid.tiles_n, k.threads, &a, "gradient of the logits", st);
+        }
+        if (rc == TGEMM_OK && kx) {
+            into_x.job[0] = MmJob{{MmOperands{s + l.dzs, wv, nullptr, 2 * l.ldz, 2 * ldw, 0, (int32_t)M, (int32_t)K, (int32_t)n}, {}},
+                                  1, {}, dx, lddx, l.dx.splits > 1 || pieces ? reinterpret_cast<float*>(s + l.dx_part) : nullptr, v0 > 0};
+            rc = mm_store(dtype, FORM_NN, l.dx, into_x, st);
+        }
+        if (rc == TGEMM_OK && kw && n > 0) {
+            into_w.job[0] = MmJob{{MmOperands{s + l.dzs, s + l.x2, nullptr, 2 * l.ldz, 2 * l.ldx, 0, (int32_t)n, (int32_t)K, (int32_t)M}, {}},
+                                  1, {}, static_cast<char*>(dw) + v0 * lddw * 2, lddw,
+                                  l.dw.splits > 1 ? reinterpret_cast<float*>(s + l.dw_part) : nullptr, 0};
+            rc = mm_store(dtype, FORM_TN, l.dw, into_w, st);
+            if (rc == TGEMM_OK && l.dw.splits > 1) rc = mm_join(dtype, l.dw, into_w, st);
+        }
+    }
+    if (rc == TGEMM_OK && kx && (l.dx.splits > 1 || pieces)) rc = mm_join(dtype, l.dx, into_x, st);
+    if (rc == TGEMM_OK) clear_error();
+    return rc;
+}
+
+}  // extern "C"

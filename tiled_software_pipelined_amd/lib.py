@@ -70,7 +70,9 @@ EXPORTS = ("gemm_plan", "gemm_plan_variant", "gemm_run", "gemm_destroy", "tgemm_
            "gemm_kernel_occupancy", "gemm_clock_slots", "gemm_run_clocked", "gemm_run_noalloc",
            "tgemm_set_c_store_policy", "tgemm_fp8_quantize", "tgemm_fp8_gemm", "tgemm_fp8_gemm_kernel",
            "tgemm_fp8_linear_bytes", "tgemm_fp8_linear_forward", "tgemm_fp8_linear_backward",
-           "tgemm_orthogonalize_workspace_bytes", "tgemm_orthogonalize")
+           "tgemm_orthogonalize_workspace_bytes", "tgemm_orthogonalize", "tgemm_ffn_bytes", "tgemm_ffn_forward",
+           "tgemm_ffn_backward", "tgemm_xent_bytes", "tgemm_xent_forward", "tgemm_xent_backward",
+           "tgemm_clip_workspace_bytes", "tgemm_clip")
 
 
 def _load():
@@ -137,6 +139,23 @@ def _load():
     lib.tgemm_orthogonalize.argtypes = [i64, i64, i64, i32, vp, i64, i64, vp, i64, i64, i32, ctypes.POINTER(f64), f64, vp,
                                         i64, vp]
     lib.tgemm_orthogonalize.restype = ctypes.c_int
+    four = [i64, i64, i64, i64]
+    lib.tgemm_ffn_bytes.argtypes = four + [i32, ctypes.POINTER(i64)]
+    lib.tgemm_ffn_bytes.restype = ctypes.c_int
+    lib.tgemm_ffn_forward.argtypes = four + [i32, i32] + [vp, i64] * 5 + [i32, vp, vp, vp]
+    lib.tgemm_ffn_forward.restype = ctypes.c_int
+    lib.tgemm_ffn_backward.argtypes = four + [i32, i32] + [vp, i64] * 5 + [i32, vp] + [vp, i64] * 4 + [vp, vp]
+    lib.tgemm_ffn_backward.restype = ctypes.c_int
+    lib.tgemm_xent_bytes.argtypes = [i64, i64, i64, i32, ctypes.POINTER(i64)]
+    lib.tgemm_xent_bytes.restype = ctypes.c_int
+    lib.tgemm_xent_forward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, i32, vp, vp, vp, vp]
+    lib.tgemm_xent_forward.restype = ctypes.c_int
+    lib.tgemm_xent_backward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i32, vp, vp, i32, vp, i64, vp, i64, vp, vp]
+    lib.tgemm_xent_backward.restype = ctypes.c_int
+    lib.tgemm_clip_workspace_bytes.argtypes = [i64, vp]
+    lib.tgemm_clip_workspace_bytes.restype = i64
+    lib.tgemm_clip.argtypes = [i64, vp, vp, vp, vp, f64, f64, vp, vp, i64, vp]
+    lib.tgemm_clip.restype = ctypes.c_int
     return lib
 
 
@@ -775,3 +794,283 @@ def orthogonalize(G, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e-7,
     _call(G.device, _lib.tgemm_orthogonalize, batch, rows, cols, code, G.data_ptr(), ldg, stride_g, out.data_ptr(), ldo,
           stride_o, steps, coef, float(eps), ws.data_ptr(), need)
     return out
+
+
+# ---- products of a training step with fused ends --------------------------------
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
+FFN_X, FFN_GATE, FFN_UP, FFN_DOWN = 1, 2, 4, 8
+MOST_STRIDE = 1 << 22  # elements from a row to the next
+_HALF_CODES = {torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _half_code(tensors, names):
+    """The type code of tensors that are all bfloat16 or all float16 on one GPU."""
+    first = tensors[0]
+    code, device = _HALF_CODES.get(first.dtype), first.device
+    if code is None:
+        raise TypeError("%s has unsupported dtype %s (bfloat16, float16)" % (names[0], first.dtype))
+    for t, name in zip(tensors, names):
+        if t.dtype != first.dtype:
+            raise TypeError("%s must have %s's dtype %s, got %s" % (name, names[0], first.dtype, t.dtype))
+        if not t.is_cuda or t.device != device:
+            raise ValueError("%s must be on one GPU (%s, got %s)" % (" and ".join(names), device, t.device))
+    return code
+
+
+def _read(t):
+    """(row-major matrix that the kernels may read, its row stride): t, or a copy."""
+    if t.is_contiguous():
+        return t, t.shape[1]
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and not t.shape[1] <= t.stride(0) <= MOST_STRIDE:
+        t = t.contiguous()
+        return t, t.shape[1]
+    return t, t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _wants_derivative(tensors):
+    """Whether a call may be differentiated (a dual tensor of forward-mode
+    differentiation counts: the autograd functions refuse it)."""
+    return forward_ad._current_level >= 0 or torch.is_grad_enabled() and any(t.requires_grad for t in tensors)
+
+
+@functools.lru_cache(maxsize=512)
+def _ffn_bytes(M, K, F, N, keep):
+    n = (ctypes.c_int64 * 3)()
+    rc = _lib.tgemm_ffn_bytes(M, K, F, N, keep, n)
+    if rc != OK:
+        raise TgemmError(rc, last_error())
+    return tuple(max(v, 1) for v in n)
+
+
+def _ffn_forward(x, w_gate, w_up, w_down, code, act, keep):
+    """y of shape (..., N), and the buffer for the backward pass (None where keep is 0)."""
+    device, K, (N, F) = x.device, x.shape[-1], w_down.shape
+    M = math.prod(x.shape[:-1])
+    (x2, ldx), (wg, ldg), (wu, ldu), (wd, ldd) = _read(x.reshape(M, K)), _read(w_gate), _read(w_up), _read(w_down)
+    sizes = _ffn_bytes(M, K, F, N, keep)
+    saved = torch.empty(sizes[0], dtype=torch.uint8, device=device) if keep else None
+    scratch = torch.empty(sizes[1], dtype=torch.uint8, device=device)
+    y = torch.empty(x.shape[:-1] + (N,), dtype=x.dtype, device=device)
+    _call(device, _lib.tgemm_ffn_forward, M, K, F, N, code, act, x2.data_ptr(), ldx, wg.data_ptr(), ldg, wu.data_ptr(), ldu,
+          wd.data_ptr(), ldd, y.data_ptr(), N, keep, saved.data_ptr() if keep else None, scratch.data_ptr())
+    return y, saved
+
+
+class _GatedFfn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, w_down, code, act):
+        keep = sum(bit for bit, needed in zip((FFN_X, FFN_GATE, FFN_UP, FFN_DOWN), ctx.needs_input_grad) if needed)
+        y, saved = _ffn_forward(x, w_gate, w_up, w_down, code, act, keep)
+        ctx.save_for_backward(x, w_gate, w_up, w_down, saved)
+        ctx.args = code, act, keep
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gy):
+        x, w_gate, w_up, w_down, saved = ctx.saved_tensors
+        code, act, keep = ctx.args
+        device, K, (N, F) = x.device, x.shape[-1], w_down.shape
+        M = math.prod(x.shape[:-1])
+        (x2, ldx), (wg, ldg), (wu, ldu), (wd, ldd) = _read(x.reshape(M, K)), _read(w_gate), _read(w_up), _read(w_down)
+        g, ldy = _read(gy.reshape(M, N))
+        scratch = torch.empty(_ffn_bytes(M, K, F, N, keep)[2], dtype=torch.uint8, device=device)
+        grads = [torch.empty(t.shape, dtype=t.dtype, device=device) if needed else None
+                 for t, needed in zip((x, w_gate, w_up, w_down), ctx.needs_input_grad)]
+        dx, dg, du, dd = (None if t is None else t.data_ptr() for t in grads)
+        _call(device, _lib.tgemm_ffn_backward, M, K, F, N, code, act, x2.data_ptr(), ldx, wg.data_ptr(), ldg, wu.data_ptr(), ldu,
+              wd.data_ptr(), ldd, g.data_ptr(), ldy, keep, saved.data_ptr(), dx, K, dg, K, du, K, dd, F, scratch.data_ptr())
+        return (*grads, None, None)
+
+
+def gated_ffn(x, w_gate, w_up, w_down, activation="silu"):
+    """The gated feed-forward block, y = (act(x @ w_gate^T) * (x @ w_up^T)) @ w_down^T,
+    differentiable.
+
+    x: (..., K), w_gate and w_up: (F, K), w_down: (N, F), all bfloat16 or all
+    float16; rows may be apart (parts of one (2 F, K) tensor serve as w_gate and
+    w_up).  ``activation``: "silu", "gelu", "gelu_tanh" or "relu".  Returns
+    (..., N) of x's dtype.  Sums are float; the inner values (and, for the
+    backward pass, both projections and their gradients) are rounded to x's dtype,
+    y and each gradient once.  The two projections, the activation and their
+    product are one kernel; up to 32 tokens without gradients take kernels that read
+    each weight once.  The backward pass keeps the two projections (two values
+    for each token and inner unit) and computes only the gradients that are asked
+    for; second derivatives and forward-mode ones are refused.  To capture a
+    training step into a graph, see :func:`linear_fp8`.
+    """
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError("activation must be one of %s, got %r" % (", ".join(map(repr, ACTIVATIONS)), activation))
+    tensors = (x, w_gate, w_up, w_down)
+    code = _half_code(tensors, ("x", "w_gate", "w_up", "w_down"))
+    if x.dim() < 1 or w_gate.dim() != 2 or w_down.dim() != 2 or w_up.shape != w_gate.shape or \
+            x.shape[-1] != w_gate.shape[1] or w_down.shape[1] != w_gate.shape[0]:
+        raise ValueError("x %s, w_gate %s, w_up %s and w_down %s do not make a feed-forward block" % tuple(
+            tuple(t.shape) for t in tensors))
+    if not _wants_derivative(tensors):
+        return _ffn_forward(x, w_gate, w_up, w_down, code, act, 0)[0]
+    return _GatedFfn.apply(x, w_gate, w_up, w_down, code, act)
+
+
+@functools.lru_cache(maxsize=512)
+def _xent_bytes(M, V, K, keep):
+    n = (ctypes.c_int64 * 3)()
+    rc = _lib.tgemm_xent_bytes(M, V, K, keep, n)
+    if rc != OK:
+        raise TgemmError(rc, last_error())
+    return tuple(max(v, 1) for v in n)
+
+
+def _xent_forward(x, w, target, ignore, reduction, code):
+    """The loss, and what the backward pass reads of the rows."""
+    device, (V, K) = x.device, w.shape
+    M = target.numel()
+    (x2, ldx), (w2, ldw), t = _read(x.reshape(M, K)), _read(w), target.contiguous()
+    loss = torch.empty(() if reduction else target.shape, dtype=torch.float32, device=device)
+    sizes = _xent_bytes(M, V, K, 0)
+    saved, scratch = (torch.empty(n, dtype=torch.uint8, device=device) for n in sizes[:2])
+    _call(device, _lib.tgemm_xent_forward, M, V, K, code, x2.data_ptr(), ldx, w2.data_ptr(), ldw, t.data_ptr(), ignore, reduction,
+          loss.data_ptr(), saved.data_ptr(), scratch.data_ptr())
+    return loss, saved
+
+
+class _LinearCrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, target, ignore, reduction, code):
+        loss, saved = _xent_forward(x, w, target, ignore, reduction, code)
+        ctx.save_for_backward(x, w, target, saved)
+        ctx.args = reduction, code
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gloss):
+        x, w, target, saved = ctx.saved_tensors
+        reduction, code = ctx.args
+        device, (V, K) = x.device, w.shape
+        M = target.numel()
+        keep = (KEEP_X if ctx.needs_input_grad[0] else 0) | (KEEP_W if ctx.needs_input_grad[1] else 0)
+        (x2, ldx), (w2, ldw), t, g = _read(x.reshape(M, K)), _read(w), target.contiguous(), gloss.contiguous()
+        scratch = torch.empty(_xent_bytes(M, V, K, keep)[2], dtype=torch.uint8, device=device)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=device) if keep & KEEP_X else None
+        dw = torch.empty(w.shape, dtype=w.dtype, device=device) if keep & KEEP_W else None
+        _call(device, _lib.tgemm_xent_backward, M, V, K, code, x2.data_ptr(), ldx, w2.data_ptr(), ldw, t.data_ptr(), reduction,
+              g.data_ptr(), saved.data_ptr(), keep, None if dx is None else dx.data_ptr(), K,
+              None if dw is None else dw.data_ptr(), K, scratch.data_ptr())
+        return dx, dw, None, None, None, None
+
+
+def linear_cross_entropy(x, w, target, ignore_index=-100, reduction="mean"):
+    """Softmax cross entropy of the logits x @ w^T, which are never stored,
+    differentiable: logsumexp(x @ w^T) - (x @ w^T)[target] of each token.
+
+    x: (..., K), w: (V, K), both bfloat16 or both float16; target: int64 of
+    x.shape[:-1].  Tokens whose target is ``ignore_index`` do not count, whatever
+    they hold, and cost nothing (the products leave them out); any other target
+    outside 0 .. V - 1 makes the loss NaN.
+    ``reduction``: "mean" over the tokens that count (NaN where none does),
+    "sum", or "none" (a loss for each token, zero where it does not count).
+    Returns float32; logits and the softmax are float throughout.  The backward
+    pass makes the logits again, a piece of the vocabulary at a time (scratch:
+    about 512 MB at most, or 16 KB a token where that is more, and dx's float sums
+    where there are several pieces), and rounds their gradients to x's dtype,
+    scaled by a power of two that the results do not keep, so that small
+    probabilities hold in float16 too.  Gradients have their inputs' dtypes;
+    second derivatives and forward-mode ones are refused.  To capture a training
+    step into a graph, see :func:`linear_fp8`.
+    """
+    how = REDUCTIONS.get(reduction)
+    if how is None:
+        raise ValueError("reduction must be one of %s, got %r" % (", ".join(map(repr, REDUCTIONS)), reduction))
+    code = _half_code((x, w), ("x", "w"))
+    if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
+        raise ValueError("x %s and w %s do not make x @ w^T" % (tuple(x.shape), tuple(w.shape)))
+    if target.dtype != torch.int64:
+        raise TypeError("target must be int64, got %s" % target.dtype)
+    if target.shape != x.shape[:-1] or target.device != x.device:
+        raise ValueError("target must be of shape %s on %s, got %s on %s" % (
+            tuple(x.shape[:-1]), x.device, tuple(target.shape), target.device))
+    if not -2 ** 63 <= ignore_index < 2 ** 63 or ignore_index != int(ignore_index):
+        raise ValueError("ignore_index must be an int64, got %r" % (ignore_index,))
+    if not _wants_derivative((x, w)):
+        return _xent_forward(x, w, target, int(ignore_index), how, code)[0]
+    return _LinearCrossEntropy.apply(x, w, target, int(ignore_index), how, code)
+
+
+def _dense(t):
+    """Whether t's elements fill a block of memory, each once."""
+    if t.is_contiguous():
+        return True
+    span = 1
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != span:
+            return False
+        span *= size
+    return True
+
+
+def clip_grad_norm(grads, max_norm, eps=1e-6, out=None):
+    """Scale tensors so that their norm, taken as one vector, is at most
+    ``max_norm``; returns the norm that they had (a float32 scalar on the GPU).
+
+    grads: one or more float32, bfloat16 or float16 tensors on one GPU, of any
+    shapes, dense (their elements fill a block of memory in any order of axes),
+    none of them twice.  Each is multiplied by min(1, max_norm / (norm + eps)) in
+    place, or into the tensor of ``out`` at its place (same shape, dtype and
+    strides; it may be the same tensor).  Squares are summed in 64 bits; the
+    product is rounded once.  A norm that is infinite makes the factor zero (and
+    infinities NaN), a NaN makes everything NaN.  Nothing waits for the GPU.  Not
+    differentiable.
+    """
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads must hold at least one tensor")
+    max_norm, eps = float(max_norm), float(eps)
+    if not max_norm >= 0 or not eps >= 0:
+        raise ValueError("max_norm and eps must not be negative or NaN, got %r and %r" % (max_norm, eps))
+    out = grads if out is None else list(out)
+    if len(out) != len(grads):
+        raise ValueError("out must hold a tensor for each of the %d of grads, got %d" % (len(grads), len(out)))
+    n, device = len(grads), grads[0].device
+    if not grads[0].is_cuda:
+        raise ValueError("grads must be GPU tensors")
+    codes, counts, ins = [], [], []
+    for t in grads:
+        code = _REAL_CODES.get(t.dtype)
+        if code is None:
+            raise TypeError("grads has unsupported dtype %s (float32, bfloat16, float16)" % t.dtype)
+        if t.device != device:
+            raise ValueError("grads must be on one GPU (%s, %s)" % (device, t.device))
+        if not _dense(t):
+            raise ValueError("grads must be dense (shape %s, strides %s)" % (tuple(t.shape), t.stride()))
+        codes.append(code)
+        counts.append(t.numel())
+        ins.append(t.data_ptr())
+    outs = ins
+    if out is not grads:
+        outs = []
+        for t, o in zip(grads, out):
+            if o.dtype != t.dtype or o.shape != t.shape or o.device != device or o.stride() != t.stride() and not (
+                    o.is_contiguous() and t.is_contiguous()):
+                raise ValueError("out must match grads: %s %s %s with strides %s, got %s %s %s with strides %s" % (
+                    t.dtype, tuple(t.shape), device, t.stride(), o.dtype, tuple(o.shape), o.device, o.stride()))
+            outs.append(o.data_ptr())
+    for pointers in (ins, outs):
+        used = [p for p, c in zip(pointers, counts) if c]
+        if len(set(used)) != len(used):
+            raise ValueError("a tensor is given twice")
+    i64s = ctypes.c_int64 * n
+    sizes = i64s(*counts)
+    need = _lib.tgemm_clip_workspace_bytes(n, sizes)
+    if need < 0:
+        raise ValueError("grads hold more elements than 2^40")
+    pointers = ctypes.c_void_p * n
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    _call(device, _lib.tgemm_clip, n, pointers(*ins), pointers(*outs), sizes, (ctypes.c_int32 * n)(*codes), max_norm, eps,
+          norm.data_ptr(), ws.data_ptr(), need)
+    torch.autograd.graph.increment_version([t for t in out if not t.is_inference()])
+    return norm
