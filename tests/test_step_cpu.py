@@ -54,8 +54,8 @@ def test_ffn_sizes():
     assert tl._lib.tgemm_ffn_bytes(4, 8, 16, 8, 15, None) == -2
     assert tl._lib.tgemm_ffn_bytes(4, 8, 2 ** 23, 8, 15, n) == -1
     assert tl._lib.tgemm_ffn_bytes(100, 64, 1000, 64, 0, n) == 0 and n[0] == 0 and n[1] >= 2 * 100 * 1000 and n[2] == 0
-    assert tl._lib.tgemm_ffn_bytes(100, 64, 1000, 64, 15, n) == 0 and n[0] == 2 * (200000 + 192) and n[2] >= 3 * 200000
-    assert tl._lib.tgemm_ffn_bytes(100, 64, 1000, 64, tl.FFN_DOWN, n) == 0 and n[0] == 200000 + 192  # h alone is kept
+    assert tl._lib.tgemm_ffn_bytes(100, 64, 1000, 64, 15, n) == 0 and n[0] == 2 * 2 * 100 * 1024 and n[2] >= 3 * 200000
+    assert tl._lib.tgemm_ffn_bytes(100, 64, 1000, 64, tl.FFN_DOWN, n) == 0 and n[0] == 2 * 100 * 1024  # h alone is kept, rows of whole lines
     assert tl._lib.tgemm_ffn_bytes(0, 64, 1000, 64, 15, n) == 0
     assert tl._lib.tgemm_ffn_bytes(2 ** 30, 2 ** 22, 2 ** 22, 2 ** 22, 15, n) == 0 and min(n) > 2 ** 52
 
@@ -100,8 +100,8 @@ def test_xent_sizes():
     assert tl._lib.tgemm_xent_bytes(4, 8, 16, 3, None) == -2 and tl._lib.tgemm_xent_bytes(4, 8, 16, 4, n) == -1
     for M, V, K in ((8192, 128256, 4096), (1, 2 ** 30, 64), (2 ** 20, 50000, 64), (0, 10, 8), (10, 0, 8), (7, 9, 0)):
         assert tl._lib.tgemm_xent_bytes(M, V, K, 3, n) == 0
-        # dz: at most 512 MB or 16 KB a row, never all of a large M V; x gathered; dx's float sums of up to 16 splits
-        assert n[2] <= max(2 ** 29, 2 ** 14 * M) + 512 * M + 2 * M * (K + 64) + 64 * M * K + 64 * min(V, 2 ** 28) * K + 2 ** 20
+        # dz: at most 512 MB or 16 KB a row, never all of a large M V; x gathered; dx's float sums; 64 MB of shared tiles
+        assert n[2] <= max(2 ** 29, 2 ** 14 * M) + 512 * M + 2 * M * (K + 64) + 4 * M * K + 2 ** 26 + 2 ** 20
     one = n[0], n[1]
     assert tl._lib.tgemm_xent_bytes(7, 9, 0, 0, n) == 0 and (n[0], n[1], n[2]) == (*one, 0)
 

@@ -4,9 +4,9 @@ namespace tg {
 typedef MmTiles<MmF16, ALONG, ALONG, false> Tiles;
 const MmKernel* mm_nt_f16() {
     static const MmKernel table[SIZE_COUNT] = {
-        {reinterpret_cast<const void*>(mm_store_kernel<Tiles::T256>), Tiles::T256::BM, Tiles::T256::TILE_N, Tiles::T256::NT},
-        {reinterpret_cast<const void*>(mm_store_kernel<Tiles::T128>), Tiles::T128::BM, Tiles::T128::TILE_N, Tiles::T128::NT},
-        {reinterpret_cast<const void*>(mm_store_kernel<Tiles::T64>), Tiles::T64::BM, Tiles::T64::TILE_N, Tiles::T64::NT},
+        mm_entry<Tiles::T256>(reinterpret_cast<const void*>(mm_store_kernel<Tiles::T256>), reinterpret_cast<const void*>(mm_join_kernel<Tiles::T256>)),
+        mm_entry<Tiles::T128>(reinterpret_cast<const void*>(mm_store_kernel<Tiles::T128>), reinterpret_cast<const void*>(mm_join_kernel<Tiles::T128>)),
+        mm_entry<Tiles::T64>(reinterpret_cast<const void*>(mm_store_kernel<Tiles::T64>), reinterpret_cast<const void*>(mm_join_kernel<Tiles::T64>)),
     };
     return table;
 }

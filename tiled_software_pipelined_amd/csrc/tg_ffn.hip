@@ -14,11 +14,13 @@ namespace tg {
 struct FfnLayout {
     int64_t g, u, h;         // forward: kept, or in scratch (h); -1: not there
     bool h_kept;             // only the down projection's gradient is wanted
-    int64_t part;            // forward's scratch: the down projection's partial sums
+    int64_t ld;              // row stride of all of them: whole 128-byte lines
+    int64_t split;           // forward's scratch: sums of the down projection's shared tiles
     int64_t dg, du, h2;      // backward's scratch
-    int64_t dx_part, dw_part[3];
+    int64_t dx_split, dw_split;
+    int64_t split_bytes, dx_split_bytes, dw_split_bytes;
     bool rows;               // few tokens: the kernels that read each weight once
-    MmPlan gate, down, dh, dx, dw;
+    MmSize gate, down, dh, dx, dw;
     int64_t bytes[3];        // saved, forward's scratch, backward's scratch
 };
 
@@ -32,38 +34,44 @@ static FfnLayout ffn_layout(int64_t M, int64_t K, int64_t F, int64_t N, int keep
         return at;
     };
     l.rows = M <= 32;
-    const MmShape inner{M, F}, y{M, N}, dx{M, K}, dw[3] = {{F, K}, {F, K}, {N, F}};
-    l.gate = mm_plan(FORM_GATE, &inner, 1, mm_slices(K), false);
-    l.down = mm_plan(FORM_NT, &y, 1, mm_slices(F), true);
+    l.ld = (F + 63) / 64 * 64;
+    const int64_t inner = 2 * M * l.ld;
+    const MmShape y{M, N}, x{M, K}, dw[3] = {{F, K}, {F, K}, {N, F}};
+    l.gate = mm_size(FORM_GATE, M, F, mm_slices(K), false);
+    l.down = mm_size(FORM_NT, M, N, mm_slices(F), true);
     l.g = l.u = l.dg = l.du = l.h2 = -1;
     l.h_kept = keep == TGEMM_FFN_DOWN;
     if (keep & FFN_INNER) {
-        l.g = take(0, 2 * M * F);
-        l.u = take(0, 2 * M * F);
+        l.g = take(0, inner);
+        l.u = take(0, inner);
     }
-    l.h = take(l.h_kept ? 0 : 1, 2 * M * F);
-    if (!l.rows) l.part = take(1, mm_part_bytes(l.down, M, N, false));
+    l.h = take(l.h_kept ? 0 : 1, inner);
+    if (!l.rows) l.split_bytes = mm_split_bytes(FORM_NT, l.down, &y, 1, mm_slices(F), false);
+    l.split = take(1, l.split_bytes);
     if (keep & FFN_INNER) {
-        l.dh = mm_plan(FORM_DH, &inner, 1, mm_slices(N), false);
-        if (keep & (TGEMM_FFN_X | TGEMM_FFN_GATE)) l.dg = take(2, 2 * M * F);
-        if (keep & (TGEMM_FFN_X | TGEMM_FFN_UP)) l.du = take(2, 2 * M * F);
-        if (keep & TGEMM_FFN_DOWN) l.h2 = take(2, 2 * M * F);
+        l.dh = mm_size(FORM_DH, M, F, mm_slices(N), false);
+        if (keep & (TGEMM_FFN_X | TGEMM_FFN_GATE)) l.dg = take(2, inner);
+        if (keep & (TGEMM_FFN_X | TGEMM_FFN_UP)) l.du = take(2, inner);
+        if (keep & TGEMM_FFN_DOWN) l.h2 = take(2, inner);
     }
     if (keep & TGEMM_FFN_X) {
-        l.dx = mm_plan(FORM_NN, &dx, 1, 2 * mm_slices(F), true);
-        l.dx_part = take(2, mm_part_bytes(l.dx, M, K, false));
+        l.dx = mm_size(FORM_NN, M, K, 2 * mm_slices(F), true);
+        l.dx_split_bytes = mm_split_bytes(FORM_NN, l.dx, &x, 1, 2 * mm_slices(F), false);
+        l.dx_split = take(2, l.dx_split_bytes);
     }
     MmShape wanted[3];
     int n = 0;
     for (int i = 0; i < 3; ++i)
         if (keep & (TGEMM_FFN_GATE << i)) wanted[n++] = dw[i];
     if (n > 0) {
-        l.dw = mm_plan(FORM_TN, wanted, n, mm_slices(M), true);
-        for (int i = 0; i < 3; ++i)
-            if (keep & (TGEMM_FFN_GATE << i)) l.dw_part[i] = take(2, mm_part_bytes(l.dw, dw[i].M, dw[i].N, false));
+        l.dw = mm_size(FORM_TN, wanted, n, mm_slices(M), true);
+        l.dw_split_bytes = mm_split_bytes(FORM_TN, l.dw, wanted, n, mm_slices(M), false);
+        l.dw_split = take(2, l.dw_split_bytes);
     }
     return l;
 }
+
+static float* room(char* base, int64_t at, int64_t bytes) { return bytes > 0 ? reinterpret_cast<float*>(base + at) : nullptr; }
 
 static bool ffn_sizes_ok(int64_t M, int64_t K, int64_t F, int64_t N, int32_t keep) {
     if (M < 0 || K < 0 || F < 0 || N < 0 || M > MM_MOST_ROWS || K > MM_MOST || F > MM_MOST || N > MM_MOST || (keep & ~15)) {
@@ -140,25 +148,24 @@ int tgemm_ffn_forward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype,
         o.b2 = static_cast<const char*>(wu);
         o.ldb2 = 2 * ldu;
         if (l.rows && l.g < 0) {
-            MmRowsArgs a{o, h, F, act};
+            MmRowsArgs a{o, h, l.ld, act};
             rc = mm_launch(rows_kernel<true>(dtype, M), (F + 15) / 16, 512, &a, "gate and up projections", st);
         } else {
-            const MmKernel& k = mm_kernels(dtype, FORM_GATE)[l.gate.size];
-            MmGateArgs a{o, mm_grid(k, l.gate, M, F), h, l.g < 0 ? nullptr : v + l.g, l.u < 0 ? nullptr : v + l.u, act};
+            const MmKernel& k = mm_kernels(dtype, FORM_GATE)[l.gate];
+            MmGateArgs a{o, mm_grid(k, M, F), h, l.g < 0 ? nullptr : v + l.g, l.u < 0 ? nullptr : v + l.u, l.ld, act};
             rc = mm_launch(k.fn, (int64_t)a.grid.tiles_m * a.grid.tiles_n, k.threads, &a, "gate and up projections", st);
         }
     }
     if (rc == TGEMM_OK && M > 0 && N > 0) {
         if (l.rows) {
-            MmRowsArgs a{operands(h, F, wd, ldd, M, N, F), y, ldy, 0};
+            MmRowsArgs a{operands(h, l.ld, wd, ldd, M, N, F), y, ldy, 0};
             rc = mm_launch(rows_kernel<false>(dtype, M), (N + 15) / 16, 512, &a, "down projection", st);
         } else {
             MmStoreArgs a{};
             a.jobs = 1;
-            a.job[0] = MmJob{{operands(h, F, wd, ldd, M, N, F), {}}, 1, {}, y, ldy,
-                             l.down.splits > 1 ? reinterpret_cast<float*>(s + l.part) : nullptr, 0};
+            a.split = room(s, l.split, l.split_bytes);
+            a.job[0] = MmJob{{operands(h, l.ld, wd, ldd, M, N, F), {}}, 1, {}, y, ldy, nullptr, 0};
             rc = mm_store(dtype, FORM_NT, l.down, a, st);
-            if (rc == TGEMM_OK && l.down.splits > 1) rc = mm_join(dtype, l.down, a, st);
         }
     }
     if (rc == TGEMM_OK) clear_error();
@@ -193,26 +200,24 @@ int tgemm_ffn_backward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype
     char *dg = in_scratch(l.dg), *du = in_scratch(l.du);
     const char* h = l.h_kept ? v + l.h : in_scratch(l.h2);
     if ((keep & FFN_INNER) && M > 0 && F > 0) {
-        const MmKernel& k = mm_kernels(dtype, FORM_DH)[l.dh.size];
-        MmDhArgs a{operands(dy, lddy, wd, ldd, M, F, N), mm_grid(k, l.dh, M, F), v + l.g, v + l.u, dg, du, in_scratch(l.h2), act};
+        const MmKernel& k = mm_kernels(dtype, FORM_DH)[l.dh];
+        MmDhArgs a{operands(dy, lddy, wd, ldd, M, F, N), mm_grid(k, M, F), v + l.g, v + l.u, dg, du, in_scratch(l.h2), l.ld, act};
         rc = mm_launch(k.fn, (int64_t)a.grid.tiles_m * a.grid.tiles_n, k.threads, &a, "gradient of the inner values", st);
     }
     if (rc == TGEMM_OK && (keep & TGEMM_FFN_X)) {
         MmStoreArgs a{};
         a.jobs = 1;
-        a.job[0] = MmJob{{operands(dg, F, wg, ldg, M, K, F), operands(du, F, wu, ldu, M, K, F)}, 2, {}, dx, lddx,
-                         l.dx.splits > 1 ? reinterpret_cast<float*>(s + l.dx_part) : nullptr, 0};
+        a.split = room(s, l.dx_split, l.dx_split_bytes);
+        a.job[0] = MmJob{{operands(dg, l.ld, wg, ldg, M, K, F), operands(du, l.ld, wu, ldu, M, K, F)}, 2, {}, dx, lddx, nullptr, 0};
         rc = mm_store(dtype, FORM_NN, l.dx, a, st);
-        if (rc == TGEMM_OK && l.dx.splits > 1) rc = mm_join(dtype, l.dx, a, st);
     }
     if (rc == TGEMM_OK && (keep & (TGEMM_FFN_GATE | TGEMM_FFN_UP | TGEMM_FFN_DOWN))) {
         MmStoreArgs a{};
-        auto part = [&](int i) { return l.dw.splits > 1 ? reinterpret_cast<float*>(s + l.dw_part[i]) : nullptr; };
-        if (keep & TGEMM_FFN_GATE) a.job[a.jobs++] = MmJob{{operands(dg, F, x, ldx, F, K, M), {}}, 1, {}, dwg, lddwg, part(0), 0};
-        if (keep & TGEMM_FFN_UP) a.job[a.jobs++] = MmJob{{operands(du, F, x, ldx, F, K, M), {}}, 1, {}, dwu, lddwu, part(1), 0};
-        if (keep & TGEMM_FFN_DOWN) a.job[a.jobs++] = MmJob{{operands(dy, lddy, h, F, N, F, M), {}}, 1, {}, dwd, lddwd, part(2), 0};
+        a.split = room(s, l.dw_split, l.dw_split_bytes);
+        if (keep & TGEMM_FFN_GATE) a.job[a.jobs++] = MmJob{{operands(dg, l.ld, x, ldx, F, K, M), {}}, 1, {}, dwg, lddwg, nullptr, 0};
+        if (keep & TGEMM_FFN_UP) a.job[a.jobs++] = MmJob{{operands(du, l.ld, x, ldx, F, K, M), {}}, 1, {}, dwu, lddwu, nullptr, 0};
+        if (keep & TGEMM_FFN_DOWN) a.job[a.jobs++] = MmJob{{operands(dy, lddy, h, l.ld, N, F, M), {}}, 1, {}, dwd, lddwd, nullptr, 0};
         rc = mm_store(dtype, FORM_TN, l.dw, a, st);
-        if (rc == TGEMM_OK && l.dw.splits > 1) rc = mm_join(dtype, l.dw, a, st);
     }
     if (rc == TGEMM_OK) clear_error();
     return rc;

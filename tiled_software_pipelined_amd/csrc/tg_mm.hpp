@@ -88,6 +88,12 @@ struct MmTile {
     // columns of C: with PAIR, of each of the two matrices
     static constexpr int TILE_N = PAIR ? BN / 2 : BN, WAVE_N = PAIR ? WTN / 2 : WTN;
 
+    // workgroups on the machine at once; nanoseconds of a slice when it is full;
+    // kilobytes of a tile's float sums
+    static constexpr int SLOTS = BM * BN >= 65536 ? 256 : 512;
+    static constexpr int SLICE_NS = BM * BN >= 65536 ? 1750 : BM * BN >= 16384 ? 1100 : 600;
+    static constexpr int TILE_KB = BM * BN / 256;
+
     typedef f32x16 Acc[FM][FN];
 
     static_assert(BM % (32 * WAVES_M) == 0 && BN % (32 * WAVES_N) == 0, "wave tile");
@@ -167,32 +173,39 @@ struct MmTile {
 
     // Slices that direct copies must not read (a row's end inside the slice, or
     // the operand's last rows): through registers, zero outside the operands.
+    // Whole chunks take one load each (of zeros where there is nothing); the
+    // chunk that a row ends in is cut out where rows are no whole chunks.
     template <int L, int W>
     __device__ static __forceinline__ i32x4 tail_chunk(int pos, int r0, int row, int rows, const char* p, int64_t ld, int t, int K) {
-        if constexpr (L == ALONG) {
-            const int c = along_chunk(pos >> 3, pos & 7);
-            return row_end_chunk(p + (int64_t)min(r0 + row, rows - 1) * ld, t * ROW + c * 16, K * 2);
-        } else {
-            const int kr = pos / (W / 8), c = across_chunk<W>(kr, pos % (W / 8)), k = t * BK + kr;
-            const i32x4 v = row_end_chunk(p + (int64_t)min(k, K - 1) * ld, (r0 + c * 8) * 2, rows * 2);
-            return k < K ? v : i32x4{0, 0, 0, 0};
+        const int line = pos / (L == ALONG ? 8 : W / 8);
+        const int c = L == ALONG ? along_chunk(line, pos & 7) : across_chunk<W>(line, pos % (W / 8));
+        // the operand's row, the chunk's first byte in it, the row's end
+        const int r = L == ALONG ? min(r0 + row, rows - 1) : t * BK + line;
+        const int at = L == ALONG ? t * ROW + c * 16 : (r0 + c * 8) * 2;
+        const int end = L == ALONG ? K * 2 : rows * 2;
+        const bool inside = L == ALONG || r < K;
+        const char* q = p + (int64_t)(inside ? r : 0) * ld;
+        const bool whole = inside && at + 16 <= end;
+        i32x4 v = load16(whole ? q + at : reinterpret_cast<const char*>(g_zeros));
+        if (end & 15) {  // wave-uniform
+            const i32x4 cut = row_end_chunk(q, at, end);
+            if (inside && !whole) v = cut;
         }
+        return v;
     }
     __device__ static __forceinline__ void fill_slice(TG_LDS char* slot, const MmOperands& g, int m0, int n0, int t) {
         const int tid = threadIdx.x;
-        i32x4 v[A_PER > B_PER ? A_PER : B_PER];
-#pragma unroll
-        for (int q = 0; q < A_PER; ++q) v[q] = tail_chunk<LA, BM>(q * NT + tid, m0, (q * NT + tid) >> 3, g.M, g.a, g.lda, t, g.K);
-#pragma unroll
-        for (int q = 0; q < A_PER; ++q) *reinterpret_cast<TG_LDS i32x4*>(slot + (q * NT + tid) * 16) = v[q];
-#pragma unroll
+#pragma unroll 4
+        for (int q = 0; q < A_PER; ++q)
+            *reinterpret_cast<TG_LDS i32x4*>(slot + (q * NT + tid) * 16) =
+                tail_chunk<LA, BM>(q * NT + tid, m0, (q * NT + tid) >> 3, g.M, g.a, g.lda, t, g.K);
+#pragma unroll 4
         for (int q = 0; q < B_PER; ++q) {
             const int p = (q * NT + tid) >> 3;
             const bool second = PAIR && b_half(p);
-            v[q] = tail_chunk<LB, BN>(q * NT + tid, n0, b_row(p), g.N, second ? g.b2 : g.b, second ? g.ldb2 : g.ldb, t, g.K);
+            *reinterpret_cast<TG_LDS i32x4*>(slot + A_BYTES + (q * NT + tid) * 16) =
+                tail_chunk<LB, BN>(q * NT + tid, n0, b_row(p), g.N, second ? g.b2 : g.b, second ? g.ldb2 : g.ldb, t, g.K);
         }
-#pragma unroll
-        for (int q = 0; q < B_PER; ++q) *reinterpret_cast<TG_LDS i32x4*>(slot + A_BYTES + (q * NT + tid) * 16) = v[q];
     }
 
     // ---- fragments -------------------------------------------------------------
@@ -382,44 +395,73 @@ struct MmTile {
     }
 
     // ---- the way out -----------------------------------------------------------
-    // Calls each(row, column, v, w) for every 8 adjacent columns of the wave's
+    // Calls each(row, column, v, w, data) for every 8 adjacent columns of the wave's
     // block: row and column relative to the block, v their sums, w (PAIR) those
-    // of the second matrix.  32 rows at a time go through the wave's own LDS.
-    template <class Each>
-    __device__ static __forceinline__ void each_row(const Acc& acc, TG_LDS char* smem, int lane, int wave, Each each) {
-        constexpr int CH = WTN / 4;           // 16-byte chunks of a row of sums
-        constexpr int PER_ROW = WAVE_N / 8;   // lanes a row
-        constexpr int ROWS = 64 / PER_ROW;    // rows an instruction
+    // of the second matrix.  32 rows at a time go through the wave's own LDS;
+    // before that, fetch(row, column, data) starts the loads that `each` will want
+    // of them, all of the 32 rows' in flight together.  The walk over the
+    // 32-row blocks is a loop, so that `each` stands in the code once.
+    static constexpr int PER_ROW = WAVE_N / 8;     // lanes a row
+    static constexpr int ROWS = 64 / PER_ROW;      // rows an instruction
+    static constexpr int PIECES = 32 / ROWS;       // instructions a block
+    template <int I>
+    __device__ static __forceinline__ void stage(int i, const Acc& acc, TG_LDS char* mine, int lane) {
+        if constexpr (I < FM) {
+            if (i == I) {
+                // the empty statements keep the compiler from merging the blocks
+                // into one that indexes acc, which would then stand in memory
+                asm volatile("; block %0 from here" ::"n"(I) : "memory");
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        *reinterpret_cast<TG_LDS f32x4*>(staged(mine, lane & 31, 8 * j + 2 * r + (lane >> 5))) =
+                            f32x4{acc[I][j][4 * r], acc[I][j][4 * r + 1], acc[I][j][4 * r + 2], acc[I][j][4 * r + 3]};
+                asm volatile("; block %0 to here" ::"n"(I) : "memory");
+            } else {
+                stage<I + 1>(i, acc, mine, lane);
+            }
+        }
+    }
+    __device__ static __forceinline__ TG_LDS char* staged(TG_LDS char* mine, int row, int c) {
+        return mine + row * (WTN * 4) + (c ^ (row & (WTN / 4 - 1))) * 16;
+    }
+    template <class Data, class Fetch, class Each>
+    __device__ static __forceinline__ void each_row(const Acc& acc, TG_LDS char* smem, int lane, int wave, Fetch fetch, Each each) {
         TG_LDS char* mine = smem + wave * (32 * WTN * 4);
-        auto at = [&](int row, int c) { return mine + row * (WTN * 4) + (c ^ (row & (CH - 1))) * 16; };
-#pragma unroll
+        const int r0 = lane / PER_ROW, c = 2 * (lane % PER_ROW);
+#pragma unroll 1
         for (int i = 0; i < FM; ++i) {
+            Data data[PIECES];
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    *reinterpret_cast<TG_LDS f32x4*>(at(lane & 31, 8 * j + 2 * r + (lane >> 5))) =
-                        f32x4{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
+            for (int q = 0; q < PIECES; ++q) fetch(32 * i + q * ROWS + r0, 4 * c, data[q]);
+            stage<0>(i, acc, mine, lane);
             asm volatile("" ::: "memory");  // a wave's LDS accesses stay in order
-#pragma unroll 2
-            for (int q = 0; q < 32 / ROWS; ++q) {
-                const int row = q * ROWS + lane / PER_ROW, c = 2 * (lane % PER_ROW);
+#pragma unroll
+            for (int q = 0; q < PIECES; ++q) {
+                const int row = q * ROWS + r0;
                 float v[8], w[8];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const f32x4 x = *reinterpret_cast<const TG_LDS f32x4*>(at(row, c + h));
+                    const f32x4 x = *reinterpret_cast<const TG_LDS f32x4*>(staged(mine, row, c + h));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[4 * h + e] = x[e];
                     if constexpr (PAIR) {
-                        const f32x4 y = *reinterpret_cast<const TG_LDS f32x4*>(at(row, CH / 2 + c + h));
+                        const f32x4 y = *reinterpret_cast<const TG_LDS f32x4*>(staged(mine, row, WTN / 8 + c + h));
 #pragma unroll
                         for (int e = 0; e < 4; ++e) w[4 * h + e] = y[e];
                     }
                 }
-                each(32 * i + row, 4 * c, v, w);
+                each(32 * i + row, 4 * c, v, w, data[q]);
             }
             asm volatile("" ::: "memory");
         }
+    }
+    struct Nothing {};
+    template <class Each>
+    __device__ static __forceinline__ void each_row(const Acc& acc, TG_LDS char* smem, int lane, int wave, Each each) {
+        each_row<Nothing>(acc, smem, lane, wave, [](int, int, Nothing&) {},
+                          [&](int r, int c, float (&v)[8], float (&w)[8], Nothing&) { each(r, c, v, w); });
     }
 };
 
@@ -437,15 +479,25 @@ __device__ __forceinline__ void store8(T* dst, const float (&v)[8], int count) {
             if (e < count) dst[e] = o[e];
     }
 }
+// 8 values as they stand in memory, zeros past the row's end.
+struct Raw8 {
+    i32x4 v;
+};
 template <class T>
-__device__ __forceinline__ void load8(float (&v)[8], const T* src, int count) {
-    T o[8];
+__device__ __forceinline__ void load8(Raw8& x, const T* src, int count) {
     if (count >= 8) {
-        __builtin_memcpy(o, src, 16);
+        x.v = load16(src);
     } else {
+        union { i32x4 v; T e[8]; } u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = load_or_zero(src + e, e < count);
+        for (int e = 0; e < 8; ++e) u.e[e] = load_or_zero(src + e, e < count);
+        x.v = u.v;
     }
+}
+template <class T>
+__device__ __forceinline__ void values8(float (&v)[8], const Raw8& x) {
+    T o[8];
+    __builtin_memcpy(o, &x.v, 16);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = (float)o[e];
 }

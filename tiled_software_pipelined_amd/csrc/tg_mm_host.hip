@@ -28,45 +28,52 @@ const MmKernel* mm_kernels(int dtype, int form) {
     return dtype == TGEMM_BF16 ? mm_kernels_bf16(form) : mm_kernels_f16(form);
 }
 
-static int tile_m(int s) { return s == SIZE_256 ? 256 : s == SIZE_128 ? 128 : 64; }
-static int tile_n(int form, int s) { return (s == SIZE_256 ? 256 : 128) / (form == FORM_GATE ? 2 : 1); }
-
-// Microseconds of one launch.
-static double mm_time(int form, int size, double tiles, double slices) {
-    (void)form;
-    const double slots = size == SIZE_256 ? 256.0 : 512.0;
-    const double slice = size == SIZE_256 ? 0.43 : size == SIZE_128 ? 0.30 : 0.20;
-    const double alone = size == SIZE_256 ? 0.43 : size == SIZE_128 ? 0.22 : 0.14;
-    if (tiles <= 256.0) return 4.0 + alone * slices;
-    return 4.0 + ceil(tiles / slots) * (1.0 + slice * slices);
+static double tiles_of(const MmKernel& k, const MmShape* shapes, int jobs) {
+    double n = 0.0;
+    for (int i = 0; i < jobs; ++i)
+        n += (double)((shapes[i].M + k.bm - 1) / k.bm) * (double)((shapes[i].N + k.bn - 1) / k.bn);
+    return n;
 }
 
-MmPlan mm_plan(int form, const MmShape* shapes, int jobs, int64_t slices, bool may_split) {
-    MmPlan best{SIZE_64, 1, (int)(slices > 0 ? slices : 1)};
-    double least = -1.0, area = 0.0;
-    for (int i = 0; i < jobs; ++i) area += (double)shapes[i].M * (double)shapes[i].N;
+// Microseconds of one launch.
+static double mm_time(const MmKernel& k, double tiles, int64_t slices, bool may_split) {
+    const double slice = k.slice * 1e-3;
+    if (tiles > 1e6) return 4.0 + tiles / k.slots * slice * (double)slices;
+    const MmSchedule s = mm_schedule((int)tiles, (int)slices, k.slots, k.slice, k.tile_kb, may_split);
+    // a lone workgroup on a compute unit is quicker than two
+    auto alone = [&](int n) { return n <= 256 && k.slots > 256 ? 0.65 : 1.0; };
+    double t = 4.0 + ceil(s.full / (double)k.slots) * (1.0 + alone((int)tiles) * slice * (double)slices);
+    if (s.rest) t += alone(s.rest * s.splits) * slice * s.per + 7.0 + s.rest * s.splits * k.tile_kb * 0.4e-3;
+    return t;
+}
+
+MmSize mm_size(int form, const MmShape* shapes, int jobs, int64_t slices, bool may_split) {
+    MmSize best = SIZE_64;
+    double least = -1.0;
+    const MmKernel* table = mm_kernels(TGEMM_BF16, form);  // the types' tiles are alike
     for (int s = 0; s < SIZE_COUNT; ++s) {
-        double tiles = 0.0;
-        for (int i = 0; i < jobs; ++i)
-            tiles += (double)((shapes[i].M + tile_m(s) - 1) / tile_m(s)) * (double)((shapes[i].N + tile_n(form, s) - 1) / tile_n(form, s));
-        for (int splits = 1; splits <= 16; ++splits) {
-            const int64_t per = (slices + splits - 1) / splits;
-            if (splits > 1 && (!may_split || per < 8 || tiles * splits > 1024.0)) break;
-            if (splits > 1 && (splits - 1) * per >= slices) continue;  // a part would be empty
-            double t = mm_time(form, s, tiles * splits, (double)per);
-            // sums written and read again, and another launch
-            if (splits > 1) t += 3.0 + area * (8.0 * splits + 2.0) / 4e6;
-            if (least < 0.0 || t < least) {
-                least = t;
-                best = MmPlan{(MmSize)s, splits, (int)(per > 0 ? per : 1)};
-            }
+        const double t = mm_time(table[s], tiles_of(table[s], shapes, jobs), slices, may_split);
+        if (least < 0.0 || t < least) {
+            least = t;
+            best = (MmSize)s;
         }
     }
     return best;
 }
 
-MmGrid mm_grid(const MmKernel& k, const MmPlan& p, int64_t M, int64_t N) {
-    return MmGrid{(int32_t)((M + k.bm - 1) / k.bm), (int32_t)((N + k.bn - 1) / k.bn), p.splits, p.per};
+int64_t mm_split_bytes(int form, MmSize size, const MmShape* shapes, int jobs, int64_t slices, bool fewer) {
+    const MmKernel& k = mm_kernels(TGEMM_BF16, form)[size];
+    const double tiles = tiles_of(k, shapes, jobs);
+    if (tiles > 1e6 || tiles < 1.0) return 0;
+    const int64_t tile = (int64_t)k.bm * k.bn * 4;
+    // up to `slots` parts, in any number of tiles
+    if (fewer) return k.slots * tile;
+    const MmSchedule s = mm_schedule((int)tiles, (int)slices, k.slots, k.slice, k.tile_kb, true);
+    return s.rest * s.splits * tile;
+}
+
+MmGrid mm_grid(const MmKernel& k, int64_t M, int64_t N) {
+    return MmGrid{(int32_t)((M + k.bm - 1) / k.bm), (int32_t)((N + k.bn - 1) / k.bn)};
 }
 
 int mm_launch(const void* fn, int64_t workgroups, int threads, void* args, const char* name, hipStream_t stream) {
@@ -83,100 +90,43 @@ int mm_launch(const void* fn, int64_t workgroups, int threads, void* args, const
     return TGEMM_OK;
 }
 
-int mm_store(int dtype, int form, const MmPlan& plan, const MmStoreArgs& given, hipStream_t stream) {
-    const MmKernel& k = mm_kernels(dtype, form)[plan.size];
-    MmStoreArgs args{};
-    args.alpha = given.alpha;
-    args.rows = given.rows;
-    args.rows_are_k = given.rows_are_k;
-    args.map = given.map;
-    int64_t n = 0;
+int mm_store(int dtype, int form, MmSize size, const MmStoreArgs& given, hipStream_t stream) {
+    const MmKernel& k = mm_kernels(dtype, form)[size];
+    MmStoreArgs args = given;
+    args.jobs = 0;
+    double tiles = 0.0;
     for (int i = 0; i < given.jobs; ++i) {
         const MmOperands& o = given.job[i].op[0];
         if (o.M == 0 || o.N == 0) continue;
         MmJob& j = args.job[args.jobs++];
         j = given.job[i];
-        j.grid = mm_grid(k, plan, o.M, o.N);
-        n += (int64_t)j.grid.tiles_m * j.grid.tiles_n * j.grid.splits;
+        j.grid = mm_grid(k, o.M, o.N);
+        tiles += (double)j.grid.tiles_m * j.grid.tiles_n;
     }
-    return n == 0 ? TGEMM_OK : mm_launch(k.fn, n, k.threads, &args, "product", stream);
+    if (args.jobs == 0) return TGEMM_OK;
+    if (tiles > 1e6) args.split = nullptr;
+    if (tiles > INT_MAX / 2) {
+        set_error("product: too many tiles");
+        return TGEMM_E_ARG;
+    }
+    int64_t slices = 0;
+    for (int p = 0; p < args.job[0].pairs; ++p) slices += mm_slices(args.job[0].op[p].K);
+    const MmSchedule s = mm_schedule((int)tiles, (int)slices, k.slots, k.slice, k.tile_kb, args.split != nullptr);
+    // fewer rows than the host knows of may be shared out in up to `slots` parts
+    const bool fewer = args.rows && args.split;
+    int rc = mm_launch(k.fn, fewer ? (int64_t)tiles + k.slots : s.total(), k.threads, &args, "product", stream);
+    const int64_t rest = fewer ? (tiles < k.slots / 2 ? (int64_t)tiles : k.slots / 2) : s.rest;
+    if (rc == TGEMM_OK && args.split && rest > 0) rc = mm_launch(k.join, rest * (k.bm * k.bn / 2048), 256, &args, "join", stream);
+    return rc;
 }
 
-// ---- partial sums ------------------------------------------------------------
-struct JoinArgs {
-    struct {
-        const float* part;
-        void* C;
-        int64_t ldc, M, N, stride;  // stride: floats from a split to the next
-        int64_t first;              // workgroups before this job's
-    } job[3];
-    int32_t jobs, splits;
-    const float* alpha;
-    const int32_t *rows, *map;  // NULL, or as MmStoreArgs has them
-};
-
-// 4 adjacent columns a thread, splits in order (the result does not depend on
-// who finished first).
-template <class T>
-__global__ __launch_bounds__(256) void mm_join_kernel(JoinArgs g) {
-    int which = 0;
-    while (which + 1 < g.jobs && (int64_t)blockIdx.x >= g.job[which + 1].first) ++which;
-    const auto& j = g.job[which];
-    const int64_t quads = (j.N + 3) / 4, q = ((int64_t)blockIdx.x - j.first) * 256 + threadIdx.x;
-    if (q >= (g.rows ? *g.rows : j.M) * quads) return;
-    const int64_t m = q / quads, n = (q - m * quads) * 4;
-    const int count = (int)min(j.N - n, (int64_t)4);
-    const float* p = j.part + m * j.N + n;
-    float v[4] = {0, 0, 0, 0};
-    for (int s = 0; s < g.splits; ++s, p += j.stride) {
-        float x[4] = {0, 0, 0, 0};
-        if (count == 4) {
-            __builtin_memcpy(x, p, 16);
-        } else {
-            for (int e = 0; e < 3; ++e)
-                if (e < count) x[e] = p[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += x[e];
-    }
-    const float alpha = g.alpha ? *g.alpha : 1.0f;
-    T o[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = (T)(v[e] * alpha);
-    T* dst = static_cast<T*>(j.C) + (g.map ? g.map[m] : m) * j.ldc + n;
-    if (count == 4) {
-        __builtin_memcpy(dst, o, 8);
-    } else {
-        for (int e = 0; e < 3; ++e)
-            if (e < count) dst[e] = o[e];
-    }
-}
-
-int mm_join(int dtype, const MmPlan& plan, const MmStoreArgs& args, hipStream_t stream) {
-    JoinArgs g{};
-    int64_t n = 0;
-    for (int i = 0; i < args.jobs; ++i) {
-        const MmJob& a = args.job[i];
-        const int64_t M = a.op[0].M, N = a.op[0].N;
-        if (M == 0 || N == 0) continue;
-        auto& j = g.job[g.jobs++];
-        j.part = a.part;
-        j.C = a.C;
-        j.ldc = a.ldc;
-        j.M = M;
-        j.N = N;
-        j.stride = M * N;
-        j.first = n;
-        n += (M * ((N + 3) / 4) + 255) / 256;
-    }
-    if (n == 0) return TGEMM_OK;
-    g.splits = plan.splits;
-    g.alpha = args.alpha;
-    if (!args.rows_are_k) g.rows = args.rows;
-    g.map = args.map;
-    const void* fn = dtype == TGEMM_BF16 ? reinterpret_cast<const void*>(mm_join_kernel<__bf16>)
-                                         : reinterpret_cast<const void*>(mm_join_kernel<_Float16>);
-    return mm_launch(fn, n, 256, &g, "join", stream);
+int mm_round(int dtype, const MmStoreArgs& args, hipStream_t stream) {
+    MmStoreArgs a = args;
+    const int64_t M = a.job[0].op[0].M, N = a.job[0].op[0].N;
+    if (M == 0 || N == 0) return TGEMM_OK;
+    const void* fn = dtype == TGEMM_BF16 ? reinterpret_cast<const void*>(mm_round_kernel<__bf16>)
+                                         : reinterpret_cast<const void*>(mm_round_kernel<_Float16>);
+    return mm_launch(fn, (M * ((N + 3) / 4) + 255) / 256, 256, &a, "rounding", stream);
 }
 
 // ---- arguments -----------------------------------------------------------------

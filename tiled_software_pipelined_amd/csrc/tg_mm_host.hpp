@@ -14,30 +14,29 @@ namespace tg {
 constexpr int64_t MM_MOST = INT64_C(1) << 22;
 constexpr int64_t MM_MOST_ROWS = INT64_C(1) << 30;
 
-// How a product is laid out on the machine.
-struct MmPlan {
-    MmSize size;
-    int splits, per;  // parts of k, slices of 64 k each
-};
-
 const MmKernel* mm_kernels(int dtype, int form);
-// The plan of one launch's products, each M x N with this many slices of k; and
-// the bytes of one product's partial sums, 0 without a split.
+inline int64_t mm_slices(int64_t K) { return (K + 63) / 64; }
+
+// The tile of one launch's products, each M x N with this many slices of k.
 struct MmShape {
     int64_t M, N;
 };
-MmPlan mm_plan(int form, const MmShape* shapes, int jobs, int64_t slices, bool may_split);
-inline int64_t mm_part_bytes(const MmPlan& p, int64_t M, int64_t N, bool add) {
-    return p.splits > 1 || add ? (4 * p.splits * M * N + 255) / 256 * 256 : 0;
+MmSize mm_size(int form, const MmShape* shapes, int jobs, int64_t slices, bool may_split);
+inline MmSize mm_size(int form, int64_t M, int64_t N, int64_t slices, bool may_split) {
+    const MmShape s{M, N};
+    return mm_size(form, &s, 1, slices, may_split);
 }
-inline int64_t mm_slices(int64_t K) { return (K + 63) / 64; }
-MmGrid mm_grid(const MmKernel& k, const MmPlan& p, int64_t M, int64_t N);
+// Bytes for the sums of tiles that a launch shares out (MmStoreArgs::split), for
+// as many rows as given or, where only the device knows them (`fewer`), less.
+int64_t mm_split_bytes(int form, MmSize size, const MmShape* shapes, int jobs, int64_t slices, bool fewer);
 
-// Launches `jobs` products of the store forms by one plan; jobs without rows or
-// columns are left out.  Partial sums (job.part set) are not joined here.
-int mm_store(int dtype, int form, const MmPlan& plan, const MmStoreArgs& args, hipStream_t stream);
-// C = alpha sum of the jobs' partial sums.
-int mm_join(int dtype, const MmPlan& plan, const MmStoreArgs& args, hipStream_t stream);
+MmGrid mm_grid(const MmKernel& k, int64_t M, int64_t N);
+
+// Launches products of the store forms on tiles of one size, and the join of
+// what it shares out; jobs without rows or columns are left out.
+int mm_store(int dtype, int form, MmSize size, const MmStoreArgs& args, hipStream_t stream);
+// The first job's float sums into its C.
+int mm_round(int dtype, const MmStoreArgs& args, hipStream_t stream);
 int mm_launch(const void* fn, int64_t workgroups, int threads, void* args, const char* name, hipStream_t stream);
 
 // A tensor argument's checks: rows x cols of `dtype`, leading dimension ld.

@@ -8,10 +8,38 @@
 
 namespace tg {
 
-// Workgroup rank -> (split of k, tile) of a job with this many tiles.
 struct MmGrid {
-    int32_t tiles_m, tiles_n, splits, per;  // per: slices of 64 k a split takes
+    int32_t tiles_m, tiles_n;
 };
+
+// How a launch's tiles are dealt to the compute units.  `slots` workgroups are on
+// the machine at once: the first `full` tiles fill it whole times, and the rest
+// are shared out along k, `splits` workgroups a tile of `per` slices each, whose
+// sums are joined by a kernel of its own.  Sharing costs that launch and the
+// sums' way through memory: about 6 us and 2.5 TB/s, against (1 - 1 / splits) of a
+// tile's slices at `slice` ns each.  Host and device come to the same answer
+// (whole numbers).
+struct MmSchedule {
+    int32_t full, rest, splits, per;
+    __host__ __device__ __forceinline__ int total() const { return full + rest * splits; }
+};
+constexpr int MM_SPLITS = 16;
+__host__ __device__ __forceinline__ MmSchedule mm_schedule(int tiles, int slices, int slots, int slice, int tile_kb, bool may_split) {
+    MmSchedule s{tiles, 0, 1, slices};
+    const int rest = tiles % slots;
+    if (!may_split || rest == 0 || 2 * rest > slots || slices < 8) return s;
+    int64_t least = (int64_t)slices * slice;
+    for (int n = 2; n <= MM_SPLITS && n * rest <= slots && slices >= 4 * n; ++n) {
+        const int per = (slices + n - 1) / n;
+        if ((n - 1) * per >= slices) continue;  // a part would be empty
+        const int64_t t = (int64_t)per * slice + 6000 + n * rest * tile_kb * 2 / 5;
+        if (t < least) {
+            least = t;
+            s = MmSchedule{tiles - rest, rest, n, per};
+        }
+    }
+    return s;
+}
 
 // ---- products that are only stored -------------------------------------------
 // One C = alpha (a b^T [+ a' b'^T]); up to three of them share a launch.
@@ -21,8 +49,8 @@ struct MmJob {
     MmGrid grid;
     void* C;        // result, row stride ldc elements
     int64_t ldc;
-    float* part;    // not NULL: float sums instead, split s at part + s M N
-    int32_t add;    // part: add to what is there
+    float* sum;     // not NULL: float sums (M x N) instead
+    int32_t add;    // sum: add to what is there
 };
 struct MmStoreArgs {
     MmJob job[3];
@@ -33,13 +61,15 @@ struct MmStoreArgs {
     const int32_t* rows;
     int32_t rows_are_k;
     const int32_t* map;  // not NULL: row m of the result is row map[m] of C
+    float* split;        // not NULL: room for the sums of tiles that are shared out
 };
 
 // ---- gated feed-forward: gate and up projections ---------------------------------
 struct MmGateArgs {
     MmOperands op;
     MmGrid grid;
-    void *h, *g, *u;  // M x N, row stride N; g and u NULL where nothing is kept
+    void *h, *g, *u;  // M x N, row stride ld; g and u NULL where nothing is kept
+    int64_t ld;
     int32_t act;
 };
 // ---- its backward: dh = dy Wd, then dg, du and h from it and g, u ----------------
@@ -47,7 +77,8 @@ struct MmDhArgs {
     MmOperands op;
     MmGrid grid;
     const void *g, *u;
-    void *dg, *du, *h;  // M x N, row stride N; any of them NULL where it is not wanted
+    void *dg, *du, *h;  // M x N, row stride ld (g's and u's too); any of them NULL where it is not wanted
+    int64_t ld;
     int32_t act;
 };
 
@@ -123,14 +154,12 @@ __device__ __forceinline__ void activate8(int act, const float (&g)[8], float (&
 // Where a workgroup's tile is, and its wave's block.
 template <class G>
 struct MmPlace {
-    int m0, n0, wm0, wn0, wave, lane, split;
-    __device__ __forceinline__ MmPlace(const MmGrid& g, int rank) {
+    int m0, n0, wm0, wn0, wave, lane;
+    __device__ __forceinline__ MmPlace(const MmGrid& g, int tile) {
         wave = wave_id();
         lane = lane_id();
-        const int tiles = g.tiles_m * g.tiles_n;
-        split = g.splits > 1 ? rank / tiles : 0;
         int tm, tn;
-        grouped_tile(rank - split * tiles, g.tiles_m, g.tiles_n, 4, tm, tn);
+        grouped_tile(tile, g.tiles_m, g.tiles_n, 4, tm, tn);
         m0 = tm * G::BM;
         n0 = tn * G::TILE_N;
         wm0 = (wave / G::WAVES_N) * G::WTM;
@@ -141,65 +170,104 @@ struct MmPlace {
     __device__ __forceinline__ int col0() const { return n0 + (wn0 / G::WTN) * G::WAVE_N; }
 };
 
+// The tiles of a launch's jobs, with what only the device knows.
+struct MmTilesOf {
+    int M, most_k, tiles, slices;  // M: of a lone job
+    MmGrid grid;                   // likewise
+};
+template <int BM>
+__device__ __forceinline__ MmTilesOf mm_tiles(const MmStoreArgs& g) {
+    MmTilesOf t;
+    t.grid = g.job[0].grid;
+    t.M = g.job[0].op[0].M;
+    t.most_k = INT_MAX;
+    if (g.rows) {
+        const int rows = *g.rows;
+        if (g.rows_are_k) {
+            t.most_k = rows;
+        } else {
+            t.M = rows;
+            t.grid.tiles_m = (rows + BM - 1) / BM;
+        }
+    }
+    t.tiles = t.grid.tiles_m * t.grid.tiles_n;
+    for (int i = 1; i < g.jobs; ++i) t.tiles += g.job[i].grid.tiles_m * g.job[i].grid.tiles_n;
+    t.slices = 0;
+    for (int p = 0; p < g.job[0].pairs; ++p) t.slices += (min(g.job[0].op[p].K, t.most_k) + 63) / 64;
+    return t;
+}
+// The job of a tile; `tile` becomes its number there.
+__device__ __forceinline__ int mm_job_of(const MmStoreArgs& g, int& tile) {
+    int which = 0;
+    for (; which + 1 < g.jobs; ++which) {
+        const int n = g.job[which].grid.tiles_m * g.job[which].grid.tiles_n;
+        if (tile < n) break;
+        tile -= n;
+    }
+    return which;
+}
+
 template <class G>
 __global__ __launch_bounds__(G::NT) void mm_store_kernel(MmStoreArgs g) {
     __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
     TG_LDS char* smem = (TG_LDS char*)smem_raw;
-    int which = 0, total = gridDim.x, M = g.job[0].op[0].M, most_k = INT_MAX;
-    MmGrid grid = g.job[0].grid;
-    if (g.rows) {
-        const int rows = *g.rows;
-        if (g.rows_are_k) {
-            most_k = rows;
-            grid.per = ((rows + 63) / 64 + grid.splits - 1) / grid.splits;
-        } else {
-            M = rows;
-            grid.tiles_m = (rows + G::BM - 1) / G::BM;
-            total = grid.tiles_m * grid.tiles_n * grid.splits;
-            if ((int)blockIdx.x >= total) return;
-        }
+    MmTilesOf all = mm_tiles<G::BM>(g);
+    const MmSchedule plan = mm_schedule(all.tiles, all.slices, G::SLOTS, G::SLICE_NS, G::TILE_KB, g.split != nullptr);
+    int tile = blockIdx.x, split = 0, t0 = 0, t1 = all.slices;
+    if (tile >= plan.total()) return;
+    float* shared = nullptr;
+    if (tile < plan.full) {
+        tile = xcd_rank(tile, plan.full);
+    } else {
+        // parts in the order of their k: workgroups of one XCD share operands
+        const int r = xcd_rank(tile - plan.full, plan.rest * plan.splits);
+        split = r / plan.rest;
+        tile = r - split * plan.rest;
+        shared = g.split + (int64_t)(tile * plan.splits + split) * (G::BM * G::BN);
+        tile += plan.full;
+        t0 = split * plan.per;
+        t1 = min(t0 + plan.per, all.slices);
     }
-    int rank = xcd_rank(blockIdx.x, total);
+    const int which = mm_job_of(g, tile);
     if (g.jobs > 1) {
-        for (; which + 1 < g.jobs; ++which) {
-            const MmGrid& r = g.job[which].grid;
-            const int n = r.tiles_m * r.tiles_n * r.splits;
-            if (rank < n) break;
-            rank -= n;
-        }
-        M = g.job[which].op[0].M;
-        grid = g.job[which].grid;
+        all.M = g.job[which].op[0].M;
+        all.grid = g.job[which].grid;
     }
     const MmJob& job = g.job[which];
-    const MmPlace<G> at(grid, rank);
+    const MmPlace<G> at(all.grid, tile);
     typename G::Acc acc;
     G::clear(acc);
-    int t0 = at.split * grid.per, t1 = t0 + grid.per;
     for (int p = 0; p < job.pairs; ++p) {
         MmOperands op = job.op[p];
-        op.M = M;
-        op.K = min(op.K, most_k);
+        op.M = all.M;
+        op.K = min(op.K, all.most_k);
         const int slices = (op.K + 63) / 64;
         if (t0 < slices && t1 > 0)
             G::product(op, at.m0, at.n0, max(t0, 0), min(t1, slices), smem, acc, at.wm0, at.wn0, at.lane, at.wave);
         t0 -= slices;
         t1 -= slices;
     }
-    const int N = job.op[0].N, m1 = at.row0(), n1 = at.col0();
-    if (job.part) {
-        float* part = job.part + (int64_t)at.split * job.op[0].M * N;
+    const int M = all.M, N = job.op[0].N, m1 = at.row0(), n1 = at.col0();
+    if (shared) {
+        float* mine = shared + (int64_t)at.wm0 * G::BN + at.wn0;
+        G::each_row(acc, smem, at.lane, at.wave,
+                    [&](int r, int c, float (&v)[8], float (&)[8]) { __builtin_memcpy(mine + r * G::BN + c, v, 32); });
+    } else if (job.sum) {
+        float* sum = job.sum;
         const bool add = job.add != 0;
-        G::each_row(acc, smem, at.lane, at.wave, [&](int r, int c, float (&v)[8], float (&)[8]) {
+        struct Before {
+            f32x4 v[2];
+        };
+        G::template each_row<Before>(acc, smem, at.lane, at.wave, [&](int r, int c, Before& b) {
+            const int m = m1 + r, n = n1 + c;
+            if (add && m < M && n + 8 <= N) __builtin_memcpy(&b, sum + (int64_t)m * N + n, 32);
+        }, [&](int r, int c, float (&v)[8], float (&)[8], Before& b) {
             const int m = m1 + r, n = n1 + c;
             if (m >= M || n >= N) return;
-            float* dst = part + (int64_t)m * N + n;
+            float* dst = sum + (int64_t)m * N + n;
             if (n + 8 <= N) {
-                if (add) {
-                    float o[8];
-                    __builtin_memcpy(o, dst, 32);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] += o[e];
-                }
+                for (int e = 0; e < 8; ++e) v[e] = add ? v[e] + b.v[e >> 2][e & 3] : v[e];
                 __builtin_memcpy(dst, v, 32);
             } else {
 #pragma unroll
@@ -212,13 +280,84 @@ __global__ __launch_bounds__(G::NT) void mm_store_kernel(MmStoreArgs g) {
         const float alpha = g.alpha ? *g.alpha : 1.0f;
         T* C = static_cast<T*>(job.C);
         const int64_t ldc = job.ldc;
-        G::each_row(acc, smem, at.lane, at.wave, [&](int r, int c, float (&v)[8], float (&)[8]) {
+        struct Row {
+            int to;
+        };
+        G::template each_row<Row>(acc, smem, at.lane, at.wave, [&](int r, int, Row& row) {
+            row.to = g.map && m1 + r < M ? g.map[m1 + r] : m1 + r;
+        }, [&](int r, int c, float (&v)[8], float (&)[8], Row& row) {
             const int m = m1 + r, n = n1 + c;
             if (m >= M || n >= N) return;
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] *= alpha;
-            store8(C + (g.map ? g.map[m] : m) * ldc + n, v, N - n);
+            store8(C + row.to * ldc + n, v, N - n);
         });
+    }
+}
+
+// C = alpha sum of the parts of the tiles that mm_store_kernel shared out, in the
+// order of k (whoever ended first).  A workgroup takes 2048 results of a tile.
+template <class T, int BM, int BN, int SLOTS>
+__device__ __forceinline__ void mm_join(const MmStoreArgs& g, int slice, int tile_kb) {
+    constexpr int PER = BM * BN / 2048;
+    const MmTilesOf all = mm_tiles<BM>(g);
+    const MmSchedule plan = mm_schedule(all.tiles, all.slices, SLOTS, slice, tile_kb, true);
+    int tile = blockIdx.x / PER;
+    if (tile >= plan.rest) return;
+    const int e = (blockIdx.x % PER) * 2048 + threadIdx.x * 8;
+    const float* p = g.split + (int64_t)tile * plan.splits * (BM * BN) + e;
+    tile += plan.full;
+    const int which = mm_job_of(g, tile);
+    const MmJob& job = g.job[which];
+    const MmGrid grid = g.jobs > 1 ? job.grid : all.grid;
+    int tm, tn;
+    grouped_tile(tile, grid.tiles_m, grid.tiles_n, 4, tm, tn);
+    const int m = tm * BM + e / BN, n = tn * BN + e % BN, M = g.jobs > 1 ? job.op[0].M : all.M, N = job.op[0].N;
+    if (m >= M || n >= N) return;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = 0; s < plan.splits; ++s, p += BM * BN) {
+        float x[8];
+        __builtin_memcpy(x, p, 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += x[i];
+    }
+    const float alpha = g.alpha ? *g.alpha : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= alpha;
+    store8(static_cast<T*>(job.C) + (int64_t)(g.map ? g.map[m] : m) * job.ldc + n, v, N - n);
+}
+template <class G>
+__global__ __launch_bounds__(256) void mm_join_kernel(MmStoreArgs g) {
+    mm_join<typename G::T, G::BM, G::BN, G::SLOTS>(g, G::SLICE_NS, G::TILE_KB);
+}
+
+// A float sum (job.sum) in the result's type and place, 4 columns a thread.
+template <class T>
+__global__ __launch_bounds__(256) void mm_round_kernel(MmStoreArgs g) {
+    const MmJob& job = g.job[0];
+    const int64_t N = job.op[0].N, quads = (N + 3) / 4, q = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (q >= (g.rows ? *g.rows : job.op[0].M) * quads) return;
+    const int64_t m = q / quads, n = (q - m * quads) * 4;
+    const int count = (int)min(N - n, (int64_t)4);
+    const float* p = job.sum + m * N + n;
+    float v[4] = {0, 0, 0, 0};
+    if (count == 4) {
+        __builtin_memcpy(v, p, 16);
+    } else {
+        for (int e = 0; e < 3; ++e)
+            if (e < count) v[e] = p[e];
+    }
+    const float alpha = g.alpha ? *g.alpha : 1.0f;
+    T o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = (T)(v[e] * alpha);
+    T* dst = static_cast<T*>(job.C) + (g.map ? g.map[m] : m) * job.ldc + n;
+    if (count == 4) {
+        __builtin_memcpy(dst, o, 8);
+    } else {
+        for (int e = 0; e < 3; ++e)
+            if (e < count) dst[e] = o[e];
     }
 }
 
@@ -235,7 +374,7 @@ __global__ __launch_bounds__(G::NT) void mm_gate_kernel(MmGateArgs g) {
     G::each_row(acc, smem, at.lane, at.wave, [&](int r, int c, float (&v)[8], float (&w)[8]) {
         const int m = m1 + r, n = n1 + c;
         if (m >= M || n >= N) return;
-        const int64_t to = (int64_t)m * N + n;
+        const int64_t to = (int64_t)m * g.ld + n;
         if (g.g) {
             store8(static_cast<T*>(g.g) + to, v, N - n);
             store8(static_cast<T*>(g.u) + to, w, N - n);
@@ -259,13 +398,22 @@ __global__ __launch_bounds__(G::NT) void mm_dh_kernel(MmDhArgs g) {
     G::clear(acc);
     G::product(g.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, smem, acc, at.wm0, at.wn0, at.lane, at.wave);
     const int M = g.op.M, N = g.op.N, m1 = at.row0(), n1 = at.col0();
-    G::each_row(acc, smem, at.lane, at.wave, [&](int r, int c, float (&v)[8], float (&)[8]) {
+    struct Kept {
+        Raw8 g, u;
+    };
+    G::template each_row<Kept>(acc, smem, at.lane, at.wave, [&](int r, int c, Kept& k) {
+        const int m = m1 + r, n = n1 + c;
+        if (m >= M || n >= N) return;
+        const int64_t to = (int64_t)m * g.ld + n;
+        load8(k.g, static_cast<const T*>(g.g) + to, N - n);
+        load8(k.u, static_cast<const T*>(g.u) + to, N - n);
+    }, [&](int r, int c, float (&v)[8], float (&)[8], Kept& k) {
         const int m = m1 + r, n = n1 + c, count = N - n;
         if (m >= M || n >= N) return;
-        const int64_t to = (int64_t)m * N + n;
+        const int64_t to = (int64_t)m * g.ld + n;
         float gate[8], up[8], a[8], d[8], o[8];
-        load8(gate, static_cast<const T*>(g.g) + to, count);
-        load8(up, static_cast<const T*>(g.u) + to, count);
+        values8<T>(gate, k.g);
+        values8<T>(up, k.u);
         activate8<true>(g.act, gate, a, d);
         // roundings of dg, du, h: operands of the products that follow
         if (g.dg) {
@@ -365,26 +513,29 @@ __global__ __launch_bounds__(G::NT) void mm_dz_kernel(MmDzArgs g) {
     typename G::Acc acc;
     G::clear(acc);
     G::product(known.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, smem, acc, at.wm0, at.wn0, at.lane, at.wave);
-    const int M = known.op.M, N = g.op.N, m1 = at.row0(), n1 = at.col0(), half = 4 * (at.lane >> 5);
-#pragma unroll
-    for (int i = 0; i < G::FM; ++i) {
-        const int m = m1 + 32 * i + (at.lane & 31);
-        const float coef = m < M ? g.coef[m] : 0.0f, lse = m < M ? g.lse[m] : 0.0f;
-        const int64_t t = (m < M ? g.target[g.map[m]] - g.v0 : -1) - n1;
-        const int want = t >= 0 && t < G::WTN ? (int)t : -1;
-#pragma unroll
-        for (int j = 0; j < G::FN; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                float p = __builtin_amdgcn_exp2f((acc[i][j][r] - lse) * LOG2E);
-                if (32 * j + 8 * (r >> 2) + half + (r & 3) == want) p -= 1.0f;
-                acc[i][j][r] = p * coef;
-            }
-    }
+    const int M = known.op.M, N = g.op.N, m1 = at.row0(), n1 = at.col0();
     T* dz = static_cast<T*>(g.dz);
-    G::each_row(acc, smem, at.lane, at.wave, [&](int r, int c, float (&v)[8], float (&)[8]) {
+    struct Row {
+        float lse, coef;
+        int64_t target;
+    };
+    G::template each_row<Row>(acc, smem, at.lane, at.wave, [&](int r, int, Row& row) {
+        const int m = min(m1 + r, M - 1);
+        row.lse = g.lse[m];
+        row.coef = g.coef[m];
+        row.target = g.target[g.map[m]] - g.v0;
+    }, [&](int r, int c, float (&v)[8], float (&)[8], Row& row) {
         const int m = m1 + r, n = n1 + c;
-        if (m < M && n < N) store8(dz + m * g.ldz + n, v, N - n);
+        if (m >= M || n >= N) return;
+        const int64_t t = row.target - n;
+        const int hit = t >= 0 && t < 8 ? (int)t : -1;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float p = __builtin_amdgcn_exp2f((v[e] - row.lse) * LOG2E);
+            if (e == hit) p -= 1.0f;
+            v[e] = p * row.coef;
+        }
+        store8(dz + m * g.ldz + n, v, N - n);
     });
 }
 
@@ -495,9 +646,14 @@ __global__ __launch_bounds__(512) void mm_rows_kernel(MmRowsArgs g) {
 enum MmForm { FORM_NT = 0, FORM_NN, FORM_TN, FORM_GATE, FORM_DH, FORM_STATS, FORM_DZ, FORM_COUNT };
 enum MmSize { SIZE_256 = 0, SIZE_128, SIZE_64, SIZE_COUNT };
 struct MmKernel {
-    const void* fn;
+    const void *fn, *join;
     int bm, bn, threads;  // rows and columns of C a workgroup takes
+    int slots, slice, tile_kb;
 };
+template <class G>
+MmKernel mm_entry(const void* fn, const void* join = nullptr) {
+    return MmKernel{fn, join, G::BM, G::TILE_N, G::NT, G::SLOTS, G::SLICE_NS, G::TILE_KB};
+}
 
 // The tiles.  256 x 256: four waves of 128 x 128, one a SIMD.  128 x 128: four
 // waves, two workgroups a compute unit.  64 x 128: likewise.

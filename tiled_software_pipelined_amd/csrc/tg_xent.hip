@@ -21,13 +21,14 @@ namespace tg {
 constexpr int64_t XENT_PIECE = INT64_C(1) << 28;
 
 struct XentLayout {
-    MmPlan stats, dz, dx, dw;
+    MmSize stats, dz, dx, dw;
     int64_t parts;             // pieces of a row that the forward pass joins
     int64_t ldx;               // row stride of the gathered rows of x
     int64_t cols, ldz;         // backward: columns of a piece, row stride of dz
     int64_t count, map, rank, lse;                  // kept
     int64_t x, hit, each, part;                     // forward's scratch
-    int64_t x2, coef, alpha, dzs, dx_part, dw_part; // backward's
+    int64_t x2, coef, alpha, dzs, sum, split;       // backward's
+    int64_t split_bytes[2];                         // of dx's and dw's launches, which use the same room
     int64_t bytes[3];
 };
 
@@ -44,10 +45,9 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
     l.map = take(0, 4 * M);   // where they stand
     l.rank = take(0, 4 * M);  // each row's number among them, -1
     l.lse = take(0, 4 * M);   // of each of them
-    const MmShape z{M, V};
     l.ldx = (K + 63) / 64 * 64;
-    l.stats = mm_plan(FORM_STATS, &z, 1, mm_slices(K), false);
-    l.parts = (V + wave_cols(l.stats.size) - 1) / wave_cols(l.stats.size);
+    l.stats = mm_size(FORM_STATS, M, V, mm_slices(K), false);
+    l.parts = (V + wave_cols(l.stats) - 1) / wave_cols(l.stats);
     l.x = take(1, 2 * M * l.ldx);
     l.hit = take(1, 4 * M);   // the target's logit of each of them
     l.each = take(1, 4 * M);  // each row's loss
@@ -61,20 +61,23 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
     if (l.cols < 256) l.cols = 256;  // of an empty vocabulary too: the walk over pieces ends
     l.ldz = l.cols;
     const int64_t cols = l.cols < V ? l.cols : V;
-    const MmShape piece{M, cols}, dx{M, K}, dw{cols, K};
-    l.dz = mm_plan(FORM_DZ, &piece, 1, mm_slices(K), false);
+    const MmShape dx{M, K}, dw{cols, K};
+    l.dz = mm_size(FORM_DZ, M, cols, mm_slices(K), false);
     l.x2 = take(2, 2 * M * l.ldx);
     l.coef = take(2, 4 * M);
     l.alpha = take(2, 4);
     l.dzs = take(2, 2 * M * l.ldz);
     if (keep & TGEMM_KEEP_X) {
-        l.dx = mm_plan(FORM_NN, &dx, 1, mm_slices(cols), true);
-        l.dx_part = take(2, mm_part_bytes(l.dx, M, K, pieces > 1));
+        // the sums over several pieces are not shared out as well
+        l.dx = mm_size(FORM_NN, M, K, mm_slices(cols), pieces == 1);
+        if (pieces > 1) l.sum = take(2, 4 * M * K);
+        else l.split_bytes[0] = mm_split_bytes(FORM_NN, l.dx, &dx, 1, mm_slices(cols), true);
     }
     if (keep & TGEMM_KEEP_W) {
-        l.dw = mm_plan(FORM_TN, &dw, 1, mm_slices(M), true);
-        l.dw_part = take(2, mm_part_bytes(l.dw, cols, K, false));
+        l.dw = mm_size(FORM_TN, cols, K, mm_slices(M), true);
+        l.split_bytes[1] = mm_split_bytes(FORM_TN, l.dw, &dw, 1, mm_slices(M), true);
     }
+    l.split = take(2, l.split_bytes[0] > l.split_bytes[1] ? l.split_bytes[0] : l.split_bytes[1]);
     return l;
 }
 
@@ -353,10 +356,10 @@ int tgemm_xent_forward(int64_t M, int64_t V, int64_t K, int32_t dtype, const voi
     if (rc == TGEMM_OK && M > 0)
         rc = gather(x, ldx, M, K, rank, s + l.x, l.ldx, reduction == TGEMM_NONE ? loss : nullptr, nullptr, 0, st);
     if (rc == TGEMM_OK && M > 0 && V > 0) {
-        const MmKernel& k = mm_kernels(dtype, FORM_STATS)[l.stats.size];
+        const MmKernel& k = mm_kernels(dtype, FORM_STATS)[l.stats];
         MmStatsArgs a{MmOperands{s + l.x, static_cast<const char*>(w), nullptr, 2 * l.ldx, 2 * ldw, 0, (int32_t)M, (int32_t)V,
                                  (int32_t)K},
-                      mm_grid(k, l.stats, M, V), count, map, target, part, hit};
+                      mm_grid(k, M, V), count, map, target, part, hit};
         rc = mm_launch(k.fn, (int64_t)a.grid.tiles_m * a.grid.tiles_n, k.threads, &a, "logits", st);
     }
     if (rc == TGEMM_OK && M > 0) {
@@ -409,31 +412,31 @@ int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const vo
     into_x.jobs = into_w.jobs = 1;
     into_x.map = map;
     into_w.rows_are_k = 1;
+    if (l.split_bytes[0] > 0) into_x.split = reinterpret_cast<float*>(s + l.split);
+    if (l.split_bytes[1] > 0) into_w.split = reinterpret_cast<float*>(s + l.split);
     // at least one round: without a vocabulary dx is zero
     for (int64_t v0 = 0; rc == TGEMM_OK && (v0 < V || v0 == 0); v0 += l.cols) {
         const int64_t n = V - v0 < l.cols ? V - v0 : l.cols;
         const char* wv = wp + v0 * ldw * 2;
         if (M > 0 && n > 0) {
-            const MmKernel& k = mm_kernels(dtype, FORM_DZ)[l.dz.size];
+            const MmKernel& k = mm_kernels(dtype, FORM_DZ)[l.dz];
             MmDzArgs a{MmOperands{s + l.x2, wv, nullptr, 2 * l.ldx, 2 * ldw, 0, (int32_t)M, (int32_t)n, (int32_t)K},
-                       mm_grid(k, l.dz, M, n), count, map, target, v0, reinterpret_cast<const float*>(v + l.lse), coef, s + l.dzs,
+                       mm_grid(k, M, n), count, map, target, v0, reinterpret_cast<const float*>(v + l.lse), coef, s + l.dzs,
                        l.ldz};
             rc = mm_launch(k.fn, (int64_t)a.grid.tiles_m * a.grid.tiles_n, k.threads, &a, "gradient of the logits", st);
         }
         if (rc == TGEMM_OK && kx) {
             into_x.job[0] = MmJob{{MmOperands{s + l.dzs, wv, nullptr, 2 * l.ldz, 2 * ldw, 0, (int32_t)M, (int32_t)K, (int32_t)n}, {}},
-                                  1, {}, dx, lddx, l.dx.splits > 1 || pieces ? reinterpret_cast<float*>(s + l.dx_part) : nullptr, v0 > 0};
+                                  1, {}, dx, lddx, pieces ? reinterpret_cast<float*>(s + l.sum) : nullptr, v0 > 0};
             rc = mm_store(dtype, FORM_NN, l.dx, into_x, st);
         }
         if (rc == TGEMM_OK && kw && n > 0) {
             into_w.job[0] = MmJob{{MmOperands{s + l.dzs, s + l.x2, nullptr, 2 * l.ldz, 2 * l.ldx, 0, (int32_t)n, (int32_t)K, (int32_t)M}, {}},
-                                  1, {}, static_cast<char*>(dw) + v0 * lddw * 2, lddw,
-                                  l.dw.splits > 1 ? reinterpret_cast<float*>(s + l.dw_part) : nullptr, 0};
+                                  1, {}, static_cast<char*>(dw) + v0 * lddw * 2, lddw, nullptr, 0};
             rc = mm_store(dtype, FORM_TN, l.dw, into_w, st);
-            if (rc == TGEMM_OK && l.dw.splits > 1) rc = mm_join(dtype, l.dw, into_w, st);
         }
     }
-    if (rc == TGEMM_OK && kx && (l.dx.splits > 1 || pieces)) rc = mm_join(dtype, l.dx, into_x, st);
+    if (rc == TGEMM_OK && kx && pieces) rc = mm_round(dtype, into_x, st);
     if (rc == TGEMM_OK) clear_error();
     return rc;
 }
