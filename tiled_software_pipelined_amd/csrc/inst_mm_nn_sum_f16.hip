@@ -1,0 +1,13 @@
+#include "tg_mm_kernels.hpp"
+
+namespace tg {
+typedef MmTiles<MmF16, ALONG, ACROSS, false> Tiles;
+const MmKernel* mm_nn_sum_f16() {
+    static const MmKernel table[SIZE_COUNT] = {
+        mm_entry<Tiles::T256>(reinterpret_cast<const void*>(mm_store_kernel<Tiles::T256, true>)),
+        mm_entry<Tiles::T128>(reinterpret_cast<const void*>(mm_store_kernel<Tiles::T128, true>)),
+        mm_entry<Tiles::T64>(reinterpret_cast<const void*>(mm_store_kernel<Tiles::T64, true>)),
+    };
+    return table;
+}
+}  // namespace tg

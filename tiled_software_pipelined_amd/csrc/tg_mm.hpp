@@ -395,11 +395,11 @@ struct MmTile {
     }
 
     // ---- the way out -----------------------------------------------------------
-    // Calls each(row, column, v, w, data) for every 8 adjacent columns of the wave's
-    // block: row and column relative to the block, v their sums, w (PAIR) those
-    // of the second matrix.  32 rows at a time go through the wave's own LDS;
-    // before that, fetch(row, column, data) starts the loads that `each` will want
-    // of them, all of the 32 rows' in flight together.  The walk over the
+    // Calls each(u, v, w, data) for every 8 adjacent columns of the wave's block:
+    // those at lane_col(lane) of row u + lane_row(lane), u the same for the whole
+    // wave; v their sums, w (PAIR) those of the second matrix.  32 rows at a time go
+    // through the wave's own LDS; before that, fetch(u, data) starts the loads that
+    // `each` will want, all of the 32 rows' in flight together.  The walk over the
     // 32-row blocks is a loop, so that `each` stands in the code once.
     static constexpr int PER_ROW = WAVE_N / 8;     // lanes a row
     static constexpr int ROWS = 64 / PER_ROW;      // rows an instruction
@@ -426,15 +426,17 @@ struct MmTile {
     __device__ static __forceinline__ TG_LDS char* staged(TG_LDS char* mine, int row, int c) {
         return mine + row * (WTN * 4) + (c ^ (row & (WTN / 4 - 1))) * 16;
     }
+    __device__ static __forceinline__ int lane_row(int lane) { return lane / PER_ROW; }
+    __device__ static __forceinline__ int lane_col(int lane) { return 8 * (lane % PER_ROW); }
     template <class Data, class Fetch, class Each>
     __device__ static __forceinline__ void each_row(const Acc& acc, TG_LDS char* smem, int lane, int wave, Fetch fetch, Each each) {
         TG_LDS char* mine = smem + wave * (32 * WTN * 4);
-        const int r0 = lane / PER_ROW, c = 2 * (lane % PER_ROW);
+        const int r0 = lane_row(lane), c = lane_col(lane) / 4;
 #pragma unroll 1
         for (int i = 0; i < FM; ++i) {
             Data data[PIECES];
 #pragma unroll
-            for (int q = 0; q < PIECES; ++q) fetch(32 * i + q * ROWS + r0, 4 * c, data[q]);
+            for (int q = 0; q < PIECES; ++q) fetch(32 * i + q * ROWS, data[q]);
             stage<0>(i, acc, mine, lane);
             asm volatile("" ::: "memory");  // a wave's LDS accesses stay in order
 #pragma unroll
@@ -452,7 +454,7 @@ struct MmTile {
                         for (int e = 0; e < 4; ++e) w[4 * h + e] = y[e];
                     }
                 }
-                each(32 * i + row, 4 * c, v, w, data[q]);
+                each(32 * i + q * ROWS, v, w, data[q]);
             }
             asm volatile("" ::: "memory");
         }
@@ -460,35 +462,55 @@ struct MmTile {
     struct Nothing {};
     template <class Each>
     __device__ static __forceinline__ void each_row(const Acc& acc, TG_LDS char* smem, int lane, int wave, Each each) {
-        each_row<Nothing>(acc, smem, lane, wave, [](int, int, Nothing&) {},
-                          [&](int r, int c, float (&v)[8], float (&w)[8], Nothing&) { each(r, c, v, w); });
+        each_row<Nothing>(acc, smem, lane, wave, [](int, Nothing&) {},
+                          [&](int u, float (&v)[8], float (&w)[8], Nothing&) { each(u, v, w); });
     }
+    // Whether the wave's block, at row m1 and column n1 of M x N results, lies
+    // inside them: decided once, the way out then has no checks.
+    __device__ static __forceinline__ bool inside(int m1, int n1, int M, int N) { return m1 + WTM <= M && n1 + WAVE_N <= N; }
 };
 
-// 8 values of 16 bits; `count` of them inside the row.
-template <class T>
-__device__ __forceinline__ void store8(T* dst, const float (&v)[8], int count) {
-    T o[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = (T)v[e];  // to nearest even
-    if (count >= 8) {
-        __builtin_memcpy(dst, o, 16);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 7; ++e)
-            if (e < count) dst[e] = o[e];
-    }
-}
-// 8 values as they stand in memory, zeros past the row's end.
+struct Yes {
+    static constexpr bool value = true;
+};
+struct No {
+    static constexpr bool value = false;
+};
+
+// 8 adjacent values in memory; `count` of them, which may be none, inside the row.
 struct Raw8 {
     i32x4 v;
 };
+template <class T>
+__device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
+    T o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = (T)v[e];  // to nearest even
+    __builtin_memcpy(dst, o, 16);
+}
+// The empty statements keep the compiler from making one run of element stores of
+// both branches.
+template <class T>
+__device__ __forceinline__ void store8(T* dst, const float (&v)[8], int count) {
+    if (count >= 8) {
+        store8(dst, v);
+    } else {
+        asm volatile("; part of 8" ::: "memory");
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < count) dst[e] = (T)v[e];
+        asm volatile("; part of 8 ends" ::: "memory");
+    }
+}
+template <class T>
+__device__ __forceinline__ void load8(Raw8& x, const T* src) { x.v = load16(src); }
 template <class T>
 __device__ __forceinline__ void load8(Raw8& x, const T* src, int count) {
     if (count >= 8) {
         x.v = load16(src);
     } else {
         union { i32x4 v; T e[8]; } u;
+        asm volatile("; part of 8" ::: "memory");
 #pragma unroll
         for (int e = 0; e < 8; ++e) u.e[e] = load_or_zero(src + e, e < count);
         x.v = u.v;

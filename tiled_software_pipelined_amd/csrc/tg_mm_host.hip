@@ -8,12 +8,13 @@
 namespace tg {
 
 #define TG_MM_TABLES(t)                                                                                         \
-    const MmKernel *mm_nt_##t(), *mm_nn_##t(), *mm_tn_##t(), *mm_gate_##t(), *mm_dh_##t(), *mm_stats_##t(), *mm_dz_##t(); \
+    const MmKernel *mm_nt_##t(), *mm_nn_##t(), *mm_tn_##t(), *mm_nn_sum_##t(), *mm_gate_##t(), *mm_dh_##t(), *mm_stats_##t(), *mm_dz_##t(); \
     static const MmKernel* mm_kernels_##t(int form) {                                                           \
         switch (form) {                                                                                         \
             case FORM_NT: return mm_nt_##t();                                                                   \
             case FORM_NN: return mm_nn_##t();                                                                   \
             case FORM_TN: return mm_tn_##t();                                                                   \
+            case FORM_NN_SUM: return mm_nn_sum_##t();                                                           \
             case FORM_GATE: return mm_gate_##t();                                                               \
             case FORM_DH: return mm_dh_##t();                                                                   \
             case FORM_STATS: return mm_stats_##t();                                                             \

@@ -165,7 +165,7 @@ struct MmPlace {
         wm0 = (wave / G::WAVES_N) * G::WTM;
         wn0 = (wave % G::WAVES_N) * G::WTN;
     }
-    // first row and column of C of the wave's block
+    // first row and column of C of the wave's block, the same for the whole wave
     __device__ __forceinline__ int row0() const { return m0 + wm0; }
     __device__ __forceinline__ int col0() const { return n0 + (wn0 / G::WTN) * G::WAVE_N; }
 };
@@ -207,7 +207,26 @@ __device__ __forceinline__ int mm_job_of(const MmStoreArgs& g, int& tile) {
     return which;
 }
 
+// Where a wave's results stand in a row-major M x N matrix: for 8 of them, at(p, u)
+// is their address and count(u) how many lie inside.
 template <class G>
+struct MmOut {
+    int m1, n1, M, N, r0, c0;
+    int64_t ld;
+    uint32_t lane_at;  // elements from the wave's first of its rows
+    __device__ __forceinline__ MmOut(const MmPlace<G>& place, int M_, int N_, int64_t ld_)
+        : m1(place.row0()), n1(place.col0()), M(M_), N(N_), r0(G::lane_row(place.lane)), c0(G::lane_col(place.lane)), ld(ld_),
+          lane_at((uint32_t)(r0 * ld_ + c0)) {}
+    __device__ __forceinline__ bool inside() const { return G::inside(m1, n1, M, N); }
+    template <class T>
+    __device__ __forceinline__ T* at(T* p, int u) const { return p + ((int64_t)(m1 + u) * ld + n1) + lane_at; }
+    __device__ __forceinline__ int row(int u) const { return m1 + u + r0; }
+    __device__ __forceinline__ int col() const { return n1 + c0; }
+    __device__ __forceinline__ int count(int u) const { return row(u) < M ? N - col() : 0; }
+};
+
+// SUM: for jobs with float sums (job.sum), which are not shared out.
+template <class G, bool SUM>
 __global__ __launch_bounds__(G::NT) void mm_store_kernel(MmStoreArgs g) {
     __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
     TG_LDS char* smem = (TG_LDS char*)smem_raw;
@@ -247,51 +266,59 @@ __global__ __launch_bounds__(G::NT) void mm_store_kernel(MmStoreArgs g) {
         t0 -= slices;
         t1 -= slices;
     }
-    const int M = all.M, N = job.op[0].N, m1 = at.row0(), n1 = at.col0();
-    if (shared) {
-        float* mine = shared + (int64_t)at.wm0 * G::BN + at.wn0;
-        G::each_row(acc, smem, at.lane, at.wave,
-                    [&](int r, int c, float (&v)[8], float (&)[8]) { __builtin_memcpy(mine + r * G::BN + c, v, 32); });
-    } else if (job.sum) {
+    const int M = all.M, N = job.op[0].N;
+    typedef float(&F8)[8];
+    if constexpr (SUM) {
+        const MmOut<G> out(at, M, N, N);
         float* sum = job.sum;
         const bool add = job.add != 0;
         struct Before {
             f32x4 v[2];
         };
-        G::template each_row<Before>(acc, smem, at.lane, at.wave, [&](int r, int c, Before& b) {
-            const int m = m1 + r, n = n1 + c;
-            if (add && m < M && n + 8 <= N) __builtin_memcpy(&b, sum + (int64_t)m * N + n, 32);
-        }, [&](int r, int c, float (&v)[8], float (&)[8], Before& b) {
-            const int m = m1 + r, n = n1 + c;
-            if (m >= M || n >= N) return;
-            float* dst = sum + (int64_t)m * N + n;
-            if (n + 8 <= N) {
+        auto way = [&](auto inside) {
+            G::template each_row<Before>(acc, smem, at.lane, at.wave, [&](int u, Before& b) {
+                if (inside.value && add) __builtin_memcpy(&b, out.at(sum, u), 32);
+            }, [&](int u, F8 v, F8, Before& b) {
+                float* dst = out.at(sum, u);
+                if (inside.value) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = add ? v[e] + b.v[e >> 2][e & 3] : v[e];
-                __builtin_memcpy(dst, v, 32);
-            } else {
+                    for (int e = 0; e < 8; ++e) v[e] = add ? v[e] + b.v[e >> 2][e & 3] : v[e];
+                    __builtin_memcpy(dst, v, 32);
+                } else {
+                    const int count = out.count(u);
 #pragma unroll
-                for (int e = 0; e < 7; ++e)
-                    if (n + e < N) dst[e] = add ? dst[e] + v[e] : v[e];
-            }
-        });
+                    for (int e = 0; e < 8; ++e)
+                        if (e < count) dst[e] = add ? dst[e] + v[e] : v[e];
+                }
+            });
+        };
+        if (out.inside()) way(Yes{});
+        else way(No{});
+    } else if (shared) {
+        float* mine = shared + (at.wm0 + G::lane_row(at.lane)) * G::BN + at.wn0 + G::lane_col(at.lane);
+        G::each_row(acc, smem, at.lane, at.wave, [&](int u, F8 v, F8) { __builtin_memcpy(mine + u * G::BN, v, 32); });
     } else {
         typedef typename G::T T;
         const float alpha = g.alpha ? *g.alpha : 1.0f;
         T* C = static_cast<T*>(job.C);
-        const int64_t ldc = job.ldc;
+        const MmOut<G> out(at, M, N, job.ldc);
         struct Row {
             int to;
         };
-        G::template each_row<Row>(acc, smem, at.lane, at.wave, [&](int r, int, Row& row) {
-            row.to = g.map && m1 + r < M ? g.map[m1 + r] : m1 + r;
-        }, [&](int r, int c, float (&v)[8], float (&)[8], Row& row) {
-            const int m = m1 + r, n = n1 + c;
-            if (m >= M || n >= N) return;
+        auto way = [&](auto inside) {
+            G::template each_row<Row>(acc, smem, at.lane, at.wave, [&](int u, Row& row) {
+                row.to = inside.value ? out.row(u) : min(out.row(u), M - 1);
+                if (g.map) row.to = g.map[row.to];
+            }, [&](int u, F8 v, F8, Row& row) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= alpha;
-            store8(C + row.to * ldc + n, v, N - n);
-        });
+                for (int e = 0; e < 8; ++e) v[e] *= alpha;
+                T* dst = C + (int64_t)row.to * out.ld + out.col();
+                if (inside.value) store8(dst, v);
+                else store8(dst, v, out.count(u));
+            });
+        };
+        if (out.inside()) way(Yes{});
+        else way(No{});
     }
 }
 
@@ -325,7 +352,9 @@ __device__ __forceinline__ void mm_join(const MmStoreArgs& g, int slice, int til
     const float alpha = g.alpha ? *g.alpha : 1.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= alpha;
-    store8(static_cast<T*>(job.C) + (int64_t)(g.map ? g.map[m] : m) * job.ldc + n, v, N - n);
+    T* dst = static_cast<T*>(job.C) + (int64_t)(g.map ? g.map[m] : m) * job.ldc + n;
+    if (n + 8 <= N) store8(dst, v);
+    else store8(dst, v, N - n);
 }
 template <class G>
 __global__ __launch_bounds__(256) void mm_join_kernel(MmStoreArgs g) {
@@ -370,22 +399,27 @@ __global__ __launch_bounds__(G::NT) void mm_gate_kernel(MmGateArgs g) {
     typename G::Acc acc;
     G::clear(acc);
     G::product(g.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, smem, acc, at.wm0, at.wn0, at.lane, at.wave);
-    const int M = g.op.M, N = g.op.N, m1 = at.row0(), n1 = at.col0();
-    G::each_row(acc, smem, at.lane, at.wave, [&](int r, int c, float (&v)[8], float (&w)[8]) {
-        const int m = m1 + r, n = n1 + c;
-        if (m >= M || n >= N) return;
-        const int64_t to = (int64_t)m * g.ld + n;
-        if (g.g) {
-            store8(static_cast<T*>(g.g) + to, v, N - n);
-            store8(static_cast<T*>(g.u) + to, w, N - n);
-        }
-        float a[8], d[8];
-        activate8<false>(g.act, v, a, d);
+    const MmOut<G> out(at, g.op.M, g.op.N, g.ld);
+    typedef float(&F8)[8];
+    auto way = [&](auto inside) {
+        G::each_row(acc, smem, at.lane, at.wave, [&](int u, F8 v, F8 w) {
+            auto put = [&](void* p, F8 x) {
+                if (inside.value) store8(out.at(static_cast<T*>(p), u), x);
+                else store8(out.at(static_cast<T*>(p), u), x, out.count(u));
+            };
+            if (g.g) {
+                put(g.g, v);
+                put(g.u, w);
+            }
+            float a[8], d[8];
+            activate8<false>(g.act, v, a, d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] *= w[e];
-        // h's rounding: the down projection's operand
-        store8(static_cast<T*>(g.h) + to, a, N - n);
-    });
+            for (int e = 0; e < 8; ++e) a[e] *= w[e];
+            put(g.h, a);  // its rounding: the down projection's operand
+        });
+    };
+    if (out.inside()) way(Yes{});
+    else way(No{});
 }
 
 template <class G>
@@ -397,41 +431,50 @@ __global__ __launch_bounds__(G::NT) void mm_dh_kernel(MmDhArgs g) {
     typename G::Acc acc;
     G::clear(acc);
     G::product(g.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, smem, acc, at.wm0, at.wn0, at.lane, at.wave);
-    const int M = g.op.M, N = g.op.N, m1 = at.row0(), n1 = at.col0();
+    const MmOut<G> out(at, g.op.M, g.op.N, g.ld);
+    typedef float(&F8)[8];
     struct Kept {
         Raw8 g, u;
     };
-    G::template each_row<Kept>(acc, smem, at.lane, at.wave, [&](int r, int c, Kept& k) {
-        const int m = m1 + r, n = n1 + c;
-        if (m >= M || n >= N) return;
-        const int64_t to = (int64_t)m * g.ld + n;
-        load8(k.g, static_cast<const T*>(g.g) + to, N - n);
-        load8(k.u, static_cast<const T*>(g.u) + to, N - n);
-    }, [&](int r, int c, float (&v)[8], float (&)[8], Kept& k) {
-        const int m = m1 + r, n = n1 + c, count = N - n;
-        if (m >= M || n >= N) return;
-        const int64_t to = (int64_t)m * g.ld + n;
-        float gate[8], up[8], a[8], d[8], o[8];
-        values8<T>(gate, k.g);
-        values8<T>(up, k.u);
-        activate8<true>(g.act, gate, a, d);
-        // roundings of dg, du, h: operands of the products that follow
-        if (g.dg) {
+    auto way = [&](auto inside) {
+        G::template each_row<Kept>(acc, smem, at.lane, at.wave, [&](int u, Kept& k) {
+            const T *pg = out.at(static_cast<const T*>(g.g), u), *pu = out.at(static_cast<const T*>(g.u), u);
+            if (inside.value) {
+                load8(k.g, pg);
+                load8(k.u, pu);
+            } else {
+                load8(k.g, pg, out.count(u));
+                load8(k.u, pu, out.count(u));
+            }
+        }, [&](int u, F8 v, F8, Kept& k) {
+            auto put = [&](void* p, F8 x) {
+                if (inside.value) store8(out.at(static_cast<T*>(p), u), x);
+                else store8(out.at(static_cast<T*>(p), u), x, out.count(u));
+            };
+            float gate[8], up[8], a[8], d[8], o[8];
+            values8<T>(gate, k.g);
+            values8<T>(up, k.u);
+            activate8<true>(g.act, gate, a, d);
+            // roundings of dg, du, h: operands of the products that follow
+            if (g.dg) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = v[e] * up[e] * d[e];
-            store8(static_cast<T*>(g.dg) + to, o, count);
-        }
-        if (g.du) {
+                for (int e = 0; e < 8; ++e) o[e] = v[e] * up[e] * d[e];
+                put(g.dg, o);
+            }
+            if (g.du) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = v[e] * a[e];
-            store8(static_cast<T*>(g.du) + to, o, count);
-        }
-        if (g.h) {
+                for (int e = 0; e < 8; ++e) o[e] = v[e] * a[e];
+                put(g.du, o);
+            }
+            if (g.h) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = a[e] * up[e];
-            store8(static_cast<T*>(g.h) + to, o, count);
-        }
-    });
+                for (int e = 0; e < 8; ++e) o[e] = a[e] * up[e];
+                put(g.h, o);
+            }
+        });
+    };
+    if (out.inside()) way(Yes{});
+    else way(No{});
 }
 
 constexpr float LOG2E = 1.44269504f;
@@ -513,30 +556,35 @@ __global__ __launch_bounds__(G::NT) void mm_dz_kernel(MmDzArgs g) {
     typename G::Acc acc;
     G::clear(acc);
     G::product(known.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, smem, acc, at.wm0, at.wn0, at.lane, at.wave);
-    const int M = known.op.M, N = g.op.N, m1 = at.row0(), n1 = at.col0();
+    const int M = known.op.M;
     T* dz = static_cast<T*>(g.dz);
+    const MmOut<G> out(at, M, g.op.N, g.ldz);
+    typedef float(&F8)[8];
     struct Row {
         float lse, coef;
         int64_t target;
     };
-    G::template each_row<Row>(acc, smem, at.lane, at.wave, [&](int r, int, Row& row) {
-        const int m = min(m1 + r, M - 1);
-        row.lse = g.lse[m];
-        row.coef = g.coef[m];
-        row.target = g.target[g.map[m]] - g.v0;
-    }, [&](int r, int c, float (&v)[8], float (&)[8], Row& row) {
-        const int m = m1 + r, n = n1 + c;
-        if (m >= M || n >= N) return;
-        const int64_t t = row.target - n;
-        const int hit = t >= 0 && t < 8 ? (int)t : -1;
+    auto way = [&](auto inside) {
+        G::template each_row<Row>(acc, smem, at.lane, at.wave, [&](int u, Row& row) {
+            const int m = inside.value ? out.row(u) : min(out.row(u), M - 1);
+            row.lse = g.lse[m];
+            row.coef = g.coef[m];
+            row.target = g.target[g.map[m]] - g.v0;
+        }, [&](int u, F8 v, F8, Row& row) {
+            const int64_t t = row.target - out.col();
+            const int hit = t >= 0 && t < 8 ? (int)t : -1;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float p = __builtin_amdgcn_exp2f((v[e] - row.lse) * LOG2E);
-            if (e == hit) p -= 1.0f;
-            v[e] = p * row.coef;
-        }
-        store8(dz + m * g.ldz + n, v, N - n);
-    });
+            for (int e = 0; e < 8; ++e) {
+                float p = __builtin_amdgcn_exp2f((v[e] - row.lse) * LOG2E);
+                if (e == hit) p -= 1.0f;
+                v[e] = p * row.coef;
+            }
+            if (inside.value) store8(out.at(dz, u), v);
+            else store8(out.at(dz, u), v, out.count(u));
+        });
+    };
+    if (out.inside()) way(Yes{});
+    else way(No{});
 }
 
 // ---- few rows of A -----------------------------------------------------------
@@ -643,7 +691,7 @@ __global__ __launch_bounds__(512) void mm_rows_kernel(MmRowsArgs g) {
 }
 
 // ---- the table ---------------------------------------------------------------
-enum MmForm { FORM_NT = 0, FORM_NN, FORM_TN, FORM_GATE, FORM_DH, FORM_STATS, FORM_DZ, FORM_COUNT };
+enum MmForm { FORM_NT = 0, FORM_NN, FORM_TN, FORM_NN_SUM, FORM_GATE, FORM_DH, FORM_STATS, FORM_DZ, FORM_COUNT };
 enum MmSize { SIZE_256 = 0, SIZE_128, SIZE_64, SIZE_COUNT };
 struct MmKernel {
     const void *fn, *join;

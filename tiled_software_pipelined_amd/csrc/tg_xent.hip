@@ -69,7 +69,7 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
     l.dzs = take(2, 2 * M * l.ldz);
     if (keep & TGEMM_KEEP_X) {
         // the sums over several pieces are not shared out as well
-        l.dx = mm_size(FORM_NN, M, K, mm_slices(cols), pieces == 1);
+        l.dx = mm_size(pieces > 1 ? FORM_NN_SUM : FORM_NN, M, K, mm_slices(cols), pieces == 1);
         if (pieces > 1) l.sum = take(2, 4 * M * K);
         else l.split_bytes[0] = mm_split_bytes(FORM_NN, l.dx, &dx, 1, mm_slices(cols), true);
     }
@@ -428,7 +428,7 @@ int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const vo
         if (rc == TGEMM_OK && kx) {
             into_x.job[0] = MmJob{{MmOperands{s + l.dzs, wv, nullptr, 2 * l.ldz, 2 * ldw, 0, (int32_t)M, (int32_t)K, (int32_t)n}, {}},
                                   1, {}, dx, lddx, pieces ? reinterpret_cast<float*>(s + l.sum) : nullptr, v0 > 0};
-            rc = mm_store(dtype, FORM_NN, l.dx, into_x, st);
+            rc = mm_store(dtype, pieces ? FORM_NN_SUM : FORM_NN, l.dx, into_x, st);
         }
         if (rc == TGEMM_OK && kw && n > 0) {
             into_w.job[0] = MmJob{{MmOperands{s + l.dzs, s + l.x2, nullptr, 2 * l.ldz, 2 * l.ldx, 0, (int32_t)n, (int32_t)K, (int32_t)M}, {}},
