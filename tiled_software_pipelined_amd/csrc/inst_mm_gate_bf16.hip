@@ -7,6 +7,7 @@ const MmKernel* mm_gate_bf16() {
         mm_entry<Tiles::T256>(reinterpret_cast<const void*>(mm_gate_kernel<Tiles::T256>)),
         mm_entry<Tiles::T128>(reinterpret_cast<const void*>(mm_gate_kernel<Tiles::T128>)),
         mm_entry<Tiles::T64>(reinterpret_cast<const void*>(mm_gate_kernel<Tiles::T64>)),
+        mm_entry<Tiles::T128Deep>(reinterpret_cast<const void*>(mm_gate_kernel<Tiles::T128Deep>)),
     };
     return table;
 }

@@ -7,6 +7,7 @@ const MmKernel* mm_nn_bf16() {
         mm_entry<Tiles::T256>(reinterpret_cast<const void*>(mm_store_kernel<Tiles::T256, false>), reinterpret_cast<const void*>(mm_join_kernel<Tiles::T256>)),
         mm_entry<Tiles::T128>(reinterpret_cast<const void*>(mm_store_kernel<Tiles::T128, false>), reinterpret_cast<const void*>(mm_join_kernel<Tiles::T128>)),
         mm_entry<Tiles::T64>(reinterpret_cast<const void*>(mm_store_kernel<Tiles::T64, false>), reinterpret_cast<const void*>(mm_join_kernel<Tiles::T64>)),
+        mm_entry<Tiles::T128Deep>(reinterpret_cast<const void*>(mm_store_kernel<Tiles::T128Deep, false>), reinterpret_cast<const void*>(mm_join_kernel<Tiles::T128Deep>)),
     };
     return table;
 }

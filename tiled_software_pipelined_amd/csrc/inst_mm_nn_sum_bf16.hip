@@ -7,6 +7,7 @@ const MmKernel* mm_nn_sum_bf16() {
         mm_entry<Tiles::T256>(reinterpret_cast<const void*>(mm_store_kernel<Tiles::T256, true>)),
         mm_entry<Tiles::T128>(reinterpret_cast<const void*>(mm_store_kernel<Tiles::T128, true>)),
         mm_entry<Tiles::T64>(reinterpret_cast<const void*>(mm_store_kernel<Tiles::T64, true>)),
+        mm_entry<Tiles::T128Deep>(reinterpret_cast<const void*>(mm_store_kernel<Tiles::T128Deep, true>)),
     };
     return table;
 }

@@ -88,10 +88,10 @@ struct MmTile {
     // columns of C: with PAIR, of each of the two matrices
     static constexpr int TILE_N = PAIR ? BN / 2 : BN, WAVE_N = PAIR ? WTN / 2 : WTN;
 
-    // workgroups on the machine at once; nanoseconds of a slice when it is full;
-    // kilobytes of a tile's float sums
-    static constexpr int SLOTS = BM * BN >= 65536 ? 256 : 512;
-    static constexpr int SLICE_NS = BM * BN >= 65536 ? 1750 : BM * BN >= 16384 ? 1100 : 600;
+    // workgroups on the machine at once; nanoseconds of a slice where it is not
+    // full; kilobytes of a tile's float sums
+    static constexpr int SLOTS = LDS_BYTES > 80 * 1024 ? 256 : 512;
+    static constexpr int SLICE_NS = BM * BN >= 65536 ? 1100 : BM * BN < 16384 ? 350 : SLOTS == 512 ? 650 : 400;
     static constexpr int TILE_KB = BM * BN / 256;
 
     typedef f32x16 Acc[FM][FN];

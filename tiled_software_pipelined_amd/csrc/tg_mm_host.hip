@@ -36,15 +36,52 @@ static double tiles_of(const MmKernel& k, const MmShape* shapes, int jobs) {
     return n;
 }
 
-// Microseconds of one launch.
-static double mm_time(const MmKernel& k, double tiles, int64_t slices, bool may_split) {
-    const double slice = k.slice * 1e-3;
-    if (tiles > 1e6) return 4.0 + tiles / k.slots * slice * (double)slices;
+// Model of a launch's time in microseconds, from runs of every form and tile at
+// 14 shapes (100 .. 4096 rows, 768 .. 50240 columns, K = 64 .. 50240).  A slice of 64
+// k: `alone` where at most 256 workgroups run, `full` where the machine is (tiles
+// that stand twice on a compute unit: of both), `cold` at least where the weight comes
+// from memory for few rows.  `fixed`: the way in and out, by form.
+//   us                          256    128     64  128 deep
+//   nt   512x1024x2816         30.6   24.2   16.1   18.0
+//   nt   1024x1024x4096        37.2   27.8   21.6   24.4
+//   nt   2048x2048x5440        61.7   55.5   55.8   46.2
+//   nt   4096x4096x4096         110    133    172    145
+//   tn   50240x768x64          27.6   22.0   36.0   36.9
+//   gate 100x11008x4096        97.0   63.3   58.4   48.6
+//   gate 2048x5440x2048         106    109    140    124
+//   dh   2048x5440x2048         107     81     92     73
+//   stats 60x50240x768         24.8   20.1   18.9   21.4
+//   stats 2048x5440x2048       45.3   52.5   59.4   49.5
+struct MmRate {
+    double alone, full, cold, fixed[FORM_COUNT];
+};
+//                                               nt   nn   tn  sum  gate  dh  stats dz
+static const MmRate MM_RATES[SIZE_COUNT] = {
+    {0.99, 1.60, 1.16, {6.3, 6.3, 6.3, 9.0, 9.5, 22.0, 6.5, 9.7}},
+    {0.60, 1.00, 0.60, {1.5, 1.5, 1.5, 3.0, 4.4, 6.8, 3.0, 4.0}},
+    {0.30, 0.65, 0.46, {3.4, 3.8, 5.0, 5.0, 3.5, 6.9, 3.7, 4.5}},
+    {0.35, 0.54, 0.60, {3.7, 4.0, 4.4, 5.0, 6.0, 6.9, 3.9, 5.0}},
+};
+
+// n workgroups of some slices each
+static double mm_rounds(int form, int size, int slots, double n, double slices, bool cold) {
+    const MmRate& r = MM_RATES[size];
+    const double fixed = r.fixed[form], alone = cold && r.cold > r.alone ? r.cold : r.alone;
+    const double whole = floor(n / slots), rest = n - whole * slots;
+    double t = whole * (fixed + r.full * slices);
+    if (rest > 0.0) {
+        const double part = slots == 256 ? alone + (r.full > alone ? (r.full - alone) * rest / 256.0 : 0.0)
+                                         : rest <= 256.0 ? alone : r.full > alone ? r.full : alone;
+        t += fixed + part * slices;
+    }
+    return t;
+}
+
+static double mm_time(int form, int size, const MmKernel& k, double tiles, int64_t slices, bool may_split, bool cold) {
+    if (tiles > 1e6) return mm_rounds(form, size, k.slots, tiles, (double)slices, cold);
     const MmSchedule s = mm_schedule((int)tiles, (int)slices, k.slots, k.slice, k.tile_kb, may_split);
-    // a lone workgroup on a compute unit is quicker than two
-    auto alone = [&](int n) { return n <= 256 && k.slots > 256 ? 0.65 : 1.0; };
-    double t = 4.0 + ceil(s.full / (double)k.slots) * (1.0 + alone((int)tiles) * slice * (double)slices);
-    if (s.rest) t += alone(s.rest * s.splits) * slice * s.per + 7.0 + s.rest * s.splits * k.tile_kb * 0.4e-3;
+    double t = mm_rounds(form, size, k.slots, s.full, (double)slices, cold);
+    if (s.rest) t += mm_rounds(form, size, k.slots, s.rest * s.splits, s.per, cold) + 9.0 + s.rest * s.splits * k.tile_kb * 0.4e-3;
     return t;
 }
 
@@ -53,7 +90,8 @@ MmSize mm_size(int form, const MmShape* shapes, int jobs, int64_t slices, bool m
     double least = -1.0;
     const MmKernel* table = mm_kernels(TGEMM_BF16, form);  // the types' tiles are alike
     for (int s = 0; s < SIZE_COUNT; ++s) {
-        const double t = mm_time(table[s], tiles_of(table[s], shapes, jobs), slices, may_split);
+        const bool cold = shapes[0].M <= 2 * table[s].bm;
+        const double t = mm_time(form, s, table[s], tiles_of(table[s], shapes, jobs), slices, may_split, cold);
         if (least < 0.0 || t < least) {
             least = t;
             best = (MmSize)s;

@@ -16,8 +16,9 @@ struct MmGrid {
 // the machine at once: the first `full` tiles fill it whole times, and the rest
 // are shared out along k, `splits` workgroups a tile of `per` slices each, whose
 // sums are joined by a kernel of its own.  Sharing costs that launch and the
-// sums' way through memory: about 6 us and 2.5 TB/s, against (1 - 1 / splits) of a
-// tile's slices at `slice` ns each.  Host and device come to the same answer
+// sums' way through memory: about 9 us and 2.5 TB/s, against (1 - 1 / splits) of a
+// tile's slices at `slice` ns each (64 tiles of 44 slices: shared out 18.7 us,
+// not 16.1; of 172 slices 35 against 79).  Host and device come to the same answer
 // (whole numbers).
 struct MmSchedule {
     int32_t full, rest, splits, per;
@@ -32,7 +33,7 @@ __host__ __device__ __forceinline__ MmSchedule mm_schedule(int tiles, int slices
     for (int n = 2; n <= MM_SPLITS && n * rest <= slots && slices >= 4 * n; ++n) {
         const int per = (slices + n - 1) / n;
         if ((n - 1) * per >= slices) continue;  // a part would be empty
-        const int64_t t = (int64_t)per * slice + 6000 + n * rest * tile_kb * 2 / 5;
+        const int64_t t = (int64_t)per * slice + 9000 + n * rest * tile_kb * 2 / 5;
         if (t < least) {
             least = t;
             s = MmSchedule{tiles - rest, rest, n, per};
@@ -692,7 +693,7 @@ __global__ __launch_bounds__(512) void mm_rows_kernel(MmRowsArgs g) {
 
 // ---- the table ---------------------------------------------------------------
 enum MmForm { FORM_NT = 0, FORM_NN, FORM_TN, FORM_NN_SUM, FORM_GATE, FORM_DH, FORM_STATS, FORM_DZ, FORM_COUNT };
-enum MmSize { SIZE_256 = 0, SIZE_128, SIZE_64, SIZE_COUNT };
+enum MmSize { SIZE_256 = 0, SIZE_128, SIZE_64, SIZE_128_DEEP, SIZE_COUNT };
 struct MmKernel {
     const void *fn, *join;
     int bm, bn, threads;  // rows and columns of C a workgroup takes
@@ -703,13 +704,21 @@ MmKernel mm_entry(const void* fn, const void* join = nullptr) {
     return MmKernel{fn, join, G::BM, G::TILE_N, G::NT, G::SLOTS, G::SLICE_NS, G::TILE_KB};
 }
 
-// The tiles.  256 x 256: four waves of 128 x 128, one a SIMD.  128 x 128: four
-// waves, two workgroups a compute unit.  64 x 128: likewise.
+// The tiles.  256 x 256: eight waves of 64 x 128 (four of 128 x 128: 4096^3 alike,
+// 110 us, but 4096x11008x4096 ended by the softmax's pieces 313 us against 294,
+// where a lone wave a SIMD does the end's arithmetic by itself; the end that loads
+// two values for each result is better off with four, 378 us against 394).  128 x
+// 128 twice a compute unit, four waves and two slots each; 64 x 128 likewise with
+// three slots, for few rows.  128 x 128 once a unit, eight waves and four slots,
+// where there are no more workgroups than units (2048x2048x5440 46 us, twice a
+// unit 56; four waves 48).
 template <class Tr, int LA, int LB, bool PAIR>
 struct MmTiles {
-    typedef MmTile<Tr, LA, LB, 256, 256, 2, 2, 2, false, PAIR> T256;
+    typedef MmTile<Tr, LA, LB, 256, 256, 4, 2, 2, false, PAIR> T256;
+    typedef MmTile<Tr, LA, LB, 256, 256, 2, 2, 2, false, PAIR> T256Loads;
     typedef MmTile<Tr, LA, LB, 128, 128, 2, 2, 2, false, PAIR> T128;
     typedef MmTile<Tr, LA, LB, 64, 128, 2, 2, 3, true, PAIR> T64;
+    typedef MmTile<Tr, LA, LB, 128, 128, 4, 2, 4, true, PAIR> T128Deep;
 };
 
 }  // namespace tg
