@@ -16,6 +16,7 @@ struct FfnLayout {
     bool h_kept;             // only the down projection's gradient is wanted
     int64_t ld;              // row stride of all of them: whole 128-byte lines
     int64_t split;           // forward's scratch: sums of the down projection's shared tiles
+    int64_t x, wg, wu, wd;   // likewise: operands on lines, -1: read where they are
     int64_t dg, du, h2;      // backward's scratch
     int64_t dx_split, dw_split;
     int64_t split_bytes, dx_split_bytes, dw_split_bytes;
@@ -37,8 +38,16 @@ static FfnLayout ffn_layout(int64_t M, int64_t K, int64_t F, int64_t N, int keep
     l.ld = (F + 63) / 64 * 64;
     const int64_t inner = 2 * M * l.ld;
     const MmShape y{M, N}, x{M, K}, dw[3] = {{F, K}, {F, K}, {N, F}};
-    l.gate = mm_size(FORM_GATE, M, F, mm_slices(K), false);
-    l.down = mm_size(FORM_NT, M, N, mm_slices(F), true);
+    const bool pack_k = mm_packs(K, M), pack_f = mm_packs(F, M);
+    l.gate = mm_size(FORM_GATE, M, F, mm_slices(K), false, pack_k ? 0 : K);
+    l.down = mm_size(FORM_NT, M, N, mm_slices(F), true, pack_f ? 0 : F);
+    l.x = l.wg = l.wu = l.wd = -1;
+    if (pack_k) {
+        l.x = take(1, 2 * M * mm_lines(K));
+        l.wg = take(1, 2 * F * mm_lines(K));
+        l.wu = take(1, 2 * F * mm_lines(K));
+    }
+    if (pack_f) l.wd = take(1, 2 * N * l.ld);
     l.g = l.u = l.dg = l.du = l.h2 = -1;
     l.h_kept = keep == TGEMM_FFN_DOWN;
     if (keep & FFN_INNER) {
@@ -49,13 +58,13 @@ static FfnLayout ffn_layout(int64_t M, int64_t K, int64_t F, int64_t N, int keep
     if (!l.rows) l.split_bytes = mm_split_bytes(FORM_NT, l.down, &y, 1, mm_slices(F), false);
     l.split = take(1, l.split_bytes);
     if (keep & FFN_INNER) {
-        l.dh = mm_size(FORM_DH, M, F, mm_slices(N), false);
+        l.dh = mm_size(FORM_DH, M, F, mm_slices(N), false, N);
         if (keep & (TGEMM_FFN_X | TGEMM_FFN_GATE)) l.dg = take(2, inner);
         if (keep & (TGEMM_FFN_X | TGEMM_FFN_UP)) l.du = take(2, inner);
         if (keep & TGEMM_FFN_DOWN) l.h2 = take(2, inner);
     }
     if (keep & TGEMM_FFN_X) {
-        l.dx = mm_size(FORM_NN, M, K, 2 * mm_slices(F), true);
+        l.dx = mm_size(FORM_NN, M, K, 2 * mm_slices(F), true, 0);
         l.dx_split_bytes = mm_split_bytes(FORM_NN, l.dx, &x, 1, 2 * mm_slices(F), false);
         l.dx_split = take(2, l.dx_split_bytes);
     }
@@ -64,7 +73,7 @@ static FfnLayout ffn_layout(int64_t M, int64_t K, int64_t F, int64_t N, int keep
     for (int i = 0; i < 3; ++i)
         if (keep & (TGEMM_FFN_GATE << i)) wanted[n++] = dw[i];
     if (n > 0) {
-        l.dw = mm_size(FORM_TN, wanted, n, mm_slices(M), true);
+        l.dw = mm_size(FORM_TN, wanted, n, mm_slices(M), true, K % 8 ? K : N);
         l.dw_split_bytes = mm_split_bytes(FORM_TN, l.dw, wanted, n, mm_slices(M), false);
         l.dw_split = take(2, l.dw_split_bytes);
     }
@@ -93,9 +102,11 @@ static int ffn_common(int32_t dtype, int32_t act) {
     return TGEMM_OK;
 }
 
-static MmOperands operands(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K) {
+// own_a, own_b: an operand of ours, whose rows are whole 128-byte lines.
+static MmOperands operands(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
+                           bool own_a = false, bool own_b = false) {
     return MmOperands{static_cast<const char*>(a), static_cast<const char*>(b), nullptr, 2 * lda, 2 * ldb, 0,
-                      (int32_t)M, (int32_t)N, (int32_t)K};
+                      (int32_t)M, (int32_t)N, (int32_t)K, own_a, own_b};
 }
 
 template <bool PAIR>
@@ -143,6 +154,24 @@ int tgemm_ffn_forward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype,
     char* v = static_cast<char*>(saved);
     char* s = static_cast<char*>(scratch);
     char* h = (l.h_kept ? v : s) + l.h;
+    if (M > 0) {
+        MmPack list[3];
+        int n = 0;
+        auto pack = [&](const void*& p, int64_t& ld, int64_t rows, int64_t cols, int64_t at) {
+            if (at < 0 || mm_aligned(p, ld)) return;
+            list[n++] = MmPack{p, ld, rows, cols, s + at};
+            p = s + at;
+            ld = mm_lines(cols);
+        };
+        pack(x, ldx, M, K, l.x);
+        pack(wg, ldg, F, K, l.wg);
+        pack(wu, ldu, F, K, l.wu);
+        rc = mm_pack(list, n, st);
+        n = 0;
+        pack(wd, ldd, N, F, l.wd);
+        if (rc == TGEMM_OK) rc = mm_pack(list, n, st);
+        if (rc != TGEMM_OK) return rc;
+    }
     if (M > 0 && F > 0) {
         MmOperands o = operands(x, ldx, wg, ldg, M, F, K);
         o.b2 = static_cast<const char*>(wu);
@@ -214,9 +243,9 @@ int tgemm_ffn_backward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype
     if (rc == TGEMM_OK && (keep & (TGEMM_FFN_GATE | TGEMM_FFN_UP | TGEMM_FFN_DOWN))) {
         MmStoreArgs a{};
         a.split = room(s, l.dw_split, l.dw_split_bytes);
-        if (keep & TGEMM_FFN_GATE) a.job[a.jobs++] = MmJob{{operands(dg, l.ld, x, ldx, F, K, M), {}}, 1, {}, dwg, lddwg, nullptr, 0};
-        if (keep & TGEMM_FFN_UP) a.job[a.jobs++] = MmJob{{operands(du, l.ld, x, ldx, F, K, M), {}}, 1, {}, dwu, lddwu, nullptr, 0};
-        if (keep & TGEMM_FFN_DOWN) a.job[a.jobs++] = MmJob{{operands(dy, lddy, h, l.ld, N, F, M), {}}, 1, {}, dwd, lddwd, nullptr, 0};
+        if (keep & TGEMM_FFN_GATE) a.job[a.jobs++] = MmJob{{operands(dg, l.ld, x, ldx, F, K, M, true), {}}, 1, {}, dwg, lddwg, nullptr, 0};
+        if (keep & TGEMM_FFN_UP) a.job[a.jobs++] = MmJob{{operands(du, l.ld, x, ldx, F, K, M, true), {}}, 1, {}, dwu, lddwu, nullptr, 0};
+        if (keep & TGEMM_FFN_DOWN) a.job[a.jobs++] = MmJob{{operands(dy, lddy, h, l.ld, N, F, M, false, true), {}}, 1, {}, dwd, lddwd, nullptr, 0};
         rc = mm_store(dtype, FORM_TN, l.dw, a, st);
     }
     if (rc == TGEMM_OK) clear_error();

@@ -49,20 +49,22 @@ struct MmF16 {
 };
 
 // The operands of one product, strides in bytes.  b2: with PAIR, the matrix of
-// the second half of each wave's columns.
+// the second half of each wave's columns.  a_padded, b_padded: every row, the
+// last too, may be read up to the next multiple of 8 elements.
 struct MmOperands {
     const char* a;
     const char* b;
     const char* b2;
     int64_t lda, ldb, ldb2;
     int32_t M, N, K;
+    int32_t a_padded, b_padded;
 };
 
 // Slices of 64 k that direct copies may read of an operand ACROSS k with
 // `width` elements a row: their 16-byte chunks may pass a row's end, which must
-// not be the last row's.  (Called on the host too, for splits of k.)
-__host__ __device__ __forceinline__ int mm_direct_slices(int lay, int K, int width, int64_t ld) {
-    if (lay == ALONG || width % 8 == 0) return K / 64;
+// not be the last row's.
+__device__ __forceinline__ int mm_direct_slices(int lay, int K, int width, int64_t ld, bool padded) {
+    if (lay == ALONG || width % 8 == 0 || padded) return K / 64;
     const int last = (int)((14 + ld - 1) / ld);  // rows that end within 14 bytes of the operand's end
     return K > last ? (K - last) / 64 : 0;
 }
@@ -343,7 +345,7 @@ struct MmTile {
     // every wave past its last LDS read.
     __device__ static __forceinline__ void product(const MmOperands& g, int m0, int n0, int t0, int t1, TG_LDS char* smem,
                                                    Acc& acc, int wm0, int wn0, int lane, int wave) {
-        const int direct = min(mm_direct_slices(LA, g.K, g.M, g.lda), mm_direct_slices(LB, g.K, g.N, g.ldb));
+        const int direct = min(mm_direct_slices(LA, g.K, g.M, g.lda, g.a_padded), mm_direct_slices(LB, g.K, g.N, g.ldb, g.b_padded));
         const int n = min(t1, direct) - t0;  // slices by direct copies
         if (n > 0) {
             Offsets off;

@@ -39,8 +39,8 @@ static double tiles_of(const MmKernel& k, const MmShape* shapes, int jobs) {
 // Model of a launch's time in microseconds, from runs of every form and tile at
 // 14 shapes (100 .. 4096 rows, 768 .. 50240 columns, K = 64 .. 50240).  A slice of 64
 // k: `alone` where at most 256 workgroups run, `full` where the machine is (tiles
-// that stand twice on a compute unit: of both), `cold` at least where the weight comes
-// from memory for few rows.  `fixed`: the way in and out, by form.
+// that stand twice on a compute unit: of both), where the weight comes from memory for
+// few rows at least `cold`.  `fixed`: the way in and out, by form.
 //   us                          256    128     64  128 deep
 //   nt   512x1024x2816         30.6   24.2   16.1   18.0
 //   nt   1024x1024x4096        37.2   27.8   21.6   24.4
@@ -53,27 +53,25 @@ static double tiles_of(const MmKernel& k, const MmShape* shapes, int jobs) {
 //   stats 60x50240x768         24.8   20.1   18.9   21.4
 //   stats 2048x5440x2048       45.3   52.5   59.4   49.5
 struct MmRate {
-    double alone, full, cold, fixed[FORM_COUNT];
+    double alone, full, cold[2], fixed[FORM_COUNT];  // cold: up to 256 workgroups, and more
 };
 //                                               nt   nn   tn  sum  gate  dh  stats dz
 static const MmRate MM_RATES[SIZE_COUNT] = {
-    {0.99, 1.60, 1.16, {6.3, 6.3, 6.3, 9.0, 9.5, 22.0, 6.5, 9.7}},
-    {0.60, 1.00, 0.60, {1.5, 1.5, 1.5, 3.0, 4.4, 6.8, 3.0, 4.0}},
-    {0.30, 0.65, 0.46, {3.4, 3.8, 5.0, 5.0, 3.5, 6.9, 3.7, 4.5}},
-    {0.35, 0.54, 0.60, {3.7, 4.0, 4.4, 5.0, 6.0, 6.9, 3.9, 5.0}},
+    {0.99, 1.60, {1.25, 1.6}, {6.3, 6.3, 6.3, 9.0, 9.5, 22.0, 6.5, 9.7}},
+    {0.60, 1.00, {0.90, 1.2}, {1.5, 1.5, 1.5, 3.0, 4.4, 6.8, 3.0, 4.0}},
+    {0.30, 0.65, {0.46, 0.85}, {3.4, 3.8, 5.0, 5.0, 3.5, 6.9, 3.7, 4.5}},
+    {0.35, 0.54, {0.65, 0.65}, {3.7, 4.0, 4.4, 5.0, 6.0, 6.9, 3.9, 5.0}},
 };
 
 // n workgroups of some slices each
 static double mm_rounds(int form, int size, int slots, double n, double slices, bool cold) {
     const MmRate& r = MM_RATES[size];
-    const double fixed = r.fixed[form], alone = cold && r.cold > r.alone ? r.cold : r.alone;
-    const double whole = floor(n / slots), rest = n - whole * slots;
-    double t = whole * (fixed + r.full * slices);
-    if (rest > 0.0) {
-        const double part = slots == 256 ? alone + (r.full > alone ? (r.full - alone) * rest / 256.0 : 0.0)
-                                         : rest <= 256.0 ? alone : r.full > alone ? r.full : alone;
-        t += fixed + part * slices;
-    }
+    const double fixed = r.fixed[form], whole = floor(n / slots), rest = n - whole * slots;
+    auto least = [&](double v, int i) { return cold && r.cold[i] > v ? r.cold[i] : v; };
+    double t = whole * (fixed + least(r.full, 1) * slices);
+    if (rest > 0.0)
+        t += fixed + slices * (slots == 256 ? least(r.alone + (r.full - r.alone) * rest / 256.0, 0)
+                                            : rest <= 256.0 ? least(r.alone, 0) : least(r.full, 1));
     return t;
 }
 
@@ -85,13 +83,19 @@ static double mm_time(int form, int size, const MmKernel& k, double tiles, int64
     return t;
 }
 
-MmSize mm_size(int form, const MmShape* shapes, int jobs, int64_t slices, bool may_split) {
+// What rows off 16-byte boundaries cost: at even elements, at odd ones.
+static const double MM_EVEN[SIZE_COUNT] = {1.2, 1.3, 1.45, 1.5}, MM_ODD[SIZE_COUNT] = {1.3, 2.3, 2.0, 2.0};
+
+MmSize mm_size(int form, const MmShape* shapes, int jobs, int64_t slices, bool may_split, int64_t row) {
     MmSize best = SIZE_64;
     double least = -1.0;
     const MmKernel* table = mm_kernels(TGEMM_BF16, form);  // the types' tiles are alike
     for (int s = 0; s < SIZE_COUNT; ++s) {
         const bool cold = shapes[0].M <= 2 * table[s].bm;
-        const double t = mm_time(form, s, table[s], tiles_of(table[s], shapes, jobs), slices, may_split, cold);
+        double t = mm_time(form, s, table[s], tiles_of(table[s], shapes, jobs), slices, may_split, cold);
+        // across k a chunk's rows are further apart and the cost is less
+        const double off = row % 8 == 0 ? 0.0 : (row % 2 ? MM_ODD[s] : MM_EVEN[s]) - 1.0;
+        t *= 1.0 + off * (form == FORM_TN ? 0.5 : 1.0);
         if (least < 0.0 || t < least) {
             least = t;
             best = (MmSize)s;
@@ -103,7 +107,7 @@ MmSize mm_size(int form, const MmShape* shapes, int jobs, int64_t slices, bool m
 int64_t mm_split_bytes(int form, MmSize size, const MmShape* shapes, int jobs, int64_t slices, bool fewer) {
     const MmKernel& k = mm_kernels(TGEMM_BF16, form)[size];
     const double tiles = tiles_of(k, shapes, jobs);
-    if (tiles > 1e6 || tiles < 1.0) return 0;
+    if (tiles > 1e6 || tiles < 1.0 || slices < MM_LEAST_SLICES) return 0;
     const int64_t tile = (int64_t)k.bm * k.bn * 4;
     // up to `slots` parts, in any number of tiles
     if (fewer) return k.slots * tile;
@@ -115,13 +119,12 @@ MmGrid mm_grid(const MmKernel& k, int64_t M, int64_t N) {
     return MmGrid{(int32_t)((M + k.bm - 1) / k.bm), (int32_t)((N + k.bn - 1) / k.bn)};
 }
 
-int mm_launch(const void* fn, int64_t workgroups, int threads, void* args, const char* name, hipStream_t stream) {
+int mm_launch_list(const void* fn, int64_t workgroups, int threads, void** args, const char* name, hipStream_t stream) {
     if (workgroups > INT_MAX || !grid_fits((double)workgroups, threads)) {
         set_error("%s: too many tiles", name);
         return TGEMM_E_ARG;
     }
-    void* list[] = {args};
-    const hipError_t err = hipLaunchKernel(fn, dim3((unsigned)workgroups), dim3(threads), list, 0, stream);
+    const hipError_t err = hipLaunchKernel(fn, dim3((unsigned)workgroups), dim3(threads), args, 0, stream);
     if (err != hipSuccess) {
         set_error("launch of %s failed: %s", name, hipGetErrorString(err));
         return TGEMM_E_HIP;
@@ -143,19 +146,19 @@ int mm_store(int dtype, int form, MmSize size, const MmStoreArgs& given, hipStre
         tiles += (double)j.grid.tiles_m * j.grid.tiles_n;
     }
     if (args.jobs == 0) return TGEMM_OK;
-    if (tiles > 1e6) args.split = nullptr;
+    int64_t slices = 0;
+    for (int p = 0; p < args.job[0].pairs; ++p) slices += mm_slices(args.job[0].op[p].K);
+    if (tiles > 1e6 || slices < MM_LEAST_SLICES) args.split = nullptr;
     if (tiles > INT_MAX / 2) {
         set_error("product: too many tiles");
         return TGEMM_E_ARG;
     }
-    int64_t slices = 0;
-    for (int p = 0; p < args.job[0].pairs; ++p) slices += mm_slices(args.job[0].op[p].K);
     const MmSchedule s = mm_schedule((int)tiles, (int)slices, k.slots, k.slice, k.tile_kb, args.split != nullptr);
     // fewer rows than the host knows of may be shared out in up to `slots` parts
     const bool fewer = args.rows && args.split;
     int rc = mm_launch(k.fn, fewer ? (int64_t)tiles + k.slots : s.total(), k.threads, &args, "product", stream);
     const int64_t rest = fewer ? (tiles < k.slots / 2 ? (int64_t)tiles : k.slots / 2) : s.rest;
-    if (rc == TGEMM_OK && args.split && rest > 0) rc = mm_launch(k.join, rest * (k.bm * k.bn / 2048), 256, &args, "join", stream);
+    if (rc == TGEMM_OK && args.split && rest > 0) rc = mm_launch(k.join, rest * (k.bm * k.bn / MM_JOIN), 256, &args, "join", stream);
     return rc;
 }
 
@@ -166,6 +169,57 @@ int mm_round(int dtype, const MmStoreArgs& args, hipStream_t stream) {
     const void* fn = dtype == TGEMM_BF16 ? reinterpret_cast<const void*>(mm_round_kernel<__bf16>)
                                          : reinterpret_cast<const void*>(mm_round_kernel<_Float16>);
     return mm_launch(fn, (M * ((N + 3) / 4) + 255) / 256, 256, &a, "rounding", stream);
+}
+
+// ---- rows on lines ---------------------------------------------------------------
+struct MmPackArgs {
+    struct {
+        const uint16_t* src;
+        uint16_t* dst;
+        int64_t ld, rows, cols, ldto, first;  // first: workgroup at which it starts
+    } job[3];
+    int32_t jobs;
+};
+
+// A wave a row; what is behind the row's end up to the line's is not written.
+__global__ __launch_bounds__(256) void mm_pack_kernel(MmPackArgs g) {
+    int which = 0;
+    while (which + 1 < g.jobs && (int64_t)blockIdx.x >= g.job[which + 1].first) ++which;
+    const auto& j = g.job[which];
+    const int64_t r = ((int64_t)blockIdx.x - j.first) * 4 + wave_id();
+    if (r >= j.rows) return;
+    const uint16_t* src = j.src + r * j.ld;
+    uint16_t* dst = j.dst + r * j.ldto;
+    for (int64_t k = 8 * lane_id(); k < j.cols; k += 512) {
+        i32x4 v;
+        if (k + 8 <= j.cols) {
+            v = load16(src + k);
+        } else {
+            union { i32x4 v; uint16_t e[8]; } u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u.e[e] = load_or_zero(src + k + e, k + e < j.cols);
+            v = u.v;
+        }
+        *reinterpret_cast<i32x4*>(dst + k) = v;
+    }
+}
+
+int mm_pack(const MmPack* list, int count, hipStream_t stream) {
+    MmPackArgs a{};
+    int64_t n = 0;
+    for (int i = 0; i < count; ++i) {
+        if (list[i].rows == 0 || list[i].cols == 0) continue;
+        auto& j = a.job[a.jobs++];
+        j.src = static_cast<const uint16_t*>(list[i].src);
+        j.dst = static_cast<uint16_t*>(list[i].dst);
+        j.ld = list[i].ld;
+        j.rows = list[i].rows;
+        j.cols = list[i].cols;
+        j.ldto = mm_lines(list[i].cols);
+        j.first = n;
+        n += (list[i].rows + 3) / 4;
+    }
+    return n == 0 ? TGEMM_OK : mm_launch(reinterpret_cast<const void*>(mm_pack_kernel), n, 256, &a, "rows on lines", stream);
 }
 
 // ---- arguments -----------------------------------------------------------------

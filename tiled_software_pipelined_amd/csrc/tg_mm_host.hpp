@@ -21,11 +21,28 @@ inline int64_t mm_slices(int64_t K) { return (K + 63) / 64; }
 struct MmShape {
     int64_t M, N;
 };
-MmSize mm_size(int form, const MmShape* shapes, int jobs, int64_t slices, bool may_split);
-inline MmSize mm_size(int form, int64_t M, int64_t N, int64_t slices, bool may_split) {
+// row: elements of an operand's row as the copies read it (K along k, else the
+// result's rows or columns); its last bits are its alignment.
+MmSize mm_size(int form, const MmShape* shapes, int jobs, int64_t slices, bool may_split, int64_t row);
+inline MmSize mm_size(int form, int64_t M, int64_t N, int64_t slices, bool may_split, int64_t row) {
     const MmShape s{M, N};
-    return mm_size(form, &s, 1, slices, may_split);
+    return mm_size(form, &s, 1, slices, may_split, row);
 }
+
+// Copies of an operand's rows to whole 128-byte lines.  Rows that start at odd
+// elements make the tile kernels' copies twice as slow (2047x2050x5461 along k:
+// 128 tiles 135 us, on lines 64; 256 tiles 81), other rows that are not on 16-byte
+// boundaries a fifth (2048x5440x2050 gate and up 128 us, 2048 wide 107), so a copy
+// of the weights pays from some rows of the other operand on.
+inline bool mm_packs(int64_t K, int64_t M) { return K % 2 ? M >= 768 : K % 8 ? M >= 4096 : false; }
+inline int64_t mm_lines(int64_t K) { return (K + 63) / 64 * 64; }
+struct MmPack {
+    const void* src;
+    int64_t ld, rows, cols;
+    void* dst;  // row stride mm_lines(cols)
+};
+inline bool mm_aligned(const void* p, int64_t ld) { return ld % 8 == 0 && (uintptr_t)p % 16 == 0; }
+int mm_pack(const MmPack* list, int count, hipStream_t stream);
 // Bytes for the sums of tiles that a launch shares out (MmStoreArgs::split), for
 // as many rows as given or, where only the device knows them (`fewer`), less.
 int64_t mm_split_bytes(int form, MmSize size, const MmShape* shapes, int jobs, int64_t slices, bool fewer);
@@ -37,7 +54,11 @@ MmGrid mm_grid(const MmKernel& k, int64_t M, int64_t N);
 int mm_store(int dtype, int form, MmSize size, const MmStoreArgs& args, hipStream_t stream);
 // The first job's float sums into its C.
 int mm_round(int dtype, const MmStoreArgs& args, hipStream_t stream);
-int mm_launch(const void* fn, int64_t workgroups, int threads, void* args, const char* name, hipStream_t stream);
+int mm_launch_list(const void* fn, int64_t workgroups, int threads, void** args, const char* name, hipStream_t stream);
+inline int mm_launch(const void* fn, int64_t workgroups, int threads, void* args, const char* name, hipStream_t stream) {
+    void* list[] = {args};
+    return mm_launch_list(fn, workgroups, threads, list, name, stream);
+}
 
 // A tensor argument's checks: rows x cols of `dtype`, leading dimension ld.
 int mm_check(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld);

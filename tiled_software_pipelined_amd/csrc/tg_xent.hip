@@ -26,8 +26,8 @@ struct XentLayout {
     int64_t ldx;               // row stride of the gathered rows of x
     int64_t cols, ldz;         // backward: columns of a piece, row stride of dz
     int64_t count, map, rank, lse;                  // kept
-    int64_t x, hit, each, part;                     // forward's scratch
-    int64_t x2, coef, alpha, dzs, sum, split;       // backward's
+    int64_t x, hit, each, part, w;                  // forward's scratch; w: on lines, -1: read where it is
+    int64_t x2, coef, alpha, dzs, sum, split, w2;   // backward's
     int64_t split_bytes[2];                         // of dx's and dw's launches, which use the same room
     int64_t bytes[3];
 };
@@ -45,13 +45,16 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
     l.map = take(0, 4 * M);   // where they stand
     l.rank = take(0, 4 * M);  // each row's number among them, -1
     l.lse = take(0, 4 * M);   // of each of them
-    l.ldx = (K + 63) / 64 * 64;
-    l.stats = mm_size(FORM_STATS, M, V, mm_slices(K), false);
+    const bool pack = mm_packs(K, M);
+    l.ldx = mm_lines(K);
+    l.w = l.w2 = -1;
+    l.stats = mm_size(FORM_STATS, M, V, mm_slices(K), false, pack ? 0 : K);
     l.parts = (V + wave_cols(l.stats) - 1) / wave_cols(l.stats);
     l.x = take(1, 2 * M * l.ldx);
     l.hit = take(1, 4 * M);   // the target's logit of each of them
     l.each = take(1, 4 * M);  // each row's loss
     l.part = take(1, 8 * M * l.parts);
+    if (pack) l.w = take(1, 2 * V * l.ldx);
     if (!keep) return l;
     // at least 8192 columns: dz is then four times as wide as x often is
     const int64_t fit = M > 0 ? XENT_PIECE / M : V;
@@ -62,21 +65,23 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
     l.ldz = l.cols;
     const int64_t cols = l.cols < V ? l.cols : V;
     const MmShape dx{M, K}, dw{cols, K};
-    l.dz = mm_size(FORM_DZ, M, cols, mm_slices(K), false);
-    l.x2 = take(2, 2 * M * l.ldx);
+    l.dz = mm_size(FORM_DZ, M, cols, mm_slices(K), false, pack ? 0 : K);
+    const int64_t padded = (M + 63) / 64 * 64;  // rows, the last of them zero
+    l.x2 = take(2, 2 * padded * l.ldx);
     l.coef = take(2, 4 * M);
     l.alpha = take(2, 4);
-    l.dzs = take(2, 2 * M * l.ldz);
+    l.dzs = take(2, 2 * padded * l.ldz);
     if (keep & TGEMM_KEEP_X) {
         // the sums over several pieces are not shared out as well
-        l.dx = mm_size(pieces > 1 ? FORM_NN_SUM : FORM_NN, M, K, mm_slices(cols), pieces == 1);
+        l.dx = mm_size(pieces > 1 ? FORM_NN_SUM : FORM_NN, M, K, mm_slices(cols), pieces == 1, 0);
         if (pieces > 1) l.sum = take(2, 4 * M * K);
         else l.split_bytes[0] = mm_split_bytes(FORM_NN, l.dx, &dx, 1, mm_slices(cols), true);
     }
     if (keep & TGEMM_KEEP_W) {
-        l.dw = mm_size(FORM_TN, cols, K, mm_slices(M), true);
+        l.dw = mm_size(FORM_TN, cols, K, mm_slices(M), true, 0);
         l.split_bytes[1] = mm_split_bytes(FORM_TN, l.dw, &dw, 1, mm_slices(M), true);
     }
+    if (pack) l.w2 = take(2, 2 * cols * l.ldx);
     l.split = take(2, l.split_bytes[0] > l.split_bytes[1] ? l.split_bytes[0] : l.split_bytes[1]);
     return l;
 }
@@ -159,23 +164,19 @@ __global__ __launch_bounds__(1024) void xent_scan_kernel(ScanArgs g) {
 struct GatherArgs {
     int64_t M, K, ldx, ldto, lddx;
     const uint16_t* x;
-    const int32_t* rank;
     uint16_t* to;
     float* loss;   // not NULL: zero for rows that do not count
     uint16_t* dx;  // likewise
+    const int32_t *count, *rank;
 };
 
-// A wave a row.
-__global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
-    const int lane = lane_id();
-    const int64_t m = (int64_t)blockIdx.x * 4 + wave_id();
-    if (m >= g.M) return;
-    const int r = g.rank[m];
+// A row by a wave: gathered, or zeros for a row that does not count.
+__device__ __forceinline__ void gather_row(const GatherArgs& g, int64_t m, int r, int lane) {
+    const i32x4 zero{0, 0, 0, 0};
     if (r < 0) {
         if (g.loss && lane == 0) g.loss[m] = 0.0f;
         if (g.dx) {
             uint16_t* dst = g.dx + m * g.lddx;
-            const i32x4 zero{0, 0, 0, 0};
             for (int64_t k = 8 * lane; k < g.K; k += 512) {
                 if (k + 8 <= g.K) __builtin_memcpy(dst + k, &zero, 16);
                 else
@@ -197,6 +198,41 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
             v = u.v;
         }
         *reinterpret_cast<i32x4*>(dst + k) = v;
+    }
+}
+__global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
+    const int64_t m = (int64_t)blockIdx.x * 4 + wave_id();
+    if (m < g.M) gather_row(g, m, g.rank[m], lane_id());
+}
+
+// Both at once for up to SCAN_ROWS rows: each workgroup counts the rows before its
+// own four by itself (a launch less: 4 us; all workgroups together read M^2 / 4
+// targets, which 4096 rows keep under 2 us).
+constexpr int64_t SCAN_ROWS = 4096;
+__global__ __launch_bounds__(256) void xent_scan_gather_kernel(ScanArgs s, GatherArgs g) {
+    __shared__ int held[4];
+    const int lane = lane_id(), wave = wave_id();
+    const int64_t m0 = (int64_t)blockIdx.x * 4, m = m0 + wave;
+    int n = 0;
+    for (int64_t i = threadIdx.x; i < m0; i += 256) n += s.target[i] != s.ignore;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d);
+    if (lane == 0) held[wave] = n;
+    __syncthreads();
+    n = held[0] + held[1] + held[2] + held[3];
+    int before = 0;
+    for (int i = 0; i < 4; ++i) {
+        const bool counts = m0 + i < s.M && s.target[m0 + i] != s.ignore;
+        if (i < wave) before += counts;
+        if (i == wave && m < s.M) {
+            const int r = counts ? n + before : -1;
+            if (lane == 0) {
+                s.rank[m] = r;
+                if (counts) s.map[r] = (int32_t)m;
+                if (m == s.M - 1) *s.count = n + before + counts;
+            }
+            gather_row(g, m, r, lane);
+        }
     }
 }
 
@@ -280,7 +316,7 @@ struct CoefArgs {
 // brought near 2^15 by a power of two, which alpha takes out again: dz holds
 // values from 2^15 down, where float16 keeps 11 bits to 2^-14 (probabilities of
 // 2^-29), whatever the loss was scaled by.
-__global__ __launch_bounds__(1024) void xent_coef_kernel(CoefArgs g) {
+__device__ __forceinline__ void xent_factors(const CoefArgs& g) {
     __shared__ float held[16];
     const int M = *g.count;
     const float scalar = g.reduction == TGEMM_NONE ? 0.0f : g.reduction == TGEMM_MEAN ? *g.dloss / (float)M : *g.dloss;
@@ -306,11 +342,25 @@ __global__ __launch_bounds__(1024) void xent_coef_kernel(CoefArgs g) {
     if (threadIdx.x == 0) *g.alpha = ldexpf(1.0f, -e);
 }
 
-static int gather(const void* x, int64_t ldx, int64_t M, int64_t K, const int32_t* rank, void* to, int64_t ldto, float* loss,
-                  void* dx, int64_t lddx, hipStream_t st) {
-    GatherArgs a{M, K, ldx, ldto, lddx, static_cast<const uint16_t*>(x), rank, static_cast<uint16_t*>(to), loss,
-                 static_cast<uint16_t*>(dx)};
-    return mm_launch(reinterpret_cast<const void*>(xent_gather_kernel), (M + 3) / 4, 256, &a, "rows that count", st);
+// The first workgroup: the factors.  The others: rows of x, 16 each, and behind
+// them the zero rows up to the next multiple of 64.
+__global__ __launch_bounds__(1024) void xent_prepare_kernel(CoefArgs c, GatherArgs g) {
+    if (blockIdx.x == 0) {
+        xent_factors(c);
+        return;
+    }
+    const int lane = lane_id();
+    const int64_t m = ((int64_t)blockIdx.x - 1) * 16 + wave_id();
+    if (m < g.M) {
+        gather_row(g, m, g.rank[m], lane);
+    } else {
+        const int count = *g.count;
+        const int64_t r = count + (m - g.M);
+        if (r < (count + 63) / 64 * 64) {
+            const i32x4 zero{0, 0, 0, 0};
+            for (int64_t k = 8 * lane; k < g.ldto; k += 512) *reinterpret_cast<i32x4*>(g.to + r * g.ldto + k) = zero;
+        }
+    }
 }
 
 }  // namespace tg
@@ -352,9 +402,22 @@ int tgemm_xent_forward(int64_t M, int64_t V, int64_t K, int32_t dtype, const voi
     float2* part = reinterpret_cast<float2*>(s + l.part);
     float* each = reduction == TGEMM_NONE ? loss : reinterpret_cast<float*>(s + l.each);
     ScanArgs c{M, ignore, target, count, map, rank};
-    rc = mm_launch(reinterpret_cast<const void*>(xent_scan_kernel), 1, 1024, &c, "rows that count", st);
-    if (rc == TGEMM_OK && M > 0)
-        rc = gather(x, ldx, M, K, rank, s + l.x, l.ldx, reduction == TGEMM_NONE ? loss : nullptr, nullptr, 0, st);
+    GatherArgs into{M, K, ldx, l.ldx, 0, static_cast<const uint16_t*>(x), reinterpret_cast<uint16_t*>(s + l.x),
+                    reduction == TGEMM_NONE ? loss : nullptr, nullptr, count, rank};
+    if (M > 0 && M <= SCAN_ROWS) {
+        void* both[] = {&c, &into};
+        rc = mm_launch_list(reinterpret_cast<const void*>(xent_scan_gather_kernel), (M + 3) / 4, 256, both, "rows that count", st);
+    } else {
+        rc = mm_launch(reinterpret_cast<const void*>(xent_scan_kernel), 1, 1024, &c, "rows that count", st);
+        if (rc == TGEMM_OK && M > 0)
+            rc = mm_launch(reinterpret_cast<const void*>(xent_gather_kernel), (M + 3) / 4, 256, &into, "rows that count", st);
+    }
+    if (rc == TGEMM_OK && M > 0 && l.w >= 0 && !mm_aligned(w, ldw)) {
+        const MmPack p{w, ldw, V, K, s + l.w};
+        rc = mm_pack(&p, 1, st);
+        w = s + l.w;
+        ldw = l.ldx;
+    }
     if (rc == TGEMM_OK && M > 0 && V > 0) {
         const MmKernel& k = mm_kernels(dtype, FORM_STATS)[l.stats];
         MmStatsArgs a{MmOperands{s + l.x, static_cast<const char*>(w), nullptr, 2 * l.ldx, 2 * ldw, 0, (int32_t)M, (int32_t)V,
@@ -402,9 +465,10 @@ int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const vo
     float *coef = reinterpret_cast<float*>(s + l.coef), *alpha = reinterpret_cast<float*>(s + l.alpha);
     const char* wp = static_cast<const char*>(w);
     CoefArgs c{V, count, map, target, dloss, coef, alpha, reduction};
-    rc = mm_launch(reinterpret_cast<const void*>(xent_coef_kernel), 1, 1024, &c, "factors of the rows", st);
-    if (rc == TGEMM_OK && M > 0)
-        rc = gather(x, ldx, M, K, reinterpret_cast<const int32_t*>(v + l.rank), s + l.x2, l.ldx, nullptr, kx ? dx : nullptr, lddx, st);
+    GatherArgs into{M, K, ldx, l.ldx, lddx, static_cast<const uint16_t*>(x), reinterpret_cast<uint16_t*>(s + l.x2), nullptr,
+                    kx ? static_cast<uint16_t*>(dx) : nullptr, count, reinterpret_cast<const int32_t*>(v + l.rank)};
+    void* both[] = {&c, &into};
+    rc = mm_launch_list(reinterpret_cast<const void*>(xent_prepare_kernel), 1 + (M + 63 + 15) / 16, 1024, both, "factors of the rows", st);
     const bool pieces = l.cols < V;
     MmStoreArgs into_x{}, into_w{};
     into_x.alpha = into_w.alpha = alpha;
@@ -418,20 +482,29 @@ int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const vo
     for (int64_t v0 = 0; rc == TGEMM_OK && (v0 < V || v0 == 0); v0 += l.cols) {
         const int64_t n = V - v0 < l.cols ? V - v0 : l.cols;
         const char* wv = wp + v0 * ldw * 2;
-        if (M > 0 && n > 0) {
+        int64_t ldv = ldw;
+        if (M > 0 && l.w2 >= 0 && !mm_aligned(wv, ldw)) {
+            const MmPack p{wv, ldw, n, K, s + l.w2};
+            rc = mm_pack(&p, 1, st);
+            wv = s + l.w2;
+            ldv = l.ldx;
+        }
+        if (rc == TGEMM_OK && M > 0 && n > 0) {
             const MmKernel& k = mm_kernels(dtype, FORM_DZ)[l.dz];
-            MmDzArgs a{MmOperands{s + l.x2, wv, nullptr, 2 * l.ldx, 2 * ldw, 0, (int32_t)M, (int32_t)n, (int32_t)K},
+            MmDzArgs a{MmOperands{s + l.x2, wv, nullptr, 2 * l.ldx, 2 * ldv, 0, (int32_t)M, (int32_t)n, (int32_t)K},
                        mm_grid(k, M, n), count, map, target, v0, reinterpret_cast<const float*>(v + l.lse), coef, s + l.dzs,
                        l.ldz};
             rc = mm_launch(k.fn, (int64_t)a.grid.tiles_m * a.grid.tiles_n, k.threads, &a, "gradient of the logits", st);
         }
         if (rc == TGEMM_OK && kx) {
-            into_x.job[0] = MmJob{{MmOperands{s + l.dzs, wv, nullptr, 2 * l.ldz, 2 * ldw, 0, (int32_t)M, (int32_t)K, (int32_t)n}, {}},
+            into_x.job[0] = MmJob{{MmOperands{s + l.dzs, wv, nullptr, 2 * l.ldz, 2 * ldv, 0, (int32_t)M, (int32_t)K, (int32_t)n, 1,
+                                              wv == s + l.w2}, {}},
                                   1, {}, dx, lddx, pieces ? reinterpret_cast<float*>(s + l.sum) : nullptr, v0 > 0};
             rc = mm_store(dtype, pieces ? FORM_NN_SUM : FORM_NN, l.dx, into_x, st);
         }
         if (rc == TGEMM_OK && kw && n > 0) {
-            into_w.job[0] = MmJob{{MmOperands{s + l.dzs, s + l.x2, nullptr, 2 * l.ldz, 2 * l.ldx, 0, (int32_t)n, (int32_t)K, (int32_t)M}, {}},
+            into_w.job[0] = MmJob{{MmOperands{s + l.dzs, s + l.x2, nullptr, 2 * l.ldz, 2 * l.ldx, 0, (int32_t)n, (int32_t)K,
+                                              (int32_t)((M + 63) / 64 * 64), 1, 1}, {}},
                                   1, {}, static_cast<char*>(dw) + v0 * lddw * 2, lddw, nullptr, 0};
             rc = mm_store(dtype, FORM_TN, l.dw, into_w, st);
         }

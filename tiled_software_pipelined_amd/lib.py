@@ -808,20 +808,21 @@ _HALF_CODES = {torch.bfloat16: BF16, torch.float16: F16}
 def _half_code(tensors, names):
     """The type code of tensors that are all bfloat16 or all float16 on one GPU."""
     first = tensors[0]
-    code, device = _HALF_CODES.get(first.dtype), first.device
+    dtype, device = first.dtype, first.device
+    code = _HALF_CODES.get(dtype)
     if code is None:
-        raise TypeError("%s has unsupported dtype %s (bfloat16, float16)" % (names[0], first.dtype))
+        raise TypeError("%s has unsupported dtype %s (bfloat16, float16)" % (names[0], dtype))
     for t, name in zip(tensors, names):
-        if t.dtype != first.dtype:
-            raise TypeError("%s must have %s's dtype %s, got %s" % (name, names[0], first.dtype, t.dtype))
-        if not t.is_cuda or t.device != device:
+        if t.dtype is not dtype:
+            raise TypeError("%s must have %s's dtype %s, got %s" % (name, names[0], dtype, t.dtype))
+        if t.device != device or not t.is_cuda:
             raise ValueError("%s must be on one GPU (%s, got %s)" % (" and ".join(names), device, t.device))
     return code
 
 
 def _read(t):
     """(row-major matrix that the kernels may read, its row stride): t, or a copy."""
-    if t.is_contiguous():
+    if t.is_contiguous() and t.shape[1] <= MOST_STRIDE:
         return t, t.shape[1]
     if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and not t.shape[1] <= t.stride(0) <= MOST_STRIDE:
         t = t.contiguous()
@@ -844,44 +845,55 @@ def _ffn_bytes(M, K, F, N, keep):
     return tuple(max(v, 1) for v in n)
 
 
-def _ffn_forward(x, w_gate, w_up, w_down, code, act, keep):
+def _ffn_call(x, w_gate, w_up, w_down):
+    """Sizes (M, K, F, N), and the operands with their row strides."""
+    K, (N, F) = x.shape[-1], w_down.shape
+    M = x.numel() // K if K else math.prod(x.shape[:-1])
+    return (M, K, F, N), (*_read(x if x.dim() == 2 else x.reshape(M, K)), *_read(w_gate), *_read(w_up), *_read(w_down))
+
+
+def _pointers(operands):
+    """The tensors of (tensor, stride, tensor, stride, ..) as their addresses."""
+    return [v if type(v) is int else v.data_ptr() for v in operands]
+
+
+def _ffn_forward(x, sizes, operands, code, act, keep):
     """y of shape (..., N), and the buffer for the backward pass (None where keep is 0)."""
-    device, K, (N, F) = x.device, x.shape[-1], w_down.shape
-    M = math.prod(x.shape[:-1])
-    (x2, ldx), (wg, ldg), (wu, ldu), (wd, ldd) = _read(x.reshape(M, K)), _read(w_gate), _read(w_up), _read(w_down)
-    sizes = _ffn_bytes(M, K, F, N, keep)
-    saved = torch.empty(sizes[0], dtype=torch.uint8, device=device) if keep else None
-    scratch = torch.empty(sizes[1], dtype=torch.uint8, device=device)
+    device, N = x.device, sizes[3]
+    room = _ffn_bytes(*sizes, keep)
+    saved = torch.empty(room[0], dtype=torch.uint8, device=device) if keep else None
+    scratch = torch.empty(room[1], dtype=torch.uint8, device=device)
     y = torch.empty(x.shape[:-1] + (N,), dtype=x.dtype, device=device)
-    _call(device, _lib.tgemm_ffn_forward, M, K, F, N, code, act, x2.data_ptr(), ldx, wg.data_ptr(), ldg, wu.data_ptr(), ldu,
-          wd.data_ptr(), ldd, y.data_ptr(), N, keep, saved.data_ptr() if keep else None, scratch.data_ptr())
+    _call(device, _lib.tgemm_ffn_forward, *sizes, code, act, *_pointers(operands), y.data_ptr(), N, keep,
+          saved.data_ptr() if keep else None, scratch.data_ptr())
     return y, saved
 
 
 class _GatedFfn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_gate, w_up, w_down, code, act):
-        keep = sum(bit for bit, needed in zip((FFN_X, FFN_GATE, FFN_UP, FFN_DOWN), ctx.needs_input_grad) if needed)
-        y, saved = _ffn_forward(x, w_gate, w_up, w_down, code, act, keep)
+        needs = ctx.needs_input_grad
+        keep = needs[0] * FFN_X + needs[1] * FFN_GATE + needs[2] * FFN_UP + needs[3] * FFN_DOWN
+        sizes, operands = _ffn_call(x, w_gate, w_up, w_down)
+        y, saved = _ffn_forward(x, sizes, operands, code, act, keep)
         ctx.save_for_backward(x, w_gate, w_up, w_down, saved)
-        ctx.args = code, act, keep
+        ctx.args = sizes, code, act, keep
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, gy):
-        x, w_gate, w_up, w_down, saved = ctx.saved_tensors
-        code, act, keep = ctx.args
-        device, K, (N, F) = x.device, x.shape[-1], w_down.shape
-        M = math.prod(x.shape[:-1])
-        (x2, ldx), (wg, ldg), (wu, ldu), (wd, ldd) = _read(x.reshape(M, K)), _read(w_gate), _read(w_up), _read(w_down)
-        g, ldy = _read(gy.reshape(M, N))
+        *inputs, saved = ctx.saved_tensors
+        sizes, code, act, keep = ctx.args
+        M, K, F, N = sizes
+        device = gy.device
+        _, operands = _ffn_call(*inputs)
+        g, ldy = _read(gy if gy.dim() == 2 else gy.reshape(M, N))
         scratch = torch.empty(_ffn_bytes(M, K, F, N, keep)[2], dtype=torch.uint8, device=device)
-        grads = [torch.empty(t.shape, dtype=t.dtype, device=device) if needed else None
-                 for t, needed in zip((x, w_gate, w_up, w_down), ctx.needs_input_grad)]
-        dx, dg, du, dd = (None if t is None else t.data_ptr() for t in grads)
-        _call(device, _lib.tgemm_ffn_backward, M, K, F, N, code, act, x2.data_ptr(), ldx, wg.data_ptr(), ldg, wu.data_ptr(), ldu,
-              wd.data_ptr(), ldd, g.data_ptr(), ldy, keep, saved.data_ptr(), dx, K, dg, K, du, K, dd, F, scratch.data_ptr())
+        grads = [torch.empty_like(t, memory_format=torch.contiguous_format) if keep >> i & 1 else None for i, t in enumerate(inputs)]
+        dx, dg, du, dd = [None if t is None else t.data_ptr() for t in grads]
+        _call(device, _lib.tgemm_ffn_backward, M, K, F, N, code, act, *_pointers(operands), g.data_ptr(), ldy, keep,
+              saved.data_ptr(), dx, K, dg, K, du, K, dd, F, scratch.data_ptr())
         return (*grads, None, None)
 
 
@@ -911,7 +923,7 @@ def gated_ffn(x, w_gate, w_up, w_down, activation="silu"):
         raise ValueError("x %s, w_gate %s, w_up %s and w_down %s do not make a feed-forward block" % tuple(
             tuple(t.shape) for t in tensors))
     if not _wants_derivative(tensors):
-        return _ffn_forward(x, w_gate, w_up, w_down, code, act, 0)[0]
+        return _ffn_forward(x, *_ffn_call(*tensors), code, act, 0)[0]
     return _GatedFfn.apply(x, w_gate, w_up, w_down, code, act)
 
 
@@ -1044,7 +1056,7 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None):
             raise TypeError("grads has unsupported dtype %s (float32, bfloat16, float16)" % t.dtype)
         if t.device != device:
             raise ValueError("grads must be on one GPU (%s, %s)" % (device, t.device))
-        if not _dense(t):
+        if not t.is_contiguous() and not _dense(t):
             raise ValueError("grads must be dense (shape %s, strides %s)" % (tuple(t.shape), t.stride()))
         codes.append(code)
         counts.append(t.numel())
@@ -1053,8 +1065,8 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None):
     if out is not grads:
         outs = []
         for t, o in zip(grads, out):
-            if o.dtype != t.dtype or o.shape != t.shape or o.device != device or o.stride() != t.stride() and not (
-                    o.is_contiguous() and t.is_contiguous()):
+            if o.dtype is not t.dtype or o.shape != t.shape or o.device != device or not (
+                    o.is_contiguous() and t.is_contiguous()) and o.stride() != t.stride():
                 raise ValueError("out must match grads: %s %s %s with strides %s, got %s %s %s with strides %s" % (
                     t.dtype, tuple(t.shape), device, t.stride(), o.dtype, tuple(o.shape), o.device, o.stride()))
             outs.append(o.data_ptr())
