@@ -4,7 +4,9 @@
 //
 // Three launches: sums of squares of pieces, the norm and the factor from them,
 // the product.  Bound by memory: every element is read twice and written once;
-// where the factor is one and the tensors stay in place, read once.  Squares are
+// where the factor is one and the tensors stay in place, read once.  The product
+// goes from the end to the beginning, so that it finds in the last-level cache
+// what the squares read last.  Squares are
 // added in 64 bits (float32 gradients of 1e20 would overflow a float's square;
 // the conversions hide behind the loads), in an order that does not depend on
 // which workgroup ends first.
@@ -39,15 +41,15 @@ static_assert(sizeof(ClipArgs) <= 4096, "kernel arguments");
 struct ClipPlace {
     int tensor;
     int64_t begin, end;
-    __device__ __forceinline__ explicit ClipPlace(const ClipArgs& g) {
+    __device__ __forceinline__ ClipPlace(const ClipArgs& g, uint32_t group) {
         int lo = 0, hi = g.tensors - 1;  // the last tensor that starts at or before this workgroup
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
-            if (g.first[mid] <= blockIdx.x) lo = mid;
+            if (g.first[mid] <= group) lo = mid;
             else hi = mid - 1;
         }
         tensor = lo;
-        begin = (int64_t)(blockIdx.x - g.first[lo]) * g.piece;
+        begin = (int64_t)(group - g.first[lo]) * g.piece;
         end = min(begin + g.piece, g.count[lo]);
     }
 };
@@ -104,7 +106,7 @@ __device__ __forceinline__ double clip_block_sum(double v) {
 }
 
 __global__ __launch_bounds__(CLIP_THREADS) void clip_squares_kernel(ClipArgs g) {
-    const ClipPlace at(g);
+    const ClipPlace at(g, blockIdx.x);
     double s;
     switch (g.dtype[at.tensor]) {
         case TGEMM_F32: s = piece_squares(static_cast<const float*>(g.in[at.tensor]), at.begin, at.end); break;
@@ -163,7 +165,11 @@ __device__ __forceinline__ void piece_times(const T* in, T* out, int64_t begin, 
 }
 
 __global__ __launch_bounds__(CLIP_THREADS) void clip_times_kernel(ClipArgs g) {
-    const ClipPlace at(g);
+    // tensors are listed from the last on; each from its end on
+    ClipPlace at(g, blockIdx.x);
+    const int64_t pieces = (g.count[at.tensor] + g.piece - 1) / g.piece;
+    at.begin = (pieces - 1) * g.piece - at.begin;
+    at.end = min(at.begin + g.piece, g.count[at.tensor]);
     const float f = *g.factor;
     const void* in = g.in[at.tensor];
     void* out = g.out[at.tensor];
@@ -248,40 +254,37 @@ int tgemm_clip(int64_t tensors, const void* const* in, void* const* out, const i
     float* factor = static_cast<float*>(workspace);
     double* sums = reinterpret_cast<double*>(static_cast<char*>(workspace) + 256);
     const int64_t piece = clip_piece(total);
-    int64_t groups = 0;
-    for (int pass = 0; pass < 2 && rc == TGEMM_OK; ++pass) {
-        int64_t done = 0;
+    // Up to CLIP_TENSORS tensors a launch, from the first on or from the last.
+    auto launches = [&](const void* fn, bool back, int64_t* groups) {
         for (int64_t i = 0; i < tensors && rc == TGEMM_OK;) {
             ClipArgs a{};
             a.piece = (int32_t)piece;
-            a.sums = sums + done;
+            a.sums = sums + *groups;
             a.factor = factor;
             int64_t n = 0;
             for (; i < tensors && a.tensors < CLIP_TENSORS; ++i) {
-                if (counts[i] == 0) continue;
+                const int64_t t = back ? tensors - 1 - i : i;
+                if (counts[t] == 0) continue;
                 const int k = a.tensors++;
-                a.in[k] = in[i];
-                a.out[k] = out[i];
-                a.count[k] = counts[i];
-                a.dtype[k] = (uint8_t)dtypes[i];
+                a.in[k] = in[t];
+                a.out[k] = out[t];
+                a.count[k] = counts[t];
+                a.dtype[k] = (uint8_t)dtypes[t];
                 a.first[k] = (uint32_t)n;
-                n += (counts[i] + piece - 1) / piece;
+                n += (counts[t] + piece - 1) / piece;
             }
             if (n == 0) continue;
-            rc = mm_launch(reinterpret_cast<const void*>(pass ? clip_times_kernel : clip_squares_kernel), n, CLIP_THREADS, &a,
-                           "clipping", st);
-            done += n;
+            rc = mm_launch(fn, n, CLIP_THREADS, &a, "clipping", st);
+            *groups += n;
         }
-        if (pass == 0 && rc == TGEMM_OK) {
-            groups = done;
-            hipLaunchKernelGGL(clip_norm_kernel, dim3(1), dim3(1024), 0, st, sums, groups, max_norm, eps, norm, factor);
-            const hipError_t err = hipGetLastError();
-            if (err != hipSuccess) {
-                set_error("launch of the norm failed: %s", hipGetErrorString(err));
-                rc = TGEMM_E_HIP;
-            }
-        }
+    };
+    int64_t groups = 0, again = 0;
+    launches(reinterpret_cast<const void*>(clip_squares_kernel), false, &groups);
+    if (rc == TGEMM_OK) {
+        void* args[] = {&sums, &groups, &max_norm, &eps, &norm, &factor};
+        rc = mm_launch_list(reinterpret_cast<const void*>(clip_norm_kernel), 1, 1024, args, "norm", st);
     }
+    launches(reinterpret_cast<const void*>(clip_times_kernel), true, &again);
     if (rc == TGEMM_OK) clear_error();
     return rc;
 }

@@ -70,7 +70,8 @@ struct MmStoreArgs {
 struct MmGateArgs {
     MmOperands op;
     MmGrid grid;
-    void *h, *g, *u;  // M x N, row stride ld; g and u NULL where nothing is kept
+    void *h, *g, *u;  // M x N, row stride ld; g and u NULL where nothing is kept.  Anything
+                      // may be written between N and ld
     int64_t ld;
     int32_t act;
 };
@@ -79,7 +80,8 @@ struct MmDhArgs {
     MmOperands op;
     MmGrid grid;
     const void *g, *u;
-    void *dg, *du, *h;  // M x N, row stride ld (g's and u's too); any of them NULL where it is not wanted
+    void *dg, *du, *h;  // M x N, row stride ld (g's and u's too); any of them NULL where it is not
+                        // wanted.  Anything may be written between N and ld
     int64_t ld;
     int32_t act;
 };
@@ -104,7 +106,7 @@ struct MmDzArgs {
     int64_t v0;
     const float* lse;
     const float* coef;  // of each row
-    void* dz;           // M x N, row stride ldz elements
+    void* dz;           // M x N, row stride ldz elements; anything may be written between
     int64_t ldz;
 };
 
@@ -342,7 +344,7 @@ __device__ __forceinline__ void mm_join(const MmStoreArgs& g, int slice, int til
     const float* p = g.split + (int64_t)tile * plan.splits * (BM * BN) + e;
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const int per = (plan.splits + 3) / 4, end = min((wave + 1) * per, plan.splits);
-#pragma unroll 4
+#pragma unroll 8
     for (int s = wave * per; s < end; ++s) {
         float x[8];
         __builtin_memcpy(x, p + (int64_t)s * (BM * BN), 32);
@@ -414,7 +416,7 @@ __global__ __launch_bounds__(G::NT) void mm_gate_kernel(MmGateArgs g) {
     typename G::Acc acc;
     G::clear(acc);
     G::product(g.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, smem, acc, at.wm0, at.wn0, at.lane, at.wave);
-    const MmOut<G> out(at, g.op.M, g.op.N, g.ld);
+    const MmOut<G> out(at, g.op.M, (int)g.ld, g.ld);  // rows whole up to their stride: no edge inside them
     typedef float(&F8)[8];
     auto way = [&](auto inside) {
         G::each_row(acc, smem, at.lane, at.wave, [&](int u, F8 v, F8 w) {
@@ -446,7 +448,7 @@ __global__ __launch_bounds__(G::NT) void mm_dh_kernel(MmDhArgs g) {
     typename G::Acc acc;
     G::clear(acc);
     G::product(g.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, smem, acc, at.wm0, at.wn0, at.lane, at.wave);
-    const MmOut<G> out(at, g.op.M, g.op.N, g.ld);
+    const MmOut<G> out(at, g.op.M, (int)g.ld, g.ld);  // rows whole up to their stride: no edge inside them
     typedef float(&F8)[8];
     struct Kept {
         Raw8 g, u;
@@ -574,7 +576,7 @@ __global__ __launch_bounds__(G::NT) void mm_dz_kernel(MmDzArgs g) {
     G::product(known.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, smem, acc, at.wm0, at.wn0, at.lane, at.wave);
     const int M = known.op.M;
     T* dz = static_cast<T*>(g.dz);
-    const MmOut<G> out(at, (M + 63) / 64 * 64, g.op.N, g.ldz);
+    const MmOut<G> out(at, (M + 63) / 64 * 64, (int)g.ldz, g.ldz);  // rows whole up to their stride
     typedef float(&F8)[8];
     struct Row {
         float lse, coef;
@@ -606,7 +608,7 @@ __global__ __launch_bounds__(G::NT) void mm_dz_kernel(MmDzArgs g) {
             }
         });
     };
-    if (G::inside(out.m1, out.n1, M, g.op.N)) way(Yes{});
+    if (G::inside(out.m1, out.n1, M, out.N)) way(Yes{});
     else way(No{});
 }
 

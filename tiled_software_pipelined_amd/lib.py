@@ -1049,12 +1049,13 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None):
     n, device = len(grads), grads[0].device
     if not grads[0].is_cuda:
         raise ValueError("grads must be GPU tensors")
+    index = device.index
     codes, counts, ins = [], [], []
     for t in grads:
         code = _REAL_CODES.get(t.dtype)
         if code is None:
             raise TypeError("grads has unsupported dtype %s (float32, bfloat16, float16)" % t.dtype)
-        if t.device != device:
+        if t.get_device() != index:
             raise ValueError("grads must be on one GPU (%s, %s)" % (device, t.device))
         if not t.is_contiguous() and not _dense(t):
             raise ValueError("grads must be dense (shape %s, strides %s)" % (tuple(t.shape), t.stride()))
@@ -1065,15 +1066,16 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None):
     if out is not grads:
         outs = []
         for t, o in zip(grads, out):
-            if o.dtype is not t.dtype or o.shape != t.shape or o.device != device or not (
+            if o.dtype is not t.dtype or o.get_device() != index or o.shape != t.shape or not (
                     o.is_contiguous() and t.is_contiguous()) and o.stride() != t.stride():
                 raise ValueError("out must match grads: %s %s %s with strides %s, got %s %s %s with strides %s" % (
                     t.dtype, tuple(t.shape), device, t.stride(), o.dtype, tuple(o.shape), o.device, o.stride()))
             outs.append(o.data_ptr())
-    for pointers in (ins, outs):
-        used = [p for p, c in zip(pointers, counts) if c]
-        if len(set(used)) != len(used):
-            raise ValueError("a tensor is given twice")
+    for pointers in (ins,) if outs is ins else (ins, outs):
+        if len(set(pointers)) != n:  # empty tensors may share an address
+            used = [p for p, c in zip(pointers, counts) if c]
+            if len(set(used)) != len(used):
+                raise ValueError("a tensor is given twice")
     i64s = ctypes.c_int64 * n
     sizes = i64s(*counts)
     need = _lib.tgemm_clip_workspace_bytes(n, sizes)
@@ -1084,5 +1086,8 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None):
     norm = torch.empty((), dtype=torch.float32, device=device)
     _call(device, _lib.tgemm_clip, n, pointers(*ins), pointers(*outs), sizes, (ctypes.c_int32 * n)(*codes), max_norm, eps,
           norm.data_ptr(), ws.data_ptr(), need)
-    torch.autograd.graph.increment_version([t for t in out if not t.is_inference()])
+    try:
+        torch.autograd.graph.increment_version(out)
+    except RuntimeError:  # inference tensors have no version
+        torch.autograd.graph.increment_version([t for t in out if not t.is_inference()])
     return norm
