@@ -34,7 +34,7 @@ static FfnLayout ffn_layout(int64_t M, int64_t K, int64_t F, int64_t N, int keep
         l.bytes[which] += (n + 255) / 256 * 256;
         return at;
     };
-    l.rows = M <= 32;
+    l.rows = M <= MM_ROWS;
     l.ld = (F + 63) / 64 * 64;
     const int64_t inner = 2 * M * l.ld;
     const MmShape y{M, N}, x{M, K}, dw[3] = {{F, K}, {F, K}, {N, F}};
@@ -110,11 +110,9 @@ static MmOperands operands(const void* a, int64_t lda, const void* b, int64_t ld
 }
 
 template <bool PAIR>
-static const void* rows_kernel(int dtype, int64_t M) {
-    typedef void (*Fn)(MmRowsArgs);
-    const Fn fn = dtype == TGEMM_BF16 ? (M <= 16 ? (Fn)mm_rows_kernel<MmBf16, 1, 4, PAIR> : (Fn)mm_rows_kernel<MmBf16, 2, 2, PAIR>)
-                                      : (M <= 16 ? (Fn)mm_rows_kernel<MmF16, 1, 4, PAIR> : (Fn)mm_rows_kernel<MmF16, 2, 2, PAIR>);
-    return reinterpret_cast<const void*>(fn);
+static const void* rows_kernel(int dtype) {
+    return dtype == TGEMM_BF16 ? reinterpret_cast<const void*>(mm_rows_kernel<MmBf16, PAIR>)
+                               : reinterpret_cast<const void*>(mm_rows_kernel<MmF16, PAIR>);
 }
 
 }  // namespace tg
@@ -178,7 +176,7 @@ int tgemm_ffn_forward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype,
         o.ldb2 = 2 * ldu;
         if (l.rows && l.g < 0) {
             MmRowsArgs a{o, h, l.ld, act};
-            rc = mm_launch(rows_kernel<true>(dtype, M), (F + 15) / 16, 512, &a, "gate and up projections", st);
+            rc = mm_launch(rows_kernel<true>(dtype), (F + 15) / 16, 512, &a, "gate and up projections", st);
         } else {
             const MmKernel& k = mm_kernels(dtype, FORM_GATE)[l.gate];
             MmGateArgs a{o, mm_grid(k, M, F), h, l.g < 0 ? nullptr : v + l.g, l.u < 0 ? nullptr : v + l.u, l.ld, act};
@@ -188,7 +186,7 @@ int tgemm_ffn_forward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype,
     if (rc == TGEMM_OK && M > 0 && N > 0) {
         if (l.rows) {
             MmRowsArgs a{operands(h, l.ld, wd, ldd, M, N, F), y, ldy, 0};
-            rc = mm_launch(rows_kernel<false>(dtype, M), (N + 15) / 16, 512, &a, "down projection", st);
+            rc = mm_launch(rows_kernel<false>(dtype), (N + 15) / 16, 512, &a, "down projection", st);
         } else {
             MmStoreArgs a{};
             a.jobs = 1;

@@ -479,7 +479,7 @@ struct No {
     static constexpr bool value = false;
 };
 
-// 8 adjacent values in memory; `count` of them, which may be none, inside the row.
+// 8 adjacent values in memory.
 struct Raw8 {
     i32x4 v;
 };
@@ -490,8 +490,8 @@ __device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
     for (int e = 0; e < 8; ++e) o[e] = (T)v[e];  // to nearest even
     __builtin_memcpy(dst, o, 16);
 }
-// The empty statements keep the compiler from making one run of element stores of
-// both branches.
+// `count` of them, which may be none, inside the row.  The empty statements keep
+// the compiler from making one run of element stores of both branches.
 template <class T>
 __device__ __forceinline__ void store8(T* dst, const float (&v)[8], int count) {
     if (count >= 8) {
@@ -506,18 +506,6 @@ __device__ __forceinline__ void store8(T* dst, const float (&v)[8], int count) {
 }
 template <class T>
 __device__ __forceinline__ void load8(Raw8& x, const T* src) { x.v = load16(src); }
-template <class T>
-__device__ __forceinline__ void load8(Raw8& x, const T* src, int count) {
-    if (count >= 8) {
-        x.v = load16(src);
-    } else {
-        union { i32x4 v; T e[8]; } u;
-        asm volatile("; part of 8" ::: "memory");
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u.e[e] = load_or_zero(src + e, e < count);
-        x.v = u.v;
-    }
-}
 template <class T>
 __device__ __forceinline__ void values8(float (&v)[8], const Raw8& x) {
     T o[8];

@@ -24,7 +24,9 @@ struct MmSchedule {
     int32_t full, rest, splits, per;
     __host__ __device__ __forceinline__ int total() const { return full + rest * splits; }
 };
-constexpr int MM_SPLITS = 64, MM_LEAST_SLICES = 8;
+// more parts than 16 pay nowhere: 60x768x50257 in 16 takes 24 us and 6 for the
+// join, in 64 27 and 15
+constexpr int MM_SPLITS = 16, MM_LEAST_SLICES = 8;
 __host__ __device__ __forceinline__ MmSchedule mm_schedule(int tiles, int slices, int slots, int slice, int tile_kb, bool may_split) {
     MmSchedule s{tiles, 0, 1, slices};
     const int rest = tiles % slots;
@@ -328,8 +330,7 @@ __global__ __launch_bounds__(G::NT) void mm_store_kernel(MmStoreArgs g) {
 
 // C = alpha sum of the parts of the tiles that mm_store_kernel shared out, in an
 // order that does not depend on who ended first.  A workgroup takes 512 results of
-// a tile: each wave adds a quarter of the parts (all of them in one wave: 17 us
-// for 64 parts of 64 x 128, so 9).
+// a tile: each wave adds a quarter of the parts.
 constexpr int MM_JOIN = 512;
 template <class T, int BM, int BN, int SLOTS>
 __device__ __forceinline__ void mm_join(const MmStoreArgs& g, int slice, int tile_kb) {
@@ -344,7 +345,7 @@ __device__ __forceinline__ void mm_join(const MmStoreArgs& g, int slice, int til
     const float* p = g.split + (int64_t)tile * plan.splits * (BM * BN) + e;
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const int per = (plan.splits + 3) / 4, end = min((wave + 1) * per, plan.splits);
-#pragma unroll 8
+#pragma unroll 4
     for (int s = wave * per; s < end; ++s) {
         float x[8];
         __builtin_memcpy(x, p + (int64_t)s * (BM * BN), 32);
@@ -421,8 +422,7 @@ __global__ __launch_bounds__(G::NT) void mm_gate_kernel(MmGateArgs g) {
     auto way = [&](auto inside) {
         G::each_row(acc, smem, at.lane, at.wave, [&](int u, F8 v, F8 w) {
             auto put = [&](void* p, F8 x) {
-                if (inside.value) store8(out.at(static_cast<T*>(p), u), x);
-                else store8(out.at(static_cast<T*>(p), u), x, out.count(u));
+                if (inside.value || out.count(u) > 0) store8(out.at(static_cast<T*>(p), u), x);
             };
             if (g.g) {
                 put(g.g, v);
@@ -456,17 +456,13 @@ __global__ __launch_bounds__(G::NT) void mm_dh_kernel(MmDhArgs g) {
     auto way = [&](auto inside) {
         G::template each_row<Kept>(acc, smem, at.lane, at.wave, [&](int u, Kept& k) {
             const T *pg = out.at(static_cast<const T*>(g.g), u), *pu = out.at(static_cast<const T*>(g.u), u);
-            if (inside.value) {
+            if (inside.value || out.count(u) > 0) {
                 load8(k.g, pg);
                 load8(k.u, pu);
-            } else {
-                load8(k.g, pg, out.count(u));
-                load8(k.u, pu, out.count(u));
             }
         }, [&](int u, F8 v, F8, Kept& k) {
             auto put = [&](void* p, F8 x) {
-                if (inside.value) store8(out.at(static_cast<T*>(p), u), x);
-                else store8(out.at(static_cast<T*>(p), u), x, out.count(u));
+                if (inside.value || out.count(u) > 0) store8(out.at(static_cast<T*>(p), u), x);
             };
             float gate[8], up[8], a[8], d[8], o[8];
             values8<T>(gate, k.g);
@@ -604,7 +600,7 @@ __global__ __launch_bounds__(G::NT) void mm_dz_kernel(MmDzArgs g) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] = 0.0f;
                 }
-                store8(out.at(dz, u), v, out.count(u));
+                if (out.count(u) > 0) store8(out.at(dz, u), v);
             }
         });
     };
@@ -613,13 +609,15 @@ __global__ __launch_bounds__(G::NT) void mm_dz_kernel(MmDzArgs g) {
 }
 
 // ---- few rows of A -----------------------------------------------------------
-// A served batch of up to 32 tokens is bound by one read of the weights.  A
-// workgroup takes 16 rows of B (PAIR: of both matrices) and all rows of A; its
-// eight waves deal blocks of 64 k among them, operands going straight to
-// registers, and add their sums through LDS.  v_mfma_f32_16x16x32: lane l
-// holds row l % 16, k 8 (l / 16) .. + 7 of 32; of a block's 128 bytes of a row it
-// reads chunks l / 16 and 4 + l / 16, so one load reads 64 adjacent bytes of
-// each of 16 rows.
+// A served batch of up to 16 tokens is bound by one read of the weights (180 MB in
+// 34 us, 5.3 TB/s, for one; 4096x11008 block in all 58 us for one token, 68 for
+// 16, and 73 on the tiles for 17 to 64).  A workgroup takes 16 rows of B (PAIR: of
+// both matrices) and all rows of A; its eight waves deal blocks of 64 k among them,
+// operands going straight to registers, U blocks in flight, and add their sums
+// through LDS.  v_mfma_f32_16x16x32: lane l holds row l % 16, k 8 (l / 16) .. + 7
+// of 32; of a block's 128 bytes of a row it reads chunks l / 16 and 4 + l / 16,
+// so one load reads 64 adjacent bytes of each of 16 rows.
+constexpr int MM_ROWS = 16;
 struct MmRowsArgs {
     MmOperands op;
     void* C;  // M x N, row stride ldc elements
@@ -627,10 +625,10 @@ struct MmRowsArgs {
     int32_t act;
 };
 
-template <class Tr, int MT, int U, bool PAIR>
+template <class Tr, bool PAIR>
 __global__ __launch_bounds__(512) void mm_rows_kernel(MmRowsArgs g) {
-    constexpr int NW = 8, NB = PAIR ? 2 : 1;
-    __shared__ float part[NW][NB * MT * 256];
+    constexpr int NW = 8, U = 4, NB = PAIR ? 2 : 1;
+    __shared__ float part[NW][NB * 256];
     typedef typename Tr::T T;
     const MmOperands& o = g.op;
     const int lane = lane_id(), wave = wave_id();
@@ -639,16 +637,12 @@ __global__ __launch_bounds__(512) void mm_rows_kernel(MmRowsArgs g) {
     const char* brow[NB];
     brow[0] = o.b + (int64_t)min(n0 + (lane & 15), o.N - 1) * o.ldb;
     if constexpr (PAIR) brow[1] = o.b2 + (int64_t)min(n0 + (lane & 15), o.N - 1) * o.ldb2;
-    const char* arow[MT];
+    const char* arow = o.a + (int64_t)min(lane & 15, o.M - 1) * o.lda;
+    f32x4 acc[NB];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) arow[t] = o.a + (int64_t)min(16 * t + (lane & 15), o.M - 1) * o.lda;
-    f32x4 acc[NB][MT];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int t = 0; t < MT; ++t) acc[b][t] = f32x4{0, 0, 0, 0};
+    for (int b = 0; b < NB; ++b) acc[b] = f32x4{0, 0, 0, 0};
     struct Block {
-        i32x4 b[NB][2], a[MT][2];
+        i32x4 b[NB][2], a[2];
     };
     auto load = [&](Block& x, int kb) {
         const int64_t k0 = (int64_t)kb * 128 + at;
@@ -657,16 +651,14 @@ __global__ __launch_bounds__(512) void mm_rows_kernel(MmRowsArgs g) {
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b) x.b[b][h] = load16(brow[b] + k0 + 64 * h);
-#pragma unroll
-                for (int t = 0; t < MT; ++t) x.a[t][h] = load16(arow[t] + k0 + 64 * h);
+                x.a[h] = load16(arow + k0 + 64 * h);
             }
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b) x.b[b][h] = row_end_chunk(brow[b], (int)k0 + 64 * h, bytes);
-#pragma unroll
-                for (int t = 0; t < MT; ++t) x.a[t][h] = row_end_chunk(arow[t], (int)k0 + 64 * h, bytes);
+                x.a[h] = row_end_chunk(arow, (int)k0 + 64 * h, bytes);
             }
         }
     };
@@ -674,9 +666,7 @@ __global__ __launch_bounds__(512) void mm_rows_kernel(MmRowsArgs g) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int t = 0; t < MT; ++t) acc[b][t] = Tr::mma16(x.a[t][h], x.b[b][h], acc[b][t]);
+            for (int b = 0; b < NB; ++b) acc[b] = Tr::mma16(x.a[h], x.b[b][h], acc[b]);
     };
     int kb = wave;
     for (; kb + (U - 1) * NW < blocks; kb += U * NW) {
@@ -694,25 +684,22 @@ __global__ __launch_bounds__(512) void mm_rows_kernel(MmRowsArgs g) {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                part[wave][(b * MT + t) * 256 + (4 * (lane >> 4) + r) * 16 + (lane & 15)] = acc[b][t][r];
+        for (int r = 0; r < 4; ++r) part[wave][b * 256 + (4 * (lane >> 4) + r) * 16 + (lane & 15)] = acc[b][r];
     __syncthreads();
-    for (int e = threadIdx.x; e < MT * 256; e += 512) {
-        float v[8] = {}, w[8] = {}, a[8], d[8];
+    const int e = threadIdx.x;
+    if (e >= 256) return;
+    float v[8] = {}, w[8] = {}, a[8], d[8];
 #pragma unroll
-        for (int k = 0; k < NW; ++k) {
-            v[0] += part[k][e];
-            if constexpr (PAIR) w[0] += part[k][MT * 256 + e];
-        }
-        if constexpr (PAIR) {
-            activate8<false>(g.act, v, a, d);
-            v[0] = a[0] * w[0];
-        }
-        const int m = e >> 4, n = n0 + (e & 15);
-        if (m < o.M && n < o.N) static_cast<T*>(g.C)[m * g.ldc + n] = (T)v[0];
+    for (int k = 0; k < NW; ++k) {
+        v[0] += part[k][e];
+        if constexpr (PAIR) w[0] += part[k][256 + e];
     }
+    if constexpr (PAIR) {
+        activate8<false>(g.act, v, a, d);
+        v[0] = a[0] * w[0];
+    }
+    const int m = e >> 4, n = n0 + (e & 15);
+    if (m < o.M && n < o.N) static_cast<T*>(g.C)[m * g.ldc + n] = (T)v[0];
 }
 
 // ---- the table ---------------------------------------------------------------

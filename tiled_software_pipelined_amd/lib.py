@@ -907,7 +907,7 @@ def gated_ffn(x, w_gate, w_up, w_down, activation="silu"):
     (..., N) of x's dtype.  Sums are float; the inner values (and, for the
     backward pass, both projections and their gradients) are rounded to x's dtype,
     y and each gradient once.  The two projections, the activation and their
-    product are one kernel; up to 32 tokens without gradients take kernels that read
+    product are one kernel; up to 16 tokens without gradients take kernels that read
     each weight once.  The backward pass keeps the two projections (two values
     for each token and inner unit) and computes only the gradients that are asked
     for; second derivatives and forward-mode ones are refused.  To capture a
