@@ -88,6 +88,27 @@ def test_layouts_neighbours_and_versions():
     assert abs(float(t.norm()) - 1) < 1e-5
 
 
+def test_refusals_on_the_gpu():
+    a, b = torch.ones(6, device="cuda"), torch.ones(6, device="cuda")
+    with pytest.raises(ValueError, match="twice"):
+        tl.clip_grad_norm([a, b, a], 1.0)
+    with pytest.raises(ValueError, match="twice"):
+        tl.clip_grad_norm([a, b], 1.0, out=[a, a])
+    with pytest.raises(ValueError, match="another"):
+        tl.clip_grad_norm([a, b], 1.0, out=[b, torch.ones(6, device="cuda")])
+    for bad in ([a.cpu(), b], [a, b.cpu()], [a, torch.ones(6, 2, device="cuda")[:, 0]]):
+        with pytest.raises(ValueError):
+            tl.clip_grad_norm(bad, 1.0)
+    with pytest.raises(TypeError):
+        tl.clip_grad_norm([a.double()], 1.0)
+    for o in (b.half(), b[:5], b.view(2, 3), b.cpu()):
+        with pytest.raises(ValueError, match="out must"):
+            tl.clip_grad_norm([a], 1.0, out=[o])
+    assert (a == 1).all() and (b == 1).all()
+    norm = tl.clip_grad_norm([a[:0], b, a[:0]], 1.0)  # empty tensors may come twice
+    assert abs(float(norm) - 6 ** 0.5) < 1e-6
+
+
 def test_captured_and_replayed_and_streams():
     shapes = [(300, 70), (70,), (1000,)] * 50  # more tensors than a launch takes
     grads = make(shapes, (torch.bfloat16, torch.float32))

@@ -37,6 +37,16 @@ def test_sizes(M, K, F, N, dtype):
         ref.check({"y": tl.gated_ffn(*leaves)}, ref.ffn(*leaves, "silu"))
 
 
+@pytest.mark.parametrize("M,K,F,N,dtype", [
+    (4100, 520, 5128, 4104, torch.bfloat16), (2050, 2056, 5000, 2056, torch.float16), (1500, 1032, 8200, 4100, torch.bfloat16),
+    (520, 2056, 2056, 2056, torch.float16), (3000, 640, 9001, 650, torch.float16), (600, 3000, 6001, 3001, torch.bfloat16),
+    (4100, 4104, 520, 72, torch.float16), (800, 333, 517, 129, torch.bfloat16), (4100, 90, 130, 70, torch.bfloat16)])
+def test_large_sizes(M, K, F, N, dtype):
+    """Every tile of every product, whole rounds of them and rests that are shared out along k; rows copied to lines."""
+    *leaves, dy = make(M, K, F, N, dtype)
+    ref.check(run(leaves, dy, "silu"), ref.ffn(*leaves, "silu", dy))
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("act", list(tl.ACTIVATIONS))
 @pytest.mark.parametrize("M", [9, 150])
@@ -59,6 +69,22 @@ def test_activations_over_their_range(act):
         # two roundings to float16; the activation is good to 2^-20 of its value and 2^-23 of its argument
         bound = 2 * 2.0 ** -11 * want.abs() + 2.0 ** -24 + 2.0 ** -20 * want.abs() + 2.0 ** -23 * gd.abs() * (gd > -20)
         assert ((y - want).abs() <= bound).all(), float(((y - want).abs() - bound).max())
+
+
+@pytest.mark.parametrize("act", list(tl.ACTIVATIONS))
+def test_activations_at_the_ends_of_bfloat16(act):
+    """Where act is 0 or its argument, so are the gradients 0 or those of a product, up to 1e30."""
+    big = torch.tensor([1e4, -1e4, 1e20, -1e20, 1e30, -1e30], dtype=torch.bfloat16, device="cuda")
+    F = big.numel()
+    one = lambda *s: torch.ones(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    eye = torch.eye(F, dtype=torch.bfloat16, device="cuda")
+    for rows in (1, 40):
+        got = run([one(rows, 1), big[:, None], one(F, 1), eye], one(rows, F), act)
+        up = big > 0
+        assert torch.equal(got["y"], torch.where(up, big, 0).expand(rows, F))
+        # dg = act'(g) = 1 or 0, du = act(g)
+        assert torch.equal(got["dw_gate"][:, 0], torch.where(up, float(rows), 0.0).bfloat16())
+        assert ((got["dw_up"][:, 0].double() - rows * torch.where(up, big, 0).double()).abs() <= 2.0 ** -8 * rows * big.abs().double()).all()
 
 
 @pytest.mark.parametrize("needs", [n for n in itertools.product((False, True), repeat=4) if any(n)])
@@ -202,3 +228,25 @@ def test_no_write_outside_the_outputs():
     got = run(leaves, dy, "silu")
     for k, t in held.items():
         assert torch.equal(t[1:-1, :-5], got[k]) and (t[0] == 7).all() and (t[-1] == 7).all() and (t[:, -5:] == 7).all(), k
+
+
+def test_derivatives_that_are_refused():
+    *leaves, dy = make(5, 8, 16, 8, torch.bfloat16)
+    x = leaves[0].requires_grad_()
+    (g,) = torch.autograd.grad(tl.gated_ffn(*leaves), x, dy.requires_grad_(), create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+    with torch.autograd.forward_ad.dual_level(), pytest.raises(RuntimeError):
+        dual = torch.autograd.forward_ad.make_dual(leaves[0].detach(), torch.ones_like(leaves[0]))
+        tl.gated_ffn(dual, *leaves[1:])
+
+
+def test_refusals_on_the_gpu():
+    x, wg, wu, wd, _ = make(4, 8, 16, 8, torch.bfloat16)
+    with pytest.raises(TypeError, match="w_up"):
+        tl.gated_ffn(x, wg, wu.half(), wd)
+    for bad in ([x, wg[:, :7], wu, wd], [x, wg, wu[:15], wd], [x, wg, wu, wd[:, :15]], [x, wg[0], wu[0], wd], [x[0, 0], wg, wu, wd]):
+        with pytest.raises(ValueError, match="feed-forward"):
+            tl.gated_ffn(*bad)
+    with pytest.raises(ValueError, match="one GPU"):
+        tl.gated_ffn(x, wg, wu.cpu(), wd)

@@ -39,6 +39,24 @@ def test_sizes(M, V, K, dtype):
         ref.check({"loss": tl.linear_cross_entropy(x, w, t)}, ref.xent(x, w, t))
 
 
+@pytest.mark.parametrize("M,V,K,dtype", [
+    (1000, 30001, 520, torch.bfloat16), (4100, 9001, 1032, torch.float16), (2050, 33000, 264, torch.bfloat16),
+    (9000, 33001, 72, torch.float16), (40000, 9000, 136, torch.bfloat16), (1024, 2048, 1024, torch.float16),
+    (1030, 4100, 2056, torch.bfloat16), (800, 1001, 333, torch.float16), (4200, 777, 90, torch.bfloat16)])
+def test_large_sizes(M, V, K, dtype):
+    """Every tile of every product, one piece of the vocabulary and several, weights copied to lines."""
+    x, w, t = make(M, V, K, dtype)
+    ref.check(run(x, w, t, 100.0), ref.xent(x, w, t, dloss=100.0))
+
+
+@pytest.mark.parametrize("M,V", [(1, 4200001), (3, 4194560)])
+def test_a_few_rows_and_millions_of_words(M, V):
+    """dz in pieces although it is small: its 64 rows are read by 32-bit offsets."""
+    x, w, t = make(M, V, 8, torch.bfloat16, ignored=0.0)
+    assert tl._xent_bytes(M, V, 8, 3)[2] < 2 ** 30
+    ref.check(run(x, w, t), ref.xent(x, w, t, dloss=1.0))
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("reduction", ["none", "sum", "mean"])
 def test_reductions(reduction, dtype):
@@ -244,3 +262,53 @@ def test_streams_side_by_side():
     torch.cuda.synchronize()
     for w, g in zip(want, got):
         assert all(torch.equal(w[k], g[k]) for k in w)
+
+
+def test_same_bits_every_time():
+    x, w, t = make(600, 9000, 256, torch.bfloat16)
+    first = run(x, w, t)
+    for _ in range(3):
+        again = run(x, w, t)
+        assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+def test_no_write_outside_the_outputs():
+    M, V, K = 37, 75, 33
+    x, w, t = make(M, V, K, torch.bfloat16)
+    held = {k: torch.full((r + 2, K + 5), 7.0, dtype=torch.bfloat16, device="cuda") for k, r in {"dx": M, "dw": V}.items()}
+    loss, dloss = torch.full((M + 2,), 7.0, device="cuda"), torch.ones(M, device="cuda")
+    saved, s1, s2 = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in tl._xent_bytes(M, V, K, 3))
+    at = lambda k: (held[k][1:].data_ptr(), K + 5)  # noqa: E731
+    tl._call(x.device, tl._lib.tgemm_xent_forward, M, V, K, tl.BF16, x.data_ptr(), K, w.data_ptr(), K, t.data_ptr(), -100, 0,
+             loss[1:].data_ptr(), saved.data_ptr(), s1.data_ptr())
+    tl._call(x.device, tl._lib.tgemm_xent_backward, M, V, K, tl.BF16, x.data_ptr(), K, w.data_ptr(), K, t.data_ptr(), 0,
+             dloss.data_ptr(), saved.data_ptr(), 3, *at("dx"), *at("dw"), s2.data_ptr())
+    got = run(x, w, t, 1.0, "none")
+    assert torch.equal(loss[1:-1], got["loss"]) and loss[0] == 7 and loss[-1] == 7
+    for k, v in held.items():
+        assert torch.equal(v[1:-1, :-5], got[k]) and (v[0] == 7).all() and (v[-1] == 7).all() and (v[:, -5:] == 7).all(), k
+
+
+def test_derivatives_that_are_refused():
+    x, w, t = make(5, 16, 8, torch.bfloat16)
+    x.requires_grad_()
+    one = torch.ones((), device="cuda", requires_grad=True)
+    (g,) = torch.autograd.grad(tl.linear_cross_entropy(x, w, t), x, one, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+    with torch.autograd.forward_ad.dual_level(), pytest.raises(RuntimeError):
+        tl.linear_cross_entropy(torch.autograd.forward_ad.make_dual(x.detach(), torch.ones_like(x)), w, t)
+
+
+def test_refusals_on_the_gpu():
+    x, w, t = make(5, 16, 8, torch.bfloat16)
+    with pytest.raises(TypeError, match="int64"):
+        tl.linear_cross_entropy(x, w, t.int())
+    with pytest.raises(TypeError, match="w must have"):
+        tl.linear_cross_entropy(x, w.half(), t)
+    for bad in ((x, w[:, :7], t), (x, w[0], t), (x, w, t[:4]), (x, w, t.cpu()), (x, w, t[:, None])):
+        with pytest.raises(ValueError):
+            tl.linear_cross_entropy(*bad)
+    for ignore in (2 ** 63, 0.5):
+        with pytest.raises(ValueError, match="ignore_index"):
+            tl.linear_cross_entropy(x, w, t, ignore_index=ignore)

@@ -141,11 +141,12 @@ __device__ __forceinline__ void activate8(int act, const float (&g)[8], float (&
         case ACT_GELU_TANH:
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // (1 + tanh t) / 2 = 1 / (1 + exp(-2 t))
-                const float g2 = g[e] * g[e];
-                const float s = __builtin_amdgcn_rcpf(1.0f + exp_neg(1.59576912f * g[e] * (1.0f + 0.044715f * g2)));
+                // (1 + tanh t) / 2 = 1 / (1 + exp(-2 t)).  Past 30 it is 0 or 1 and the
+                // powers of g would only overflow
+                const float c = g[e] != g[e] ? g[e] : fminf(fmaxf(g[e], -30.0f), 30.0f), c2 = c * c;
+                const float s = __builtin_amdgcn_rcpf(1.0f + exp_neg(1.59576912f * c * (1.0f + 0.044715f * c2)));
                 a[e] = g[e] * s;
-                if (D) d[e] = s * (1.0f + (1.0f - s) * 1.59576912f * g[e] * (1.0f + 0.134145f * g2));
+                if (D) d[e] = s * (1.0f + (1.0f - s) * 1.59576912f * c * (1.0f + 0.134145f * c2));
             }
             break;
         default:

@@ -32,6 +32,8 @@ struct XentLayout {
     int64_t bytes[3];
 };
 
+static_assert(XENT_PIECE / 64 <= MM_MOST, "row stride of dz");
+
 static int wave_cols(MmSize s) { return s == SIZE_256 ? 128 : 64; }
 
 static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
@@ -56,8 +58,11 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
     l.part = take(1, 8 * M * l.parts);
     if (pack) l.w = take(1, 2 * V * l.ldx);
     if (!keep) return l;
-    // at least 8192 columns: dz is then four times as wide as x often is
-    const int64_t fit = M > 0 ? XENT_PIECE / M : V;
+    const int64_t padded = (M + 63) / 64 * 64;  // rows, the last of them zero
+    // at least 8192 columns: dz is then four times as wide as x often is; at most
+    // 2^22, as XENT_PIECE has them for 64 rows: the products' copies reach 64 rows
+    // by 32-bit offsets
+    const int64_t fit = M > 0 ? XENT_PIECE / padded : V;
     const int64_t most = fit < 8192 ? 8192 : fit;
     const int64_t pieces = V > 0 ? (V + most - 1) / most : 1;
     l.cols = ((V + pieces - 1) / pieces + 255) / 256 * 256;
@@ -66,7 +71,6 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
     const int64_t cols = l.cols < V ? l.cols : V;
     const MmShape dx{M, K}, dw{cols, K};
     l.dz = mm_size(FORM_DZ, M, cols, mm_slices(K), false, pack ? 0 : K);
-    const int64_t padded = (M + 63) / 64 * 64;  // rows, the last of them zero
     l.x2 = take(2, 2 * padded * l.ldx);
     l.coef = take(2, 4 * M);
     l.alpha = take(2, 4);

@@ -1076,6 +1076,10 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None):
             used = [p for p, c in zip(pointers, counts) if c]
             if len(set(used)) != len(used):
                 raise ValueError("a tensor is given twice")
+    if outs is not ins and outs != ins:
+        known = {p for p, c in zip(ins, counts) if c}
+        if any(q != p and q in known for p, q, c in zip(ins, outs, counts) if c):
+            raise ValueError("a tensor of out is another one of grads")
     i64s = ctypes.c_int64 * n
     sizes = i64s(*counts)
     need = _lib.tgemm_clip_workspace_bytes(n, sizes)
