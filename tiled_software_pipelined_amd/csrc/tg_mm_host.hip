@@ -48,6 +48,8 @@ static double tiles_of(const MmKernel& k, const MmShape* shapes, int jobs) {
 //   nt   4096x4096x4096         110    133    172    145
 //   tn   50240x768x64          27.6   22.0   36.0   36.9
 //   gate 100x11008x4096        97.0   63.3   58.4   48.6
+//   gate 256x11008x4096        99.1   78.2   86.2   84.2
+//   nt   256x4096x11008        59.8   51.2   51.7   44.6
 //   gate 2048x5440x2048         106    109    140    124
 //   dh   2048x5440x2048         107     81     92     73
 //   stats 60x50240x768         24.8   20.1   18.9   21.4
@@ -57,9 +59,9 @@ struct MmRate {
 };
 //                                               nt   nn   tn  sum  gate  dh  stats dz
 static const MmRate MM_RATES[SIZE_COUNT] = {
-    {0.99, 1.60, {1.25, 1.6}, {6.3, 6.3, 6.3, 9.0, 9.5, 22.0, 6.5, 9.7}},
+    {0.99, 1.60, {1.40, 1.6}, {6.3, 6.3, 6.3, 9.0, 9.5, 22.0, 6.5, 9.7}},
     {0.60, 1.00, {0.90, 1.2}, {1.5, 1.5, 1.5, 3.0, 4.4, 6.8, 3.0, 4.0}},
-    {0.30, 0.65, {0.46, 0.85}, {3.4, 3.8, 5.0, 5.0, 3.5, 6.9, 3.7, 4.5}},
+    {0.30, 0.70, {0.46, 0.85}, {3.4, 3.8, 5.0, 5.0, 3.5, 6.9, 3.7, 4.5}},
     {0.35, 0.54, {0.65, 0.65}, {3.7, 4.0, 4.4, 5.0, 6.0, 6.9, 3.9, 5.0}},
 };
 
@@ -91,7 +93,7 @@ MmSize mm_size(int form, const MmShape* shapes, int jobs, int64_t slices, bool m
     double least = -1.0;
     const MmKernel* table = mm_kernels(TGEMM_BF16, form);  // the types' tiles are alike
     for (int s = 0; s < SIZE_COUNT; ++s) {
-        const bool cold = shapes[0].M <= 2 * table[s].bm;
+        const bool cold = shapes[0].M <= 256;
         double t = mm_time(form, s, table[s], tiles_of(table[s], shapes, jobs), slices, may_split, cold);
         // across k a chunk's rows are further apart and the cost is less
         const double off = row % 8 == 0 ? 0.0 : (row % 2 ? MM_ODD[s] : MM_EVEN[s]) - 1.0;
