@@ -490,6 +490,16 @@ __device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
     for (int e = 0; e < 8; ++e) o[e] = (T)v[e];  // to nearest even
     __builtin_memcpy(dst, o, 16);
 }
+// The same past the caches.
+template <class T>
+__device__ __forceinline__ void stream8(T* dst, const float (&v)[8]) {
+    T o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = (T)v[e];
+    i32x4 w;
+    __builtin_memcpy(&w, o, 16);
+    __builtin_nontemporal_store(w, reinterpret_cast<i32x4*>(dst));
+}
 // `count` of them, which may be none, inside the row.  The empty statements keep
 // the compiler from making one run of element stores of both branches.
 template <class T>

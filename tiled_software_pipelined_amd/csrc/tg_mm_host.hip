@@ -145,6 +145,7 @@ int mm_store(int dtype, int form, MmSize size, const MmStoreArgs& given, hipStre
         MmJob& j = args.job[args.jobs++];
         j = given.job[i];
         j.grid = mm_grid(k, o.M, o.N);
+        j.stream = (uintptr_t)j.C % 128 == 0 && j.ldc % 64 == 0;
         tiles += (double)j.grid.tiles_m * j.grid.tiles_n;
     }
     if (args.jobs == 0) return TGEMM_OK;

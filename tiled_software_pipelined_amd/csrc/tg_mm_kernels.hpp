@@ -54,6 +54,9 @@ struct MmJob {
     int64_t ldc;
     float* sum;     // not NULL: float sums (M x N) instead
     int32_t add;    // sum: add to what is there
+    // C's rows are whole cache lines: they go past the caches, which keep the
+    // operands (32000x4096x2048 across k 467 -> 444 us)
+    int32_t stream;
 };
 struct MmStoreArgs {
     MmJob job[3];
@@ -309,6 +312,7 @@ __global__ __launch_bounds__(G::NT) void mm_store_kernel(MmStoreArgs g) {
         const float alpha = g.alpha ? *g.alpha : 1.0f;
         T* C = static_cast<T*>(job.C);
         const MmOut<G> out(at, M, N, job.ldc);
+        const bool stream = job.stream != 0;
         struct Row {
             int to;
         };
@@ -320,8 +324,12 @@ __global__ __launch_bounds__(G::NT) void mm_store_kernel(MmStoreArgs g) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] *= alpha;
                 T* dst = C + (int64_t)row.to * out.ld + out.col();
-                if (inside.value) store8(dst, v);
-                else store8(dst, v, out.count(u));
+                if (inside.value) {
+                    if (stream) stream8(dst, v);
+                    else store8(dst, v);
+                } else {
+                    store8(dst, v, out.count(u));
+                }
             });
         };
         if (out.inside()) way(Yes{});
@@ -425,9 +433,12 @@ __global__ __launch_bounds__(G::NT) void mm_gate_kernel(MmGateArgs g) {
             auto put = [&](void* p, F8 x) {
                 if (inside.value || out.count(u) > 0) store8(out.at(static_cast<T*>(p), u), x);
             };
-            if (g.g) {
-                put(g.g, v);
-                put(g.u, w);
+            if (g.g) {  // for the backward pass: past the caches
+                auto keep = [&](void* p, F8 x) {
+                    if (inside.value || out.count(u) > 0) stream8(out.at(static_cast<T*>(p), u), x);
+                };
+                keep(g.g, v);
+                keep(g.u, w);
             }
             float a[8], d[8];
             activate8<false>(g.act, v, a, d);
