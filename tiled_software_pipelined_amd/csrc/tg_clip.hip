@@ -129,9 +129,13 @@ __global__ __launch_bounds__(1024) void clip_norm_kernel(const double* sums, int
     }
 }
 
+// Results go past the caches, which then keep what the squares have read (67
+// million values in float16, read once more for the product: 84.5 us to 68; 1.4
+// billion in bfloat16: 1584 to 1538).
 template <class T>
 __device__ __forceinline__ void piece_times(const T* in, T* out, int64_t begin, int64_t end, float f) {
     constexpr int N = Packed<T>::N, U = 4;
+    typedef int32_t Loose __attribute__((ext_vector_type(4), aligned(2)));  // at any element
     auto times = [&](Packed<T>& x) {
 #pragma unroll
         for (int e = 0; e < N; ++e) x.v[e] = (T)((float)x.v[e] * f);
@@ -144,7 +148,9 @@ __device__ __forceinline__ void piece_times(const T* in, T* out, int64_t begin, 
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             times(x[u]);
-            __builtin_memcpy(out + i + u * CLIP_THREADS * N, &x[u], 16);
+            Loose w;
+            __builtin_memcpy(&w, &x[u], 16);
+            __builtin_nontemporal_store(w, reinterpret_cast<Loose*>(out + i + u * CLIP_THREADS * N));
         }
     }
     for (; i < end; i += CLIP_THREADS * N) {
