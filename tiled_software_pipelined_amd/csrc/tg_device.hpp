@@ -91,10 +91,14 @@ struct ClockMark {
 // finish before each read and serialise the pipeline); completion is tracked
 // explicitly with wait_vm_then_barrier.  M0 is written here: the kernels that
 // use this issue every LDS copy through it and nothing else of theirs uses
-// M0.  On gfx9-family chips a global/buffer load with LDS=1 that follows a
-// scalar write of M0 needs one wait state in between, which the hardware
-// does not insert and the compiler only inserts between instructions it
-// emits itself, so the asm carries its own s_nop 0.
+// M0.  Two waits that the hardware does not make, and that the compiler makes
+// only between instructions it emits itself, are the asm's own.  A
+// global/buffer load with LDS=1 needs one wait state after a scalar write of
+// M0.  A vector memory instruction needs five after a vector instruction
+// (v_readfirstlane below) wrote the scalar pair it takes its address from,
+// while a scalar instruction may read that pair at once.  The scalar copy of
+// the address is both: it stands between M0's write and the load, and the
+// load reads the copy.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy16_to_lds(uint32_t lds, uint32_t voff, const void* base) {
@@ -105,7 +109,10 @@ __device__ __forceinline__ void copy16_to_lds(uint32_t lds, uint32_t voff, const
     const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
     const uint64_t sb = ((uint64_t)hi << 32) | lo;
     const uint32_t sl = __builtin_amdgcn_readfirstlane(lds);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(sl), "v"(voff), "s"(sb)
+    uint64_t at;
+    asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
+                 : "=&s"(at)
+                 : "s"(sl), "v"(voff), "s"(sb)
                  : "m0");
 }
 // The same copy, 4 bytes per lane: lane l's 4 bytes land at lds + 4 l.
@@ -115,7 +122,10 @@ __device__ __forceinline__ void copy4_to_lds(uint32_t lds, uint32_t voff, const 
     const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
     const uint64_t sb = ((uint64_t)hi << 32) | lo;
     const uint32_t sl = __builtin_amdgcn_readfirstlane(lds);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(sl), "v"(voff), "s"(sb)
+    uint64_t at;
+    asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dword %2, %0"
+                 : "=&s"(at)
+                 : "s"(sl), "v"(voff), "s"(sb)
                  : "m0");
 }
 #pragma clang diagnostic pop
