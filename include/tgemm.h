@@ -535,18 +535,25 @@ int tgemm_ffn_backward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype
  *
  * c the row's share of dloss.  It makes z again, a piece of the vocabulary at a
  * time, and rounds dz to `dtype`, scaled by a power of two to at most 2^15; dx is
- * summed in float over the pieces and rounded once.  keep: TGEMM_KEEP_X (dx) and
- * TGEMM_KEEP_W (dw).  tgemm_xent_bytes fills bytes[0 .. 2] with the sizes of
- * `saved`, forward's `scratch` (both for any keep) and backward's: device memory,
- * 256-byte aligned; a scratch's contents are overwritten.  Sizes of zero are the
- * empty sums they make.  Each returns TGEMM_OK or a TGEMM_E_* code. */
+ * summed in float over the pieces and rounded once.
+ *
+ * keep: TGEMM_KEEP_X (dx), TGEMM_KEEP_W (dw) and TGEMM_KEEP_POWERS, of which
+ * forward looks at the last alone; it must be the same in all calls.  With it (V up
+ * to 2^28) forward leaves 2^15 exp(z - max) of every logit, max a maximum of part of
+ * its row, rounded to `dtype`, in `saved`, about 2 V bytes a row, and backward
+ * takes p from there (the target's from its logit, in float).  tgemm_xent_bytes
+ * fills bytes[0 .. 2] with the sizes of `saved`, forward's `scratch` (whatever
+ * TGEMM_KEEP_X and _W) and backward's: device memory, 256-byte aligned; a scratch's
+ * contents are overwritten.  Sizes of zero are the empty sums they make.  Each
+ * returns TGEMM_OK or a TGEMM_E_* code. */
 #define TGEMM_NONE 0
 #define TGEMM_SUM 1
 #define TGEMM_MEAN 2
+#define TGEMM_KEEP_POWERS 8
 int tgemm_xent_bytes(int64_t M, int64_t V, int64_t K, int32_t keep, int64_t* bytes);
 int tgemm_xent_forward(int64_t M, int64_t V, int64_t K, int32_t dtype, const void* x, int64_t ldx, const void* w,
-                       int64_t ldw, const int64_t* target, int64_t ignore, int32_t reduction, float* loss, void* saved,
-                       void* scratch, void* stream);
+                       int64_t ldw, const int64_t* target, int64_t ignore, int32_t reduction, int32_t keep, float* loss,
+                       void* saved, void* scratch, void* stream);
 int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const void* x, int64_t ldx, const void* w,
                         int64_t ldw, const int64_t* target, int32_t reduction, const float* dloss, const void* saved,
                         int32_t keep, void* dx, int64_t lddx, void* dw, int64_t lddw, void* scratch, void* stream);

@@ -80,8 +80,9 @@ def ffn(x, wg, wu, wd, name, dy=None):
     return out
 
 
-def xent(x, w, target, ignore=-100, reduction="mean", dloss=None):
-    """{output: (value, bound)}; dloss: one number, or one for each row."""
+def xent(x, w, target, ignore=-100, reduction="mean", dloss=None, kept=None):
+    """{output: (value, bound)}; dloss: one number, or one for each row; kept: whether the powers are kept for
+    the backward pass (None: as the library does by itself)."""
     t = x.dtype
     u, tiny = U[t], TINY[t]
     x, w = x.double(), w.double()
@@ -113,6 +114,10 @@ def xent(x, w, target, ignore=-100, reduction="mean", dloss=None):
     # dz is rounded after its scale brought the largest factor to 2^14 or more; a
     # probability below float's normal numbers (2^-126) may be taken as zero
     edz = edz + tiny * 2.0 ** -14 * coef.abs().max() + 2.0 ** -126 * coef.abs()
+    if kept if kept is not None else K >= 512:
+        # p comes as exp(max - lse) times the kept exp(z - max), 2^15 times as much of which was rounded: half a step
+        # more, relative or of the type's least (the exponents add up to z - lse's); the target's p is made in float
+        edz = edz + (1 - torch.zeros_like(p).scatter_(1, at, 1.0)) * coef.abs() * (p * (u + 16 * F32) + tiny * 2.0 ** -15)
     out["dx"] = product(dz, w, edz, u, tiny)
     out["dw"] = product(dz.t(), x, edz.t(), u, tiny)
     return out

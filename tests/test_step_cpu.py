@@ -65,8 +65,8 @@ def test_ffn_of_no_rows_needs_no_device(kw):
     assert fwd(**kw, x=None, y=None, keep=0, saved=None) == 0 and tl.last_error() == ""
 
 
-def xf(M=4, V=32, K=8, dtype=1, x=A, ldx=None, w=A, ldw=None, target=A, ignore=-100, reduction=2, loss=A, saved=A, scratch=A):
-    return tl._lib.tgemm_xent_forward(M, V, K, dtype, x, d(ldx, K), w, d(ldw, K), target, ignore, reduction, loss, saved, scratch,
+def xf(M=4, V=32, K=8, dtype=1, x=A, ldx=None, w=A, ldw=None, target=A, ignore=-100, reduction=2, keep=0, loss=A, saved=A, scratch=A):
+    return tl._lib.tgemm_xent_forward(M, V, K, dtype, x, d(ldx, K), w, d(ldw, K), target, ignore, reduction, keep, loss, saved, scratch,
                                       None)
 
 
@@ -83,7 +83,8 @@ XCOMMON = [
     (dict(saved=P(8)), -3), (dict(scratch=None), -2), (dict(scratch=P(8)), -3)]
 
 
-@pytest.mark.parametrize("kw,code", XCOMMON + [(dict(loss=None), -2), (dict(loss=P(2)), -3)])
+@pytest.mark.parametrize("kw,code", XCOMMON + [
+    (dict(loss=None), -2), (dict(loss=P(2)), -3), (dict(keep=4), -1), (dict(keep=8, V=2 ** 28 + 1), -1)])
 def test_xent_forward_refuses(kw, code):
     assert xf(**kw) == code and tl.last_error()
 
@@ -106,6 +107,9 @@ def test_xent_sizes():
         assert n[2] <= max(2 ** 29 * rows // max(M, 1), 2 ** 14 * rows) + 512 * rows + 2 * rows * (K + 64) + 4 * M * K + 2 ** 26 + 2 ** 20
     one = n[0], n[1]
     assert tl._lib.tgemm_xent_bytes(7, 9, 0, 0, n) == 0 and (n[0], n[1], n[2]) == (*one, 0)
+    # kept powers: rows of whole lines, 16 bits each, and what the loss's rows were joined from
+    assert tl._lib.tgemm_xent_bytes(100, 1000, 64, 8 + 3, n) == 0 and 2 * 100 * 1024 < n[0] < 2 * 100 * 1024 + 2 ** 15
+    assert tl._lib.tgemm_xent_bytes(4, 2 ** 28 + 1, 16, 8, n) == -1 and tl._lib.tgemm_xent_bytes(0, 9, 8, 11, n) == 0
 
 
 def clip(tensors=2, counts=(5, 7), dtypes=(0, 1), ins=(64, 128), outs=(64, 128), max_norm=1.0, eps=1e-6, norm=A, ws=A, size=1 << 20):

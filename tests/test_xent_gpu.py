@@ -20,9 +20,9 @@ def make(M, V, K, dtype, seed=0, ignored=0.25, scale=1.0):
     return x, w, torch.where(gone, -100, target)
 
 
-def run(x, w, target, dloss=1.0, reduction="mean", ignore=-100):
+def run(x, w, target, dloss=1.0, reduction="mean", ignore=-100, **kw):
     x, w = x.detach().requires_grad_(), w.detach().requires_grad_()
-    loss = tl.linear_cross_entropy(x, w, target, ignore, reduction)
+    loss = tl.linear_cross_entropy(x, w, target, ignore, reduction, **kw)
     g = torch.as_tensor(dloss, dtype=torch.float32, device=x.device).expand(loss.shape)
     dx, dw = torch.autograd.grad(loss, (x, w), g)
     return {"loss": loss.detach(), "dx": dx, "dw": dw}
@@ -228,6 +228,111 @@ def test_several_pieces_of_the_vocabulary(dtype):
     assert torch.equal(run(x, w, t)["dx"], got["dx"])
 
 
+@pytest.fixture
+def powers(monkeypatch):
+    """The powers are kept whatever K is."""
+    monkeypatch.setattr(tl, "POWERS_LEAST", 0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,V,K", [
+    (1, 1, 1), (1, 2, 3), (2, 7, 5), (1, 1000, 64), (5, 129, 16), (64, 128, 64), (65, 127, 66), (33, 1000, 100), (130, 513, 200),
+    (2050, 4100, 40), (3, 50257, 24), (4100, 5, 9), (17, 2049, 8), (1030, 6001, 264)])
+def test_kept_powers(M, V, K, dtype, powers):
+    x, w, t = make(M, V, K, dtype)
+    got = run(x, w, t, 3.0)
+    ref.check(got, ref.xent(x, w, t, dloss=3.0, kept=True))
+    assert torch.equal(run(x, w, t, 3.0, keep_bytes=0)["loss"], got["loss"])
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-3, 30.0, 300.0])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_kept_powers_of_flat_and_peaked_rows(scale, dtype, powers):
+    x, w, t = make(140, 600, 128, dtype, scale=scale)
+    for reduction, dloss in (("mean", 1024.0), ("none", torch.linspace(-1, 2, 140, device="cuda"))):
+        ref.check(run(x, w, t, dloss, reduction), ref.xent(x, w, t, reduction=reduction, dloss=dloss, kept=True))
+
+
+def test_kept_powers_of_likely_targets(powers):
+    """p - 1 of a target that is nearly certain is not lost to the powers' rounding."""
+    x, w, t = make(100, 300, 64, torch.bfloat16, ignored=0.0)
+    w[:, 0], x[:, 0] = -4.0, 2.0
+    w[5, 0], t[:] = 4.0, 5  # 16 above the others
+    want = ref.xent(x, w, t, reduction="sum", dloss=1.0, kept=True)
+    got = run(x, w, t, reduction="sum")
+    ref.check(got, want)
+    p = torch.softmax(x.double() @ w.double().t(), 1)[:, 5]
+    assert p.min() > 0.99 and (1 - p).median() < 2.0 ** -9
+    row = got["dw"][5].double()  # the sum of (p - 1) x: dz's and dw's roundings are 2^-8 of each value
+    assert (row - want["dw"][0][5]).norm() < 2.0 ** -8 * 2 * ((1 - p)[:, None] * x.double().abs()).sum(0).norm()
+
+
+def test_kept_powers_in_pieces(powers):
+    """More logits than one piece of dz holds; a saved state above 2^31 bytes."""
+    M, V, K = 33000, 33001, 24
+    x, w, t = make(M, V, K, torch.bfloat16)
+    assert tl._xent_bytes(M, V, K, 11)[0] > 2 ** 31 and tl._xent_bytes(M, V, K, 11)[2] < 2 ** 30
+    got = run(x, w, t)
+    some = torch.arange(0, M, 97, device="cuda")
+    by = 1.0 / int((t != -100).sum())
+    ref.check({"dx": got["dx"][some]}, ref.xent(x[some], w, t[some], reduction="sum", dloss=by, kept=True), ("dx",))
+    dw, bound = 0.0, 0.0  # added up over blocks of rows
+    for rows in torch.arange(M, device="cuda").split(4096):
+        v, b = ref.xent(x[rows], w, t[rows], reduction="sum", dloss=by, kept=True)["dw"]
+        dw, bound = dw + v, bound + b
+    assert ((got["dw"].double() - dw).abs() <= bound + ref.U[torch.bfloat16] * dw.abs()).all()
+
+
+@pytest.mark.parametrize("bad", [-1, 500, 2 ** 33])
+def test_kept_powers_of_rows_without_a_number(bad, powers):
+    x, w, t = make(100, 500, 64, torch.bfloat16, ignored=0.1)
+    t[10:13] = torch.tensor([bad, 3, 4], device="cuda")
+    x[11, 0], x[12, 0] = float("nan"), float("inf")
+    x[t == -100] = float("nan")
+    got, rest = run(x, w, t, 1.0, "none"), [i for i in range(100) if i not in (10, 11, 12)]
+    assert got["loss"][10].isnan() and got["dx"][10:13].isnan().all() and got["dw"].isnan().all()
+    assert got["loss"][rest].isfinite().all() and not got["dx"][t == -100].any()
+    keep = [i for i in rest if int(t[i]) != -100]
+    want = ref.xent(x[keep], w, t[keep], reduction="none", dloss=1.0, kept=True)
+    ref.check({"dx": got["dx"][keep]}, want, ("dx",))
+
+
+@pytest.mark.parametrize("M,V", [(0, 10), (5, 0), (0, 0)])
+def test_kept_powers_of_empty_sizes(M, V, powers):
+    x, w, t = make(M, V, 16, torch.bfloat16)
+    t[:] = -100
+    got = run(x, w, t, reduction="sum")
+    assert got["loss"] == 0 and not got["dx"].any() and not got["dw"].any()
+
+
+def test_kept_powers_serve_a_graph_twice(powers):
+    """The backward pass only reads them; single gradients are the same bits."""
+    x, w, t = make(120, 700, 96, torch.bfloat16)
+    want = run(x, w, t)
+    x, w = x.requires_grad_(), w.requires_grad_()
+    loss = tl.linear_cross_entropy(x, w, t)
+    for inputs, names in (((x, w), ("dx", "dw")), ((x,), ("dx",)), ((w,), ("dw",)), ((x, w), ("dx", "dw"))):
+        for g, name in zip(torch.autograd.grad(loss, inputs, retain_graph=True), names):
+            assert torch.equal(g, want[name])
+
+
+def test_kept_powers_captured_and_replayed(powers):
+    test_captured_and_replayed()
+
+
+def test_bytes_that_may_be_kept():
+    x, w, t = make(64, 1000, 512, torch.bfloat16)
+    bits = {}
+    for keep in (0, 2 * 64 * 1024 - 1, 2 * 64 * 1024, float("inf")):
+        x.requires_grad_()
+        loss = tl.linear_cross_entropy(x, w, t, keep_bytes=keep)
+        bits[keep] = loss.grad_fn.saved_tensors[3].numel()
+    a, b, c, d = bits.values()
+    assert a == b and c == d and c >= a + 2 * 64 * 1024
+    with torch.no_grad():
+        assert torch.equal(tl.linear_cross_entropy(x, w, t), loss)
+
+
 def test_captured_and_replayed():
     x, w, t = make(100, 1000, 64, torch.bfloat16)
     x, w = x.requires_grad_(), w.requires_grad_()
@@ -279,7 +384,7 @@ def test_no_write_outside_the_outputs():
     loss, dloss = torch.full((M + 2,), 7.0, device="cuda"), torch.ones(M, device="cuda")
     saved, s1, s2 = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in tl._xent_bytes(M, V, K, 3))
     at = lambda k: (held[k][1:].data_ptr(), K + 5)  # noqa: E731
-    tl._call(x.device, tl._lib.tgemm_xent_forward, M, V, K, tl.BF16, x.data_ptr(), K, w.data_ptr(), K, t.data_ptr(), -100, 0,
+    tl._call(x.device, tl._lib.tgemm_xent_forward, M, V, K, tl.BF16, x.data_ptr(), K, w.data_ptr(), K, t.data_ptr(), -100, 0, 0,
              loss[1:].data_ptr(), saved.data_ptr(), s1.data_ptr())
     tl._call(x.device, tl._lib.tgemm_xent_backward, M, V, K, tl.BF16, x.data_ptr(), K, w.data_ptr(), K, t.data_ptr(), 0,
              dloss.data_ptr(), saved.data_ptr(), 3, *at("dx"), *at("dw"), s2.data_ptr())
@@ -309,6 +414,9 @@ def test_refusals_on_the_gpu():
     for bad in ((x, w[:, :7], t), (x, w[0], t), (x, w, t[:4]), (x, w, t.cpu()), (x, w, t[:, None])):
         with pytest.raises(ValueError):
             tl.linear_cross_entropy(*bad)
+    for keep in (-1, float("nan")):
+        with pytest.raises(ValueError, match="keep_bytes"):
+            tl.linear_cross_entropy(x, w, t, keep_bytes=keep)
     for ignore in (2 ** 63, 0.5):
         with pytest.raises(ValueError, match="ignore_index"):
             tl.linear_cross_entropy(x, w, t, ignore_index=ignore)

@@ -1,0 +1,14 @@
+#include "tg_mm_kernels.hpp"
+
+namespace tg {
+typedef MmTiles<MmBf16, ALONG, ALONG, false> Tiles;
+const MmKernel* mm_stats_keep_bf16() {
+    static const MmKernel table[SIZE_COUNT] = {
+        mm_entry<Tiles::T256>(reinterpret_cast<const void*>(mm_stats_kernel<Tiles::T256, true>)),
+        mm_entry<Tiles::T128>(reinterpret_cast<const void*>(mm_stats_kernel<Tiles::T128, true>)),
+        mm_entry<Tiles::T64>(reinterpret_cast<const void*>(mm_stats_kernel<Tiles::T64, true>)),
+        mm_entry<Tiles::T128Deep>(reinterpret_cast<const void*>(mm_stats_kernel<Tiles::T128Deep, true>)),
+    };
+    return table;
+}
+}  // namespace tg

@@ -8,7 +8,8 @@
 namespace tg {
 
 #define TG_MM_TABLES(t)                                                                                         \
-    const MmKernel *mm_nt_##t(), *mm_nn_##t(), *mm_tn_##t(), *mm_nn_sum_##t(), *mm_gate_##t(), *mm_dh_##t(), *mm_stats_##t(), *mm_dz_##t(); \
+    const MmKernel *mm_nt_##t(), *mm_nn_##t(), *mm_tn_##t(), *mm_nn_sum_##t(), *mm_gate_##t(), *mm_dh_##t(), *mm_stats_##t(), *mm_dz_##t(), \
+        *mm_stats_keep_##t();                                                                                   \
     static const MmKernel* mm_kernels_##t(int form) {                                                           \
         switch (form) {                                                                                         \
             case FORM_NT: return mm_nt_##t();                                                                   \
@@ -18,6 +19,7 @@ namespace tg {
             case FORM_GATE: return mm_gate_##t();                                                               \
             case FORM_DH: return mm_dh_##t();                                                                   \
             case FORM_STATS: return mm_stats_##t();                                                             \
+            case FORM_STATS_KEEP: return mm_stats_keep_##t();                                                   \
             default: return mm_dz_##t();                                                                        \
         }                                                                                                       \
     }

@@ -101,7 +101,11 @@ struct MmStatsArgs {
     const int64_t* target;
     float2* part;  // (max, sum of 2^((z - max) log2 e)) of each wave's columns: part[piece M + row]
     float* hit;    // the target's logit of a row, where it has one
+    void* powers;  // KEEP: POWER 2^((z - max) log2 e) of every logit, rounded, M x N
+    int64_t ldp;   // their row stride; anything may be written between
 };
+// Powers are at most one.  float16 holds 11 bits of them down to 2^-14 / POWER.
+constexpr float POWER = 32768.0f;
 struct MmDzArgs {
     MmOperands op;   // b: rows v0 .. of W
     MmGrid grid;
@@ -519,7 +523,8 @@ struct MmKnown {
 
 // The piece of the softmax that a wave's columns make: for each row their
 // maximum and the sum of the powers above it.  A row is in lanes l and l + 32.
-template <class G>
+// KEEP: the powers are stored too, for a backward pass that then needs no logits.
+template <class G, bool KEEP>
 __global__ __launch_bounds__(G::NT) void mm_stats_kernel(MmStatsArgs g) {
     __shared__ __attribute__((aligned(1024))) char smem_raw[G::LDS_BYTES];
     const MmKnown<G> known(g.op, g.grid, g.rows);
@@ -527,7 +532,8 @@ __global__ __launch_bounds__(G::NT) void mm_stats_kernel(MmStatsArgs g) {
     const MmPlace<G> at(known.grid, xcd_rank(blockIdx.x, known.total));
     typename G::Acc acc;
     G::clear(acc);
-    G::product(known.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, (TG_LDS char*)smem_raw, acc, at.wm0, at.wn0, at.lane, at.wave);
+    TG_LDS char* smem = (TG_LDS char*)smem_raw;
+    G::product(known.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, smem, acc, at.wm0, at.wn0, at.lane, at.wave);
     const int M = known.op.M, N = g.op.N, n1 = at.col0(), half = 4 * (at.lane >> 5);
     if (n1 >= N) return;                // wave-uniform, as is the next
     const bool edge = n1 + G::WTN > N;
@@ -549,13 +555,6 @@ __global__ __launch_bounds__(G::NT) void mm_stats_kernel(MmStatsArgs g) {
             for (int r = 0; r < 16; ++r) most = fmaxf(most, acc[i][j][r]);
         most = fmaxf(most, __shfl_xor(most, 32));
         const float base = most == -INFINITY ? 0.0f : most;  // nothing here, or nothing but -inf
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < G::FN; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f((acc[i][j][r] - base) * LOG2E);
-        sum += __shfl_xor(sum, 32);
-        if (at.lane < 32 && m < M) part[m] = float2{most, sum};
         const int64_t t = (m < M ? g.target[g.map[m]] : -1) - n1;
         const int want = t >= 0 && t < G::WTN ? (int)t : -1;
         if (__any(want >= 0)) {
@@ -565,6 +564,31 @@ __global__ __launch_bounds__(G::NT) void mm_stats_kernel(MmStatsArgs g) {
                 for (int r = 0; r < 16; ++r)
                     if (32 * j + 8 * (r >> 2) + half + (r & 3) == want) g.hit[m] = acc[i][j][r];
         }
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float power = __builtin_amdgcn_exp2f((acc[i][j][r] - base) * LOG2E);
+                sum += power;
+                if constexpr (KEEP) acc[i][j][r] = power;
+            }
+        sum += __shfl_xor(sum, 32);
+        if (at.lane < 32 && m < M) part[m] = float2{most, sum};
+    }
+    if constexpr (KEEP) {
+        typedef typename G::T T;
+        T* to = static_cast<T*>(g.powers);
+        const MmOut<G> out(at, M, (int)g.ldp, g.ldp);  // rows whole up to their stride
+        auto way = [&](auto inside) {
+            G::each_row(acc, smem, at.lane, at.wave, [&](int u, float (&v)[8], float (&)[8]) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= POWER;
+                if (inside.value || out.count(u) > 0) store8(out.at(to, u), v);
+            });
+        };
+        if (out.inside()) way(Yes{});
+        else way(No{});
     }
 }
 
@@ -715,7 +739,7 @@ __global__ __launch_bounds__(512) void mm_rows_kernel(MmRowsArgs g) {
 }
 
 // ---- the table ---------------------------------------------------------------
-enum MmForm { FORM_NT = 0, FORM_NN, FORM_TN, FORM_NN_SUM, FORM_GATE, FORM_DH, FORM_STATS, FORM_DZ, FORM_COUNT };
+enum MmForm { FORM_NT = 0, FORM_NN, FORM_TN, FORM_NN_SUM, FORM_GATE, FORM_DH, FORM_STATS, FORM_DZ, FORM_COUNT, FORM_STATS_KEEP /* sized as FORM_STATS */ };
 enum MmSize { SIZE_256 = 0, SIZE_128, SIZE_64, SIZE_128_DEEP, SIZE_COUNT };
 struct MmKernel {
     const void *fn, *join;

@@ -10,6 +10,10 @@
 // row's sum, and the row's loss.  Backward: pieces of the vocabulary, for each the
 // product again, ended by dz = coef (exp(z - lse) - [target]), and the two
 // products that take it, dx += dz W and dW = dz^T x.
+//
+// With TGEMM_KEEP_POWERS the forward pass also stores each power, rounded to 16
+// bits (2 V bytes a row that counts), and dz is a pass over them: 6 M V K
+// operations for the step, not 8.
 #include <climits>
 
 #include "tg_mm_host.hpp"
@@ -26,6 +30,7 @@ struct XentLayout {
     int64_t ldx;               // row stride of the gathered rows of x
     int64_t cols, ldz;         // backward: columns of a piece, row stride of dz
     int64_t count, map, rank, lse;                  // kept
+    int64_t powers, ldp;                            // kept as well, or -1; then so are hit and part
     int64_t x, hit, each, part, w;                  // forward's scratch; w: on lines, -1: read where it is
     int64_t x2, coef, alpha, dzs, sum, split, w2;   // backward's
     int64_t split_bytes[2];                         // of dx's and dw's launches, which use the same room
@@ -33,6 +38,8 @@ struct XentLayout {
 };
 
 static_assert(XENT_PIECE / 64 <= MM_MOST, "row stride of dz");
+// A row of powers: a lane's place in eight rows is a 32-bit offset.
+constexpr int64_t MOST_POWERS = INT64_C(1) << 28;
 
 static int wave_cols(MmSize s) { return s == SIZE_256 ? 128 : 64; }
 
@@ -52,12 +59,15 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
     l.w = l.w2 = -1;
     l.stats = mm_size(FORM_STATS, M, V, mm_slices(K), false, pack ? 0 : K);
     l.parts = (V + wave_cols(l.stats) - 1) / wave_cols(l.stats);
+    const bool powers = keep & TGEMM_KEEP_POWERS;
     l.x = take(1, 2 * M * l.ldx);
-    l.hit = take(1, 4 * M);   // the target's logit of each of them
-    l.each = take(1, 4 * M);  // each row's loss
-    l.part = take(1, 8 * M * l.parts);
+    l.hit = take(!powers, 4 * M);  // the target's logit of each of them
+    l.each = take(1, 4 * M);       // each row's loss
+    l.part = take(!powers, 8 * M * l.parts);
     if (pack) l.w = take(1, 2 * V * l.ldx);
-    if (!keep) return l;
+    l.ldp = mm_lines(V);
+    l.powers = powers ? take(0, 2 * M * l.ldp) : -1;
+    if (!(keep & (TGEMM_KEEP_X | TGEMM_KEEP_W))) return l;
     const int64_t padded = (M + 63) / 64 * 64;  // rows, the last of them zero
     // at least 8192 columns: dz is then four times as wide as x often is; at most
     // 2^22, as XENT_PIECE has them for 64 rows: the products' copies reach 64 rows
@@ -91,7 +101,8 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
 }
 
 static bool xent_sizes_ok(int64_t M, int64_t V, int64_t K, int32_t keep) {
-    if (M < 0 || V < 0 || K < 0 || M > MM_MOST_ROWS || V > MM_MOST_ROWS || K > MM_MOST || (keep & ~3)) {
+    if (M < 0 || V < 0 || K < 0 || M > MM_MOST_ROWS || V > MM_MOST_ROWS || K > MM_MOST ||
+        (keep & ~(TGEMM_KEEP_X | TGEMM_KEEP_W | TGEMM_KEEP_POWERS)) || ((keep & TGEMM_KEEP_POWERS) && V > MOST_POWERS)) {
         set_error("M=%lld V=%lld K=%lld keep=%d out of range", (long long)M, (long long)V, (long long)K, keep);
         return false;
     }
@@ -367,6 +378,61 @@ __global__ __launch_bounds__(1024) void xent_prepare_kernel(CoefArgs c, GatherAr
     }
 }
 
+struct PowersArgs {
+    int32_t V, n, wide, chunks;  // columns of this piece; columns that share a maximum; workgroups of a row
+    int64_t M, v0, ldp, ldz;
+    const int32_t *count, *map;
+    const int64_t* target;
+    const float2* part;
+    const float *hit, *lse, *coef;
+    const void* powers;
+    void* dz;
+};
+
+// dz of a piece of the vocabulary from the kept powers: one pass over them.  A
+// workgroup takes 16 rows and 16 maxima's columns (1024 or 2048): a thread makes
+// the factor coef 2^((max - lse) log2 e) of one row and maximum, then each wave
+// walks four rows.  The target's element is coef (exp(z - lse) - 1) from its logit
+// in float: near one, a rounded power would leave nothing of the difference.
+// Zero in the rows up to the next multiple of 64.
+template <class T>
+__global__ __launch_bounds__(256) void xent_powers_kernel(PowersArgs g) {
+    __shared__ float held[16][17];
+    __shared__ float one[16];
+    __shared__ int64_t aim[16];
+    const int M = *g.count, group = (int)blockIdx.x / g.chunks, m0 = 16 * group, c0 = 16 * g.wide * ((int)blockIdx.x - group * g.chunks);
+    if (m0 >= (M + 63) / 64 * 64) return;
+    {
+        const int r = threadIdx.x & 15, p = threadIdx.x >> 4, m = m0 + r;
+        const int64_t v = g.v0 + c0 + p * g.wide;
+        float f = 0.0f;
+        if (m < M && v < g.V) f = g.coef[m] * __builtin_amdgcn_exp2f((g.part[v / g.wide * g.M + m].x - g.lse[m]) * LOG2E);
+        held[r][p] = f;
+        if (p == 0) {
+            aim[r] = m < M ? g.target[g.map[m]] - g.v0 : -1;
+            one[r] = aim[r] >= 0 && aim[r] < g.n ? g.coef[m] * (__builtin_amdgcn_exp2f((g.hit[m] - g.lse[m]) * LOG2E) - 1.0f) : 0.0f;
+        }
+    }
+    __syncthreads();
+    const int c1 = min(c0 + 16 * g.wide, (int)g.ldz);
+    for (int r = wave_id(); r < 16; r += 4) {
+        const T* from = static_cast<const T*>(g.powers) + (int64_t)(m0 + r) * g.ldp + g.v0;
+        T* to = static_cast<T*>(g.dz) + (int64_t)(m0 + r) * g.ldz;
+        const bool zero = m0 + r >= M;
+        for (int c = c0 + 8 * lane_id(); c < c1; c += 512) {
+            Raw8 raw{};
+            if (!zero && g.v0 + c < g.ldp) load8(raw, from + c);
+            float v[8];
+            values8<T>(v, raw);
+            const float f = zero ? 0.0f : held[r][(c - c0) / g.wide];
+            const int64_t t = aim[r] - c;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = zero ? 0.0f : e == t ? one[r] : v[e] * (1.0f / POWER) * f;
+            store8(to + c, v);
+        }
+    }
+}
+
 }  // namespace tg
 
 extern "C" {
@@ -385,11 +451,11 @@ int tgemm_xent_bytes(int64_t M, int64_t V, int64_t K, int32_t keep, int64_t* byt
 }
 
 int tgemm_xent_forward(int64_t M, int64_t V, int64_t K, int32_t dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
-                       const int64_t* target, int64_t ignore, int32_t reduction, float* loss, void* saved, void* scratch,
-                       void* stream) {
+                       const int64_t* target, int64_t ignore, int32_t reduction, int32_t keep, float* loss, void* saved,
+                       void* scratch, void* stream) {
     using namespace tg;
-    if (!xent_sizes_ok(M, V, K, 0)) return TGEMM_E_ARG;
-    const XentLayout l = xent_layout(M, V, K, 0);
+    if (!xent_sizes_ok(M, V, K, keep)) return TGEMM_E_ARG;
+    const XentLayout l = xent_layout(M, V, K, keep & TGEMM_KEEP_POWERS);
     int rc = xent_common(dtype, reduction, target, M);
     if (rc == TGEMM_OK) rc = mm_check("x", x, M, K, ldx);
     if (rc == TGEMM_OK) rc = mm_check("w", w, V, K, ldw);
@@ -402,8 +468,9 @@ int tgemm_xent_forward(int64_t M, int64_t V, int64_t K, int32_t dtype, const voi
     char *v = static_cast<char*>(saved), *s = static_cast<char*>(scratch);
     int32_t *count = reinterpret_cast<int32_t*>(v + l.count), *map = reinterpret_cast<int32_t*>(v + l.map),
             *rank = reinterpret_cast<int32_t*>(v + l.rank);
-    float *hit = reinterpret_cast<float*>(s + l.hit), *lse = reinterpret_cast<float*>(v + l.lse);
-    float2* part = reinterpret_cast<float2*>(s + l.part);
+    char* where = l.powers >= 0 ? v : s;
+    float *hit = reinterpret_cast<float*>(where + l.hit), *lse = reinterpret_cast<float*>(v + l.lse);
+    float2* part = reinterpret_cast<float2*>(where + l.part);
     float* each = reduction == TGEMM_NONE ? loss : reinterpret_cast<float*>(s + l.each);
     ScanArgs c{M, ignore, target, count, map, rank};
     GatherArgs into{M, K, ldx, l.ldx, 0, static_cast<const uint16_t*>(x), reinterpret_cast<uint16_t*>(s + l.x),
@@ -423,10 +490,10 @@ int tgemm_xent_forward(int64_t M, int64_t V, int64_t K, int32_t dtype, const voi
         ldw = l.ldx;
     }
     if (rc == TGEMM_OK && M > 0 && V > 0) {
-        const MmKernel& k = mm_kernels(dtype, FORM_STATS)[l.stats];
+        const MmKernel& k = mm_kernels(dtype, l.powers >= 0 ? FORM_STATS_KEEP : FORM_STATS)[l.stats];
         MmStatsArgs a{MmOperands{s + l.x, static_cast<const char*>(w), nullptr, 2 * l.ldx, 2 * ldw, 0, (int32_t)M, (int32_t)V,
                                  (int32_t)K},
-                      mm_grid(k, M, V), count, map, target, part, hit};
+                      mm_grid(k, M, V), count, map, target, part, hit, l.powers >= 0 ? v + l.powers : nullptr, l.ldp};
         rc = mm_launch(k.fn, (int64_t)a.grid.tiles_m * a.grid.tiles_n, k.threads, &a, "logits", st);
     }
     if (rc == TGEMM_OK && M > 0) {
@@ -456,9 +523,9 @@ int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const vo
     if (rc == TGEMM_OK) rc = check_floats("dloss", dloss, reduction == TGEMM_NONE ? M : 1);
     if (rc == TGEMM_OK) rc = mm_check_buffer("saved", saved, l.bytes[0]);
     if (rc == TGEMM_OK) rc = mm_check_buffer("scratch", scratch, l.bytes[2]);
-    if (rc == TGEMM_OK && keep && (M > 0 || V > 0)) rc = current_device_ok();
+    if (rc == TGEMM_OK && (kx || kw) && (M > 0 || V > 0)) rc = current_device_ok();
     if (rc != TGEMM_OK) return rc;
-    if (!keep) {
+    if (!kx && !kw) {
         clear_error();
         return TGEMM_OK;
     }
@@ -487,13 +554,22 @@ int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const vo
         const int64_t n = V - v0 < l.cols ? V - v0 : l.cols;
         const char* wv = wp + v0 * ldw * 2;
         int64_t ldv = ldw;
-        if (M > 0 && l.w2 >= 0 && !mm_aligned(wv, ldw)) {
+        if (M > 0 && l.w2 >= 0 && (kx || l.powers < 0) && !mm_aligned(wv, ldw)) {
             const MmPack p{wv, ldw, n, K, s + l.w2};
             rc = mm_pack(&p, 1, st);
             wv = s + l.w2;
             ldv = l.ldx;
         }
-        if (rc == TGEMM_OK && M > 0 && n > 0) {
+        if (rc == TGEMM_OK && M > 0 && n > 0 && l.powers >= 0) {
+            const int wide = wave_cols(l.stats);
+            const int64_t chunks = (l.ldz + 16 * wide - 1) / (16 * wide);
+            PowersArgs a{(int32_t)V, (int32_t)n, wide, (int32_t)chunks, M, v0, l.ldp, l.ldz, count, map, target,
+                         reinterpret_cast<const float2*>(v + l.part), reinterpret_cast<const float*>(v + l.hit),
+                         reinterpret_cast<const float*>(v + l.lse), coef, v + l.powers, s + l.dzs};
+            const void* fn = dtype == TGEMM_BF16 ? reinterpret_cast<const void*>(xent_powers_kernel<__bf16>)
+                                                 : reinterpret_cast<const void*>(xent_powers_kernel<_Float16>);
+            rc = mm_launch(fn, chunks * ((M + 63) / 64 * 4), 256, &a, "gradient of the logits", st);
+        } else if (rc == TGEMM_OK && M > 0 && n > 0) {
             const MmKernel& k = mm_kernels(dtype, FORM_DZ)[l.dz];
             MmDzArgs a{MmOperands{s + l.x2, wv, nullptr, 2 * l.ldx, 2 * ldv, 0, (int32_t)M, (int32_t)n, (int32_t)K},
                        mm_grid(k, M, n), count, map, target, v0, reinterpret_cast<const float*>(v + l.lse), coef, s + l.dzs,

@@ -148,7 +148,7 @@ def _load():
     lib.tgemm_ffn_backward.restype = ctypes.c_int
     lib.tgemm_xent_bytes.argtypes = [i64, i64, i64, i32, ctypes.POINTER(i64)]
     lib.tgemm_xent_bytes.restype = ctypes.c_int
-    lib.tgemm_xent_forward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, i32, vp, vp, vp, vp]
+    lib.tgemm_xent_forward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, i32, i32, vp, vp, vp, vp]
     lib.tgemm_xent_forward.restype = ctypes.c_int
     lib.tgemm_xent_backward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i32, vp, vp, i32, vp, i64, vp, i64, vp, vp]
     lib.tgemm_xent_backward.restype = ctypes.c_int
@@ -459,7 +459,7 @@ from torch.autograd import forward_ad  # noqa: E402
 FP8_BLOCK = 128  # elements of a row that share a scale
 E4M3, E5M2 = 0, 1
 BLOCKS = {"row": 0, "square": 1}
-KEEP_X, KEEP_W = 1, 2
+KEEP_X, KEEP_W, KEEP_POWERS = 1, 2, 8
 _FP8_CODES = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
 _REAL_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
@@ -927,6 +927,14 @@ def gated_ffn(x, w_gate, w_up, w_down, activation="silu"):
     return _GatedFfn.apply(x, w_gate, w_up, w_down, code, act)
 
 
+# Keeping the powers of the logits spares a product of 2 K operations an element
+# and costs two passes of two bytes.  Training step in us, made again and kept:
+#   4096x32000x512   619  595      4096x32000x1024  1022   896
+#   1000x50257x768   408  368      8192x128256x4096 27228 21344
+#   500x1000x512     142  142      256x32000x2048    202   178
+POWERS_LEAST = 512
+
+
 @functools.lru_cache(maxsize=512)
 def _xent_bytes(M, V, K, keep):
     n = (ctypes.c_int64 * 3)()
@@ -936,35 +944,35 @@ def _xent_bytes(M, V, K, keep):
     return tuple(max(v, 1) for v in n)
 
 
-def _xent_forward(x, w, target, ignore, reduction, code):
+def _xent_forward(x, w, target, ignore, reduction, code, keep):
     """The loss, and what the backward pass reads of the rows."""
     device, (V, K) = x.device, w.shape
     M = target.numel()
     (x2, ldx), (w2, ldw), t = _read(x.reshape(M, K)), _read(w), target.contiguous()
     loss = torch.empty(() if reduction else target.shape, dtype=torch.float32, device=device)
-    sizes = _xent_bytes(M, V, K, 0)
+    sizes = _xent_bytes(M, V, K, keep)
     saved, scratch = (torch.empty(n, dtype=torch.uint8, device=device) for n in sizes[:2])
     _call(device, _lib.tgemm_xent_forward, M, V, K, code, x2.data_ptr(), ldx, w2.data_ptr(), ldw, t.data_ptr(), ignore, reduction,
-          loss.data_ptr(), saved.data_ptr(), scratch.data_ptr())
+          keep, loss.data_ptr(), saved.data_ptr(), scratch.data_ptr())
     return loss, saved
 
 
 class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, target, ignore, reduction, code):
-        loss, saved = _xent_forward(x, w, target, ignore, reduction, code)
+    def forward(ctx, x, w, target, ignore, reduction, code, powers):
+        loss, saved = _xent_forward(x, w, target, ignore, reduction, code, powers)
         ctx.save_for_backward(x, w, target, saved)
-        ctx.args = reduction, code
+        ctx.args = reduction, code, powers
         return loss
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, gloss):
         x, w, target, saved = ctx.saved_tensors
-        reduction, code = ctx.args
+        reduction, code, powers = ctx.args
         device, (V, K) = x.device, w.shape
         M = target.numel()
-        keep = (KEEP_X if ctx.needs_input_grad[0] else 0) | (KEEP_W if ctx.needs_input_grad[1] else 0)
+        keep = (KEEP_X if ctx.needs_input_grad[0] else 0) | (KEEP_W if ctx.needs_input_grad[1] else 0) | powers
         (x2, ldx), (w2, ldw), t, g = _read(x.reshape(M, K)), _read(w), target.contiguous(), gloss.contiguous()
         scratch = torch.empty(_xent_bytes(M, V, K, keep)[2], dtype=torch.uint8, device=device)
         dx = torch.empty(x.shape, dtype=x.dtype, device=device) if keep & KEEP_X else None
@@ -972,11 +980,11 @@ class _LinearCrossEntropy(torch.autograd.Function):
         _call(device, _lib.tgemm_xent_backward, M, V, K, code, x2.data_ptr(), ldx, w2.data_ptr(), ldw, t.data_ptr(), reduction,
               g.data_ptr(), saved.data_ptr(), keep, None if dx is None else dx.data_ptr(), K,
               None if dw is None else dw.data_ptr(), K, scratch.data_ptr())
-        return dx, dw, None, None, None, None
+        return dx, dw, None, None, None, None, None
 
 
-def linear_cross_entropy(x, w, target, ignore_index=-100, reduction="mean"):
-    """Softmax cross entropy of the logits x @ w^T, which are never stored,
+def linear_cross_entropy(x, w, target, ignore_index=-100, reduction="mean", keep_bytes=4 * 2 ** 30):
+    """Softmax cross entropy of the logits x @ w^T, which are not stored,
     differentiable: logsumexp(x @ w^T) - (x @ w^T)[target] of each token.
 
     x: (..., K), w: (V, K), both bfloat16 or both float16; target: int64 of
@@ -985,12 +993,17 @@ def linear_cross_entropy(x, w, target, ignore_index=-100, reduction="mean"):
     outside 0 .. V - 1 makes the loss NaN.
     ``reduction``: "mean" over the tokens that count (NaN where none does),
     "sum", or "none" (a loss for each token, zero where it does not count).
-    Returns float32; logits and the softmax are float throughout.  The backward
-    pass makes the logits again, a piece of the vocabulary at a time (scratch:
-    about 512 MB at most, or 16 KB a token where that is more, and dx's float sums
-    where there are several pieces), and rounds their gradients to x's dtype,
-    scaled by a power of two that the results do not keep, so that small
-    probabilities hold in float16 too.  Gradients have their inputs' dtypes;
+    Returns float32; the loss's logits and softmax are float throughout.
+
+    The backward pass goes by pieces of the vocabulary (scratch: about 512 MB at
+    most, or 16 KB a token where that is more, and dx's float sums where there are
+    several pieces).  With gradients wanted and K of at least 512, the forward pass
+    keeps each logit's power of e, relative to a maximum of its row and rounded to
+    x's dtype, where all of them take at most ``keep_bytes`` (2 V bytes a token;
+    0: never); otherwise the backward pass makes the logits again, which takes up
+    to 1.3 times as long for the step.  It rounds the logits' gradients to x's
+    dtype, scaled, like the powers, by a power of two that the results do not keep,
+    so that small probabilities hold in float16 too.  Gradients have their inputs' dtypes;
     second derivatives and forward-mode ones are refused.  To capture a training
     step into a graph, see :func:`linear_fp8`.
     """
@@ -1007,9 +1020,13 @@ def linear_cross_entropy(x, w, target, ignore_index=-100, reduction="mean"):
             tuple(x.shape[:-1]), x.device, tuple(target.shape), target.device))
     if not -2 ** 63 <= ignore_index < 2 ** 63 or ignore_index != int(ignore_index):
         raise ValueError("ignore_index must be an int64, got %r" % (ignore_index,))
+    if not keep_bytes >= 0:
+        raise ValueError("keep_bytes must not be negative, got %r" % (keep_bytes,))
     if not _wants_derivative((x, w)):
-        return _xent_forward(x, w, target, int(ignore_index), how, code)[0]
-    return _LinearCrossEntropy.apply(x, w, target, int(ignore_index), how, code)
+        return _xent_forward(x, w, target, int(ignore_index), how, code, 0)[0]
+    V, K = w.shape
+    powers = KEEP_POWERS if K >= POWERS_LEAST and V <= 2 ** 28 and 2 * target.numel() * ((V + 63) // 64 * 64) <= keep_bytes else 0
+    return _LinearCrossEntropy.apply(x, w, target, int(ignore_index), how, code, powers)
 
 
 def _dense(t):
