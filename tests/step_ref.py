@@ -111,7 +111,7 @@ def xent(x, w, target, ignore=-100, reduction="mean", dloss=None, kept=None):
     coef = torch.where(counts, dloss / n if reduction == "mean" else dloss, 0.0)[:, None]
     dz = p.scatter_add(1, at, -torch.ones_like(lse)[:, None]) * coef
     edz = coef.abs() * p * (ez + elogsum[:, None] + (8 + (z - lse[:, None]).abs()) * 2 * F32) + (u + 6 * F32) * dz.abs()
-    # dz is rounded after its scale brought the largest factor to 2^14 or more; a
+    # dz is rounded after its scale brought the largest factor to 2^14; a
     # probability below float's normal numbers (2^-126) may be taken as zero
     edz = edz + tiny * 2.0 ** -14 * coef.abs().max() + 2.0 ** -126 * coef.abs()
     if kept if kept is not None else K >= 512:

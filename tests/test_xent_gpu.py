@@ -78,6 +78,21 @@ def test_gradients_of_scaled_losses(size, dtype):
         assert ((got[k].double() - want[k][0]).abs() <= want[k][1])[fits].all() and got[k][over].isinf().all()
 
 
+@pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
+@pytest.mark.parametrize("dloss", [1.9, -1.1, 1000.3])
+def test_the_losses_factor_is_not_rounded(dloss, reduction):
+    """Of 256 words as likely as each other, p - 1 and p hold in bfloat16: dx is rounded once, not by a factor that
+    is common to all rows as well."""
+    M, V, K = 60, 256, 40
+    x, w, t = make(M, V, K, torch.bfloat16, ignored=0.0)
+    got = run(torch.zeros_like(x), w, t, dloss, reduction)["dx"].double()
+    c = float(torch.tensor(dloss, dtype=torch.float32)) / (M if reduction == "mean" else 1)
+    p = torch.full((M, V), 2.0 ** -8, dtype=torch.float64, device="cuda")
+    p[torch.arange(M), t] -= 1
+    want, size = c * (p @ w.double()), abs(c) * (p.abs() @ w.double().abs())
+    assert ((got - want).abs() <= 2.0 ** -8 * 1.001 * want.abs() + (V + 20) * 2.0 ** -24 * size).all()
+
+
 def test_small_probabilities_in_float16():
     """dw rows of unlikely words come from probabilities around 2^-23, below float16's normal numbers."""
     K, V, M = 64, 2000, 90

@@ -1002,8 +1002,8 @@ def linear_cross_entropy(x, w, target, ignore_index=-100, reduction="mean", keep
     x's dtype, where all of them take at most ``keep_bytes`` (2 V bytes a token;
     0: never); otherwise the backward pass makes the logits again, which takes up
     to 1.3 times as long for the step.  It rounds the logits' gradients to x's
-    dtype, scaled, like the powers, by a power of two that the results do not keep,
-    so that small probabilities hold in float16 too.  Gradients have their inputs' dtypes;
+    dtype, scaled, like the powers, by a factor that the results do not keep, so that
+    small probabilities hold in float16 too.  Gradients have their inputs' dtypes;
     second derivatives and forward-mode ones are refused.  To capture a training
     step into a graph, see :func:`linear_fp8`.
     """
