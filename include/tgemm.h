@@ -489,13 +489,13 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
  *
  * act: silu g / (1 + e^-g), gelu g Phi(g), its tanh form, or relu.  h is rounded
  * to `dtype` (the operand of the second product), y once from float sums.  `keep`
- * says which gradients will be asked for; g and u, rounded, are then kept in
- * `saved` (only h for TGEMM_FFN_DOWN alone).  backward, for dy (M x N):
+ * says which gradients will be asked for; what they need of a = act(g), b =
+ * act'(g) u and h is then kept in `saved`, rounded.  backward, for dy (M x N):
  *
- *     dh = dy wd,  dg = dh u act'(g),  du = dh act(g),
+ *     dh = dy wd,  dg = dh b,  du = dh a,
  *     dx = dg wg + du wu,  dwg = dg^T x,  dwu = du^T x,  dwd = dy^T h
  *
- * with dg, du and h rounded to `dtype`; outputs are written where `keep` (the same
+ * with dg and du rounded to `dtype`; outputs are written where `keep` (the same
  * as before) has their bit, and ignored otherwise.  relu'(0) = 0.  tgemm_ffn_bytes
  * fills bytes[0 .. 2] with the sizes of `saved`, of forward's `scratch` and of
  * backward's `scratch`: device memory, 256-byte aligned; a scratch's contents are

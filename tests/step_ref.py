@@ -51,7 +51,9 @@ def ffn(x, wg, wu, wd, name, dy=None):
     eg, eu = ((K + 2) * F32 * mm(x.abs(), w.abs().t()) for w in (wg, wu))
     a, d, d2 = act(g, name)
     # the activation itself: a few units of float's last place, relative and of g
-    ea = d.abs() * eg + 2.0 ** -20 * (a.abs() + 2.0 ** -3 * g.abs() * (d.abs() + 1e-3))
+    # where relu's argument is within its error of zero, either slope
+    jump = (g.abs() <= eg).double() * (name == "relu")
+    ea = (d.abs() + jump) * eg + 2.0 ** -20 * (a.abs() + 2.0 ** -3 * g.abs() * (d.abs() + 1e-3))
     h = a * up
     eh = u * h.abs() + ea * up.abs() + a.abs() * eu + tiny
     out = {"y": product(h, wd.t(), eh, u, tiny)}
@@ -60,16 +62,14 @@ def ffn(x, wg, wu, wd, name, dy=None):
     dy = dy.double()
     dh = mm(dy, wd)
     edh = (N + 2) * F32 * mm(dy.abs(), wd.abs())
-    # the backward pass reads g and u rounded
-    eg, eu = eg + u * g.abs() + tiny, eu + u * up.abs() + tiny
-    # where relu's argument is within its error of zero, either slope
-    jump = (g.abs() <= eg).double() * (name == "relu")
     ea = (d.abs() + jump) * eg + d2 * eg * eg + 2.0 ** -20 * (a.abs() + g.abs())
     ed = d2 * eg + jump + 2.0 ** -20 * (1 + g.abs())
-    dg, du, h = dh * up * d, dh * a, a * up
-    edg = u * dg.abs() + edh * (up * d).abs() + dh.abs() * (eu * d.abs() + (up.abs() + eu) * ed) + tiny
-    edu = u * du.abs() + edh * a.abs() + dh.abs() * ea + tiny
-    eh = u * h.abs() + ea * (up.abs() + eu) + a.abs() * eu + tiny
+    dg, du = dh * up * d, dh * a
+    # act'(g) u, act(g) and h are kept, each rounded once from float, and dg and du rounded again
+    eb = u * (up * d).abs() + eu * d.abs() + (up.abs() + eu) * ed + tiny
+    ea = u * a.abs() + ea + tiny
+    edg = u * dg.abs() + edh * ((up * d).abs() + eb) + dh.abs() * eb + tiny
+    edu = u * du.abs() + edh * (a.abs() + ea) + dh.abs() * ea + tiny
     c1, b1 = product(dg, wg, edg, u, tiny)
     c2, b2 = product(du, wu, edu, u, tiny)
     out["dx"] = c1 + c2, b1 + b2 + SLACK * F * F32 * (mm(dg.abs(), wg.abs()) + mm(du.abs(), wu.abs()))

@@ -33,7 +33,7 @@ COMMON = [
     (dict(M=-1), -1), (dict(M=2 ** 30 + 1), -1), (dict(K=2 ** 22 + 1), -1), (dict(F=-3), -1), (dict(N=2 ** 40), -1), (dict(keep=16), -1),
     (dict(keep=-1), -1), (dict(dtype=0), -1), (dict(dtype=2), -1), (dict(act=-1), -1), (dict(act=4), -1), (dict(ldx=7), -1),
     (dict(ldg=7), -1), (dict(ldu=7), -1), (dict(ldd=15), -1), (dict(ldx=2 ** 22 + 1), -1), (dict(ldd=2 ** 62), -1), (dict(x=None), -2),
-    (dict(wg=None), -2), (dict(wu=None), -2), (dict(wd=None), -2), (dict(saved=None), -2), (dict(scratch=None), -2), (dict(x=P(257)), -3),
+    (dict(wg=None), -2), (dict(wu=None), -2), (dict(wd=None), -2), (dict(saved=None), -2), (dict(scratch=None, keep=1), -2), (dict(x=P(257)), -3),
     (dict(wd=P(3)), -3), (dict(saved=P(128)), -3), (dict(scratch=P(64)), -3)]
 
 
@@ -54,10 +54,10 @@ def test_ffn_sizes():
     assert tl._lib.tgemm_ffn_bytes(4, 8, 16, 8, 15, None) == -2
     assert tl._lib.tgemm_ffn_bytes(4, 8, 2 ** 23, 8, 15, n) == -1
     assert tl._lib.tgemm_ffn_bytes(100, 64, 1000, 64, 0, n) == 0 and n[0] == 0 and n[1] >= 2 * 100 * 1000 and n[2] == 0
-    assert tl._lib.tgemm_ffn_bytes(100, 64, 1000, 64, 15, n) == 0 and n[0] == 2 * 2 * 100 * 1024 and n[2] >= 3 * 200000
+    assert tl._lib.tgemm_ffn_bytes(100, 64, 1000, 64, 15, n) == 0 and n[0] == 3 * 2 * 100 * 1024 and n[2] >= 2 * 200000
     assert tl._lib.tgemm_ffn_bytes(100, 64, 1000, 64, tl.FFN_DOWN, n) == 0 and n[0] == 2 * 100 * 1024  # h alone is kept, rows of whole lines
     assert tl._lib.tgemm_ffn_bytes(0, 64, 1000, 64, 15, n) == 0
-    assert tl._lib.tgemm_ffn_bytes(2 ** 30, 2 ** 22, 2 ** 22, 2 ** 22, 15, n) == 0 and min(n) > 2 ** 52
+    assert tl._lib.tgemm_ffn_bytes(2 ** 30, 2 ** 22, 2 ** 22, 2 ** 22, 1, n) == 0 and min(n) > 2 ** 52
 
 
 @pytest.mark.parametrize("kw", [dict(M=0, N=0), dict(M=0)])

@@ -75,20 +75,19 @@ struct MmStoreArgs {
 struct MmGateArgs {
     MmOperands op;
     MmGrid grid;
-    void *h, *g, *u;  // M x N, row stride ld; g and u NULL where nothing is kept.  Anything
-                      // may be written between N and ld
+    void *h, *a, *b;  // M x N, row stride ld: act(g) u, act(g), act'(g) u; a and b NULL where they
+                      // are not kept.  Anything may be written between N and ld
     int64_t ld;
     int32_t act;
 };
-// ---- its backward: dh = dy Wd, then dg, du and h from it and g, u ----------------
+// ---- its backward: dh = dy Wd, then du = dh a and dg = dh b ----------------------
 struct MmDhArgs {
     MmOperands op;
     MmGrid grid;
-    const void *g, *u;
-    void *dg, *du, *h;  // M x N, row stride ld (g's and u's too); any of them NULL where it is not
-                        // wanted.  Anything may be written between N and ld
+    const void *a, *b;  // both of them there: a branch at each load costs 70 us of 4096x4096x11008's 480
+    void *dg, *du;      // M x N, row stride ld (a's and b's too); either NULL where it is not wanted.
+                        // Anything may be written between N and ld
     int64_t ld;
-    int32_t act;
 };
 
 // ---- cross entropy ---------------------------------------------------------------
@@ -437,15 +436,19 @@ __global__ __launch_bounds__(G::NT) void mm_gate_kernel(MmGateArgs g) {
             auto put = [&](void* p, F8 x) {
                 if (inside.value || out.count(u) > 0) store8(out.at(static_cast<T*>(p), u), x);
             };
-            if (g.g) {  // for the backward pass: past the caches
-                auto keep = [&](void* p, F8 x) {
-                    if (inside.value || out.count(u) > 0) stream8(out.at(static_cast<T*>(p), u), x);
-                };
-                keep(g.g, v);
-                keep(g.u, w);
-            }
             float a[8], d[8];
-            activate8<false>(g.act, v, a, d);
+            if (g.a || g.b) {  // for the backward pass: past the caches
+                auto keep = [&](void* p, F8 x) {
+                    if (p && (inside.value || out.count(u) > 0)) stream8(out.at(static_cast<T*>(p), u), x);
+                };
+                activate8<true>(g.act, v, a, d);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d[e] *= w[e];
+                keep(g.a, a);
+                keep(g.b, d);
+            } else {
+                activate8<false>(g.act, v, a, d);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) a[e] *= w[e];
             put(g.h, a);  // its rounding: the down projection's operand
@@ -467,39 +470,25 @@ __global__ __launch_bounds__(G::NT) void mm_dh_kernel(MmDhArgs g) {
     const MmOut<G> out(at, g.op.M, (int)g.ld, g.ld);  // rows whole up to their stride: no edge inside them
     typedef float(&F8)[8];
     struct Kept {
-        Raw8 g, u;
+        Raw8 a, b;
     };
     auto way = [&](auto inside) {
         G::template each_row<Kept>(acc, smem, at.lane, at.wave, [&](int u, Kept& k) {
-            const T *pg = out.at(static_cast<const T*>(g.g), u), *pu = out.at(static_cast<const T*>(g.u), u);
             if (inside.value || out.count(u) > 0) {
-                load8(k.g, pg);
-                load8(k.u, pu);
+                load8(k.a, out.at(static_cast<const T*>(g.a), u));
+                load8(k.b, out.at(static_cast<const T*>(g.b), u));
             }
         }, [&](int u, F8 v, F8, Kept& k) {
-            auto put = [&](void* p, F8 x) {
+            // roundings of du and dg: operands of the products that follow
+            auto put = [&](void* p, const Raw8& raw) {
+                float x[8];
+                values8<T>(x, raw);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= v[e];
                 if (inside.value || out.count(u) > 0) store8(out.at(static_cast<T*>(p), u), x);
             };
-            float gate[8], up[8], a[8], d[8], o[8];
-            values8<T>(gate, k.g);
-            values8<T>(up, k.u);
-            activate8<true>(g.act, gate, a, d);
-            // roundings of dg, du, h: operands of the products that follow
-            if (g.dg) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = v[e] * up[e] * d[e];
-                put(g.dg, o);
-            }
-            if (g.du) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = v[e] * a[e];
-                put(g.du, o);
-            }
-            if (g.h) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = a[e] * up[e];
-                put(g.h, o);
-            }
+            if (g.du) put(g.du, k.a);
+            if (g.dg) put(g.dg, k.b);
         });
     };
     if (out.inside()) way(Yes{});
@@ -754,7 +743,8 @@ MmKernel mm_entry(const void* fn, const void* join = nullptr) {
 // The tiles.  256 x 256: eight waves of 64 x 128 (four of 128 x 128: 4096^3 alike,
 // 110 us, but 4096x11008x4096 ended by the softmax's pieces 313 us against 294,
 // where a lone wave a SIMD does the end's arithmetic by itself; the end that loads
-// two values for each result is better off with four, 378 us against 394).  128 x
+// two values for each result is better off with four, 355 us; eight 394 when
+// it still made the activation).  128 x
 // 128 twice a compute unit, four waves and two slots each; 64 x 128 likewise with
 // three slots, for few rows.  128 x 128 once a unit, eight waves and four slots,
 // where there are no more workgroups than units (2048x2048x5440 46 us, twice a

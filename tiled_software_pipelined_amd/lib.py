@@ -904,12 +904,12 @@ def gated_ffn(x, w_gate, w_up, w_down, activation="silu"):
     x: (..., K), w_gate and w_up: (F, K), w_down: (N, F), all bfloat16 or all
     float16; rows may be apart (parts of one (2 F, K) tensor serve as w_gate and
     w_up).  ``activation``: "silu", "gelu", "gelu_tanh" or "relu".  Returns
-    (..., N) of x's dtype.  Sums are float; the inner values (and, for the
-    backward pass, both projections and their gradients) are rounded to x's dtype,
-    y and each gradient once.  The two projections, the activation and their
+    (..., N) of x's dtype.  Sums are float; the inner values are rounded to
+    x's dtype (for the backward pass the activation, its slope times the up
+    projection, and both projections' gradients too), y and each gradient once.  The two projections, the activation and their
     product are one kernel; up to 16 tokens without gradients take kernels that read
-    each weight once.  The backward pass keeps the two projections (two values
-    for each token and inner unit) and computes only the gradients that are asked
+    each weight once.  For the backward pass up to three values are kept for each
+    token and inner unit; it computes only the gradients that are asked
     for; second derivatives and forward-mode ones are refused.  To capture a
     training step into a graph, see :func:`linear_fp8`.
     """
