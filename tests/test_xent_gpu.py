@@ -435,3 +435,29 @@ def test_refusals_on_the_gpu():
     for ignore in (2 ** 63, 0.5):
         with pytest.raises(ValueError, match="ignore_index"):
             tl.linear_cross_entropy(x, w, t, ignore_index=ignore)
+
+
+@pytest.mark.parametrize("kept", [False, True])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("base", [1, 16, 128, 256])
+def test_nearly_certain_targets_of_large_logits(base, dtype, kept, monkeypatch):
+    """Logits base^2 (+ 12 for the target), all of them whole numbers that float holds: neither the loss nor p - 1 loses
+    digits to their size."""
+    monkeypatch.setattr(tl, "POWERS_LEAST", 0)
+    M, V = 64, 256
+    x = torch.tensor([[float(base), 1.0]], device="cuda").to(dtype).expand(M, 2).contiguous()
+    w = torch.tensor([[float(base), 0.0]], device="cuda").to(dtype).repeat(V, 1)
+    w[5, 1] = 12.0
+    t = torch.full((M,), 5, device="cuda")
+    got = run(x, w, t, 1024.0, "sum", keep_bytes=2 ** 34 * kept)
+    others = (V - 1) * torch.exp(torch.tensor(-12.0, dtype=torch.float64))
+    loss = torch.log1p(others)
+    # the sum of powers is near one, and each addition to it is off by up to 2^-24: 64 of them in a lane, 64 for the pieces
+    far = 130 * 2.0 ** -24
+    assert abs(float(got["loss"]) / M - float(loss)) <= far + 2.0 ** -22 * float(loss)
+    left = others / (1 + others)  # 1 - p
+    want = -1024 * left * 12  # the one column in which the words differ: dx = sum of dz w
+    u = ref.U[dtype]
+    assert ((got["dx"][:, 1].double() - want).abs() <= (2 * u * left + far + 2.0 ** -20) * 1024 * 12 + 2.0 ** -25).all()
+    dw = got["dw"][5, 1].double()
+    assert abs(dw + M * 1024 * left) <= (2 * u * left + far + 2.0 ** -20) * 1024 * M

@@ -112,8 +112,8 @@ struct MmDzArgs {
     const int32_t* map;
     const int64_t* target;
     int64_t v0;
-    const float* lse;
-    const float* coef;  // of each row
+    const float2* lse;  // (max, log2 of the sum above it) of each row
+    const float* coef;  // likewise
     void* dz;           // M x N, row stride ldz elements; anything may be written between
     int64_t ldz;
 };
@@ -496,6 +496,10 @@ __global__ __launch_bounds__(G::NT) void mm_dh_kernel(MmDhArgs g) {
 }
 
 constexpr float LOG2E = 1.44269504f;
+// exp(z - max) / sum, from (max, log2 sum).  z - max is exact where p is near one.
+__device__ __forceinline__ float softmax_of(float z, float2 lse) {
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(z - lse.x, LOG2E, -lse.y));
+}
 
 // A product with as many rows as the device says.
 template <class G>
@@ -600,7 +604,8 @@ __global__ __launch_bounds__(G::NT) void mm_dz_kernel(MmDzArgs g) {
     const MmOut<G> out(at, (M + 63) / 64 * 64, (int)g.ldz, g.ldz);  // rows whole up to their stride
     typedef float(&F8)[8];
     struct Row {
-        float lse, coef;
+        float2 lse;
+        float coef;
         int64_t target;
     };
     auto way = [&](auto inside) {
@@ -614,7 +619,7 @@ __global__ __launch_bounds__(G::NT) void mm_dz_kernel(MmDzArgs g) {
             const int hit = t >= 0 && t < 8 ? (int)t : -1;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float p = __builtin_amdgcn_exp2f((v[e] - row.lse) * LOG2E);
+                float p = softmax_of(v[e], row.lse);
                 if (e == hit) p -= 1.0f;
                 v[e] = p * row.coef;
             }

@@ -6,10 +6,13 @@
 // then), their number stays on the device, and workgroups past it end at once.
 //
 // Forward: the product's kernel ends with the maximum and the sum of powers of
-// each wave's 64 or 128 columns; a second one joins them to lse, the logarithm of the
-// row's sum, and the row's loss.  Backward: pieces of the vocabulary, for each the
-// product again, ended by dz = coef (exp(z - lse) - [target]), and the two
-// products that take it, dx += dz W and dW = dz^T x.
+// each wave's 64 or 128 columns; a second one joins them to the row's maximum, the
+// logarithm of its sum above that, and the row's loss.  The two stay apart: in
+// their sum, of which float holds 24 bits, a likely target's loss and its p - 1
+// would lose what the logits' size takes (a loss of 1.6e-3 was 2.0e-3 at logits of
+// 16384, and 0 at 65536).  Backward: pieces of the vocabulary, for each the
+// product again, ended by dz = coef (p - [target]), p = exp(z - max) / sum, and the
+// two products that take it, dx += dz W and dW = dz^T x.
 //
 // With TGEMM_KEEP_POWERS the forward pass also stores each power, rounded to 16
 // bits (2 V bytes a row that counts), and dz is a pass over them: 6 M V K
@@ -53,7 +56,7 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
     l.count = take(0, 4);  // how many rows count
     l.map = take(0, 4 * M);   // where they stand
     l.rank = take(0, 4 * M);  // each row's number among them, -1
-    l.lse = take(0, 4 * M);   // of each of them
+    l.lse = take(0, 8 * M);   // of each of them
     const bool pack = mm_packs(K, M);
     l.ldx = mm_lines(K);
     l.w = l.w2 = -1;
@@ -258,7 +261,8 @@ struct RowsArgs {
     const int64_t* target;
     const float2* part;
     const float* hit;
-    float *lse, *loss;  // lse of each row that counts, loss of each row
+    float2* lse;  // (max, log2 of the sum of 2^((z - max) log2 e)) of each row that counts
+    float* loss;  // of each row
 };
 
 // 16 rows a workgroup, 32 threads a row.
@@ -289,12 +293,11 @@ __global__ __launch_bounds__(512) void xent_rows_kernel(RowsArgs g) {
     __syncthreads();
     if (y != 0 || m >= M) return;
     for (int k = 1; k < 32; ++k) join(held[k][r]);
-    const float lse = most + logf(sum);
-    g.lse[m] = lse;
+    g.lse[m] = float2{most, log2f(sum)};
     const int to = g.map[m];
     const int64_t t = g.target[to];
     // a target outside the vocabulary has no logit: its loss is NaN
-    g.loss[to] = t >= 0 && t < g.V ? lse - g.hit[m] : NAN;
+    g.loss[to] = t >= 0 && t < g.V ? (most - g.hit[m]) + logf(sum) : NAN;
 }
 
 struct ReduceArgs {
@@ -388,7 +391,8 @@ struct PowersArgs {
     const int32_t *count, *map;
     const int64_t* target;
     const float2* part;
-    const float *hit, *lse, *coef;
+    const float *hit, *coef;
+    const float2* lse;
     const void* powers;
     void* dz;
 };
@@ -396,8 +400,8 @@ struct PowersArgs {
 // dz of a piece of the vocabulary from the kept powers: one pass over them, bound by
 // memory (3686 rows of 32000 in 86 us, 5.5 TB/s read and written).  A workgroup
 // takes 16 rows and 16 maxima's columns (1024 or 2048): a thread makes the factor
-// coef 2^((max - lse) log2 e) of one row and maximum, then each wave walks four
-// rows.  The target's element is coef (exp(z - lse) - 1) from its logit
+// coef exp(max' - max) / sum of one row and maximum, then each wave walks four
+// rows.  The target's element is coef (exp(z - max) / sum - 1) from its logit
 // in float: near one, a rounded power would leave nothing of the difference.
 // Zero in the rows up to the next multiple of 64.
 template <class T>
@@ -411,11 +415,11 @@ __global__ __launch_bounds__(256) void xent_powers_kernel(PowersArgs g) {
         const int r = threadIdx.x & 15, p = threadIdx.x >> 4, m = m0 + r;
         const int64_t v = g.v0 + c0 + p * g.wide;
         float f = 0.0f;
-        if (m < M && v < g.V) f = g.coef[m] * __builtin_amdgcn_exp2f((g.part[v / g.wide * g.M + m].x - g.lse[m]) * LOG2E);
+        if (m < M && v < g.V) f = g.coef[m] * softmax_of(g.part[v / g.wide * g.M + m].x, g.lse[m]);
         held[r][p] = f;
         if (p == 0) {
             aim[r] = m < M ? g.target[g.map[m]] - g.v0 : -1;
-            one[r] = aim[r] >= 0 && aim[r] < g.n ? g.coef[m] * (__builtin_amdgcn_exp2f((g.hit[m] - g.lse[m]) * LOG2E) - 1.0f) : 0.0f;
+            one[r] = aim[r] >= 0 && aim[r] < g.n ? g.coef[m] * (softmax_of(g.hit[m], g.lse[m]) - 1.0f) : 0.0f;
         }
     }
     __syncthreads();
@@ -474,8 +478,8 @@ int tgemm_xent_forward(int64_t M, int64_t V, int64_t K, int32_t dtype, const voi
     int32_t *count = reinterpret_cast<int32_t*>(v + l.count), *map = reinterpret_cast<int32_t*>(v + l.map),
             *rank = reinterpret_cast<int32_t*>(v + l.rank);
     char* where = l.powers >= 0 ? v : s;
-    float *hit = reinterpret_cast<float*>(where + l.hit), *lse = reinterpret_cast<float*>(v + l.lse);
-    float2* part = reinterpret_cast<float2*>(where + l.part);
+    float* hit = reinterpret_cast<float*>(where + l.hit);
+    float2 *lse = reinterpret_cast<float2*>(v + l.lse), *part = reinterpret_cast<float2*>(where + l.part);
     float* each = reduction == TGEMM_NONE ? loss : reinterpret_cast<float*>(s + l.each);
     ScanArgs c{M, ignore, target, count, map, rank};
     GatherArgs into{M, K, ldx, l.ldx, 0, static_cast<const uint16_t*>(x), reinterpret_cast<uint16_t*>(s + l.x),
@@ -569,15 +573,15 @@ int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const vo
             const int wide = wave_cols(l.stats);
             const int64_t chunks = (l.ldz + 16 * wide - 1) / (16 * wide);
             PowersArgs a{(int32_t)V, (int32_t)n, wide, (int32_t)chunks, M, v0, l.ldp, l.ldz, count, map, target,
-                         reinterpret_cast<const float2*>(v + l.part), reinterpret_cast<const float*>(v + l.hit),
-                         reinterpret_cast<const float*>(v + l.lse), coef, v + l.powers, s + l.dzs};
+                         reinterpret_cast<const float2*>(v + l.part), reinterpret_cast<const float*>(v + l.hit), coef,
+                         reinterpret_cast<const float2*>(v + l.lse), v + l.powers, s + l.dzs};
             const void* fn = dtype == TGEMM_BF16 ? reinterpret_cast<const void*>(xent_powers_kernel<__bf16>)
                                                  : reinterpret_cast<const void*>(xent_powers_kernel<_Float16>);
             rc = mm_launch(fn, chunks * ((M + 63) / 64 * 4), 256, &a, "gradient of the logits", st);
         } else if (rc == TGEMM_OK && M > 0 && n > 0) {
             const MmKernel& k = mm_kernels(dtype, FORM_DZ)[l.dz];
             MmDzArgs a{MmOperands{s + l.x2, wv, nullptr, 2 * l.ldx, 2 * ldv, 0, (int32_t)M, (int32_t)n, (int32_t)K},
-                       mm_grid(k, M, n), count, map, target, v0, reinterpret_cast<const float*>(v + l.lse), coef, s + l.dzs,
+                       mm_grid(k, M, n), count, map, target, v0, reinterpret_cast<const float2*>(v + l.lse), coef, s + l.dzs,
                        l.ldz};
             rc = mm_launch(k.fn, (int64_t)a.grid.tiles_m * a.grid.tiles_n, k.threads, &a, "gradient of the logits", st);
         }
