@@ -539,9 +539,10 @@ int tgemm_ffn_backward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype
  *
  * keep: TGEMM_KEEP_X (dx), TGEMM_KEEP_W (dw) and TGEMM_KEEP_POWERS, of which
  * forward looks at the last alone; it must be the same in all calls.  With it (V up
- * to 2^28) forward leaves 2^15 exp(z - max) of every logit, max a maximum of part of
- * its row, rounded to `dtype`, in `saved`, about 2 V bytes a row, and backward
- * takes p from there (the target's from its logit, in float).  tgemm_xent_bytes
+ * to 2^28) forward leaves exp(z - max) of every logit, max a maximum of part of its
+ * row, in `saved`, about 2 V bytes a row: in 16 bits without a sign, off by 2^-10
+ * of itself (float16: 2^-12, or 2^-42).  Backward takes p from there (the target's
+ * from its logit, in float).  tgemm_xent_bytes
  * fills bytes[0 .. 2] with the sizes of `saved`, forward's `scratch` (whatever
  * TGEMM_KEEP_X and _W) and backward's: device memory, 256-byte aligned; a scratch's
  * contents are overwritten.  Sizes of zero are the empty sums they make.  Each

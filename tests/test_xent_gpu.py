@@ -461,3 +461,24 @@ def test_nearly_certain_targets_of_large_logits(base, dtype, kept, monkeypatch):
     assert ((got["dx"][:, 1].double() - want).abs() <= (2 * u * left + far + 2.0 ** -20) * 1024 * 12 + 2.0 ** -25).all()
     dw = got["dw"][5, 1].double()
     assert abs(dw + M * 1024 * left) <= (2 * u * left + far + 2.0 ** -20) * 1024 * M
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_kept_powers_do_not_add_a_rounding(dtype):
+    """With the unit matrix for w, dx is dz: each element is off by dz's rounding and a small part of one."""
+    M, K = 256, 512
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = (torch.randn((M, K), generator=g, device="cuda") * 0.7).to(dtype)
+    w = torch.eye(K, dtype=dtype, device="cuda")
+    t = torch.randint(0, K, (M,), generator=g, device="cuda")
+    scale = 2.0 ** 10
+    z = x.double()
+    want = scale * (torch.softmax(z, 1) - torch.nn.functional.one_hot(t, K))
+    dx = {}
+    for keep in (0, 2 ** 30):
+        dx[keep] = run(x, w, t, scale, "sum", keep_bytes=keep)["dx"].double()
+        off = (dx[keep] - want).abs() / want.abs()
+        # dz is rounded; the logits are exact, p is good to 2^-19, and a kept power to half a step of 10 or 12 bits
+        power = {torch.bfloat16: 2.0 ** -10, torch.float16: 2.0 ** -12}[dtype]
+        assert off.max() <= ref.U[dtype] + 2.0 ** -18 + (power * 1.01 if keep else 0), (keep, float(off.max() / ref.U[dtype]))
+    assert abs(float(((dx[2 ** 30] - want) / want).mean())) < 2.0 ** -15

@@ -100,11 +100,37 @@ struct MmStatsArgs {
     const int64_t* target;
     float2* part;  // (max, sum of 2^((z - max) log2 e)) of each wave's columns: part[piece M + row]
     float* hit;    // the target's logit of a row, where it has one
-    void* powers;  // KEEP: POWER 2^((z - max) log2 e) of every logit, rounded, M x N
-    int64_t ldp;   // their row stride; anything may be written between
+    uint16_t* powers;  // KEEP: 2^((z - max) log2 e) of every logit, as power_code has it, M x N
+    int64_t ldp;       // their row stride; anything may be written between
 };
-// Powers are at most one.  float16 holds 11 bits of them down to 2^-14 / POWER.
-constexpr float POWER = 32768.0f;
+// A kept power, which is at most one, in 16 bits without a sign.  For bfloat16: 7
+// bits of an exponent and 9 behind the point, over float's normal numbers up to
+// one, as far as bfloat16 itself reaches; off by 2^-10, a quarter of what rounding
+// dz adds (elements of dz off by 1.71e-3; 1.66e-3 from logits made again, 2.35e-3
+// from powers kept as bfloat16 numbers).  For float16: 5 and 11, off by 2^-12, half
+// of what rounding dz adds; evenly spaced by 2^-41 below 2^-30, finer than float16's
+// dz.  Times SCALE, a float's own bits are the code with more behind it; SHIFT
+// brings the code to the upper half.  A NaN becomes some number: its row's sum has
+// it.
+template <class T>
+struct Power {
+    static constexpr int SHIFT = 2;
+    static constexpr float SCALE = 1.0f, BACK = 1.0f;
+};
+template <>
+struct Power<_Float16> {
+    static constexpr int SHIFT = 4;
+    static constexpr float SCALE = 0x1p-96f, BACK = 0x1p96f;
+};
+template <class T>
+__device__ __forceinline__ uint32_t power_code(float power) {
+    return (__builtin_bit_cast(uint32_t, power * Power<T>::SCALE) << Power<T>::SHIFT) + 0x8000u;
+}
+// SCALE times the power of a code that stands in the lower half.
+template <class T>
+__device__ __forceinline__ float power_of(uint32_t code) {
+    return __builtin_bit_cast(float, (code & 0xffffu) << (16 - Power<T>::SHIFT));
+}
 struct MmDzArgs {
     MmOperands op;   // b: rows v0 .. of W
     MmGrid grid;
@@ -571,13 +597,14 @@ __global__ __launch_bounds__(G::NT) void mm_stats_kernel(MmStatsArgs g) {
     }
     if constexpr (KEEP) {
         typedef typename G::T T;
-        T* to = static_cast<T*>(g.powers);
         const MmOut<G> out(at, M, (int)g.ldp, g.ldp);  // rows whole up to their stride
         auto way = [&](auto inside) {
             G::each_row(acc, smem, at.lane, at.wave, [&](int u, float (&v)[8], float (&)[8]) {
+                i32x4 codes;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= POWER;
-                if (inside.value || out.count(u) > 0) store8(out.at(to, u), v);
+                for (int e = 0; e < 4; ++e)  // two upper halves
+                    codes[e] = (int)__builtin_amdgcn_perm(power_code<T>(v[2 * e + 1]), power_code<T>(v[2 * e]), 0x07060302u);
+                if (inside.value || out.count(u) > 0) __builtin_memcpy(out.at(g.powers, u), &codes, 16);
             });
         };
         if (out.inside()) way(Yes{});

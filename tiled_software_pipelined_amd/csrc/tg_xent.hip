@@ -14,9 +14,10 @@
 // product again, ended by dz = coef (p - [target]), p = exp(z - max) / sum, and the
 // two products that take it, dx += dz W and dW = dz^T x.
 //
-// With TGEMM_KEEP_POWERS the forward pass also stores each power, rounded to 16
-// bits (2 V bytes a row that counts), and dz is a pass over them: 6 M V K
-// operations for the step, not 8 (8192x4096x128256 25.0 ms -> 19.4).
+// With TGEMM_KEEP_POWERS the forward pass also stores each power in 16 bits (2 V
+// bytes written for a row that counts, and room for every row: only the device
+// knows how many count), and dz is a pass over them: 6 M V K operations for the
+// step, not 8 (8192x4096x128256, 90 % of the rows counting, 25.0 ms -> 19.4).
 #include <climits>
 
 #include "tg_mm_host.hpp"
@@ -393,7 +394,7 @@ struct PowersArgs {
     const float2* part;
     const float *hit, *coef;
     const float2* lse;
-    const void* powers;
+    const uint16_t* powers;
     void* dz;
 };
 
@@ -415,7 +416,7 @@ __global__ __launch_bounds__(256) void xent_powers_kernel(PowersArgs g) {
         const int r = threadIdx.x & 15, p = threadIdx.x >> 4, m = m0 + r;
         const int64_t v = g.v0 + c0 + p * g.wide;
         float f = 0.0f;
-        if (m < M && v < g.V) f = g.coef[m] * softmax_of(g.part[v / g.wide * g.M + m].x, g.lse[m]);
+        if (m < M && v < g.V) f = Power<T>::BACK * g.coef[m] * softmax_of(g.part[v / g.wide * g.M + m].x, g.lse[m]);
         held[r][p] = f;
         if (p == 0) {
             aim[r] = m < M ? g.target[g.map[m]] - g.v0 : -1;
@@ -425,18 +426,20 @@ __global__ __launch_bounds__(256) void xent_powers_kernel(PowersArgs g) {
     __syncthreads();
     const int c1 = min(c0 + 16 * g.wide, (int)g.ldz);
     for (int r = wave_id(); r < 16; r += 4) {
-        const T* from = static_cast<const T*>(g.powers) + (int64_t)(m0 + r) * g.ldp + g.v0;
+        const uint16_t* from = g.powers + (int64_t)(m0 + r) * g.ldp + g.v0;
         T* to = static_cast<T*>(g.dz) + (int64_t)(m0 + r) * g.ldz;
         const bool zero = m0 + r >= M;
         for (int c = c0 + 8 * lane_id(); c < c1; c += 512) {
             Raw8 raw{};
             if (!zero && g.v0 + c < g.ldp) load8(raw, from + c);
             float v[8];
-            values8<T>(v, raw);
             const float f = zero ? 0.0f : held[r][(c - c0) / g.wide];
             const int64_t t = aim[r] - c;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = zero ? 0.0f : e == t ? one[r] : v[e] * (1.0f / POWER) * f;
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t two = (uint32_t)raw.v[e >> 1];
+                v[e] = zero ? 0.0f : e == t ? one[r] : power_of<T>(e & 1 ? two >> 16 : two) * f;
+            }
             store8(to + c, v);
         }
     }
@@ -502,7 +505,8 @@ int tgemm_xent_forward(int64_t M, int64_t V, int64_t K, int32_t dtype, const voi
         const MmKernel& k = mm_kernels(dtype, l.powers >= 0 ? FORM_STATS_KEEP : FORM_STATS)[l.stats];
         MmStatsArgs a{MmOperands{s + l.x, static_cast<const char*>(w), nullptr, 2 * l.ldx, 2 * ldw, 0, (int32_t)M, (int32_t)V,
                                  (int32_t)K},
-                      mm_grid(k, M, V), count, map, target, part, hit, l.powers >= 0 ? v + l.powers : nullptr, l.ldp};
+                      mm_grid(k, M, V), count, map, target, part, hit,
+                      l.powers >= 0 ? reinterpret_cast<uint16_t*>(v + l.powers) : nullptr, l.ldp};
         rc = mm_launch(k.fn, (int64_t)a.grid.tiles_m * a.grid.tiles_n, k.threads, &a, "logits", st);
     }
     if (rc == TGEMM_OK && M > 0) {
@@ -574,7 +578,7 @@ int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const vo
             const int64_t chunks = (l.ldz + 16 * wide - 1) / (16 * wide);
             PowersArgs a{(int32_t)V, (int32_t)n, wide, (int32_t)chunks, M, v0, l.ldp, l.ldz, count, map, target,
                          reinterpret_cast<const float2*>(v + l.part), reinterpret_cast<const float*>(v + l.hit), coef,
-                         reinterpret_cast<const float2*>(v + l.lse), v + l.powers, s + l.dzs};
+                         reinterpret_cast<const float2*>(v + l.lse), reinterpret_cast<const uint16_t*>(v + l.powers), s + l.dzs};
             const void* fn = dtype == TGEMM_BF16 ? reinterpret_cast<const void*>(xent_powers_kernel<__bf16>)
                                                  : reinterpret_cast<const void*>(xent_powers_kernel<_Float16>);
             rc = mm_launch(fn, chunks * ((M + 63) / 64 * 4), 256, &a, "gradient of the logits", st);

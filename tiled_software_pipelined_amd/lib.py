@@ -999,11 +999,11 @@ def linear_cross_entropy(x, w, target, ignore_index=-100, reduction="mean", keep
     most, or 16 KB a token where that is more, and dx's float sums where there are
     several pieces).  With gradients wanted and K of at least 512, the forward pass
     keeps each logit's power of e, relative to a maximum of its row and rounded to
-    x's dtype, where all of them take at most ``keep_bytes`` (2 V bytes a token;
-    0: never); otherwise the backward pass makes the logits again, which takes up
-    to 1.3 times as long for the step.  It rounds the logits' gradients to x's
-    dtype, scaled, like the powers, by a factor that the results do not keep, so that
-    small probabilities hold in float16 too.  Gradients have their inputs' dtypes;
+    10 bits (float16: 12), where all of them take at most ``keep_bytes`` (2 V bytes a token, whether
+    it counts or not: as much as logits of 16 bits; 0: never); otherwise the backward
+    pass makes the logits again, which takes up to 1.3 times as long for the step.  It
+    rounds the logits' gradients to x's dtype, scaled by a factor that the results do
+    not keep, so that small probabilities hold in float16 too.  Gradients have their inputs' dtypes;
     second derivatives and forward-mode ones are refused.  To capture a training
     step into a graph, see :func:`linear_fp8`.
     """
