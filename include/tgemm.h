@@ -534,8 +534,9 @@ int tgemm_ffn_backward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype
  *     dz = c (exp(z - lse) - [target]),  dx = dz w,  dw = dz^T x,
  *
  * c the row's share of dloss.  It makes z again, a piece of the vocabulary at a
- * time, and rounds dz to `dtype`, scaled so that the largest |c| is 2^14; dx is
- * summed in float over the pieces and rounded once.
+ * time, and rounds dz to `dtype`, scaled so that the largest |c| is 2^14 (float16
+ * and TGEMM_NONE: for dx, each row's); dx is summed in float over the pieces and
+ * rounded once.
  *
  * keep: TGEMM_KEEP_X (dx), TGEMM_KEEP_W (dw) and TGEMM_KEEP_POWERS, of which
  * forward looks at the last alone; it must be the same in all calls.  With it (V up

@@ -482,3 +482,35 @@ def test_kept_powers_do_not_add_a_rounding(dtype):
         power = {torch.bfloat16: 2.0 ** -10, torch.float16: 2.0 ** -12}[dtype]
         assert off.max() <= ref.U[dtype] + 2.0 ** -18 + (power * 1.01 if keep else 0), (keep, float(off.max() / ref.U[dtype]))
     assert abs(float(((dx[2 ** 30] - want) / want).mean())) < 2.0 ** -15
+
+
+@pytest.mark.parametrize("M,V,K", [(90, 700, 64), (200, 3001, 520), (33000, 20001, 24)])
+def test_a_rows_gradient_does_not_depend_on_other_rows_factors(M, V, K):
+    """Float16 and a loss for each row: a row's dx keeps its digits whatever the largest factor of the batch is."""
+    x, w, t = make(M, V, K, torch.float16, ignored=0.1)
+    by = torch.exp2(torch.linspace(-3, 3, M, device="cuda"))
+    by[1::7] *= -1
+    by[5], t[5] = 2.0 ** 60, 1  # its own dx is past the type
+    by[6] = 0.0
+    by[7], t[7] = float("nan"), 2
+    some = torch.arange(0, M, max(1, M // 500), device="cuda")
+    some = some[(some != 5) & (some != 7)]
+    for keep in (0, 2 ** 34):
+        dx = run(x, w, t, by, "none", keep_bytes=keep)["dx"]
+        want = ref.xent(x[some], w, t[some], reduction="none", dloss=by[some])
+        ref.check({"dx": dx[some]}, want, ("dx",))
+        # each row against the largest of its own
+        for rows, values in zip(some.split(64), want["dx"][0].split(64)):
+            off = (dx[rows].double() - values).norm(dim=1)
+            assert (off <= 2e-3 * values.norm(dim=1)).all()
+        assert dx[7].isnan().all() and not dx[t == -100].any()
+
+
+def test_rows_factors_of_all_sizes_serve_dw():
+    x, w, t = make(130, 500, 72, torch.float16, ignored=0.1)
+    by = torch.exp2(torch.linspace(-28, 6, 130, device="cuda"))
+    for keep in (0, 2 ** 34):
+        ref.check(run(x, w, t, by, "none", keep_bytes=keep), ref.xent(x, w, t, reduction="none", dloss=by))
+        one = w.detach().requires_grad_()
+        (alone,) = torch.autograd.grad(tl.linear_cross_entropy(x, one, t, reduction="none", keep_bytes=keep), one, by)
+        ref.check({"dw": alone}, ref.xent(x, w, t, reduction="none", dloss=by), ("dw",))

@@ -62,6 +62,7 @@ struct MmStoreArgs {
     MmJob job[3];
     int32_t jobs;
     const float* alpha;  // NULL: one
+    const float* row_alpha;  // not NULL: that of each row, in alpha's place
     // A number of rows that only the device knows (NULL: as the operands say): the
     // first job's M, or its K (rows_are_k; then rounded up to 64, operands being
     // zero between), up to what the operands say.
@@ -344,14 +345,16 @@ __global__ __launch_bounds__(G::NT) void mm_store_kernel(MmStoreArgs g) {
         const bool stream = job.stream != 0;
         struct Row {
             int to;
+            float alpha;
         };
         auto way = [&](auto inside) {
             G::template each_row<Row>(acc, smem, at.lane, at.wave, [&](int u, Row& row) {
                 row.to = inside.value ? out.row(u) : min(out.row(u), M - 1);
+                row.alpha = g.row_alpha ? g.row_alpha[row.to] : alpha;
                 if (g.map) row.to = g.map[row.to];
             }, [&](int u, F8 v, F8, Row& row) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= alpha;
+                for (int e = 0; e < 8; ++e) v[e] *= row.alpha;
                 T* dst = C + (int64_t)row.to * out.ld + out.col();
                 if (inside.value) {
                     if (stream) stream8(dst, v);
@@ -404,7 +407,7 @@ __device__ __forceinline__ void mm_join(const MmStoreArgs& g, int slice, int til
     grouped_tile(tile, grid.tiles_m, grid.tiles_n, 4, tm, tn);
     const int m = tm * BM + e / BN, n = tn * BN + e % BN, M = g.jobs > 1 ? job.op[0].M : all.M, N = job.op[0].N;
     if (m >= M || n >= N) return;
-    const float alpha = g.alpha ? *g.alpha : 1.0f;
+    const float alpha = g.row_alpha ? g.row_alpha[m] : g.alpha ? *g.alpha : 1.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         v[i] = (v[i] + held[0][i >> 2][lane][i & 3] + held[1][i >> 2][lane][i & 3] + held[2][i >> 2][lane][i & 3]) * alpha;
@@ -433,7 +436,7 @@ __global__ __launch_bounds__(256) void mm_round_kernel(MmStoreArgs g) {
         for (int e = 0; e < 3; ++e)
             if (e < count) v[e] = p[e];
     }
-    const float alpha = g.alpha ? *g.alpha : 1.0f;
+    const float alpha = g.row_alpha ? g.row_alpha[m] : g.alpha ? *g.alpha : 1.0f;
     T o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = (T)(v[e] * alpha);

@@ -36,7 +36,7 @@ struct XentLayout {
     int64_t count, map, rank, lse;                  // kept
     int64_t powers, ldp;                            // kept as well, or -1; then so are hit and part
     int64_t x, hit, each, part, w;                  // forward's scratch; w: on lines, -1: read where it is
-    int64_t x2, coef, alpha, dzs, sum, split, w2;   // backward's
+    int64_t x2, coef, alpha, row_alpha, back, dzs, sum, split, w2;  // backward's
     int64_t split_bytes[2];                         // of dx's and dw's launches, which use the same room
     int64_t bytes[3];
 };
@@ -88,6 +88,8 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
     l.x2 = take(2, 2 * padded * l.ldx);
     l.coef = take(2, 4 * M);
     l.alpha = take(2, 4);
+    l.row_alpha = take(2, 4 * M);
+    l.back = take(2, 4 * M);
     l.dzs = take(2, 2 * padded * l.ldz);
     if (keep & TGEMM_KEEP_X) {
         // the sums over several pieces are not shared out as well
@@ -328,6 +330,7 @@ struct CoefArgs {
     const int64_t* target;
     const float* dloss;
     float *coef, *alpha;
+    float *row_alpha, *back;  // not NULL: rows have scales of their own
     int32_t reduction;
 };
 
@@ -339,6 +342,12 @@ struct CoefArgs {
 // power of two alone, an unlikely target's element is the factor itself, and its
 // rounding, the same in every row, does not average out of dx and dw
 // (8192x4096x128256: 3.5e-3 of their norm, now 1.8e-3).
+//
+// In float16 a row whose factor is 2^-25 of the largest would have no normal number
+// left in dz, though its dx may hold it (reduction "none").  Where rows have scales
+// of their own, each factor is brought to 2^13 .. 2^14 by a power of two more, 2^k;
+// dx's product takes it out again, row_alpha = alpha 2^-k, and dz is multiplied by
+// back = 2^-k before dw's, which adds rows up.
 __device__ __forceinline__ void xent_factors(const CoefArgs& g) {
     __shared__ float held[16];
     const int M = *g.count;
@@ -361,7 +370,29 @@ __device__ __forceinline__ void xent_factors(const CoefArgs& g) {
     for (int w = 0; w < 16; ++w) most = fmaxf(most, held[w]);
     if (most == 0.0f) most = 1.0f;
     const int low = ilogbf(most) + 100, e = low < 14 ? low : 14;  // alpha is a normal number
-    for (int m = threadIdx.x; m < M; m += 1024) g.coef[m] = ldexpf(of(m) / most, e);
+    int top;
+    const float top_part = frexpf(most, &top);
+    for (int m = threadIdx.x; m < M; m += 1024) {
+        const float c = of(m);
+        if (!g.row_alpha) {
+            g.coef[m] = ldexpf(c / most, e);
+            continue;
+        }
+        float r = c / most;
+        int k = 0;
+        if (c != 0.0f && fabsf(c) < INFINITY) {
+            int at;
+            r = frexpf(c, &at) / top_part;  // c / most = r 2^-k
+            k = top - at;
+            if (fabsf(r) > 1.0f) {
+                r *= 0.5f;
+                --k;
+            }
+        }
+        g.coef[m] = ldexpf(r, e);
+        g.row_alpha[m] = ldexpf(most, -e - k);
+        g.back[m] = ldexpf(1.0f, -k);
+    }
     if (threadIdx.x == 0) *g.alpha = ldexpf(most, -e);
 }
 
@@ -441,6 +472,37 @@ __global__ __launch_bounds__(256) void xent_powers_kernel(PowersArgs g) {
                 v[e] = zero ? 0.0f : e == t ? one[r] : power_of<T>(e & 1 ? two >> 16 : two) * f;
             }
             store8(to + c, v);
+        }
+    }
+}
+
+struct BackArgs {
+    int32_t n, chunks;  // columns; workgroups of 16 rows
+    int64_t ldz;
+    const int32_t* count;
+    const float* back;
+    void* dz;
+};
+
+// dz from the rows' own scales to the common one, where they differ: 16 rows and
+// 2048 columns a workgroup.
+template <class T>
+__global__ __launch_bounds__(256) void xent_back_kernel(BackArgs g) {
+    const int M = *g.count, group = (int)blockIdx.x / g.chunks, c0 = 2048 * ((int)blockIdx.x - group * g.chunks), c1 = min(c0 + 2048, g.n);
+    for (int r = wave_id(); r < 16; r += 4) {
+        const int m = 16 * group + r;
+        if (m >= M) return;
+        const float f = g.back[m];
+        if (f == 1.0f) continue;
+        T* row = static_cast<T*>(g.dz) + (int64_t)m * g.ldz;  // whole up to its stride
+        for (int c = c0 + 8 * lane_id(); c < c1; c += 512) {
+            Raw8 raw;
+            load8<T>(raw, row + c);
+            float v[8];
+            values8<T>(v, raw);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= f;
+            store8(row + c, v);
         }
     }
 }
@@ -548,7 +610,10 @@ int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const vo
     const int32_t *count = reinterpret_cast<const int32_t*>(v + l.count), *map = reinterpret_cast<const int32_t*>(v + l.map);
     float *coef = reinterpret_cast<float*>(s + l.coef), *alpha = reinterpret_cast<float*>(s + l.alpha);
     const char* wp = static_cast<const char*>(w);
-    CoefArgs c{V, count, map, target, dloss, coef, alpha, reduction};
+    // rows' own scales: dx's alone, and needed where they differ and the type is short of range
+    const bool own = kx && reduction == TGEMM_NONE && dtype == TGEMM_F16;
+    float *row_alpha = own ? reinterpret_cast<float*>(s + l.row_alpha) : nullptr, *back = own ? reinterpret_cast<float*>(s + l.back) : nullptr;
+    CoefArgs c{V, count, map, target, dloss, coef, alpha, row_alpha, back, reduction};
     GatherArgs into{M, K, ldx, l.ldx, lddx, static_cast<const uint16_t*>(x), reinterpret_cast<uint16_t*>(s + l.x2), nullptr,
                     kx ? static_cast<uint16_t*>(dx) : nullptr, count, reinterpret_cast<const int32_t*>(v + l.rank)};
     void* both[] = {&c, &into};
@@ -556,6 +621,7 @@ int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const vo
     const bool pieces = l.cols < V;
     MmStoreArgs into_x{}, into_w{};
     into_x.alpha = into_w.alpha = alpha;
+    into_x.row_alpha = row_alpha;
     into_x.rows = into_w.rows = count;
     into_x.jobs = into_w.jobs = 1;
     into_x.map = map;
@@ -594,6 +660,11 @@ int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const vo
                                               wv == s + l.w2}, {}},
                                   1, {}, dx, lddx, pieces ? reinterpret_cast<float*>(s + l.sum) : nullptr, v0 > 0};
             rc = mm_store(dtype, pieces ? FORM_NN_SUM : FORM_NN, l.dx, into_x, st);
+        }
+        if (rc == TGEMM_OK && kw && own && M > 0 && n > 0) {
+            const int64_t chunks = (n + 2047) / 2048;
+            BackArgs a{(int32_t)n, (int32_t)chunks, l.ldz, count, back, s + l.dzs};
+            rc = mm_launch(reinterpret_cast<const void*>(xent_back_kernel<_Float16>), chunks * ((M + 15) / 16), 256, &a, "scales of the rows", st);
         }
         if (rc == TGEMM_OK && kw && n > 0) {
             into_w.job[0] = MmJob{{MmOperands{s + l.dzs, s + l.x2, nullptr, 2 * l.ldz, 2 * l.ldx, 0, (int32_t)n, (int32_t)K,
