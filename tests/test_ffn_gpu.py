@@ -250,3 +250,55 @@ def test_refusals_on_the_gpu():
             tl.gated_ffn(*bad)
     with pytest.raises(ValueError, match="one GPU"):
         tl.gated_ffn(x, wg, wu.cpu(), wd)
+
+
+CLOSED = {"silu": (10.0, 20.0), "gelu": (3.0, 5.4), "gelu_tanh": (3.0, 4.6)}
+
+
+@pytest.mark.parametrize("needs", [(True,) * 4, (True, False, False, False), (False, True, False, False), (False, False, True, False),
+                                   (False, True, True, True), (False, True, False, True), (False, False, True, True)])
+@pytest.mark.parametrize("act", list(CLOSED))
+def test_gradients_of_closed_gates_in_float16(act, needs):
+    """act(g) and act'(g) u of closed gates are below float16's normal numbers (silu(-20) -4e-8); a scaled loss makes their
+    products with dh numbers that the type holds, to its precision."""
+    M, F, t = 40, 200, torch.float16
+    lo, hi = CLOSED[act]
+    gate = -torch.linspace(lo, hi, F, device="cuda").to(t)
+    dy = (torch.rand(M, F, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda") * 4000 + 4000).to(t)
+    one = lambda *s: torch.ones(*s, dtype=t, device="cuda")  # noqa: E731
+    got = run([one(M, 1), gate[:, None], one(F, 1), torch.eye(F, dtype=t, device="cuda")], dy, act, needs)
+    g = gate.double()
+    a, d, _ = ref.act(g, act)
+    da, dd = dy.double() * a, dy.double() * d
+    assert da.abs().min() > 2.0 ** -14 and dd.abs().min() > 2.0 ** -14 and a.abs().min() < 2.0 ** -14
+    # dg and du are rounded once, then the results; sums of 40 and the activation: 2^-15
+    near = 2.0 ** -11 * 2 + 2.0 ** -15
+    if needs[2]:
+        want = da.sum(0)
+        assert ((got["dw_up"][:, 0].double() - want).abs() <= near * want.abs()).all()
+    if needs[1]:
+        want = dd.sum(0)
+        assert ((got["dw_gate"][:, 0].double() - want).abs() <= near * want.abs()).all()
+    if needs[3]:  # h itself is an operand in float16
+        want, size = (dy.double().t() @ a.expand(M, F).contiguous()), dy.double().sum(0)[:, None]
+        assert ((got["dw_down"].double() - want).abs() <= near * want.abs() + 2.0 ** -25 * size).all()
+    if needs[0]:
+        want = dd @ g[:, None] + da.sum(1, keepdim=True)
+        size = dd.abs() @ g.abs()[:, None] + da.abs().sum(1, keepdim=True)
+        assert ((got["dx"].double() - want).abs() <= (2.0 ** -11 + 2.0 ** -14) * size + 2.0 ** -11 * want.abs()).all()
+
+
+def test_projections_beyond_float16():
+    """u = 2.4e5: act'(g) u has no place in the type, its product with a small dy has."""
+    t = torch.float16
+    gate = torch.tensor([-6e4, -30.0, -17.0, 17.0, 30.0, 200.0], dtype=t, device="cuda")
+    F = gate.numel()
+    up = torch.full((F, 1), 6e4, dtype=t, device="cuda")
+    x, eye, dy = torch.full((40, 1), 4.0, dtype=t, device="cuda"), torch.eye(F, dtype=t, device="cuda"), torch.full((40, F), 2.0 ** -12, dtype=t, device="cuda")
+    u = 4 * float(up[0, 0])
+    for act in tl.ACTIVATIONS:
+        got = run([x, gate[:, None], up, eye], dy, act, (False, True, True, False))
+        a, d, _ = ref.act(4 * gate.double(), act)
+        for name, want in {"dw_gate": 160 * 2.0 ** -12 * d * u, "dw_up": 160 * 2.0 ** -12 * a}.items():
+            # two roundings; g and u in 24 bits, the activation and 40 additions: 2^-14
+            assert ((got[name][:, 0].double() - want).abs() <= (2 * 2.0 ** -11 + 2.0 ** -14) * want.abs() + 160 * 2.0 ** -25).all(), (act, name)

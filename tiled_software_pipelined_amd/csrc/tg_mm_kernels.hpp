@@ -76,20 +76,60 @@ struct MmStoreArgs {
 struct MmGateArgs {
     MmOperands op;
     MmGrid grid;
-    void *h, *a, *b;  // M x N, row stride ld: act(g) u, act(g), act'(g) u; a and b NULL where they
-                      // are not kept.  Anything may be written between N and ld
+    // M x N, row stride ld; anything may be written between N and ld.  h: act(g) u.
+    // bfloat16: a act(g), b act'(g) u, each NULL where it is not kept, low NULL.
+    // float16: Kept24 of g and u, all NULL where they are not kept
+    void *h, *a, *b, *low;
     int64_t ld;
     int32_t act;
 };
-// ---- its backward: dh = dy Wd, then du = dh a and dg = dh b ----------------------
+// ---- its backward: dh = dy Wd, then du = dh act(g) and dg = dh act'(g) u ---------
 struct MmDhArgs {
     MmOperands op;
     MmGrid grid;
-    const void *a, *b;  // both of them there: a branch at each load costs 70 us of 4096x4096x11008's 480
-    void *dg, *du;      // M x N, row stride ld (a's and b's too); either NULL where it is not wanted.
-                        // Anything may be written between N and ld
+    // all of them there (low: in float16): a branch at each load costs 70 us of 4096x4096x11008's 480
+    const void *a, *b, *low;
+    void *dg, *du;  // M x N, row stride ld (a's, b's, low's and h's too); either NULL where it is not wanted.
+                    // Anything may be written between N and ld
+    void* h;        // float16: act(g) u again, rounded; NULL where it is not wanted
     int64_t ld;
+    int32_t act;
 };
+
+// g and u in 24 bits each, for a backward pass in float16: a sign, float's 8 bits
+// of exponent and 15 behind the point (off by 2^-16), the upper halves of eight g,
+// those of eight u, and a byte more of each.  act(g) and act'(g) u of a closed gate
+// are below float16's normal numbers and would lose their digits in it (silu(-18)
+// 9 % of it, silu(-21) all), though a scaled loss's dh makes numbers of them that
+// it holds; from g they are made in float.
+struct Kept24 {
+    i32x4 g, u, low;
+    __device__ static __forceinline__ uint32_t rounded(float v) {
+        // a NaN's bits could be carried over into a number's
+        return v != v ? 0x7fc00000u : __builtin_bit_cast(uint32_t, v) + 0x80u;
+    }
+    __device__ __forceinline__ void set(const float (&gs)[8], const float (&us)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t g0 = rounded(gs[2 * i]), g1 = rounded(gs[2 * i + 1]), u0 = rounded(us[2 * i]), u1 = rounded(us[2 * i + 1]);
+            g[i] = (int)__builtin_amdgcn_perm(g1, g0, 0x07060302u);
+            u[i] = (int)__builtin_amdgcn_perm(u1, u0, 0x07060302u);
+            // the bytes below: of g0, u0, g1, u1
+            low[i] = (int)__builtin_amdgcn_perm(__builtin_amdgcn_perm(u1, g1, 0x0c0c0501u), __builtin_amdgcn_perm(u0, g0, 0x0c0c0501u), 0x05040100u);
+        }
+    }
+    __device__ __forceinline__ void get(float (&gs)[8], float (&us)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            gs[2 * i] = __builtin_bit_cast(float, __builtin_amdgcn_perm((uint32_t)g[i], (uint32_t)low[i], 0x0504000cu));
+            gs[2 * i + 1] = __builtin_bit_cast(float, __builtin_amdgcn_perm((uint32_t)g[i], (uint32_t)low[i], 0x0706020cu));
+            us[2 * i] = __builtin_bit_cast(float, __builtin_amdgcn_perm((uint32_t)u[i], (uint32_t)low[i], 0x0504010cu));
+            us[2 * i + 1] = __builtin_bit_cast(float, __builtin_amdgcn_perm((uint32_t)u[i], (uint32_t)low[i], 0x0706030cu));
+        }
+    }
+};
+template <class T>
+constexpr bool KEEPS_24 = __is_same(T, _Float16);
 
 // ---- cross entropy ---------------------------------------------------------------
 // Rows of x are those that count, gathered; how many only the device knows.
@@ -466,7 +506,16 @@ __global__ __launch_bounds__(G::NT) void mm_gate_kernel(MmGateArgs g) {
                 if (inside.value || out.count(u) > 0) store8(out.at(static_cast<T*>(p), u), x);
             };
             float a[8], d[8];
-            if (g.a || g.b) {  // for the backward pass: past the caches
+            if (KEEPS_24<T> && g.low) {  // for the backward pass: past the caches
+                Kept24 k;
+                k.set(v, w);
+                if (inside.value || out.count(u) > 0) {
+                    __builtin_nontemporal_store(k.g, reinterpret_cast<i32x4*>(out.at(static_cast<T*>(g.a), u)));
+                    __builtin_nontemporal_store(k.u, reinterpret_cast<i32x4*>(out.at(static_cast<T*>(g.b), u)));
+                    __builtin_nontemporal_store(k.low, reinterpret_cast<i32x4*>(out.at(static_cast<T*>(g.low), u)));
+                }
+                activate8<false>(g.act, v, a, d);
+            } else if (!KEEPS_24<T> && (g.a || g.b)) {
                 auto keep = [&](void* p, F8 x) {
                     if (p && (inside.value || out.count(u) > 0)) stream8(out.at(static_cast<T*>(p), u), x);
                 };
@@ -499,25 +548,42 @@ __global__ __launch_bounds__(G::NT) void mm_dh_kernel(MmDhArgs g) {
     const MmOut<G> out(at, g.op.M, (int)g.ld, g.ld);  // rows whole up to their stride: no edge inside them
     typedef float(&F8)[8];
     struct Kept {
-        Raw8 a, b;
+        Raw8 a, b, low;
     };
     auto way = [&](auto inside) {
         G::template each_row<Kept>(acc, smem, at.lane, at.wave, [&](int u, Kept& k) {
             if (inside.value || out.count(u) > 0) {
                 load8(k.a, out.at(static_cast<const T*>(g.a), u));
                 load8(k.b, out.at(static_cast<const T*>(g.b), u));
+                if constexpr (KEEPS_24<T>) load8(k.low, out.at(static_cast<const T*>(g.low), u));
             }
         }, [&](int u, F8 v, F8, Kept& k) {
-            // roundings of du and dg: operands of the products that follow
-            auto put = [&](void* p, const Raw8& raw) {
-                float x[8];
-                values8<T>(x, raw);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= v[e];
+            // roundings of du, dg and h: operands of the products that follow
+            auto put = [&](void* p, F8 x) {
                 if (inside.value || out.count(u) > 0) store8(out.at(static_cast<T*>(p), u), x);
             };
-            if (g.du) put(g.du, k.a);
-            if (g.dg) put(g.dg, k.b);
+            float a[8], b[8];
+            if constexpr (KEEPS_24<T>) {
+                float gate[8], up[8], h[8];
+                Kept24{k.a.v, k.b.v, k.low.v}.get(gate, up);
+                activate8<true>(g.act, gate, a, b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    b[e] *= up[e];
+                    h[e] = a[e] * up[e];
+                }
+                if (g.h) put(g.h, h);
+            } else {
+                values8<T>(a, k.a);
+                values8<T>(b, k.b);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                a[e] *= v[e];
+                b[e] *= v[e];
+            }
+            if (g.du) put(g.du, a);
+            if (g.dg) put(g.dg, b);
         });
     };
     if (out.inside()) way(Yes{});
