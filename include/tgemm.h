@@ -480,7 +480,9 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
  *
  * bfloat16 or float16 operands (`dtype`, the same for every tensor of a call),
  * row-major with leading dimensions, float sums on the matrix cores.  Sizes that
- * are contracted and leading dimensions: up to 2^22; rows up to 2^30.  Operands may
+ * are contracted and leading dimensions: up to 2^22; rows up to 2^30, those of the
+ * loss up to 2^26 - 128, as far as grids (2^32 - 1 threads) hold a call's launches:
+ * one that they do not hold is refused before anything is queued.  Operands may
  * start at any element.  Outputs must not overlap anything else. */
 
 /* The gated feed-forward block, for x (M x K), wg and wu (F x K), wd (N x F):

@@ -125,6 +125,31 @@ def test_xent_sizes():
     assert tl._lib.tgemm_xent_bytes(4, 2 ** 28 + 1, 16, 8, n) == -1 and tl._lib.tgemm_xent_bytes(0, 9, 8, 11, n) == 0
 
 
+MOST_ROWS = 2 ** 26 - 128
+
+
+@pytest.mark.parametrize("call", [
+    lambda: fwd(M=2 ** 30, F=2 ** 20), lambda: fwd(M=2 ** 30, F=8, N=2 ** 22, keep=0), lambda: fwd(M=2 ** 20, K=2 ** 22, F=2 ** 22, N=8, keep=2),
+    lambda: bwd(M=2 ** 30, F=2 ** 20), lambda: bwd(M=2 ** 20, K=2 ** 22, F=2 ** 22, keep=2), lambda: bwd(M=2 ** 30, K=2 ** 22, keep=1),
+    lambda: xf(M=MOST_ROWS, V=2 ** 20), lambda: xf(M=2 ** 20, V=2 ** 30), lambda: xf(M=MOST_ROWS, V=2 ** 28, keep=8), lambda: xf(M=MOST_ROWS + 1),
+    lambda: xb(M=MOST_ROWS, V=2 ** 20, keep=11), lambda: xb(M=2 ** 24, V=9000, K=2 ** 22, keep=1), lambda: xb(M=2 ** 26, V=8)])
+def test_launches_that_no_grid_holds_are_refused_first(call):
+    """Before the device is looked at, and so before anything is queued."""
+    assert call() == -1 and ("too many tiles" in tl.last_error() or "out of range" in tl.last_error())
+
+
+def test_launches_that_a_grid_holds():
+    """Without a device the calls end where it is looked for, with their arguments found right."""
+    n = (ctypes.c_int64 * 3)()
+    assert tl._lib.tgemm_xent_bytes(MOST_ROWS, 64, 8, 3, n) == 0 and tl._lib.tgemm_xent_bytes(MOST_ROWS + 1, 64, 8, 3, n) == -1
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    calls = [lambda: xf(M=MOST_ROWS, V=64), lambda: xb(M=MOST_ROWS, V=64), lambda: xf(M=1, V=2 ** 30, K=7), lambda: xb(M=1, V=2 ** 30, K=7),
+             lambda: xf(M=800, V=2 ** 27, K=7), lambda: fwd(M=2 ** 28, K=7, F=8, N=8), lambda: bwd(M=2 ** 28, K=7, F=8, N=8)]
+    codes = {c() for c in calls}
+    assert len(codes) == 1 and -1 not in codes
+
+
 def clip(tensors=2, counts=(5, 7), dtypes=(0, 1), ins=(64, 128), outs=(64, 128), max_norm=1.0, eps=1e-6, norm=A, ws=A, size=1 << 20):
     p = lambda v: None if v is None else (P * len(v))(*v)  # noqa: E731
     return tl._lib.tgemm_clip(tensors, p(ins), p(outs), (ctypes.c_int64 * len(counts))(*counts), (ctypes.c_int32 * len(dtypes))(*dtypes),

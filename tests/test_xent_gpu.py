@@ -514,3 +514,17 @@ def test_rows_factors_of_all_sizes_serve_dw():
         one = w.detach().requires_grad_()
         (alone,) = torch.autograd.grad(tl.linear_cross_entropy(x, one, t, reduction="none", keep_bytes=keep), one, by)
         ref.check({"dw": alone}, ref.xent(x, w, t, reduction="none", dloss=by), ("dw",))
+
+
+def test_as_many_rows_as_a_grid_holds():
+    """A wave for each row: 2^26 - 128 of them."""
+    M, V, K = 2 ** 26 - 128, 40, 8
+    x, w, t = make(M, V, K, torch.bfloat16)
+    some = torch.cat([torch.arange(0, M, 200003, device="cuda"), torch.arange(M - 300, M, device="cuda")])
+    one = x.requires_grad_()
+    loss = tl.linear_cross_entropy(one, w, t, reduction="none")
+    (dx,) = torch.autograd.grad(loss, one, torch.ones((), device="cuda").expand(M))
+    want = ref.xent(x.detach()[some], w, t[some], reduction="none", dloss=1.0)
+    ref.check({"loss": loss.detach()[some], "dx": dx[some]}, want, ("loss", "dx"))
+    with pytest.raises(tl.TgemmError, match="out of range"):
+        tl.linear_cross_entropy(x.detach()[:1].expand(M + 1, K), w, t[:1].expand(M + 1))

@@ -46,7 +46,8 @@ static FfnLayout ffn_layout(int64_t M, int64_t K, int64_t F, int64_t N, int dtyp
     l.ld = (F + 63) / 64 * 64;
     const int64_t inner = 2 * M * l.ld;
     const MmShape y{M, N}, x{M, K}, dw[3] = {{F, K}, {F, K}, {N, F}};
-    const bool pack_k = mm_packs(K, M), pack_f = mm_packs(F, M);
+    // as far as a launch of a wave a row reaches
+    const bool pack_k = mm_packs(K, M) && M + 2 * F <= MM_WAVE_ROWS, pack_f = mm_packs(F, M);
     l.gate = mm_size(FORM_GATE, M, F, mm_slices(K), false, pack_k ? 0 : K);
     l.down = mm_size(FORM_NT, M, N, mm_slices(F), true, pack_f ? 0 : F);
     l.x = l.wg = l.wu = l.wd = -1;
@@ -98,6 +99,22 @@ static bool ffn_sizes_ok(int64_t M, int64_t K, int64_t F, int64_t N, int32_t kee
         return false;
     }
     return true;
+}
+
+// Whether grids hold the launches of the backward pass (forward: those of both).
+static int ffn_check_grids(const FfnLayout& l, int64_t M, int64_t K, int64_t F, int64_t N, int keep, bool forward) {
+    int rc = TGEMM_OK;
+    if (M == 0) return rc;
+    if (forward && !l.rows) {
+        rc = mm_check_tiles("gate and up projections", FORM_GATE, l.gate, M, F);
+        if (rc == TGEMM_OK) rc = mm_check_tiles("down projection", FORM_NT, l.down, M, N);
+    }
+    if (rc == TGEMM_OK && (keep & FFN_INNER)) rc = mm_check_tiles("gradient of the inner values", FORM_DH, l.dh, M, F);
+    if (rc == TGEMM_OK && (keep & TGEMM_FFN_X)) rc = mm_check_tiles("gradient of x", FORM_NN, l.dx, M, K);
+    const MmShape dw[3] = {{F, K}, {F, K}, {N, F}};
+    if (rc == TGEMM_OK && (keep & (TGEMM_FFN_GATE | TGEMM_FFN_UP | TGEMM_FFN_DOWN)))
+        rc = mm_check_tiles("gradients of the weights", FORM_TN, l.dw, dw, 3);
+    return rc;
 }
 
 static int ffn_common(int32_t dtype, int32_t act) {
@@ -158,6 +175,7 @@ int tgemm_ffn_forward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype,
     if (rc == TGEMM_OK) rc = mm_check("y", y, M, N, ldy);
     if (rc == TGEMM_OK) rc = mm_check_buffer("saved", saved, l.bytes[0]);
     if (rc == TGEMM_OK) rc = mm_check_buffer("scratch", scratch, l.bytes[1]);
+    if (rc == TGEMM_OK) rc = ffn_check_grids(l, M, K, F, N, keep, true);
     if (rc == TGEMM_OK && M > 0) rc = current_device_ok();
     if (rc != TGEMM_OK) return rc;
     const hipStream_t st = static_cast<hipStream_t>(stream);
@@ -231,6 +249,7 @@ int tgemm_ffn_backward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype
     if (rc == TGEMM_OK && (keep & TGEMM_FFN_DOWN)) rc = mm_check("dw_down", dwd, N, F, lddwd);
     if (rc == TGEMM_OK) rc = mm_check_buffer("saved", saved, l.bytes[0]);
     if (rc == TGEMM_OK) rc = mm_check_buffer("scratch", scratch, l.bytes[2]);
+    if (rc == TGEMM_OK) rc = ffn_check_grids(l, M, K, F, N, keep, false);
     if (rc == TGEMM_OK && keep && (M > 0 || F > 0)) rc = current_device_ok();
     if (rc != TGEMM_OK) return rc;
     const hipStream_t st = static_cast<hipStream_t>(stream);

@@ -123,11 +123,23 @@ MmGrid mm_grid(const MmKernel& k, int64_t M, int64_t N) {
     return MmGrid{(int32_t)((M + k.bm - 1) / k.bm), (int32_t)((N + k.bn - 1) / k.bn)};
 }
 
-int mm_launch_list(const void* fn, int64_t workgroups, int threads, void** args, const char* name, hipStream_t stream) {
-    if (workgroups > INT_MAX || !grid_fits((double)workgroups, threads)) {
+int mm_check_grid(const char* name, double workgroups, int threads) {
+    if (workgroups > INT_MAX || !grid_fits(workgroups, threads)) {
         set_error("%s: too many tiles", name);
         return TGEMM_E_ARG;
     }
+    return TGEMM_OK;
+}
+
+int mm_check_tiles(const char* name, int form, MmSize size, const MmShape* shapes, int jobs) {
+    const MmKernel& k = mm_kernels(TGEMM_BF16, form)[size];
+    // `slots` more: parts of tiles that a launch shares out
+    return mm_check_grid(name, tiles_of(k, shapes, jobs) + k.slots, k.threads);
+}
+
+int mm_launch_list(const void* fn, int64_t workgroups, int threads, void** args, const char* name, hipStream_t stream) {
+    const int rc = mm_check_grid(name, (double)workgroups, threads);
+    if (rc != TGEMM_OK) return rc;
     const hipError_t err = hipLaunchKernel(fn, dim3((unsigned)workgroups), dim3(threads), args, 0, stream);
     if (err != hipSuccess) {
         set_error("launch of %s failed: %s", name, hipGetErrorString(err));

@@ -13,6 +13,9 @@ namespace tg {
 // reaches 255 rows past its tile's first by a 32-bit byte offset.
 constexpr int64_t MM_MOST = INT64_C(1) << 22;
 constexpr int64_t MM_MOST_ROWS = INT64_C(1) << 30;
+// Rows that a launch with a wave for each reaches (a grid holds 2^32 - 1 threads),
+// with some workgroups to spare.
+constexpr int64_t MM_WAVE_ROWS = (INT64_C(1) << 26) - 128;
 
 const MmKernel* mm_kernels(int dtype, int form);
 inline int64_t mm_slices(int64_t K) { return (K + 63) / 64; }
@@ -48,6 +51,14 @@ int mm_pack(const MmPack* list, int count, hipStream_t stream);
 int64_t mm_split_bytes(int form, MmSize size, const MmShape* shapes, int jobs, int64_t slices, bool fewer);
 
 MmGrid mm_grid(const MmKernel& k, int64_t M, int64_t N);
+// TGEMM_OK where a grid holds a launch: the entry points ask for all of theirs
+// before the first.
+int mm_check_grid(const char* name, double workgroups, int threads);
+int mm_check_tiles(const char* name, int form, MmSize size, const MmShape* shapes, int jobs);
+inline int mm_check_tiles(const char* name, int form, MmSize size, int64_t M, int64_t N) {
+    const MmShape s{M, N};
+    return mm_check_tiles(name, form, size, &s, 1);
+}
 
 // Launches products of the store forms on tiles of one size, and the join of
 // what it shares out; jobs without rows or columns are left out.

@@ -58,7 +58,7 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
     l.map = take(0, 4 * M);   // where they stand
     l.rank = take(0, 4 * M);  // each row's number among them, -1
     l.lse = take(0, 8 * M);   // of each of them
-    const bool pack = mm_packs(K, M);
+    const bool pack = mm_packs(K, M) && V <= MM_WAVE_ROWS;  // as far as a launch of a wave a row reaches
     l.ldx = mm_lines(K);
     l.w = l.w2 = -1;
     l.stats = mm_size(FORM_STATS, M, V, mm_slices(K), false, pack ? 0 : K);
@@ -107,12 +107,31 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
 }
 
 static bool xent_sizes_ok(int64_t M, int64_t V, int64_t K, int32_t keep) {
-    if (M < 0 || V < 0 || K < 0 || M > MM_MOST_ROWS || V > MM_MOST_ROWS || K > MM_MOST ||
+    if (M < 0 || V < 0 || K < 0 || M > MM_WAVE_ROWS || V > MM_MOST_ROWS || K > MM_MOST ||
         (keep & ~(TGEMM_KEEP_X | TGEMM_KEEP_W | TGEMM_KEEP_POWERS)) || ((keep & TGEMM_KEEP_POWERS) && V > MOST_POWERS)) {
         set_error("M=%lld V=%lld K=%lld keep=%d out of range", (long long)M, (long long)V, (long long)K, keep);
         return false;
     }
     return true;
+}
+
+// Workgroups of a row in the pass over the powers.
+static int64_t powers_chunks(const XentLayout& l) { return (l.ldz + 16 * wave_cols(l.stats) - 1) / (16 * wave_cols(l.stats)); }
+// Whether grids hold the launches of the backward pass.
+static int xent_check_grids(const XentLayout& l, int64_t M, int64_t V, int64_t K, int keep) {
+    int rc = TGEMM_OK;
+    if (!(keep & (TGEMM_KEEP_X | TGEMM_KEEP_W))) return rc;
+    const int64_t cols = l.cols < V ? l.cols : V;
+    rc = l.powers >= 0 ? mm_check_grid("gradient of the logits", (double)powers_chunks(l) * (double)((M + 63) / 64 * 4), 256)
+                       : mm_check_tiles("gradient of the logits", FORM_DZ, l.dz, M, cols);
+    // scales of the rows: no more workgroups than 16 rows and 1024 columns make
+    if (rc == TGEMM_OK) rc = mm_check_grid("gradient of the logits", (double)((cols + 1023) / 1024) * (double)((M + 15) / 16), 256);
+    if (rc == TGEMM_OK && (keep & TGEMM_KEEP_X)) {
+        rc = mm_check_tiles("gradient of x", l.cols < V ? FORM_NN_SUM : FORM_NN, l.dx, M, K);
+        if (rc == TGEMM_OK && l.cols < V) rc = mm_check_grid("gradient of x", (double)M * (double)((K + 3) / 4) / 256 + 1, 256);
+    }
+    if (rc == TGEMM_OK && (keep & TGEMM_KEEP_W)) rc = mm_check_tiles("gradient of w", FORM_TN, l.dw, cols, K);
+    return rc;
 }
 
 static int xent_common(int32_t dtype, int32_t reduction, const void* target, int64_t M) {
@@ -536,6 +555,7 @@ int tgemm_xent_forward(int64_t M, int64_t V, int64_t K, int32_t dtype, const voi
     if (rc == TGEMM_OK) rc = check_floats("loss", loss, reduction == TGEMM_NONE ? M : 1);
     if (rc == TGEMM_OK) rc = mm_check_buffer("saved", saved, l.bytes[0]);
     if (rc == TGEMM_OK) rc = mm_check_buffer("scratch", scratch, l.bytes[1]);
+    if (rc == TGEMM_OK && M > 0 && V > 0) rc = mm_check_tiles("logits", FORM_STATS, l.stats, M, V);
     if (rc == TGEMM_OK) rc = current_device_ok();
     if (rc != TGEMM_OK) return rc;
     const hipStream_t st = static_cast<hipStream_t>(stream);
@@ -598,6 +618,7 @@ int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const vo
     if (rc == TGEMM_OK) rc = check_floats("dloss", dloss, reduction == TGEMM_NONE ? M : 1);
     if (rc == TGEMM_OK) rc = mm_check_buffer("saved", saved, l.bytes[0]);
     if (rc == TGEMM_OK) rc = mm_check_buffer("scratch", scratch, l.bytes[2]);
+    if (rc == TGEMM_OK) rc = xent_check_grids(l, M, V, K, keep);
     if (rc == TGEMM_OK && (kx || kw) && (M > 0 || V > 0)) rc = current_device_ok();
     if (rc != TGEMM_OK) return rc;
     if (!kx && !kw) {
@@ -641,7 +662,7 @@ int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const vo
         }
         if (rc == TGEMM_OK && M > 0 && n > 0 && l.powers >= 0) {
             const int wide = wave_cols(l.stats);
-            const int64_t chunks = (l.ldz + 16 * wide - 1) / (16 * wide);
+            const int64_t chunks = powers_chunks(l);
             PowersArgs a{(int32_t)V, (int32_t)n, wide, (int32_t)chunks, M, v0, l.ldp, l.ldz, count, map, target,
                          reinterpret_cast<const float2*>(v + l.part), reinterpret_cast<const float*>(v + l.hit), coef,
                          reinterpret_cast<const float2*>(v + l.lse), reinterpret_cast<const uint16_t*>(v + l.powers), s + l.dzs};
