@@ -571,9 +571,9 @@ int tgemm_xent_backward(int64_t M, int64_t V, int64_t K, int32_t dtype, const vo
  * out[i] = in[i] min(1, max_norm / (norm + eps)), the factor rounded to float and
  * the product to the tensor's type.  Tensor i has counts[i] adjacent elements of
  * type dtypes[i] (TGEMM_F32, TGEMM_BF16, TGEMM_F16); out[i] may be in[i], and
- * otherwise must not overlap any tensor; no tensor may be given twice.  A norm of
- * infinity makes the factor zero (infinite elements become NaN), a NaN makes
- * everything NaN.  in, out, counts, dtypes are host arrays, read during the call.
+ * otherwise shares no element with any tensor (refused).  A norm of infinity makes
+ * the factor zero (infinite elements become NaN), a NaN makes everything NaN, as do
+ * quotients that have no value (max_norm infinite as well; 0 / 0).  in, out, counts, dtypes are host arrays, read during the call.
  * workspace: tgemm_clip_workspace_bytes(tensors, counts) bytes (-1 for sizes out of
  * range: 2^40 elements in all) of device memory, 256-byte aligned, overwritten.
  * Returns TGEMM_OK or a TGEMM_E_* code. */

@@ -166,3 +166,28 @@ def test_a_training_step_of_a_block_and_its_head():
             w -= 0.02 * update
     after = tl.linear_cross_entropy(tl.gated_ffn(x, *weights[:3]), head, target)
     assert after.isfinite()
+
+
+def test_tensors_that_share_elements_are_refused():
+    """Those would be scaled twice; tensors that are only read may share some."""
+    t, far = torch.ones(1000, device="cuda"), torch.ones(1000, device="cuda")
+    for grads, out in (([t[:600], t[500:]], None), ([t, far, t[10:20]], None), ([t.view(torch.bfloat16)[:7], t[3:5]], None),
+                       ([t[:500], far[:500]], [t[100:600], torch.empty(500, device="cuda")]),
+                       ([t[:500], far[:500]], [torch.empty(500, device="cuda"), t[100:600]]),
+                       ([far[:500], far[500:]], [t[:500], t[499:999]])):
+        with pytest.raises(tl.TgemmError, match="overlap"):
+            tl.clip_grad_norm(grads, 1.0, out=out)
+    assert (t == 1).all() and (far == 1).all()
+    parts = [t[:500], t[500:]]
+    assert abs(float(tl.clip_grad_norm(parts, 1.0)) - 1000 ** 0.5) < 1e-4 and abs(float(t.norm()) - 1) < 1e-5
+    t.fill_(1)
+    out = [far[:600], torch.empty(500, device="cuda")]
+    tl.clip_grad_norm([t[:600], t[500:]], 1100 ** 0.5 / 2, out=out)
+    assert (t == 1).all() and all(((o - 0.5).abs() < 1e-6).all() for o in out) and (far[600:] == 1).all()
+
+
+def test_quotients_without_a_value():
+    for value, limit, eps in ((float("inf"), float("inf"), 1e-6), (0.0, 0.0, 0.0)):
+        t = torch.full((7,), value, device="cuda")
+        tl.clip_grad_norm([t], limit, eps)
+        assert t.isnan().all()

@@ -166,6 +166,23 @@ def test_clip_refuses(kw, code):
     assert clip(**kw) == code and tl.last_error()
 
 
+@pytest.mark.parametrize("kw", [
+    dict(ins=(64, 80), outs=(64, 80)), dict(ins=(80, 64), outs=(80, 64), counts=(7, 9)), dict(ins=(64, 128), outs=(64, 140), counts=(32, 7)),
+    dict(ins=(64, 128), outs=(140, 200), counts=(5, 7)), dict(ins=(64, 128), outs=(256, 272)), dict(ins=(64, 128), outs=(60, 128)),
+    dict(tensors=3, ins=(64, 1024, 4096), outs=(64, 1024, 4096), counts=(2000, 1, 1), dtypes=(1, 1, 1))])
+def test_clip_refuses_tensors_that_share_elements(kw):
+    assert clip(**kw) == -1 and "overlap" in tl.last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(ins=(64, 84), outs=(64, 84)), dict(ins=(64, 78), outs=(1024, 2048), dtypes=(1, 1)), dict(ins=(64, 64), outs=(1024, 64), counts=(5, 0)),
+    dict(ins=(64, 128), outs=(128 + 16, 64 + 20))])
+def test_clip_takes_neighbours_and_inputs_that_share_elements(kw):
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    assert clip(**kw) == clip() != -1 and "overlap" not in tl.last_error()
+
+
 def test_clip_sizes():
     c = lambda *v: tl._lib.tgemm_clip_workspace_bytes(len(v), (ctypes.c_int64 * len(v))(*v))  # noqa: E731
     assert c() == 256 and c(0) == 256 and c(1) == 264 and c(8192, 0, 8193) == 256 + 8 * 3 and c(-1) == -1 and c(2 ** 41) == -1

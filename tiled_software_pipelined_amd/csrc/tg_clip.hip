@@ -12,7 +12,9 @@
 // which workgroup ends first.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <climits>
+#include <cstdlib>
 
 #include "tg_device.hpp"
 #include "tg_host.hpp"
@@ -204,6 +206,38 @@ static bool clip_total(int64_t tensors, const int64_t* counts, double* total) {
     return *total <= 1099511627776.0;  // 2^40
 }
 
+// Whether a tensor that is written shares elements with another one: they would be
+// scaled twice, or read half scaled.  Tensors that are only read may.
+static int clip_check_overlap(int64_t tensors, const void* const* in, void* const* out, const int64_t* counts, const int32_t* dtypes) {
+    struct Span {
+        uintptr_t begin, end;
+        bool written;
+    };
+    Span* spans = static_cast<Span*>(std::malloc(sizeof(Span) * 2 * (size_t)tensors + 1));
+    if (!spans) {
+        set_error("no host memory for the table of %lld tensors", (long long)tensors);
+        return TGEMM_E_ARG;
+    }
+    int64_t n = 0;
+    for (int64_t i = 0; i < tensors; ++i) {
+        if (counts[i] == 0) continue;
+        const uintptr_t bytes = (uintptr_t)counts[i] * (dtypes[i] == TGEMM_F32 ? 4 : 2), a = (uintptr_t)in[i], b = (uintptr_t)out[i];
+        spans[n++] = Span{b, b + bytes, true};
+        if (a != b) spans[n++] = Span{a, a + bytes, false};
+    }
+    std::sort(spans, spans + n, [](const Span& x, const Span& y) { return x.begin < y.begin; });
+    uintptr_t any = 0, written = 0;  // where what was passed ends
+    bool overlap = false;
+    for (int64_t i = 0; i < n && !overlap; ++i) {
+        overlap = spans[i].begin < (spans[i].written ? any : written);
+        any = std::max(any, spans[i].end);
+        if (spans[i].written) written = std::max(written, spans[i].end);
+    }
+    std::free(spans);
+    if (overlap) set_error("tensors overlap");
+    return overlap ? TGEMM_E_ARG : TGEMM_OK;
+}
+
 }  // namespace tg
 
 extern "C" {
@@ -254,7 +288,8 @@ int tgemm_clip(int64_t tensors, const void* const* in, void* const* out, const i
             return TGEMM_E_ALIGN;
         }
     }
-    int rc = current_device_ok();
+    int rc = clip_check_overlap(tensors, in, out, counts, dtypes);
+    if (rc == TGEMM_OK) rc = current_device_ok();
     if (rc != TGEMM_OK) return rc;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     float* factor = static_cast<float*>(workspace);

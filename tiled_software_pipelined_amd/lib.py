@@ -1049,11 +1049,12 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None):
 
     grads: one or more float32, bfloat16 or float16 tensors on one GPU, of any
     shapes, dense (their elements fill a block of memory in any order of axes),
-    none of them twice.  Each is multiplied by min(1, max_norm / (norm + eps)) in
+    none of them twice and no two with elements in common.  Each is multiplied by min(1, max_norm / (norm + eps)) in
     place, or into the tensor of ``out`` at its place (same shape, dtype and
-    strides; it may be the same tensor).  Squares are summed in 64 bits; the
+    strides; it may be the same tensor, and shares no element with another).  Squares are summed in 64 bits; the
     product is rounded once.  A norm that is infinite makes the factor zero (and
-    infinities NaN), a NaN makes everything NaN.  Nothing waits for the GPU.  Not
+    infinities NaN), a NaN makes everything NaN, as does a quotient that has no
+    value (``max_norm`` infinite as well; 0 / 0).  Nothing waits for the GPU.  Not
     differentiable.
     """
     grads = list(grads)
