@@ -302,3 +302,14 @@ def test_projections_beyond_float16():
         for name, want in {"dw_gate": 160 * 2.0 ** -12 * d * u, "dw_up": 160 * 2.0 ** -12 * a}.items():
             # two roundings; g and u in 24 bits, the activation and 40 additions: 2^-14
             assert ((got[name][:, 0].double() - want).abs() <= (2 * 2.0 ** -11 + 2.0 ** -14) * want.abs() + 160 * 2.0 ** -25).all(), (act, name)
+
+
+@pytest.mark.parametrize("M,K,F,N", [(0, 8, 8, 8), (4, 0, 8, 8), (4, 8, 0, 8), (4, 8, 8, 0), (40, 0, 8, 8), (40, 8, 0, 8)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_empty_sizes_one_by_one(M, K, F, N, dtype):
+    *leaves, dy = make(M, K, F, N, dtype)
+    got = run(leaves, dy, "silu")
+    assert got["y"].shape == (M, N)
+    assert not got["y"].any()
+    for name, t in zip(NAMES, leaves):
+        assert got[name].shape == t.shape and not got[name].any()
