@@ -528,3 +528,24 @@ def test_as_many_rows_as_a_grid_holds():
     ref.check({"loss": loss.detach()[some], "dx": dx[some]}, want, ("loss", "dx"))
     with pytest.raises(tl.TgemmError, match="out of range"):
         tl.linear_cross_entropy(x.detach()[:1].expand(M + 1, K), w, t[:1].expand(M + 1))
+
+
+@pytest.mark.parametrize("M,V,K,dtype", [
+    (1, 3001, 512, torch.bfloat16), (130, 1000, 520, torch.float16), (700, 2049, 1000, torch.bfloat16), (1030, 4100, 2056, torch.bfloat16),
+    (1030, 4100, 2056, torch.float16), (2050, 9001, 777, torch.float16), (4100, 12000, 513, torch.bfloat16), (70000, 9000, 512, torch.bfloat16)])
+def test_logits_made_again_for_long_rows(M, V, K, dtype):
+    """The backward pass of batches whose powers do not fit: no power is kept though K is at least 512."""
+    x, w, t = make(M, V, K, dtype)
+    some = torch.arange(0, M, max(1, M // 2000), device="cuda")
+    got = run(x, w, t, 100.0, keep_bytes=0)
+    by = 100.0 / int((t != -100).sum())
+    want = ref.xent(x[some], w, t[some], reduction="sum", dloss=by, kept=False)
+    ref.check({"dx": got["dx"][some]}, want, ("dx",))
+    if len(some) == M:
+        ref.check({"dw": got["dw"]}, want, ("dw",))
+    else:  # added up over blocks of rows
+        dw, bound = 0.0, 0.0
+        for rows in torch.arange(M, device="cuda").split(4096):
+            v, b = ref.xent(x[rows], w, t[rows], reduction="sum", dloss=by, kept=False)["dw"]
+            dw, bound = dw + v, bound + b
+        assert ((got["dw"].double() - dw).abs() <= bound + ref.U[dtype] * dw.abs()).all()
