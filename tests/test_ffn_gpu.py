@@ -313,3 +313,15 @@ def test_empty_sizes_one_by_one(M, K, F, N, dtype):
     assert not got["y"].any()
     for name, t in zip(NAMES, leaves):
         assert got[name].shape == t.shape and not got[name].any()
+
+
+@pytest.mark.parametrize("M,K,F,N,dtype", [
+    (3000, 513, 640, 72, torch.bfloat16), (3001, 1025, 1003, 130, torch.float16), (3100, 640, 777, 521, torch.float16), (2999, 1025, 515, 70, torch.bfloat16)])
+def test_rows_at_odd_elements(M, K, F, N, dtype):
+    """Weights and x copied to lines, from 3000 tokens on, or read where they are; views of wider rows as well."""
+    *leaves, dy = make(M, K, F, N, dtype)
+    want = ref.ffn(*leaves, "silu", dy)
+    got = run(leaves, dy, "silu")
+    ref.check(got, want)
+    wide = [torch.nn.functional.pad(t, (1, 7), value=float("nan"))[:, 1:-7] for t in leaves]
+    ref.check(run(wide, dy, "silu"), want)

@@ -549,3 +549,15 @@ def test_logits_made_again_for_long_rows(M, V, K, dtype):
             v, b = ref.xent(x[rows], w, t[rows], reduction="sum", dloss=by, kept=False)["dw"]
             dw, bound = dw + v, bound + b
         assert ((got["dw"].double() - dw).abs() <= bound + ref.U[dtype] * dw.abs()).all()
+
+
+@pytest.mark.parametrize("M,V,K,dtype", [
+    (3000, 2001, 513, torch.bfloat16), (3001, 3001, 1025, torch.float16), (2999, 1500, 777, torch.float16), (4000, 70000, 521, torch.bfloat16)])
+def test_rows_at_odd_elements(M, V, K, dtype):
+    """w copied to lines for the backward pass, from 3000 tokens on, in one piece and in several, or read where it is."""
+    x, w, t = make(M, V, K, dtype)
+    wide = torch.nn.functional.pad(w, (1, 7), value=float("nan"))[:, 1:-7]
+    for keep in (0, 2 ** 34):
+        want = ref.xent(x, w, t, dloss=100.0, kept=keep > 0)
+        ref.check(run(x, w, t, 100.0, keep_bytes=keep), want)
+        ref.check(run(x, wide, t, 100.0, keep_bytes=keep), want)

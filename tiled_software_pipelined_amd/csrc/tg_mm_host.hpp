@@ -33,11 +33,20 @@ inline MmSize mm_size(int form, int64_t M, int64_t N, int64_t slices, bool may_s
 }
 
 // Copies of an operand's rows to whole 128-byte lines.  Rows that start at odd
-// elements make the tile kernels' copies twice as slow (2047x2050x5461 along k:
-// 128 tiles 135 us, on lines 64; 256 tiles 81), other rows that are not on 16-byte
-// boundaries a fifth (2048x5440x2050 gate and up 128 us, 2048 wide 107), so a copy
-// of the weights pays from some rows of the other operand on.
-inline bool mm_packs(int64_t K, int64_t M) { return K % 2 ? M >= 768 : K % 8 ? M >= 4096 : false; }
+// elements make the tile kernels' copies up to twice as slow (2047x2050x5461 along k:
+// 128 tiles 135 us, on lines 64; 256 tiles 81), so a copy of the weights pays where
+// many rows of the other operand M read them, each at least K wide.  Forward passes
+// of eight blocks (K 769 .. 4097), bfloat16 and float16, time without copies over
+// time with them, geometric means:
+//   M                512   768  1024  1500  2047  3000  4096  6000  8192
+//   odd K, odd F    0.95  0.97  0.99  0.98  0.96  1.01  1.05  1.10  1.07
+// and of a training step's loss, whose backward pass reads w twice (V 32000 .. 128001):
+//   K 513 .. 4097               0.93        0.99  1.02  1.02  1.04  1.04
+//   K 65 .. 385                 0.96        0.94  0.97  0.95  1.02  1.00
+// Of the loss's forward pass, which reads it once, 0.94 to 1.01.  Rows at other even
+// elements cost a fifth at most (2048x5440x2050 gate and up 128 us, 2048 wide 107), and
+// copies of theirs pay nowhere (block 0.82 to 1.05, loss 0.44 to 1.00).
+inline bool mm_packs(int64_t K, int64_t M) { return K % 2 && K >= 512 && M >= 3000; }
 inline int64_t mm_lines(int64_t K) { return (K + 63) / 64 * 64; }
 struct MmPack {
     const void* src;

@@ -35,8 +35,8 @@ struct XentLayout {
     int64_t cols, ldz;         // backward: columns of a piece, row stride of dz
     int64_t count, map, rank, lse;                  // kept
     int64_t powers, ldp;                            // kept as well, or -1; then so are hit and part
-    int64_t x, hit, each, part, w;                  // forward's scratch; w: on lines, -1: read where it is
-    int64_t x2, coef, alpha, row_alpha, back, dzs, sum, split, w2;  // backward's
+    int64_t x, hit, each, part;                     // forward's scratch
+    int64_t x2, coef, alpha, row_alpha, back, dzs, sum, split, w2;  // backward's; w2: w on lines, -1: read where it is
     int64_t split_bytes[2];                         // of dx's and dw's launches, which use the same room
     int64_t bytes[3];
 };
@@ -58,17 +58,15 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
     l.map = take(0, 4 * M);   // where they stand
     l.rank = take(0, 4 * M);  // each row's number among them, -1
     l.lse = take(0, 8 * M);   // of each of them
-    const bool pack = mm_packs(K, M) && V <= MM_WAVE_ROWS;  // as far as a launch of a wave a row reaches
     l.ldx = mm_lines(K);
-    l.w = l.w2 = -1;
-    l.stats = mm_size(FORM_STATS, M, V, mm_slices(K), false, pack ? 0 : K);
+    l.w2 = -1;
+    l.stats = mm_size(FORM_STATS, M, V, mm_slices(K), false, K);
     l.parts = (V + wave_cols(l.stats) - 1) / wave_cols(l.stats);
     const bool powers = keep & TGEMM_KEEP_POWERS;
     l.x = take(1, 2 * M * l.ldx);
     l.hit = take(!powers, 4 * M);  // the target's logit of each of them
     l.each = take(1, 4 * M);       // each row's loss
     l.part = take(!powers, 8 * M * l.parts);
-    if (pack) l.w = take(1, 2 * V * l.ldx);
     l.ldp = mm_lines(V);
     l.powers = powers ? take(0, 2 * M * l.ldp) : -1;
     if (!(keep & (TGEMM_KEEP_X | TGEMM_KEEP_W))) return l;
@@ -84,6 +82,7 @@ static XentLayout xent_layout(int64_t M, int64_t V, int64_t K, int keep) {
     l.ldz = l.cols;
     const int64_t cols = l.cols < V ? l.cols : V;
     const MmShape dx{M, K}, dw{cols, K};
+    const bool pack = mm_packs(K, M) && cols <= MM_WAVE_ROWS;  // as far as a launch of a wave a row reaches
     l.dz = mm_size(FORM_DZ, M, cols, mm_slices(K), false, pack ? 0 : K);
     l.x2 = take(2, 2 * padded * l.ldx);
     l.coef = take(2, 4 * M);
@@ -576,12 +575,6 @@ int tgemm_xent_forward(int64_t M, int64_t V, int64_t K, int32_t dtype, const voi
         rc = mm_launch(reinterpret_cast<const void*>(xent_scan_kernel), 1, 1024, &c, "rows that count", st);
         if (rc == TGEMM_OK && M > 0)
             rc = mm_launch(reinterpret_cast<const void*>(xent_gather_kernel), (M + 3) / 4, 256, &into, "rows that count", st);
-    }
-    if (rc == TGEMM_OK && M > 0 && l.w >= 0 && !mm_aligned(w, ldw)) {
-        const MmPack p{w, ldw, V, K, s + l.w};
-        rc = mm_pack(&p, 1, st);
-        w = s + l.w;
-        ldw = l.ldx;
     }
     if (rc == TGEMM_OK && M > 0 && V > 0) {
         const MmKernel& k = mm_kernels(dtype, l.powers >= 0 ? FORM_STATS_KEEP : FORM_STATS)[l.stats];
