@@ -325,3 +325,43 @@ def test_rows_at_odd_elements(M, K, F, N, dtype):
     ref.check(got, want)
     wide = [torch.nn.functional.pad(t, (1, 7), value=float("nan"))[:, 1:-7] for t in leaves]
     ref.check(run(wide, dy, "silu"), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("act", list(tl.ACTIVATIONS))
+def test_gradients_of_values_that_are_not_finite_stay_in_their_rows(act, dtype):
+    *leaves, dy = make(200, 80, 96, 64, dtype)
+    clean = run(leaves, dy, act)
+    rows = [i for i in range(200) if i not in (3, 150, 170)]
+    leaves[0][3, 5], leaves[0][150, 0], dy[170, 1] = float("nan"), float("inf"), float("nan")
+    got = run(leaves, dy, act)
+    assert torch.equal(got["dx"][rows], clean["dx"][rows]) and torch.equal(got["y"][rows], clean["y"][rows])
+    assert got["y"][3].isnan().all() and not got["y"][150].isfinite().any() and torch.equal(got["y"][170], clean["y"][170])
+    if act == "relu":  # a comparison has no value for a gate without one: its slope is 0
+        assert got["dx"][170].isnan().all() and not got["dw_down"].isfinite().all()
+    else:
+        assert got["dx"][[3, 170]].isnan().all() and got["dw_up"].isnan().all() and got["dw_gate"].isnan().all()
+
+
+def test_float16_captured_and_replayed():
+    *leaves, dy = make(100, 128, 344, 128, torch.float16)
+    leaves = [t.requires_grad_() for t in leaves]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(tl.gated_ffn(*leaves, activation="gelu"), leaves, dy)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = tl.gated_ffn(*leaves, activation="gelu")
+        out = (y, *torch.autograd.grad(y, leaves, dy))
+    for seed in range(3):
+        *new, ndy = make(100, 128, 344, 128, torch.float16, seed=100 + seed)
+        with torch.no_grad():
+            for t, n in zip((*leaves, dy), (*new, ndy)):
+                t.copy_(n)
+        want = run(new, ndy, "gelu")
+        g.replay()
+        torch.cuda.synchronize()
+        for name, o in zip(("y",) + NAMES, out):
+            assert torch.equal(o, want[name]), (seed, name)

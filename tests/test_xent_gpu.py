@@ -561,3 +561,41 @@ def test_rows_at_odd_elements(M, V, K, dtype):
         want = ref.xent(x, w, t, dloss=100.0, kept=keep > 0)
         ref.check(run(x, w, t, 100.0, keep_bytes=keep), want)
         ref.check(run(x, wide, t, 100.0, keep_bytes=keep), want)
+
+
+@pytest.mark.parametrize("K", [64, 520])
+def test_rows_scales_captured_and_replayed(K):
+    """Float16 and a loss for each row: as many launches whatever the rows' factors are."""
+    x, w, t = make(100, 1000, K, torch.float16)
+    x, w, by = x.requires_grad_(), w.requires_grad_(), torch.ones(100, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(tl.linear_cross_entropy(x, w, t, reduction="none"), (x, w), by)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        loss = tl.linear_cross_entropy(x, w, t, reduction="none")
+        out = (loss, *torch.autograd.grad(loss, (x, w), by))
+    for seed in range(3):
+        nx, nw, nt = make(100, 1000, K, torch.float16, seed=50 + seed)
+        nby = torch.exp2(torch.linspace(-20.0 * seed, 4.0, 100, device="cuda"))
+        with torch.no_grad():
+            x.copy_(nx), w.copy_(nw), t.copy_(nt), by.copy_(nby)
+        want = run(nx, nw, nt, nby, "none")
+        g.replay()
+        torch.cuda.synchronize()
+        for name, o in zip(("loss", "dx", "dw"), out):
+            assert torch.equal(o, want[name]), (seed, name)
+
+
+def test_factors_that_are_not_finite_stay_in_their_rows():
+    for dtype in DTYPES:
+        x, w, t = make(90, 400, 64, dtype, ignored=0.0)
+        by = torch.linspace(0.5, 2, 90, device="cuda")
+        clean = run(x, w, t, by, "none")
+        by[4], by[40] = float("inf"), float("nan")
+        got = run(x, w, t, by, "none")
+        rows = [i for i in range(90) if i not in (4, 40)]
+        assert torch.equal(got["dx"][rows], clean["dx"][rows]) and torch.equal(got["loss"], clean["loss"])
+        assert not got["dx"][[4, 40]].isfinite().any() and not got["dw"].isfinite().any()
