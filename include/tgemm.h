@@ -491,21 +491,19 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
  *
  * act: silu g / (1 + e^-g), gelu g Phi(g), its tanh form, or relu.  h is rounded
  * to `dtype` (the operand of the second product), y once from float sums.  `keep`
- * says which gradients will be asked for; what they need is then kept in `saved`:
- * in bfloat16 a = act(g), b = act'(g) u and h, rounded to it; in float16, whose
- * numbers end above the a and b of closed gates, g and u in 24 bits each (h alone
- * for TGEMM_FFN_DOWN alone).  backward, for dy (M x N) and forward's `act`:
+ * says which gradients will be asked for; with any of TGEMM_FFN_X, _GATE and _UP g
+ * and u are then kept in `saved`, in 24 bits each, with TGEMM_FFN_DOWN alone h.
+ * backward, for dy (M x N) and forward's `act` and `keep`:
  *
- *     dh = dy wd,  dg = dh b,  du = dh a,
+ *     dh = dy wd,  dg = dh act'(g) u,  du = dh act(g),
  *     dx = dg wg + du wu,  dwg = dg^T x,  dwu = du^T x,  dwd = dy^T h
  *
- * with dg and du rounded to `dtype`; outputs are written where `keep` (the same
- * as before) has their bit, and ignored otherwise.  relu'(0) = 0.  tgemm_ffn_bytes
- * fills bytes[0 .. 2] with the sizes of `saved`, of forward's `scratch` and of
- * backward's `scratch`, enough for either type (with TGEMM_FFN_BF16 in `keep`, which
- * this call alone takes, for bfloat16): device memory, 256-byte aligned; a scratch's
- * contents are overwritten, `saved` is only read by backward.  Sizes of zero are the empty
- * products they make.  Each returns TGEMM_OK or a TGEMM_E_* code. */
+ * with dg and du rounded to `dtype`; outputs are written where `keep` has their
+ * bit, and ignored otherwise.  relu'(0) = 0.  tgemm_ffn_bytes fills bytes[0 .. 2]
+ * with the sizes of `saved`, of forward's `scratch` and of backward's `scratch`:
+ * device memory, 256-byte aligned; a scratch's contents are overwritten, `saved` is
+ * only read by backward.  Sizes of zero are the empty products they make.  Each
+ * returns TGEMM_OK or a TGEMM_E_* code. */
 #define TGEMM_SILU 0
 #define TGEMM_GELU 1
 #define TGEMM_GELU_TANH 2
@@ -514,7 +512,6 @@ int tgemm_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t dtype
 #define TGEMM_FFN_GATE 2
 #define TGEMM_FFN_UP 4
 #define TGEMM_FFN_DOWN 8
-#define TGEMM_FFN_BF16 256
 int tgemm_ffn_bytes(int64_t M, int64_t K, int64_t F, int64_t N, int32_t keep, int64_t* bytes);
 int tgemm_ffn_forward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype, int32_t act, const void* x, int64_t ldx,
                       const void* wg, int64_t ldg, const void* wu, int64_t ldu, const void* wd, int64_t ldd, void* y,

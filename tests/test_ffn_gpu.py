@@ -365,3 +365,20 @@ def test_float16_captured_and_replayed():
         torch.cuda.synchronize()
         for name, o in zip(("y",) + NAMES, out):
             assert torch.equal(o, want[name]), (seed, name)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("act", list(tl.ACTIVATIONS))
+def test_gradients_have_two_roundings(act, dtype):
+    """One token and units of their own: dg and du are rounded, and the results; act(g) and act'(g) u are not."""
+    F = 4096
+    g = torch.Generator(device="cuda").manual_seed(11)
+    gate, up, dy = [(torch.randn(F, generator=g, device="cuda") * s).to(dtype) for s in (2.0, 1.0, 1.0)]
+    one = torch.ones(1, 1, dtype=dtype, device="cuda")
+    got = run([one, gate[:, None], up[:, None], torch.eye(F, dtype=dtype, device="cuda")], dy[None], act)
+    a, d, _ = ref.act(gate.double(), act)
+    u, v, w = ref.U[dtype], up.double(), dy.double()
+    for name, want, size in (("dw_gate", w * d * v, w * v), ("dw_up", w * a, w)):
+        # g and u in 24 bits are exact here; the activation: 2^-18 of its terms
+        off = (got[name][:, 0].double() - want).abs()
+        assert (off <= 2 * u * (1 + u) * want.abs() + 2.0 ** -18 * size.abs() * (1 + gate.double().abs()) + 2 * ref.TINY[dtype]).all(), name

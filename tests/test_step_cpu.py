@@ -60,17 +60,10 @@ def test_ffn_sizes():
     assert tl._lib.tgemm_ffn_bytes(2 ** 30, 2 ** 22, 2 ** 22, 2 ** 22, 1, n) == 0 and min(n) > 2 ** 52
 
 
-def test_bytes_kept_in_either_type():
-    """One size query serves both types; bfloat16 by itself keeps no more than it needs."""
-    sizes = 100, 64, 1000, 72
+def test_bytes_kept_for_the_backward_pass():
+    """Six for each token and inner unit where a gradient passes the activation, two for w_down's alone."""
     for keep in range(16):
-        either, bf16 = tl._ffn_bytes(*sizes, keep), tl._ffn_bytes(*sizes, keep | tl.FFN_BF16)
-        plane, n = 2 * 100 * 1024, bool(keep & 5) + bool(keep & 3) + bool(keep & 8)
-        assert bf16[0] == max(1, n * plane) and either[0] == max(1, (3 if keep & 7 else n) * plane)
-        assert all(a >= b for a, b in zip(either, bf16))
-    n = (ctypes.c_int64 * 3)()
-    assert tl._lib.tgemm_ffn_bytes(*sizes, 256 + 16, n) == -1 and tl._lib.tgemm_ffn_bytes(*sizes, -256, n) == -1
-    assert fwd(keep=256) == -1 and bwd(keep=256) == -1
+        assert tl._ffn_bytes(100, 64, 1000, 72, keep)[0] == max(1, (6 if keep & 7 else 2 if keep else 0) * 100 * 1024)
 
 
 @pytest.mark.parametrize("kw", [dict(M=0, N=0), dict(M=0)])

@@ -2,16 +2,10 @@
 // gradients: what stands where in the caller's buffers, and the launches.
 //
 // Forward: gate and up projections in one kernel that ends with h, and for the
-// backward pass with a = act(g) and b = act'(g) u; the down projection.
-// Backward: dh = dy Wd in one that ends with dg = dh b and du = dh a; dx = dg Wg +
-// du Wu as one product; the three weights' gradients in one launch.
-//
-// In bfloat16 a, b and h are kept, each rounded once from float.  In place of g and
-// u so rounded, they leave out a rounding of each gradient (their errors are 2.9e-3
-// of the norm, 2.4e-3 for w_down's, with g and u kept 3.5e-3) and the activation
-// from the backward pass.  float16 has no room for the a and b of closed gates:
-// there g and u are kept in 24 bits each (Kept24), in as many bytes, and backward
-// makes a, b and h from them.
+// backward pass keeps g and u in 24 bits each (Kept24); the down projection.
+// Backward: dh = dy Wd in one that ends with dg = dh act'(g) u, du = dh act(g) and,
+// for w_down's gradient, h again; dx = dg Wg + du Wu as one product; the three
+// weights' gradients in one launch.
 #include <climits>
 
 #include "tg_mm_host.hpp"
@@ -19,9 +13,9 @@
 namespace tg {
 
 struct FfnLayout {
-    bool kept24;             // g and u are kept, not a, b and h
-    int64_t a, b, low, h;    // forward: kept, or in scratch (h); -1: not there
-    bool h_kept;             // bfloat16, or h alone: the down projection's gradient is wanted
+    int64_t g, u, low;       // forward: g and u, kept; -1: not there
+    int64_t h;               // kept, or in scratch
+    bool h_kept;             // the down projection's gradient is wanted alone
     int64_t ld;              // row stride of all of them: whole 128-byte lines
     int64_t split;           // forward's scratch: sums of the down projection's shared tiles
     int64_t x, wg, wu, wd;   // likewise: operands on lines, -1: read where they are
@@ -35,7 +29,7 @@ struct FfnLayout {
 
 static const int FFN_INNER = TGEMM_FFN_X | TGEMM_FFN_GATE | TGEMM_FFN_UP;
 
-static FfnLayout ffn_layout(int64_t M, int64_t K, int64_t F, int64_t N, int dtype, int keep) {
+static FfnLayout ffn_layout(int64_t M, int64_t K, int64_t F, int64_t N, int keep) {
     FfnLayout l{};
     auto take = [&](int which, int64_t n) {
         const int64_t at = l.bytes[which];
@@ -57,12 +51,11 @@ static FfnLayout ffn_layout(int64_t M, int64_t K, int64_t F, int64_t N, int dtyp
         l.wu = take(1, 2 * F * mm_lines(K));
     }
     if (pack_f) l.wd = take(1, 2 * N * l.ld);
-    l.a = l.b = l.low = l.dg = l.du = l.h2 = -1;
-    l.kept24 = dtype == TGEMM_F16 && (keep & FFN_INNER);
-    l.h_kept = !l.kept24 && (keep & TGEMM_FFN_DOWN);
-    if (l.kept24 || (keep & (TGEMM_FFN_X | TGEMM_FFN_UP))) l.a = take(0, inner);
-    if (l.kept24 || (keep & (TGEMM_FFN_X | TGEMM_FFN_GATE))) l.b = take(0, inner);
-    if (l.kept24) {
+    l.g = l.u = l.low = l.dg = l.du = l.h2 = -1;
+    l.h_kept = keep == TGEMM_FFN_DOWN;
+    if (keep & FFN_INNER) {
+        l.g = take(0, inner);
+        l.u = take(0, inner);
         l.low = take(0, inner);
         if (keep & TGEMM_FFN_DOWN) l.h2 = take(2, inner);
     }
@@ -152,11 +145,9 @@ int tgemm_ffn_bytes(int64_t M, int64_t K, int64_t F, int64_t N, int32_t keep, in
         set_error("NULL bytes");
         return TGEMM_E_NULL;
     }
-    const bool lone = keep >= 0 && (keep & TGEMM_FFN_BF16);
-    if (lone) keep &= ~TGEMM_FFN_BF16;
     if (!ffn_sizes_ok(M, K, F, N, keep)) return TGEMM_E_ARG;
-    const FfnLayout l = ffn_layout(M, K, F, N, TGEMM_BF16, keep), other = ffn_layout(M, K, F, N, TGEMM_F16, keep);
-    for (int i = 0; i < 3; ++i) bytes[i] = lone || l.bytes[i] > other.bytes[i] ? l.bytes[i] : other.bytes[i];
+    const FfnLayout l = ffn_layout(M, K, F, N, keep);
+    for (int i = 0; i < 3; ++i) bytes[i] = l.bytes[i];
     clear_error();
     return TGEMM_OK;
 }
@@ -166,7 +157,7 @@ int tgemm_ffn_forward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype,
                       int64_t ldy, int32_t keep, void* saved, void* scratch, void* stream) {
     using namespace tg;
     if (!ffn_sizes_ok(M, K, F, N, keep)) return TGEMM_E_ARG;
-    const FfnLayout l = ffn_layout(M, K, F, N, dtype, keep);
+    const FfnLayout l = ffn_layout(M, K, F, N, keep);
     int rc = ffn_common(dtype, act);
     if (rc == TGEMM_OK) rc = mm_check("x", x, M, K, ldx);
     if (rc == TGEMM_OK) rc = mm_check("w_gate", wg, F, K, ldg);
@@ -209,8 +200,8 @@ int tgemm_ffn_forward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype,
             rc = mm_launch(rows_kernel<true>(dtype), (F + 15) / 16, 512, &a, "gate and up projections", st);
         } else {
             const MmKernel& k = mm_kernels(dtype, FORM_GATE)[l.gate];
-            MmGateArgs a{o, mm_grid(k, M, F), h, l.a < 0 ? nullptr : v + l.a, l.b < 0 ? nullptr : v + l.b,
-                         l.low < 0 ? nullptr : v + l.low, l.ld, act};
+            auto kept = [&](int64_t at) { return at < 0 ? nullptr : v + at; };
+            MmGateArgs a{o, mm_grid(k, M, F), h, kept(l.g), kept(l.u), kept(l.low), l.ld, act};
             rc = mm_launch(k.fn, (int64_t)a.grid.tiles_m * a.grid.tiles_n, k.threads, &a, "gate and up projections", st);
         }
     }
@@ -236,7 +227,7 @@ int tgemm_ffn_backward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype
                        void* dwu, int64_t lddwu, void* dwd, int64_t lddwd, void* scratch, void* stream) {
     using namespace tg;
     if (!ffn_sizes_ok(M, K, F, N, keep)) return TGEMM_E_ARG;
-    const FfnLayout l = ffn_layout(M, K, F, N, dtype, keep);
+    const FfnLayout l = ffn_layout(M, K, F, N, keep);
     int rc = ffn_common(dtype, act);
     if (rc == TGEMM_OK) rc = mm_check("x", x, M, K, ldx);
     if (rc == TGEMM_OK) rc = mm_check("w_gate", wg, F, K, ldg);
@@ -257,11 +248,11 @@ int tgemm_ffn_backward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype
     char* s = static_cast<char*>(scratch);
     auto in_scratch = [&](int64_t at) { return at < 0 ? nullptr : s + at; };
     char *dg = in_scratch(l.dg), *du = in_scratch(l.du);
-    const char* h = l.kept24 ? in_scratch(l.h2) : v + l.h;
+    const char* h = l.h_kept ? v + l.h : in_scratch(l.h2);
     if ((keep & FFN_INNER) && M > 0 && F > 0) {
         const MmKernel& k = mm_kernels(dtype, FORM_DH)[l.dh];
-        MmDhArgs a{operands(dy, lddy, wd, ldd, M, F, N), mm_grid(k, M, F), v + (l.a < 0 ? l.b : l.a), v + (l.b < 0 ? l.a : l.b),
-                   l.low < 0 ? nullptr : v + l.low, dg, du, in_scratch(l.h2), l.ld, act};
+        MmDhArgs a{operands(dy, lddy, wd, ldd, M, F, N), mm_grid(k, M, F), v + l.g, v + l.u, v + l.low, dg, du,
+                   in_scratch(l.h2), l.ld, act};
         rc = mm_launch(k.fn, (int64_t)a.grid.tiles_m * a.grid.tiles_n, k.threads, &a, "gradient of the inner values", st);
     }
     if (rc == TGEMM_OK && (keep & TGEMM_FFN_X)) {

@@ -76,10 +76,9 @@ struct MmStoreArgs {
 struct MmGateArgs {
     MmOperands op;
     MmGrid grid;
-    // M x N, row stride ld; anything may be written between N and ld.  h: act(g) u.
-    // bfloat16: a act(g), b act'(g) u, each NULL where it is not kept, low NULL.
-    // float16: Kept24 of g and u, all NULL where they are not kept
-    void *h, *a, *b, *low;
+    // M x N, row stride ld; anything may be written between N and ld.  h: act(g) u; the
+    // others: Kept24 of g and u, NULL where they are not kept
+    void *h, *gate, *up, *low;
     int64_t ld;
     int32_t act;
 };
@@ -87,21 +86,22 @@ struct MmGateArgs {
 struct MmDhArgs {
     MmOperands op;
     MmGrid grid;
-    // all of them there (low: in float16): a branch at each load costs 70 us of 4096x4096x11008's 480
-    const void *a, *b, *low;
-    void *dg, *du;  // M x N, row stride ld (a's, b's, low's and h's too); either NULL where it is not wanted.
-                    // Anything may be written between N and ld
-    void* h;        // float16: act(g) u again, rounded; NULL where it is not wanted
+    const void *gate, *up, *low;  // Kept24 of g and u
+    // M x N, row stride ld, as the others; NULL where they are not wanted.  h: act(g) u
+    // again, rounded.  Anything may be written between N and ld
+    void *dg, *du, *h;
     int64_t ld;
     int32_t act;
 };
 
-// g and u in 24 bits each, for a backward pass in float16: a sign, float's 8 bits
-// of exponent and 15 behind the point (off by 2^-16), the upper halves of eight g,
-// those of eight u, and a byte more of each.  act(g) and act'(g) u of a closed gate
-// are below float16's normal numbers and would lose their digits in it (silu(-18)
-// 9 % of it, silu(-21) all), though a scaled loss's dh makes numbers of them that
-// it holds; from g they are made in float.
+// g and u in 24 bits each, for the backward pass: a sign, float's 8 bits of exponent
+// and 15 behind the point (off by 2^-16), the upper halves of eight g, those of
+// eight u, and a byte more of each.  act(g) and act'(g) u are made from them in
+// float and rounded with dh, as du and dg.  In 16 bits themselves, in as many bytes
+// with h, they would add a rounding (gradients off by 2.9e-3 of their norm in
+// bfloat16, 2.3e-3 so) and those of closed gates would have no digits in float16
+// (silu(-18) off by 9 %, silu(-21) zero), though a scaled loss's dh makes numbers of
+// them that it holds.  It costs 2 % of a training step of 4096x4096x11008.
 struct Kept24 {
     i32x4 g, u, low;
     __device__ static __forceinline__ uint32_t rounded(float v) {
@@ -128,8 +128,6 @@ struct Kept24 {
         }
     }
 };
-template <class T>
-constexpr bool KEEPS_24 = __is_same(T, _Float16);
 
 // ---- cross entropy ---------------------------------------------------------------
 // Rows of x are those that count, gathered; how many only the device knows.
@@ -506,27 +504,17 @@ __global__ __launch_bounds__(G::NT) void mm_gate_kernel(MmGateArgs g) {
                 if (inside.value || out.count(u) > 0) store8(out.at(static_cast<T*>(p), u), x);
             };
             float a[8], d[8];
-            if (KEEPS_24<T> && g.low) {  // for the backward pass: past the caches
+            if (g.low) {  // for the backward pass: past the caches
                 Kept24 k;
                 k.set(v, w);
-                if (inside.value || out.count(u) > 0) {
-                    __builtin_nontemporal_store(k.g, reinterpret_cast<i32x4*>(out.at(static_cast<T*>(g.a), u)));
-                    __builtin_nontemporal_store(k.u, reinterpret_cast<i32x4*>(out.at(static_cast<T*>(g.b), u)));
-                    __builtin_nontemporal_store(k.low, reinterpret_cast<i32x4*>(out.at(static_cast<T*>(g.low), u)));
-                }
-                activate8<false>(g.act, v, a, d);
-            } else if (!KEEPS_24<T> && (g.a || g.b)) {
-                auto keep = [&](void* p, F8 x) {
-                    if (p && (inside.value || out.count(u) > 0)) stream8(out.at(static_cast<T*>(p), u), x);
+                auto keep = [&](void* p, i32x4 x) {
+                    if (inside.value || out.count(u) > 0) __builtin_nontemporal_store(x, reinterpret_cast<i32x4*>(out.at(static_cast<T*>(p), u)));
                 };
-                activate8<true>(g.act, v, a, d);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] *= w[e];
-                keep(g.a, a);
-                keep(g.b, d);
-            } else {
-                activate8<false>(g.act, v, a, d);
+                keep(g.gate, k.g);
+                keep(g.up, k.u);
+                keep(g.low, k.low);
             }
+            activate8<false>(g.act, v, a, d);
 #pragma unroll
             for (int e = 0; e < 8; ++e) a[e] *= w[e];
             put(g.h, a);  // its rounding: the down projection's operand
@@ -547,41 +535,28 @@ __global__ __launch_bounds__(G::NT) void mm_dh_kernel(MmDhArgs g) {
     G::product(g.op, at.m0, at.n0, 0, (g.op.K + 63) / 64, smem, acc, at.wm0, at.wn0, at.lane, at.wave);
     const MmOut<G> out(at, g.op.M, (int)g.ld, g.ld);  // rows whole up to their stride: no edge inside them
     typedef float(&F8)[8];
-    struct Kept {
-        Raw8 a, b, low;
-    };
     auto way = [&](auto inside) {
-        G::template each_row<Kept>(acc, smem, at.lane, at.wave, [&](int u, Kept& k) {
+        G::template each_row<Kept24>(acc, smem, at.lane, at.wave, [&](int u, Kept24& k) {
             if (inside.value || out.count(u) > 0) {
-                load8(k.a, out.at(static_cast<const T*>(g.a), u));
-                load8(k.b, out.at(static_cast<const T*>(g.b), u));
-                if constexpr (KEEPS_24<T>) load8(k.low, out.at(static_cast<const T*>(g.low), u));
+                k.g = load16(out.at(static_cast<const T*>(g.gate), u));
+                k.u = load16(out.at(static_cast<const T*>(g.up), u));
+                k.low = load16(out.at(static_cast<const T*>(g.low), u));
             }
-        }, [&](int u, F8 v, F8, Kept& k) {
+        }, [&](int u, F8 v, F8, Kept24& k) {
             // roundings of du, dg and h: operands of the products that follow
             auto put = [&](void* p, F8 x) {
                 if (inside.value || out.count(u) > 0) store8(out.at(static_cast<T*>(p), u), x);
             };
-            float a[8], b[8];
-            if constexpr (KEEPS_24<T>) {
-                float gate[8], up[8], h[8];
-                Kept24{k.a.v, k.b.v, k.low.v}.get(gate, up);
-                activate8<true>(g.act, gate, a, b);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    b[e] *= up[e];
-                    h[e] = a[e] * up[e];
-                }
-                if (g.h) put(g.h, h);
-            } else {
-                values8<T>(a, k.a);
-                values8<T>(b, k.b);
-            }
+            float gate[8], up[8], a[8], b[8], h[8];
+            k.get(gate, up);
+            activate8<true>(g.act, gate, a, b);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
+                h[e] = a[e] * up[e];
                 a[e] *= v[e];
-                b[e] *= v[e];
+                b[e] *= up[e] * v[e];
             }
+            if (g.h) put(g.h, h);
             if (g.du) put(g.du, a);
             if (g.dg) put(g.dg, b);
         });

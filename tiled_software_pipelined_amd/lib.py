@@ -801,7 +801,6 @@ def orthogonalize(G, steps=5, coefficients=ORTHOGONALIZE_COEFFICIENTS, eps=1e-7,
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
 FFN_X, FFN_GATE, FFN_UP, FFN_DOWN = 1, 2, 4, 8
-FFN_BF16 = 256  # sizes for bfloat16 alone
 MOST_STRIDE = 1 << 22  # elements from a row to the next
 _HALF_CODES = {torch.bfloat16: BF16, torch.float16: F16}
 
@@ -861,7 +860,7 @@ def _pointers(operands):
 def _ffn_forward(x, sizes, operands, code, act, keep):
     """y of shape (..., N), and the buffer for the backward pass (None where keep is 0)."""
     device, N = x.device, sizes[3]
-    room = _ffn_bytes(*sizes, keep | FFN_BF16 if code == BF16 else keep)
+    room = _ffn_bytes(*sizes, keep)
     saved = torch.empty(room[0], dtype=torch.uint8, device=device) if keep else None
     scratch = torch.empty(room[1], dtype=torch.uint8, device=device)
     y = torch.empty(x.shape[:-1] + (N,), dtype=x.dtype, device=device)
@@ -890,7 +889,7 @@ class _GatedFfn(torch.autograd.Function):
         device = gy.device
         _, operands = _ffn_call(*inputs)
         g, ldy = _read(gy if gy.dim() == 2 else gy.reshape(M, N))
-        scratch = torch.empty(_ffn_bytes(M, K, F, N, keep | FFN_BF16 if code == BF16 else keep)[2], dtype=torch.uint8, device=device)
+        scratch = torch.empty(_ffn_bytes(M, K, F, N, keep)[2], dtype=torch.uint8, device=device)
         grads = [torch.empty_like(t, memory_format=torch.contiguous_format) if keep >> i & 1 else None for i, t in enumerate(inputs)]
         dx, dg, du, dd = [None if t is None else t.data_ptr() for t in grads]
         _call(device, _lib.tgemm_ffn_backward, M, K, F, N, code, act, *_pointers(operands), g.data_ptr(), ldy, keep,
@@ -906,13 +905,12 @@ def gated_ffn(x, w_gate, w_up, w_down, activation="silu"):
     float16; rows may be apart (parts of one (2 F, K) tensor serve as w_gate and
     w_up).  ``activation``: "silu", "gelu", "gelu_tanh" or "relu".  Returns
     (..., N) of x's dtype.  Sums are float; the inner values are rounded to
-    x's dtype (so are both projections' gradients and, in bfloat16, the activation and
-    its slope times the up projection; float16 keeps both projections in 24 bits
-    instead, since closed gates' activations end below its numbers), y and each
-    gradient once.  The two projections, the activation and their product are one
-    kernel; up to 16 tokens without gradients take kernels that read each weight once.
-    For the backward pass up to six bytes are kept for each token and inner unit; it
-    computes only the gradients that are asked for; second derivatives and forward-mode ones are refused.  To capture a
+    x's dtype (so are both projections' gradients), y and each gradient once.  The two
+    projections, the activation and their product are one kernel; up to 16 tokens
+    without gradients take kernels that read each weight once.  For the backward pass
+    both projections are kept in 24 bits, six bytes for each token and inner unit (two
+    where w_down's gradient alone is wanted); it computes only the gradients that are
+    asked for; second derivatives and forward-mode ones are refused.  To capture a
     training step into a graph, see :func:`linear_fp8`.
     """
     act = ACTIVATIONS.get(activation)
