@@ -526,13 +526,14 @@ int tgemm_ffn_backward(int64_t M, int64_t K, int64_t F, int64_t N, int32_t dtype
  *
  *     lse = log sum_v exp z_v,   loss = lse - z[target]
  *
- * The logits are not stored.  Rows whose target is `ignore` do not count: they
- * are left out of every product, and their loss and gradient are zero, whatever
- * they hold.  A target that is neither `ignore` nor in [0, V) makes its row's loss
- * NaN, and the gradients that the row enters.  reduction: TGEMM_NONE (loss: M
- * floats), TGEMM_SUM, or TGEMM_MEAN over the rows that count (one float; NaN where
- * none does).  saved: which rows count, their maximum and lse above it, for the
- * backward pass, which only reads it.  backward, with dloss the gradient of the loss (M floats or one):
+ * There is no tensor of logits (but see TGEMM_KEEP_POWERS).  Rows whose target is
+ * `ignore` do not count: they are left out of every product, and their loss and
+ * gradient are zero, whatever they hold.  A target that is neither `ignore` nor in
+ * [0, V) makes its row's loss NaN, and the gradients that the row enters.
+ * reduction: TGEMM_NONE (loss: M floats), TGEMM_SUM, or TGEMM_MEAN over the rows
+ * that count (one float; NaN where none does).  saved: which rows count, their
+ * maximum and lse above it, for the backward pass, which only reads it.  backward,
+ * with dloss the gradient of the loss (M floats or one):
  *
  *     dz = c (exp(z - lse) - [target]),  dx = dz w,  dw = dz^T x,
  *

@@ -819,11 +819,12 @@ MmKernel mm_entry(const void* fn, const void* join = nullptr) {
 // The tiles.  256 x 256: eight waves of 64 x 128 (four of 128 x 128: 4096^3 alike,
 // 110 us, but 4096x11008x4096 ended by the softmax's pieces 313 us against 294,
 // where a lone wave a SIMD does the end's arithmetic by itself; the end that loads
-// two values for each result is better off with four, 378 us against 394 while it
-// made the activation as well, 355 now).  128 x 128 twice a compute unit, four
-// waves and two slots each; 64 x 128 likewise with three slots, for few rows.  128 x
-// 128 once a unit, eight waves and four slots, where there are no more workgroups
-// than units (2048x2048x5440 46 us, twice a unit 56; four waves 48).
+// values for each result and makes the activation is better off with four, 378 us
+// against 394 with two loads, 419 in a later run with the three of Kept24).  128 x
+// 128 twice a compute unit, four waves and two slots each; 64 x 128 likewise with
+// three slots, for few rows.  128 x 128 once a unit, eight waves and four slots,
+// where there are no more workgroups than units (2048x2048x5440 46 us, twice a unit
+// 56; four waves 48).
 template <class Tr, int LA, int LB, bool PAIR>
 struct MmTiles {
     typedef MmTile<Tr, LA, LB, 256, 256, 4, 2, 2, false, PAIR> T256;

@@ -1,5 +1,5 @@
-// Softmax cross entropy of a linear layer's logits z = x W^T, which are not
-// stored: loss = log sum exp z - z[target].
+// Softmax cross entropy of a linear layer's logits z = x W^T, without a tensor of
+// them: loss = log sum exp z - z[target].
 //
 // Rows that do not count (a prompt's tokens, padding) are left out of every
 // product: the rows of x that count are gathered (and stand on 128-byte lines
@@ -245,7 +245,7 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(GatherArgs g) {
 }
 
 // Both at once for up to SCAN_ROWS rows: each workgroup counts the rows before its
-// own four by itself (a launch less: 4 us; all workgroups together read M^2 / 4
+// own four by itself (a launch less: 4 us; all workgroups together read M^2 / 8
 // targets, which 4096 rows keep under 2 us).
 constexpr int64_t SCAN_ROWS = 4096;
 __global__ __launch_bounds__(256) void xent_scan_gather_kernel(ScanArgs s, GatherArgs g) {

@@ -928,10 +928,11 @@ def gated_ffn(x, w_gate, w_up, w_down, activation="silu"):
 
 
 # Keeping the powers of the logits spares a product of 2 K operations an element
-# and costs two passes of two bytes.  Training step in us, made again and kept:
-#   4096x32000x512   619  595      4096x32000x1024  1022   896
-#   1000x50257x768   408  368      8192x128256x4096 27228 21344
-#   500x1000x512     142  142      256x32000x2048    202   178
+# and costs two passes of two bytes.  Training step in us, made again and kept,
+# every token counting:
+#   4096x32000x256   453  482      1000x50257x768    415   372
+#   4096x32000x512   649  607      8192x128256x4096 28045 21903
+#   4096x32000x1024 1058  912      256x32000x2048    209   182
 POWERS_LEAST = 512
 
 
@@ -984,8 +985,9 @@ class _LinearCrossEntropy(torch.autograd.Function):
 
 
 def linear_cross_entropy(x, w, target, ignore_index=-100, reduction="mean", keep_bytes=4 * 2 ** 30):
-    """Softmax cross entropy of the logits x @ w^T, which are not stored,
-    differentiable: logsumexp(x @ w^T) - (x @ w^T)[target] of each token.
+    """Softmax cross entropy of the logits x @ w^T, without a tensor of them (but see
+    ``keep_bytes``), differentiable: logsumexp(x @ w^T) - (x @ w^T)[target] of each
+    token.
 
     x: (..., K), w: (V, K), both bfloat16 or both float16; target: int64 of
     x.shape[:-1].  Tokens whose target is ``ignore_index`` do not count, whatever
@@ -999,11 +1001,12 @@ def linear_cross_entropy(x, w, target, ignore_index=-100, reduction="mean", keep
     most, or 16 KB a token where that is more, and dx's float sums where there are
     several pieces).  With gradients wanted and K of at least 512, the forward pass
     keeps each logit's power of e, relative to a maximum of its row and rounded to
-    10 bits (float16: 12), where all of them take at most ``keep_bytes`` (2 V bytes a token, whether
-    it counts or not: as much as logits of 16 bits; 0: never); otherwise the backward
-    pass makes the logits again, which takes up to 1.3 times as long for the step.  It
-    rounds the logits' gradients to x's dtype, scaled by a factor that the results do
-    not keep, so that small probabilities hold in float16 too.  Gradients have their inputs' dtypes;
+    10 bits (float16: 12), where all of them take at most ``keep_bytes`` (2 V bytes a
+    token, whether it counts or not: as much as logits of 16 bits; 0: never); otherwise
+    the backward pass makes the logits again, which takes up to 1.3 times as long for
+    the step.  It rounds the logits' gradients to x's dtype, scaled by a factor that the
+    results do not keep, so that small probabilities hold in float16 too.  Gradients
+    have their inputs' dtypes;
     second derivatives and forward-mode ones are refused.  To capture a training
     step into a graph, see :func:`linear_fp8`.
     """
