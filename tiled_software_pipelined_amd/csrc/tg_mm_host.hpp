@@ -36,7 +36,7 @@ inline MmSize mm_size(int form, int64_t M, int64_t N, int64_t slices, bool may_s
 // elements make the tile kernels' copies up to twice as slow (2047x2050x5461 along k:
 // 128 tiles 135 us, on lines 64; 256 tiles 81), so a copy of the weights pays where
 // many rows of the other operand M read them, each at least K wide.  Forward passes
-// of eight blocks (K 769 .. 4097), bfloat16 and float16, time without copies over
+// of seven blocks (K 769 .. 4097), bfloat16 and float16, time without copies over
 // time with them, geometric means:
 //   M                512   768  1024  1500  2047  3000  4096  6000  8192
 //   odd K, odd F    0.95  0.97  0.99  0.98  0.96  1.01  1.05  1.10  1.07
